@@ -132,6 +132,41 @@ pkv_status paged_kv_write(const void* k, const void* v, const int64_t* slot_mapp
                           pkv_dtype dtype, void* stream);
 
 /*
+ * paged_kv_write_rope - rotary positions of a step's q and k, and
+ * paged_kv_write of its K/V rows, in one pass.
+ *
+ * For token t at position p = positions[t], and pair i < rotary_dim / 2 of a
+ * head of q or k, with the angle a = p * inv_freq[i] (radians):
+ *   y1 = amplitude * (x1 cos a - x2 sin a)
+ *   y2 = amplitude * (x2 cos a + x1 sin a)
+ * The pair is elements (i, i + rotary_dim / 2), or (2i, 2i + 1) with
+ * interleaved != 0; elements from rotary_dim on are copied.  q_out gets the
+ * rotated q; the pools get the rotated k and v as it is, at slot_mapping (as
+ * paged_kv_write: slots < 0 are skipped, slots past the pool too, with
+ * PKV_DEVERR_SLOT_OUT_OF_RANGE; q_out gets every token).  Rotated in fp32,
+ * angles reduced exactly for any int64 position, rounded once.
+ *
+ *   q           device, [num_tokens, num_q_heads, head_dim], token stride
+ *               q_token_stride ELEMENTS (>= num_q_heads*head_dim; 0 means dense)
+ *   k, v        as paged_kv_write
+ *   positions   device int64 [num_tokens] (need not match the slots: after an
+ *               eviction they run ahead of the cache index)
+ *   inv_freq    device float64 [rotary_dim / 2], finite, radians per position
+ *               (long-context scalings change these)
+ *   q_out       device, [num_tokens, num_q_heads, head_dim], dense; may be q
+ *               itself when q is dense, must not overlap q otherwise
+ *   rotary_dim  even, 2 .. head_dim
+ *   amplitude   positive and finite (1: none); some scalings use another
+ * num_q_heads and num_kv_heads are independent.  num_tokens == 0 is a no-op.
+ */
+pkv_status paged_kv_write_rope(const void* q, const void* k, const void* v, const int64_t* positions,
+                               const double* inv_freq, const int64_t* slot_mapping, void* q_out, void* k_cache,
+                               void* v_cache, int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                               int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                               int32_t interleaved, float amplitude, int64_t q_token_stride, int64_t k_token_stride,
+                               int64_t v_token_stride, pkv_dtype dtype, void* stream);
+
+/*
  * paged_attention_workspace_size - bytes of device workspace that
  * paged_attention_forward wants for a batch of this shape (an upper bound
  * of what it uses; any smaller size >= paged_attention_workspace_min also
@@ -268,6 +303,19 @@ pkv_status paged_kv_write_fp8(const void* k, const void* v, const int64_t* slot_
                               int32_t num_kv_heads, int32_t head_dim,
                               int64_t k_token_stride, int64_t v_token_stride,
                               pkv_dtype dtype, float k_scale, float v_scale, void* stream);
+
+/*
+ * paged_kv_write_rope_fp8 - paged_kv_write_rope into FP8 pools: the codes are
+ * those of the rotated fp32 values (no rounding to `dtype` in between), by
+ * paged_kv_write_fp8's rule; q_out has q's dtype (bf16 or f32).
+ */
+pkv_status paged_kv_write_rope_fp8(const void* q, const void* k, const void* v, const int64_t* positions,
+                                   const double* inv_freq, const int64_t* slot_mapping, void* q_out, void* k_cache,
+                                   void* v_cache, int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                                   int32_t interleaved, float amplitude, int64_t q_token_stride,
+                                   int64_t k_token_stride, int64_t v_token_stride, pkv_dtype dtype, float k_scale,
+                                   float v_scale, void* stream);
 
 /*
  * paged_attention_forward_fp8kv - paged_attention_forward with FP8 pools:

@@ -13,6 +13,10 @@ tensors are not on a CUDA device, the calls raise.
     paged_attention_forward_fp8kv(q, k_cache, v_cache, ..., scale, k_scale, v_scale)
     BlockManager(num_blocks, block_size, max_blocks_per_seq)   (host, C++)
     copy_blocks(k_cache, v_cache, copies)                      (copy-on-write)
+    paged_kv_write_rope(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
+    paged_attention_scores(q, k_cache, block_tables, ..., scores, scale)
+    paged_kv_select(scores, context_lens, budget)
+    paged_kv_compact(k_cache, v_cache, block_tables, kept)     (eviction)
 
 Block pool per layer: ``[num_blocks, block_size, num_kv_heads, head_dim]``
 ("ADR 004: Paged Attention Serving Integration", Decision 4 - a per-layer
@@ -22,6 +26,7 @@ blocks named by block tables).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -33,6 +38,9 @@ __all__ = [
     "device_errors", "debug_fault", "set_profile_events", "set_profile_mid_event", "profile_elapsed_ms", "lib", "LibraryError", "DEVERR",
     "BlockManager", "OutOfBlocks", "copy_blocks", "paged_kv_write_fp8", "paged_attention_forward_fp8kv",
     "paged_kv_write_attention_forward", "paged_kv_write_attention_forward_fp8kv",
+    "paged_kv_write_rope", "paged_kv_write_rope_fp8", "rope_frequencies", "rope_amplitude",
+    "paged_attention_scores", "paged_attention_scores_fp8kv", "scores_workspace_size", "scores_workspace_min",
+    "paged_kv_select", "paged_kv_compact",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -68,6 +76,8 @@ _lib = None
 _lock = threading.Lock()
 
 c_vp, c_i32, c_i64, c_sz, c_f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_ROPE_ARGS = [c_vp] * 9 + [c_i64, c_i64] + [c_i32] * 6 + [c_f, c_i64, c_i64, c_i64, c_i32]
+_SCORES_ARGS = [c_vp] * 8 + [c_i32, c_i64, c_i32, c_i32, c_i32, c_i64] + [c_i32] * 5 + [c_f, c_i32, c_f]
 
 
 def lib() -> ctypes.CDLL:
@@ -131,9 +141,18 @@ def lib() -> ctypes.CDLL:
                                             c_i64, c_i32, c_f, c_f, c_vp]),
                     ("paged_attention_forward_fp8kv", [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i32,
                                                        c_i32, c_i32, c_i64, c_i32, c_i32, c_i32, c_f, c_i32, c_f,
-                                                       c_f, c_i32, c_vp, c_sz, c_vp])):
+                                                       c_f, c_i32, c_vp, c_sz, c_vp]),
+                    ("paged_kv_write_rope", _ROPE_ARGS + [c_vp]),
+                    ("paged_kv_write_rope_fp8", _ROPE_ARGS + [c_f, c_f, c_vp]),
+                    ("paged_attention_scores", _SCORES_ARGS + [c_vp, c_sz, c_i32, c_vp]),
+                    ("paged_attention_scores_fp8kv", _SCORES_ARGS + [c_f, c_vp, c_sz, c_vp]),
+                    ("paged_kv_select", [c_vp] * 4 + [c_i32] * 7 + [c_vp]),
+                    ("paged_kv_compact", [c_vp] * 7 + [c_i32] * 3 + [c_i64] + [c_i32] * 6 + [c_vp])):
                 getattr(L, name).restype = c_i32
                 getattr(L, name).argtypes = args
+            for name in ("paged_attention_scores_workspace_size", "paged_attention_scores_workspace_min"):
+                getattr(L, name).restype = c_sz
+                getattr(L, name).argtypes = [c_i32, c_i64, c_i32, c_i32, c_i64]
             L.pkv_bm_destroy.restype = None
             L.pkv_bm_destroy.argtypes = [c_vp]
             _lib = L
@@ -611,3 +630,322 @@ def _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_sta
             int(max_query_len), float(scale), 1 if causal else 0, float(k_scale), float(v_scale), 0,
             workspace.data_ptr(), workspace.numel(), _stream(dev))
     return args, out
+
+
+# ----------------------------------------------------------------------------
+# rotary positions with the K/V write (include/paged_kv.h: paged_kv_write_rope)
+# ----------------------------------------------------------------------------
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original_max_position: int = 0, low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                     beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda") -> torch.Tensor:
+    """Rotary frequencies, float64 ``[rotary_dim / 2]`` in radians per
+    position: ``base ** (-2 i / rotary_dim)``, changed for contexts ``factor``
+    times longer than the ``original_max_position`` a model was trained on:
+
+    * ``None``: unchanged;
+    * ``"linear"``: every frequency / factor (positions interpolated);
+    * ``"ntk"``: base * factor ** (rotary_dim / (rotary_dim - 2)), which leaves
+      the highest frequency and divides the lowest by factor;
+    * ``"bands"``: with t = the turns a pair makes over the original context,
+      frequencies of t > high_freq_factor are kept, of t < low_freq_factor
+      divided by factor, and blended linearly in t between;
+    * ``"yarn"``: the same with the blend linear in the pair's index between
+      those that make beta_fast turns (kept) and beta_slow turns (divided); its
+      amplitude is ``rope_amplitude(factor)``.
+    """
+    if rotary_dim < 2 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be even and positive")
+    if not base > 1.0 or not math.isfinite(base):
+        raise ValueError("base must be finite and above 1")
+    if not factor > 0.0 or not math.isfinite(factor):
+        raise ValueError("factor must be positive and finite")
+    i = np.arange(0, rotary_dim, 2, dtype=np.float64)
+    if scaling == "ntk":
+        if rotary_dim <= 2:
+            raise ValueError("ntk scaling needs rotary_dim > 2")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-i / rotary_dim)
+    if scaling in ("bands", "yarn"):
+        if original_max_position <= 0:
+            raise ValueError(f"{scaling} scaling needs original_max_position")
+        if scaling == "bands":
+            if not high_freq_factor > low_freq_factor:
+                raise ValueError("high_freq_factor must exceed low_freq_factor")
+            turns = original_max_position * f / (2 * math.pi)
+            keep = (turns - low_freq_factor) / (high_freq_factor - low_freq_factor)
+        else:
+            if not beta_fast > beta_slow > 0:
+                raise ValueError("beta_fast must exceed beta_slow, both positive")
+
+            def pair_of(turns):  # index (not whole) of the pair that makes so many turns
+                return rotary_dim * math.log(original_max_position / (turns * 2 * math.pi)) / (2 * math.log(base))
+            low = max(math.floor(pair_of(beta_fast)), 0)
+            high = min(math.ceil(pair_of(beta_slow)), rotary_dim - 1)
+            keep = 1.0 - (i / 2 - low) / max(high - low, 1e-3)
+        keep = np.clip(keep, 0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    elif scaling == "linear":
+        f = f / factor
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return torch.from_numpy(np.ascontiguousarray(f)).to(device)
+
+
+def rope_amplitude(factor: float) -> float:
+    """The amplitude of "yarn"-scaled rotations: 0.1 ln(factor) + 1 (1 for
+    factor <= 1)."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+
+
+def _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude, q_out, dev):
+    """Checks paged_kv_write_rope's tensors; returns (its C arguments up to
+    the dtype, q_out)."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() or \
+            not v_cache.is_contiguous():
+        raise ValueError("caches must be contiguous [num_blocks, block_size, num_kv_heads, head_dim]")
+    NB, bs, Hkv, D = k_cache.shape
+    if q.dtype not in DTYPE or q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or q.stride(1) != D:
+        raise ValueError(f"q must be bfloat16 or float32 [T, Hq, {D}] with contiguous heads")
+    T, ks, vs = _new_rows(k, v, slot_mapping, Hkv, D, {q.dtype})
+    if q.shape[0] != T:
+        raise ValueError("q, k and v differ in their number of tokens")
+    if positions.shape != (T,) or positions.dtype != torch.int64 or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int64 [T]")
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() or \
+            not 0 < 2 * inv_freq.shape[0] <= D:
+        raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2] with rotary_dim <= head_dim")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous() or q_out.device != dev:
+        raise ValueError("q_out must be contiguous and match q")
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
+            slot_mapping.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, NB, bs, q.shape[1],
+            Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, float(amplitude), q.stride(0) if T else 0, ks, vs,
+            DTYPE[q.dtype])
+    return args, q_out
+
+
+def paged_kv_write_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                        inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                        v_cache: torch.Tensor, *, interleaved: bool = False, amplitude: float = 1.0,
+                        q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotate a step's ``q [T, Hq, D]`` and ``k [T, Hkv, D]`` to ``positions
+    [T]`` (int64) and scatter ``k`` and ``v`` into the pools at
+    ``slot_mapping`` (< 0 skips), in one pass; returns the rotated q.
+
+    ``inv_freq`` (float64 ``[rotary_dim / 2]``, see ``rope_frequencies``) sets
+    how much of a head is rotated: elements from rotary_dim on are copied.
+    Pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) with ``interleaved``.
+    q, k and v may be views with a token stride (a fused projection);
+    ``q_out`` may be ``q`` itself when q is contiguous."""
+    dev = _need_cuda(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
+    if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
+        raise ValueError("q, k, v, k_cache, v_cache must share dtype bfloat16 or float32")
+    args, q_out = _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude,
+                             q_out, dev)
+    with torch.cuda.device(dev):
+        _check(lib().paged_kv_write_rope(*args, _stream(dev)))
+    return q_out
+
+
+def paged_kv_write_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                            inv_freq: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, k_scale: float, v_scale: float, *, interleaved: bool = False,
+                            amplitude: float = 1.0, q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """``paged_kv_write_rope`` into FP8 pools: the codes are those of the
+    rotated fp32 values, encoded as ``paged_kv_write_fp8`` does."""
+    dev = _need_cuda(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
+    _check_fp8_pools(k_cache, v_cache)
+    args, q_out = _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude,
+                             q_out, dev)
+    with torch.cuda.device(dev):
+        _check(lib().paged_kv_write_rope_fp8(*args, float(k_scale), float(v_scale), _stream(dev)))
+    return q_out
+
+
+# ----------------------------------------------------------------------------
+# keeping the cache within a budget (include/paged_kv_budget.h)
+# ----------------------------------------------------------------------------
+
+def scores_workspace_size(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                          max_context: int) -> int:
+    return int(lib().paged_attention_scores_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                           max_context))
+
+
+def scores_workspace_min(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int,
+                         max_context: int) -> int:
+    return int(lib().paged_attention_scores_workspace_min(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                          max_context))
+
+
+def _check_scores(scores, Hkv, score_rows, B) -> None:
+    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[1] != Hkv or not scores.is_contiguous():
+        raise ValueError(f"scores must be contiguous float32 [num_rows, {Hkv}, max_len]")
+    if score_rows is not None:
+        if score_rows.dtype != torch.int32 or tuple(score_rows.shape) != (B,) or not score_rows.is_contiguous():
+            raise ValueError("score_rows must be contiguous int32 [num_seqs]")
+    elif scores.shape[0] < B:
+        raise ValueError("scores has fewer rows than the batch has sequences (pass score_rows)")
+
+
+def _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay, score_rows,
+                 out, workspace, max_query_len, dev):
+    """Checks paged_attention_scores' tensors; returns (its C arguments up to
+    the decay, (workspace, bytes), out)."""
+    if q.dim() != 3 or not q.is_contiguous():
+        raise ValueError("q must be contiguous [T, Hq, D]")
+    if k_cache.dim() != 4 or not k_cache.is_contiguous():
+        raise ValueError("the cache must be contiguous [num_blocks, block_size, num_kv_heads, head_dim]")
+    T, Hq, D = q.shape
+    NB, bs, Hkv, Dk = k_cache.shape
+    if Dk != D:
+        raise ValueError("head_dim of q and the cache differ")
+    B = context_lens.shape[0]
+    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B or \
+            (B > 0 and block_tables.shape[1] == 0) or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq > 0")
+    for name, t, n in (("context_lens", context_lens, B), ("query_start_loc", query_start_loc, B + 1)):
+        if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int32 [{n}]")
+    _check_scores(scores, Hkv, score_rows, B)
+    if out is None:
+        out = scores
+    elif out.shape != scores.shape or out.dtype != scores.dtype or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be contiguous and match scores")
+    width = max(1, block_tables.shape[1])
+    context = min(scores.shape[2], width * bs)
+    if workspace is None:
+        workspace = _workspace(dev, scores_workspace_size(B, T, Hq, Hkv, context))
+    elif workspace.dtype != torch.uint8 or workspace.device != dev or \
+            workspace.numel() < scores_workspace_min(B, T, Hq, Hkv, context):
+        raise ValueError("workspace must be a uint8 CUDA tensor of at least scores_workspace_min bytes")
+    args = (q.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            query_start_loc.data_ptr(), None if score_rows is None else score_rows.data_ptr(), scores.data_ptr(),
+            out.data_ptr(), B, T, Hq, Hkv, D, NB, bs, width, scores.shape[0], scores.shape[2], int(max_query_len),
+            float(scale), 1 if causal else 0, float(decay))
+    return args, (workspace.data_ptr(), workspace.numel()), out
+
+
+def paged_attention_scores(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                           context_lens: torch.Tensor, query_start_loc: torch.Tensor, scores: torch.Tensor,
+                           scale: float, causal: bool = True, *, decay: float = 1.0,
+                           score_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, max_query_len: int = 0) -> torch.Tensor:
+    """Add the attention weight that ``q [T, Hq, D]`` pays to each cached
+    token to the running ``scores`` (float32 ``[num_rows, Hkv, max_len]``).
+
+    ``scores[row, h, j]`` becomes ``decay`` times itself plus the softmax
+    weights of cache position j, summed over the sequence's queries and the q
+    heads of kv head h; at the positions of the step's own tokens (the last
+    ones) it becomes that sum alone.  ``score_rows`` (int32 ``[num_seqs]``)
+    names each sequence's row (default: its place in the batch; < 0 leaves it
+    out).  The result goes to ``out`` (default: ``scores``, in place); entries
+    past a sequence's length are left as they were.  The other arguments are
+    ``paged_attention_forward``'s; ``workspace`` (uint8, >=
+    ``scores_workspace_min``) defaults to the cached buffer per (device, stream)."""
+    dev = _need_cuda(q, k_cache, block_tables, context_lens, query_start_loc, scores)
+    if score_rows is not None:
+        _need_cuda(q, score_rows)
+    if q.dtype not in DTYPE or k_cache.dtype != q.dtype:
+        raise ValueError("q and k_cache must share dtype bfloat16 or float32")
+    with torch.cuda.device(dev):
+        args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal,
+                                     decay, score_rows, out, workspace, max_query_len, dev)
+        _check(lib().paged_attention_scores(*args, *ws, DTYPE[q.dtype], _stream(dev)))
+    return out
+
+
+def paged_attention_scores_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
+                                 context_lens: torch.Tensor, query_start_loc: torch.Tensor, scores: torch.Tensor,
+                                 scale: float, k_scale: float, causal: bool = True, *, decay: float = 1.0,
+                                 score_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                                 workspace: torch.Tensor | None = None, max_query_len: int = 0) -> torch.Tensor:
+    """``paged_attention_scores`` over an FP8 K pool read as code * k_scale
+    (q bf16, head_dim 128)."""
+    dev = _need_cuda(q, k_cache, block_tables, context_lens, query_start_loc, scores)
+    if score_rows is not None:
+        _need_cuda(q, score_rows)
+    _check_fp8_pools(k_cache, k_cache)
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bfloat16 with an FP8 cache")
+    with torch.cuda.device(dev):
+        args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal,
+                                     decay, score_rows, out, workspace, max_query_len, dev)
+        _check(lib().paged_attention_scores_fp8kv(*args, float(k_scale), *ws, _stream(dev)))
+    return out
+
+
+def paged_kv_select(scores: torch.Tensor, context_lens: torch.Tensor, budget: int, *, num_sink: int = 0,
+                    num_recent: int = 0, score_rows: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The positions ``budget`` keeps of each (sequence, kv head): int32
+    ``[num_seqs, Hkv, budget]``, ascending, then -1.
+
+    All of a sequence's L positions when L <= budget; else the first
+    ``num_sink``, the last ``num_recent`` and the highest-scored between (ties
+    to the lowest position)."""
+    dev = _need_cuda(scores, context_lens)
+    if context_lens.dtype != torch.int32 or context_lens.dim() != 1 or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be contiguous int32 [num_seqs]")
+    B = context_lens.shape[0]
+    if scores.dim() != 3:
+        raise ValueError("scores must be contiguous float32 [num_rows, num_kv_heads, max_len]")
+    _check_scores(scores, scores.shape[1], score_rows, B)
+    if score_rows is not None:
+        _need_cuda(scores, score_rows)
+    shape = (B, scores.shape[1], int(budget))
+    if out is None:
+        out = torch.empty((B, scores.shape[1], max(int(budget), 0)), dtype=torch.int32, device=dev)
+    elif tuple(out.shape) != shape or out.dtype != torch.int32 or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out must be contiguous int32 {list(shape)}")
+    with torch.cuda.device(dev):
+        _check(lib().paged_kv_select(scores.data_ptr(), None if score_rows is None else score_rows.data_ptr(),
+                                     context_lens.data_ptr(), out.data_ptr(), B, scores.shape[1], scores.shape[0],
+                                     scores.shape[2], int(budget), int(num_sink), int(num_recent), _stream(dev)))
+    return out
+
+
+_POOL_DTYPE = dict(DTYPE)
+_POOL_DTYPE.update({t: 2 for t in _FP8_TYPES})
+
+
+def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, kept: torch.Tensor, *,
+                     dst_block_tables: torch.Tensor | None = None, scores: torch.Tensor | None = None,
+                     score_rows: torch.Tensor | None = None) -> None:
+    """Move the kept tokens of each (sequence, kv head) to the front of its
+    cache: position r becomes what position ``kept[s, h, r]`` was, in K, V
+    and, if given, the running ``scores``.
+
+    ``kept`` is ``paged_kv_select``'s int32 ``[num_seqs, Hkv, budget]``.  The
+    rows go to ``dst_block_tables`` (default: in place): each of its blocks is
+    the same entry of ``block_tables`` or a block no sequence of the call
+    reads, as ``BlockManager.compact`` returns.  Pools are bf16, f32 or FP8."""
+    dev = _need_cuda(k_cache, v_cache, block_tables, kept)
+    for t in (dst_block_tables, scores, score_rows):
+        if t is not None:
+            _need_cuda(k_cache, t)
+    if k_cache.dtype not in _POOL_DTYPE or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must share dtype bfloat16, float32 or FP8 (uint8, float8_e4m3fn)")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() or \
+            not v_cache.is_contiguous():
+        raise ValueError("caches must be contiguous [num_blocks, block_size, num_kv_heads, head_dim]")
+    NB, bs, Hkv, D = k_cache.shape
+    if kept.dtype != torch.int32 or kept.dim() != 3 or kept.shape[1] != Hkv or not kept.is_contiguous():
+        raise ValueError(f"kept must be contiguous int32 [num_seqs, {Hkv}, budget]")
+    B = kept.shape[0]
+    for name, t in (("block_tables", block_tables), ("dst_block_tables", dst_block_tables)):
+        if t is not None and (t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous() or
+                              t.shape[1] != block_tables.shape[1] or (B > 0 and t.shape[1] == 0)):
+            raise ValueError(f"{name} must be contiguous int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq > 0")
+    rows = length = 0
+    if scores is not None:
+        _check_scores(scores, Hkv, score_rows, B)
+        rows, length = scores.shape[0], scores.shape[2]
+    ptr = lambda t: None if t is None else t.data_ptr()
+    with torch.cuda.device(dev):
+        _check(lib().paged_kv_compact(k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                                      ptr(dst_block_tables), kept.data_ptr(), ptr(score_rows), ptr(scores), B, Hkv, D,
+                                      NB, bs, max(1, block_tables.shape[1]), kept.shape[2], rows, length,
+                                      _POOL_DTYPE[k_cache.dtype], _stream(dev)))

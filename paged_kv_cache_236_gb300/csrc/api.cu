@@ -135,6 +135,17 @@ namespace pkv {
 
 void set_last_error(const char* msg) { snprintf(g_msg, sizeof(g_msg), "%s", msg); }
 
+pkv_status device_state(int* sms, int** err) {
+  DeviceInfo* d = nullptr;
+  const pkv_status st = device_info(&d);
+  if (st != PKV_OK) return st;
+  *sms = d->sms;
+  *err = d->err;
+  return PKV_OK;
+}
+
+pkv_status cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
 WorkspaceLayout workspace_layout(int B, int64_t T, int Hq, int Hkv, int D, size_t bytes_available, int /*num_sms*/,
                                  bool want_default_parts) {
   WorkspaceLayout L{};

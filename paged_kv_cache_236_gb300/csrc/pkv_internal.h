@@ -10,6 +10,8 @@
 
 #include <utility>
 
+#include "paged_kv.h"
+
 namespace pkv {
 
 // Rows of one kv head of one sequence are (query token i, head-in-group g)
@@ -216,6 +218,13 @@ cudaError_t launch_dectc_fp8(const AttnParams& p, int rows, const CUtensorMap& q
 
 // Sets the thread-local message pkv_last_error returns.
 void set_last_error(const char* msg);
+
+// The current device's SM count and the address of its sticky error word
+// (checks that the device is an sm_103a one).
+pkv_status device_state(int* sms, int** err);
+
+// Sets the message to `what` and the error's name; returns PKV_ERR_CUDA.
+pkv_status cuda_error(cudaError_t e, const char* what);
 
 // Shared-memory bytes of the CUDA-core kernel, and its resident CTAs per SM
 // (also sets the kernel's shared-memory opt-in on the current device).

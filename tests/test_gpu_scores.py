@@ -1,0 +1,308 @@
+"""paged_attention_scores and its FP8 form against the fp64 definition.
+
+Tolerance.  A logit (in log2 units) is a dot product of D terms, summed in
+fp32 in any order, times a constant: it is off by at most
+  e = scale * log2(e) * (D + 2) * 2^-24 * sum |q k|.
+A weight is exp2 of a logit less the row's log-sum-exp, itself as far off, so
+its relative error is at most 2 ln2 e plus the exponentials' (2^-22 each, two of
+them) and the sums' (each running sum of up to 512 terms, rescaled with
+exponentials: 512 * 2^-22 < 1.3e-4).  Weights below 2^-126 flush to zero.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_236_gb300 as pkv
+import workloads as wl
+from gpu_util import to_f64
+from oracle import budget as ob
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+
+class Batch:
+    """A ragged batch over a shuffled pool whose other slots are NaN."""
+
+    def __init__(self, seed, lens, qlens, Hq, Hkv, D, bs, dtype=torch.bfloat16, f8=False, gain=1.5, rows=None,
+                 max_len=None, extra_blocks=3):
+        rng = np.random.default_rng(seed)
+        need = [-(-L // bs) for L in lens]
+        NB = sum(need) + extra_blocks
+        order = rng.permutation(NB)
+        self.tables = np.full((len(lens), max(max(need, default=1), 1)), -1, np.int32)
+        at = 0
+        for s, c in enumerate(need):
+            self.tables[s, :c] = order[at:at + c]
+            at += c
+        pool = rng.standard_normal((NB, bs, Hkv, D)).astype(np.float32)
+        live = np.zeros((NB, bs), bool)
+        for s, L in enumerate(lens):
+            for j in range(L):
+                live[self.tables[s, j // bs], j % bs] = True
+        self.k_scale = 0.011 if f8 else 1.0
+        if f8:
+            codes = fp8.quantize(pool, self.k_scale)
+            codes[~live] = 0x7F
+            self.kc = torch.from_numpy(codes).cuda()
+            self.K = fp8.dequantize(codes, self.k_scale)
+        else:
+            pool[~live] = np.nan
+            self.kc = torch.from_numpy(pool).to(dtype).cuda()
+            self.K = to_f64(self.kc)
+        T = int(sum(qlens))
+        self.q = torch.from_numpy((gain * rng.standard_normal((T, Hq, D))).astype(np.float32)).to(dtype).cuda()
+        self.lens, self.qlens, self.bs, self.Hq, self.Hkv, self.D, self.f8 = lens, qlens, bs, Hq, Hkv, D, f8
+        self.qsl = np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+        self.scale = 1 / math.sqrt(D)
+        self.rows = list(range(len(lens))) if rows is None else rows
+        self.old = torch.from_numpy(rng.random((max(self.rows, default=0) + 2, Hkv,
+                                                max_len or max(lens, default=1) + 5)).astype(np.float32) * 3).cuda()
+        dev = lambda a: torch.from_numpy(np.asarray(a, np.int32)).cuda()  # noqa: E731
+        self.args = dict(block_tables=dev(self.tables), context_lens=dev(lens), query_start_loc=dev(self.qsl))
+        self.row_arg = None if rows is None else dev(rows)
+
+    def run(self, causal=True, decay=1.0, out=None, q=None, **kw):
+        args = {**self.args, **kw}
+        q = self.q if q is None else q
+        scores = args.pop("scores", self.old)
+        if self.f8:
+            return pkv.paged_attention_scores_fp8kv(q, self.kc, args.pop("block_tables"), args.pop("context_lens"),
+                                                    args.pop("query_start_loc"), scores, self.scale, self.k_scale,
+                                                    causal, decay=decay, score_rows=self.row_arg, out=out, **args)
+        return pkv.paged_attention_scores(q, self.kc, args.pop("block_tables"), args.pop("context_lens"),
+                                          args.pop("query_start_loc"), scores, self.scale, causal, decay=decay,
+                                          score_rows=self.row_arg, out=out, **args)
+
+    def keys(self, s):
+        L = self.lens[s]
+        return self.K[self.tables[s, :-(-L // self.bs)]].reshape(-1, self.Hkv, self.D)[:L]
+
+    def check(self, got, before, old=None, causal=True, decay=1.0, seqs=None):
+        got, before = got.cpu().numpy(), before.cpu().numpy()
+        old = before if old is None else old.cpu().numpy()
+        want_all = before.astype(np.float64)
+        tol_all = np.zeros_like(want_all)
+        qf = to_f64(self.q)
+        for s, L in enumerate(self.lens):
+            r, n = self.rows[s], self.qlens[s]
+            if r < 0 or n == 0 or (seqs is not None and s not in seqs):
+                continue
+            q, K = qf[self.qsl[s]:self.qsl[s + 1]], self.keys(s)
+            w = ob.scores_update(q, K, old[r, :, :L], self.scale, causal, decay)
+            dots = np.abs(q).reshape(-1, self.D).max(0) @ np.abs(K).reshape(-1, self.D).max(0)
+            rel = 2 * self.scale * (self.D + 2) * 2.0 ** -24 * dots + 2 * 2.0 ** -22 + 1.3e-4
+            paid = ob.scores_update(q, K, old[r, :, :L], self.scale, causal, 0.0)
+            want_all[r, :, :L] = w
+            tol_all[r, :, :L] = rel * paid + 2.0 ** -22 * w + n * self.Hq * 2.0 ** -120
+            total = got[r, :, :L].astype(np.float64).sum() - (decay * old[r, :, :L - n].astype(np.float64)).sum()
+            assert total == pytest.approx(n * self.Hq, rel=2e-4, abs=1e-3 * max(1.0, L * self.Hkv * 2e-4))
+        err = np.abs(got - want_all)
+        assert np.all(np.isfinite(got)) and np.all(err <= tol_all), float((err - tol_all).max())
+
+
+SHAPES = [  # Hq, Hkv, D, bs
+    (8, 2, 128, 16), (4, 4, 64, 8), (16, 2, 128, 32), (14, 2, 64, 64), (6, 2, 128, 64), (32, 1, 128, 16),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda c: "-".join(map(str, c)))
+def test_ragged_batches(shape, dtype):
+    Hq, Hkv, D, bs = shape
+    if dtype == "fp8" and D != 128:
+        pytest.skip("FP8 pools: head_dim 128")
+    b = Batch(Hq * D + bs, [1, 2, 300, 129, 64, 517, 40, 0, 33], [1, 2, 1, 5, 1, 40, 40, 0, 3], Hq, Hkv, D, bs,
+              torch.float32 if dtype == "f32" else torch.bfloat16, dtype == "fp8")
+    for causal, decay in ((True, 1.0), (True, 0.0), (False, 0.5)):
+        before = b.old.clone()
+        got = b.run(causal, decay, out=b.old.clone())
+        assert torch.equal(b.old, before)
+        b.check(got, before, causal=causal, decay=decay)
+    assert pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("group", [1, 2, 3, 4, 8, 16])
+def test_decode(group, dtype, hint):
+    """Single tokens, one length on each side of the tiles' edges."""
+    lens = [1, 15, 16, 17, 127, 128, 129, 255, 256, 257, 1000]
+    b = Batch(group, lens, [1] * len(lens), 2 * group, 2, 128, 16,
+              torch.float32 if dtype == "f32" else torch.bfloat16, dtype == "fp8")
+    before = b.old.clone()
+    b.check(b.run(max_query_len=hint), before)
+    assert pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+def test_long_context_and_large_logits(dtype):
+    """A 20 000-key context, logits up to about +-40: most weights underflow."""
+    b = Batch(5, [20000, 7000], [1, 4], 8, 2, 128, 16, f8=dtype == "fp8", gain=12.0)
+    before = b.old.clone()
+    b.check(b.run(decay=0.5), before, decay=0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("n,L", [(33, 700), (64, 64), (128, 2000), (200, 1111), (513, 600)])
+def test_many_queries(n, L, dtype):
+    if dtype != "bf16" and n > 200:
+        pytest.skip("covered by bf16")
+    b = Batch(n, [L, 50], [n, 1], 8, 2, 128, 16, torch.float32 if dtype == "f32" else torch.bfloat16, dtype == "fp8")
+    before = b.old.clone()
+    b.check(b.run(), before)
+
+
+def test_chunk_equals_steps():
+    """Scores of a prompt's tokens: all queries at once, or one step after
+    another with decay 1, add up to the same."""
+    b = Batch(21, [40], [40], 4, 2, 64, 8, torch.float32)
+    whole = b.run(decay=0.0, out=torch.zeros_like(b.old))
+    step = torch.full_like(b.old, 7.0)  # stale scores of other tokens
+    one = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for i in range(40):
+        b.run(q=b.q[i:i + 1].contiguous(), scores=step, context_lens=torch.tensor([i + 1], dtype=torch.int32, device="cuda"),
+              query_start_loc=one)
+    # fp32 sums of up to 40 weights below 1 each, and each weight within 1.3e-4 + 2^-21
+    assert torch.allclose(step[0, :, :40], whole[0, :, :40], rtol=3e-4, atol=1e-6)
+    assert torch.all(step[0, :, 40:] == 7.0)
+
+
+def test_rows_left_out_and_shared_blocks():
+    """score_rows: permuted, -1 (left out), out of range (flagged); blocks
+    that two sequences share are scored in each one's own row."""
+    b = Batch(31, [100, 60, 200, 30], [1, 3, 1, 2], 8, 2, 128, 16, rows=[3, -1, 0, 1])
+    b.tables[2, :3] = b.tables[0, :3]
+    b.args["block_tables"] = torch.from_numpy(b.tables).cuda()
+    before = b.old.clone()
+    b.check(b.run(), before)
+    assert pkv.device_errors() == 0
+    b.row_arg = torch.tensor([3, -1, 0, b.old.shape[0]], dtype=torch.int32, device="cuda")
+    b.rows = [3, -1, 0, -1]
+    before = b.old.clone()
+    b.check(b.run(), before)
+    assert pkv.device_errors() == pkv.DEVERR["bad_sequence"]
+
+
+def test_invalid_metadata():
+    """Bad sequences leave their rows as they were; an out-of-pool block
+    reads as zeros; nothing faults."""
+    b = Batch(41, [100, 60, 80, 50], [1, 2, 1, 1], 8, 2, 128, 16)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    for kw, good in ((dict(context_lens=i32([100, 1, 80, 50])), [0, 2, 3]),          # more queries than tokens
+                     (dict(context_lens=i32([100, 60, 81 * 16, 50])), [0, 1, 3]),    # past its table
+                     (dict(context_lens=i32([100, 60, -4, 50])), [0, 1, 3]),
+                     (dict(query_start_loc=i32([0, 1, 3, 4, 9])), [0, 1, 2]),        # past q
+                     (dict(query_start_loc=i32([0, 4, 0, 4, 5])), [3])):             # overlapping queries
+        before = b.old.clone()
+        if kw.get("query_start_loc") is not None and len(good) == 1:
+            got = b.run(out=b.old.clone(), **kw)
+            assert torch.equal(got[1:3], before[1:3])
+            pkv.device_errors()
+            continue
+        got = b.run(out=b.old.clone(), **kw)
+        b.check(got, before, seqs=good)
+        assert pkv.device_errors() == pkv.DEVERR["bad_sequence"], kw
+    short = b.old[:, :, :70].contiguous()
+    before = short.clone()
+    got = b.run(scores=short)
+    b.check(got, before, seqs=[1, 3])
+    assert pkv.device_errors() == pkv.DEVERR["bad_sequence"]
+    # a block of zeros in place of an id outside the pool
+    for bad in (-1, b.kc.shape[0], 2 ** 31 - 1):
+        t = b.tables.copy()
+        t[0, 2] = bad
+        keep = b.K.copy()
+        b.K = np.concatenate([b.K, np.zeros((1,) + b.K.shape[1:])])
+        held, b.tables = b.tables, t.copy()
+        b.tables[0, 2] = len(keep)
+        before = b.old.clone()
+        b.check(b.run(out=b.old.clone(), block_tables=torch.from_numpy(t).cuda()), before)
+        assert pkv.device_errors() == pkv.DEVERR["block_out_of_range"]
+        b.K, b.tables = keep, held
+
+
+def test_nan_in_masked_places():
+    """NaN old scores count only where they are read: at the step's own
+    tokens, and everywhere with decay 0, they are overwritten."""
+    b = Batch(51, [90, 90], [2, 1], 4, 1, 128, 16)
+    b.old[:, :, 88:] = float("nan")
+    got = b.run(out=torch.zeros_like(b.old))
+    assert torch.isfinite(got[0, :, :90]).all() and torch.isnan(got[1, :, 88]).all()
+    b.old.fill_(float("nan"))
+    got = b.run(decay=0.0)
+    assert torch.isfinite(got[:2, :, :90]).all() and torch.isnan(got[:2, :, 90:]).all()
+
+
+def test_same_bits_each_time_and_workspaces():
+    """Equal calls give equal bits, with the least workspace too the same
+    numbers; back-to-back calls share the cached workspace."""
+    b = Batch(61, [3000, 500, 40, 1500], [1, 1, 40, 4], 8, 2, 128, 16)
+    T = b.q.shape[0]
+    first = b.run(out=torch.zeros_like(b.old)).clone()
+    for _ in range(3):
+        assert torch.equal(b.run(out=torch.zeros_like(b.old)), first)
+    context = min(b.old.shape[2], b.tables.shape[1] * 16)
+    need = pkv.scores_workspace_min(4, T, 8, 2, context)
+    small = b.run(out=torch.zeros_like(b.old), workspace=torch.empty(need, dtype=torch.uint8, device="cuda"))
+    assert torch.allclose(small, first, rtol=5e-4, atol=1e-7)
+    with pytest.raises(ValueError):
+        b.run(workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+    other = Batch(62, [700, 900], [3, 1], 8, 2, 128, 16)
+    want = other.run(out=torch.zeros_like(other.old)).clone()
+    for _ in range(10):
+        x = b.run(out=torch.zeros_like(b.old))
+        y = other.run(out=torch.zeros_like(other.old))
+    assert torch.equal(x, first) and torch.equal(y, want)
+
+
+def test_graph_replay_follows_its_inputs():
+    """A captured step replayed with longer sequences and other queries."""
+    b = Batch(71, [300, 900], [1, 1], 8, 2, 128, 16)
+    ctx = torch.tensor([100, 200], dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(b.old)
+    ws = torch.empty(pkv.scores_workspace_size(2, 2, 8, 2, 1 << 10), dtype=torch.uint8, device="cuda")
+    b.run(out=out, context_lens=ctx, workspace=ws, max_query_len=1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.run(out=out, context_lens=ctx, workspace=ws, max_query_len=1)
+    for lens in ([300, 900], [1, 17], [257, 128]):
+        ctx.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.copy_(b.old)
+        g.replay()
+        torch.cuda.synchronize()
+        held, b.lens = b.lens, lens
+        b.check(out, b.old)
+        b.lens = held
+
+
+def test_other_stream():
+    b = Batch(81, [5000, 300], [1, 1], 8, 2, 128, 16)
+    want = b.run(out=torch.zeros_like(b.old)).clone()
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = b.run(out=torch.zeros_like(b.old))
+    st.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_refusals():
+    b = Batch(91, [30], [1], 4, 2, 64, 16)
+    for bad in (dict(scores=b.old.double()), dict(scores=b.old[:, :1]), dict(scores=b.old[0]), dict(q=b.q.float()),
+                dict(context_lens=b.args["context_lens"].long()), dict(block_tables=b.args["block_tables"].long()),
+                dict(query_start_loc=b.args["query_start_loc"][:1]), dict(scores=b.old.transpose(1, 2)),
+                dict(out=b.old[:1]), dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                dict(q=b.q.cpu()), dict(score_rows=torch.zeros(2, dtype=torch.int32, device="cuda"))):
+        if "score_rows" in bad:
+            b.row_arg, bad = bad["score_rows"], {}
+        with pytest.raises(ValueError):
+            b.run(**bad)
+        b.row_arg = None
+    with pytest.raises(pkv.LibraryError):
+        b.run(decay=-1.0)
+    assert torch.equal(b.run(q=b.q[:0], out=torch.zeros_like(b.old),
+                             query_start_loc=torch.zeros(2, dtype=torch.int32, device="cuda")), torch.zeros_like(b.old))
