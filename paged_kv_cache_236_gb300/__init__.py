@@ -698,6 +698,35 @@ def rope_amplitude(factor: float) -> float:
     return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device_of(*tensors: torch.Tensor) -> int:
+    """The CUDA device index all the tensors share (None entries are skipped)."""
+    dev = -1
+    for t in tensors:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError("all tensors must be CUDA tensors (no CPU path)")
+        i = t.get_device()
+        if dev < 0:
+            dev = i
+        elif i != dev:
+            raise ValueError("all tensors must be on the same device")
+    return dev
+
+
+def _call(fn, dev: int, *args) -> None:
+    """fn(*args, the current stream of device dev) with dev current."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return _call(fn, dev, *args)
+    status = fn(*args, _raw_stream(dev) if _raw_stream else _stream(torch.device("cuda", dev)))
+    if status != PKV_OK:
+        _check(status)
+
+
 def _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude, q_out, dev):
     """Checks paged_kv_write_rope's tensors; returns (its C arguments up to
     the dtype, q_out)."""
@@ -705,24 +734,30 @@ def _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, int
             not v_cache.is_contiguous():
         raise ValueError("caches must be contiguous [num_blocks, block_size, num_kv_heads, head_dim]")
     NB, bs, Hkv, D = k_cache.shape
-    if q.dtype not in DTYPE or q.dim() != 3 or q.shape[2] != D or q.stride(2) != 1 or q.stride(1) != D:
-        raise ValueError(f"q must be bfloat16 or float32 [T, Hq, {D}] with contiguous heads")
-    T, ks, vs = _new_rows(k, v, slot_mapping, Hkv, D, {q.dtype})
-    if q.shape[0] != T:
-        raise ValueError("q, k and v differ in their number of tokens")
+    dtype, shape, qs, ks, vs = q.dtype, q.shape, q.stride(), k.stride(), v.stride()
+    if dtype not in DTYPE or k.dtype != dtype or v.dtype != dtype:
+        raise ValueError("q, k and v must share dtype bfloat16 or float32")
+    T = shape[0] if len(shape) == 3 else -1
+    if T < 0 or shape[2] != D or qs[2] != 1 or qs[1] != D:
+        raise ValueError(f"q must be [T, Hq, {D}] with contiguous heads")
+    rows = (T, Hkv, D)
+    if k.shape != rows or v.shape != rows or ks[2] != 1 or ks[1] != D or vs[2] != 1 or vs[1] != D:
+        raise ValueError(f"k and v must be [{T}, {Hkv}, {D}] with contiguous heads")
     if positions.shape != (T,) or positions.dtype != torch.int64 or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int64 [T]")
+    if slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous int64 [T]")
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() or \
             not 0 < 2 * inv_freq.shape[0] <= D:
         raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2] with rotary_dim <= head_dim")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    elif q_out.shape != q.shape or q_out.dtype != q.dtype or not q_out.is_contiguous() or q_out.device != dev:
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    elif q_out.shape != shape or q_out.dtype != dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
         raise ValueError("q_out must be contiguous and match q")
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
-            slot_mapping.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, NB, bs, q.shape[1],
-            Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, float(amplitude), q.stride(0) if T else 0, ks, vs,
-            DTYPE[q.dtype])
+            slot_mapping.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, NB, bs, shape[1],
+            Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude, qs[0] if T else 0, ks[0] if T else 0,
+            vs[0] if T else 0, DTYPE[dtype])
     return args, q_out
 
 
@@ -739,13 +774,12 @@ def paged_kv_write_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, posit
     Pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) with ``interleaved``.
     q, k and v may be views with a token stride (a fused projection);
     ``q_out`` may be ``q`` itself when q is contiguous."""
-    dev = _need_cuda(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
+    dev = _device_of(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
     if k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise ValueError("q, k, v, k_cache, v_cache must share dtype bfloat16 or float32")
     args, q_out = _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude,
                              q_out, dev)
-    with torch.cuda.device(dev):
-        _check(lib().paged_kv_write_rope(*args, _stream(dev)))
+    _call(lib().paged_kv_write_rope, dev, *args)
     return q_out
 
 
@@ -755,12 +789,11 @@ def paged_kv_write_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, p
                             amplitude: float = 1.0, q_out: torch.Tensor | None = None) -> torch.Tensor:
     """``paged_kv_write_rope`` into FP8 pools: the codes are those of the
     rotated fp32 values, encoded as ``paged_kv_write_fp8`` does."""
-    dev = _need_cuda(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
+    dev = _device_of(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache)
     _check_fp8_pools(k_cache, v_cache)
     args, q_out = _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude,
                              q_out, dev)
-    with torch.cuda.device(dev):
-        _check(lib().paged_kv_write_rope_fp8(*args, float(k_scale), float(v_scale), _stream(dev)))
+    _call(lib().paged_kv_write_rope_fp8, dev, *args, k_scale, v_scale)
     return q_out
 
 
@@ -780,51 +813,58 @@ def scores_workspace_min(num_seqs: int, num_tokens: int, num_q_heads: int, num_k
                                                           max_context))
 
 
-def _check_scores(scores, Hkv, score_rows, B) -> None:
-    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[1] != Hkv or not scores.is_contiguous():
-        raise ValueError(f"scores must be contiguous float32 [num_rows, {Hkv}, max_len]")
+def _check_scores(scores, Hkv, score_rows, B) -> tuple:
+    """Checks the running scores and their rows; returns scores' shape."""
+    shape = scores.shape
+    if scores.dtype != torch.float32 or len(shape) != 3 or (Hkv is not None and shape[1] != Hkv) or \
+            not scores.is_contiguous():
+        raise ValueError("scores must be contiguous float32 [num_rows, num_kv_heads, max_len]")
     if score_rows is not None:
-        if score_rows.dtype != torch.int32 or tuple(score_rows.shape) != (B,) or not score_rows.is_contiguous():
+        if score_rows.dtype != torch.int32 or score_rows.shape != (B,) or not score_rows.is_contiguous():
             raise ValueError("score_rows must be contiguous int32 [num_seqs]")
-    elif scores.shape[0] < B:
+    elif shape[0] < B:
         raise ValueError("scores has fewer rows than the batch has sequences (pass score_rows)")
+    return shape
 
 
 def _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay, score_rows,
                  out, workspace, max_query_len, dev):
     """Checks paged_attention_scores' tensors; returns (its C arguments up to
     the decay, (workspace, bytes), out)."""
-    if q.dim() != 3 or not q.is_contiguous():
+    qs, pool, table = q.shape, k_cache.shape, block_tables.shape
+    if len(qs) != 3 or not q.is_contiguous():
         raise ValueError("q must be contiguous [T, Hq, D]")
-    if k_cache.dim() != 4 or not k_cache.is_contiguous():
+    if len(pool) != 4 or not k_cache.is_contiguous():
         raise ValueError("the cache must be contiguous [num_blocks, block_size, num_kv_heads, head_dim]")
-    T, Hq, D = q.shape
-    NB, bs, Hkv, Dk = k_cache.shape
+    T, Hq, D = qs
+    NB, bs, Hkv, Dk = pool
     if Dk != D:
         raise ValueError("head_dim of q and the cache differ")
+    if context_lens.dtype != torch.int32 or context_lens.dim() != 1 or not context_lens.is_contiguous():
+        raise ValueError("context_lens must be contiguous int32 [num_seqs]")
     B = context_lens.shape[0]
-    if block_tables.dtype != torch.int32 or block_tables.dim() != 2 or block_tables.shape[0] != B or \
-            (B > 0 and block_tables.shape[1] == 0) or not block_tables.is_contiguous():
+    if block_tables.dtype != torch.int32 or len(table) != 2 or table[0] != B or (B > 0 and table[1] == 0) or \
+            not block_tables.is_contiguous():
         raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq > 0")
-    for name, t, n in (("context_lens", context_lens, B), ("query_start_loc", query_start_loc, B + 1)):
-        if t.dtype != torch.int32 or tuple(t.shape) != (n,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous int32 [{n}]")
-    _check_scores(scores, Hkv, score_rows, B)
+    if query_start_loc.dtype != torch.int32 or query_start_loc.shape != (B + 1,) or \
+            not query_start_loc.is_contiguous():
+        raise ValueError(f"query_start_loc must be contiguous int32 [{B + 1}]")
+    rows, _, length = _check_scores(scores, Hkv, score_rows, B)
     if out is None:
         out = scores
-    elif out.shape != scores.shape or out.dtype != scores.dtype or not out.is_contiguous() or out.device != dev:
+    elif out.shape != scores.shape or out.dtype != scores.dtype or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be contiguous and match scores")
-    width = max(1, block_tables.shape[1])
-    context = min(scores.shape[2], width * bs)
+    width = max(1, table[1])
+    context = min(length, width * bs)
     if workspace is None:
-        workspace = _workspace(dev, scores_workspace_size(B, T, Hq, Hkv, context))
-    elif workspace.dtype != torch.uint8 or workspace.device != dev or \
+        workspace = _workspace(q.device, scores_workspace_size(B, T, Hq, Hkv, context))
+    elif workspace.dtype != torch.uint8 or workspace.get_device() != dev or \
             workspace.numel() < scores_workspace_min(B, T, Hq, Hkv, context):
         raise ValueError("workspace must be a uint8 CUDA tensor of at least scores_workspace_min bytes")
     args = (q.data_ptr(), k_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
             query_start_loc.data_ptr(), None if score_rows is None else score_rows.data_ptr(), scores.data_ptr(),
-            out.data_ptr(), B, T, Hq, Hkv, D, NB, bs, width, scores.shape[0], scores.shape[2], int(max_query_len),
-            float(scale), 1 if causal else 0, float(decay))
+            out.data_ptr(), B, T, Hq, Hkv, D, NB, bs, width, rows, length, int(max_query_len),
+            scale, 1 if causal else 0, decay)
     return args, (workspace.data_ptr(), workspace.numel()), out
 
 
@@ -845,15 +885,12 @@ def paged_attention_scores(q: torch.Tensor, k_cache: torch.Tensor, block_tables:
     past a sequence's length are left as they were.  The other arguments are
     ``paged_attention_forward``'s; ``workspace`` (uint8, >=
     ``scores_workspace_min``) defaults to the cached buffer per (device, stream)."""
-    dev = _need_cuda(q, k_cache, block_tables, context_lens, query_start_loc, scores)
-    if score_rows is not None:
-        _need_cuda(q, score_rows)
+    dev = _device_of(q, k_cache, block_tables, context_lens, query_start_loc, scores, score_rows)
     if q.dtype not in DTYPE or k_cache.dtype != q.dtype:
         raise ValueError("q and k_cache must share dtype bfloat16 or float32")
-    with torch.cuda.device(dev):
-        args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal,
-                                     decay, score_rows, out, workspace, max_query_len, dev)
-        _check(lib().paged_attention_scores(*args, *ws, DTYPE[q.dtype], _stream(dev)))
+    args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay,
+                                 score_rows, out, workspace, max_query_len, dev)
+    _call(lib().paged_attention_scores, dev, *args, *ws, DTYPE[q.dtype])
     return out
 
 
@@ -864,16 +901,13 @@ def paged_attention_scores_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, block_t
                                  workspace: torch.Tensor | None = None, max_query_len: int = 0) -> torch.Tensor:
     """``paged_attention_scores`` over an FP8 K pool read as code * k_scale
     (q bf16, head_dim 128)."""
-    dev = _need_cuda(q, k_cache, block_tables, context_lens, query_start_loc, scores)
-    if score_rows is not None:
-        _need_cuda(q, score_rows)
+    dev = _device_of(q, k_cache, block_tables, context_lens, query_start_loc, scores, score_rows)
     _check_fp8_pools(k_cache, k_cache)
     if q.dtype != torch.bfloat16:
         raise ValueError("q must be bfloat16 with an FP8 cache")
-    with torch.cuda.device(dev):
-        args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal,
-                                     decay, score_rows, out, workspace, max_query_len, dev)
-        _check(lib().paged_attention_scores_fp8kv(*args, float(k_scale), *ws, _stream(dev)))
+    args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay,
+                                 score_rows, out, workspace, max_query_len, dev)
+    _call(lib().paged_attention_scores_fp8kv, dev, *args, k_scale, *ws)
     return out
 
 
@@ -886,24 +920,19 @@ def paged_kv_select(scores: torch.Tensor, context_lens: torch.Tensor, budget: in
     All of a sequence's L positions when L <= budget; else the first
     ``num_sink``, the last ``num_recent`` and the highest-scored between (ties
     to the lowest position)."""
-    dev = _need_cuda(scores, context_lens)
+    dev = _device_of(scores, context_lens, score_rows)
     if context_lens.dtype != torch.int32 or context_lens.dim() != 1 or not context_lens.is_contiguous():
         raise ValueError("context_lens must be contiguous int32 [num_seqs]")
     B = context_lens.shape[0]
-    if scores.dim() != 3:
-        raise ValueError("scores must be contiguous float32 [num_rows, num_kv_heads, max_len]")
-    _check_scores(scores, scores.shape[1], score_rows, B)
-    if score_rows is not None:
-        _need_cuda(scores, score_rows)
-    shape = (B, scores.shape[1], int(budget))
+    rows, Hkv, length = _check_scores(scores, None, score_rows, B)
+    budget = int(budget)
     if out is None:
-        out = torch.empty((B, scores.shape[1], max(int(budget), 0)), dtype=torch.int32, device=dev)
-    elif tuple(out.shape) != shape or out.dtype != torch.int32 or not out.is_contiguous() or out.device != dev:
-        raise ValueError(f"out must be contiguous int32 {list(shape)}")
-    with torch.cuda.device(dev):
-        _check(lib().paged_kv_select(scores.data_ptr(), None if score_rows is None else score_rows.data_ptr(),
-                                     context_lens.data_ptr(), out.data_ptr(), B, scores.shape[1], scores.shape[0],
-                                     scores.shape[2], int(budget), int(num_sink), int(num_recent), _stream(dev)))
+        out = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=scores.device)
+    elif out.shape != (B, Hkv, budget) or out.dtype != torch.int32 or not out.is_contiguous() or \
+            out.get_device() != dev:
+        raise ValueError(f"out must be contiguous int32 {[B, Hkv, budget]}")
+    _call(lib().paged_kv_select, dev, scores.data_ptr(), None if score_rows is None else score_rows.data_ptr(),
+          context_lens.data_ptr(), out.data_ptr(), B, Hkv, rows, length, budget, int(num_sink), int(num_recent))
     return out
 
 
@@ -922,30 +951,26 @@ def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     rows go to ``dst_block_tables`` (default: in place): each of its blocks is
     the same entry of ``block_tables`` or a block no sequence of the call
     reads, as ``BlockManager.compact`` returns.  Pools are bf16, f32 or FP8."""
-    dev = _need_cuda(k_cache, v_cache, block_tables, kept)
-    for t in (dst_block_tables, scores, score_rows):
-        if t is not None:
-            _need_cuda(k_cache, t)
-    if k_cache.dtype not in _POOL_DTYPE or v_cache.dtype != k_cache.dtype:
+    dev = _device_of(k_cache, v_cache, block_tables, kept, dst_block_tables, scores, score_rows)
+    pool, table, dtype = k_cache.shape, block_tables.shape, k_cache.dtype
+    if dtype not in _POOL_DTYPE or v_cache.dtype != dtype:
         raise ValueError("k_cache and v_cache must share dtype bfloat16, float32 or FP8 (uint8, float8_e4m3fn)")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() or \
-            not v_cache.is_contiguous():
+    if len(pool) != 4 or v_cache.shape != pool or not k_cache.is_contiguous() or not v_cache.is_contiguous():
         raise ValueError("caches must be contiguous [num_blocks, block_size, num_kv_heads, head_dim]")
-    NB, bs, Hkv, D = k_cache.shape
+    NB, bs, Hkv, D = pool
     if kept.dtype != torch.int32 or kept.dim() != 3 or kept.shape[1] != Hkv or not kept.is_contiguous():
         raise ValueError(f"kept must be contiguous int32 [num_seqs, {Hkv}, budget]")
-    B = kept.shape[0]
-    for name, t in (("block_tables", block_tables), ("dst_block_tables", dst_block_tables)):
-        if t is not None and (t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or not t.is_contiguous() or
-                              t.shape[1] != block_tables.shape[1] or (B > 0 and t.shape[1] == 0)):
-            raise ValueError(f"{name} must be contiguous int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq > 0")
+    B, _, budget = kept.shape
+    if block_tables.dtype != torch.int32 or len(table) != 2 or table[0] != B or (B > 0 and table[1] == 0) or \
+            not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [num_seqs, max_blocks_per_seq], max_blocks_per_seq > 0")
+    if dst_block_tables is not None and (dst_block_tables.dtype != torch.int32 or dst_block_tables.shape != table or
+                                         not dst_block_tables.is_contiguous()):
+        raise ValueError("dst_block_tables must be contiguous int32 of block_tables' shape")
     rows = length = 0
     if scores is not None:
-        _check_scores(scores, Hkv, score_rows, B)
-        rows, length = scores.shape[0], scores.shape[2]
-    ptr = lambda t: None if t is None else t.data_ptr()
-    with torch.cuda.device(dev):
-        _check(lib().paged_kv_compact(k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                                      ptr(dst_block_tables), kept.data_ptr(), ptr(score_rows), ptr(scores), B, Hkv, D,
-                                      NB, bs, max(1, block_tables.shape[1]), kept.shape[2], rows, length,
-                                      _POOL_DTYPE[k_cache.dtype], _stream(dev)))
+        rows, _, length = _check_scores(scores, Hkv, score_rows, B)
+    _call(lib().paged_kv_compact, dev, k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+          None if dst_block_tables is None else dst_block_tables.data_ptr(), kept.data_ptr(),
+          None if score_rows is None else score_rows.data_ptr(), None if scores is None else scores.data_ptr(), B, Hkv,
+          D, NB, bs, max(1, table[1]), budget, rows, length, _POOL_DTYPE[dtype])

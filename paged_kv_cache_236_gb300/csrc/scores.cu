@@ -5,12 +5,26 @@
 //   paid[j] = sum_r exp2(z[r][j] - lse[r]),   z = scale * log2(e) * q K^T,
 //   lse[r] = log2 sum_j exp2(z[r][j]),
 // with the causal mask at each row's position.  A row's normaliser needs all
-// its keys before any weight is known, so the keys are passed over twice:
-//   plan     per sequence: checks, and the offsets of its work and partials;
-//   stats    (max, sum) of each row over each chunk of keys;
-//   columns  lse from the chunks' (max, sum), then the weights, summed over
-//            the rows key by key, and the score update.
+// its keys before any weight is known, so the keys are passed over twice.
+//
+// plan_scores_kernel (one block) checks each sequence and lays out its work:
+//
+// Few rows (at most 16: decode, short verify windows): few_kernel, one launch
+// for both passes.  HBM-bound on K, which is read once: the logits are kept
+// (4 bytes a row and key, 16 bytes next to K's 256 for a group of 4 in bf16)
+// and the second pass reads them back from L2.  Work units belong to warps,
+// taken from one queue: first all stats units (a head's chunk of keys: logits,
+// and each row's (max, sum) over the chunk; the warp that completes a head's
+// last chunk combines them to the row's lse), then all column units (weights
+// summed over the rows, the score update).  A column unit waits for its
+// head's lse; every stats unit was taken earlier by a warp that is running,
+// so the wait ends, and it is bounded all the same.
+//
+// Other rows: stats_kernel, lse_kernel, columns_kernel, which compute the
+// logits twice.
+//
 // Every sum has a fixed order (no float atomics).
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 #include <math_constants.h>
@@ -24,15 +38,23 @@
 namespace pkv {
 namespace {
 
-constexpr int kChunk = 256;   // keys of a work unit
-constexpr int kRowGroup = 8;  // rows of a work unit
+constexpr int kFewRows = 16;    // rows of a few-row sequence's kv head
+constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
+constexpr int kColChunk = 256;  // keys of a column unit (few rows)
+constexpr int kChunk = 256;   // keys of a work unit (other rows)
+constexpr int kRowGroup = 8;  // rows of a work unit (other rows)
 constexpr int kThreads = 256;
+constexpr int kFewThreads = 128;
+
+// Offsets of each sequence's work, as prefix sums: the unit queues of the
+// kernels below (few-row stats and columns; other rows' stats and columns),
+// the partial (max, sum)s, the lse rows and the kept logits.
+enum { kFewStat, kFewCol, kStat, kCol, kPart, kLse, kLogit, kOffsets };
 
 struct SeqPlan {
-  int64_t stat_unit;  // first stats unit
-  int64_t col_unit;   // first columns unit
-  int64_t part;       // first partial (max, sum)
+  int64_t part, lse, logit;
   int L, n, row, chunks;
+  int rows, pad;  // rows of a kv head; rows a key's logits are padded to (few rows)
 };
 
 struct ScoreParams {
@@ -44,28 +66,60 @@ struct ScoreParams {
   const int32_t* rows;
   const float* scores;
   float* out;
-  SeqPlan* plan;   // [B + 1]; the last entry holds the totals
-  float2* part;    // (m, l) per (kv head, row, chunk) of a sequence
-  float* lse;      // [T, Hq]
+  int64_t* off[4];  // [B + 1] each: first unit of each sequence in the four queues
+  SeqPlan* plan;    // [B]
+  int* tickets;     // [B, Hkv] chunks done, then [B, Hkv] lse ready, then the few-row queue's counter
+  float2* part;     // (m, l) per (kv head, row, chunk) of a sequence
+  float* lse;       // per (kv head, row) of a sequence
+  float* logit;     // per (kv head, key, padded row) of a few-row sequence
+  int64_t logit_cap;
   int64_t T, num_blocks;
-  int B, Hq, Hkv, G, bs, max_blocks, num_rows, max_len, causal;
+  int B, Hq, Hkv, G, bs, bs_log, max_blocks, num_rows, max_len, causal;
   float scale_log2, decay;
   int* err;
 };
 
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Exclusive prefix sum of v over the block, plus *carry, which moves on.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* carry, int lane, int warp) {
+  const int64_t x = warp_scan(v, lane);
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    const int64_t w = warp_sums[lane], y = warp_scan(w, lane);
+    warp_sums[lane] = *carry + y - w;
+    __syncwarp();
+    if (lane == 31) *carry += y;
+  }
+  __syncthreads();
+  const int64_t r = warp_sums[warp] + x - v;
+  __syncthreads();
+  return r;
+}
+
 __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) {
-  __shared__ int64_t part[3][32];
-  __shared__ int64_t carry[3];
+  __shared__ int64_t sums[32];
+  __shared__ int64_t carry[kOffsets];
   __shared__ int top[32];
   __shared__ int top_carry;  // the largest query_start_loc entry so far
+  pdl_launch_dependents();  // few_kernel waits for this grid first of all
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < 3) carry[tid] = 0;
-  if (tid == 3) top_carry = 0;
+  if (tid < kOffsets) carry[tid] = 0;
+  if (tid == 0) top_carry = 0;
+  for (int64_t i = tid; i < 2 * (int64_t)p.B * p.Hkv + 1; i += 1024) p.tickets[i] = 0;
   __syncthreads();
   for (int s0 = 0; s0 < p.B; s0 += 1024) {
     const int s = s0 + tid;
-    int L = 0, n = 0, row = -1, chunks = 0;
-    int64_t v[3] = {0, 0, 0};
+    SeqPlan sp{};
+    sp.row = -1;
     // a sequence whose queries start below an earlier entry is invalid: the
     // valid ones' query ranges are disjoint, and so are their partials
     const int a = s < p.B ? p.qsl[s] : 0;
@@ -80,71 +134,470 @@ __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) 
     for (int w = 0; w < warp; ++w) high = max(high, top[w]);
     high = max(high, top_carry);
     if (s < p.B) {
-      const int b = p.qsl[s + 1];
-      L = p.lens[s];
-      n = b - a;
-      row = p.rows ? p.rows[s] : s;
+      const int b = p.qsl[s + 1], L = p.lens[s], n = b - a;
+      sp.row = p.rows ? p.rows[s] : s;
       const bool bad = a < high || a < 0 || n < 0 || b > p.T || L < 0 || n > L || L > p.max_len ||
-                       L > (int64_t)p.max_blocks * p.bs || row >= p.num_rows;
-      if (bad && row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
-      if (bad || row < 0 || n == 0) L = n = 0;
-      chunks = (L + kChunk - 1) / kChunk;
-      const int64_t rows = (int64_t)n * p.G;
-      v[0] = (int64_t)p.Hkv * ((rows + kRowGroup - 1) / kRowGroup) * chunks;
-      v[1] = (int64_t)p.Hkv * chunks;
-      v[2] = (int64_t)p.Hkv * rows * chunks;
-    }
-    int64_t ex[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      int64_t x = v[k];
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      ex[k] = x - v[k];
-      if (lane == 31) part[k][warp] = x;
-    }
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        const int64_t w = part[k][lane];
-        int64_t x = w;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-          if (lane >= d) x += y;
-        }
-        part[k][lane] = carry[k] + x - w;
-        if (lane == 31) carry[k] += x;
+                       L > (int64_t)p.max_blocks * p.bs || sp.row >= p.num_rows;
+      if (bad && sp.row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
+      if (!bad && sp.row >= 0 && n > 0) {
+        sp.L = L;
+        sp.n = n;
+        sp.rows = n * p.G;  // n <= L <= 2^30 only for a batch of as many tokens: T * Hq fits 31 bits
       }
     }
-    __syncthreads();
+    const bool want_few = sp.n > 0 && sp.rows <= kFewRows;
+    const int pad = sp.rows <= 2 ? 2 : sp.rows <= 4 ? 4 : sp.rows <= 8 ? 8 : 16;
+    const int64_t logits = want_few ? (int64_t)p.Hkv * sp.L * pad : 0;
+    sp.logit = block_scan(logits, sums, &carry[kLogit], lane, warp);
+    const bool few = want_few && sp.logit + logits <= p.logit_cap;
+    sp.pad = few ? pad : 0;
+    const int chunk = few ? kFewChunk : kChunk;
+    sp.chunks = (sp.L + chunk - 1) / chunk;
+    const int64_t groups = (sp.rows + kRowGroup - 1) / kRowGroup, work = (int64_t)p.Hkv * sp.chunks;
+    const int64_t units[4] = {few ? work : 0, few ? (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk) : 0,
+                              few ? 0 : work * groups, few ? 0 : work};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t at = block_scan(units[k], sums, &carry[k], lane, warp);
+      if (s < p.B) p.off[k][s] = at;
+    }
+    sp.part = block_scan(work * sp.rows, sums, &carry[kPart], lane, warp);
+    sp.lse = block_scan((int64_t)p.Hkv * sp.rows, sums, &carry[kLse], lane, warp);
+    if (s < p.B) p.plan[s] = sp;
     if (tid == 1023) top_carry = high;
-    if (s < p.B)
-      p.plan[s] = SeqPlan{part[0][warp] + ex[0], part[1][warp] + ex[1], part[2][warp] + ex[2], L, n, row, chunks};
     __syncthreads();
   }
-  if (tid == 0) p.plan[p.B] = SeqPlan{carry[0], carry[1], carry[2], 0, 0, -1, 0};
+  if (tid < 4) p.off[tid][p.B] = carry[tid];
 }
 
-// The sequence whose units hold unit u (kCol: columns units).
-template <bool kCol>
-__device__ __forceinline__ int find_seq(const ScoreParams& p, int64_t u) {
-  int lo = 0, hi = p.B;  // plan[lo] <= u < plan[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    const int64_t at = kCol ? p.plan[mid].col_unit : p.plan[mid].stat_unit;
-    if (at <= u)
-      lo = mid;
-    else
-      hi = mid;
+// The sequence s with off[s] <= u < off[s + 1] (the whole warp calls it).
+__device__ __forceinline__ int find_seq(const int64_t* off, int B, int64_t u, int lane) {
+  int lo = 0, len = B;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < len && __ldg(off + i) <= u);
+    const int k = 31 - __clz(le);  // lane 0 always holds
+    const int skip = k * step;
+    lo += skip;
+    len = min(step, len - skip);
   }
   return lo;
 }
 
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+// Logits of 16 keys against 8 or 16 rows on one warp, in the accumulator
+// layout of mma.m16n8k16: lane (g = lane / 4, t = lane % 4) holds keys g and
+// g + 8, rows 2t and 2t + 1 (and 8 more of each with two row tiles).
+//
+// The contraction may run over d in any order, so lane t of a key takes whole
+// 16-byte pieces of its row, straight from global memory to the fragment
+// registers, and the q fragments follow the same order: no shared memory.
+
+__device__ __forceinline__ uint4 ld_row16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// bf16 rows: 16-byte piece c of lane t is d = 32 c + 8 t .. + 7, two k-steps.
+template <int D>
+struct DotBf16 {
+  static constexpr int kPieces = D / 32;   // 16-byte pieces of a key a lane holds
+  static constexpr int kPieceStride = 64;  // bytes between them
+  static constexpr int kRowBytes = D * 2;
+  static constexpr int kQBytes = D * 2;
+  static constexpr bool kAhead = true;     // a tile is loaded while another is in use
+  template <int NT>
+  struct Q {
+    uint4 w[NT][kPieces];
+  };
+  template <int NT>
+  __device__ static void load_q(Q<NT>& q, int nt, const void* row, int t) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+      q.w[nt][c] = row ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + c * 64 + t * 16))
+                       : make_uint4(0, 0, 0, 0);
+  }
+  template <int NT>
+  __device__ static void dot(float (&acc)[NT][4], const uint4 (&k0)[kPieces], const uint4 (&k1)[kPieces], const Q<NT>& q) {
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_bf16(acc[nt], k0[c].x, k1[c].x, k0[c].y, k1[c].y, q.w[nt][c].x, q.w[nt][c].y);
+        mma_bf16(acc[nt], k0[c].z, k1[c].z, k0[c].w, k1[c].w, q.w[nt][c].z, q.w[nt][c].w);
+      }
+  }
+};
+
+// E4M3 rows (D = 128): piece c of lane t is d = 64 c + 16 t .. + 15, four
+// k-steps; codes are exact in fp16, and so is a bf16 q of ordinary magnitude
+// (|q| < 65504; bits below 2^-24 are rounded away).
+struct DotFp8 {
+  static constexpr int kPieces = 2;
+  static constexpr int kPieceStride = 64;
+  static constexpr int kRowBytes = 128;
+  static constexpr int kQBytes = 256;
+  static constexpr bool kAhead = true;
+  template <int NT>
+  struct Q {
+    uint32_t w[NT][16];
+  };
+  template <int NT>
+  __device__ static void load_q(Q<NT>& q, int nt, const void* row, int t) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 v = row ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + (c >> 1) * 128 + t * 32 +
+                                                                 (c & 1) * 16))
+                          : make_uint4(0, 0, 0, 0);
+      q.w[nt][4 * c + 0] = bf16x2_to_f16x2(v.x);
+      q.w[nt][4 * c + 1] = bf16x2_to_f16x2(v.y);
+      q.w[nt][4 * c + 2] = bf16x2_to_f16x2(v.z);
+      q.w[nt][4 * c + 3] = bf16x2_to_f16x2(v.w);
+    }
+  }
+  template <int NT>
+  __device__ static void dot(float (&acc)[NT][4], const uint4 (&k0)[2], const uint4 (&k1)[2], const Q<NT>& q) {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t x0[4] = {k0[c].x, k0[c].y, k0[c].z, k0[c].w}, x1[4] = {k1[c].x, k1[c].y, k1[c].z, k1[c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = codes_to_f16(x0[i] & 0xffffu), a2 = codes_to_f16(x0[i] >> 16);
+        const uint32_t a1 = codes_to_f16(x1[i] & 0xffffu), a3 = codes_to_f16(x1[i] >> 16);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(acc[nt], a0, a1, a2, a3, q.w[nt][8 * c + 2 * i], q.w[nt][8 * c + 2 * i + 1]);
+      }
+    }
+  }
+};
+
+// fp32 rows: no tensor-core format keeps fp32 products, so FMAs; piece c of
+// lane t is d = 16 c + 4 t .. + 3, summed over the quad at the end.  q is read
+// per piece (it stays in L1).
+template <int D>
+struct DotF32 {
+  static constexpr int kPieces = D / 16;
+  static constexpr int kPieceStride = 64;
+  static constexpr int kRowBytes = D * 4;
+  static constexpr int kQBytes = D * 4;
+  static constexpr bool kAhead = false;
+  template <int NT>
+  struct Q {
+    const float* row[NT];  // this lane's row g of each tile, exchanged by shuffles
+    int t;
+  };
+  template <int NT>
+  __device__ static void load_q(Q<NT>& q, int nt, const void* row, int t) {
+    q.row[nt] = static_cast<const float*>(row);
+    q.t = t;
+  }
+  template <int NT>
+  __device__ static void dot(float (&acc)[NT][4], const uint4 (&k0)[kPieces], const uint4 (&k1)[kPieces], const Q<NT>& q) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float* row = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q.row[nt]), r * 4));
+        float x0 = 0.f, x1 = 0.f;
+        if (row) {
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(row + 16 * c + 4 * q.t));
+            x0 = fmaf(__uint_as_float(k0[c].x), w.x, x0);
+            x1 = fmaf(__uint_as_float(k1[c].x), w.x, x1);
+            x0 = fmaf(__uint_as_float(k0[c].y), w.y, x0);
+            x1 = fmaf(__uint_as_float(k1[c].y), w.y, x1);
+            x0 = fmaf(__uint_as_float(k0[c].z), w.z, x0);
+            x1 = fmaf(__uint_as_float(k1[c].z), w.z, x1);
+            x0 = fmaf(__uint_as_float(k0[c].w), w.w, x0);
+            x1 = fmaf(__uint_as_float(k1[c].w), w.w, x1);
+          }
+          x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
+          x1 += __shfl_xor_sync(0xffffffffu, x1, 1);
+          x0 += __shfl_xor_sync(0xffffffffu, x0, 2);
+          x1 += __shfl_xor_sync(0xffffffffu, x1, 2);
+        }
+        if ((r >> 1) == q.t) {
+          acc[nt][r & 1] = x0;
+          acc[nt][2 + (r & 1)] = x1;
+        }
+      }
+  }
+};
+
+// A key's logits against `rows` padded rows start at (kv head, key) * pad.
+template <typename Dot, int NT>
+__device__ __forceinline__ void few_stats(const ScoreParams& p, const SeqPlan& sp, int s, int h, int c, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  const int qstart = p.qsl[s];
+  typename Dot::template Q<NT> q;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int r = nt * 8 + g, i = r / p.G;
+    const void* row = r < sp.rows ? static_cast<const uint8_t*>(p.q) +
+                                        ((int64_t)(qstart + i) * p.Hq + h * p.G + (r - i * p.G)) * Dot::kQBytes
+                                  : nullptr;
+    Dot::load_q(q, nt, row, t);
+  }
+  // rows of this lane: nt * 8 + 2t and + 1; keys they see
+  int vis[NT][2];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * t + e;
+      vis[nt][e] = p.causal ? min(sp.L, sp.L - sp.n + r / p.G + 1) : sp.L;
+      m[nt][e] = -CUDART_INF_F;
+      l[nt][e] = 0.f;
+    }
+  const int kb = c * kFewChunk, ke = min(sp.L, kb + kFewChunk);
+  // block ids of the chunk, one a lane (kFewChunk / bs <= 16)
+  const int nblk = (ke - kb + p.bs - 1) / p.bs;
+  int blk = -1;
+  if (lane < nblk) {
+    blk = p.tables[(int64_t)s * p.max_blocks + kb / p.bs + lane];
+    if (blk < 0 || blk >= p.num_blocks) {
+      raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+      blk = -1;
+    }
+  }
+  const uint8_t* base = static_cast<const uint8_t*>(p.kc) + (int64_t)h * Dot::kRowBytes + t * 16;
+  const int64_t token_bytes = (int64_t)p.Hkv * Dot::kRowBytes;
+  auto load = [&](int j, uint4 (&k)[Dot::kPieces]) {  // key j's pieces; zeros past the end or outside the pool
+    const int rel = j - kb;
+    const int b = __shfl_sync(0xffffffffu, blk, (rel >> p.bs_log) & 31);
+    const bool ok = j < ke && b >= 0;
+    const uint8_t* src = base + (((int64_t)b << p.bs_log) + (j & (p.bs - 1))) * token_bytes;
+#pragma unroll
+    for (int i = 0; i < Dot::kPieces; ++i) k[i] = ok ? ld_row16(src + i * Dot::kPieceStride) : make_uint4(0, 0, 0, 0);
+  };
+  float* zout = p.logit + sp.logit + (int64_t)h * sp.L * sp.pad;
+  auto use = [&](int j, const uint4 (&k0)[Dot::kPieces], const uint4 (&k1)[Dot::kPieces]) {
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+    Dot::dot(acc, k0, k1, q);
+    const int ja = j + g, jb = j + g + 8;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float za[2], zb[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        za[e] = ja < vis[nt][e] ? acc[nt][e] * p.scale_log2 : -CUDART_INF_F;
+        zb[e] = jb < vis[nt][e] ? acc[nt][2 + e] * p.scale_log2 : -CUDART_INF_F;
+        const float mn = fmax3(m[nt][e], za[e], zb[e]);
+        const float mu = mn == -CUDART_INF_F ? 0.f : mn;
+        l[nt][e] = l[nt][e] * fast_exp2(m[nt][e] - mu) + (fast_exp2(za[e] - mu) + fast_exp2(zb[e] - mu));
+        m[nt][e] = mn;
+      }
+      const int r = nt * 8 + 2 * t;
+      if (r < sp.pad) {
+        if (ja < ke) *reinterpret_cast<float2*>(zout + (int64_t)ja * sp.pad + r) = make_float2(za[0], za[1]);
+        if (jb < ke) *reinterpret_cast<float2*>(zout + (int64_t)jb * sp.pad + r) = make_float2(zb[0], zb[1]);
+      }
+    }
+  };
+  // two tiles of 16 keys a turn, one in use while the other is loaded
+  uint4 ka[2][Dot::kPieces], kc[2][Dot::kPieces];
+  load(kb + g, ka[0]);
+  load(kb + g + 8, ka[1]);
+#pragma unroll 1
+  for (int j = kb; j < ke; j += 32) {
+    if constexpr (Dot::kAhead) {
+      if (j + 16 < ke) {
+        load(j + 16 + g, kc[0]);
+        load(j + 24 + g, kc[1]);
+      }
+      use(j, ka[0], ka[1]);
+      if (j + 32 < ke) {
+        load(j + 32 + g, ka[0]);
+        load(j + 40 + g, ka[1]);
+      }
+      if (j + 16 < ke) use(j + 16, kc[0], kc[1]);
+    } else {
+      use(j, ka[0], ka[1]);
+      if (j + 16 < ke) {
+        load(j + 16 + g, ka[0]);
+        load(j + 24 + g, ka[1]);
+        use(j + 16, ka[0], ka[1]);
+      }
+      if (j + 32 < ke) {
+        load(j + 32 + g, ka[0]);
+        load(j + 40 + g, ka[1]);
+      }
+    }
+  }
+  // over the 8 lanes (keys) that share a row
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float mm = m[nt][e];
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+      float ll = l[nt][e] * fast_exp2(m[nt][e] - (mm == -CUDART_INF_F ? 0.f : mm));
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+      const int r = nt * 8 + 2 * t + e;
+      if (g == 0 && r < sp.rows) p.part[sp.part + ((int64_t)h * sp.rows + r) * sp.chunks + c] = make_float2(mm, ll);
+    }
+}
+
+// lse of one row from its chunks' (max, sum), on a whole warp; 0 for a row
+// without a finite logit (none of its weights is taken).
+__device__ __forceinline__ float row_lse(const float2* part, int chunks, int lane) {
+  float m = -CUDART_INF_F, l = 0.f;
+  for (int c = lane; c < chunks; c += 32) m = fmaxf(m, __ldcg(part + c).x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  for (int c = lane; c < chunks; c += 32) {
+    const float2 v = __ldcg(part + c);
+    l += v.x == -CUDART_INF_F ? 0.f : v.y * fast_exp2(v.x - m);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  return m + log2f(l);
+}
+
+template <int PAD>
+__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int c, int lane) {
+  float lse[PAD];
+#pragma unroll
+  for (int r = 0; r < PAD; ++r)
+    lse[r] = r < sp.rows ? __ldcg(p.lse + sp.lse + (int64_t)h * sp.rows + r) : CUDART_INF_F;  // padding weighs 0
+  const float* z = p.logit + sp.logit + (int64_t)h * sp.L * PAD;
+  const int ke = min(sp.L, (c + 1) * kColChunk);
+  const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len;
+#pragma unroll 2
+  for (int j = c * kColChunk + lane; j < ke; j += 32) {
+    float x[PAD];
+    if constexpr (PAD == 2) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(z + (int64_t)j * 2));
+      x[0] = v.x;
+      x[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < PAD / 4; ++i) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(z + (int64_t)j * PAD) + i);
+        x[4 * i] = v.x;
+        x[4 * i + 1] = v.y;
+        x[4 * i + 2] = v.z;
+        x[4 * i + 3] = v.w;
+      }
+    }
+    float paid = 0.f;
+#pragma unroll
+    for (int r = 0; r < PAD; ++r) paid += fast_exp2(x[r] - lse[r]);
+    if (j < sp.L - sp.n && p.decay != 0.f) paid = fmaf(p.decay, p.scores[at + j], paid);
+    p.out[at + j] = paid;
+  }
+}
+
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(int* p, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// NT: tiles of 8 rows (1 where every sequence has at most 8 rows).
+template <typename Dot, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) few_kernel(const ScoreParams p) {
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t n_stat = __ldg(p.off[kFewStat] + p.B), n_all = n_stat + __ldg(p.off[kFewCol] + p.B);
+  int* ticket = p.tickets;
+  int* ready = p.tickets + (int64_t)p.B * p.Hkv;
+  int* queue = ready + (int64_t)p.B * p.Hkv;
+  int64_t next = 0;
+  if (lane == 0) next = atomicAdd(queue, 1);
+  for (;;) {
+    const int64_t u = __shfl_sync(0xffffffffu, next, 0);
+    if (u >= n_all) break;
+    if (lane == 0) next = atomicAdd(queue, 1);
+    const bool stat = u < n_stat;
+    const int64_t* off = stat ? p.off[kFewStat] : p.off[kFewCol];
+    const int64_t v = stat ? u : u - n_stat;
+    const int s = find_seq(off, p.B, v, lane);
+    const SeqPlan sp = p.plan[s];
+    // heads innermost: neighbouring warps read neighbouring parts of the same tokens' rows
+    const int w = (int)(v - __ldg(off + s));
+    const int c = w / p.Hkv, h = w - c * p.Hkv;
+    const int64_t sh = (int64_t)s * p.Hkv + h;
+    if (stat) {
+      few_stats<Dot, NT>(p, sp, s, h, c, lane);
+      __threadfence();
+      __syncwarp();
+      int done = 0;
+      if (lane == 0) done = atomicAdd(ticket + sh, 1);
+      if (__shfl_sync(0xffffffffu, done, 0) == sp.chunks - 1) {
+        __threadfence();
+        for (int r = 0; r < sp.rows; ++r) {
+          const float x = row_lse(p.part + sp.part + ((int64_t)h * sp.rows + r) * sp.chunks, sp.chunks, lane);
+          if (lane == 0) p.lse[sp.lse + (int64_t)h * sp.rows + r] = x;
+        }
+        __syncwarp();
+        if (lane == 0) st_release(ready + sh, 1);
+      }
+    } else {
+      bool ok = true;
+      if (lane == 0) {
+        const uint64_t t0 = globaltimer();
+        while (ld_acquire(ready + sh) == 0) {
+          if (globaltimer() - t0 > kWaitTimeoutNs) {
+            raise_error(p.err, PKV_DEVERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, (int)ok, 0)) continue;
+      __syncwarp();
+      switch (sp.pad) {
+        case 2: few_columns<2>(p, sp, h, c, lane); break;
+        case 4: few_columns<4>(p, sp, h, c, lane); break;
+        case 8: few_columns<8>(p, sp, h, c, lane); break;
+        default: few_columns<16>(p, sp, h, c, lane); break;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// other rows
+// ---------------------------------------------------------------------------
 // E of a lane's consecutive elements of a row, as fp32.
 template <typename T, int E>
 __device__ __forceinline__ void load_row(const T* p, float (&x)[E]) {
@@ -220,12 +673,12 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const ScoreParams p) {
   using X = Tile<TQ, TK, D>;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int64_t total = p.plan[p.B].stat_unit;
+  const int64_t total = p.off[kStat][p.B];
   for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < total; u += warps) {
-    const int s = find_seq<false>(p, u);
+    const int s = find_seq(p.off[kStat], p.B, u, lane);
     const SeqPlan sp = p.plan[s];
-    const int rows = sp.n * p.G, groups = (rows + kRowGroup - 1) / kRowGroup;
-    int64_t v = u - sp.stat_unit;
+    const int rows = sp.rows, groups = (rows + kRowGroup - 1) / kRowGroup;
+    int64_t v = u - p.off[kStat][s];
     const int c = (int)(v % sp.chunks);
     v /= sp.chunks;
     const int rg = (int)(v % groups), h = (int)(v / groups);
@@ -253,30 +706,13 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const ScoreParams p) {
 // lse of each row (one warp a row).
 __global__ void __launch_bounds__(kThreads) lse_kernel(const ScoreParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  for (int64_t w = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; w < p.T * p.Hq; w += warps) {
-    const int t = (int)(w / p.Hq), hq = (int)(w - (int64_t)t * p.Hq);
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.qsl[mid] <= t)
-        lo = mid;
-      else
-        hi = mid;
+  for (int s = 0; s < p.B; ++s) {
+    const SeqPlan sp = p.plan[s];
+    if (sp.pad != 0 || sp.n == 0) continue;
+    for (int w = (blockIdx.x * kThreads + threadIdx.x) >> 5; w < p.Hkv * sp.rows; w += (gridDim.x * kThreads) >> 5) {
+      const float x = row_lse(p.part + sp.part + (int64_t)w * sp.chunks, sp.chunks, lane);
+      if (lane == 0) p.lse[sp.lse + w] = x;
     }
-    const SeqPlan sp = p.plan[lo];
-    const int i = t - p.qsl[lo];
-    if (i < 0 || i >= sp.n) continue;
-    const int rows = sp.n * p.G, h = hq / p.G, row = i * p.G + (hq - h * p.G);
-    const float2* part = p.part + sp.part + ((int64_t)h * rows + row) * sp.chunks;
-    float m = -CUDART_INF_F, l = 0.f;
-    for (int c = lane; c < sp.chunks; c += 32) m = fmaxf(m, part[c].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    for (int c = lane; c < sp.chunks; c += 32) l += part[c].y * fast_exp2(part[c].x - m);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    if (lane == 0) p.lse[w] = m + log2f(l);
   }
 }
 
@@ -285,12 +721,12 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const ScoreParams p) 
   using X = Tile<TQ, TK, D>;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const int64_t total = p.plan[p.B].col_unit;
+  const int64_t total = p.off[kCol][p.B];
   for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < total; u += warps) {
-    const int s = find_seq<true>(p, u);
+    const int s = find_seq(p.off[kCol], p.B, u, lane);
     const SeqPlan sp = p.plan[s];
-    const int rows = sp.n * p.G, groups = (rows + kRowGroup - 1) / kRowGroup;
-    const int64_t v = u - sp.col_unit;
+    const int rows = sp.rows, groups = (rows + kRowGroup - 1) / kRowGroup;
+    const int64_t v = u - p.off[kCol][s];
     const int c = (int)(v % sp.chunks), h = (int)(v / sp.chunks);
     const int32_t* bt = p.tables + (int64_t)s * p.max_blocks;
     const int qstart = p.qsl[s];
@@ -303,7 +739,7 @@ __global__ void __launch_bounds__(kThreads) columns_kernel(const ScoreParams p) 
         const int row = rg * kRowGroup + (lane >> 2);
         const int i = row / p.G;
         const int vis = row >= rows ? 0 : p.causal ? sp.L - sp.n + i + 1 : sp.L;
-        const float lse = row < rows ? p.lse[(int64_t)(qstart + i) * p.Hq + h * p.G + (row - i * p.G)] : 0.f;
+        const float lse = row < rows ? p.lse[sp.lse + (int64_t)h * rows + row] : 0.f;
         for (int j = 0; j < nk; ++j) {
           float k[X::E];
           X::load_k(p, bt, j0 + j, h, lane, k);
@@ -333,28 +769,77 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  size_t plan, lse, part, total;
+  size_t off[4], plan, tickets, lse, part, logit, least, total;
 };
 
-Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t keys) {
+// Kept logits: at most 16 padded rows of each kv head, or twice the rows
+// there are, times the keys; no more than kLogitMax is asked for.
+constexpr size_t kLogitMax = (size_t)512 << 20;
+
+Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   Layout l{};
-  const size_t chunks = (size_t)((keys + kChunk - 1) / kChunk);
-  l.plan = 0;
-  l.lse = align_up((size_t)(B + 1) * sizeof(SeqPlan));
-  l.part = align_up(l.lse + (size_t)(T * Hq) * sizeof(float));
-  l.total = align_up(l.part + (size_t)(T * Hq) * chunks * sizeof(float2));
+  size_t at = 0;
+  for (int k = 0; k < 4; ++k) {
+    l.off[k] = at;
+    at = align_up(at + (size_t)(B + 1) * sizeof(int64_t));
+  }
+  l.plan = at;
+  at = align_up(at + (size_t)B * sizeof(SeqPlan));
+  l.tickets = at;
+  at = align_up(at + (size_t)(2 * B * Hkv + 1) * sizeof(int));
+  l.lse = at;
+  at = align_up(at + (size_t)(T * Hq) * sizeof(float));
+  l.part = at;
+  const int64_t chunk = std::min(kChunk, kFewChunk);
+  at = align_up(at + (size_t)(T * Hq) * (size_t)((keys + chunk - 1) / chunk) * sizeof(float2));
+  l.logit = l.least = at;
+  const size_t rows = (size_t)std::min(2 * T * Hq, kFewRows * B * Hkv);
+  l.total = align_up(at + std::min(rows * (size_t)keys * sizeof(float), kLogitMax));
   return l;
 }
 
-template <typename TQ, typename TK, int D>
-void launch(const ScoreParams& p, int sms, cudaStream_t s) {
+template <typename TQ, typename TK, int D, typename Dot>
+cudaError_t launch(const ScoreParams& p, bool only_few, bool one_tile, int sms, cudaStream_t s) {
+  plan_scores_kernel<<<1, 1024, 0, s>>>(p);
+  cudaError_t e = one_tile ? launch_pdl(few_kernel<Dot, 1>, dim3(sms * 4), dim3(kFewThreads), 0, s, p)
+                           : launch_pdl(few_kernel<Dot, 2>, dim3(sms * 3), dim3(kFewThreads), 0, s, p);
+  if (e != cudaSuccess || only_few) return e;
   const int grid = sms * 8;
   stats_kernel<TQ, TK, D><<<grid, kThreads, 0, s>>>(p);
   lse_kernel<<<grid, kThreads, 0, s>>>(p);
   columns_kernel<TQ, TK, D><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
-pkv_status scores_impl(ScoreParams p, int D, bool f8, float k_scale, float scale, void* workspace, size_t ws_bytes,
+ScoreParams score_params(const void* q, const void* kc, const int32_t* tables, const int32_t* lens, const int32_t* qsl,
+                         const int32_t* rows, const float* scores, float* out, int B, int64_t T, int Hq, int Hkv,
+                         int64_t num_blocks, int bs, int max_blocks, int num_rows, int max_len, int causal,
+                         float decay) {
+  ScoreParams p{};
+  p.q = q;
+  p.kc = kc;
+  p.tables = tables;
+  p.lens = lens;
+  p.qsl = qsl;
+  p.rows = rows;
+  p.scores = scores;
+  p.out = out;
+  p.B = B;
+  p.T = T;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.num_blocks = num_blocks;
+  p.bs = bs;
+  p.bs_log = bs == 8 ? 3 : bs == 16 ? 4 : bs == 32 ? 5 : 6;
+  p.max_blocks = max_blocks;
+  p.num_rows = num_rows;
+  p.max_len = max_len;
+  p.causal = causal ? 1 : 0;
+  p.decay = decay;
+  return p;
+}
+
+pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k_scale, float scale, void* workspace, size_t ws_bytes,
                        pkv_dtype dtype, void* stream) {
   set_last_error("");
   if (dtype != PKV_DTYPE_BF16 && dtype != PKV_DTYPE_F32) return fail(PKV_ERR_UNSUPPORTED, "dtype");
@@ -383,25 +868,36 @@ pkv_status scores_impl(ScoreParams p, int D, bool f8, float k_scale, float scale
   if ((bits(p.q) | bits(p.kc)) & 15u) return fail(PKV_ERR_INVALID_ARG, "q and the cache must be 16-byte aligned");
   if (!workspace || (bits(workspace) & (kAlign - 1)))
     return fail(PKV_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
-  const Layout lay = layout(p.B, p.T, p.Hq, std::min<int64_t>(p.max_len, (int64_t)p.max_blocks * p.bs));
-  if (ws_bytes < lay.total) return fail(PKV_ERR_WORKSPACE, "workspace smaller than required");
+  const int64_t keys = std::min<int64_t>(p.max_len, (int64_t)p.max_blocks * p.bs);
+  const Layout lay = layout(p.B, p.T, p.Hq, p.Hkv, keys);
+  if (ws_bytes < lay.least) return fail(PKV_ERR_WORKSPACE, "workspace smaller than required");
   int sms = 0;
   const pkv_status st = device_state(&sms, &p.err);
   if (st != PKV_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  for (int k = 0; k < 4; ++k) p.off[k] = reinterpret_cast<int64_t*>(ws + lay.off[k]);
   p.plan = reinterpret_cast<SeqPlan*>(ws + lay.plan);
+  p.tickets = reinterpret_cast<int*>(ws + lay.tickets);
   p.lse = reinterpret_cast<float*>(ws + lay.lse);
   p.part = reinterpret_cast<float2*>(ws + lay.part);
+  p.logit = reinterpret_cast<float*>(ws + lay.logit);
+  p.logit_cap = (int64_t)((ws_bytes - lay.least) / sizeof(float));
   p.scale_log2 = (f8 ? scale * k_scale : scale) * 1.4426950408889634f;
+  // every sequence has few rows, and their logits fit: the other kernels have nothing to do
+  const int64_t most_rows = std::min<int64_t>(p.T, max_query_len > 0 ? max_query_len : p.T) * p.G;
+  const bool only_few = most_rows <= kFewRows && std::min(2 * p.T * p.Hq, (int64_t)kFewRows * p.B * p.Hkv) * keys <= p.logit_cap;
+  const bool one_tile = most_rows <= 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  plan_scores_kernel<<<1, 1024, 0, s>>>(p);
+  typedef __nv_bfloat16 bf16;
+  cudaError_t e;
   if (f8)
-    launch<__nv_bfloat16, __nv_fp8_e4m3, 128>(p, sms, s);
+    e = launch<bf16, __nv_fp8_e4m3, 128, DotFp8>(p, only_few, one_tile, sms, s);
   else if (dtype == PKV_DTYPE_BF16)
-    D == 128 ? launch<__nv_bfloat16, __nv_bfloat16, 128>(p, sms, s) : launch<__nv_bfloat16, __nv_bfloat16, 64>(p, sms, s);
+    e = D == 128 ? launch<bf16, bf16, 128, DotBf16<128>>(p, only_few, one_tile, sms, s)
+                 : launch<bf16, bf16, 64, DotBf16<64>>(p, only_few, one_tile, sms, s);
   else
-    D == 128 ? launch<float, float, 128>(p, sms, s) : launch<float, float, 64>(p, sms, s);
-  const cudaError_t e = cudaGetLastError();
+    e = D == 128 ? launch<float, float, 128, DotF32<128>>(p, only_few, one_tile, sms, s)
+                 : launch<float, float, 64, DotF32<64>>(p, only_few, one_tile, sms, s);
   if (e != cudaSuccess) return cuda_error(e, "paged_attention_scores launch");
   return PKV_OK;
 }
@@ -414,12 +910,13 @@ extern "C" {
 size_t paged_attention_scores_workspace_size(int32_t num_seqs, int64_t num_tokens, int32_t num_q_heads,
                                              int32_t num_kv_heads, int64_t max_context) {
   if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_context < 0) return 0;
-  return pkv::layout(num_seqs, num_tokens, num_q_heads, max_context).total;
+  return pkv::layout(num_seqs, num_tokens, num_q_heads, num_kv_heads, max_context).total;
 }
 
 size_t paged_attention_scores_workspace_min(int32_t num_seqs, int64_t num_tokens, int32_t num_q_heads,
                                             int32_t num_kv_heads, int64_t max_context) {
-  return paged_attention_scores_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, max_context);
+  if (num_seqs < 0 || num_tokens < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_context < 0) return 0;
+  return pkv::layout(num_seqs, num_tokens, num_q_heads, num_kv_heads, max_context).least;
 }
 
 pkv_status paged_attention_scores(const void* q, const void* k_cache, const int32_t* block_tables,
@@ -430,11 +927,11 @@ pkv_status paged_attention_scores(const void* q, const void* k_cache, const int3
                                   int32_t max_blocks_per_seq, int32_t num_rows, int32_t max_len,
                                   int32_t max_query_len, float scale, int32_t causal, float decay, void* workspace,
                                   size_t workspace_bytes, pkv_dtype dtype, void* stream) {
-  (void)max_query_len;
-  pkv::ScoreParams p{q, k_cache, block_tables, context_lens, query_start_loc, score_rows, scores, scores_out,
-                     nullptr, nullptr, nullptr, num_tokens, num_blocks, num_seqs, num_q_heads, num_kv_heads, 0,
-                     block_size, max_blocks_per_seq, num_rows, max_len, causal ? 1 : 0, 0.f, decay, nullptr};
-  return pkv::scores_impl(p, head_dim, false, 1.f, scale, workspace, workspace_bytes, dtype, stream);
+  const pkv::ScoreParams p =
+      pkv::score_params(q, k_cache, block_tables, context_lens, query_start_loc, score_rows, scores, scores_out,
+                        num_seqs, num_tokens, num_q_heads, num_kv_heads, num_blocks, block_size, max_blocks_per_seq,
+                        num_rows, max_len, causal, decay);
+  return pkv::scores_impl(p, head_dim, max_query_len, false, 1.f, scale, workspace, workspace_bytes, dtype, stream);
 }
 
 pkv_status paged_attention_scores_fp8kv(const void* q, const void* k_cache, const int32_t* block_tables,
@@ -446,11 +943,11 @@ pkv_status paged_attention_scores_fp8kv(const void* q, const void* k_cache, cons
                                         int32_t max_len, int32_t max_query_len, float scale, int32_t causal,
                                         float decay, float k_scale, void* workspace, size_t workspace_bytes,
                                         void* stream) {
-  (void)max_query_len;
-  pkv::ScoreParams p{q, k_cache, block_tables, context_lens, query_start_loc, score_rows, scores, scores_out,
-                     nullptr, nullptr, nullptr, num_tokens, num_blocks, num_seqs, num_q_heads, num_kv_heads, 0,
-                     block_size, max_blocks_per_seq, num_rows, max_len, causal ? 1 : 0, 0.f, decay, nullptr};
-  return pkv::scores_impl(p, head_dim, true, k_scale, scale, workspace, workspace_bytes, PKV_DTYPE_BF16, stream);
+  const pkv::ScoreParams p =
+      pkv::score_params(q, k_cache, block_tables, context_lens, query_start_loc, score_rows, scores, scores_out,
+                        num_seqs, num_tokens, num_q_heads, num_kv_heads, num_blocks, block_size, max_blocks_per_seq,
+                        num_rows, max_len, causal, decay);
+  return pkv::scores_impl(p, head_dim, max_query_len, true, k_scale, scale, workspace, workspace_bytes, PKV_DTYPE_BF16, stream);
 }
 
 }  // extern "C"
