@@ -146,6 +146,14 @@ pkv_status device_state(int* sms, int** err) {
 
 pkv_status cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
+pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D) {
+  return encode_pool_map(map, pool, PKV_DTYPE_BF16, NB, bs, Hkv, D, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+pkv_status rows_map(CUtensorMap* map, const void* q, int64_t T, int Hq, int D, int G, int tokens) {
+  return encode_q_map(map, q, T, Hq, D, 64, G, tokens);
+}
+
 WorkspaceLayout workspace_layout(int B, int64_t T, int Hq, int Hkv, int D, size_t bytes_available, int /*num_sms*/,
                                  bool want_default_parts) {
   WorkspaceLayout L{};

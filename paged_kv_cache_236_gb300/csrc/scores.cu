@@ -20,6 +20,8 @@
 // head's lse; every stats unit was taken earlier by a warp that is running,
 // so the wait ends, and it is bounded all the same.
 //
+// More rows in bf16: the tensor-core kernel of scores_mma.cu.
+//
 // Other rows: stats_kernel, lse_kernel, columns_kernel, which compute the
 // logits twice.
 //
@@ -34,50 +36,13 @@
 #include "paged_kv_budget.h"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "scores.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kFewRows = 16;    // rows of a few-row sequence's kv head
-constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
-constexpr int kColChunk = 256;  // keys of a column unit (few rows)
-constexpr int kChunk = 256;   // keys of a work unit (other rows)
-constexpr int kRowGroup = 8;  // rows of a work unit (other rows)
 constexpr int kThreads = 256;
 constexpr int kFewThreads = 128;
-
-// Offsets of each sequence's work, as prefix sums: the unit queues of the
-// kernels below (few-row stats and columns; other rows' stats and columns),
-// the partial (max, sum)s, the lse rows and the kept logits.
-enum { kFewStat, kFewCol, kStat, kCol, kPart, kLse, kLogit, kOffsets };
-
-struct SeqPlan {
-  int64_t part, lse, logit;
-  int L, n, row, chunks;
-  int rows, pad;  // rows of a kv head; rows a key's logits are padded to (few rows)
-};
-
-struct ScoreParams {
-  const void* q;
-  const void* kc;
-  const int32_t* tables;
-  const int32_t* lens;
-  const int32_t* qsl;
-  const int32_t* rows;
-  const float* scores;
-  float* out;
-  int64_t* off[4];  // [B + 1] each: first unit of each sequence in the four queues
-  SeqPlan* plan;    // [B]
-  int* tickets;     // [B, Hkv] chunks done, then [B, Hkv] lse ready, then the few-row queue's counter
-  float2* part;     // (m, l) per (kv head, row, chunk) of a sequence
-  float* lse;       // per (kv head, row) of a sequence
-  float* logit;     // per (kv head, key, padded row) of a few-row sequence
-  int64_t logit_cap;
-  int64_t T, num_blocks;
-  int B, Hq, Hkv, G, bs, bs_log, max_blocks, num_rows, max_len, causal;
-  float scale_log2, decay;
-  int* err;
-};
 
 __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
 #pragma unroll
@@ -107,14 +72,15 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int
 
 __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) {
   __shared__ int64_t sums[32];
-  __shared__ int64_t carry[kOffsets];
+  enum { kPart = 6, kLse, kLogit, kSums };
+  __shared__ int64_t carry[kSums];
   __shared__ int top[32];
   __shared__ int top_carry;  // the largest query_start_loc entry so far
   pdl_launch_dependents();  // few_kernel waits for this grid first of all
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kOffsets) carry[tid] = 0;
+  if (tid < kSums) carry[tid] = 0;
   if (tid == 0) top_carry = 0;
-  for (int64_t i = tid; i < 2 * (int64_t)p.B * p.Hkv + 1; i += 1024) p.tickets[i] = 0;
+  for (int64_t i = tid; i < 2 * (int64_t)p.B * p.Hkv + 2; i += 1024) p.tickets[i] = 0;
   __syncthreads();
   for (int s0 = 0; s0 < p.B; s0 += 1024) {
     const int s = s0 + tid;
@@ -150,39 +116,44 @@ __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) 
     const int64_t logits = want_few ? (int64_t)p.Hkv * sp.L * pad : 0;
     sp.logit = block_scan(logits, sums, &carry[kLogit], lane, warp);
     const bool few = want_few && sp.logit + logits <= p.logit_cap;
+    sp.kind = sp.n == 0 ? 0 : few ? kFew : p.tensor ? kTensor : kOther;
     sp.pad = few ? pad : 0;
-    const int chunk = few ? kFewChunk : kChunk;
+    const int chunk = sp.kind == kFew ? kFewChunk : sp.kind == kTensor ? kTcRange : kChunk;
     sp.chunks = (sp.L + chunk - 1) / chunk;
+    sp.tiles = sp.kind == kTensor ? (sp.n + p.tile_tok - 1) / p.tile_tok : 0;
     const int64_t groups = (sp.rows + kRowGroup - 1) / kRowGroup, work = (int64_t)p.Hkv * sp.chunks;
-    const int64_t units[4] = {few ? work : 0, few ? (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk) : 0,
-                              few ? 0 : work * groups, few ? 0 : work};
+    int64_t units[6] = {0, 0, 0, 0, 0, 0};
+    int64_t parts = work * sp.rows;
+    if (sp.kind == kFew) {
+      units[kFewStat] = work;
+      units[kFewCol] = (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk);
+    } else if (sp.kind == kOther) {
+      units[kStat] = work * groups;
+      units[kCol] = work;
+    } else if (sp.kind == kTensor) {
+      // one row tile: the columns of a range of keys; more: those of one 128-key tile
+      units[kTcStat] = work * sp.tiles;
+      units[kTcCol] = sp.tiles == 1 ? work : (int64_t)p.Hkv * ((sp.L + 127) / 128);
+      parts *= 2;  // each of the two epilogue groups writes its own
+    }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 6; ++k) {
       const int64_t at = block_scan(units[k], sums, &carry[k], lane, warp);
       if (s < p.B) p.off[k][s] = at;
     }
-    sp.part = block_scan(work * sp.rows, sums, &carry[kPart], lane, warp);
+    sp.part = block_scan(parts, sums, &carry[kPart], lane, warp);
     sp.lse = block_scan((int64_t)p.Hkv * sp.rows, sums, &carry[kLse], lane, warp);
     if (s < p.B) p.plan[s] = sp;
     if (tid == 1023) top_carry = high;
     __syncthreads();
   }
-  if (tid < 4) p.off[tid][p.B] = carry[tid];
-}
-
-// The sequence s with off[s] <= u < off[s + 1] (the whole warp calls it).
-__device__ __forceinline__ int find_seq(const int64_t* off, int B, int64_t u, int lane) {
-  int lo = 0, len = B;
-  while (len > 1) {
-    const int step = (len + 31) / 32;
-    const int i = lo + lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < len && __ldg(off + i) <= u);
-    const int k = 31 - __clz(le);  // lane 0 always holds
-    const int skip = k * step;
-    lo += skip;
-    len = min(step, len - skip);
+  if (tid < 6) p.off[tid][p.B] = carry[tid];
+  __syncthreads();
+  // places of the column items among the tensor-core kernel's items
+  for (int s = tid; s < p.B; s += 1024) {
+    const int64_t after = s + 1 < p.B ? p.off[kTcStat][s + 1] : carry[kTcStat];
+    p.off[kTcAt][s] = min(carry[kTcStat], after + p.tc_lag) + p.off[kTcCol][s];
   }
-  return lo;
 }
 
 // ---------------------------------------------------------------------------
@@ -523,15 +494,6 @@ __device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan&
   }
 }
 
-__device__ __forceinline__ int ld_acquire(const int* p) {
-  int v;
-  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_release(int* p, int v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
 // NT: tiles of 8 rows (1 where every sequence has at most 8 rows).
 template <typename Dot, int NT>
 __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) few_kernel(const ScoreParams p) {
@@ -708,7 +670,7 @@ __global__ void __launch_bounds__(kThreads) lse_kernel(const ScoreParams p) {
   const int lane = threadIdx.x & 31;
   for (int s = 0; s < p.B; ++s) {
     const SeqPlan sp = p.plan[s];
-    if (sp.pad != 0 || sp.n == 0) continue;
+    if (sp.kind != kOther) continue;
     for (int w = (blockIdx.x * kThreads + threadIdx.x) >> 5; w < p.Hkv * sp.rows; w += (gridDim.x * kThreads) >> 5) {
       const float x = row_lse(p.part + sp.part + (int64_t)w * sp.chunks, sp.chunks, lane);
       if (lane == 0) p.lse[sp.lse + w] = x;
@@ -769,7 +731,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  size_t off[4], plan, tickets, lse, part, logit, least, total;
+  size_t off[kQueues], plan, tickets, lse, part, logit, least, total;
 };
 
 // Kept logits: at most 16 padded rows of each kv head, or twice the rows
@@ -779,19 +741,21 @@ constexpr size_t kLogitMax = (size_t)512 << 20;
 Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   Layout l{};
   size_t at = 0;
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kQueues; ++k) {
     l.off[k] = at;
     at = align_up(at + (size_t)(B + 1) * sizeof(int64_t));
   }
   l.plan = at;
   at = align_up(at + (size_t)B * sizeof(SeqPlan));
   l.tickets = at;
-  at = align_up(at + (size_t)(2 * B * Hkv + 1) * sizeof(int));
+  at = align_up(at + (size_t)(2 * B * Hkv + 2) * sizeof(int));
   l.lse = at;
   at = align_up(at + (size_t)(T * Hq) * sizeof(float));
   l.part = at;
   const int64_t chunk = std::min(kChunk, kFewChunk);
-  at = align_up(at + (size_t)(T * Hq) * (size_t)((keys + chunk - 1) / chunk) * sizeof(float2));
+  // the tensor-core kernel's two partials a range of 256 keys or more take at
+  // most one entry more than one a chunk of 128 does
+  at = align_up(at + (size_t)(T * Hq) * (size_t)((keys + chunk - 1) / chunk + 1) * sizeof(float2));
   l.logit = l.least = at;
   const size_t rows = (size_t)std::min(2 * T * Hq, kFewRows * B * Hkv);
   l.total = align_up(at + std::min(rows * (size_t)keys * sizeof(float), kLogitMax));
@@ -803,7 +767,7 @@ cudaError_t launch(const ScoreParams& p, bool only_few, bool one_tile, int sms, 
   plan_scores_kernel<<<1, 1024, 0, s>>>(p);
   cudaError_t e = one_tile ? launch_pdl(few_kernel<Dot, 1>, dim3(sms * 4), dim3(kFewThreads), 0, s, p)
                            : launch_pdl(few_kernel<Dot, 2>, dim3(sms * 3), dim3(kFewThreads), 0, s, p);
-  if (e != cudaSuccess || only_few) return e;
+  if (e != cudaSuccess || only_few || p.tensor) return e;
   const int grid = sms * 8;
   stats_kernel<TQ, TK, D><<<grid, kThreads, 0, s>>>(p);
   lse_kernel<<<grid, kThreads, 0, s>>>(p);
@@ -875,7 +839,7 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   const pkv_status st = device_state(&sms, &p.err);
   if (st != PKV_OK) return st;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  for (int k = 0; k < 4; ++k) p.off[k] = reinterpret_cast<int64_t*>(ws + lay.off[k]);
+  for (int k = 0; k < kQueues; ++k) p.off[k] = reinterpret_cast<int64_t*>(ws + lay.off[k]);
   p.plan = reinterpret_cast<SeqPlan*>(ws + lay.plan);
   p.tickets = reinterpret_cast<int*>(ws + lay.tickets);
   p.lse = reinterpret_cast<float*>(ws + lay.lse);
@@ -889,6 +853,16 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   const bool one_tile = most_rows <= 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   typedef __nv_bfloat16 bf16;
+  // bf16: more rows go to the tensor-core kernel (its operands come through tensor maps)
+  p.tensor = !f8 && dtype == PKV_DTYPE_BF16;
+  p.tile_tok = 128 / p.G;
+  p.tc_lag = 2 * sms;
+  CUtensorMap qmap, kmap;
+  pkv_status mst;
+  if (p.tensor && !only_few) {
+    if ((mst = rows_map(&qmap, p.q, p.T, p.Hq, D, p.G, p.tile_tok)) != PKV_OK) return mst;
+    if ((mst = pool_map(&kmap, p.kc, p.num_blocks, p.bs, p.Hkv, D)) != PKV_OK) return mst;
+  }
   cudaError_t e;
   if (f8)
     e = launch<bf16, __nv_fp8_e4m3, 128, DotFp8>(p, only_few, one_tile, sms, s);
@@ -898,6 +872,7 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   else
     e = D == 128 ? launch<float, float, 128, DotF32<128>>(p, only_few, one_tile, sms, s)
                  : launch<float, float, 64, DotF32<64>>(p, only_few, one_tile, sms, s);
+  if (e == cudaSuccess && p.tensor && !only_few) e = launch_scores_mma(p, D, qmap, kmap, sms, s);
   if (e != cudaSuccess) return cuda_error(e, "paged_attention_scores launch");
   return PKV_OK;
 }

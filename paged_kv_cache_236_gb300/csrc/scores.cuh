@@ -1,0 +1,87 @@
+// What the kernels of paged_attention_scores share: the plan of each
+// sequence's work and the queues the kernels take it from.
+#pragma once
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+constexpr int kFewRows = 16;    // rows of a few-row sequence's kv head
+constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
+constexpr int kColChunk = 256;  // keys of a column unit (few rows)
+constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
+constexpr int kChunk = 256;   // keys of a work unit (other rows)
+enum { kFew = 1, kTensor = 2, kOther = 3 };
+constexpr int kRowGroup = 8;  // rows of a work unit (other rows)
+
+// Offsets of each sequence's work, as prefix sums: the unit queues of the
+// kernels below (few-row stats and columns; other rows' stats and columns),
+// the partial (max, sum)s, the lse rows and the kept logits.
+// The tensor-core kernel's two kinds of items share one queue: the column
+// items of sequence s start at place kTcAt[s] of it.
+enum { kFewStat, kFewCol, kStat, kCol, kTcStat, kTcCol, kTcAt, kQueues };
+
+struct SeqPlan {
+  int64_t part, lse, logit;
+  int L, n, row, chunks;
+  int rows, pad;  // rows of a kv head; rows a key's logits are padded to (few rows)
+  int kind;       // which kernels: kFew, kTensor, kOther (0: none)
+  int tiles;      // row tiles of the tensor-core kernel (whole tokens that fit 128 rows)
+};
+
+struct ScoreParams {
+  const void* q;
+  const void* kc;
+  const int32_t* tables;
+  const int32_t* lens;
+  const int32_t* qsl;
+  const int32_t* rows;
+  const float* scores;
+  float* out;
+  int64_t* off[kQueues];  // [B + 1] each: first unit of each sequence in the queues
+  SeqPlan* plan;    // [B]
+  int* tickets;     // [B, Hkv] chunks done, then [B, Hkv] lse ready, then the counters of the two dynamic queues
+  float2* part;     // (m, l) per (kv head, row, chunk) of a sequence
+  float* lse;       // per (kv head, row) of a sequence
+  float* logit;     // per (kv head, key, padded row) of a few-row sequence
+  int64_t logit_cap;
+  int tensor;       // sequences of more rows go to the tensor-core kernel
+  int tc_lag;       // column items follow this many later stats items in its queue
+  int tile_tok;     // tokens of a row tile: floor(128 / G)
+  int64_t T, num_blocks;
+  int B, Hq, Hkv, G, bs, bs_log, max_blocks, num_rows, max_len, causal;
+  float scale_log2, decay;
+  int* err;
+};
+
+// The sequence s with off[s] <= u < off[s + 1] (the whole warp calls it).
+__device__ __forceinline__ int find_seq(const int64_t* off, int B, int64_t u, int lane) {
+  int lo = 0, len = B;
+  while (len > 1) {
+    const int step = (len + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < len && __ldg(off + i) <= u);
+    const int k = 31 - __clz(le);  // lane 0 always holds
+    const int skip = k * step;
+    lo += skip;
+    len = min(step, len - skip);
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release(int* p, int v) {
+  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+// The tensor-core kernel for bf16 sequences of more than kFewRows rows
+// (scores_mma.cu).
+cudaError_t launch_scores_mma(const ScoreParams& p, int D, const CUtensorMap& qmap, const CUtensorMap& kmap, int sms,
+                              cudaStream_t s);
+
+}  // namespace pkv
