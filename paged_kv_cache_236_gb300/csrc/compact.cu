@@ -10,12 +10,16 @@
 // them at a time: load the round into registers, barrier, store it.  Loads of
 // later rounds may run ahead of the stores freely.
 //
-// The rows of one head are independent of the other heads', K of V, and
-// every 16-byte column slice of the others: the grid is
-// (sequences x heads) x (K slices + V slices + scores).
+// The rows of one head are independent of the other heads', and K, V and the
+// scores of each other: each (sequence, head, array) is a cluster's work.  With
+// few of those the cluster has several blocks, which share each round (a block
+// its rows in order, the blocks in order) and pass a cluster barrier between
+// its loads and its stores.
 //
 // HBM-bound: every kept row is read and written once; rows that stay where
-// they are (the kept prefix) are neither read nor written.
+// they are (the kept prefix) are neither read nor written.  The next round's
+// rows are loaded before the barrier of the current one, and the positions of
+// the round after that.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -27,7 +31,7 @@ namespace pkv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVecs = 4;  // 16-byte vectors a thread holds per round
+constexpr int kVecs = 4;  // 16-byte vectors of one row (scores: values) a thread holds per round
 
 struct CompactParams {
   uint8_t* kc;
@@ -38,92 +42,183 @@ struct CompactParams {
   const int32_t* rows;
   float* scores;
   int64_t num_blocks;
-  int Hkv, bs, max_blocks, budget, num_rows, max_len;
-  int row_bytes;     // head_dim * element size
-  int slice_vecs;    // 16-byte vectors of a column slice
-  int slices;        // column slices of a row
+  int Hkv, bs, bs_log, max_blocks, budget, num_rows, max_len;  // bs_log < 0: not a power of two
+  int row_bytes;  // head_dim * element size
+  int cluster;    // blocks of a cluster
   int* err;
 };
 
-__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p) {
-  const int per = 2 * p.slices + (p.scores ? 1 : 0);
-  const int sh = blockIdx.x / per, part = blockIdx.x - sh * per;
+// Threads that share a row of `vecs` 16-byte vectors, at most kVecs each.
+__host__ __device__ constexpr int row_team(int vecs) { return (vecs + kVecs - 1) / kVecs; }
+
+// Every thread of the cluster has performed its loads so far; stores of any
+// of them may follow.
+__device__ __forceinline__ void round_barrier(int cluster) {
+  if (cluster == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+
+// What a thread moves: Mover::Slot holds its part of `kTokens` kept tokens on
+// their way, load() starts token i of them (kept token r, from position src;
+// src < 0: none), store() ends it.
+//
+// Rows: up to four 16-byte vectors of one token's row, `apart` bytes from one
+// another so that the threads of a row read whole sectors side by side; one
+// address computation serves them.
+struct RowMover {
+  static constexpr int kTokens = 1;
+  struct Slot {
+    int4 x[kVecs];
+    uint8_t* to;  // null: nothing to store
+  };
+  uint8_t* pool;
+  const int32_t* bt;
+  const int32_t* dt;
+  int64_t col, token_bytes, num_blocks;
+  int bs, bs_log, max_blocks, apart, vecs;
+  bool bad;
+
+  __device__ __forceinline__ void load(Slot& v, int, int r, int src) {
+    v.to = nullptr;
+    if (src < 0) return;
+    int sb, so, db, dof;
+    if (bs_log >= 0) {
+      sb = src >> bs_log;
+      db = r >> bs_log;
+      so = src & (bs - 1);
+      dof = r & (bs - 1);
+    } else {
+      sb = src / bs;
+      db = r / bs;
+      so = src - sb * bs;
+      dof = r - db * bs;
+    }
+    const int sblk = sb < max_blocks ? __ldg(bt + sb) : -1;
+    const int dblk = db < max_blocks ? __ldg(dt + db) : -1;
+    const bool s_ok = sblk >= 0 && sblk < num_blocks, d_ok = dblk >= 0 && dblk < num_blocks;
+    bad |= !s_ok || !d_ok;
+    const int64_t from = ((int64_t)sblk * bs + so) * token_bytes + col;
+    const int64_t dst = ((int64_t)dblk * bs + dof) * token_bytes + col;
+    if (d_ok && !(s_ok && from == dst)) {
+      v.to = pool + dst;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        v.x[i] = make_int4(0, 0, 0, 0);
+        if (s_ok && i < vecs) v.x[i] = *reinterpret_cast<const int4*>(pool + from + i * apart);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const Slot& v) {
+    if (!v.to) return;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (i < vecs) *reinterpret_cast<int4*>(v.to + i * apart) = v.x[i];
+  }
+};
+
+struct ScoreMover {
+  static constexpr int kTokens = kVecs;
+  struct Slot {
+    float x[kVecs];
+    int to[kVecs];  // < 0: nothing to store
+  };
+  float* sc;
+  int max_len;
+  bool bad;
+
+  __device__ __forceinline__ void load(Slot& v, int i, int r, int src) {
+    v.to[i] = -1;
+    if (src < 0 || src == r || r >= max_len) return;
+    v.to[i] = r;
+    v.x[i] = 0.f;
+    if (src < max_len)
+      v.x[i] = sc[src];
+    else
+      bad = true;
+  }
+  __device__ __forceinline__ void store(const Slot& v) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (v.to[i] >= 0) sc[v.to[i]] = v.x[i];
+  }
+};
+
+// The rounds of one (sequence, head, array).  A round is `per` tokens for each
+// block of the cluster; this thread moves tokens base + i * lanes + mine of
+// its block's (mine < 0: it moves none, but keeps the barriers).
+template <typename Mover>
+__device__ __forceinline__ bool move_rounds(Mover& m, const int32_t* kept, int budget, int cluster, int block, int lanes,
+                                            int mine) {
+  typedef typename Mover::Slot Slot;
+  constexpr int N = Mover::kTokens;
+  const int per = lanes * N, round = per * cluster;
+  bool bad_order = false;
+  auto positions = [&](int base, int (&src)[N]) {  // of the round at base; -1 past the kept ones
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = base + block * per + i * lanes + mine;
+      src[i] = mine >= 0 && r < budget ? __ldg(kept + r) : -1;
+      if (src[i] >= 0 && r > 0 && __ldg(kept + r - 1) >= src[i]) bad_order = true;
+    }
+  };
+  auto load = [&](int base, const int (&src)[N], Slot& v) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) m.load(v, i, base + block * per + i * lanes + mine, src[i]);
+  };
+  // every thread of the cluster sees the same rounds: the kept ones end at the first -1
+  int src[N];
+  Slot now, next;
+  positions(0, src);
+  load(0, src, now);
+  positions(round, src);
+  for (int base = 0; base < budget && __ldg(kept + base) >= 0; base += round) {
+    load(base + round, src, next);
+    positions(base + 2 * round, src);
+    round_barrier(cluster);  // every load of this round has been performed
+    m.store(now);
+    now = next;
+  }
+  return bad_order;
+}
+
+__global__ void __launch_bounds__(kThreads, 3) compact_kernel(const CompactParams p) {
+  const int block = p.cluster == 1 ? 0 : blockIdx.x % p.cluster;
+  const int64_t work = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
+  const int per = p.scores ? 3 : 2;
+  const int sh = (int)(work / per), part = (int)(work - (int64_t)sh * per);
   const int s = sh / p.Hkv, h = sh - s * p.Hkv;
   const int32_t* kept = p.kept + (int64_t)sh * p.budget;
-  bool bad_block = false, bad_order = false;
-
-  if (part == 2 * p.slices) {  // the running scores
+  if (part == 2) {  // the running scores
     const int row = p.rows ? p.rows[s] : s;
     if (row < 0 || row >= p.num_rows) {
       if (row >= 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
       return;
     }
-    float* sc = p.scores + ((int64_t)row * p.Hkv + h) * p.max_len;
-    for (int base = 0; base < p.budget && kept[base] >= 0; base += kThreads * kVecs) {
-      float x[kVecs];
-      bool live[kVecs];
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int r = base + i * kThreads + threadIdx.x;
-        const int src = r < p.budget ? kept[r] : -1;
-        live[i] = src >= 0 && r < p.max_len && src != r;
-        x[i] = 0.f;
-        if (live[i]) {
-          if (src < p.max_len)
-            x[i] = sc[src];
-          else
-            bad_block = true;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        if (live[i]) sc[base + i * kThreads + threadIdx.x] = x[i];
-    }
-    if (bad_block) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+    ScoreMover m{p.scores + ((int64_t)row * p.Hkv + h) * p.max_len, p.max_len, false};
+    move_rounds(m, kept, p.budget, p.cluster, block, kThreads, threadIdx.x);
+    if (m.bad) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
     return;
   }
-
-  uint8_t* pool = part < p.slices ? p.kc : p.vc;
-  const int slice = part < p.slices ? part : part - p.slices;
+  const int vecs = p.row_bytes / 16, team = row_team(vecs), lanes = kThreads / team;
+  const int mine = threadIdx.x / team, member = threadIdx.x - mine * team;
   const int32_t* bt = p.tables + (int64_t)s * p.max_blocks;
-  const int32_t* dt = (p.dst_tables ? p.dst_tables : p.tables) + (int64_t)s * p.max_blocks;
-  const int rpr = kThreads / p.slice_vecs;  // rows per pass of the block
-  const int my_row = threadIdx.x / p.slice_vecs, my_vec = threadIdx.x - my_row * p.slice_vecs;
-  const bool idle = my_row >= rpr;
-  const int64_t col = (int64_t)h * p.row_bytes + (slice * p.slice_vecs + my_vec) * 16;
-  const bool in_row = (slice * p.slice_vecs + my_vec) * 16 < p.row_bytes;
-  const int64_t token_bytes = (int64_t)p.Hkv * p.row_bytes;
-  for (int base = 0; base < p.budget && kept[base] >= 0; base += rpr * kVecs) {
-    int4 x[kVecs];
-    uint8_t* to[kVecs];
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int r = base + i * rpr + my_row;
-      const int src = !idle && in_row && r < p.budget ? kept[r] : -1;
-      x[i] = make_int4(0, 0, 0, 0);
-      to[i] = nullptr;
-      if (src >= 0) {
-        if (r > 0 && kept[r - 1] >= src) bad_order = true;
-        const int sb = src / p.bs, db = r / p.bs;
-        const int64_t sblk = sb < p.max_blocks ? bt[sb] : -1;
-        const int64_t dblk = db < p.max_blocks ? dt[db] : -1;
-        const bool s_ok = sblk >= 0 && sblk < p.num_blocks, d_ok = dblk >= 0 && dblk < p.num_blocks;
-        bad_block |= !s_ok || !d_ok;
-        uint8_t* from = pool + (sblk * p.bs + (src - sb * p.bs)) * token_bytes + col;
-        uint8_t* dst = pool + (dblk * p.bs + (r - db * p.bs)) * token_bytes + col;
-        if (d_ok && !(s_ok && from == dst)) {
-          to[i] = dst;
-          if (s_ok) x[i] = *reinterpret_cast<const int4*>(from);
-        }
-      }
-    }
-    __syncthreads();  // every row of this round is read
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i)
-      if (to[i]) *reinterpret_cast<int4*>(to[i]) = x[i];
-  }
-  if (bad_block) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+  RowMover m{part ? p.vc : p.kc,
+             bt,
+             p.dst_tables ? p.dst_tables + (int64_t)s * p.max_blocks : bt,
+             (int64_t)h * p.row_bytes + member * 16,
+             (int64_t)p.Hkv * p.row_bytes,
+             p.num_blocks,
+             p.bs,
+             p.bs_log,
+             p.max_blocks,
+             team * 16,
+             (vecs - member + team - 1) / team,
+             false};
+  const bool bad_order = move_rounds(m, kept, p.budget, p.cluster, block, lanes, mine < lanes ? mine : -1);
+  if (m.bad) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
   if (bad_order) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
 }
 
@@ -176,17 +271,33 @@ extern "C" pkv_status paged_kv_compact(void* k_cache, void* v_cache, const int32
   p.num_blocks = num_blocks;
   p.Hkv = num_kv_heads;
   p.bs = block_size;
+  p.bs_log = -1;
+  for (int k = 0; k < 31; ++k)
+    if (block_size == 1 << k) p.bs_log = k;
   p.max_blocks = max_blocks_per_seq;
   p.budget = budget;
   p.num_rows = num_rows;
   p.max_len = max_len;
   p.row_bytes = (int)row_bytes;
-  p.slices = 1;
-  p.slice_vecs = (int)(row_bytes / 16);
-  const int64_t grid = (int64_t)num_seqs * num_kv_heads * (2 * p.slices + (scores ? 1 : 0));
-  if (grid > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "too many sequences and heads");
-  compact_kernel<<<(unsigned)grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  // Several blocks to a (sequence, head, array) while there are too few of
+  // them to keep the SMs' loads in flight, and each has rounds to share.
+  const int64_t units = (int64_t)num_seqs * num_kv_heads * (scores ? 3 : 2);
+  const int round = kThreads / row_team((int)(row_bytes / 16));
+  int cluster = 1;
+  while (cluster < 8 && units * cluster < 4 * sms && cluster * 2 * round <= budget) cluster *= 2;
+  p.cluster = cluster;
+  if (units * cluster > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "too many sequences and heads");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, compact_kernel, p);
   if (e != cudaSuccess) return cuda_error(e, "paged_kv_compact launch");
   return PKV_OK;
 }

@@ -11,20 +11,29 @@
 //
 // The angle: a position of 2^17 and a frequency of 1 leave an fp32 product
 // 2^-7 radians off, so the angle is kept in turns as a 64-bit fraction: the
-// frequency in turns per position, rounded to a multiple of 2^-64 (a few fp64
-// operations per frequency and block), times the position modulo 2^64 is the
-// fraction of a turn exactly but for p * 2^-53 relative of the frequency's own
-// rounding.  sincospif of its signed value is then good to fp32.  All of a
-// token's heads share its rotary/2 (cos, sin) pairs, in shared memory.
+// frequency in turns per position, a multiple of 2^-64 (its 53-bit mantissa
+// times 2^64 / (2 pi), shifted: integer arithmetic, the SM's fp64 units are
+// few), times the position modulo 2^64 is the fraction of a turn exactly but
+// for the frequency's own 2^-53.  sincospif of its signed value is then good to
+// fp32.
 //
 // HBM-bound: q, k and v are read once and q_out and the pool rows written
-// once; a separate rotation would move q and k twice.  A thread holds kVec
-// pairs (two 16-byte vectors of one head), two heads' worth in flight.
+// once; a separate rotation would move q and k twice.  A warp takes one token,
+// or, with few tokens, some of its heads.  It computes the token's angles once
+// (shared by its lanes through shared memory); then a lane owns one place of
+// a head, two 16-byte vectors (kVec pairs of the rotary part, or two vectors
+// past it), keeps that place's (cos, sin) in registers and goes through the
+// heads, kBatch heads' loads in flight at a time.  The first version, a block
+// of 256 threads to one or two tokens with the angles read from shared memory
+// for every head, spent its time on instructions and the block's barrier
+// (16384 tokens into FP8 pools: 168 us; 4216 tokens: 27 us).
 // Values are rotated in fp32 and rounded once, to the output's type: an FP8
 // pool takes the code of the fp32 value, with no rounding to the row's type
 // in between.
 #include <cuda_fp8.h>
 #include <math.h>
+
+#include <algorithm>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -44,13 +53,13 @@ struct RopeParams {
   void* vc;
   int64_t T, num_slots, q_stride, k_stride, v_stride;  // strides in elements
   int Hq, Hkv, D, half;  // half: pairs per head (rotary / 2)
-  int interleaved, tokens_per_cta;
+  int interleaved, splits;  // splits: warps that share a token's heads
   float amp, k_scale, v_scale;
   int* err;
 };
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens of a CTA
+constexpr int kWarps = 4;   // of a block
+constexpr int kBatch = 2;   // heads a lane loads at a time
 
 template <typename U, int N>
 struct alignas(sizeof(U) * N) Vec {
@@ -62,135 +71,184 @@ __device__ __forceinline__ float to_f(uint16_t b) { return __uint_as_float((uint
 __device__ __forceinline__ void from_f(float x, float& y) { y = x; }
 __device__ __forceinline__ void from_f(float x, uint16_t& y) { y = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 
-// E4M3 code of x / scale (IEEE division, nearest even, saturating), as
+// E4M3 codes of x / scale (IEEE division, nearest even, saturating), as
 // paged_kv_write_fp8 encodes.
-__device__ __forceinline__ uint8_t code_of(float x, float scale) {
-  return (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3);
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], float scale) {
+  Vec<uint8_t, N> o;
+  if constexpr (N >= 2) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[i], scale), __fdiv_rn(x[i + 1], scale)),
+                                                    __NV_SATFINITE, __NV_E4M3);
+      o.e[i] = (uint8_t)two;
+      o.e[i + 1] = (uint8_t)(two >> 8);
+    }
+  } else {
+    o.e[0] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(x[0], scale), __NV_SATFINITE, __NV_E4M3);
+  }
+  *reinterpret_cast<Vec<uint8_t, N>*>(dst) = o;
+}
+template <typename U, int N>
+__device__ __forceinline__ void store_rows(U* dst, const float (&x)[N]) {
+  Vec<U, N> o;
+#pragma unroll
+  for (int i = 0; i < N; ++i) from_f(x[i], o.e[i]);
+  *reinterpret_cast<Vec<U, N>*>(dst) = o;
 }
 
-// One head row's unit x of a token: VEC pairs (the first half / VEC units) or
-// VEC copied elements.
-template <typename U, int VEC>
-struct Unit {
-  Vec<U, VEC> a, b;
-};
+// Turns per position, times 2^64 (modulo 2^64), of a frequency in radians per
+// position: |f| = m * 2^(e - 52) with a whole m < 2^53, and 2^64 / (2 pi) as a
+// whole number.
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int e = (int)((bits >> 52) & 2047) - 1023;
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e == -1023 ? 0 : 1ull << 52);
+  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;
+  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * kInv2Pi >> sh
+  uint64_t r;
+  if (sh >= 128) r = 0;
+  else if (sh >= 64) r = hi >> (sh - 64);
+  else if (sh > 0) r = (lo >> sh) | (hi << (64 - sh));
+  else r = sh > -64 ? lo << -sh : 0;
+  return bits >> 63 ? 0 - r : r;
+}
 
 // F8: the pools hold E4M3 codes.  U: the rows' element (uint16_t: bf16 bits).
-template <typename U, int VEC, bool F8>
-__global__ void __launch_bounds__(kThreads) rope_write_kernel(const RopeParams p) {
+template <typename U, int VEC, bool F8, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32, 5) rope_write_kernel(const RopeParams p) {
   pdl_launch_dependents();  // what follows with programmatic launch reads nothing written here before it waits
-  extern __shared__ float2 trig[];  // [tokens][half]
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_cta;
-  const int nt = (int)min((int64_t)p.tokens_per_cta, p.T - t0);
-  for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < nt * p.half; i += blockDim.x * blockDim.y) {
-    const int t = i / p.half, j = i - t * p.half;
-    const double turns = p.inv_freq[j] * 0.15915494309189535;  // 1 / (2 pi)
-    const long long fix = __double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
-    const long long ang = (long long)((unsigned long long)p.positions[t0 + t] * (unsigned long long)fix);
+  extern __shared__ float2 trig_all[];  // [warps][half]
+  typedef Vec<U, VEC> V;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t tok = w / p.splits;
+  const int split = (int)(w - tok * p.splits);
+  if (tok >= p.T) return;
+  float2* trig = trig_all + warp * p.half;
+  const uint64_t pos = (uint64_t)p.positions[tok];
+  int64_t slot = p.slots[tok];
+  if (slot >= p.num_slots) {
+    if (lane == 0 && split == 0) raise_error(p.err, PKV_DEVERR_SLOT_OUT_OF_RANGE);
+    slot = -1;
+  }
+  for (int j = lane; j < p.half; j += 32) {
+    const long long ang = (long long)(pos * turns_of(p.inv_freq[j]));
     float s, c;
     sincospif(__ll2float_rn(ang) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
-    trig[i] = make_float2(c * p.amp, s * p.amp);
+    trig[j] = make_float2(c * p.amp, s * p.amp);
   }
-  __syncthreads();
+  __syncwarp();
 
-  const int heads = p.Hq + 2 * p.Hkv;
-  const int rot_units = p.half / VEC;
-  const int units = rot_units + (p.D - 2 * p.half) / VEC;  // of a rotated head
-  const int vunits = p.D / VEC;
-  const int rows = nt * heads;
-  for (int r = blockIdx.y * blockDim.y + threadIdx.y; r < rows; r += gridDim.y * blockDim.y) {
-    const int t = r / heads, h = r - t * heads;
-    const int64_t tok = t0 + t;
-    const bool is_q = h < p.Hq;
-    int64_t slot = 0;
-    if (!is_q) {
-      slot = p.slots[tok];
-      if (slot >= p.num_slots) {
-        if (threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_SLOT_OUT_OF_RANGE);
-        slot = -1;
-      }
-      if (slot < 0) continue;
-    }
-    if (h >= p.Hq + p.Hkv) {  // v: copied, or encoded
-      const int hv = h - p.Hq - p.Hkv;
-      const U* src = static_cast<const U*>(p.v) + tok * p.v_stride + (int64_t)hv * p.D;
-      const int64_t at = (slot * p.Hkv + hv) * p.D;
-      for (int x = threadIdx.x; x < vunits; x += blockDim.x) {
-        const Vec<U, VEC> a = *reinterpret_cast<const Vec<U, VEC>*>(src + x * VEC);
-        if constexpr (F8) {
-          Vec<uint8_t, VEC> o;
+  const int places = (p.D / VEC + 1) / 2;  // of a head; the last may hold one vector
+  const int rot_places = p.half / VEC;
+  const int side = places < 32 ? 32 / places : 1;  // heads side by side
+  const int y = places < 32 ? lane / places : 0;
+  if (y >= side) return;
+  const int hstep = side * p.splits;
+  for (int x = places < 32 ? lane - y * places : lane; x < places; x += 32) {
+    const bool rot = x < rot_places;
+    // the place's two columns
+    const int ca = rot ? (INTER ? 2 * x * VEC : x * VEC) : 2 * p.half + 2 * (x - rot_places) * VEC;
+    const int cb = rot && !INTER ? p.half + x * VEC : ca + VEC;
+    const bool two = cb + VEC <= p.D;
+    float2 cs[VEC];
+    if (rot) {
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) o.e[i] = code_of(to_f(a.e[i]), p.v_scale);
-          *reinterpret_cast<Vec<uint8_t, VEC>*>(static_cast<uint8_t*>(p.vc) + at + x * VEC) = o;
-        } else {
-          *reinterpret_cast<Vec<U, VEC>*>(static_cast<U*>(p.vc) + at + x * VEC) = a;
+      for (int e = 0; e < VEC; ++e) cs[e] = trig[x * VEC + e];
+    }
+    // this warp's heads of one of q, k, v (src: the token's head 0)
+    auto go = [&](const U* src, int heads, auto put) {
+      for (int h0 = split * side + y; h0 < heads; h0 += kBatch * hstep) {
+        V a[kBatch], b[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = h0 + i * hstep;
+          if (h < heads) {
+            a[i] = *reinterpret_cast<const V*>(src + (int64_t)h * p.D + ca);
+            if (two) b[i] = *reinterpret_cast<const V*>(src + (int64_t)h * p.D + cb);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = h0 + i * hstep;
+          if (h < heads) put(h, a[i], b[i]);
         }
       }
-      continue;
-    }
-    const int hk = h - p.Hq;
-    const U* src = is_q ? static_cast<const U*>(p.q) + tok * p.q_stride + (int64_t)h * p.D
-                        : static_cast<const U*>(p.k) + tok * p.k_stride + (int64_t)hk * p.D;
-    const int64_t at = is_q ? (tok * p.Hq + h) * (int64_t)p.D : (slot * p.Hkv + hk) * (int64_t)p.D;
-    U* dst = is_q ? static_cast<U*>(p.q_out) : static_cast<U*>(p.kc);
-    auto put = [&](int col, const float (&y)[VEC]) {
-      if (F8 && !is_q) {
-        Vec<uint8_t, VEC> o;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o.e[i] = code_of(y[i], p.k_scale);
-        *reinterpret_cast<Vec<uint8_t, VEC>*>(static_cast<uint8_t*>(p.kc) + at + col) = o;
-      } else {
-        Vec<U, VEC> o;
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) from_f(y[i], o.e[i]);
-        *reinterpret_cast<Vec<U, VEC>*>(dst + at + col) = o;
-      }
     };
-    for (int x = threadIdx.x; x < units; x += blockDim.x) {
-      if (x >= rot_units) {  // past the rotary part
-        const int col = 2 * p.half + (x - rot_units) * VEC;
-        const Vec<U, VEC> a = *reinterpret_cast<const Vec<U, VEC>*>(src + col);
-        float y[VEC];
+    auto turned = [&](const V& a, const V& b, float (&ya)[VEC], float (&yb)[VEC]) {
+      if (!rot) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) y[i] = to_f(a.e[i]);
-        put(col, y);
-        continue;
-      }
-      const int ca = p.interleaved ? 2 * x * VEC : x * VEC;
-      const int cb = p.interleaved ? ca + VEC : p.half + x * VEC;
-      const Vec<U, VEC> a = *reinterpret_cast<const Vec<U, VEC>*>(src + ca);
-      const Vec<U, VEC> b = *reinterpret_cast<const Vec<U, VEC>*>(src + cb);
-      const float2* cs = trig + t * p.half + x * VEC;
-      float ya[VEC], yb[VEC];
-      if (p.interleaved) {
+        for (int e = 0; e < VEC; ++e) {
+          ya[e] = to_f(a.e[e]);
+          yb[e] = two ? to_f(b.e[e]) : 0.f;
+        }
+      } else if (INTER) {
         // the 2 * VEC elements a, b hold pairs (0, 1), (2, 3), ...
         float in[2 * VEC], out[2 * VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          in[i] = to_f(a.e[i]);
-          in[VEC + i] = to_f(b.e[i]);
+        for (int e = 0; e < VEC; ++e) {
+          in[e] = to_f(a.e[e]);
+          in[VEC + e] = to_f(b.e[e]);
         }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          out[2 * i] = fmaf(in[2 * i], cs[i].x, -in[2 * i + 1] * cs[i].y);
-          out[2 * i + 1] = fmaf(in[2 * i + 1], cs[i].x, in[2 * i] * cs[i].y);
+        for (int e = 0; e < VEC; ++e) {
+          out[2 * e] = fmaf(in[2 * e], cs[e].x, -in[2 * e + 1] * cs[e].y);
+          out[2 * e + 1] = fmaf(in[2 * e + 1], cs[e].x, in[2 * e] * cs[e].y);
         }
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          ya[i] = out[i];
-          yb[i] = out[VEC + i];
+        for (int e = 0; e < VEC; ++e) {
+          ya[e] = out[e];
+          yb[e] = out[VEC + e];
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float x1 = to_f(a.e[i]), x2 = to_f(b.e[i]);
-          ya[i] = fmaf(x1, cs[i].x, -x2 * cs[i].y);
-          yb[i] = fmaf(x2, cs[i].x, x1 * cs[i].y);
+        for (int e = 0; e < VEC; ++e) {
+          const float x1 = to_f(a.e[e]), x2 = to_f(b.e[e]);
+          ya[e] = fmaf(x1, cs[e].x, -x2 * cs[e].y);
+          yb[e] = fmaf(x2, cs[e].x, x1 * cs[e].y);
         }
       }
-      put(ca, ya);
-      put(cb, yb);
-    }
+    };
+    U* qo = static_cast<U*>(p.q_out) + tok * p.Hq * (int64_t)p.D;
+    go(static_cast<const U*>(p.q) + tok * p.q_stride, p.Hq, [&](int h, const V& a, const V& b) {
+      float ya[VEC], yb[VEC];
+      turned(a, b, ya, yb);
+      U* dst = qo + (int64_t)h * p.D;
+      store_rows<U, VEC>(dst + ca, ya);
+      if (two) store_rows<U, VEC>(dst + cb, yb);
+    });
+    if (slot < 0) continue;
+    const int64_t at = slot * p.Hkv * (int64_t)p.D;
+    go(static_cast<const U*>(p.k) + tok * p.k_stride, p.Hkv, [&](int h, const V& a, const V& b) {
+      float ya[VEC], yb[VEC];
+      turned(a, b, ya, yb);
+      const int64_t to = at + (int64_t)h * p.D;
+      if constexpr (F8) {
+        store_codes<VEC>(static_cast<uint8_t*>(p.kc) + to + ca, ya, p.k_scale);
+        if (two) store_codes<VEC>(static_cast<uint8_t*>(p.kc) + to + cb, yb, p.k_scale);
+      } else {
+        store_rows<U, VEC>(static_cast<U*>(p.kc) + to + ca, ya);
+        if (two) store_rows<U, VEC>(static_cast<U*>(p.kc) + to + cb, yb);
+      }
+    });
+    go(static_cast<const U*>(p.v) + tok * p.v_stride, p.Hkv, [&](int h, const V& a, const V& b) {
+      const int64_t to = at + (int64_t)h * p.D;
+      if constexpr (F8) {
+        float ya[VEC], yb[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          ya[e] = to_f(a.e[e]);
+          yb[e] = two ? to_f(b.e[e]) : 0.f;
+        }
+        store_codes<VEC>(static_cast<uint8_t*>(p.vc) + to + ca, ya, p.v_scale);
+        if (two) store_codes<VEC>(static_cast<uint8_t*>(p.vc) + to + cb, yb, p.v_scale);
+      } else {
+        *reinterpret_cast<V*>(static_cast<U*>(p.vc) + to + ca) = a;
+        if (two) *reinterpret_cast<V*>(static_cast<U*>(p.vc) + to + cb) = b;
+      }
+    });
   }
 }
 
@@ -199,30 +257,28 @@ pkv_status fail(pkv_status st, const char* msg) {
   return st;
 }
 
+template <typename U, int VEC, bool F8>
+cudaError_t launch_v(const RopeParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  if (p.interleaved)
+    rope_write_kernel<U, VEC, F8, true><<<grid, kWarps * 32, smem, s>>>(p);
+  else
+    rope_write_kernel<U, VEC, F8, false><<<grid, kWarps * 32, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename U, bool F8>
 cudaError_t launch(const RopeParams& p0, bool vec, int sms, cudaStream_t s) {
   RopeParams p = p0;
   constexpr int kV = 16 / sizeof(U);
-  const int V = vec ? kV : 1;
-  const int units = p.half / V + (p.D - 2 * p.half) / V;
-  dim3 block((unsigned)(units < kThreads ? units : kThreads), 1, 1);
-  block.y = kThreads / block.x;
-  // one token a CTA until there are a few waves of them
-  int64_t per = p.T / ((int64_t)sms * 16);
-  per = per < 1 ? 1 : per > kMaxTokens ? kMaxTokens : per;
-  p.tokens_per_cta = (int)per;
-  const int64_t ctas = (p.T + per - 1) / per;
-  const int heads = p.Hq + 2 * p.Hkv;
-  // few tokens: a token's heads are spread over several CTAs
-  int split = 1;
-  while (ctas * split < sms && split * (int)block.y < heads) split *= 2;
-  dim3 grid((unsigned)ctas, (unsigned)split, 1);
-  const size_t smem = (size_t)per * p.half * sizeof(float2);
-  if (vec)
-    rope_write_kernel<U, kV, F8><<<grid, block, smem, s>>>(p);
-  else
-    rope_write_kernel<U, 1, F8><<<grid, block, smem, s>>>(p);
-  return cudaGetLastError();
+  const int places = (p.D / (vec ? kV : 1) + 1) / 2, side = places < 32 ? 32 / places : 1;
+  // few tokens: a token's heads are spread over several warps, down to one
+  // load of each lane
+  const int most = (std::max(p.Hq, p.Hkv) + side - 1) / side;
+  p.splits = 1;
+  while (p.T * p.splits < (int64_t)sms * 8 && p.splits < most) p.splits *= 2;
+  const dim3 grid((unsigned)((p.T * p.splits + kWarps - 1) / kWarps));
+  const size_t smem = (size_t)kWarps * p.half * sizeof(float2);
+  return vec ? launch_v<U, kV, F8>(p, grid, smem, s) : launch_v<U, 1, F8>(p, grid, smem, s);
 }
 
 pkv_status rope_write(RopeParams p, int64_t num_blocks, int block_size, int rotary, pkv_dtype dtype, bool f8,

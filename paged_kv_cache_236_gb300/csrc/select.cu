@@ -3,12 +3,21 @@
 // the last num_recent and the highest between, in ascending position order.
 //
 // A radix select: the scores map to 32-bit keys whose unsigned order is
-// theirs (NaN lowest, -0 as +0); four passes of 8-bit histograms over the
+// theirs (NaN lowest, -0 as +0); histograms of 11, 11 and 10 bits over the
 // middle positions narrow down the value of the last key kept and how many
-// equal to it are kept; one more pass writes the kept positions in order,
+// equal to it are kept; a last pass writes the kept positions in order,
 // taking equals from the lowest position.
+//
+// Latency-bound: a (sequence, head) has a few thousand scores.  Its keys are
+// read from memory once and kept in shared memory for the four passes over
+// them; long rows are cut over the blocks of a cluster, which add up their
+// histograms and counts through distributed shared memory.  The first digit
+// takes 11 bits (sign, exponent, two bits of mantissa) so that scores of one
+// magnitude do not all meet in one counter.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "paged_kv_budget.h"
 #include "pkv_device.cuh"
@@ -17,7 +26,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kHeld = 16384;     // keys of a block kept in shared memory, at most
+constexpr int kPerBlock = 8192;  // scores a block takes before a cluster is made larger
+constexpr int kMaxCluster = 8;
+constexpr int kAhead = 8;        // scores a thread loads at a time
 
 struct SelectParams {
   const float* scores;
@@ -25,6 +38,7 @@ struct SelectParams {
   const int32_t* lens;
   int32_t* kept;
   int Hkv, num_rows, max_len, budget, sink, recent;
+  int cluster, held;  // blocks of a (sequence, head); keys of shared memory each has
   int* err;
 };
 
@@ -44,89 +58,207 @@ __device__ __forceinline__ int warp_scan(int x, int lane) {  // inclusive
   return x;
 }
 
+__device__ __forceinline__ void cluster_sync(int cluster) {
+  if (cluster == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The ints at `p` (this block's shared memory) in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(const int* p, int rank) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  return at;
+}
+__device__ __forceinline__ int peer_int(const int* p, int rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(peer_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ int4 peer_int4(const int* p, int rank) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(peer_addr(p, rank))
+               : "memory");
+  return v;
+}
+
+// kThreads: 128 where a row has at most 4096 scores (what a block does for a
+// row whatever its length, the histograms' bins above all, is then half of
+// the work: 64 x 8 rows of 512 to 4096 scores take 18 us with 512 threads),
+// 512 for longer rows.
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
-  __shared__ int hist[256];
-  __shared__ int wsum[2][32];
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kPer = kBins / kThreads;        // bins of a thread
+  extern __shared__ uint32_t keys[];            // [held]
+  __shared__ __align__(16) int hist[2][kBins];  // this block's counts (by digit parity; peers read them)
+  __shared__ int sum[2 * kWarps];
+  __shared__ int wsum[kWarps];
+  __shared__ int counts[2];  // this block's keys above / equal to the last one kept (peers read them)
   __shared__ int s_bin, s_need;
-  const int s = blockIdx.x / p.Hkv, h = blockIdx.x - s * p.Hkv;
+  const int block = p.cluster == 1 ? 0 : blockIdx.x % p.cluster;
+  const int sh = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
+  const int s = sh / p.Hkv, h = sh - s * p.Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int32_t* out = p.kept + (int64_t)blockIdx.x * p.budget;
+  int32_t* out = p.kept + (int64_t)sh * p.budget;
   const int row = p.rows ? p.rows[s] : s;
   int L = p.lens[s];
   if (row < 0 || row >= p.num_rows || L < 0 || L > p.max_len) {
-    if (tid == 0 && row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
+    if (tid == 0 && block == 0 && row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
     L = 0;
   }
+  const int all = p.cluster * kThreads, me = block * kThreads + tid;
   if (L <= p.budget) {
-    for (int i = tid; i < p.budget; i += kThreads) out[i] = i < L ? i : -1;
-    return;
+    for (int i = me; i < p.budget; i += all) out[i] = i < L ? i : -1;
+    return;  // all blocks of the cluster alike
   }
-  const float* sc = p.scores + ((int64_t)row * p.Hkv + h) * p.max_len;
-  const int lo = p.sink, hi = L - p.recent;  // lo <= hi: sink + recent <= budget < L
-  int need = p.budget - p.sink - p.recent;   // of the hi - lo > need middle positions
-  for (int i = tid; i < p.sink; i += kThreads) out[i] = i;
-  for (int i = tid; i < p.recent; i += kThreads) out[p.budget - p.recent + i] = hi + i;
+  int need = p.budget - p.sink - p.recent;  // of the L - sink - recent > need middle positions
+  for (int i = me; i < p.sink; i += all) out[i] = i;
+  for (int i = me; i < p.recent; i += all) out[p.budget - p.recent + i] = L - p.recent + i;
   if (need == 0) return;
-  uint32_t prefix = 0, mask = 0;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    for (int i = lo + tid; i < hi; i += kThreads) {
-      const uint32_t k = key_of(sc[i]);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {
-      // bins from the highest down, 8 a lane: the bin holding the need-th key
-      int c[8], sum = 0;
+  // this block's part of the middle: positions lo .. hi - 1
+  const int middle = L - p.recent - p.sink, per = (middle + p.cluster - 1) / p.cluster;
+  const int lo = p.sink + min(middle, block * per), hi = p.sink + min(middle, (block + 1) * per);
+  const float* sc = p.scores + ((int64_t)row * p.Hkv + h) * p.max_len + lo;
+  const int n = hi - lo, held = min(n, p.held);
+  for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  __syncthreads();
+  // digit 0 is counted as the keys arrive
+  for (int i0 = tid; i0 < n; i0 += kAhead * kThreads) {
+    float x[kAhead];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        c[j] = hist[255 - (lane * 8 + j)];
-        sum += c[j];
+    for (int j = 0; j < kAhead; ++j) x[j] = i0 + j * kThreads < n ? sc[i0 + j * kThreads] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < n) {
+        const uint32_t k = key_of(x[j]);
+        if (i < held) keys[i] = k;
+        atomicAdd(&hist[0][k >> 21], 1);
       }
-      const int incl = warp_scan(sum, lane);
-      int before = incl - sum;
-      if (before < need && need <= incl) {
+    }
+  }
+  auto key = [&](int i) { return i < held ? keys[i] : key_of(sc[i]); };
+  uint32_t prefix = 0, mask = 0;
+#pragma unroll 1
+  for (int digit = 0; digit < 3; ++digit) {
+    const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
+    const int bins = digit == 2 ? 1024 : 2048;
+    int* mine = hist[digit & 1];
+    if (digit > 0) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kThreads) {
+        const uint32_t k = key(i);
+        if ((k & mask) == prefix) atomicAdd(&mine[(k >> shift) & (bins - 1)], 1);
+      }
+    }
+    cluster_sync(p.cluster);  // the counts of every block are complete
+    // thread t: the cluster's counts of kPer bins, the highest first
+    int c[kPer], total = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (before < need && need <= before + c[j]) {
-            s_bin = 255 - (lane * 8 + j);
-            s_need = need - before;
+    for (int j = 0; j < kPer; ++j) c[j] = 0;
+    const int top = bins - 1 - kPer * tid;
+    if (top >= 0) {
+#pragma unroll
+      for (int j = 0; j < kPer; j += 4) {
+        const int* at = &mine[top - j - 3];
+        if (p.cluster == 1) {
+          const int4 v = *reinterpret_cast<const int4*>(at);
+          c[j] = v.w;
+          c[j + 1] = v.z;
+          c[j + 2] = v.y;
+          c[j + 3] = v.x;
+        } else {
+          int4 v[kMaxCluster];
+#pragma unroll
+          for (int b = 0; b < kMaxCluster; ++b) v[b] = b < p.cluster ? peer_int4(at, b) : make_int4(0, 0, 0, 0);
+#pragma unroll
+          for (int b = 0; b < kMaxCluster; ++b) {
+            c[j] += v[b].w;
+            c[j + 1] += v[b].z;
+            c[j + 2] += v[b].y;
+            c[j + 3] += v[b].x;
           }
-          before += c[j];
         }
       }
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) total += c[j];
     }
+    const int incl = warp_scan(total, lane);
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int before = incl - total;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (before < need && need <= before + total) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (before < need && need <= before + c[j]) {
+          s_bin = top - j;
+          s_need = need - before;
+        }
+        before += c[j];
+      }
+    }
+    // the other digit's counts, read by peers before the barrier above, start again
+    if (digit == 1)
+      for (int i = tid; i < kBins; i += kThreads) hist[0][i] = 0;
     __syncthreads();
     prefix |= (uint32_t)s_bin << shift;
-    mask |= 255u << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
     need = s_need;
   }
-  // `need` of the keys equal to `prefix` are kept, from the lowest position
-  int base = p.sink, eq_seen = 0;
-  for (int i0 = lo; i0 < hi; i0 += kThreads) {
-    const int i = i0 + tid;
-    const uint32_t k = i < hi ? key_of(sc[i]) : 0u;
-    const bool gt = i < hi && k > prefix, eq = i < hi && k == prefix;
-    const uint32_t beq = __ballot_sync(0xffffffffu, eq);
-    const uint32_t below = (1u << lane) - 1u;
-    if (lane == 0) wsum[0][warp] = __popc(beq);
-    __syncthreads();
-    int w = wsum[0][lane];
-    int inc = warp_scan(w, lane);
-    const int eq_total = __shfl_sync(0xffffffffu, inc, 31);
-    const int eq_rank = eq_seen + __shfl_sync(0xffffffffu, inc - w, warp) + __popc(beq & below);
-    const bool take = gt || (eq && eq_rank < need);
-    const uint32_t bt = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) wsum[1][warp] = __popc(bt);
-    __syncthreads();
-    w = wsum[1][lane];
-    inc = warp_scan(w, lane);
-    const int total = __shfl_sync(0xffffffffu, inc, 31);
-    const int at = base + __shfl_sync(0xffffffffu, inc - w, warp) + __popc(bt & below);
-    if (take) out[at] = i;
-    base += total;
-    eq_seen += eq_total;
+  // `need` of the keys equal to `prefix` are kept, from the lowest position.
+  // A warp takes a run of the block's positions: it counts its keys above and
+  // equal, then knows where its first kept one goes, and writes.
+  const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
+  const int a = min(n, warp * run), b = min(n, a + run);
+  int gt = 0, eq = 0;
+#pragma unroll 4
+  for (int i = a + lane; i < b; i += 32) {
+    const uint32_t k = key(i);
+    gt += k > prefix;
+    eq += k == prefix;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    gt += __shfl_xor_sync(0xffffffffu, gt, d);
+    eq += __shfl_xor_sync(0xffffffffu, eq, d);
+  }
+  if (lane == 0) {
+    sum[2 * warp] = gt;
+    sum[2 * warp + 1] = eq;
+  }
+  __syncthreads();
+  int gt0 = 0, eq0 = 0;  // before this warp's run
+  for (int w = 0; w < warp; ++w) {
+    gt0 += sum[2 * w];
+    eq0 += sum[2 * w + 1];
+  }
+  if (p.cluster > 1) {
+    if (tid == kThreads - 1) {  // the last warp: the block's totals
+      counts[0] = gt0 + gt;
+      counts[1] = eq0 + eq;
+    }
+    cluster_sync(p.cluster);
+    for (int r = 0; r < block; ++r) {
+      gt0 += peer_int(&counts[0], r);
+      eq0 += peer_int(&counts[1], r);
+    }
+    cluster_sync(p.cluster);  // a block's shared memory outlives its readers
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = a; i0 < b; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < b ? key(i) : 0u;
+    const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
+    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
+    const int g = gt0 + __popc(mg & below), e = eq0 + __popc(me_ & below);
+    if (is_gt || (is_eq && e < need)) out[p.sink + g + min(e, need)] = lo + i;
+    gt0 += __popc(mg);
+    eq0 += __popc(me_);
   }
 }
 
@@ -154,12 +286,41 @@ extern "C" pkv_status paged_kv_select(const float* scores, const int32_t* score_
   if (num_seqs == 0) return PKV_OK;
   if (!scores || !context_lens || !kept) return fail(PKV_ERR_INVALID_ARG, "null pointer");
   SelectParams p{scores, score_rows, context_lens, kept, num_kv_heads, num_rows, max_len, budget,
-                 num_sink, num_recent, nullptr};
+                 num_sink, num_recent, 1, 0, nullptr};
   int sms = 0;
   const pkv_status st = device_state(&sms, &p.err);
   if (st != PKV_OK) return st;
-  select_kernel<<<(unsigned)((int64_t)num_seqs * num_kv_heads), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  // blocks of a (sequence, head) by the longest row there can be
+  while (p.cluster < kMaxCluster && (int64_t)p.cluster * kPerBlock < max_len) p.cluster *= 2;
+  p.held = std::min((max_len + p.cluster - 1) / p.cluster, kHeld);
+  const int64_t grid = (int64_t)num_seqs * num_kv_heads * p.cluster;
+  if (grid > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "too many sequences and heads");
+  const size_t smem = (size_t)p.held * sizeof(uint32_t);
+  cudaError_t e = cudaSuccess;
+  if (p.cluster > 1 || p.held > kPerBlock / 2) {  // with the static arrays, past the 48 KB every kernel may use
+    static unsigned long long done_mask = 0;  // devices set up
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_error(e, "cudaGetDevice");
+    if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << (dev & 63)))) {
+      e = cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kHeld * (int)sizeof(uint32_t));
+      if (e != cudaSuccess) return cuda_error(e, "paged_kv_select set-up");
+      __atomic_fetch_or(&done_mask, 1ull << (dev & 63), __ATOMIC_RELEASE);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  const bool small = p.cluster == 1 && max_len <= kPerBlock / 2;
+  cfg.blockDim = dim3(small ? 128 : 512);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  e = small ? cudaLaunchKernelEx(&cfg, select_kernel<128>, p) : cudaLaunchKernelEx(&cfg, select_kernel<512>, p);
   if (e != cudaSuccess) return cuda_error(e, "paged_kv_select launch");
   return PKV_OK;
 }
