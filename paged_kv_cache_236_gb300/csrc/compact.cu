@@ -10,16 +10,17 @@
 // them at a time: load the round into registers, barrier, store it.  Loads of
 // later rounds may run ahead of the stores freely.
 //
-// The rows of one head are independent of the other heads', and K, V and the
-// scores of each other: each (sequence, head, array) is a cluster's work.  With
-// few of those the cluster has several blocks, which share each round (a block
-// its rows in order, the blocks in order) and pass a cluster barrier between
-// its loads and its stores.
+// The heads' rows are independent of each other, and the scores of the rows: a
+// (sequence, head)'s rows, K and V together (one address computation), are
+// one cluster's work and its scores another's.  With few of those a cluster
+// has several blocks, which share each round (a block its rows in order, the
+// blocks in order) and pass a cluster barrier between loads and stores.
 //
 // HBM-bound: every kept row is read and written once; rows that stay where
-// they are (the kept prefix) are neither read nor written.  The next round's
-// rows are loaded before the barrier of the current one, and the positions of
-// the round after that.
+// they are (the kept prefix) are neither read nor written.  A round's loads
+// are issued before the stores of the round before it; the arrival that
+// publishes them comes before those stores too, since a releasing arrival
+// waits for the stores already under way.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,8 +31,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kVecs = 4;  // 16-byte vectors of one row (scores: values) a thread holds per round
+constexpr int kMaxThreads = 256;
+constexpr int kVecs = 4;  // 16-byte vectors of one K and one V row (scores: values) a thread holds per round
 
 struct CompactParams {
   uint8_t* kc;
@@ -51,30 +52,34 @@ struct CompactParams {
 // Threads that share a row of `vecs` 16-byte vectors, at most kVecs each.
 __host__ __device__ constexpr int row_team(int vecs) { return (vecs + kVecs - 1) / kVecs; }
 
-// Every thread of the cluster has performed its loads so far; stores of any
-// of them may follow.
-__device__ __forceinline__ void round_barrier(int cluster) {
-  if (cluster == 1) {
+// The barrier of a round in two halves: arrive() after this thread's loads of
+// the round, wait() before its stores: every thread of the cluster (block) has
+// then performed its loads.  One block: the whole barrier is the second half.
+__device__ __forceinline__ void round_arrive(int cluster) {
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void round_wait(int cluster) {
+  if (cluster > 1)
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
     __syncthreads();
-  } else {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
 }
 
 // What a thread moves: Mover::Slot holds its part of `kTokens` kept tokens on
 // their way, load() starts token i of them (kept token r, from position src;
 // src < 0: none), store() ends it.
 //
-// Rows: up to four 16-byte vectors of one token's row, `apart` bytes from one
-// another so that the threads of a row read whole sectors side by side; one
-// address computation serves them.
+// Rows: up to four 16-byte vectors of one token's K and V rows each, `apart`
+// bytes from one another so that the threads of a row read whole sectors side
+// by side.
 struct RowMover {
   static constexpr int kTokens = 1;
   struct Slot {
-    int4 x[kVecs];
-    uint8_t* to;  // null: nothing to store
+    int4 k[kVecs], v[kVecs];
+    int64_t to;  // byte offset in the pools; < 0: nothing to store
   };
-  uint8_t* pool;
+  uint8_t* kc;
+  uint8_t* vc;
   const int32_t* bt;
   const int32_t* dt;
   int64_t col, token_bytes, num_blocks;
@@ -82,7 +87,7 @@ struct RowMover {
   bool bad;
 
   __device__ __forceinline__ void load(Slot& v, int, int r, int src) {
-    v.to = nullptr;
+    v.to = -1;
     if (src < 0) return;
     int sb, so, db, dof;
     if (bs_log >= 0) {
@@ -103,19 +108,25 @@ struct RowMover {
     const int64_t from = ((int64_t)sblk * bs + so) * token_bytes + col;
     const int64_t dst = ((int64_t)dblk * bs + dof) * token_bytes + col;
     if (d_ok && !(s_ok && from == dst)) {
-      v.to = pool + dst;
+      v.to = dst;
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
-        v.x[i] = make_int4(0, 0, 0, 0);
-        if (s_ok && i < vecs) v.x[i] = *reinterpret_cast<const int4*>(pool + from + i * apart);
+        v.k[i] = v.v[i] = make_int4(0, 0, 0, 0);
+        if (s_ok && i < vecs) {
+          v.k[i] = *reinterpret_cast<const int4*>(kc + from + i * apart);
+          v.v[i] = *reinterpret_cast<const int4*>(vc + from + i * apart);
+        }
       }
     }
   }
   __device__ __forceinline__ void store(const Slot& v) {
-    if (!v.to) return;
+    if (v.to < 0) return;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if (i < vecs) *reinterpret_cast<int4*>(v.to + i * apart) = v.x[i];
+      if (i < vecs) {
+        *reinterpret_cast<int4*>(kc + v.to + i * apart) = v.k[i];
+        *reinterpret_cast<int4*>(vc + v.to + i * apart) = v.v[i];
+      }
   }
 };
 
@@ -146,7 +157,7 @@ struct ScoreMover {
   }
 };
 
-// The rounds of one (sequence, head, array).  A round is `per` tokens for each
+// The rounds of one (sequence, head)'s rows or scores.  A round is `per` tokens for each
 // block of the cluster; this thread moves tokens base + i * lanes + mine of
 // its block's (mine < 0: it moves none, but keeps the barriers).
 template <typename Mover>
@@ -172,40 +183,49 @@ __device__ __forceinline__ bool move_rounds(Mover& m, const int32_t* kept, int b
   int src[N];
   Slot now, next;
   positions(0, src);
+  if (__ldg(kept) < 0) return false;
   load(0, src, now);
+  round_arrive(cluster);
   positions(round, src);
-  for (int base = 0; base < budget && __ldg(kept + base) >= 0; base += round) {
-    load(base + round, src, next);
-    positions(base + 2 * round, src);
-    round_barrier(cluster);  // every load of this round has been performed
+  for (int base = 0;; base += round) {
+    const bool more = base + round < budget && __ldg(kept + base + round) >= 0;
+    if (more) {
+      load(base + round, src, next);
+      positions(base + 2 * round, src);
+    }
+    round_wait(cluster);  // every load of the round at base has been performed
+    if (!more) break;
+    round_arrive(cluster);
     m.store(now);
     now = next;
   }
+  m.store(now);
   return bad_order;
 }
 
-__global__ void __launch_bounds__(kThreads, 3) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 2) compact_kernel(const CompactParams p) {
   const int block = p.cluster == 1 ? 0 : blockIdx.x % p.cluster;
-  const int64_t work = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
-  const int per = p.scores ? 3 : 2;
-  const int sh = (int)(work / per), part = (int)(work - (int64_t)sh * per);
+  const int work = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
+  const int threads = blockDim.x;
+  const int sh = p.scores ? work >> 1 : work;
   const int s = sh / p.Hkv, h = sh - s * p.Hkv;
   const int32_t* kept = p.kept + (int64_t)sh * p.budget;
-  if (part == 2) {  // the running scores
+  if (p.scores && (work & 1)) {  // the running scores
     const int row = p.rows ? p.rows[s] : s;
     if (row < 0 || row >= p.num_rows) {
       if (row >= 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
       return;
     }
     ScoreMover m{p.scores + ((int64_t)row * p.Hkv + h) * p.max_len, p.max_len, false};
-    move_rounds(m, kept, p.budget, p.cluster, block, kThreads, threadIdx.x);
+    move_rounds(m, kept, p.budget, p.cluster, block, threads, threadIdx.x);
     if (m.bad) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
     return;
   }
-  const int vecs = p.row_bytes / 16, team = row_team(vecs), lanes = kThreads / team;
+  const int vecs = p.row_bytes / 16, team = row_team(vecs), lanes = threads / team;
   const int mine = threadIdx.x / team, member = threadIdx.x - mine * team;
   const int32_t* bt = p.tables + (int64_t)s * p.max_blocks;
-  RowMover m{part ? p.vc : p.kc,
+  RowMover m{p.kc,
+             p.vc,
              bt,
              p.dst_tables ? p.dst_tables + (int64_t)s * p.max_blocks : bt,
              (int64_t)h * p.row_bytes + member * 16,
@@ -279,17 +299,19 @@ extern "C" pkv_status paged_kv_compact(void* k_cache, void* v_cache, const int32
   p.num_rows = num_rows;
   p.max_len = max_len;
   p.row_bytes = (int)row_bytes;
-  // Several blocks to a (sequence, head, array) while there are too few of
-  // them to keep the SMs' loads in flight, and each has rounds to share.
-  const int64_t units = (int64_t)num_seqs * num_kv_heads * (scores ? 3 : 2);
-  const int round = kThreads / row_team((int)(row_bytes / 16));
-  int cluster = 1;
-  while (cluster < 8 && units * cluster < 4 * sms && cluster * 2 * round <= budget) cluster *= 2;
+  // Enough (sequence, head)s: one block of 128 threads each, so that about as
+  // many are resident as there are (64 x 8 rows of 512 kept tokens).  Few: up
+  // to 8 blocks of 256 threads, while each has rounds to share.
+  const int64_t pairs = (int64_t)num_seqs * num_kv_heads, units = pairs * (scores ? 2 : 1);
+  const int team = row_team((int)(row_bytes / 16));
+  int threads = 128, cluster = 1;
+  if (pairs < 2 * sms || team > threads) threads = 256;
+  while (cluster < 8 && pairs * cluster < 2 * sms && cluster * 2 * (threads / team) <= budget) cluster *= 2;
   p.cluster = cluster;
   if (units * cluster > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "too many sequences and heads");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cluster));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -127,6 +127,17 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rope_write_kernel(const RopePa
   const int split = (int)(w - tok * p.splits);
   if (tok >= p.T) return;
   float2* trig = trig_all + warp * p.half;
+  // this token's rows on their way to L2 while the angles are computed
+  if (p.splits == 1) {
+    auto fetch = [&](const void* rows, int64_t stride, int heads) {
+      const char* at = static_cast<const char*>(rows) + tok * stride * (int64_t)sizeof(U);
+      for (int i = lane * 128; i < heads * p.D * (int)sizeof(U); i += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+    };
+    fetch(p.q, p.q_stride, p.Hq);
+    fetch(p.k, p.k_stride, p.Hkv);
+    fetch(p.v, p.v_stride, p.Hkv);
+  }
   const uint64_t pos = (uint64_t)p.positions[tok];
   int64_t slot = p.slots[tok];
   if (slot >= p.num_slots) {

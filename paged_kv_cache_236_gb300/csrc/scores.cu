@@ -43,6 +43,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFewThreads = 128;
+constexpr int kHeldSeqs = 256;
 
 __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
 #pragma unroll
@@ -53,42 +54,46 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
   return x;
 }
 
-// Exclusive prefix sum of v over the block, plus *carry, which moves on.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t* carry, int lane, int warp) {
-  const int64_t x = warp_scan(v, lane);
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    const int64_t w = warp_sums[lane], y = warp_scan(w, lane);
-    warp_sums[lane] = *carry + y - w;
-    __syncwarp();
-    if (lane == 31) *carry += y;
-  }
-  __syncthreads();
-  const int64_t r = warp_sums[warp] + x - v;
-  __syncthreads();
-  return r;
-}
+constexpr int kPlanThreads = 1024;
 
-__global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) {
-  __shared__ int64_t sums[32];
-  enum { kPart = 6, kLse, kLogit, kSums };
-  __shared__ int64_t carry[kSums];
+// One block; threads = sequences, in passes of the block's size.  The sums are
+// scanned within warps and then, one warp to a sum, over the warps.
+__global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScoreParams p) {
+  enum { kPart = 6, kLse, kSums };
+  __shared__ int64_t warp_sum[kSums + 1][32];
+  __shared__ int64_t carry[kSums + 1];  // the last: kept logits
   __shared__ int top[32];
   __shared__ int top_carry;  // the largest query_start_loc entry so far
   pdl_launch_dependents();  // few_kernel waits for this grid first of all
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kSums) carry[tid] = 0;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
+  if (tid <= kSums) carry[tid] = 0;
   if (tid == 0) top_carry = 0;
-  for (int64_t i = tid; i < 2 * (int64_t)p.B * p.Hkv + 2; i += 1024) p.tickets[i] = 0;
-  __syncthreads();
-  for (int s0 = 0; s0 < p.B; s0 += 1024) {
+  for (int64_t i = tid; i < 2 * (int64_t)p.B * p.Hkv + 2; i += threads) p.tickets[i] = 0;
+  // after a barrier: the exclusive sums over the warps of sums k0 .. k0 + n - 1, carried on
+  auto over_warps = [&](int k0, int n) {
+    __syncthreads();
+    for (int k = k0 + warp; k < k0 + n; k += warps) {
+      const int64_t w = lane < warps ? warp_sum[k][lane] : 0, x = warp_scan(w, lane);
+      const int64_t c = carry[k];
+      __syncwarp();
+      warp_sum[k][lane] = c + x - w;
+      if (lane == 31) carry[k] = c + x;
+    }
+    __syncthreads();
+  };
+  for (int s0 = 0; s0 < p.B; s0 += threads) {
     const int s = s0 + tid;
     SeqPlan sp{};
     sp.row = -1;
+    int a = 0, b = 0, L = 0;
+    if (s < p.B) {
+      a = p.qsl[s];
+      b = p.qsl[s + 1];
+      L = p.lens[s];
+      sp.row = p.rows ? p.rows[s] : s;
+    }
     // a sequence whose queries start below an earlier entry is invalid: the
     // valid ones' query ranges are disjoint, and so are their partials
-    const int a = s < p.B ? p.qsl[s] : 0;
     int high = a;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -97,24 +102,27 @@ __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) 
     }
     if (lane == 31) top[warp] = high;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) high = max(high, top[w]);
     high = max(high, top_carry);
+    for (int w = 0; w < warp; ++w) high = max(high, top[w]);
     if (s < p.B) {
-      const int b = p.qsl[s + 1], L = p.lens[s], n = b - a;
-      sp.row = p.rows ? p.rows[s] : s;
+      const int n = b - a;
       const bool bad = a < high || a < 0 || n < 0 || b > p.T || L < 0 || n > L || L > p.max_len ||
                        L > (int64_t)p.max_blocks * p.bs || sp.row >= p.num_rows;
       if (bad && sp.row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
       if (!bad && sp.row >= 0 && n > 0) {
         sp.L = L;
         sp.n = n;
-        sp.rows = n * p.G;  // n <= L <= 2^30 only for a batch of as many tokens: T * Hq fits 31 bits
+        sp.rows = n * p.G;  // n tokens of the batch's T, and T * Hq fits 31 bits
       }
     }
     const bool want_few = sp.n > 0 && sp.rows <= kFewRows;
     const int pad = sp.rows <= 2 ? 2 : sp.rows <= 4 ? 4 : sp.rows <= 8 ? 8 : 16;
     const int64_t logits = want_few ? (int64_t)p.Hkv * sp.L * pad : 0;
-    sp.logit = block_scan(logits, sums, &carry[kLogit], lane, warp);
+    int64_t x = warp_scan(logits, lane);
+    if (lane == 31) warp_sum[kSums][warp] = x;
+    over_warps(kSums, 1);
+    sp.logit = warp_sum[kSums][warp] + x - logits;
+    if (tid == threads - 1) top_carry = high;
     const bool few = want_few && sp.logit + logits <= p.logit_cap;
     sp.kind = sp.n == 0 ? 0 : few ? kFew : p.tensor ? kTensor : kOther;
     sp.pad = few ? pad : 0;
@@ -122,37 +130,44 @@ __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) 
     sp.chunks = (sp.L + chunk - 1) / chunk;
     sp.tiles = sp.kind == kTensor ? (sp.n + p.tile_tok - 1) / p.tile_tok : 0;
     const int64_t groups = (sp.rows + kRowGroup - 1) / kRowGroup, work = (int64_t)p.Hkv * sp.chunks;
-    int64_t units[6] = {0, 0, 0, 0, 0, 0};
-    int64_t parts = work * sp.rows;
+    int64_t v[kSums] = {0, 0, 0, 0, 0, 0, work * sp.rows, (int64_t)p.Hkv * sp.rows};
     if (sp.kind == kFew) {
-      units[kFewStat] = work;
-      units[kFewCol] = (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk);
+      v[kFewStat] = work;
+      v[kFewCol] = (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk);
     } else if (sp.kind == kOther) {
-      units[kStat] = work * groups;
-      units[kCol] = work;
+      v[kStat] = work * groups;
+      v[kCol] = work;
     } else if (sp.kind == kTensor) {
       // one row tile: the columns of a range of keys; more: those of one 128-key tile
-      units[kTcStat] = work * sp.tiles;
-      units[kTcCol] = sp.tiles == 1 ? work : (int64_t)p.Hkv * ((sp.L + 127) / 128);
-      parts *= 2;  // each of the two epilogue groups writes its own
+      v[kTcStat] = work * sp.tiles;
+      v[kTcCol] = sp.tiles == 1 ? work : (int64_t)p.Hkv * ((sp.L + 127) / 128);
+      v[kPart] *= 2;  // each of the two epilogue groups writes its own
     }
+    int64_t at[kSums];
 #pragma unroll
-    for (int k = 0; k < 6; ++k) {
-      const int64_t at = block_scan(units[k], sums, &carry[k], lane, warp);
-      if (s < p.B) p.off[k][s] = at;
+    for (int k = 0; k < kSums; ++k) {
+      const int64_t y = warp_scan(v[k], lane);
+      at[k] = y - v[k];
+      if (lane == 31) warp_sum[k][warp] = y;
     }
-    sp.part = block_scan(parts, sums, &carry[kPart], lane, warp);
-    sp.lse = block_scan((int64_t)p.Hkv * sp.rows, sums, &carry[kLse], lane, warp);
-    if (s < p.B) p.plan[s] = sp;
-    if (tid == 1023) top_carry = high;
+    over_warps(0, kSums);
+    if (s < p.B) {
+#pragma unroll
+      for (int k = 0; k < 6; ++k) p.off[k][s] = warp_sum[k][warp] + at[k];
+      sp.part = warp_sum[kPart][warp] + at[kPart];
+      sp.lse = warp_sum[kLse][warp] + at[kLse];
+      p.plan[s] = sp;
+    }
     __syncthreads();
   }
   if (tid < 6) p.off[tid][p.B] = carry[tid];
-  __syncthreads();
-  // places of the column items among the tensor-core kernel's items
-  for (int s = tid; s < p.B; s += 1024) {
-    const int64_t after = s + 1 < p.B ? p.off[kTcStat][s + 1] : carry[kTcStat];
-    p.off[kTcAt][s] = min(carry[kTcStat], after + p.tc_lag) + p.off[kTcCol][s];
+  if (!p.tensor) return;
+  // places of the column items among the tensor-core kernel's items (this
+  // thread wrote its own sequences' offsets)
+  for (int s = tid; s < p.B; s += threads) {
+    const SeqPlan sp = p.plan[s];
+    const int64_t mine = sp.kind == kTensor ? (int64_t)p.Hkv * sp.chunks * sp.tiles : 0;
+    p.off[kTcAt][s] = min(carry[kTcStat], p.off[kTcStat][s] + mine + p.tc_lag) + p.off[kTcCol][s];
   }
 }
 
@@ -164,15 +179,30 @@ __global__ void __launch_bounds__(1024) plan_scores_kernel(const ScoreParams p) 
 // g + 8, rows 2t and 2t + 1 (and 8 more of each with two row tiles).
 //
 // The contraction may run over d in any order, so lane t of a key takes whole
-// 16-byte pieces of its row, straight from global memory to the fragment
-// registers, and the q fragments follow the same order: no shared memory.
+// 16-byte pieces of its row for its fragments, and the q fragments follow the
+// same order.
+//
+// K comes through a ring of 16-key tiles in shared memory that is the warp's
+// own, by asynchronous copies issued kStages tiles ahead, across units: while
+// a warp ends one unit (partials, fence, ticket) the first tiles of its next
+// are on their way.  With the tiles loaded into registers, two ahead but none
+// across units, the decode batch took 95 us instead of FEWTIME: a unit of 32 KB is
+// 12 us of streaming at the rate a warp gets, and about 10 us of its end and
+// its successor's start were not covered.
+//
+// Row r's 16-byte piece i of a tile sits at piece i ^ 4 (r & 1), so that the
+// eight lanes (two keys, four pieces) of a shared-memory read take all banks.
 
-__device__ __forceinline__ uint4 ld_row16(const void* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -200,11 +230,11 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
 // bf16 rows: 16-byte piece c of lane t is d = 32 c + 8 t .. + 7, two k-steps.
 template <int D>
 struct DotBf16 {
-  static constexpr int kPieces = D / 32;   // 16-byte pieces of a key a lane holds
-  static constexpr int kPieceStride = 64;  // bytes between them
+  static constexpr int kPieces = D / 32;  // 16-byte pieces of a key a lane holds
   static constexpr int kRowBytes = D * 2;
   static constexpr int kQBytes = D * 2;
-  static constexpr bool kAhead = true;     // a tile is loaded while another is in use
+  static constexpr int kStages = D == 128 ? 3 : 6;  // tiles of a warp's ring
+  static constexpr int kBlocks = 4;                 // of an SM
   template <int NT>
   struct Q {
     uint4 w[NT][kPieces];
@@ -233,10 +263,10 @@ struct DotBf16 {
 // (|q| < 65504; bits below 2^-24 are rounded away).
 struct DotFp8 {
   static constexpr int kPieces = 2;
-  static constexpr int kPieceStride = 64;
   static constexpr int kRowBytes = 128;
   static constexpr int kQBytes = 256;
-  static constexpr bool kAhead = true;
+  static constexpr int kStages = 6;
+  static constexpr int kBlocks = 4;
   template <int NT>
   struct Q {
     uint32_t w[NT][16];
@@ -276,10 +306,10 @@ struct DotFp8 {
 template <int D>
 struct DotF32 {
   static constexpr int kPieces = D / 16;
-  static constexpr int kPieceStride = 64;
   static constexpr int kRowBytes = D * 4;
   static constexpr int kQBytes = D * 4;
-  static constexpr bool kAhead = false;
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kBlocks = D == 128 ? 3 : 4;
   template <int NT>
   struct Q {
     const float* row[NT];  // this lane's row g of each tile, exchanged by shuffles
@@ -325,55 +355,90 @@ struct DotF32 {
   }
 };
 
-// A key's logits against `rows` padded rows start at (kv head, key) * pad.
+// One unit of a warp's work: a head's chunk of keys (stats) or of columns.
+enum { kUnitStat, kUnitCol, kUnitEnd };
+struct Unit {
+  int kind, s, h, c;
+  int kb, ke;  // keys kb .. ke - 1 (stats)
+  int blk;     // lane i: physical block of the chunk's i-th block, -1 outside the pool
+};
+
+// Issues the copies of the 16 keys at j (of a stats unit) into a ring tile;
+// keys past the end and blocks outside the pool become zeros.  lane_src: the
+// lane's place in a block (kv head, first key, piece).
+template <typename Dot>
+__device__ __forceinline__ void fetch_tile(const ScoreParams& p, const Unit& u, int j, uint32_t tile, int64_t lane_src,
+                                           int64_t token_bytes, int lane) {
+  constexpr int kChunks = Dot::kRowBytes / 16;                // of a key
+  constexpr int kRows = 32 / kChunks < 1 ? 1 : 32 / kChunks;  // keys the warp copies at a time
+  const int row0 = lane / kChunks, piece = lane % kChunks;
+  const uint32_t dst = tile + row0 * Dot::kRowBytes;
+  const uint32_t even = (uint32_t)piece << 4, odd = (uint32_t)(piece ^ 4) << 4;
+  const uint32_t mine = kRows == 1 ? even : row0 & 1 ? odd : even;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {  // 8 keys lie in one block
+    const int j8 = j + 8 * half;
+    const int b = __shfl_sync(0xffffffffu, u.blk, ((j8 - u.kb) >> p.bs_log) & 31);
+    const uint8_t* src = static_cast<const uint8_t*>(p.kc) + lane_src +
+                         (((int64_t)b << p.bs_log) + (j8 & (p.bs - 1))) * token_bytes;
+    if (b >= 0 && j8 + 8 <= u.ke) {
+#pragma unroll
+      for (int i = 0; i < 8; i += kRows) {
+        copy16(dst + (half * 8 + i) * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), src);
+        src += kRows * token_bytes;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i += kRows) {
+        const bool ok = b >= 0 && j8 + i + row0 < u.ke;
+        copy16(dst + (half * 8 + i) * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), ok ? src : p.kc, ok);
+        src += kRows * token_bytes;
+      }
+    }
+  }
+}
+
+// The warp's running state of a stats unit.
 template <typename Dot, int NT>
-__device__ __forceinline__ void few_stats(const ScoreParams& p, const SeqPlan& sp, int s, int h, int c, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  const int qstart = p.qsl[s];
+struct Stats {
   typename Dot::template Q<NT> q;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g, i = r / p.G;
-    const void* row = r < sp.rows ? static_cast<const uint8_t*>(p.q) +
-                                        ((int64_t)(qstart + i) * p.Hq + h * p.G + (r - i * p.G)) * Dot::kQBytes
-                                  : nullptr;
-    Dot::load_q(q, nt, row, t);
-  }
-  // rows of this lane: nt * 8 + 2t and + 1; keys they see
-  int vis[NT][2];
+  int vis[NT][2];  // keys that rows nt * 8 + 2t, + 1 see
   float m[NT][2], l[NT][2];
+
+  __device__ __forceinline__ void begin(const ScoreParams& p, const SeqPlan& sp, const Unit& u, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int qstart = __ldg(p.qsl + u.s);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g, i = r / p.G;
+      const void* row = r < sp.rows ? static_cast<const uint8_t*>(p.q) +
+                                          ((int64_t)(qstart + i) * p.Hq + u.h * p.G + (r - i * p.G)) * Dot::kQBytes
+                                    : nullptr;
+      Dot::load_q(q, nt, row, t);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = nt * 8 + 2 * t + e;
-      vis[nt][e] = p.causal ? min(sp.L, sp.L - sp.n + r / p.G + 1) : sp.L;
-      m[nt][e] = -CUDART_INF_F;
-      l[nt][e] = 0.f;
-    }
-  const int kb = c * kFewChunk, ke = min(sp.L, kb + kFewChunk);
-  // block ids of the chunk, one a lane (kFewChunk / bs <= 16)
-  const int nblk = (ke - kb + p.bs - 1) / p.bs;
-  int blk = -1;
-  if (lane < nblk) {
-    blk = p.tables[(int64_t)s * p.max_blocks + kb / p.bs + lane];
-    if (blk < 0 || blk >= p.num_blocks) {
-      raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
-      blk = -1;
+      for (int e = 0; e < 2; ++e) {
+        vis[nt][e] = p.causal ? min(sp.L, sp.L - sp.n + (nt * 8 + 2 * t + e) / p.G + 1) : sp.L;
+        m[nt][e] = -CUDART_INF_F;
+        l[nt][e] = 0.f;
+      }
     }
   }
-  const uint8_t* base = static_cast<const uint8_t*>(p.kc) + (int64_t)h * Dot::kRowBytes + t * 16;
-  const int64_t token_bytes = (int64_t)p.Hkv * Dot::kRowBytes;
-  auto load = [&](int j, uint4 (&k)[Dot::kPieces]) {  // key j's pieces; zeros past the end or outside the pool
-    const int rel = j - kb;
-    const int b = __shfl_sync(0xffffffffu, blk, (rel >> p.bs_log) & 31);
-    const bool ok = j < ke && b >= 0;
-    const uint8_t* src = base + (((int64_t)b << p.bs_log) + (j & (p.bs - 1))) * token_bytes;
+
+  // The 16 keys at j, in `tile`; z: where the lane keeps its logits of key
+  // j + g (null: its rows are past the padding), those of j + g + 8 follow at
+  // z8.  kAll: every row sees all 16 keys.
+  template <bool kAll>
+  __device__ __forceinline__ void use(const ScoreParams& p, int j, int ke, const uint8_t* tile, float* z, int z8, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint4 k0[Dot::kPieces], k1[Dot::kPieces];
+    // piece 4i + t: the swizzle flips bit 2 of it, the low bit of i
+    const uint8_t* row = tile + g * Dot::kRowBytes + (t << 4);
+    const uint8_t* rows[2] = {row + (g & 1) * 64, row + ((g & 1) ^ 1) * 64};
 #pragma unroll
-    for (int i = 0; i < Dot::kPieces; ++i) k[i] = ok ? ld_row16(src + i * Dot::kPieceStride) : make_uint4(0, 0, 0, 0);
-  };
-  float* zout = p.logit + sp.logit + (int64_t)h * sp.L * sp.pad;
-  auto use = [&](int j, const uint4 (&k0)[Dot::kPieces], const uint4 (&k1)[Dot::kPieces]) {
+    for (int i = 0; i < Dot::kPieces; ++i) {
+      k0[i] = *reinterpret_cast<const uint4*>(rows[i & 1] + (i >> 1) * 128);
+      k1[i] = *reinterpret_cast<const uint4*>(rows[i & 1] + (i >> 1) * 128 + 8 * Dot::kRowBytes);
+    }
     float acc[NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
@@ -384,65 +449,43 @@ __device__ __forceinline__ void few_stats(const ScoreParams& p, const SeqPlan& s
       float za[2], zb[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        za[e] = ja < vis[nt][e] ? acc[nt][e] * p.scale_log2 : -CUDART_INF_F;
-        zb[e] = jb < vis[nt][e] ? acc[nt][2 + e] * p.scale_log2 : -CUDART_INF_F;
+        za[e] = acc[nt][e] * p.scale_log2;
+        zb[e] = acc[nt][2 + e] * p.scale_log2;
+        if (!kAll) {
+          if (ja >= vis[nt][e]) za[e] = -CUDART_INF_F;
+          if (jb >= vis[nt][e]) zb[e] = -CUDART_INF_F;
+        }
         const float mn = fmax3(m[nt][e], za[e], zb[e]);
-        const float mu = mn == -CUDART_INF_F ? 0.f : mn;
-        l[nt][e] = l[nt][e] * fast_exp2(m[nt][e] - mu) + (fast_exp2(za[e] - mu) + fast_exp2(zb[e] - mu));
+        const float mu = !kAll && mn == -CUDART_INF_F ? 0.f : mn;
+        l[nt][e] = fmaf(l[nt][e], fast_exp2(m[nt][e] - mu), fast_exp2(za[e] - mu) + fast_exp2(zb[e] - mu));
         m[nt][e] = mn;
       }
-      const int r = nt * 8 + 2 * t;
-      if (r < sp.pad) {
-        if (ja < ke) *reinterpret_cast<float2*>(zout + (int64_t)ja * sp.pad + r) = make_float2(za[0], za[1]);
-        if (jb < ke) *reinterpret_cast<float2*>(zout + (int64_t)jb * sp.pad + r) = make_float2(zb[0], zb[1]);
-      }
-    }
-  };
-  // two tiles of 16 keys a turn, one in use while the other is loaded
-  uint4 ka[2][Dot::kPieces], kc[2][Dot::kPieces];
-  load(kb + g, ka[0]);
-  load(kb + g + 8, ka[1]);
-#pragma unroll 1
-  for (int j = kb; j < ke; j += 32) {
-    if constexpr (Dot::kAhead) {
-      if (j + 16 < ke) {
-        load(j + 16 + g, kc[0]);
-        load(j + 24 + g, kc[1]);
-      }
-      use(j, ka[0], ka[1]);
-      if (j + 32 < ke) {
-        load(j + 32 + g, ka[0]);
-        load(j + 40 + g, ka[1]);
-      }
-      if (j + 16 < ke) use(j + 16, kc[0], kc[1]);
-    } else {
-      use(j, ka[0], ka[1]);
-      if (j + 16 < ke) {
-        load(j + 16 + g, ka[0]);
-        load(j + 24 + g, ka[1]);
-        use(j + 16, ka[0], ka[1]);
-      }
-      if (j + 32 < ke) {
-        load(j + 32 + g, ka[0]);
-        load(j + 40 + g, ka[1]);
+      if (z && (NT == 1 || z8 >= 128 || nt == 0)) {  // 16 padded rows: 8 more at z + 8
+        if (kAll || ja < ke) *reinterpret_cast<float2*>(z + nt * 8) = make_float2(za[0], za[1]);
+        if (kAll || jb < ke) *reinterpret_cast<float2*>(z + z8 + nt * 8) = make_float2(zb[0], zb[1]);
       }
     }
   }
-  // over the 8 lanes (keys) that share a row
+
+  // (max, sum) of each row over the chunk: over the 8 lanes (keys) that share it.
+  __device__ __forceinline__ void end(const ScoreParams& p, const SeqPlan& sp, const Unit& u, int lane) {
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float mm = m[nt][e];
+      for (int e = 0; e < 2; ++e) {
+        float mm = m[nt][e];
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-      float ll = l[nt][e] * fast_exp2(m[nt][e] - (mm == -CUDART_INF_F ? 0.f : mm));
+        for (int d = 4; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+        float ll = l[nt][e] * fast_exp2(m[nt][e] - (mm == -CUDART_INF_F ? 0.f : mm));
 #pragma unroll
-      for (int d = 4; d < 32; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-      const int r = nt * 8 + 2 * t + e;
-      if (g == 0 && r < sp.rows) p.part[sp.part + ((int64_t)h * sp.rows + r) * sp.chunks + c] = make_float2(mm, ll);
-    }
-}
+        for (int d = 4; d < 32; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+        const int r = nt * 8 + 2 * t + e;
+        if (g == 0 && r < sp.rows)
+          p.part[sp.part + ((int64_t)u.h * sp.rows + r) * sp.chunks + u.c] = make_float2(mm, ll);
+      }
+  }
+};
 
 // lse of one row from its chunks' (max, sum), on a whole warp; 0 for a row
 // without a finite logit (none of its weights is taken).
@@ -496,30 +539,132 @@ __device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan&
 
 // NT: tiles of 8 rows (1 where every sequence has at most 8 rows).
 template <typename Dot, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) few_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const ScoreParams p) {
+  constexpr int kStages = Dot::kStages, kTileBytes = 16 * Dot::kRowBytes;
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t n_stat = __ldg(p.off[kFewStat] + p.B), n_all = n_stat + __ldg(p.off[kFewCol] + p.B);
+  // the plan of up to kHeldSeqs sequences, in shared memory: a unit's look-up
+  // is then a few dozen cycles, not a chain of global reads
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t *off_stat = p.off[kFewStat], *off_col = p.off[kFewCol];
+  const SeqPlan* plan = p.plan;
+  if (p.B <= kHeldSeqs) {
+    int64_t* offs = reinterpret_cast<int64_t*>(smem + kFewThreads / 32 * kStages * kTileBytes);
+    SeqPlan* plans = reinterpret_cast<SeqPlan*>(offs + 2 * (p.B + 1));
+    for (int i = threadIdx.x; i <= p.B; i += kFewThreads) {
+      offs[i] = off_stat[i];
+      offs[p.B + 1 + i] = off_col[i];
+    }
+    const int64_t* src = reinterpret_cast<const int64_t*>(plan);
+    for (int i = threadIdx.x; i < p.B * (int)(sizeof(SeqPlan) / 8); i += kFewThreads)
+      reinterpret_cast<int64_t*>(plans)[i] = src[i];
+    __syncthreads();
+    off_stat = offs;
+    off_col = offs + p.B + 1;
+    plan = plans;
+  }
+  const int64_t n_stat = off_stat[p.B], n_all = n_stat + off_col[p.B];
   int* ticket = p.tickets;
   int* ready = p.tickets + (int64_t)p.B * p.Hkv;
   int* queue = ready + (int64_t)p.B * p.Hkv;
-  int64_t next = 0;
+  uint8_t* ring = smem + warp * kStages * kTileBytes;
+  const uint32_t ring_u32 = smem_u32(ring);
+
+  int64_t next = 0;  // lane 0: the unit after the one being looked up
   if (lane == 0) next = atomicAdd(queue, 1);
-  for (;;) {
-    const int64_t u = __shfl_sync(0xffffffffu, next, 0);
-    if (u >= n_all) break;
+  auto look_up = [&]() {
+    Unit u{kUnitEnd, 0, 0, 0, 0, 0, -1};
+    const int64_t at = __shfl_sync(0xffffffffu, next, 0);
+    if (at >= n_all) return u;
     if (lane == 0) next = atomicAdd(queue, 1);
-    const bool stat = u < n_stat;
-    const int64_t* off = stat ? p.off[kFewStat] : p.off[kFewCol];
-    const int64_t v = stat ? u : u - n_stat;
-    const int s = find_seq(off, p.B, v, lane);
-    const SeqPlan sp = p.plan[s];
+    const bool stat = at < n_stat;
+    const int64_t* off = stat ? off_stat : off_col;
+    const int64_t v = stat ? at : at - n_stat;
+    u.kind = stat ? kUnitStat : kUnitCol;
+    u.s = find_seq(off, p.B, v, lane);
     // heads innermost: neighbouring warps read neighbouring parts of the same tokens' rows
-    const int w = (int)(v - __ldg(off + s));
-    const int c = w / p.Hkv, h = w - c * p.Hkv;
-    const int64_t sh = (int64_t)s * p.Hkv + h;
+    const int w = (int)(v - off[u.s]);
+    u.c = w / p.Hkv;
+    u.h = w - u.c * p.Hkv;
     if (stat) {
-      few_stats<Dot, NT>(p, sp, s, h, c, lane);
+      u.kb = u.c * kFewChunk;
+      u.ke = min(plan[u.s].L, u.kb + kFewChunk);
+      if (lane < ((u.ke - u.kb + p.bs - 1) >> p.bs_log)) {  // kFewChunk / bs <= 16 blocks
+        u.blk = __ldg(p.tables + (int64_t)u.s * p.max_blocks + (u.kb >> p.bs_log) + lane);
+        if (u.blk < 0 || u.blk >= p.num_blocks) {
+          raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+          u.blk = -1;
+        }
+      }
+    }
+    return u;
+  };
+
+  int ahead_by = 0;                     // tiles issued and not used yet
+  int put = 0, get = 0;                 // their ring slots: the next to fill, the next to use
+  Unit now = look_up(), after{kUnitEnd, 0, 0, 0, 0, 0, -1};
+  bool ahead = false;                   // the next tile to issue is `after`'s (or else `now`'s)
+  int at = now.kb;                      // its first key
+  constexpr int kChunks = Dot::kRowBytes / 16;
+  const int64_t token_bytes = (int64_t)p.Hkv * Dot::kRowBytes;
+  const int64_t lane_src = (lane / kChunks) * token_bytes + (lane % kChunks) * 16;
+  auto fetch = [&](const Unit& u) {
+    fetch_tile<Dot>(p, u, at, ring_u32 + put * kTileBytes, lane_src + u.h * Dot::kRowBytes, token_bytes, lane);
+    copy_commit();
+    put = put + 1 == kStages ? 0 : put + 1;
+    ++ahead_by;
+    at += 16;
+  };
+  // issue a tile of `now`, or then of `after`, if there is one and room for it
+  auto issue = [&](bool may_go_on) {
+    if (ahead_by == kStages) return false;
+    if (!ahead) {
+      if (now.kind == kUnitStat && at < now.ke) {
+        fetch(now);
+        return true;
+      }
+      if (!may_go_on) return false;
+      ahead = true;
+      at = after.kb;
+    }
+    if (after.kind != kUnitStat || at >= after.ke) return false;
+    fetch(after);
+    return true;
+  };
+  while (now.kind != kUnitEnd) {
+    while (issue(false)) {
+    }
+    after = look_up();  // while the tiles come
+    const SeqPlan sp = plan[now.s];
+    const int64_t sh = (int64_t)now.s * p.Hkv + now.h;
+    if (now.kind == kUnitStat) {
+      Stats<Dot, NT> st;
+      st.begin(p, sp, now, lane);
+      const int g = lane >> 2, t2 = 2 * (lane & 3);
+      float* z = t2 < sp.pad ? p.logit + sp.logit + ((int64_t)now.h * sp.L + now.kb + g) * sp.pad + t2 : nullptr;
+      const int seen = p.causal ? sp.L - sp.n + 1 : sp.L;  // keys that every row sees
+#pragma unroll 1
+      for (int j = now.kb; j < now.ke; j += 16) {
+        while (issue(true)) {
+        }
+        if (ahead_by == kStages)
+          copy_wait<kStages - 1>();
+        else
+          copy_wait<0>();
+        __syncwarp();  // every lane's copies of the tile have landed
+        const uint8_t* tile = ring + get * kTileBytes;
+        if (j + 16 <= seen)
+          st.template use<true>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
+        else
+          st.template use<false>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
+        __syncwarp();  // the tile may be overwritten
+        get = get + 1 == kStages ? 0 : get + 1;
+        --ahead_by;
+        if (z) z += 16 * sp.pad;
+      }
+      while (issue(true)) {
+      }
+      st.end(p, sp, now, lane);
       __threadfence();
       __syncwarp();
       int done = 0;
@@ -527,8 +672,8 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) few_kernel(const
       if (__shfl_sync(0xffffffffu, done, 0) == sp.chunks - 1) {
         __threadfence();
         for (int r = 0; r < sp.rows; ++r) {
-          const float x = row_lse(p.part + sp.part + ((int64_t)h * sp.rows + r) * sp.chunks, sp.chunks, lane);
-          if (lane == 0) p.lse[sp.lse + (int64_t)h * sp.rows + r] = x;
+          const float x = row_lse(p.part + sp.part + ((int64_t)now.h * sp.rows + r) * sp.chunks, sp.chunks, lane);
+          if (lane == 0) p.lse[sp.lse + (int64_t)now.h * sp.rows + r] = x;
         }
         __syncwarp();
         if (lane == 0) st_release(ready + sh, 1);
@@ -545,16 +690,22 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 4 : 3) few_kernel(const
           }
         }
       }
-      if (!__shfl_sync(0xffffffffu, (int)ok, 0)) continue;
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
       __syncwarp();
-      switch (sp.pad) {
-        case 2: few_columns<2>(p, sp, h, c, lane); break;
-        case 4: few_columns<4>(p, sp, h, c, lane); break;
-        case 8: few_columns<8>(p, sp, h, c, lane); break;
-        default: few_columns<16>(p, sp, h, c, lane); break;
+      if (ok) {
+        switch (sp.pad) {
+          case 2: few_columns<2>(p, sp, now.h, now.c, lane); break;
+          case 4: few_columns<4>(p, sp, now.h, now.c, lane); break;
+          case 8: few_columns<8>(p, sp, now.h, now.c, lane); break;
+          default: few_columns<16>(p, sp, now.h, now.c, lane); break;
+        }
       }
     }
+    if (!ahead) at = after.kb;
+    ahead = false;  // what was issued of `after` is now `now`'s
+    now = after;
   }
+  copy_wait<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -762,11 +913,27 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   return l;
 }
 
+template <typename Dot, int NT>
+cudaError_t launch_few(const ScoreParams& p, int sms, cudaStream_t s) {
+  constexpr int kRing = kFewThreads / 32 * Dot::kStages * 16 * Dot::kRowBytes;
+  constexpr int kMost = kRing + 2 * (kHeldSeqs + 1) * (int)sizeof(int64_t) + kHeldSeqs * (int)sizeof(SeqPlan);
+  static unsigned long long done_mask = 0;  // devices set up
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << (dev & 63)))) {
+    e = cudaFuncSetAttribute(few_kernel<Dot, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&done_mask, 1ull << (dev & 63), __ATOMIC_RELEASE);
+  }
+  const size_t held = p.B <= kHeldSeqs ? 2 * (p.B + 1) * sizeof(int64_t) + p.B * sizeof(SeqPlan) : 0;
+  return launch_pdl(few_kernel<Dot, NT>, dim3(sms * Dot::kBlocks), dim3(kFewThreads), kRing + held, s, p);
+}
+
 template <typename TQ, typename TK, int D, typename Dot>
 cudaError_t launch(const ScoreParams& p, bool only_few, bool one_tile, int sms, cudaStream_t s) {
-  plan_scores_kernel<<<1, 1024, 0, s>>>(p);
-  cudaError_t e = one_tile ? launch_pdl(few_kernel<Dot, 1>, dim3(sms * 4), dim3(kFewThreads), 0, s, p)
-                           : launch_pdl(few_kernel<Dot, 2>, dim3(sms * 3), dim3(kFewThreads), 0, s, p);
+  plan_scores_kernel<<<1, std::min(kPlanThreads, (p.B + 31) / 32 * 32), 0, s>>>(p);
+  cudaError_t e = one_tile ? launch_few<Dot, 1>(p, sms, s) : launch_few<Dot, 2>(p, sms, s);
   if (e != cudaSuccess || only_few || p.tensor) return e;
   const int grid = sms * 8;
   stats_kernel<TQ, TK, D><<<grid, kThreads, 0, s>>>(p);
@@ -825,6 +992,9 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   if ((int64_t)p.max_blocks * p.bs > (int64_t)1 << 30 || p.max_len > 1 << 30)
     return fail(PKV_ERR_UNSUPPORTED, "context too long");
   if (p.T > ((int64_t)1 << 31) / ((int64_t)p.Hq * D)) return fail(PKV_ERR_UNSUPPORTED, "num_tokens too large");
+  const int64_t keys = std::min<int64_t>(p.max_len, (int64_t)p.max_blocks * p.bs);
+  if ((p.B + p.T) * p.Hkv > (((int64_t)1 << 31) - 1) / ((keys + 127) / 128))
+    return fail(PKV_ERR_UNSUPPORTED, "too much work for one call");
   if (p.B == 0 || p.T == 0) return PKV_OK;
   if (!p.q || !p.kc || !p.tables || !p.lens || !p.qsl || !p.scores || !p.out)
     return fail(PKV_ERR_INVALID_ARG, "null pointer");
@@ -832,7 +1002,6 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   if ((bits(p.q) | bits(p.kc)) & 15u) return fail(PKV_ERR_INVALID_ARG, "q and the cache must be 16-byte aligned");
   if (!workspace || (bits(workspace) & (kAlign - 1)))
     return fail(PKV_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
-  const int64_t keys = std::min<int64_t>(p.max_len, (int64_t)p.max_blocks * p.bs);
   const Layout lay = layout(p.B, p.T, p.Hq, p.Hkv, keys);
   if (ws_bytes < lay.least) return fail(PKV_ERR_WORKSPACE, "workspace smaller than required");
   int sms = 0;

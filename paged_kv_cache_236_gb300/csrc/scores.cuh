@@ -61,7 +61,7 @@ __device__ __forceinline__ int find_seq(const int64_t* off, int B, int64_t u, in
   while (len > 1) {
     const int step = (len + 31) / 32;
     const int i = lo + lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < len && __ldg(off + i) <= u);
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < len && off[i] <= u);
     const int k = 31 - __clz(le);  // lane 0 always holds
     const int skip = k * step;
     lo += skip;

@@ -85,20 +85,19 @@ __device__ __forceinline__ int4 peer_int4(const int* p, int rank) {
   return v;
 }
 
-// kThreads: 128 where a row has at most 4096 scores (what a block does for a
-// row whatever its length, the histograms' bins above all, is then half of
-// the work: 64 x 8 rows of 512 to 4096 scores take 18 us with 512 threads),
-// 512 for longer rows.
+// kThreads: 256 where a row has at most 4096 scores (some of a block's work,
+// the histograms' bins above all, does not depend on the row's length), 512
+// for longer rows.
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kernel(const SelectParams p) {
   constexpr int kWarps = kThreads / 32;
-  constexpr int kPer = kBins / kThreads;        // bins of a thread
+  constexpr int kPer = kBins / kThreads < 4 ? 4 : kBins / kThreads;  // bins of a thread
   extern __shared__ uint32_t keys[];            // [held]
   __shared__ __align__(16) int hist[2][kBins];  // this block's counts (by digit parity; peers read them)
   __shared__ int sum[2 * kWarps];
   __shared__ int wsum[kWarps];
   __shared__ int counts[2];  // this block's keys above / equal to the last one kept (peers read them)
-  __shared__ int s_bin, s_need;
+  __shared__ int s_bin, s_need, s_count;
   const int block = p.cluster == 1 ? 0 : blockIdx.x % p.cluster;
   const int sh = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
   const int s = sh / p.Hkv, h = sh - s * p.Hkv;
@@ -143,8 +142,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
   }
   auto key = [&](int i) { return i < held ? keys[i] : key_of(sc[i]); };
   uint32_t prefix = 0, mask = 0;
+  bool whole = false;  // every key that starts like prefix is kept
 #pragma unroll 1
-  for (int digit = 0; digit < 3; ++digit) {
+  for (int digit = 0; digit < 3 && !whole; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0;
     const int bins = digit == 2 ? 1024 : 2048;
     int* mine = hist[digit & 1];
@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
         if (before < need && need <= before + c[j]) {
           s_bin = top - j;
           s_need = need - before;
+          s_count = c[j];
         }
         before += c[j];
       }
@@ -209,7 +210,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
     prefix |= (uint32_t)s_bin << shift;
     mask |= (uint32_t)(bins - 1) << shift;
     need = s_need;
+    whole = s_count == need;
   }
+  auto above = [&](uint32_t k) { return whole ? k >= prefix : k > prefix; };
+  auto equal = [&](uint32_t k) { return !whole && k == prefix; };
   // `need` of the keys equal to `prefix` are kept, from the lowest position.
   // A warp takes a run of the block's positions: it counts its keys above and
   // equal, then knows where its first kept one goes, and writes.
@@ -219,8 +223,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
 #pragma unroll 4
   for (int i = a + lane; i < b; i += 32) {
     const uint32_t k = key(i);
-    gt += k > prefix;
-    eq += k == prefix;
+    gt += above(k);
+    eq += equal(k);
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) {
@@ -243,17 +247,21 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectParams p) 
       counts[1] = eq0 + eq;
     }
     cluster_sync(p.cluster);
-    for (int r = 0; r < block; ++r) {
-      gt0 += peer_int(&counts[0], r);
-      eq0 += peer_int(&counts[1], r);
+    int g = lane < block ? peer_int(&counts[0], lane) : 0, e = lane < block ? peer_int(&counts[1], lane) : 0;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) {  // over the at most kMaxCluster lanes that read
+      g += __shfl_xor_sync(0xffffffffu, g, d);
+      e += __shfl_xor_sync(0xffffffffu, e, d);
     }
+    gt0 += __shfl_sync(0xffffffffu, g, 0);
+    eq0 += __shfl_sync(0xffffffffu, e, 0);
     cluster_sync(p.cluster);  // a block's shared memory outlives its readers
   }
   const uint32_t below = (1u << lane) - 1u;
   for (int i0 = a; i0 < b; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t k = i < b ? key(i) : 0u;
-    const bool is_gt = i < b && k > prefix, is_eq = i < b && k == prefix;
+    const bool is_gt = i < b && above(k), is_eq = i < b && equal(k);
     const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
     const int g = gt0 + __popc(mg & below), e = eq0 + __popc(me_ & below);
     if (is_gt || (is_eq && e < need)) out[p.sink + g + min(e, need)] = lo + i;
@@ -311,7 +319,7 @@ extern "C" pkv_status paged_kv_select(const float* scores, const int32_t* score_
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   const bool small = p.cluster == 1 && max_len <= kPerBlock / 2;
-  cfg.blockDim = dim3(small ? 128 : 512);
+  cfg.blockDim = dim3(small ? 256 : 512);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
@@ -320,7 +328,7 @@ extern "C" pkv_status paged_kv_select(const float* scores, const int32_t* score_
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-  e = small ? cudaLaunchKernelEx(&cfg, select_kernel<128>, p) : cudaLaunchKernelEx(&cfg, select_kernel<512>, p);
+  e = small ? cudaLaunchKernelEx(&cfg, select_kernel<256>, p) : cudaLaunchKernelEx(&cfg, select_kernel<512>, p);
   if (e != cudaSuccess) return cuda_error(e, "paged_kv_select launch");
   return PKV_OK;
 }
