@@ -7,18 +7,20 @@
 // with the causal mask at each row's position.  A row's normaliser needs all
 // its keys before any weight is known, so the keys are passed over twice.
 //
-// plan_scores_kernel (one block) checks each sequence and lays out its work:
+// A plan of the call (plan_block) checks each sequence and lays out its work.
 //
-// Few rows (at most 16: decode, short verify windows): few_kernel, one launch
-// for both passes.  HBM-bound on K, which is read once: the logits are kept
+// Few rows (at most 16: decode, short verify windows): few_kernel, then
+// few_columns_kernel.  HBM-bound on K, which is read once: the logits are kept
 // (4 bytes a row and key, 16 bytes next to K's 256 for a group of 4 in bf16)
-// and the second pass reads them back from L2.  Work units belong to warps,
-// taken from one queue: first all stats units (a head's chunk of keys: logits,
-// and each row's (max, sum) over the chunk; the warp that completes a head's
-// last chunk combines them to the row's lse), then all column units (weights
-// summed over the rows, the score update).  A column unit waits for its
-// head's lse; every stats unit was taken earlier by a warp that is running,
-// so the wait ends, and it is bounded all the same.
+// and the second pass reads them back, mostly from L2.  The stats units (a
+// head's chunk of keys: logits, and each row's (max, sum) over the chunk)
+// belong to warps, dealt out in turn; a column unit is a block's: each row's
+// lse from its chunks, the weights summed over the rows, the score update.
+// Both passes in one kernel, the warp that ends a head's last chunk announcing
+// its lse, was slower: the fence of every unit waits for the copies in flight
+// (4 x 131072 keys: 274 us, 178 us without fences; the decode batch 84 us).
+// When only these kernels have work, each block of few_kernel makes the plan
+// itself, in shared memory, instead of a launch before it.
 //
 // More rows in bf16: the tensor-core kernel of scores_mma.cu.
 //
@@ -43,7 +45,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFewThreads = 128;
-constexpr int kHeldSeqs = 256;
+constexpr int kColThreads = 256;
 
 __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusive
 #pragma unroll
@@ -56,19 +58,27 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
 
 constexpr int kPlanThreads = 1024;
 
-// One block; threads = sequences, in passes of the block's size.  The sums are
-// scanned within warps and then, one warp to a sum, over the warps.
-__global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScoreParams p) {
-  enum { kPart = 6, kLse, kSums };
+// Where a plan goes: the global arrays, or one block's shared memory.
+struct PlanOut {
+  int64_t* off[kQueues];
+  SeqPlan* plan;
+};
+
+// A whole block makes the plan; threads = sequences, in passes of the block's
+// size.  The sums are scanned within warps and then, one warp to a sum, over
+// the warps.  kOnlyFew: no sequence but few-row ones, and only what their
+// kernels ask for.  report: this block sets the error word.
+template <bool kOnlyFew>
+__device__ __forceinline__ void plan_block(const ScoreParams& p, const PlanOut& out, bool report) {
+  // sums 0 .. 5: the queues kFewStat .. kTcCol
+  enum { kPart = kOnlyFew ? 2 : 6, kLse, kSums = kOnlyFew ? 3 : 8 };
   __shared__ int64_t warp_sum[kSums + 1][32];
   __shared__ int64_t carry[kSums + 1];  // the last: kept logits
   __shared__ int top[32];
   __shared__ int top_carry;  // the largest query_start_loc entry so far
-  pdl_launch_dependents();  // few_kernel waits for this grid first of all
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
   if (tid <= kSums) carry[tid] = 0;
   if (tid == 0) top_carry = 0;
-  for (int64_t i = tid; i < 2 * (int64_t)p.B * p.Hkv + 2; i += threads) p.tickets[i] = 0;
   // after a barrier: the exclusive sums over the warps of sums k0 .. k0 + n - 1, carried on
   auto over_warps = [&](int k0, int n) {
     __syncthreads();
@@ -108,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScorePa
       const int n = b - a;
       const bool bad = a < high || a < 0 || n < 0 || b > p.T || L < 0 || n > L || L > p.max_len ||
                        L > (int64_t)p.max_blocks * p.bs || sp.row >= p.num_rows;
-      if (bad && sp.row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
+      if (bad && sp.row >= 0 && report) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
       if (!bad && sp.row >= 0 && n > 0) {
         sp.L = L;
         sp.n = n;
@@ -126,22 +136,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScorePa
     const bool few = want_few && sp.logit + logits <= p.logit_cap;
     sp.kind = sp.n == 0 ? 0 : few ? kFew : p.tensor ? kTensor : kOther;
     sp.pad = few ? pad : 0;
-    const int chunk = sp.kind == kFew ? kFewChunk : sp.kind == kTensor ? kTcRange : kChunk;
-    sp.chunks = (sp.L + chunk - 1) / chunk;
+    // few rows: longer chunks for long sequences (fewer partials), whose block
+    // ids a warp's lanes hold
+    sp.chunk = sp.kind == kTensor ? kTcRange : sp.kind != kFew ? kChunk : sp.L <= 32768 ? kFewChunk : min(512, 32 * p.bs);
+    sp.chunks = (sp.L + sp.chunk - 1) / sp.chunk;
     sp.tiles = sp.kind == kTensor ? (sp.n + p.tile_tok - 1) / p.tile_tok : 0;
-    const int64_t groups = (sp.rows + kRowGroup - 1) / kRowGroup, work = (int64_t)p.Hkv * sp.chunks;
-    int64_t v[kSums] = {0, 0, 0, 0, 0, 0, work * sp.rows, (int64_t)p.Hkv * sp.rows};
+    const int64_t work = (int64_t)p.Hkv * sp.chunks;
+    int64_t v[kSums];
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) v[k] = 0;
+    v[kPart] = work * sp.rows;
     if (sp.kind == kFew) {
       v[kFewStat] = work;
       v[kFewCol] = (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk);
-    } else if (sp.kind == kOther) {
-      v[kStat] = work * groups;
-      v[kCol] = work;
-    } else if (sp.kind == kTensor) {
-      // one row tile: the columns of a range of keys; more: those of one 128-key tile
-      v[kTcStat] = work * sp.tiles;
-      v[kTcCol] = sp.tiles == 1 ? work : (int64_t)p.Hkv * ((sp.L + 127) / 128);
-      v[kPart] *= 2;  // each of the two epilogue groups writes its own
+    }
+    if constexpr (!kOnlyFew) {
+      v[kLse] = (int64_t)p.Hkv * sp.rows;
+      if (sp.kind == kOther) {
+        v[kStat] = work * ((sp.rows + kRowGroup - 1) / kRowGroup);
+        v[kCol] = work;
+      } else if (sp.kind == kTensor) {
+        // one row tile: the columns of a range of keys; more: those of one 128-key tile
+        v[kTcStat] = work * sp.tiles;
+        v[kTcCol] = sp.tiles == 1 ? work : (int64_t)p.Hkv * ((sp.L + 127) / 128);
+        v[kPart] *= 2;  // each of the two epilogue groups writes its own
+      }
     }
     int64_t at[kSums];
 #pragma unroll
@@ -153,22 +172,79 @@ __global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScorePa
     over_warps(0, kSums);
     if (s < p.B) {
 #pragma unroll
-      for (int k = 0; k < 6; ++k) p.off[k][s] = warp_sum[k][warp] + at[k];
+      for (int k = 0; k < kPart; ++k) out.off[k][s] = warp_sum[k][warp] + at[k];
       sp.part = warp_sum[kPart][warp] + at[kPart];
-      sp.lse = warp_sum[kLse][warp] + at[kLse];
-      p.plan[s] = sp;
+      if constexpr (!kOnlyFew) sp.lse = warp_sum[kLse][warp] + at[kLse];
+      out.plan[s] = sp;
     }
     __syncthreads();
   }
-  if (tid < 6) p.off[tid][p.B] = carry[tid];
-  if (!p.tensor) return;
+  if (tid < kPart) out.off[tid][p.B] = carry[tid];
+  __syncthreads();
+  if (kOnlyFew || !p.tensor) return;
   // places of the column items among the tensor-core kernel's items (this
   // thread wrote its own sequences' offsets)
   for (int s = tid; s < p.B; s += threads) {
-    const SeqPlan sp = p.plan[s];
+    const SeqPlan sp = out.plan[s];
     const int64_t mine = sp.kind == kTensor ? (int64_t)p.Hkv * sp.chunks * sp.tiles : 0;
-    p.off[kTcAt][s] = min(carry[kTcStat], p.off[kTcStat][s] + mine + p.tc_lag) + p.off[kTcCol][s];
+    out.off[kTcAt][s] = min(carry[kTcStat], out.off[kTcStat][s] + mine + p.tc_lag) + out.off[kTcCol][s];
   }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScoreParams p) {
+  pdl_launch_dependents();  // few_kernel waits for this grid first of all
+  for (int64_t i = threadIdx.x; i < 2 * (int64_t)p.B * p.Hkv + 1; i += blockDim.x) p.tickets[i] = 0;
+  PlanOut out;
+  for (int k = 0; k < kQueues; ++k) out.off[k] = p.off[k];
+  out.plan = p.plan;
+  plan_block<false>(p, out, true);
+}
+
+// The few-row kernels' view of the plan: their two queues and the sequences,
+// in shared memory when there are at most kHeldSeqs (a unit's look-up is then
+// a few dozen cycles, not a chain of global reads).
+constexpr int kHeldSeqs = 256;
+struct Held {
+  const int64_t* stat;
+  const int64_t* col;
+  const SeqPlan* plan;
+};
+__host__ __device__ constexpr int held_bytes(int B) {
+  return B > kHeldSeqs ? 0 : 2 * (B + 1) * (int)sizeof(int64_t) + B * (int)sizeof(SeqPlan);
+}
+// own: make the plan here (and publish it, in block 0, for the columns
+// kernel), else read the global one (after pdl_wait).
+template <bool kMayOwn>
+__device__ __forceinline__ Held hold_plan(const ScoreParams& p, uint8_t* smem) {
+  Held h{p.off[kFewStat], p.off[kFewCol], p.plan};
+  if (p.B > kHeldSeqs) return h;
+  int64_t* offs = reinterpret_cast<int64_t*>(smem);
+  SeqPlan* plans = reinterpret_cast<SeqPlan*>(offs + 2 * (p.B + 1));
+  constexpr int kWords = sizeof(SeqPlan) / 8;
+  const int64_t* src = reinterpret_cast<const int64_t*>(p.plan);
+  int64_t* dst = reinterpret_cast<int64_t*>(plans);
+  if (kMayOwn && p.own_plan) {
+    PlanOut out{};
+    out.off[kFewStat] = offs;
+    out.off[kFewCol] = offs + p.B + 1;
+    out.plan = plans;
+    plan_block<true>(p, out, blockIdx.x == 0);
+    if (blockIdx.x == 0) {
+      for (int i = threadIdx.x; i <= p.B; i += blockDim.x) {
+        p.off[kFewStat][i] = offs[i];
+        p.off[kFewCol][i] = offs[p.B + 1 + i];
+      }
+      for (int i = threadIdx.x; i < p.B * kWords; i += blockDim.x) reinterpret_cast<int64_t*>(p.plan)[i] = dst[i];
+    }
+  } else {
+    for (int i = threadIdx.x; i <= p.B; i += blockDim.x) {
+      offs[i] = h.stat[i];
+      offs[p.B + 1 + i] = h.col[i];
+    }
+    for (int i = threadIdx.x; i < p.B * kWords; i += blockDim.x) dst[i] = src[i];
+    __syncthreads();
+  }
+  return Held{offs, offs + p.B + 1, plans};
 }
 
 // ---------------------------------------------------------------------------
@@ -355,15 +431,14 @@ struct DotF32 {
   }
 };
 
-// One unit of a warp's work: a head's chunk of keys (stats) or of columns.
-enum { kUnitStat, kUnitCol, kUnitEnd };
+// One unit of a warp's work: a head's chunk of keys.
 struct Unit {
-  int kind, s, h, c;
-  int kb, ke;  // keys kb .. ke - 1 (stats)
-  int blk;     // lane i: physical block of the chunk's i-th block, -1 outside the pool
+  int s, h, c;  // s < 0: none
+  int kb, ke;   // keys kb .. ke - 1
+  int blk;      // lane i: physical block of the chunk's i-th block, -1 outside the pool
 };
 
-// Issues the copies of the 16 keys at j (of a stats unit) into a ring tile;
+// Issues the copies of the 16 keys at j into a ring tile;
 // keys past the end and blocks outside the pool become zeros.  lane_src: the
 // lane's place in a block (kv head, first key, piece).
 template <typename Dot>
@@ -503,98 +578,37 @@ __device__ __forceinline__ float row_lse(const float2* part, int chunks, int lan
   return m + log2f(l);
 }
 
-template <int PAD>
-__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int c, int lane) {
-  float lse[PAD];
-#pragma unroll
-  for (int r = 0; r < PAD; ++r)
-    lse[r] = r < sp.rows ? __ldcg(p.lse + sp.lse + (int64_t)h * sp.rows + r) : CUDART_INF_F;  // padding weighs 0
-  const float* z = p.logit + sp.logit + (int64_t)h * sp.L * PAD;
-  const int ke = min(sp.L, (c + 1) * kColChunk);
-  const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len;
-#pragma unroll 2
-  for (int j = c * kColChunk + lane; j < ke; j += 32) {
-    float x[PAD];
-    if constexpr (PAD == 2) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(z + (int64_t)j * 2));
-      x[0] = v.x;
-      x[1] = v.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < PAD / 4; ++i) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(z + (int64_t)j * PAD) + i);
-        x[4 * i] = v.x;
-        x[4 * i + 1] = v.y;
-        x[4 * i + 2] = v.z;
-        x[4 * i + 3] = v.w;
-      }
-    }
-    float paid = 0.f;
-#pragma unroll
-    for (int r = 0; r < PAD; ++r) paid += fast_exp2(x[r] - lse[r]);
-    if (j < sp.L - sp.n && p.decay != 0.f) paid = fmaf(p.decay, p.scores[at + j], paid);
-    p.out[at + j] = paid;
-  }
-}
-
 // NT: tiles of 8 rows (1 where every sequence has at most 8 rows).
 template <typename Dot, int NT>
 __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const ScoreParams p) {
   constexpr int kStages = Dot::kStages, kTileBytes = 16 * Dot::kRowBytes;
-  pdl_wait();
-  // the plan of up to kHeldSeqs sequences, in shared memory: a unit's look-up
-  // is then a few dozen cycles, not a chain of global reads
+  pdl_launch_dependents();  // few_columns_kernel waits for this grid
+  if (!p.own_plan) pdl_wait();
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t *off_stat = p.off[kFewStat], *off_col = p.off[kFewCol];
-  const SeqPlan* plan = p.plan;
-  if (p.B <= kHeldSeqs) {
-    int64_t* offs = reinterpret_cast<int64_t*>(smem + kFewThreads / 32 * kStages * kTileBytes);
-    SeqPlan* plans = reinterpret_cast<SeqPlan*>(offs + 2 * (p.B + 1));
-    for (int i = threadIdx.x; i <= p.B; i += kFewThreads) {
-      offs[i] = off_stat[i];
-      offs[p.B + 1 + i] = off_col[i];
-    }
-    const int64_t* src = reinterpret_cast<const int64_t*>(plan);
-    for (int i = threadIdx.x; i < p.B * (int)(sizeof(SeqPlan) / 8); i += kFewThreads)
-      reinterpret_cast<int64_t*>(plans)[i] = src[i];
-    __syncthreads();
-    off_stat = offs;
-    off_col = offs + p.B + 1;
-    plan = plans;
-  }
-  const int64_t n_stat = off_stat[p.B], n_all = n_stat + off_col[p.B];
-  int* ticket = p.tickets;
-  int* ready = p.tickets + (int64_t)p.B * p.Hkv;
-  int* queue = ready + (int64_t)p.B * p.Hkv;
+  const Held held = hold_plan<true>(p, smem + kFewThreads / 32 * kStages * kTileBytes);
+  const SeqPlan* plan = held.plan;
+  const int64_t n_units = held.stat[p.B];
   uint8_t* ring = smem + warp * kStages * kTileBytes;
   const uint32_t ring_u32 = smem_u32(ring);
 
-  int64_t next = 0;  // lane 0: the unit after the one being looked up
-  if (lane == 0) next = atomicAdd(queue, 1);
+  int64_t next = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;  // the units are dealt out to the warps in turn
   auto look_up = [&]() {
-    Unit u{kUnitEnd, 0, 0, 0, 0, 0, -1};
-    const int64_t at = __shfl_sync(0xffffffffu, next, 0);
-    if (at >= n_all) return u;
-    if (lane == 0) next = atomicAdd(queue, 1);
-    const bool stat = at < n_stat;
-    const int64_t* off = stat ? off_stat : off_col;
-    const int64_t v = stat ? at : at - n_stat;
-    u.kind = stat ? kUnitStat : kUnitCol;
-    u.s = find_seq(off, p.B, v, lane);
+    Unit u{-1, 0, 0, 0, 0, -1};
+    if (next >= n_units) return u;
+    u.s = find_seq(held.stat, p.B, next, lane);
     // heads innermost: neighbouring warps read neighbouring parts of the same tokens' rows
-    const int w = (int)(v - off[u.s]);
+    const int w = (int)(next - held.stat[u.s]);
+    next += (int64_t)gridDim.x * (kFewThreads / 32);
     u.c = w / p.Hkv;
     u.h = w - u.c * p.Hkv;
-    if (stat) {
-      u.kb = u.c * kFewChunk;
-      u.ke = min(plan[u.s].L, u.kb + kFewChunk);
-      if (lane < ((u.ke - u.kb + p.bs - 1) >> p.bs_log)) {  // kFewChunk / bs <= 16 blocks
-        u.blk = __ldg(p.tables + (int64_t)u.s * p.max_blocks + (u.kb >> p.bs_log) + lane);
-        if (u.blk < 0 || u.blk >= p.num_blocks) {
-          raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
-          u.blk = -1;
-        }
+    u.kb = u.c * plan[u.s].chunk;
+    u.ke = min(plan[u.s].L, u.kb + plan[u.s].chunk);
+    if (lane < ((u.ke - u.kb + p.bs - 1) >> p.bs_log)) {  // chunk / bs <= 32 blocks
+      u.blk = __ldg(p.tables + (int64_t)u.s * p.max_blocks + (u.kb >> p.bs_log) + lane);
+      if (u.blk < 0 || u.blk >= p.num_blocks) {
+        raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+        u.blk = -1;
       }
     }
     return u;
@@ -602,7 +616,7 @@ __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const Sc
 
   int ahead_by = 0;                     // tiles issued and not used yet
   int put = 0, get = 0;                 // their ring slots: the next to fill, the next to use
-  Unit now = look_up(), after{kUnitEnd, 0, 0, 0, 0, 0, -1};
+  Unit now = look_up(), after{-1, 0, 0, 0, 0, -1};
   bool ahead = false;                   // the next tile to issue is `after`'s (or else `now`'s)
   int at = now.kb;                      // its first key
   constexpr int kChunks = Dot::kRowBytes / 16;
@@ -619,7 +633,7 @@ __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const Sc
   auto issue = [&](bool may_go_on) {
     if (ahead_by == kStages) return false;
     if (!ahead) {
-      if (now.kind == kUnitStat && at < now.ke) {
+      if (at < now.ke) {
         fetch(now);
         return true;
       }
@@ -627,85 +641,131 @@ __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const Sc
       ahead = true;
       at = after.kb;
     }
-    if (after.kind != kUnitStat || at >= after.ke) return false;
+    if (at >= after.ke) return false;
     fetch(after);
     return true;
   };
-  while (now.kind != kUnitEnd) {
+  while (now.s >= 0) {
     while (issue(false)) {
     }
     after = look_up();  // while the tiles come
     const SeqPlan sp = plan[now.s];
-    const int64_t sh = (int64_t)now.s * p.Hkv + now.h;
-    if (now.kind == kUnitStat) {
-      Stats<Dot, NT> st;
-      st.begin(p, sp, now, lane);
-      const int g = lane >> 2, t2 = 2 * (lane & 3);
-      float* z = t2 < sp.pad ? p.logit + sp.logit + ((int64_t)now.h * sp.L + now.kb + g) * sp.pad + t2 : nullptr;
-      const int seen = p.causal ? sp.L - sp.n + 1 : sp.L;  // keys that every row sees
+    Stats<Dot, NT> st;
+    st.begin(p, sp, now, lane);
+    const int g = lane >> 2, t2 = 2 * (lane & 3);
+    float* z = t2 < sp.pad ? p.logit + sp.logit + ((int64_t)now.h * sp.L + now.kb + g) * sp.pad + t2 : nullptr;
+    const int seen = p.causal ? sp.L - sp.n + 1 : sp.L;  // keys that every row sees
 #pragma unroll 1
-      for (int j = now.kb; j < now.ke; j += 16) {
-        while (issue(true)) {
-        }
-        if (ahead_by == kStages)
-          copy_wait<kStages - 1>();
-        else
-          copy_wait<0>();
-        __syncwarp();  // every lane's copies of the tile have landed
-        const uint8_t* tile = ring + get * kTileBytes;
-        if (j + 16 <= seen)
-          st.template use<true>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
-        else
-          st.template use<false>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
-        __syncwarp();  // the tile may be overwritten
-        get = get + 1 == kStages ? 0 : get + 1;
-        --ahead_by;
-        if (z) z += 16 * sp.pad;
-      }
+    for (int j = now.kb; j < now.ke; j += 16) {
       while (issue(true)) {
       }
-      st.end(p, sp, now, lane);
-      __threadfence();
-      __syncwarp();
-      int done = 0;
-      if (lane == 0) done = atomicAdd(ticket + sh, 1);
-      if (__shfl_sync(0xffffffffu, done, 0) == sp.chunks - 1) {
-        __threadfence();
-        for (int r = 0; r < sp.rows; ++r) {
-          const float x = row_lse(p.part + sp.part + ((int64_t)now.h * sp.rows + r) * sp.chunks, sp.chunks, lane);
-          if (lane == 0) p.lse[sp.lse + (int64_t)now.h * sp.rows + r] = x;
-        }
-        __syncwarp();
-        if (lane == 0) st_release(ready + sh, 1);
-      }
-    } else {
-      bool ok = true;
-      if (lane == 0) {
-        const uint64_t t0 = globaltimer();
-        while (ld_acquire(ready + sh) == 0) {
-          if (globaltimer() - t0 > kWaitTimeoutNs) {
-            raise_error(p.err, PKV_DEVERR_TIMEOUT);
-            ok = false;
-            break;
-          }
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      __syncwarp();
-      if (ok) {
-        switch (sp.pad) {
-          case 2: few_columns<2>(p, sp, now.h, now.c, lane); break;
-          case 4: few_columns<4>(p, sp, now.h, now.c, lane); break;
-          case 8: few_columns<8>(p, sp, now.h, now.c, lane); break;
-          default: few_columns<16>(p, sp, now.h, now.c, lane); break;
-        }
-      }
+      if (ahead_by == kStages)
+        copy_wait<kStages - 1>();
+      else
+        copy_wait<0>();
+      __syncwarp();  // every lane's copies of the tile have landed
+      const uint8_t* tile = ring + get * kTileBytes;
+      if (j + 16 <= seen)
+        st.template use<true>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
+      else
+        st.template use<false>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
+      __syncwarp();  // the tile may be overwritten
+      get = get + 1 == kStages ? 0 : get + 1;
+      --ahead_by;
+      if (z) z += 16 * sp.pad;
     }
+    while (issue(true)) {
+    }
+    st.end(p, sp, now, lane);
     if (!ahead) at = after.kb;
     ahead = false;  // what was issued of `after` is now `now`'s
     now = after;
   }
   copy_wait<0>();
+}
+
+// Weights and scores from the kept logits: a block takes kColChunk keys of a
+// head, kAt keys a thread at a time; the first keys' logits are loaded before
+// the rows' lse are put together.
+template <int PAD>
+__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int kb, float* lse_sh) {
+  const float* z = p.logit + sp.logit + (int64_t)h * sp.L * PAD;
+  const int ke = min(sp.L, kb + kColChunk);
+  const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len;
+  constexpr int kAt = PAD <= 4 ? 4 : PAD == 8 ? 2 : 1;
+  float x[kAt][PAD], old[kAt];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const int j = j0 + i * kColThreads;
+      old[i] = j < sp.L - sp.n && p.decay != 0.f ? p.scores[at + j] : 0.f;
+      if (j >= ke) continue;
+      if constexpr (PAD == 2) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(z + (int64_t)j * 2));
+        x[i][0] = v.x;
+        x[i][1] = v.y;
+      } else {
+#pragma unroll
+        for (int k = 0; k < PAD / 4; ++k) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(z + (int64_t)j * PAD) + k);
+          x[i][4 * k] = v.x;
+          x[i][4 * k + 1] = v.y;
+          x[i][4 * k + 2] = v.z;
+          x[i][4 * k + 3] = v.w;
+        }
+      }
+    }
+  };
+  int j0 = kb + threadIdx.x;
+  load(j0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int r = warp; r < PAD; r += kColThreads / 32) {
+    // padding weighs nothing
+    const float v = r < sp.rows
+                        ? row_lse(p.part + sp.part + ((int64_t)h * sp.rows + r) * sp.chunks, sp.chunks, lane)
+                        : CUDART_INF_F;
+    if (lane == 0) lse_sh[r] = v;
+  }
+  __syncthreads();
+  float lse[PAD];
+#pragma unroll
+  for (int r = 0; r < PAD; ++r) lse[r] = lse_sh[r];
+  while (j0 < ke) {
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      const int j = j0 + i * kColThreads;
+      if (j >= ke) continue;
+      float paid = 0.f;
+#pragma unroll
+      for (int r = 0; r < PAD; ++r) paid += fast_exp2(x[i][r] - lse[r]);
+      p.out[at + j] = j < sp.L - sp.n && p.decay != 0.f ? fmaf(p.decay, old[i], paid) : paid;
+    }
+    j0 += kAt * kColThreads;
+    if (j0 < ke) load(j0);
+  }
+  __syncthreads();  // lse_sh may be rewritten
+}
+
+constexpr int kColBlocks = 4;  // of an SM
+
+__global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(const ScoreParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float lse[kFewRows];
+  pdl_wait();
+  const Held held = hold_plan<false>(p, smem);
+  const int64_t n_units = held.col[p.B];
+  for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
+    const int s = find_seq(held.col, p.B, u, threadIdx.x & 31);
+    const SeqPlan sp = held.plan[s];
+    const int w = (int)(u - held.col[s]);
+    const int c = w / p.Hkv, h = w - c * p.Hkv;
+    switch (sp.pad) {
+      case 2: few_columns<2>(p, sp, h, c * kColChunk, lse); break;
+      case 4: few_columns<4>(p, sp, h, c * kColChunk, lse); break;
+      case 8: few_columns<8>(p, sp, h, c * kColChunk, lse); break;
+      default: few_columns<16>(p, sp, h, c * kColChunk, lse); break;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -899,7 +959,7 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   l.plan = at;
   at = align_up(at + (size_t)B * sizeof(SeqPlan));
   l.tickets = at;
-  at = align_up(at + (size_t)(2 * B * Hkv + 2) * sizeof(int));
+  at = align_up(at + (size_t)(2 * B * Hkv + 1) * sizeof(int));
   l.lse = at;
   at = align_up(at + (size_t)(T * Hq) * sizeof(float));
   l.part = at;
@@ -916,7 +976,7 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
 template <typename Dot, int NT>
 cudaError_t launch_few(const ScoreParams& p, int sms, cudaStream_t s) {
   constexpr int kRing = kFewThreads / 32 * Dot::kStages * 16 * Dot::kRowBytes;
-  constexpr int kMost = kRing + 2 * (kHeldSeqs + 1) * (int)sizeof(int64_t) + kHeldSeqs * (int)sizeof(SeqPlan);
+  constexpr int kMost = kRing + held_bytes(kHeldSeqs);
   static unsigned long long done_mask = 0;  // devices set up
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -926,13 +986,23 @@ cudaError_t launch_few(const ScoreParams& p, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << (dev & 63), __ATOMIC_RELEASE);
   }
-  const size_t held = p.B <= kHeldSeqs ? 2 * (p.B + 1) * sizeof(int64_t) + p.B * sizeof(SeqPlan) : 0;
-  return launch_pdl(few_kernel<Dot, NT>, dim3(sms * Dot::kBlocks), dim3(kFewThreads), kRing + held, s, p);
+  const int smem = kRing + held_bytes(p.B);
+  // as many blocks as are resident (the units are dealt out to all of them):
+  // shared memory is 228 KB an SM, 1 KB a block goes to the system and 2.5 KB to the plan's sums
+  const dim3 grid(sms * std::max(1, std::min(Dot::kBlocks, 228 * 1024 / (smem + 3600))));
+  if (p.own_plan) {  // the first kernel of the call: an ordinary launch
+    few_kernel<Dot, NT><<<grid, kFewThreads, smem, s>>>(p);
+    e = cudaGetLastError();
+  } else {
+    e = launch_pdl(few_kernel<Dot, NT>, grid, dim3(kFewThreads), smem, s, p);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_pdl(few_columns_kernel, dim3(sms * kColBlocks), dim3(kColThreads), held_bytes(p.B), s, p);
 }
 
 template <typename TQ, typename TK, int D, typename Dot>
 cudaError_t launch(const ScoreParams& p, bool only_few, bool one_tile, int sms, cudaStream_t s) {
-  plan_scores_kernel<<<1, std::min(kPlanThreads, (p.B + 31) / 32 * 32), 0, s>>>(p);
+  if (!p.own_plan) plan_scores_kernel<<<1, std::min(kPlanThreads, (p.B + 31) / 32 * 32), 0, s>>>(p);
   cudaError_t e = one_tile ? launch_few<Dot, 1>(p, sms, s) : launch_few<Dot, 2>(p, sms, s);
   if (e != cudaSuccess || only_few || p.tensor) return e;
   const int grid = sms * 8;
@@ -1019,6 +1089,7 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   // every sequence has few rows, and their logits fit: the other kernels have nothing to do
   const int64_t most_rows = std::min<int64_t>(p.T, max_query_len > 0 ? max_query_len : p.T) * p.G;
   const bool only_few = most_rows <= kFewRows && std::min(2 * p.T * p.Hq, (int64_t)kFewRows * p.B * p.Hkv) * keys <= p.logit_cap;
+  p.own_plan = only_few && p.B <= kHeldSeqs;
   const bool one_tile = most_rows <= 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   typedef __nv_bfloat16 bf16;

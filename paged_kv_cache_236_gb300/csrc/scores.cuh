@@ -9,7 +9,7 @@ namespace pkv {
 
 constexpr int kFewRows = 16;    // rows of a few-row sequence's kv head
 constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
-constexpr int kColChunk = 256;  // keys of a column unit (few rows)
+constexpr int kColChunk = 1024;  // keys of a column unit (few rows)
 constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
 constexpr int kChunk = 256;   // keys of a work unit (other rows)
 enum { kFew = 1, kTensor = 2, kOther = 3 };
@@ -28,6 +28,7 @@ struct SeqPlan {
   int rows, pad;  // rows of a kv head; rows a key's logits are padded to (few rows)
   int kind;       // which kernels: kFew, kTensor, kOther (0: none)
   int tiles;      // row tiles of the tensor-core kernel (whole tokens that fit 128 rows)
+  int chunk;      // keys of a chunk
 };
 
 struct ScoreParams {
@@ -41,11 +42,12 @@ struct ScoreParams {
   float* out;
   int64_t* off[kQueues];  // [B + 1] each: first unit of each sequence in the queues
   SeqPlan* plan;    // [B]
-  int* tickets;     // [B, Hkv] chunks done, then [B, Hkv] lse ready, then the counters of the two dynamic queues
+  int* tickets;     // tensor-core kernel: [B, Hkv] partials done, then [B, Hkv] lse ready, then its queue's counter
   float2* part;     // (m, l) per (kv head, row, chunk) of a sequence
   float* lse;       // per (kv head, row) of a sequence
   float* logit;     // per (kv head, key, padded row) of a few-row sequence
   int64_t logit_cap;
+  int own_plan;     // the few-row kernels make the plan themselves (no other kernel runs)
   int tensor;       // sequences of more rows go to the tensor-core kernel
   int tc_lag;       // column items follow this many later stats items in its queue
   int tile_tok;     // tokens of a row tile: floor(128 / G)

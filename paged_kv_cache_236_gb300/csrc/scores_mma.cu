@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
   if (warp == 2) {
     // ================================================================ items
     const int64_t n_stat = __ldg(p.off[kTcStat] + p.B), n_all = n_stat + __ldg(p.off[kTcCol] + p.B);
-    int* queue = ready + (int64_t)p.B * p.Hkv + 1;
+    int* queue = ready + (int64_t)p.B * p.Hkv;
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
       if (!wait_all(&bars->item_empty[sl], ((it / kItems) & 1) ^ 1, wc)) break;
