@@ -55,8 +55,10 @@ extern "C" {
  * Everything is accumulated in fp32; sums are taken in a fixed order, so equal
  * calls give equal bits.
  *
- *   q, k_cache, block_tables, context_lens, query_start_loc, max_query_len,
- *   scale, causal, dtype   as paged_attention_forward (same shapes supported)
+ *   q, k_cache, block_tables, context_lens, query_start_loc, scale, causal,
+ *   dtype       as paged_attention_forward (same shapes supported)
+ *   max_query_len  0, or a promise that no sequence has more queries (it picks
+ *               the kernels): one that does is invalid, below
  *   scores      device float32 [num_rows, num_kv_heads, max_len]: the old scores
  *   scores_out  where the new ones go: the same layout; may be `scores` itself,
  *               must not overlap it otherwise
@@ -64,9 +66,9 @@ extern "C" {
  *   workspace   device scratch of workspace_bytes >=
  *               paged_attention_scores_workspace_min, 256-byte aligned;
  *               overwritten; not shared by calls that may run concurrently
- * A sequence with L > max_len, L > max_blocks_per_seq * block_size, n > L or a
- * non-monotone query_start_loc sets PKV_DEVERR_BAD_SEQUENCE and leaves its row
- * as it was.  An out-of-pool block id is read as a block of zeros and sets
+ * A sequence with L > max_len, L > max_blocks_per_seq * block_size, n > L, n >
+ * max_query_len > 0 or a non-monotone query_start_loc (an entry below an
+ * earlier one) sets PKV_DEVERR_BAD_SEQUENCE and leaves its row as it was.  An out-of-pool block id is read as a block of zeros and sets
  * PKV_DEVERR_BLOCK_OUT_OF_RANGE, as in paged_attention_forward.
  */
 pkv_status paged_attention_scores(const void* q, const void* k_cache, const int32_t* block_tables,

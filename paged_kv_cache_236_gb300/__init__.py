@@ -882,9 +882,11 @@ def paged_attention_scores(q: torch.Tensor, k_cache: torch.Tensor, block_tables:
     ones) it becomes that sum alone.  ``score_rows`` (int32 ``[num_seqs]``)
     names each sequence's row (default: its place in the batch; < 0 leaves it
     out).  The result goes to ``out`` (default: ``scores``, in place); entries
-    past a sequence's length are left as they were.  The other arguments are
-    ``paged_attention_forward``'s; ``workspace`` (uint8, >=
-    ``scores_workspace_min``) defaults to the cached buffer per (device, stream)."""
+    past a sequence's length are left as they were.  ``max_query_len`` > 0
+    promises that no sequence has more queries (a sequence that does is flagged
+    and left out).  The other arguments are ``paged_attention_forward``'s;
+    ``workspace`` (uint8, >= ``scores_workspace_min``) defaults to the cached
+    buffer per (device, stream)."""
     dev = _device_of(q, k_cache, block_tables, context_lens, query_start_loc, scores, score_rows)
     if q.dtype not in DTYPE or k_cache.dtype != q.dtype:
         raise ValueError("q and k_cache must share dtype bfloat16 or float32")

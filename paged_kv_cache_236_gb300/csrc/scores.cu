@@ -14,8 +14,10 @@
 // (4 bytes a row and key, 16 bytes next to K's 256 for a group of 4 in bf16)
 // and the second pass reads them back, mostly from L2.  The stats units (a
 // head's chunk of keys: logits, and each row's (max, sum) over the chunk)
-// belong to warps, dealt out in turn; a column unit is a block's: each row's
-// lse from its chunks, the weights summed over the rows, the score update.
+// belong to warps, which take them from a counter (dealt out in turn instead,
+// the slower SMs finished last: 69 us against 60 on the decode batch); the
+// columns are cut into equal spans, one a warp: each row's lse from its
+// chunks, the weights summed over the rows, the score update.
 // Both passes in one kernel, the warp that ends a head's last chunk announcing
 // its lse, was slower: the fence of every unit waits for the copies in flight
 // (4 x 131072 keys: 274 us, 178 us without fences; the decode batch 84 us).
@@ -58,20 +60,24 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
 
 constexpr int kPlanThreads = 1024;
 
-// Where a plan goes: the global arrays, or one block's shared memory.
-struct PlanOut {
-  int64_t* off[kQueues];
-  SeqPlan* plan;
-};
+// Keys of a few-row stats unit: longer for long sequences (fewer partials),
+// whose block ids a warp's lanes hold.
+__device__ __forceinline__ int few_chunk(const ScoreParams& p, int L) {
+  return L <= 32768 ? kFewChunk : min(512, 32 * p.bs);
+}
+
+// Whether sequence s, of queries a .. b - 1 and L tokens, is left out as
+// invalid; high: the largest earlier entry of query_start_loc.
+__device__ __forceinline__ bool bad_seq(const ScoreParams& p, int a, int b, int high, int L, int row) {
+  return a < high || a < 0 || b < a || b > p.T || L < 0 || b - a > L || L > p.max_len ||
+         L > (int64_t)p.max_blocks * p.bs || row >= p.num_rows || (p.max_query > 0 && b - a > p.max_query);
+}
 
 // A whole block makes the plan; threads = sequences, in passes of the block's
 // size.  The sums are scanned within warps and then, one warp to a sum, over
-// the warps.  kOnlyFew: no sequence but few-row ones, and only what their
-// kernels ask for.  report: this block sets the error word.
-template <bool kOnlyFew>
-__device__ __forceinline__ void plan_block(const ScoreParams& p, const PlanOut& out, bool report) {
-  // sums 0 .. 5: the queues kFewStat .. kTcCol
-  enum { kPart = kOnlyFew ? 2 : 6, kLse, kSums = kOnlyFew ? 3 : 8 };
+// the warps.
+__device__ __forceinline__ void plan_block(const ScoreParams& p) {
+  enum { kPart = kQueues, kLse, kSums };  // sums 0 .. kQueues - 1: the queues
   __shared__ int64_t warp_sum[kSums + 1][32];
   __shared__ int64_t carry[kSums + 1];  // the last: kept logits
   __shared__ int top[32];
@@ -116,9 +122,8 @@ __device__ __forceinline__ void plan_block(const ScoreParams& p, const PlanOut& 
     for (int w = 0; w < warp; ++w) high = max(high, top[w]);
     if (s < p.B) {
       const int n = b - a;
-      const bool bad = a < high || a < 0 || n < 0 || b > p.T || L < 0 || n > L || L > p.max_len ||
-                       L > (int64_t)p.max_blocks * p.bs || sp.row >= p.num_rows;
-      if (bad && sp.row >= 0 && report) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
+      const bool bad = bad_seq(p, a, b, high, L, sp.row);
+      if (bad && sp.row >= 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
       if (!bad && sp.row >= 0 && n > 0) {
         sp.L = L;
         sp.n = n;
@@ -136,31 +141,26 @@ __device__ __forceinline__ void plan_block(const ScoreParams& p, const PlanOut& 
     const bool few = want_few && sp.logit + logits <= p.logit_cap;
     sp.kind = sp.n == 0 ? 0 : few ? kFew : p.tensor ? kTensor : kOther;
     sp.pad = few ? pad : 0;
-    // few rows: longer chunks for long sequences (fewer partials), whose block
-    // ids a warp's lanes hold
-    sp.chunk = sp.kind == kTensor ? kTcRange : sp.kind != kFew ? kChunk : sp.L <= 32768 ? kFewChunk : min(512, 32 * p.bs);
+    sp.chunk = sp.kind == kTensor ? kTcRange : sp.kind == kFew ? few_chunk(p, sp.L) : kChunk;
     sp.chunks = (sp.L + sp.chunk - 1) / sp.chunk;
     sp.tiles = sp.kind == kTensor ? (sp.n + p.tile_tok - 1) / p.tile_tok : 0;
     const int64_t work = (int64_t)p.Hkv * sp.chunks;
     int64_t v[kSums];
 #pragma unroll
     for (int k = 0; k < kSums; ++k) v[k] = 0;
-    v[kPart] = work * sp.rows;
+    v[kPart] = (work * sp.rows + 1) & ~(int64_t)1;  // even: the tensor-core kernel reads pairs
     if (sp.kind == kFew) {
       v[kFewStat] = work;
       v[kFewCol] = (int64_t)p.Hkv * ((sp.L + kColChunk - 1) / kColChunk);
     }
-    if constexpr (!kOnlyFew) {
-      v[kLse] = (int64_t)p.Hkv * sp.rows;
-      if (sp.kind == kOther) {
-        v[kStat] = work * ((sp.rows + kRowGroup - 1) / kRowGroup);
-        v[kCol] = work;
-      } else if (sp.kind == kTensor) {
-        // one row tile: the columns of a range of keys; more: those of one 128-key tile
-        v[kTcStat] = work * sp.tiles;
-        v[kTcCol] = sp.tiles == 1 ? work : (int64_t)p.Hkv * ((sp.L + 127) / 128);
-        v[kPart] *= 2;  // each of the two epilogue groups writes its own
-      }
+    v[kLse] = (int64_t)p.Hkv * sp.rows;
+    if (sp.kind == kOther) {
+      v[kStat] = work * ((sp.rows + kRowGroup - 1) / kRowGroup);
+      v[kCol] = work;
+    } else if (sp.kind == kTensor) {
+      v[kTcStat] = work * sp.tiles;
+      v[kTcCol] = work;
+      v[kPart] = 2 * work * sp.rows;  // each of the two epilogue groups writes its own
     }
     int64_t at[kSums];
 #pragma unroll
@@ -172,32 +172,117 @@ __device__ __forceinline__ void plan_block(const ScoreParams& p, const PlanOut& 
     over_warps(0, kSums);
     if (s < p.B) {
 #pragma unroll
-      for (int k = 0; k < kPart; ++k) out.off[k][s] = warp_sum[k][warp] + at[k];
+      for (int k = 0; k < kQueues; ++k) p.off[k][s] = warp_sum[k][warp] + at[k];
       sp.part = warp_sum[kPart][warp] + at[kPart];
-      if constexpr (!kOnlyFew) sp.lse = warp_sum[kLse][warp] + at[kLse];
-      out.plan[s] = sp;
+      sp.lse = warp_sum[kLse][warp] + at[kLse];
+      p.plan[s] = sp;
     }
     __syncthreads();
   }
-  if (tid < kPart) out.off[tid][p.B] = carry[tid];
-  __syncthreads();
-  if (kOnlyFew || !p.tensor) return;
-  // places of the column items among the tensor-core kernel's items (this
-  // thread wrote its own sequences' offsets)
-  for (int s = tid; s < p.B; s += threads) {
-    const SeqPlan sp = out.plan[s];
-    const int64_t mine = sp.kind == kTensor ? (int64_t)p.Hkv * sp.chunks * sp.tiles : 0;
-    out.off[kTcAt][s] = min(carry[kTcStat], out.off[kTcStat][s] + mine + p.tc_lag) + out.off[kTcCol][s];
-  }
+  if (tid < kQueues) p.off[tid][p.B] = carry[tid];
 }
 
 __global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScoreParams p) {
   pdl_launch_dependents();  // few_kernel waits for this grid first of all
-  for (int64_t i = threadIdx.x; i < 2 * (int64_t)p.B * p.Hkv + 1; i += blockDim.x) p.tickets[i] = 0;
-  PlanOut out;
-  for (int k = 0; k < kQueues; ++k) out.off[k] = p.off[k];
-  out.plan = p.plan;
-  plan_block<false>(p, out, true);
+  for (int64_t i = threadIdx.x; i < 2 * (int64_t)p.B * p.Hkv; i += blockDim.x) p.tickets[i] = 0;
+  if (threadIdx.x < 2) p.counters[threadIdx.x] = 0;
+  plan_block(p);
+}
+
+// With own_plan: zeroes the few-row queue's counter while few_kernel, started
+// early, makes its plan.
+__global__ void start_few_kernel(int* counters) {
+  pdl_launch_dependents();
+  if (threadIdx.x < 2) counters[threadIdx.x] = 0;
+}
+
+// plan_block for few-row sequences only, at most two a thread: two scans
+// between three barriers.
+__device__ __forceinline__ void plan_few(const ScoreParams& p, int64_t* stat, int64_t* col, SeqPlan* plan, bool report) {
+  __shared__ int64_t sum[4][8];
+  __shared__ int top[8];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int a[3], L[2], row[2];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) a[i] = 2 * tid + i <= p.B ? p.qsl[2 * tid + i] : 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = 2 * tid + i;
+    L[i] = s < p.B ? p.lens[s] : 0;
+    row[i] = s < p.B ? p.rows ? p.rows[s] : s : -1;
+  }
+  int high = max(a[0], 2 * tid + 1 < p.B ? a[1] : a[0]);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, high, d);
+    if (lane >= d) high = max(high, y);
+  }
+  int before = __shfl_up_sync(0xffffffffu, high, 1);
+  if (lane == 0) before = 0;
+  if (lane == 31) top[warp] = high;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before = max(before, top[w]);
+  SeqPlan sp[2];
+  int64_t v[4] = {0, 0, 0, 0};  // stats units, column units, partials, logits
+  int64_t mine[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    SeqPlan& q = sp[i];
+    q = SeqPlan{};
+    q.row = row[i];
+    if (2 * tid + i < p.B) {
+      const int n = a[i + 1] - a[i];
+      const bool bad = bad_seq(p, a[i], a[i + 1], before, L[i], q.row);
+      if (bad && q.row >= 0 && report) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
+      if (!bad && q.row >= 0 && n > 0) {
+        q.L = L[i];
+        q.n = n;
+        q.rows = n * p.G;
+        q.kind = kFew;
+        q.pad = q.rows <= 2 ? 2 : q.rows <= 4 ? 4 : q.rows <= 8 ? 8 : 16;
+        q.chunk = few_chunk(p, q.L);
+        q.chunks = (q.L + q.chunk - 1) / q.chunk;
+      }
+      before = max(before, a[i]);
+    }
+    mine[i][0] = (int64_t)p.Hkv * q.chunks;
+    mine[i][1] = (int64_t)p.Hkv * ((q.L + kColChunk - 1) / kColChunk);
+    mine[i][2] = mine[i][0] * q.rows;
+    mine[i][3] = (int64_t)p.Hkv * q.L * q.pad;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += mine[i][k];
+  }
+  int64_t at[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t x = warp_scan(v[k], lane);
+    at[k] = x - v[k];
+    if (lane == 31) sum[k][warp] = x;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    for (int w = 0; w < warp; ++w) at[k] += sum[k][w];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = 2 * tid + i;
+    if (s <= p.B) {  // the entry after the last sequence holds the totals
+      stat[s] = at[0];
+      col[s] = at[1];
+    }
+    if (s < p.B) {
+      sp[i].part = at[2];
+      sp[i].logit = at[3];
+      plan[s] = sp[i];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at[k] += mine[i][k];
+  }
+  if (tid == (int)blockDim.x - 1 && 2 * tid + 2 <= p.B) {  // two sequences to every thread
+    stat[p.B] = at[0];
+    col[p.B] = at[1];
+  }
+  __syncthreads();
 }
 
 // The few-row kernels' view of the plan: their two queues and the sequences,
@@ -224,11 +309,7 @@ __device__ __forceinline__ Held hold_plan(const ScoreParams& p, uint8_t* smem) {
   const int64_t* src = reinterpret_cast<const int64_t*>(p.plan);
   int64_t* dst = reinterpret_cast<int64_t*>(plans);
   if (kMayOwn && p.own_plan) {
-    PlanOut out{};
-    out.off[kFewStat] = offs;
-    out.off[kFewCol] = offs + p.B + 1;
-    out.plan = plans;
-    plan_block<true>(p, out, blockIdx.x == 0);
+    plan_few(p, offs, offs + p.B + 1, plans, blockIdx.x == 0);
     if (blockIdx.x == 0) {
       for (int i = threadIdx.x; i <= p.B; i += blockDim.x) {
         p.off[kFewStat][i] = offs[i];
@@ -562,20 +643,30 @@ struct Stats {
   }
 };
 
-// lse of one row from its chunks' (max, sum), on a whole warp; 0 for a row
-// without a finite logit (none of its weights is taken).
+// lse of one row from its chunks' (max, sum), on a whole warp.
 __device__ __forceinline__ float row_lse(const float2* part, int chunks, int lane) {
   float m = -CUDART_INF_F, l = 0.f;
-  for (int c = lane; c < chunks; c += 32) m = fmaxf(m, __ldcg(part + c).x);
+  for (int c0 = 0; c0 < chunks; c0 += 128) {
+    float2 v[4];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  for (int c = lane; c < chunks; c += 32) {
-    const float2 v = __ldcg(part + c);
-    l += v.x == -CUDART_INF_F ? 0.f : v.y * fast_exp2(v.x - m);
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + i * 32 + lane;
+      v[i] = c < chunks ? __ldcg(part + c) : make_float2(-CUDART_INF_F, 0.f);
+    }
+    const float mn = fmaxf(fmax3(m, v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
+    if (mn == -CUDART_INF_F) continue;
+    l *= fast_exp2(m - mn);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l = fmaf(v[i].y, fast_exp2(v[i].x - mn), l);
+    m = mn;
   }
+  float top = m;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  l = m == -CUDART_INF_F ? 0.f : l * fast_exp2(m - top);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  return m + log2f(l);
+  return top + log2f(l);
 }
 
 // NT: tiles of 8 rows (1 where every sequence has at most 8 rows).
@@ -583,23 +674,26 @@ template <typename Dot, int NT>
 __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const ScoreParams p) {
   constexpr int kStages = Dot::kStages, kTileBytes = 16 * Dot::kRowBytes;
   pdl_launch_dependents();  // few_columns_kernel waits for this grid
-  if (!p.own_plan) pdl_wait();
+  if (!p.own_plan) pdl_wait();  // the plan; else only the queue's counter is waited for, below
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Held held = hold_plan<true>(p, smem + kFewThreads / 32 * kStages * kTileBytes);
   const SeqPlan* plan = held.plan;
+  if (p.own_plan) pdl_wait();
   const int64_t n_units = held.stat[p.B];
   uint8_t* ring = smem + warp * kStages * kTileBytes;
   const uint32_t ring_u32 = smem_u32(ring);
 
-  int64_t next = (int64_t)blockIdx.x * (kFewThreads / 32) + warp;  // the units are dealt out to the warps in turn
+  int next = 0;  // lane 0: the unit after the one being looked up
+  if (lane == 0) next = atomicAdd(p.counters + 1, 1);
   auto look_up = [&]() {
     Unit u{-1, 0, 0, 0, 0, -1};
-    if (next >= n_units) return u;
-    u.s = find_seq(held.stat, p.B, next, lane);
+    const int at = __shfl_sync(0xffffffffu, next, 0);
+    if (at >= n_units) return u;
+    if (lane == 0) next = atomicAdd(p.counters + 1, 1);
+    u.s = find_seq(held.stat, p.B, at, lane);
     // heads innermost: neighbouring warps read neighbouring parts of the same tokens' rows
-    const int w = (int)(next - held.stat[u.s]);
-    next += (int64_t)gridDim.x * (kFewThreads / 32);
+    const int w = (int)(at - held.stat[u.s]);
     u.c = w / p.Hkv;
     u.h = w - u.c * p.Hkv;
     u.kb = u.c * plan[u.s].chunk;
@@ -684,21 +778,59 @@ __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const Sc
   copy_wait<0>();
 }
 
-// Weights and scores from the kept logits: a block takes kColChunk keys of a
-// head, kAt keys a thread at a time; the first keys' logits are loaded before
-// the rows' lse are put together.
+// lse of rows r0 .. r0 + 3 of a head from their chunks' (max, sum), on a whole
+// warp, all four in flight; +inf past the rows (padding weighs nothing).
+__device__ __forceinline__ void rows_lse(const float2* part, int chunks, int rows, int r0, int lane, float (&lse)[4]) {
+  float m[4], l[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    m[r] = -CUDART_INF_F;
+    l[r] = 0.f;
+  }
+  for (int c0 = 0; c0 < chunks; c0 += 64) {
+    float2 v[4][2];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = c0 + i * 32 + lane;
+        v[r][i] = r0 + r < rows && c < chunks ? __ldcg(part + (int64_t)(r0 + r) * chunks + c)
+                                              : make_float2(-CUDART_INF_F, 0.f);
+      }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float mn = fmax3(m[r], v[r][0].x, v[r][1].x);
+      if (mn == -CUDART_INF_F) continue;
+      l[r] = l[r] * fast_exp2(m[r] - mn) + (v[r][0].y * fast_exp2(v[r][0].x - mn) + v[r][1].y * fast_exp2(v[r][1].x - mn));
+      m[r] = mn;
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    float top = m[r];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = m[r] == -CUDART_INF_F ? 0.f : l[r] * fast_exp2(m[r] - top);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    lse[r] = r0 + r < rows ? top + log2f(sum) : CUDART_INF_F;
+  }
+}
+
+// Weights and scores of keys kb .. ke - 1 of a head from the kept logits, on a
+// warp, kAt keys a lane at a time; the first keys' logits and the rows'
+// partials are loaded together.
 template <int PAD>
-__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int kb, float* lse_sh) {
+__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int kb, int ke, int lane) {
   const float* z = p.logit + sp.logit + (int64_t)h * sp.L * PAD;
-  const int ke = min(sp.L, kb + kColChunk);
   const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len;
-  constexpr int kAt = PAD <= 4 ? 4 : PAD == 8 ? 2 : 1;
+  constexpr int kAt = PAD <= 4 ? 8 : PAD == 8 ? 4 : 2;
   float x[kAt][PAD], old[kAt];
   auto load = [&](int j0) {
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
-      const int j = j0 + i * kColThreads;
-      old[i] = j < sp.L - sp.n && p.decay != 0.f ? p.scores[at + j] : 0.f;
+      const int j = j0 + i * 32;
+      old[i] = j < ke && j < sp.L - sp.n && p.decay != 0.f ? p.scores[at + j] : 0.f;
       if (j >= ke) continue;
       if constexpr (PAD == 2) {
         const float2 v = __ldcg(reinterpret_cast<const float2*>(z + (int64_t)j * 2));
@@ -716,54 +848,52 @@ __device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan&
       }
     }
   };
-  int j0 = kb + threadIdx.x;
+  int j0 = kb + lane;
   load(j0);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int r = warp; r < PAD; r += kColThreads / 32) {
-    // padding weighs nothing
-    const float v = r < sp.rows
-                        ? row_lse(p.part + sp.part + ((int64_t)h * sp.rows + r) * sp.chunks, sp.chunks, lane)
-                        : CUDART_INF_F;
-    if (lane == 0) lse_sh[r] = v;
-  }
-  __syncthreads();
-  float lse[PAD];
+  float lse[(PAD + 3) / 4][4];
 #pragma unroll
-  for (int r = 0; r < PAD; ++r) lse[r] = lse_sh[r];
-  while (j0 < ke) {
+  for (int g = 0; g < (PAD + 3) / 4; ++g)
+    rows_lse(p.part + sp.part + (int64_t)h * sp.rows * sp.chunks, sp.chunks, sp.rows, 4 * g, lane, lse[g]);
+  while (kb < ke) {
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
-      const int j = j0 + i * kColThreads;
+      const int j = j0 + i * 32;
       if (j >= ke) continue;
       float paid = 0.f;
 #pragma unroll
-      for (int r = 0; r < PAD; ++r) paid += fast_exp2(x[i][r] - lse[r]);
+      for (int r = 0; r < PAD; ++r) paid += fast_exp2(x[i][r] - lse[r / 4][r % 4]);
       p.out[at + j] = j < sp.L - sp.n && p.decay != 0.f ? fmaf(p.decay, old[i], paid) : paid;
     }
-    j0 += kAt * kColThreads;
-    if (j0 < ke) load(j0);
+    kb += kAt * 32;
+    j0 += kAt * 32;
+    if (kb < ke) load(j0);
   }
-  __syncthreads();  // lse_sh may be rewritten
 }
 
 constexpr int kColBlocks = 4;  // of an SM
 
 __global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(const ScoreParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float lse[kFewRows];
+  const int lane = threadIdx.x & 31;
   pdl_wait();
   const Held held = hold_plan<false>(p, smem);
+  // this warp's span of all heads' keys, in units of kColChunk keys of a head
   const int64_t n_units = held.col[p.B];
-  for (int64_t u = blockIdx.x; u < n_units; u += gridDim.x) {
-    const int s = find_seq(held.col, p.B, u, threadIdx.x & 31);
-    const SeqPlan sp = held.plan[s];
-    const int w = (int)(u - held.col[s]);
-    const int c = w / p.Hkv, h = w - c * p.Hkv;
+  const int warp = blockIdx.x * (kColThreads / 32) + (threadIdx.x >> 5), warps = gridDim.x * (kColThreads / 32);
+  int64_t u = n_units * warp / warps;
+  const int64_t end = n_units * (warp + 1) / warps;
+  while (u < end) {
+    const int s = find_seq(held.col, p.B, u, lane);
+    const SeqPlan& sp = held.plan[s];
+    const int w = (int)(u - held.col[s]), per_head = (sp.L + kColChunk - 1) / kColChunk;
+    const int h = w / per_head, c = w - h * per_head, count = (int)min(end - u, (int64_t)(per_head - c));
+    const int kb = c * kColChunk, ke = min(sp.L, (c + count) * kColChunk);
+    u += count;
     switch (sp.pad) {
-      case 2: few_columns<2>(p, sp, h, c * kColChunk, lse); break;
-      case 4: few_columns<4>(p, sp, h, c * kColChunk, lse); break;
-      case 8: few_columns<8>(p, sp, h, c * kColChunk, lse); break;
-      default: few_columns<16>(p, sp, h, c * kColChunk, lse); break;
+      case 2: few_columns<2>(p, sp, h, kb, ke, lane); break;
+      case 4: few_columns<4>(p, sp, h, kb, ke, lane); break;
+      case 8: few_columns<8>(p, sp, h, kb, ke, lane); break;
+      default: few_columns<16>(p, sp, h, kb, ke, lane); break;
     }
   }
 }
@@ -942,7 +1072,7 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  size_t off[kQueues], plan, tickets, lse, part, logit, least, total;
+  size_t off[kQueues], plan, tickets, counters, lse, part, logit, least, total;
 };
 
 // Kept logits: at most 16 padded rows of each kv head, or twice the rows
@@ -959,14 +1089,16 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   l.plan = at;
   at = align_up(at + (size_t)B * sizeof(SeqPlan));
   l.tickets = at;
-  at = align_up(at + (size_t)(2 * B * Hkv + 1) * sizeof(int));
+  at = align_up(at + (size_t)(2 * B * Hkv) * sizeof(int));
+  l.counters = at;
+  at = align_up(at + 2 * sizeof(int));
   l.lse = at;
   at = align_up(at + (size_t)(T * Hq) * sizeof(float));
   l.part = at;
   const int64_t chunk = std::min(kChunk, kFewChunk);
   // the tensor-core kernel's two partials a range of 256 keys or more take at
-  // most one entry more than one a chunk of 128 does
-  at = align_up(at + (size_t)(T * Hq) * (size_t)((keys + chunk - 1) / chunk + 1) * sizeof(float2));
+  // most one entry more than one a chunk of 128 does; a sequence's are rounded to pairs
+  at = align_up(at + ((size_t)(T * Hq) * (size_t)((keys + chunk - 1) / chunk + 1) + B) * sizeof(float2));
   l.logit = l.least = at;
   const size_t rows = (size_t)std::min(2 * T * Hq, kFewRows * B * Hkv);
   l.total = align_up(at + std::min(rows * (size_t)keys * sizeof(float), kLogitMax));
@@ -987,22 +1119,18 @@ cudaError_t launch_few(const ScoreParams& p, int sms, cudaStream_t s) {
     __atomic_fetch_or(&done_mask, 1ull << (dev & 63), __ATOMIC_RELEASE);
   }
   const int smem = kRing + held_bytes(p.B);
-  // as many blocks as are resident (the units are dealt out to all of them):
-  // shared memory is 228 KB an SM, 1 KB a block goes to the system and 2.5 KB to the plan's sums
+  // as many blocks as are resident: shared memory is 228 KB an SM, 1 KB a block goes to the system and 2.5 KB to the plan's sums
   const dim3 grid(sms * std::max(1, std::min(Dot::kBlocks, 228 * 1024 / (smem + 3600))));
-  if (p.own_plan) {  // the first kernel of the call: an ordinary launch
-    few_kernel<Dot, NT><<<grid, kFewThreads, smem, s>>>(p);
-    e = cudaGetLastError();
-  } else {
-    e = launch_pdl(few_kernel<Dot, NT>, grid, dim3(kFewThreads), smem, s, p);
-  }
-  if (e != cudaSuccess) return e;
+  if ((e = launch_pdl(few_kernel<Dot, NT>, grid, dim3(kFewThreads), smem, s, p)) != cudaSuccess) return e;
   return launch_pdl(few_columns_kernel, dim3(sms * kColBlocks), dim3(kColThreads), held_bytes(p.B), s, p);
 }
 
 template <typename TQ, typename TK, int D, typename Dot>
 cudaError_t launch(const ScoreParams& p, bool only_few, bool one_tile, int sms, cudaStream_t s) {
-  if (!p.own_plan) plan_scores_kernel<<<1, std::min(kPlanThreads, (p.B + 31) / 32 * 32), 0, s>>>(p);
+  if (p.own_plan)
+    start_few_kernel<<<1, 32, 0, s>>>(p.counters);
+  else
+    plan_scores_kernel<<<1, std::min(kPlanThreads, (p.B + 31) / 32 * 32), 0, s>>>(p);
   cudaError_t e = one_tile ? launch_few<Dot, 1>(p, sms, s) : launch_few<Dot, 2>(p, sms, s);
   if (e != cudaSuccess || only_few || p.tensor) return e;
   const int grid = sms * 8;
@@ -1057,12 +1185,14 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
     return fail(PKV_ERR_UNSUPPORTED, "block_size (supported: 8, 16, 32, 64)");
   if (!(scale > 0.f) || !isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale must be positive and finite");
   if (!(p.decay >= 0.f) || !isfinite(p.decay)) return fail(PKV_ERR_INVALID_ARG, "decay must be finite and >= 0");
+  if (max_query_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_query_len must be >= 0");
   if (f8 && (!(k_scale > 0.f) || !isfinite(k_scale)))
     return fail(PKV_ERR_INVALID_ARG, "k_scale must be positive and finite");
   if ((int64_t)p.max_blocks * p.bs > (int64_t)1 << 30 || p.max_len > 1 << 30)
     return fail(PKV_ERR_UNSUPPORTED, "context too long");
   if (p.T > ((int64_t)1 << 31) / ((int64_t)p.Hq * D)) return fail(PKV_ERR_UNSUPPORTED, "num_tokens too large");
   const int64_t keys = std::min<int64_t>(p.max_len, (int64_t)p.max_blocks * p.bs);
+  if (p.num_blocks > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "num_blocks exceeds int32");
   if ((p.B + p.T) * p.Hkv > (((int64_t)1 << 31) - 1) / ((keys + 127) / 128))
     return fail(PKV_ERR_UNSUPPORTED, "too much work for one call");
   if (p.B == 0 || p.T == 0) return PKV_OK;
@@ -1081,22 +1211,24 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   for (int k = 0; k < kQueues; ++k) p.off[k] = reinterpret_cast<int64_t*>(ws + lay.off[k]);
   p.plan = reinterpret_cast<SeqPlan*>(ws + lay.plan);
   p.tickets = reinterpret_cast<int*>(ws + lay.tickets);
+  p.counters = reinterpret_cast<int*>(ws + lay.counters);
   p.lse = reinterpret_cast<float*>(ws + lay.lse);
   p.part = reinterpret_cast<float2*>(ws + lay.part);
   p.logit = reinterpret_cast<float*>(ws + lay.logit);
   p.logit_cap = (int64_t)((ws_bytes - lay.least) / sizeof(float));
   p.scale_log2 = (f8 ? scale * k_scale : scale) * 1.4426950408889634f;
-  // every sequence has few rows, and their logits fit: the other kernels have nothing to do
+  // every sequence has few rows (the plan holds them to the promised query
+  // length), and their logits fit: the other kernels have nothing to do
   const int64_t most_rows = std::min<int64_t>(p.T, max_query_len > 0 ? max_query_len : p.T) * p.G;
   const bool only_few = most_rows <= kFewRows && std::min(2 * p.T * p.Hq, (int64_t)kFewRows * p.B * p.Hkv) * keys <= p.logit_cap;
   p.own_plan = only_few && p.B <= kHeldSeqs;
   const bool one_tile = most_rows <= 8;
+  p.max_query = max_query_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   typedef __nv_bfloat16 bf16;
   // bf16: more rows go to the tensor-core kernel (its operands come through tensor maps)
   p.tensor = !f8 && dtype == PKV_DTYPE_BF16;
   p.tile_tok = 128 / p.G;
-  p.tc_lag = 2 * sms;
   CUtensorMap qmap, kmap;
   pkv_status mst;
   if (p.tensor && !only_few) {

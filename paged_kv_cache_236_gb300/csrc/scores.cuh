@@ -9,7 +9,7 @@ namespace pkv {
 
 constexpr int kFewRows = 16;    // rows of a few-row sequence's kv head
 constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
-constexpr int kColChunk = 1024;  // keys of a column unit (few rows)
+constexpr int kColChunk = 256;  // keys of a column unit (few rows)
 constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
 constexpr int kChunk = 256;   // keys of a work unit (other rows)
 enum { kFew = 1, kTensor = 2, kOther = 3 };
@@ -17,10 +17,8 @@ constexpr int kRowGroup = 8;  // rows of a work unit (other rows)
 
 // Offsets of each sequence's work, as prefix sums: the unit queues of the
 // kernels below (few-row stats and columns; other rows' stats and columns),
-// the partial (max, sum)s, the lse rows and the kept logits.
-// The tensor-core kernel's two kinds of items share one queue: the column
-// items of sequence s start at place kTcAt[s] of it.
-enum { kFewStat, kFewCol, kStat, kCol, kTcStat, kTcCol, kTcAt, kQueues };
+// the tensor-core kernel's).
+enum { kFewStat, kFewCol, kStat, kCol, kTcStat, kTcCol, kQueues };
 
 struct SeqPlan {
   int64_t part, lse, logit;
@@ -42,14 +40,15 @@ struct ScoreParams {
   float* out;
   int64_t* off[kQueues];  // [B + 1] each: first unit of each sequence in the queues
   SeqPlan* plan;    // [B]
-  int* tickets;     // tensor-core kernel: [B, Hkv] partials done, then [B, Hkv] lse ready, then its queue's counter
+  int* tickets;     // tensor-core kernel: [B, Hkv] partials done, then [B, Hkv] lse ready
+  int* counters;    // next of the tensor-core kernel's and of the few-row kernel's queue
   float2* part;     // (m, l) per (kv head, row, chunk) of a sequence
   float* lse;       // per (kv head, row) of a sequence
   float* logit;     // per (kv head, key, padded row) of a few-row sequence
   int64_t logit_cap;
+  int max_query;    // the promised longest query, 0: none
   int own_plan;     // the few-row kernels make the plan themselves (no other kernel runs)
   int tensor;       // sequences of more rows go to the tensor-core kernel
-  int tc_lag;       // column items follow this many later stats items in its queue
   int tile_tok;     // tokens of a row tile: floor(128 / G)
   int64_t T, num_blocks;
   int B, Hq, Hkv, G, bs, bs_log, max_blocks, num_rows, max_len, causal;

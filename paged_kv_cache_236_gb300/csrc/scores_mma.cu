@@ -14,34 +14,43 @@
 //
 // What bounds it: the exponentials.  A 128 x 128 tile is 16384 of them, 1024
 // cycles of the SM's 16 a cycle, in each pass, next to 512 cycles of MMA; with
-// few rows (a verify window of 40) K's 32 KB a tile from HBM instead.  K is
-// read from HBM once: a sequence's column items follow its stats items in the
-// queue at a distance of two items an SM, so the second pass finds K in L2.
+// few rows (a verify window of 40) K's 32 KB a tile from HBM instead, twice.
+// All stats items come before the column items.  Interleaved, a sequence's
+// column items a short way behind its stats items so that they find K in L2,
+// the waits for the lse cost more than the reads (verify batch 199 to 280 us
+// over distances of one to two items an SM, 194 us this way; prompt windows
+// 140 to 210 us against 121).
 //
-// An item pairs one resident tile with a list of streamed ones:
-//   stats          Q tile resident, K tiles of the range streamed;
-//   columns, one row tile in all:  the same (each K tile's keys are done
-//                  after one pair);
-//   columns, more row tiles:  a K tile resident, the row tiles that see it
-//                  streamed, sums kept in registers.
+// An item is a range of keys of a head against one row tile (stats) or all row
+// tiles that see any of it, one after the other (columns; each thread keeps its
+// keys' sums in shared memory between row tiles).  The Q tile is resident, the
+// range's K tiles are streamed.
 //
-// Roles (384 threads, one CTA per SM, persistent):
+// Roles (416 threads, one CTA per SM, persistent):
 //   warps 0, 3   producers, one per 64-column half of the tiles (one warp's
 //                2 KB boxes go at about 100 cycles each): K by one
 //                {64, 1, block_size, 1} box per physical block, Q by one
 //                {64, G, 128 / G} box;
 //   warp 1       TMEM allocation, and the thread that issues the MMAs;
-//   warp 2       takes items from the queue and publishes them in a ring;
+//   warp 2       takes items from the queue, looks them up in the plan (in shared memory up to kHeldSeqs sequences), reads the
+//                range's block ids and publishes both in a ring (a producer
+//                reading the ids of the next tile itself, a tile ahead, was
+//                held to their latency: 1.7 us a tile).  A column item is
+//                published once its head's lse are complete;
 //   warps 4-11   two groups of 128 threads (thread = accumulator lane), which
-//                take the item's pairs in turn.
+//                take the item's tiles in turn;
+//   warp 12      closes stats items: when both groups have written an item's
+//                partials it counts the item, and the head's last one makes it
+//                combine the rows' lse and announce them; the groups go on
+//                without a fence or a wait for the count.
 // Shared memory: 2 resident tiles and a 4-stage ring of streamed ones (192 KB
 // at head_dim 128).  TMEM: four 128-column accumulators.
 //
-// A column item waits until its head's lse are complete: every stats item it
-// depends on was taken from the queue before it, by a CTA that works its
-// items off in order, so the wait ends.  All waits are bounded (2 s, then the
-// device error word says so and every role leaves); the 128 threads of a
-// group settle failures at barriers that OR them, so none is left waiting.
+// The wait for a head's lse ends: every stats item it depends on was taken
+// from the queue before the column item, by a CTA that works its items off in
+// order.  All waits are bounded (2 s, then the device error word says so and
+// every role leaves); the 128 threads of a group settle failures at barriers
+// that OR them, so none is left waiting.
 #include <math_constants.h>
 
 #include "pkv_device.cuh"
@@ -52,33 +61,33 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreadsMma = 384;
-constexpr int kTile = 128;     // rows or keys of a tile
-constexpr int kStages = 4;     // streamed tiles
-constexpr int kAccs = 4;       // accumulators
-constexpr int kItems = 3;      // item ring
+constexpr int kThreadsMma = 416;
+constexpr int kTile = 128;      // rows or keys of a tile
+constexpr int kStages = 4;      // streamed tiles
+constexpr int kAccs = 4;        // accumulators
+constexpr int kItems = 2;       // item ring
+constexpr int kRangeTiles = kTcRange / kTile;
+constexpr int kIds = kTcRange / 8;  // block ids of a range, at most
+constexpr int kHeldSeqs = 256;  // sequences whose plan is kept in shared memory
 constexpr float kRaise = 8.0f;  // log2 units a row maximum may exceed its reference by
-
 constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
 constexpr uint32_t kIdesc16 = idesc_bf16(128, 16, false, false);  // N = 16; N / 8 sits at bit 17
 
-enum { kDone = 0, kStats = 1, kColsK = 2, kColsQ = 3 };
+enum { kDone = 0, kStats = 1, kCols = 2 };
 
 struct alignas(16) Item {
   int64_t lse, part;
   int type, s, h, row;
   int L, n, rows, qstart;
-  int x;       // resident tile: row tile (kStats, kColsK) or first key (kColsQ)
-  int y0, ny;  // streamed tiles: first key / first row tile, and how many
-  int chunk, chunks, tiles;
+  int tile0, tiles;   // row tiles: the first, and how many (stats: one)
+  int key0, chunk, chunks, all_tiles;
 };
 
 struct Bars {
   uint64_t x_full[2][2], x_empty[2];             // resident tile [buffer][half]
   uint64_t y_full[kStages][2], y_empty[kStages];  // streamed tile [stage][half]
   uint64_t acc_full[kAccs], acc_empty[kAccs];
-  uint64_t item_full[kItems], item_empty[kItems];
-  uint64_t xch_full, xch_empty;  // the second group's column sums
+  uint64_t item_full[kItems], item_empty[kItems], item_closed[kItems];
 };
 
 template <int D>
@@ -87,16 +96,25 @@ struct Lay {
   static constexpr int kXOff = 0;
   static constexpr int kYOff = 2 * kTileBytes;
   static constexpr int kItemOff = kYOff + kStages * kTileBytes;
-  static constexpr int kLseOff = kItemOff + kItems * (int)sizeof(Item);
-  static constexpr int kXchOff = kLseOff + 2 * 2 * kTile * 4;  // [group][2][128] negated lse
-  static constexpr int kBarOff = (kXchOff + kTile * 4 + 15) & ~15;
-  static constexpr int kSmem = kBarOff + (int)sizeof(Bars) + 32 + 1024;
+  static constexpr int kIdOff = kItemOff + kItems * (int)sizeof(Item);
+  static constexpr int kLseOff = kIdOff + kItems * kIds * 4;   // [group][2][128] negated lse
+  static constexpr int kSumOff = kLseOff + 2 * 2 * kTile * 4;  // [tile of the range][128] column sums
+  static constexpr int kBarOff = kSumOff + kRangeTiles * kTile * 4;
+  static constexpr int kPlanOff = (kBarOff + (int)sizeof(Bars) + 16 + 15) & ~15;
+  static constexpr int kSmem = kPlanOff + kHeldSeqs * (int)sizeof(SeqPlan) + 2 * (kHeldSeqs + 1) * 8 + 1024;
 };
 static_assert(sizeof(Item) % 16 == 0, "item slot");
 static_assert(Lay<128>::kSmem <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+
+// K tiles of the item's range that row tile `tile` sees any key of.
+__device__ __forceinline__ int tiles_seen(const ScoreParams& p, const Item& im, int tile) {
+  const int last = min(im.n, (tile + 1) * p.tile_tok) - 1;  // the tile's last token
+  const int ke = min(p.causal ? im.L - im.n + last + 1 : im.L, min(im.L, im.key0 + kTcRange));
+  return ke > im.key0 ? (ke - im.key0 + kTile - 1) / kTile : 0;
 }
 
 // Column items: 32 logits of one key against rows' negated lse: the sum of
@@ -122,8 +140,8 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bars = reinterpret_cast<Bars*>(smem + Y::kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Y::kBarOff + sizeof(Bars));
-  int* last_flag = reinterpret_cast<int*>(tmem_slot + 1);  // [2]
   Item* items = reinterpret_cast<Item*>(smem + Y::kItemOff);
+  int* ids = reinterpret_cast<int*>(smem + Y::kIdOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{p.err, (uint32_t)kWaitTimeoutNs};
 
@@ -142,10 +160,9 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], kHalves + 1 + 8);  // producers, the MMA thread, eight epilogue warps
+      mbar_init(&bars->item_empty[i], kHalves + 1 + 8 + 1);  // producers, the MMA thread, the groups' warps, the closer
+      mbar_init(&bars->item_closed[i], 256);
     }
-    mbar_init(&bars->xch_full, 128);
-    mbar_init(&bars->xch_empty, 128);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -162,33 +179,39 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
 
   if (warp == 2) {
     // ================================================================ items
-    const int64_t n_stat = __ldg(p.off[kTcStat] + p.B), n_all = n_stat + __ldg(p.off[kTcCol] + p.B);
-    int* queue = ready + (int64_t)p.B * p.Hkv;
+    const int64_t *o_stat = p.off[kTcStat], *o_col = p.off[kTcCol];
+    const SeqPlan* plan = p.plan;
+    if (p.B <= kHeldSeqs) {
+      SeqPlan* plans = reinterpret_cast<SeqPlan*>(smem + Y::kPlanOff);
+      int64_t* offs = reinterpret_cast<int64_t*>(plans + kHeldSeqs);
+      for (int i = lane; i < p.B * (int)(sizeof(SeqPlan) / 8); i += 32)
+        reinterpret_cast<int64_t*>(plans)[i] = reinterpret_cast<const int64_t*>(plan)[i];
+      for (int i = lane; i <= p.B; i += 32) {
+        offs[i] = o_stat[i];
+        offs[kHeldSeqs + 1 + i] = o_col[i];
+      }
+      __syncwarp();
+      plan = plans;
+      o_stat = offs;
+      o_col = offs + kHeldSeqs + 1;
+    }
+    const int64_t n_stat = o_stat[p.B], n_all = n_stat + o_col[p.B];
+    // Items are taken no earlier than a slot is free: with three slots and one
+    // item more in hand the SMs ended unevenly (prompt windows 145 us, not 121).
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
       if (!wait_all(&bars->item_empty[sl], ((it / kItems) & 1) ^ 1, wc)) break;
       int64_t u = 0;
-      if (lane == 0) u = atomicAdd(queue, 1);
+      if (lane == 0) u = atomicAdd(p.counters, 1);
       u = __shfl_sync(0xffffffffu, u, 0);
       Item item{};
       if (u < n_all) {
-        // a place of the queue is a column item of the last sequence whose
-        // column items start at or before it, or else a stats item
-        int64_t v = u;
-        bool cols = false;
-        int s = 0;
-        if (u >= __ldg(p.off[kTcAt])) {
-          s = find_seq(p.off[kTcAt], p.B, u, lane);
-          const int64_t at = __ldg(p.off[kTcAt] + s), before = __ldg(p.off[kTcCol] + s),
-                        after = __ldg(p.off[kTcCol] + s + 1);
-          cols = u < at + (after - before);
-          v = cols ? u - at : u - after;
-        }
-        if (!cols) {
-          s = find_seq(p.off[kTcStat], p.B, v, lane);
-          v -= __ldg(p.off[kTcStat] + s);
-        }
-        const SeqPlan sp = p.plan[s];
+        const bool cols = u >= n_stat;
+        const int64_t* off = cols ? o_col : o_stat;
+        const int64_t v = cols ? u - n_stat : u;
+        const int s = find_seq(off, p.B, v, lane);
+        const SeqPlan sp = plan[s];
+        item.type = cols ? kCols : kStats;
         item.lse = sp.lse;
         item.part = sp.part;
         item.s = s;
@@ -198,30 +221,54 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
         item.rows = sp.rows;
         item.qstart = p.qsl[s];
         item.chunks = sp.chunks;
-        item.tiles = sp.tiles;
-        const int w = (int)v;
-        if (cols && sp.tiles > 1) {
-          // heads innermost; rows that see the tile's first key
-          item.type = kColsQ;
-          const int kt = w / p.Hkv;
-          item.h = w - kt * p.Hkv;
-          item.x = kt * kTile;
-          item.y0 = p.causal ? max(0, item.x - (sp.L - sp.n)) / p.tile_tok : 0;
-          item.ny = sp.tiles - item.y0;
-        } else {
-          item.type = cols ? kColsK : kStats;
-          const int tile = w % sp.tiles, ch = w / sp.tiles;
-          item.chunk = ch / p.Hkv;
-          item.h = ch - item.chunk * p.Hkv;
-          item.x = tile;
-          item.y0 = item.chunk * kTcRange;
-          // keys its last row sees (columns: all keys, each gets its score)
-          const int last = min(sp.n, (tile + 1) * p.tile_tok) - 1;
-          const int see = cols || !p.causal ? sp.L : sp.L - sp.n + last + 1;
-          const int ke = min(see, min(sp.L, item.y0 + kTcRange));
-          item.ny = ke > item.y0 ? (ke - item.y0 + kTile - 1) / kTile : 0;
+        item.all_tiles = sp.tiles;
+        // row tiles innermost, then heads
+        int w = (int)(v - off[s]);
+        if (!cols) {
+          item.tile0 = w % sp.tiles;
+          item.tiles = 1;
+          w /= sp.tiles;
+        }
+        item.chunk = w / p.Hkv;
+        item.h = w - item.chunk * p.Hkv;
+        item.key0 = item.chunk * kTcRange;
+        if (cols) {  // from the first row tile that sees any of the range
+          item.tile0 = p.causal ? max(0, item.key0 - (sp.L - sp.n)) / p.tile_tok : 0;
+          item.tiles = sp.tiles - item.tile0;
+        }
+        // the range's blocks (outside the pool: read as zeros)
+        const int nblk = (min(sp.L, item.key0 + kTcRange) - item.key0 + p.bs - 1) >> p.bs_log;
+        const int32_t* bt = p.tables + (int64_t)s * p.max_blocks + (item.key0 >> p.bs_log);
+        int id[kIds / 32];
+#pragma unroll
+        for (int k = 0; k < kIds / 32; ++k) {
+          const int i = k * 32 + lane;
+          id[k] = i < nblk ? __ldg(bt + i) : (int)p.num_blocks;
+        }
+#pragma unroll
+        for (int k = 0; k < kIds / 32; ++k) {
+          if (id[k] < 0 || id[k] > p.num_blocks || (id[k] == p.num_blocks && k * 32 + lane < nblk)) {
+            raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+            id[k] = (int)p.num_blocks;
+          }
+          ids[sl * kIds + k * 32 + lane] = id[k];
+        }
+        if (cols) {
+          bool ok = true;
+          if (lane == 0) {
+            const uint64_t t0 = globaltimer();
+            while (ld_acquire(ready + (int64_t)s * p.Hkv + item.h) == 0) {
+              if (globaltimer() - t0 > kWaitTimeoutNs) {
+                raise_error(p.err, PKV_DEVERR_TIMEOUT);
+                ok = false;
+                break;
+              }
+            }
+          }
+          if (!__shfl_sync(0xffffffffu, (int)ok, 0)) break;
         }
       }
+      __syncwarp();  // the ids are written
       if (lane == 0) {
         items[sl] = item;
         mbar_arrive(&bars->item_full[sl]);
@@ -245,58 +292,41 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
         const int sl = it % kItems;
         if (!wait_all(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
         const Item im = items[sl];
+        int id[kRangeTiles];  // this lane's block of each K tile
+#pragma unroll
+        for (int i = 0; i < kRangeTiles; ++i) id[i] = ids[sl * kIds + min(kIds - 1, i * nb_per_tile + lane)];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
         if (im.type == kDone) break;
-        if (im.ny == 0) continue;
-        const int32_t* bt = p.tables + (int64_t)im.s * p.max_blocks;
-        const int nblk = (im.L + p.bs - 1) / p.bs;
-        auto block_of = [&](int key) {  // this lane's physical block of the tile (outside the pool: reads as zeros)
-          const int lb = key / p.bs + lane;
-          int b = (int)p.num_blocks;
-          if (lane < nb_per_tile && lb < nblk) {
-            const int x = __ldg(bt + lb);
-            if (x >= 0 && x < p.num_blocks)
-              b = x;
-            else if (half == 0)
-              raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
-          }
-          return b;
-        };
-        auto load_k = [&](uint8_t* dst, uint64_t* bar, int phys) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, kTile * 128);
-          __syncwarp();
-          if (lane < nb_per_tile)
-            tma_load_4d(dst + half * kHalf + lane * p.bs * 128, &kmap, bar, half * 64, im.h, 0, phys);
-        };
-        auto load_q = [&](uint8_t* dst, uint64_t* bar, int tile) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar, q_bytes);
-            tma_load_3d(dst + half * kHalf, &qmap, bar, half * 64, im.h * p.G, im.qstart + tile * p.tile_tok);
-          }
-        };
-        const int xb = nx & 1;
-        if (!wait_all(&bars->x_empty[xb], ((nx >> 1) & 1) ^ 1, wc)) break;
-        uint8_t* xd = smem + Y::kXOff + xb * Y::kTileBytes;
-        if (im.type == kColsQ)
-          load_k(xd, &bars->x_full[xb][half], block_of(im.x));
-        else
-          load_q(xd, &bars->x_full[xb][half], im.x);
-        ++nx;
-        int phys = im.type == kColsQ ? 0 : block_of(im.y0);
-        for (int i = 0; i < im.ny; ++i, ++g) {
-          const int st = g % kStages;
-          const int next = im.type != kColsQ && i + 1 < im.ny ? block_of(im.y0 + (i + 1) * kTile) : 0;
-          if (!wait_all(&bars->y_empty[st], ((g / kStages) & 1) ^ 1, wc)) {
+        for (int tile = im.tile0; tile < im.tile0 + im.tiles && ok; ++tile) {
+          const int ny = tiles_seen(p, im, tile);
+          if (ny == 0) continue;
+          const int xb = nx & 1;
+          if (!wait_all(&bars->x_empty[xb], ((nx >> 1) & 1) ^ 1, wc)) {
             ok = false;
             break;
           }
-          uint8_t* yd = smem + Y::kYOff + st * Y::kTileBytes;
-          if (im.type == kColsQ)
-            load_q(yd, &bars->y_full[st][half], im.y0 + i);
-          else
-            load_k(yd, &bars->y_full[st][half], phys);
-          phys = next;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&bars->x_full[xb][half], q_bytes);
+            tma_load_3d(smem + Y::kXOff + xb * Y::kTileBytes + half * kHalf, &qmap, &bars->x_full[xb][half], half * 64,
+                        im.h * p.G, im.qstart + tile * p.tile_tok);
+          }
+          ++nx;
+#pragma unroll
+          for (int i = 0; i < kRangeTiles; ++i) {
+            if (i < ny && ok) {
+              const int st = g % kStages;
+              ok = wait_all(&bars->y_empty[st], ((g / kStages) & 1) ^ 1, wc);
+              if (ok) {
+                if (lane == 0) mbar_arrive_expect_tx(&bars->y_full[st][half], kTile * 128);
+                __syncwarp();
+                if (lane < nb_per_tile)
+                  tma_load_4d(smem + Y::kYOff + st * Y::kTileBytes + half * kHalf + lane * p.bs * 128, &kmap,
+                              &bars->y_full[st][half], half * 64, im.h, 0, id[i]);
+                ++g;
+              }
+            }
+          }
         }
       }
       // none of this warp's copies may be in flight when the CTA ends (after
@@ -313,43 +343,83 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
       for (int it = 0; ok; ++it) {
         const int sl = it % kItems;
         if (!mbar_wait(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
-        const int type = items[sl].type, ny = items[sl].ny, rows = items[sl].rows, x = items[sl].x, y0 = items[sl].y0;
+        const Item im = items[sl];
         mbar_arrive(&bars->item_empty[sl]);
-        if (type == kDone) break;
-        if (ny == 0) continue;
-        const int xb = nx & 1;
-        for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
-        if (!ok) break;
+        if (im.type == kDone) break;
         const int tile_rows = p.tile_tok * p.G;
-        const uint64_t dx = desc_add(dx0, xb * Y::kTileBytes);
-        for (int i = 0; i < ny; ++i, ++g) {
-          const int st = g % kStages, acc = g % kAccs;
-          for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->y_full[st][h], (g / kStages) & 1, wc);
-          if (!ok || !mbar_wait(&bars->acc_empty[acc], ((g / kAccs) & 1) ^ 1, wc)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t dy = desc_add(dy0, st * Y::kTileBytes);
-          // rows on N in a column item: a multiple of 16
-          const int tile = type == kColsQ ? y0 + i : x;
-          const int nr = (min(tile_rows, rows - tile * tile_rows) + 15) & ~15;
-          const uint32_t idesc = type == kStats ? kIdesc128 : kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
-          const uint64_t da = type == kColsK ? dy : dx, db = type == kColsK ? dx : dy;
+        for (int tile = im.tile0; tile < im.tile0 + im.tiles && ok; ++tile) {
+          const int ny = tiles_seen(p, im, tile);
+          if (ny == 0) continue;
+          const int xb = nx & 1;
+          for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
+          if (!ok) break;
+          ++nx;
+          const uint64_t dx = desc_add(dx0, xb * Y::kTileBytes);
+          // stats: rows on M; columns: rows on N, a multiple of 16 of them
+          const int nr = (min(tile_rows, im.rows - tile * tile_rows) + 15) & ~15;
+          const uint32_t idesc = im.type == kStats ? kIdesc128 : kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
+          for (int i = 0; i < ny; ++i, ++g) {
+            const int st = g % kStages, acc = g % kAccs;
+            for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->y_full[st][h], (g / kStages) & 1, wc);
+            if (!ok || !mbar_wait(&bars->acc_empty[acc], ((g / kAccs) & 1) ^ 1, wc)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t dy = desc_add(dy0, st * Y::kTileBytes);
+            const uint64_t da = im.type == kStats ? dx : dy, db = im.type == kStats ? dy : dx;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(tmem + acc * 128, desc_add(da, (kk >> 2) * kHalf + (kk & 3) * 32),
-                      desc_add(db, (kk >> 2) * kHalf + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
-          umma_commit(&bars->acc_full[acc]);
-          umma_commit(&bars->y_empty[st]);
-          if (i == ny - 1) umma_commit(&bars->x_empty[xb]);
+            for (int kk = 0; kk < D / 16; ++kk)
+              umma_bf16(tmem + acc * 128, desc_add(da, (kk >> 2) * kHalf + (kk & 3) * 32),
+                        desc_add(db, (kk >> 2) * kHalf + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
+            umma_commit(&bars->acc_full[acc]);
+            umma_commit(&bars->y_empty[st]);
+            if (i == ny - 1) umma_commit(&bars->x_empty[xb]);
+          }
         }
-        ++nx;
       }
       // leaving: the MMAs already issued finish before TMEM is freed
       for (int j = max(0, g - kAccs); j < g; ++j) mbar_wait(&bars->acc_full[j % kAccs], (j / kAccs) & 1, wc);
     }
     __syncwarp();
+  } else if (warp == 12) {
+    // ================================================================ closer
+    for (int it = 0;; ++it) {
+      const int sl = it % kItems;
+      const uint32_t ph = (it / kItems) & 1;
+      if (!wait_all(&bars->item_full[sl], ph, wc)) break;
+      const Item im = items[sl];
+      if (im.type == kDone) break;
+      // the slot is not given back before its closing phase has been seen: the
+      // groups cannot be a phase further
+      if (!wait_all(&bars->item_closed[sl], ph, wc)) break;
+      if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
+      if (im.type != kStats) continue;
+      const int64_t sh = (int64_t)im.s * p.Hkv + im.h;
+      // the groups' writes are ordered before this fence by their arrivals
+      __threadfence();
+      int done = 0;
+      if (lane == 0) done = atomicAdd(p.tickets + sh, 1);
+      if (__shfl_sync(0xffffffffu, done, 0) != im.chunks * im.all_tiles - 1) continue;
+      // the head's last item: each row's lse from its partials, two a chunk
+      __threadfence();
+      const int parts = 2 * im.chunks;
+      for (int r = lane; r < im.rows; r += 32) {
+        const float4* part = reinterpret_cast<const float4*>(p.part + im.part + ((int64_t)im.h * im.rows + r) * parts);
+        float m = -CUDART_INF_F, l = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < im.chunks; ++c) {
+          const float4 v = __ldcg(part + c);
+          const float mn = fmax3(m, v.x, v.z);
+          if (mn != -CUDART_INF_F) l = l * fast_exp2(m - mn) + (v.y * fast_exp2(v.x - mn) + v.w * fast_exp2(v.z - mn));
+          m = mn;
+        }
+        p.lse[im.lse + (int64_t)im.h * im.rows + r] = m + log2f(l);
+      }
+      __threadfence();
+      __syncwarp();
+      if (lane == 0) st_release(ready + sh, 1);
+    }
   } else {
     // ================================================================ epilogue groups
     const int wg = (warp - 4) >> 2;
@@ -357,10 +427,10 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
     const int t = q4 * 32 + lane;  // accumulator lane
     const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
     float* nlse = reinterpret_cast<float*>(smem + Y::kLseOff) + wg * 2 * kTile;
-    float* xch = reinterpret_cast<float*>(smem + Y::kXchOff);
+    float* sums = reinterpret_cast<float*>(smem + Y::kSumOff) + t;
     const int tile_rows = p.tile_tok * p.G;
     const f32x2 scale2 = pk2(p.scale_log2, p.scale_log2);
-    int g = 0, n_xch = 0;
+    int g = 0, n_nl = 0;  // K tiles and lse buffers so far
     bool pending = false;
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
@@ -370,22 +440,22 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
       if (im.type == kDone) break;
-      const int64_t sh = (int64_t)im.s * p.Hkv + im.h;
       if (im.type == kStats) {
         // ------------------------------------------------------- stats
-        const int row = im.x * tile_rows + t;
+        const int ny = tiles_seen(p, im, im.tile0);
+        const int row = im.tile0 * tile_rows + t;
         const bool valid = t < tile_rows && row < im.rows;
         const int vis = p.causal ? min(im.L, im.L - im.n + row / p.G + 1) : im.L;
         float m = -CUDART_INF_F, l = 0.f;
         const bool live = __any_sync(0xffffffffu, valid);
-        for (int i = 0; i < im.ny; ++i, ++g) {
+        for (int i = 0; i < ny; ++i, ++g) {
           if ((i & 1) != wg || pending) continue;
           const int acc = g % kAccs;
           pending = !wait_all(&bars->acc_full[acc], (g / kAccs) & 1, wc);
           if (pending) continue;
           tc_fence_after();
           if (live) {
-            const int kb = im.y0 + i * kTile;
+            const int kb = im.key0 + i * kTile;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               uint32_t z[32];
@@ -426,44 +496,13 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->acc_empty[acc]);
         }
-        const int parts = 2 * im.chunks;
-        if (valid && !pending)
-          p.part[im.part + ((int64_t)im.h * im.rows + row) * parts + im.chunk * 2 + wg] = make_float2(m, l);
-        __threadfence();
-        if (barrier_any(1 + wg, 128, pending)) break;
-        if (t == 0) last_flag[wg] = atomicAdd(p.tickets + sh, 1);
-        named_barrier(1 + wg, 128);
-        if (last_flag[wg] == parts * im.tiles - 1) {
-          // the head's last item: each row's lse from its partials
-          __threadfence();
-          for (int r = t; r < im.rows; r += 128) {
-            const float2* part = p.part + im.part + ((int64_t)im.h * im.rows + r) * parts;
-            float mm = -CUDART_INF_F, ll = 0.f;
-            for (int c = 0; c < parts; ++c) mm = fmaxf(mm, __ldcg(part + c).x);
-            for (int c = 0; c < parts; ++c) {
-              const float2 v = __ldcg(part + c);
-              if (v.x != -CUDART_INF_F) ll += v.y * fast_exp2(v.x - mm);
-            }
-            p.lse[im.lse + (int64_t)im.h * im.rows + r] = mm + log2f(ll);
-          }
-          __threadfence();
-          named_barrier(1 + wg, 128);
-          if (t == 0) st_release(ready + sh, 1);
-        }
+        if (pending) continue;  // leaves at the next agreement; the closer's wait runs out
+        if (valid)
+          p.part[im.part + ((int64_t)im.h * im.rows + row) * (2 * im.chunks) + im.chunk * 2 + wg] = make_float2(m, l);
+        mbar_arrive(&bars->item_closed[sl]);
         continue;
       }
       // --------------------------------------------------------- columns
-      if (t == 0) {
-        const uint64_t t0 = globaltimer();
-        while (ld_acquire(ready + sh) == 0) {
-          if (globaltimer() - t0 > kWaitTimeoutNs) {
-            raise_error(p.err, PKV_DEVERR_TIMEOUT);
-            pending = true;
-            break;
-          }
-        }
-      }
-      if (barrier_any(1 + wg, 128, pending)) break;
       const float* lse = p.lse + im.lse + (int64_t)im.h * im.rows;
       const int64_t at0 = ((int64_t)im.row * p.Hkv + im.h) * p.max_len;
       // rows of a row tile as negated lse; rows that are not there weigh nothing
@@ -471,91 +510,62 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
         const int row = tile * tile_rows + t;
         return t < tile_rows && row < im.rows ? -__ldcg(lse + row) : -CUDART_INF_F;
       };
-      // the weights of key j's accumulator lane against the rows of `tile`
-      auto weigh = [&](int acc, int tile, int j, const float* nl, f32x2 (&sum)[2]) {
-        const int first = tile * tile_rows, nr = min(tile_rows, im.rows - first);
-        // rows below `from` do not see key j
-        const int from = p.causal ? max(0, j - (im.L - im.n)) * p.G - first : 0;
-#pragma unroll 1
-        for (int c = 0; c < nr; c += 32) {
-          uint32_t z[32];
-          tmem_ld32(lane_base + acc * 128 + c, z);
-          tmem_wait_ld();
-          if (!__all_sync(0xffffffffu, from <= c) || c + 32 > nr) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e < from || c + e >= nr) z[e] = 0xff800000u;  // -inf
-          }
-          add_weights(z, nl + c, scale2, sum);
+      const int end = im.tile0 + im.tiles;  // the last row tile sees every key
+      float next = lse_of(im.tile0);
+      bool left = false;
+      for (int tile = im.tile0; tile < end; ++tile) {
+        const int ny = tiles_seen(p, im, tile);
+        float* nl = nlse + (n_nl++ & 1) * kTile;
+        nl[t] = next;
+        // everyone's entry is written; the buffer's last readers passed the row tile before
+        if (barrier_any(1 + wg, 128, pending)) {
+          left = true;
+          break;
         }
-      };
-      auto store = [&](int j, float paid, float old) {
-        if (j < im.L) p.out[at0 + j] = j < im.L - im.n && p.decay != 0.f ? fmaf(p.decay, old, paid) : paid;
-      };
-      auto old_of = [&](int j) { return j < im.L - im.n && p.decay != 0.f ? p.scores[at0 + j] : 0.f; };
-      if (im.type == kColsK) {
-        nlse[t] = lse_of(im.x);
-        if (barrier_any(1 + wg, 128, false)) break;
-        for (int i = 0; i < im.ny; ++i, ++g) {
+        if (tile + 1 < end) next = lse_of(tile + 1);
+        const int first = tile * tile_rows, nr = min(tile_rows, im.rows - first);
+        for (int i = 0; i < ny; ++i, ++g) {
           if ((i & 1) != wg || pending) continue;
-          const int acc = g % kAccs, j = im.y0 + i * kTile + t;
-          const float old = old_of(j);
+          const int acc = g % kAccs, j = im.key0 + i * kTile + t;
+          const bool keeps = tile + 1 == end && j < im.L;  // this key's sum is complete: store it
+          const bool adds = keeps && j < im.L - im.n && p.decay != 0.f;
+          const float old = adds ? p.scores[at0 + j] : 0.f;
           pending = !wait_all(&bars->acc_full[acc], (g / kAccs) & 1, wc);
           if (pending) continue;
           tc_fence_after();
+          // rows below `from` do not see key j
+          const int from = p.causal ? max(0, j - (im.L - im.n)) * p.G - first : 0;
           f32x2 sum[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
-          weigh(acc, im.x, j, nlse, sum);
+#pragma unroll 1
+          for (int c = 0; c < nr; c += 32) {
+            uint32_t z[32];
+            tmem_ld32(lane_base + acc * 128 + c, z);
+            tmem_wait_ld();
+            if (!__all_sync(0xffffffffu, from <= c) || c + 32 > nr) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e < from || c + e >= nr) z[e] = 0xff800000u;  // -inf
+            }
+            add_weights(z, nl + c, scale2, sum);
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->acc_empty[acc]);
           const float2 r = up2(add2(sum[0], sum[1]));
-          store(j, r.x + r.y, old);
+          float paid = r.x + r.y;
+          if (tile > im.tile0) paid += sums[i * kTile];  // this thread's own entry
+          if (tile + 1 < end)
+            sums[i * kTile] = paid;
+          else if (keeps)
+            p.out[at0 + j] = adds ? fmaf(p.decay, old, paid) : paid;
         }
-        // nlse is rewritten only after the next item's agreement
-      } else {
-        const int j = im.x + t;
-        const float old = wg == 0 ? old_of(j) : 0.f;
-        f32x2 sum[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
-        float next = wg < im.ny ? lse_of(im.y0 + wg) : 0.f;
-        bool left = false;
-        for (int i = 0; i < im.ny; ++i, ++g) {
-          if ((i & 1) != wg) continue;
-          const int acc = g % kAccs;
-          float* nl = nlse + ((i >> 1) & 1) * kTile;
-          nl[t] = next;
-          // everyone's entry is written; the buffer's last readers passed the tile before
-          if (barrier_any(1 + wg, 128, pending)) {
-            left = true;
-            break;
-          }
-          next = i + 2 < im.ny ? lse_of(im.y0 + i + 2) : 0.f;
-          pending = !wait_all(&bars->acc_full[acc], (g / kAccs) & 1, wc);
-          if (pending) continue;
-          tc_fence_after();
-          weigh(acc, im.y0 + i, j, nl, sum);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->acc_empty[acc]);
-        }
-        if (left) break;
-        const float2 r = up2(add2(sum[0], sum[1]));
-        // the second group hands its sums to the first
-        if (wg == 1) {
-          if (!pending) pending = !wait_all(&bars->xch_empty, (n_xch & 1) ^ 1, wc);
-          if (!pending) {
-            xch[t] = r.x + r.y;
-            mbar_arrive(&bars->xch_full);
-          }
-        } else {
-          if (!pending) pending = !wait_all(&bars->xch_full, n_xch & 1, wc);
-          if (!pending) {
-            const float other = xch[t];
-            mbar_arrive(&bars->xch_empty);
-            store(j, (r.x + r.y) + other, old);
-          }
-        }
-        ++n_xch;
+        // K tiles that this row tile does not see start at the next one that does
+        if (tile + 1 < end)
+          for (int i = ny; i < kRangeTiles; ++i)
+            if ((i & 1) == wg && tile == im.tile0) sums[i * kTile] = 0.f;
       }
+      if (left) break;
+      if (!pending) mbar_arrive(&bars->item_closed[sl]);
     }
   }
 

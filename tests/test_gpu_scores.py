@@ -195,7 +195,8 @@ def test_invalid_metadata():
                      (dict(context_lens=i32([100, 60, 81 * 16, 50])), [0, 1, 3]),    # past its table
                      (dict(context_lens=i32([100, 60, -4, 50])), [0, 1, 3]),
                      (dict(query_start_loc=i32([0, 1, 3, 4, 9])), [0, 1, 2]),        # past q
-                     (dict(query_start_loc=i32([0, 4, 0, 4, 5])), [3])):             # overlapping queries
+                     (dict(query_start_loc=i32([0, 4, 0, 4, 5])), [3]),              # overlapping queries
+                     (dict(query_start_loc=i32([0, 4, 0, 4, 5]), max_query_len=4), [3])):
         before = b.old.clone()
         if kw.get("query_start_loc") is not None and len(good) == 1:
             got = b.run(out=b.old.clone(), **kw)
@@ -222,6 +223,34 @@ def test_invalid_metadata():
         b.check(b.run(out=b.old.clone(), block_tables=torch.from_numpy(t).cuda()), before)
         assert pkv.device_errors() == pkv.DEVERR["block_out_of_range"]
         b.K, b.tables = keep, held
+
+
+def test_broken_query_length_promise():
+    """A sequence with more queries than max_query_len is flagged and left
+    out; the others get their scores."""
+    b = Batch(45, [300, 200, 90], [1, 30, 2], 8, 2, 128, 16)
+    for most, good in ((1, [0]), (2, [0, 2]), (29, [0, 2]), (30, [0, 1, 2]), (0, [0, 1, 2])):
+        before = b.old.clone()
+        b.check(b.run(out=b.old.clone(), max_query_len=most), before, seqs=good)
+        assert pkv.device_errors() == (0 if len(good) == 3 else pkv.DEVERR["bad_sequence"])
+
+
+@pytest.mark.parametrize("count", [31, 33, 64, 255, 256, 257, 700])
+def test_many_sequences(count):
+    """Plans of one, two and more sequences a thread, and past what shared
+    memory holds; every seventh sequence has no queries, one is invalid."""
+    rng = np.random.default_rng(count)
+    lens = rng.integers(1, 60, count).tolist()
+    q = [0 if s % 7 == 3 else 1 for s in range(count)]
+    b = Batch(count, lens, q, 4, 2, 64, 8)
+    bad = count // 2
+    ctx = b.args["context_lens"].clone()
+    ctx[bad] = 61 * 8
+    for hint in (0, 1):
+        before = b.old.clone()
+        good = [s for s in range(count) if s != bad or q[s] == 0]
+        b.check(b.run(out=b.old.clone(), max_query_len=hint, context_lens=ctx), before, seqs=good)
+        assert pkv.device_errors() == pkv.DEVERR["bad_sequence"]
 
 
 def test_nan_in_masked_places():
