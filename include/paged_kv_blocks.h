@@ -118,6 +118,30 @@ pkv_status pkv_bm_free(pkv_block_manager* bm, int64_t seq_id);
 pkv_status pkv_bm_fork(pkv_block_manager* bm, int64_t parent_seq_id, int64_t child_seq_id);
 
 /*
+ * pkv_bm_compact - shorten sequences to their first num_tokens tokens' worth of
+ * cache, as paged_kv_compact (paged_kv_budget.h) rewrites it: sequence i of
+ * the batch keeps min(its length, num_tokens[i]) tokens, all or nothing.
+ *   seq_ids           int64 [num_seqs], distinct, known
+ *   num_tokens        int32 [num_seqs], >= 0
+ *   block_tables      int32 [num_seqs, max_blocks_per_seq]: the tables before
+ *   dst_block_tables  the same: the tables after, -1 past each one's end
+ *   context_lens      int32 [num_seqs]: the lengths after
+ * A sequence that is not shortened keeps its table.  In a shortened one's
+ * table every block that another table names or the prefix cache holds is
+ * replaced by a new block (its rows are about to change), the others stay;
+ * the blocks past the new length are given back, like the replaced ones,
+ * after every new block of the call has been taken: no block written by
+ * paged_kv_compact on these tables is read by another sequence of the call.
+ * The device copy must run before later steps write the blocks given back
+ * (the same stream will do).
+ * A shortened sequence's cache no longer holds its tokens in order, so
+ * pkv_bm_add_prefix refuses it and its forks from then on.
+ */
+pkv_status pkv_bm_compact(pkv_block_manager* bm, const int64_t* seq_ids, const int32_t* num_tokens,
+                          int32_t num_seqs, int32_t* block_tables, int32_t* dst_block_tables,
+                          int32_t* context_lens);
+
+/*
  * pkv_bm_add_prefix - make the full blocks of seq_id findable by
  * pkv_bm_try_get_prefix_blocks ("ADR 004", Limitations: add_prefix).
  *   token_ids  host int64 [num_tokens]: all of the sequence's tokens

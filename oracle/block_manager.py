@@ -58,6 +58,13 @@ B9  add_prefix(seq, tokens), tokens = all of the sequence's tokens: walks its
     that entry (even on another physical block, which then stays
     unregistered); an unregistered block gets a new entry; a block cached
     under a key that no longer chains from the root is re-keyed.
+B10 compact(seq_ids, n_tokens) shortens each sequence to its first
+    min(length, n_tokens) tokens' worth of blocks, all or nothing.  In a
+    shortened table, every block that was named more than once before the
+    call, or is cached, is replaced by a new one; all new blocks are taken,
+    members in order, before anything is given back; then, member by member,
+    the replaced blocks and those past the end are released from the last to
+    the first.  A shortened sequence and its forks take no more add_prefix.
 """
 from __future__ import annotations
 
@@ -83,6 +90,7 @@ class BlockManagerModel:
         self.ref = [0] * num_blocks                             # B2
         self.tables: dict[int, list[int]] = {}
         self.lens: dict[int, int] = {}
+        self.compacted: set[int] = set()                        # B10
         self.entries: dict[tuple, tuple[int, int]] = {}         # key -> (entry id, block)  B3
         self.entry_of_block: dict[int, tuple[tuple, int]] = {}  # block -> (key, entry id)
         self.idle: list[int] = []                               # cached blocks with count 0, oldest first
@@ -181,6 +189,7 @@ class BlockManagerModel:
         """B6: release from the last block to the first; forget the sequence."""
         table = self.tables.pop(seq)
         del self.lens[seq]
+        self.compacted.discard(seq)
         for b in reversed(table):
             self._release(b)
 
@@ -191,13 +200,51 @@ class BlockManagerModel:
         table = self.tables[parent]
         self.tables[child] = list(table)
         self.lens[child] = self.lens[parent]
+        if parent in self.compacted:
+            self.compacted.add(child)
         for b in table:
             self.ref[b] += 1
+
+    def compact(self, seq_ids, n_tokens):
+        """B10: the tables before and after, and the lengths after."""
+        if len(set(seq_ids)) != len(seq_ids):
+            raise ValueError("a sequence twice in one call")
+        if any(n < 0 for n in n_tokens):
+            raise ValueError("negative length")
+        B = len(seq_ids)
+        src = np.full((B, self.max_blocks), -1, dtype=np.int32)
+        dst = src.copy()
+        lens = np.zeros(B, dtype=np.int32)
+
+        def run():
+            held = {b for b in range(self.num_blocks) if self.ref[b] > 1 or b in self.entry_of_block}
+            after = []
+            for i, (s, n) in enumerate(zip(seq_ids, n_tokens)):
+                table, L = self.tables[s], self.lens[s]
+                src[i, :len(table)] = table
+                lens[i] = min(L, n)
+                keep = table[:self._blocks_for(int(lens[i]))]
+                after.append([self._take() if n < L and b in held else b for b in keep])
+                dst[i, :len(keep)] = after[-1]
+            for i, (s, n) in enumerate(zip(seq_ids, n_tokens)):
+                if n >= self.lens[s]:
+                    continue
+                for j in reversed(range(len(self.tables[s]))):
+                    if j >= len(after[i]) or after[i][j] != self.tables[s][j]:
+                        self._release(self.tables[s][j])
+                self.tables[s] = after[i]
+                self.lens[s] = int(lens[i])
+                self.compacted.add(s)
+            return src, dst, lens
+
+        return self._atomic(run)
 
     # -- prefix cache ----------------------------------------------------
     def add_prefix(self, seq: int, tokens) -> None:
         """B9: cache the sequence's full blocks under their token prefix."""
         tokens = [int(t) for t in tokens]
+        if seq in self.compacted:
+            raise ValueError("compacted sequence")
         if len(tokens) != self.lens[seq]:
             raise ValueError("tokens must be all of the sequence's tokens")
         table, bs, parent = self.tables[seq], self.block_size, 0
@@ -234,6 +281,7 @@ class BlockManagerModel:
                 self.idle.remove(b)
             self.ref[b] += 1
         self.tables[seq] = hits
+        self.compacted.discard(seq)
         self.lens[seq] = len(hits) * bs
         return len(hits) * bs
 

@@ -131,6 +131,7 @@ def lib() -> ctypes.CDLL:
                     ("pkv_bm_step", [c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_p32]),
                     ("pkv_bm_free", [c_vp, c_i64]),
                     ("pkv_bm_fork", [c_vp, c_i64, c_i64]),
+                    ("pkv_bm_compact", [c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp]),
                     ("pkv_bm_add_prefix", [c_vp, c_i64, c_vp, c_i32]),
                     ("pkv_bm_try_get_prefix_blocks", [c_vp, c_i64, c_vp, c_i32, c_p32]),
                     ("pkv_bm_block_table", [c_vp, c_i64, c_vp, c_p32, c_p32]),
@@ -375,8 +376,8 @@ class BlockManager:
     ``update(seq, n)`` -> (slots int64 [n], copies int32 [c, 2]);
     ``step(seq_ids, n_new)`` -> dict of the call metadata (host numpy
     arrays: slot_mapping, block_tables, context_lens, query_start_loc,
-    copies); ``free``, ``fork``, ``add_prefix``, ``try_get_prefix_blocks``,
-    ``block_table``, ``stats``.  Refused requests raise ``OutOfBlocks`` or
+    copies); ``compact``, ``free``, ``fork``, ``add_prefix``,
+    ``try_get_prefix_blocks``, ``block_table``, ``stats``.  Refused requests raise ``OutOfBlocks`` or
     ``LibraryError`` and change nothing.
     """
 
@@ -464,6 +465,25 @@ class BlockManager:
 
     def fork(self, parent: int, child: int) -> None:
         _check(lib().pkv_bm_fork(self._h, int(parent), int(child)))
+
+    def compact(self, seq_ids, num_tokens) -> dict:
+        """Shorten sequences to at most ``num_tokens`` (an int, or one for
+        each), as ``paged_kv_compact`` rewrites their caches: host arrays
+        ``block_tables`` and ``dst_block_tables`` (before and after, its two
+        tables) and ``context_lens`` (after).  Blocks past the new lengths are
+        given back; shared or cached blocks are replaced by new ones."""
+        ids = _host(seq_ids, np.int64)
+        B = len(ids)
+        n = np.full(B, num_tokens, dtype=np.int32) if np.ndim(num_tokens) == 0 else _host(num_tokens, np.int32)
+        if len(n) != B:
+            raise ValueError("seq_ids and num_tokens differ in length")
+        out = {"block_tables": np.empty((B, self.max_blocks), dtype=np.int32),
+               "dst_block_tables": np.empty((B, self.max_blocks), dtype=np.int32),
+               "context_lens": np.empty(B, dtype=np.int32)}
+        ptr = lambda a: a.ctypes.data if a.size else None
+        _check(lib().pkv_bm_compact(self._h, ptr(ids), ptr(n), B, ptr(out["block_tables"]),
+                                    ptr(out["dst_block_tables"]), ptr(out["context_lens"])))
+        return out
 
     def add_prefix(self, seq: int, tokens) -> None:
         t = _host(tokens, np.int64)

@@ -46,6 +46,7 @@ struct KeyHash {
 struct Seq {
   std::vector<int32_t> table;
   int64_t len = 0;
+  bool compacted = false;  // its cache no longer holds its tokens in order
 };
 
 struct CacheEntry {
@@ -283,6 +284,66 @@ pkv_status pkv_bm_step(pkv_block_manager* bm, const int64_t* seq_ids, const int3
   return PKV_OK;
 }
 
+pkv_status pkv_bm_compact(pkv_block_manager* bm, const int64_t* seq_ids, const int32_t* num_tokens, int32_t num_seqs,
+                          int32_t* block_tables, int32_t* dst_block_tables, int32_t* context_lens) {
+  pkv::set_last_error("");
+  if (!bm || num_seqs < 0) return fail(PKV_ERR_INVALID_ARG, "null pointer or num_seqs < 0");
+  if (num_seqs == 0) return PKV_OK;
+  if (!seq_ids || !num_tokens || !block_tables || !dst_block_tables || !context_lens)
+    return fail(PKV_ERR_INVALID_ARG, "null pointer");
+  std::vector<int64_t>& ids = bm->ids_scratch_;
+  ids.assign(seq_ids, seq_ids + num_seqs);
+  std::sort(ids.begin(), ids.end());
+  const auto dup = std::adjacent_find(ids.begin(), ids.end());
+  if (dup != ids.end()) return fail(PKV_ERR_INVALID_ARG, "sequence %lld twice in one call", (long long)*dup);
+  // Blocks that a shortened table may not keep: named more than once, or
+  // cached.  The counts are those before the call, so that of several members
+  // sharing a block none keeps it.
+  auto moves = [&](int32_t b) { return bm->ref_[b] > 1 || bm->block_entry_[b] != 0; };
+  int64_t need = 0;
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    auto it = bm->seqs_.find(seq_ids[i]);
+    if (it == bm->seqs_.end()) return fail(PKV_ERR_INVALID_ARG, "unknown sequence %lld", (long long)seq_ids[i]);
+    if (num_tokens[i] < 0) return fail(PKV_ERR_INVALID_ARG, "num_tokens[%lld] < 0", i);
+    const Seq& s = it->second;
+    if (num_tokens[i] >= s.len) continue;
+    for (int64_t j = 0; j < bm->blocks_for(num_tokens[i]); ++j) need += moves(s.table[j]);
+  }
+  if (need > bm->available())
+    return fail(PKV_ERR_OUT_OF_BLOCKS, "compaction needs %lld blocks, %lld free or evictable", need, bm->available());
+  // The tables after (the counts stay as they were until all are made), then
+  // the new blocks in their places, then what is given back.
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    const Seq& s = bm->seqs_[seq_ids[i]];
+    int32_t* src = block_tables + (int64_t)i * bm->max_blocks;
+    int32_t* dst = dst_block_tables + (int64_t)i * bm->max_blocks;
+    const int64_t len = std::min<int64_t>(s.len, num_tokens[i]);
+    for (int32_t j = 0; j < bm->max_blocks; ++j) {
+      src[j] = j < (int32_t)s.table.size() ? s.table[j] : -1;
+      dst[j] = j < bm->blocks_for(len) ? s.table[j] : -1;
+      if (dst[j] >= 0 && len < s.len && moves(dst[j])) dst[j] = -2;
+    }
+    context_lens[i] = (int32_t)len;
+  }
+  for (int32_t i = 0; i < num_seqs; ++i)
+    for (int32_t j = 0; j < bm->max_blocks; ++j) {
+      int32_t& b = dst_block_tables[(int64_t)i * bm->max_blocks + j];
+      if (b == -2) b = bm->take();
+    }
+  for (int32_t i = 0; i < num_seqs; ++i) {
+    Seq& s = bm->seqs_[seq_ids[i]];
+    if (context_lens[i] >= s.len) continue;
+    const int32_t* dst = dst_block_tables + (int64_t)i * bm->max_blocks;
+    const int32_t kept = (int32_t)bm->blocks_for(context_lens[i]);
+    for (int32_t j = (int32_t)s.table.size() - 1; j >= 0; --j)  // from the last to the first, as free does
+      if (j >= kept || dst[j] != s.table[j]) bm->release(s.table[j]);
+    s.table.assign(dst, dst + kept);
+    s.len = context_lens[i];
+    s.compacted = true;
+  }
+  return PKV_OK;
+}
+
 pkv_status pkv_bm_free(pkv_block_manager* bm, int64_t seq_id) {
   pkv::set_last_error("");
   if (!bm) return fail(PKV_ERR_INVALID_ARG, "null handle");
@@ -312,6 +373,9 @@ pkv_status pkv_bm_add_prefix(pkv_block_manager* bm, int64_t seq_id, const int64_
   auto it = bm->seqs_.find(seq_id);
   if (it == bm->seqs_.end()) return fail(PKV_ERR_INVALID_ARG, "unknown sequence %lld", (long long)seq_id);
   const Seq& s = it->second;
+  if (s.compacted)
+    return fail(PKV_ERR_INVALID_ARG, "sequence %lld was compacted: its cache does not hold its tokens in order",
+                (long long)seq_id);
   if (num_tokens != s.len)
     return fail(PKV_ERR_INVALID_ARG, "%lld tokens given, the sequence has %lld", num_tokens, s.len);
   if (num_tokens > 0 && !token_ids) return fail(PKV_ERR_INVALID_ARG, "null token_ids");
@@ -359,6 +423,7 @@ pkv_status pkv_bm_try_get_prefix_blocks(pkv_block_manager* bm, int64_t seq_id, c
   }
   for (int32_t b : hits) bm->acquire(b);
   Seq& s = bm->seqs_[seq_id];
+  s.compacted = false;
   s.table = std::move(hits);
   s.len = (int64_t)s.table.size() * bm->bs;
   *num_cached_tokens = (int32_t)s.len;

@@ -60,10 +60,11 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
 
 constexpr int kPlanThreads = 1024;
 
-// Keys of a few-row stats unit: longer for long sequences (fewer partials),
-// whose block ids a warp's lanes hold.
+// Keys of a few-row stats unit: the launch's (few units: short ones, so that
+// they spread over the SMs), longer for long sequences (fewer partials), whose
+// block ids a warp's lanes hold.
 __device__ __forceinline__ int few_chunk(const ScoreParams& p, int L) {
-  return L <= 32768 ? kFewChunk : min(512, 32 * p.bs);
+  return L <= 32768 ? p.few_chunk : min(512, 32 * p.bs);
 }
 
 // Whether sequence s, of queries a .. b - 1 and L tokens, is left out as
@@ -395,6 +396,7 @@ struct DotBf16 {
   template <int NT>
   struct Q {
     uint4 w[NT][kPieces];
+    int rows;
   };
   template <int NT>
   __device__ static void load_q(Q<NT>& q, int nt, const void* row, int t) {
@@ -427,6 +429,7 @@ struct DotFp8 {
   template <int NT>
   struct Q {
     uint32_t w[NT][16];
+    int rows;
   };
   template <int NT>
   __device__ static void load_q(Q<NT>& q, int nt, const void* row, int t) {
@@ -470,7 +473,7 @@ struct DotF32 {
   template <int NT>
   struct Q {
     const float* row[NT];  // this lane's row g of each tile, exchanged by shuffles
-    int t;
+    int t, rows;           // rows of the head
   };
   template <int NT>
   __device__ static void load_q(Q<NT>& q, int nt, const void* row, int t) {
@@ -481,32 +484,35 @@ struct DotF32 {
   __device__ static void dot(float (&acc)[NT][4], const uint4 (&k0)[kPieces], const uint4 (&k1)[kPieces], const Q<NT>& q) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
+#pragma unroll 2
+      for (int r = 0; r < min(8, q.rows - nt * 8); ++r) {
         const float* row = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(q.row[nt]), r * 4));
         float x0 = 0.f, x1 = 0.f;
-        if (row) {
 #pragma unroll
-          for (int c = 0; c < kPieces; ++c) {
-            const float4 w = __ldg(reinterpret_cast<const float4*>(row + 16 * c + 4 * q.t));
-            x0 = fmaf(__uint_as_float(k0[c].x), w.x, x0);
-            x1 = fmaf(__uint_as_float(k1[c].x), w.x, x1);
-            x0 = fmaf(__uint_as_float(k0[c].y), w.y, x0);
-            x1 = fmaf(__uint_as_float(k1[c].y), w.y, x1);
-            x0 = fmaf(__uint_as_float(k0[c].z), w.z, x0);
-            x1 = fmaf(__uint_as_float(k1[c].z), w.z, x1);
-            x0 = fmaf(__uint_as_float(k0[c].w), w.w, x0);
-            x1 = fmaf(__uint_as_float(k1[c].w), w.w, x1);
-          }
-          x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
-          x1 += __shfl_xor_sync(0xffffffffu, x1, 1);
-          x0 += __shfl_xor_sync(0xffffffffu, x0, 2);
-          x1 += __shfl_xor_sync(0xffffffffu, x1, 2);
+        for (int c = 0; c < kPieces; ++c) {
+          const float4 w = __ldg(reinterpret_cast<const float4*>(row + 16 * c + 4 * q.t));
+          x0 = fmaf(__uint_as_float(k0[c].x), w.x, x0);
+          x1 = fmaf(__uint_as_float(k1[c].x), w.x, x1);
+          x0 = fmaf(__uint_as_float(k0[c].y), w.y, x0);
+          x1 = fmaf(__uint_as_float(k1[c].y), w.y, x1);
+          x0 = fmaf(__uint_as_float(k0[c].z), w.z, x0);
+          x1 = fmaf(__uint_as_float(k1[c].z), w.z, x1);
+          x0 = fmaf(__uint_as_float(k0[c].w), w.w, x0);
+          x1 = fmaf(__uint_as_float(k1[c].w), w.w, x1);
         }
+        x0 += __shfl_xor_sync(0xffffffffu, x0, 1);
+        x1 += __shfl_xor_sync(0xffffffffu, x1, 1);
+        x0 += __shfl_xor_sync(0xffffffffu, x0, 2);
+        x1 += __shfl_xor_sync(0xffffffffu, x1, 2);
         if ((r >> 1) == q.t) {
-          acc[nt][r & 1] = x0;
-          acc[nt][2 + (r & 1)] = x1;
+          if (r & 1) {
+            acc[nt][1] = x0;
+            acc[nt][3] = x1;
+          } else {
+            acc[nt][0] = x0;
+            acc[nt][2] = x1;
+          }
         }
       }
   }
@@ -531,25 +537,27 @@ __device__ __forceinline__ void fetch_tile(const ScoreParams& p, const Unit& u, 
   const uint32_t dst = tile + row0 * Dot::kRowBytes;
   const uint32_t even = (uint32_t)piece << 4, odd = (uint32_t)(piece ^ 4) << 4;
   const uint32_t mine = kRows == 1 ? even : row0 & 1 ? odd : even;
+  const int b0 = __shfl_sync(0xffffffffu, u.blk, ((j - u.kb) >> p.bs_log) & 31);
+  const int b1 = __shfl_sync(0xffffffffu, u.blk, ((j + 8 - u.kb) >> p.bs_log) & 31);
+  const uint8_t* base = static_cast<const uint8_t*>(p.kc) + lane_src;
+  // 8 keys lie in one block
+  const uint8_t* src0 = base + (((int64_t)b0 << p.bs_log) + (j & (p.bs - 1))) * token_bytes;
+  const uint8_t* src1 = base + (((int64_t)b1 << p.bs_log) + ((j + 8) & (p.bs - 1))) * token_bytes;
+  if (b0 >= 0 && b1 >= 0 && j + 16 <= u.ke) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {  // 8 keys lie in one block
-    const int j8 = j + 8 * half;
-    const int b = __shfl_sync(0xffffffffu, u.blk, ((j8 - u.kb) >> p.bs_log) & 31);
-    const uint8_t* src = static_cast<const uint8_t*>(p.kc) + lane_src +
-                         (((int64_t)b << p.bs_log) + (j8 & (p.bs - 1))) * token_bytes;
-    if (b >= 0 && j8 + 8 <= u.ke) {
-#pragma unroll
-      for (int i = 0; i < 8; i += kRows) {
-        copy16(dst + (half * 8 + i) * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), src);
-        src += kRows * token_bytes;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; i += kRows) {
-        const bool ok = b >= 0 && j8 + i + row0 < u.ke;
-        copy16(dst + (half * 8 + i) * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), ok ? src : p.kc, ok);
-        src += kRows * token_bytes;
-      }
+    for (int i = 0; i < 8; i += kRows) {
+      copy16(dst + i * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), src0);
+      copy16(dst + (8 + i) * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), src1);
+      src0 += kRows * token_bytes;
+      src1 += kRows * token_bytes;
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 16; i += kRows) {
+      const int k = i & 7;
+      const bool ok = (i < 8 ? b0 : b1) >= 0 && j + i + row0 < u.ke;
+      const uint8_t* src = (i < 8 ? src0 : src1) + k * token_bytes;
+      copy16(dst + i * Dot::kRowBytes + (kRows == 1 && (i & 1) ? odd : mine), ok ? src : p.kc, ok);
     }
   }
 }
@@ -564,6 +572,7 @@ struct Stats {
   __device__ __forceinline__ void begin(const ScoreParams& p, const SeqPlan& sp, const Unit& u, int lane) {
     const int g = lane >> 2, t = lane & 3;
     const int qstart = __ldg(p.qsl + u.s);
+    q.rows = sp.rows;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = nt * 8 + g, i = r / p.G;
@@ -582,8 +591,7 @@ struct Stats {
 
   // The 16 keys at j, in `tile`; z: where the lane keeps its logits of key
   // j + g (null: its rows are past the padding), those of j + g + 8 follow at
-  // z8.  kAll: every row sees all 16 keys.
-  template <bool kAll>
+  // z8.
   __device__ __forceinline__ void use(const ScoreParams& p, int j, int ke, const uint8_t* tile, float* z, int z8, int lane) {
     const int g = lane >> 2, t = lane & 3;
     uint4 k0[Dot::kPieces], k1[Dot::kPieces];
@@ -607,18 +615,16 @@ struct Stats {
       for (int e = 0; e < 2; ++e) {
         za[e] = acc[nt][e] * p.scale_log2;
         zb[e] = acc[nt][2 + e] * p.scale_log2;
-        if (!kAll) {
-          if (ja >= vis[nt][e]) za[e] = -CUDART_INF_F;
-          if (jb >= vis[nt][e]) zb[e] = -CUDART_INF_F;
-        }
+        if (ja >= vis[nt][e]) za[e] = -CUDART_INF_F;
+        if (jb >= vis[nt][e]) zb[e] = -CUDART_INF_F;
         const float mn = fmax3(m[nt][e], za[e], zb[e]);
-        const float mu = !kAll && mn == -CUDART_INF_F ? 0.f : mn;
+        const float mu = mn == -CUDART_INF_F ? 0.f : mn;
         l[nt][e] = fmaf(l[nt][e], fast_exp2(m[nt][e] - mu), fast_exp2(za[e] - mu) + fast_exp2(zb[e] - mu));
         m[nt][e] = mn;
       }
       if (z && (NT == 1 || z8 >= 128 || nt == 0)) {  // 16 padded rows: 8 more at z + 8
-        if (kAll || ja < ke) *reinterpret_cast<float2*>(z + nt * 8) = make_float2(za[0], za[1]);
-        if (kAll || jb < ke) *reinterpret_cast<float2*>(z + z8 + nt * 8) = make_float2(zb[0], zb[1]);
+        if (ja < ke) *reinterpret_cast<float2*>(z + nt * 8) = make_float2(za[0], za[1]);
+        if (jb < ke) *reinterpret_cast<float2*>(z + z8 + nt * 8) = make_float2(zb[0], zb[1]);
       }
     }
   }
@@ -716,64 +722,63 @@ __global__ void __launch_bounds__(kFewThreads, Dot::kBlocks) few_kernel(const Sc
   constexpr int kChunks = Dot::kRowBytes / 16;
   const int64_t token_bytes = (int64_t)p.Hkv * Dot::kRowBytes;
   const int64_t lane_src = (lane / kChunks) * token_bytes + (lane % kChunks) * 16;
-  auto fetch = [&](const Unit& u) {
+  // issue a tile of `now`, or then of `after`, if there is one and room for it
+  auto issue = [&](bool may_go_on) {
+    if (ahead_by == kStages) return false;
+    if (!ahead && at >= now.ke) {
+      if (!may_go_on) return false;
+      ahead = true;
+      at = after.kb;
+    }
+    if (ahead && at >= after.ke) return false;
+    Unit u = now;
+    if (ahead) u = after;
     fetch_tile<Dot>(p, u, at, ring_u32 + put * kTileBytes, lane_src + u.h * Dot::kRowBytes, token_bytes, lane);
     copy_commit();
     put = put + 1 == kStages ? 0 : put + 1;
     ++ahead_by;
     at += 16;
-  };
-  // issue a tile of `now`, or then of `after`, if there is one and room for it
-  auto issue = [&](bool may_go_on) {
-    if (ahead_by == kStages) return false;
-    if (!ahead) {
-      if (at < now.ke) {
-        fetch(now);
-        return true;
-      }
-      if (!may_go_on) return false;
-      ahead = true;
-      at = after.kb;
-    }
-    if (at >= after.ke) return false;
-    fetch(after);
     return true;
   };
+  // One loop with each step in one place: units are short, and what runs once
+  // a unit is bound by the fetch of its instructions.
+  Stats<Dot, NT> st;
+  SeqPlan sp{};
+  float* z = nullptr;
+  int j = 0;
+  bool fresh = true;  // `now` has not been begun
   while (now.s >= 0) {
-    while (issue(false)) {
+    while (issue(!fresh)) {
     }
-    after = look_up();  // while the tiles come
-    const SeqPlan sp = plan[now.s];
-    Stats<Dot, NT> st;
-    st.begin(p, sp, now, lane);
-    const int g = lane >> 2, t2 = 2 * (lane & 3);
-    float* z = t2 < sp.pad ? p.logit + sp.logit + ((int64_t)now.h * sp.L + now.kb + g) * sp.pad + t2 : nullptr;
-    const int seen = p.causal ? sp.L - sp.n + 1 : sp.L;  // keys that every row sees
-#pragma unroll 1
-    for (int j = now.kb; j < now.ke; j += 16) {
-      while (issue(true)) {
-      }
-      if (ahead_by == kStages)
-        copy_wait<kStages - 1>();
-      else
-        copy_wait<0>();
-      __syncwarp();  // every lane's copies of the tile have landed
-      const uint8_t* tile = ring + get * kTileBytes;
-      if (j + 16 <= seen)
-        st.template use<true>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
-      else
-        st.template use<false>(p, j, now.ke, tile, z, 8 * sp.pad, lane);
-      __syncwarp();  // the tile may be overwritten
-      get = get + 1 == kStages ? 0 : get + 1;
-      --ahead_by;
-      if (z) z += 16 * sp.pad;
+    if (fresh) {
+      after = look_up();  // while the tiles come
+      sp = plan[now.s];
+      st.begin(p, sp, now, lane);
+      const int g = lane >> 2, t2 = 2 * (lane & 3);
+      z = t2 < sp.pad ? p.logit + sp.logit + ((int64_t)now.h * sp.L + now.kb + g) * sp.pad + t2 : nullptr;
+      j = now.kb;
+      fresh = false;
+      continue;
     }
-    while (issue(true)) {
+    if (j >= now.ke) {
+      st.end(p, sp, now, lane);
+      if (!ahead) at = after.kb;
+      ahead = false;  // what was issued of `after` is now `now`'s
+      now = after;
+      fresh = true;
+      continue;
     }
-    st.end(p, sp, now, lane);
-    if (!ahead) at = after.kb;
-    ahead = false;  // what was issued of `after` is now `now`'s
-    now = after;
+    if (ahead_by == kStages)
+      copy_wait<kStages - 1>();
+    else
+      copy_wait<0>();
+    __syncwarp();  // every lane's copies of the tile have landed
+    st.use(p, j, now.ke, ring + get * kTileBytes, z, 8 * sp.pad, lane);
+    __syncwarp();  // the tile may be overwritten
+    get = get + 1 == kStages ? 0 : get + 1;
+    --ahead_by;
+    if (z) z += 16 * sp.pad;
+    j += 16;
   }
   copy_wait<0>();
 }
@@ -818,55 +823,57 @@ __device__ __forceinline__ void rows_lse(const float2* part, int chunks, int row
 }
 
 // Weights and scores of keys kb .. ke - 1 of a head from the kept logits, on a
-// warp, kAt keys a lane at a time; the first keys' logits and the rows'
-// partials are loaded together.
-template <int PAD>
-__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int kb, int ke, int lane) {
-  const float* z = p.logit + sp.logit + (int64_t)h * sp.L * PAD;
+// warp, kAt keys a lane at a time; lse: 16 floats of the warp's own.
+__device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan& sp, int h, int kb, int ke, float* lse,
+                                            int lane) {
+  constexpr int kAt = 4;
+  const int pad = sp.pad, quads = (pad + 3) / 4;
+  const float* z = p.logit + sp.logit + (int64_t)h * sp.L * pad;
   const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len;
-  constexpr int kAt = PAD <= 4 ? 8 : PAD == 8 ? 4 : 2;
-  float x[kAt][PAD], old[kAt];
-  auto load = [&](int j0) {
+  __syncwarp();  // the last head's lse have been read
+#pragma unroll 1
+  for (int r0 = 0; r0 < pad; r0 += 4) {
+    float x[4];
+    rows_lse(p.part + sp.part + (int64_t)h * sp.rows * sp.chunks, sp.chunks, sp.rows, r0, lane, x);
+    if (lane < 4) lse[r0 + lane] = lane == 0 ? x[0] : lane == 1 ? x[1] : lane == 2 ? x[2] : x[3];
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int j0 = kb + lane; j0 - lane < ke; j0 += kAt * 32) {
+    float paid[kAt], old[kAt];
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
       const int j = j0 + i * 32;
       old[i] = j < ke && j < sp.L - sp.n && p.decay != 0.f ? p.scores[at + j] : 0.f;
-      if (j >= ke) continue;
-      if constexpr (PAD == 2) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(z + (int64_t)j * 2));
-        x[i][0] = v.x;
-        x[i][1] = v.y;
-      } else {
+      paid[i] = 0.f;
+    }
+#pragma unroll 1
+    for (int k = 0; k < quads; ++k) {
+      const float4 l = *reinterpret_cast<const float4*>(lse + 4 * k);
+      float4 x[kAt];
 #pragma unroll
-        for (int k = 0; k < PAD / 4; ++k) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(z + (int64_t)j * PAD) + k);
-          x[i][4 * k] = v.x;
-          x[i][4 * k + 1] = v.y;
-          x[i][4 * k + 2] = v.z;
-          x[i][4 * k + 3] = v.w;
+      for (int i = 0; i < kAt; ++i) {
+        const int j = j0 + i * 32;
+        x[i] = make_float4(0.f, 0.f, -CUDART_INF_F, -CUDART_INF_F);
+        if (j < ke) {
+          if (pad == 2) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(z + (int64_t)j * 2));
+            x[i].x = v.x;
+            x[i].y = v.y;
+          } else {
+            x[i] = __ldcg(reinterpret_cast<const float4*>(z + (int64_t)j * pad) + k);
+          }
         }
       }
-    }
-  };
-  int j0 = kb + lane;
-  load(j0);
-  float lse[(PAD + 3) / 4][4];
 #pragma unroll
-  for (int g = 0; g < (PAD + 3) / 4; ++g)
-    rows_lse(p.part + sp.part + (int64_t)h * sp.rows * sp.chunks, sp.chunks, sp.rows, 4 * g, lane, lse[g]);
-  while (kb < ke) {
+      for (int i = 0; i < kAt; ++i)
+        paid[i] += (fast_exp2(x[i].x - l.x) + fast_exp2(x[i].y - l.y)) + (fast_exp2(x[i].z - l.z) + fast_exp2(x[i].w - l.w));
+    }
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
       const int j = j0 + i * 32;
-      if (j >= ke) continue;
-      float paid = 0.f;
-#pragma unroll
-      for (int r = 0; r < PAD; ++r) paid += fast_exp2(x[i][r] - lse[r / 4][r % 4]);
-      p.out[at + j] = j < sp.L - sp.n && p.decay != 0.f ? fmaf(p.decay, old[i], paid) : paid;
+      if (j < ke) p.out[at + j] = j < sp.L - sp.n && p.decay != 0.f ? fmaf(p.decay, old[i], paid[i]) : paid[i];
     }
-    kb += kAt * 32;
-    j0 += kAt * 32;
-    if (kb < ke) load(j0);
   }
 }
 
@@ -874,6 +881,7 @@ constexpr int kColBlocks = 4;  // of an SM
 
 __global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(const ScoreParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float lse[kColThreads / 32][kFewRows];
   const int lane = threadIdx.x & 31;
   pdl_wait();
   const Held held = hold_plan<false>(p, smem);
@@ -889,12 +897,7 @@ __global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(co
     const int h = w / per_head, c = w - h * per_head, count = (int)min(end - u, (int64_t)(per_head - c));
     const int kb = c * kColChunk, ke = min(sp.L, (c + count) * kColChunk);
     u += count;
-    switch (sp.pad) {
-      case 2: few_columns<2>(p, sp, h, kb, ke, lane); break;
-      case 4: few_columns<4>(p, sp, h, kb, ke, lane); break;
-      case 8: few_columns<8>(p, sp, h, kb, ke, lane); break;
-      default: few_columns<16>(p, sp, h, kb, ke, lane); break;
-    }
+    few_columns(p, sp, h, kb, ke, lse[threadIdx.x >> 5], lane);
   }
 }
 
@@ -1095,12 +1098,14 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   l.lse = at;
   at = align_up(at + (size_t)(T * Hq) * sizeof(float));
   l.part = at;
-  const int64_t chunk = std::min(kChunk, kFewChunk);
-  // the tensor-core kernel's two partials a range of 256 keys or more take at
-  // most one entry more than one a chunk of 128 does; a sequence's are rounded to pairs
-  at = align_up(at + ((size_t)(T * Hq) * (size_t)((keys + chunk - 1) / chunk + 1) + B) * sizeof(float2));
-  l.logit = l.least = at;
   const size_t rows = (size_t)std::min(2 * T * Hq, kFewRows * B * Hkv);
+  // few rows: a partial a row and chunk of kFewLeast keys or more.  Other rows: chunks of
+  // 256; the tensor-core kernel's two partials a range of 1024 keys take no more than
+  // one entry beside one a 512 keys.  A sequence's are rounded to pairs.
+  const size_t parts = rows * (size_t)((keys + kFewLeast - 1) / kFewLeast) +
+                       (size_t)(T * Hq) * (size_t)((keys + kChunk - 1) / kChunk + 1) + (size_t)B;
+  at = align_up(at + parts * sizeof(float2));
+  l.logit = l.least = at;
   l.total = align_up(at + std::min(rows * (size_t)keys * sizeof(float), kLogitMax));
   return l;
 }
@@ -1223,6 +1228,9 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   const bool only_few = most_rows <= kFewRows && std::min(2 * p.T * p.Hq, (int64_t)kFewRows * p.B * p.Hkv) * keys <= p.logit_cap;
   p.own_plan = only_few && p.B <= kHeldSeqs;
   const bool one_tile = most_rows <= 8;
+  // stats units there may be at most, against the warps that take them
+  const int64_t units = (int64_t)p.B * p.Hkv * ((keys + kFewChunk - 1) / kFewChunk), warps = (int64_t)sms * 8;
+  p.few_chunk = std::max(p.bs, 4 * units <= warps ? kFewLeast : 2 * units <= warps ? 2 * kFewLeast : kFewChunk);
   p.max_query = max_query_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   typedef __nv_bfloat16 bf16;

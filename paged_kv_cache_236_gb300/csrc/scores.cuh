@@ -9,6 +9,7 @@ namespace pkv {
 
 constexpr int kFewRows = 16;    // rows of a few-row sequence's kv head
 constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
+constexpr int kFewLeast = 32;   // of a short one
 constexpr int kColChunk = 256;  // keys of a column unit (few rows)
 constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
 constexpr int kChunk = 256;   // keys of a work unit (other rows)
@@ -46,6 +47,7 @@ struct ScoreParams {
   float* lse;       // per (kv head, row) of a sequence
   float* logit;     // per (kv head, key, padded row) of a few-row sequence
   int64_t logit_cap;
+  int few_chunk;    // keys of a stats unit (few rows)
   int max_query;    // the promised longest query, 0: none
   int own_plan;     // the few-row kernels make the plan themselves (no other kernel runs)
   int tensor;       // sequences of more rows go to the tensor-core kernel
