@@ -5,22 +5,23 @@
 // position r of the sequence's cache, in K, V and the running scores.  The
 // positions ascend, so kept[r] >= r: in place, a row's new position is never
 // the old position of a LATER kept row, and the only hazard is to overwrite
-// position r before the earlier row that lives there has been read.  So one
-// block walks the rows of its (sequence, head, slice) in order, a round of
-// them at a time: load the round into registers, barrier, store it.  Loads of
-// later rounds may run ahead of the stores freely.
+// position r before the earlier row that lives there has been read.  So the
+// rows are walked in order, a round of them at a time, loads ahead of stores;
+// and before the stores of a round, which reach up to position y, the rounds
+// that hold a row from below y must have been loaded by everyone.  Which round
+// that is, is known from the kept positions; a barrier is passed only when
+// the last one did not cover it.  With an eighth of the tokens kept, a round's
+// rows come from eight times as far, and few barriers are left (one a round
+// instead cost the long case below 73 us).
 //
 // The heads' rows are independent of each other, and the scores of the rows: a
 // (sequence, head)'s rows, K and V together (one address computation), are
 // one cluster's work and its scores another's.  With few of those a cluster
 // has several blocks, which share each round (a block its rows in order, the
-// blocks in order) and pass a cluster barrier between loads and stores.
+// blocks in order) and pass cluster barriers.
 //
 // HBM-bound: every kept row is read and written once; rows that stay where
-// they are (the kept prefix) are neither read nor written.  A round's loads
-// are issued before the stores of the round before it; the arrival that
-// publishes them comes before those stores too, since a releasing arrival
-// waits for the stores already under way.
+// they are (the kept prefix) are neither read nor written.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -46,28 +47,27 @@ struct CompactParams {
   int Hkv, bs, bs_log, max_blocks, budget, num_rows, max_len;  // bs_log < 0: not a power of two
   int row_bytes;  // head_dim * element size
   int cluster;    // blocks of a cluster
+  int pairs;      // (sequence, head)s
   int* err;
 };
 
 // Threads that share a row of `vecs` 16-byte vectors, at most kVecs each.
 __host__ __device__ constexpr int row_team(int vecs) { return (vecs + kVecs - 1) / kVecs; }
 
-// The barrier of a round in two halves: arrive() after this thread's loads of
-// the round, wait() before its stores: every thread of the cluster (block) has
-// then performed its loads.  One block: the whole barrier is the second half.
-__device__ __forceinline__ void round_arrive(int cluster) {
-  if (cluster > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void round_wait(int cluster) {
+// Every thread of the cluster has performed its loads so far; stores of any
+// of them may follow.
+__device__ __forceinline__ void load_barrier(int cluster) {
   if (cluster > 1)
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   else
     __syncthreads();
 }
 
 // What a thread moves: Mover::Slot holds its part of `kTokens` kept tokens on
-// their way, load() starts token i of them (kept token r, from position src;
-// src < 0: none), store() ends it.
+// their way.  locate() looks up where token i of them (kept token r, from
+// position src; src < 0: none) comes from and goes to, load() starts it,
+// store() ends it; each is done a round ahead of the next, so that none waits
+// for the reads of the one before.
 //
 // Rows: up to four 16-byte vectors of one token's K and V rows each, `apart`
 // bytes from one another so that the threads of a row read whole sectors side
@@ -86,27 +86,25 @@ struct RowMover {
   int bs, bs_log, max_blocks, apart, vecs;
   bool bad;
 
-  __device__ __forceinline__ void load(Slot& v, int, int r, int src) {
-    v.to = -1;
+  struct Place {
+    int src, r, sblk, dblk;
+  };
+  __device__ __forceinline__ void locate(Place& l, int, int r, int src) {
+    l.src = src;
     if (src < 0) return;
-    int sb, so, db, dof;
-    if (bs_log >= 0) {
-      sb = src >> bs_log;
-      db = r >> bs_log;
-      so = src & (bs - 1);
-      dof = r & (bs - 1);
-    } else {
-      sb = src / bs;
-      db = r / bs;
-      so = src - sb * bs;
-      dof = r - db * bs;
-    }
-    const int sblk = sb < max_blocks ? __ldg(bt + sb) : -1;
-    const int dblk = db < max_blocks ? __ldg(dt + db) : -1;
-    const bool s_ok = sblk >= 0 && sblk < num_blocks, d_ok = dblk >= 0 && dblk < num_blocks;
+    l.r = r;
+    const int sb = bs_log >= 0 ? src >> bs_log : src / bs, db = bs_log >= 0 ? r >> bs_log : r / bs;
+    l.sblk = sb < max_blocks ? __ldg(bt + sb) : -1;
+    l.dblk = db < max_blocks ? __ldg(dt + db) : -1;
+  }
+  __device__ __forceinline__ void load(Slot& v, const Place& l) {
+    v.to = -1;
+    if (l.src < 0) return;
+    const int so = bs_log >= 0 ? l.src & (bs - 1) : l.src % bs, dof = bs_log >= 0 ? l.r & (bs - 1) : l.r % bs;
+    const bool s_ok = l.sblk >= 0 && l.sblk < num_blocks, d_ok = l.dblk >= 0 && l.dblk < num_blocks;
     bad |= !s_ok || !d_ok;
-    const int64_t from = ((int64_t)sblk * bs + so) * token_bytes + col;
-    const int64_t dst = ((int64_t)dblk * bs + dof) * token_bytes + col;
+    const int64_t from = ((int64_t)l.sblk * bs + so) * token_bytes + col;
+    const int64_t dst = ((int64_t)l.dblk * bs + dof) * token_bytes + col;
     if (d_ok && !(s_ok && from == dst)) {
       v.to = dst;
 #pragma unroll
@@ -140,15 +138,25 @@ struct ScoreMover {
   int max_len;
   bool bad;
 
-  __device__ __forceinline__ void load(Slot& v, int i, int r, int src) {
-    v.to[i] = -1;
-    if (src < 0 || src == r || r >= max_len) return;
-    v.to[i] = r;
-    v.x[i] = 0.f;
-    if (src < max_len)
-      v.x[i] = sc[src];
-    else
-      bad = true;
+  struct Place {
+    int src[kVecs], r[kVecs];
+  };
+  __device__ __forceinline__ void locate(Place& l, int i, int r, int src) {
+    l.src[i] = src;
+    l.r[i] = r;
+  }
+  __device__ __forceinline__ void load(Slot& v, const Place& l) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      v.to[i] = -1;
+      if (l.src[i] < 0 || l.src[i] == l.r[i] || l.r[i] >= max_len) continue;
+      v.to[i] = l.r[i];
+      v.x[i] = 0.f;
+      if (l.src[i] < max_len)
+        v.x[i] = sc[l.src[i]];
+      else
+        bad = true;
+    }
   }
   __device__ __forceinline__ void store(const Slot& v) {
 #pragma unroll
@@ -175,31 +183,46 @@ __device__ __forceinline__ bool move_rounds(Mover& m, const int32_t* kept, int b
       if (src[i] >= 0 && r > 0 && __ldg(kept + r - 1) >= src[i]) bad_order = true;
     }
   };
-  auto load = [&](int base, const int (&src)[N], Slot& v) {
+  auto locate = [&](int base, const int (&src)[N], typename Mover::Place& l) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) m.load(v, i, base + block * per + i * lanes + mine, src[i]);
+    for (int i = 0; i < N; ++i) m.locate(l, i, base + block * per + i * lanes + mine, src[i]);
   };
   // every thread of the cluster sees the same rounds: the kept ones end at the first -1
   int src[N];
+  typename Mover::Place place;
   Slot now, next;
-  positions(0, src);
   if (__ldg(kept) < 0) return false;
-  load(0, src, now);
-  round_arrive(cluster);
+  positions(0, src);
+  locate(0, src, place);
   positions(round, src);
-  for (int base = 0;; base += round) {
+  m.load(now, place);
+  locate(round, src, place);
+  positions(2 * round, src);
+  int needed = 0;    // the last round that holds a row from below where this one's stores reach
+  int covered = -1;  // the last round whose loads a barrier has covered
+  int k = 0, base = 0;
+  // round k, held in `cur`: the next one's loads, the barrier if it is needed,
+  // the stores.  The two slots change places by unrolling: copying one to the
+  // other would wait for the loads that are under way.
+  auto turn = [&](Slot& cur, Slot& other) {
     const bool more = base + round < budget && __ldg(kept + base + round) >= 0;
     if (more) {
-      load(base + round, src, next);
-      positions(base + 2 * round, src);
+      m.load(other, place);
+      locate(base + 2 * round, src, place);
+      positions(base + 3 * round, src);
     }
-    round_wait(cluster);  // every load of the round at base has been performed
-    if (!more) break;
-    round_arrive(cluster);
-    m.store(now);
-    now = next;
+    while (needed < k && __ldg(kept + (needed + 1) * round) < base + round) ++needed;
+    if (needed > covered) {
+      load_barrier(cluster);
+      covered = k + (more ? 1 : 0);
+    }
+    m.store(cur);
+    ++k;
+    base += round;
+    return more;
+  };
+  while (turn(now, next) && turn(next, now)) {
   }
-  m.store(now);
   return bad_order;
 }
 
@@ -207,10 +230,13 @@ __global__ void __launch_bounds__(kMaxThreads, 2) compact_kernel(const CompactPa
   const int block = p.cluster == 1 ? 0 : blockIdx.x % p.cluster;
   const int work = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
   const int threads = blockDim.x;
-  const int sh = p.scores ? work >> 1 : work;
+  // the rows' clusters first: taking turns with the scores' short ones, a part of
+  // them was left for a second wave of blocks (the long case below: 72 us)
+  const bool rows = work < p.pairs;
+  const int sh = rows ? work : work - p.pairs;
   const int s = sh / p.Hkv, h = sh - s * p.Hkv;
   const int32_t* kept = p.kept + (int64_t)sh * p.budget;
-  if (p.scores && (work & 1)) {  // the running scores
+  if (!rows) {  // the running scores
     const int row = p.rows ? p.rows[s] : s;
     if (row < 0 || row >= p.num_rows) {
       if (row >= 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_BAD_SEQUENCE);
@@ -308,6 +334,7 @@ extern "C" pkv_status paged_kv_compact(void* k_cache, void* v_cache, const int32
   if (pairs < 2 * sms || team > threads) threads = 256;
   while (cluster < 8 && pairs * cluster < 2 * sms && cluster * 2 * (threads / team) <= budget) cluster *= 2;
   p.cluster = cluster;
+  p.pairs = (int)pairs;
   if (units * cluster > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "too many sequences and heads");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * cluster));

@@ -5,12 +5,13 @@
 // A radix select: the scores map to 32-bit keys whose unsigned order is
 // theirs (NaN lowest, -0 as +0); histograms of 11, 11 and 10 bits over the
 // middle positions narrow down the value of the last key kept and how many
-// equal to it are kept; a last pass writes the kept positions in order,
-// taking equals from the lowest position.
+// equal to it are kept; a pass turns the keys into bit masks (above it, equal to
+// it) of 32 positions each, and the masks, counted, say where each kept
+// position goes, equals being taken from the lowest position.
 //
-// Latency-bound: a (sequence, head) has a few thousand scores.  Its keys are
-// read from memory once and kept in shared memory for the four passes over
-// them; long rows are cut over the blocks of a cluster, which add up their
+// Bound by latency and instructions: a (sequence, head) has a few thousand
+// scores.  Its keys are read from memory once and kept in shared memory for
+// the passes over them; long rows are cut over the blocks of a cluster, which add up their
 // histograms and counts through distributed shared memory.  The first digit
 // takes 11 bits (sign, exponent, two bits of mantissa) so that scores of one
 // magnitude do not all meet in one counter.
@@ -92,7 +93,7 @@ template <int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kernel(const SelectParams p) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kPer = kBins / kThreads < 4 ? 4 : kBins / kThreads;  // bins of a thread
-  extern __shared__ uint32_t keys[];            // [held]
+  extern __shared__ uint32_t keys[];            // [held], then masks [2][held / 32]
   __shared__ __align__(16) int hist[2][kBins];  // this block's counts (by digit parity; peers read them)
   __shared__ int sum[2 * kWarps];
   __shared__ int wsum[kWarps];
@@ -140,7 +141,6 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kern
       }
     }
   }
-  auto key = [&](int i) { return i < held ? keys[i] : key_of(sc[i]); };
   uint32_t prefix = 0, mask = 0;
   bool whole = false;  // every key that starts like prefix is kept
 #pragma unroll 1
@@ -149,11 +149,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kern
     const int bins = digit == 2 ? 1024 : 2048;
     int* mine = hist[digit & 1];
     if (digit > 0) {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kThreads) {
-        const uint32_t k = key(i);
+      auto count = [&](uint32_t k) {
         if ((k & mask) == prefix) atomicAdd(&mine[(k >> shift) & (bins - 1)], 1);
-      }
+      };
+#pragma unroll 4
+      for (int i = tid; i < held; i += kThreads) count(keys[i]);
+#pragma unroll 1
+      for (int i = held + tid; i < n; i += kThreads) count(key_of(sc[i]));  // what shared memory could not hold
     }
     cluster_sync(p.cluster);  // the counts of every block are complete
     // thread t: the cluster's counts of kPer bins, the highest first
@@ -172,15 +174,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kern
           c[j + 2] = v.y;
           c[j + 3] = v.x;
         } else {
-          int4 v[kMaxCluster];
-#pragma unroll
-          for (int b = 0; b < kMaxCluster; ++b) v[b] = b < p.cluster ? peer_int4(at, b) : make_int4(0, 0, 0, 0);
-#pragma unroll
-          for (int b = 0; b < kMaxCluster; ++b) {
-            c[j] += v[b].w;
-            c[j + 1] += v[b].z;
-            c[j + 2] += v[b].y;
-            c[j + 3] += v[b].x;
+#pragma unroll 1
+          for (int b0 = 0; b0 < p.cluster; b0 += 2) {  // a cluster has an even number of blocks
+            const int4 v = peer_int4(at, b0), w = peer_int4(at, b0 + 1);
+            c[j] += v.w + w.w;
+            c[j + 1] += v.z + w.z;
+            c[j + 2] += v.y + w.y;
+            c[j + 3] += v.x + w.x;
           }
         }
       }
@@ -215,21 +215,24 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kern
   auto above = [&](uint32_t k) { return whole ? k >= prefix : k > prefix; };
   auto equal = [&](uint32_t k) { return !whole && k == prefix; };
   // `need` of the keys equal to `prefix` are kept, from the lowest position.
-  // A warp takes a run of the block's positions: it counts its keys above and
-  // equal, then knows where its first kept one goes, and writes.
-  const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
-  const int a = min(n, warp * run), b = min(n, a + run);
-  int gt = 0, eq = 0;
-#pragma unroll 4
-  for (int i = a + lane; i < b; i += 32) {
-    const uint32_t k = key(i);
-    gt += above(k);
-    eq += equal(k);
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    gt += __shfl_xor_sync(0xffffffffu, gt, d);
-    eq += __shfl_xor_sync(0xffffffffu, eq, d);
+  // A warp takes a run of the block's positions, in groups of 32.
+  const int groups = (n + 31) >> 5, run = (groups + kWarps - 1) / kWarps, held_groups = held == n ? groups : held >> 5;
+  const int ga = min(groups, warp * run), gb = min(groups, ga + run);
+  uint32_t* masks = keys + ((p.held + 31) & ~31);  // a group's keys above, and equal
+  int gt = 0, eq = 0;  // of the run, in every lane
+  auto group_masks = [&](int g, uint32_t& mg, uint32_t& me) {
+    const int i = 32 * g + lane;
+    const uint32_t k = i < n ? g < held_groups ? keys[i] : key_of(sc[i]) : 0u;
+    mg = __ballot_sync(0xffffffffu, i < n && above(k));
+    me = __ballot_sync(0xffffffffu, i < n && equal(k));
+  };
+#pragma unroll 2
+  for (int g = ga; g < gb; ++g) {
+    uint32_t mg, me;
+    group_masks(g, mg, me);
+    if (g < held_groups && lane < 2) masks[2 * g + lane] = lane ? me : mg;
+    gt += __popc(mg);
+    eq += __popc(me);
   }
   if (lane == 0) {
     sum[2 * warp] = gt;
@@ -258,15 +261,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 2 : 4) select_kern
     cluster_sync(p.cluster);  // a block's shared memory outlives its readers
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = a; i0 < b; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < b ? key(i) : 0u;
-    const bool is_gt = i < b && above(k), is_eq = i < b && equal(k);
-    const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me_ = __ballot_sync(0xffffffffu, is_eq);
-    const int g = gt0 + __popc(mg & below), e = eq0 + __popc(me_ & below);
-    if (is_gt || (is_eq && e < need)) out[p.sink + g + min(e, need)] = lo + i;
+  out += p.sink;
+#pragma unroll 2
+  for (int g = ga; g < gb; ++g) {
+    uint32_t mg, me;
+    if (g < held_groups) {
+      mg = masks[2 * g];
+      me = masks[2 * g + 1];
+    } else {
+      group_masks(g, mg, me);
+    }
+    const int e = eq0 + __popc(me & below);
+    if ((mg >> lane & 1) || ((me >> lane & 1) && e < need))
+      out[gt0 + __popc(mg & below) + min(e, need)] = lo + 32 * g + lane;
     gt0 += __popc(mg);
-    eq0 += __popc(me_);
+    eq0 += __popc(me);
   }
 }
 
@@ -300,10 +309,10 @@ extern "C" pkv_status paged_kv_select(const float* scores, const int32_t* score_
   if (st != PKV_OK) return st;
   // blocks of a (sequence, head) by the longest row there can be
   while (p.cluster < kMaxCluster && (int64_t)p.cluster * kPerBlock < max_len) p.cluster *= 2;
-  p.held = std::min((max_len + p.cluster - 1) / p.cluster, kHeld);
+  p.held = (std::min((max_len + p.cluster - 1) / p.cluster, kHeld) + 31) & ~31;
   const int64_t grid = (int64_t)num_seqs * num_kv_heads * p.cluster;
   if (grid > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "too many sequences and heads");
-  const size_t smem = (size_t)p.held * sizeof(uint32_t);
+  const size_t smem = (size_t)(p.held + p.held / 16) * sizeof(uint32_t);  // keys, and two masks for 32
   cudaError_t e = cudaSuccess;
   if (p.cluster > 1 || p.held > kPerBlock / 2) {  // with the static arrays, past the 48 KB every kernel may use
     static unsigned long long done_mask = 0;  // devices set up
@@ -311,7 +320,7 @@ extern "C" pkv_status paged_kv_select(const float* scores, const int32_t* score_
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_error(e, "cudaGetDevice");
     if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << (dev & 63)))) {
       e = cudaFuncSetAttribute(select_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kHeld * (int)sizeof(uint32_t));
+                               (kHeld + kHeld / 16) * (int)sizeof(uint32_t));
       if (e != cudaSuccess) return cuda_error(e, "paged_kv_select set-up");
       __atomic_fetch_or(&done_mask, 1ull << (dev & 63), __ATOMIC_RELEASE);
     }
