@@ -64,7 +64,13 @@ namespace {
 constexpr int kThreadsMma = 416;
 constexpr int kTile = 128;      // rows or keys of a tile
 constexpr int kStages = 4;      // streamed tiles
-constexpr int kAccs = 4;        // accumulators
+// Accumulators: two for each epilogue group, counted by group.  A ring that
+// both groups share would let a group that has few K tiles (row tiles that see
+// one K tile of the range all belong to group 0) test a barrier whose previous
+// phase is not complete, and take the phase before that one, of the same
+// parity, for its own.
+constexpr int kGroupAccs = 2;
+constexpr int kAccs = 2 * kGroupAccs;
 constexpr int kItems = 2;       // item ring
 constexpr int kRangeTiles = kTcRange / kTile;
 constexpr int kIds = kTcRange / 8;  // block ids of a range, at most
@@ -338,7 +344,8 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
     // ================================================================ MMA issuer
     if (lane == 0) {
       const uint64_t dx0 = desc_k(smem_base + Y::kXOff), dy0 = desc_k(smem_base + Y::kYOff);
-      int g = 0, nx = 0;
+      int g = 0, nx = 0;       // streamed and resident tiles so far
+      int na[2] = {0, 0};      // accumulators of each group so far
       bool ok = true;
       for (int it = 0; ok; ++it) {
         const int sl = it % kItems;
@@ -359,9 +366,10 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
           const int nr = (min(tile_rows, im.rows - tile * tile_rows) + 15) & ~15;
           const uint32_t idesc = im.type == kStats ? kIdesc128 : kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
           for (int i = 0; i < ny; ++i, ++g) {
-            const int st = g % kStages, acc = g % kAccs;
+            const int st = g % kStages, wg = i & 1, k = wg == 0 ? na[0] : na[1];
+            const int acc = wg * kGroupAccs + k % kGroupAccs;
             for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->y_full[st][h], (g / kStages) & 1, wc);
-            if (!ok || !mbar_wait(&bars->acc_empty[acc], ((g / kAccs) & 1) ^ 1, wc)) {
+            if (!ok || !mbar_wait(&bars->acc_empty[acc], ((k / kGroupAccs) & 1) ^ 1, wc)) {
               ok = false;
               break;
             }
@@ -373,13 +381,20 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
               umma_bf16(tmem + acc * 128, desc_add(da, (kk >> 2) * kHalf + (kk & 3) * 32),
                         desc_add(db, (kk >> 2) * kHalf + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
             umma_commit(&bars->acc_full[acc]);
+            if (wg == 0)
+              ++na[0];
+            else
+              ++na[1];
             umma_commit(&bars->y_empty[st]);
             if (i == ny - 1) umma_commit(&bars->x_empty[xb]);
           }
         }
       }
       // leaving: the MMAs already issued finish before TMEM is freed
-      for (int j = max(0, g - kAccs); j < g; ++j) mbar_wait(&bars->acc_full[j % kAccs], (j / kAccs) & 1, wc);
+#pragma unroll
+      for (int w = 0; w < 2; ++w)
+        for (int j = max(0, na[w] - kGroupAccs); j < na[w]; ++j)
+          mbar_wait(&bars->acc_full[w * kGroupAccs + j % kGroupAccs], (j / kGroupAccs) & 1, wc);
     }
     __syncwarp();
   } else if (warp == 12) {
@@ -430,7 +445,7 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
     float* sums = reinterpret_cast<float*>(smem + Y::kSumOff) + t;
     const int tile_rows = p.tile_tok * p.G;
     const f32x2 scale2 = pk2(p.scale_log2, p.scale_log2);
-    int g = 0, n_nl = 0;  // K tiles and lse buffers so far
+    int na = 0, n_nl = 0;  // this group's accumulators and lse buffers so far
     bool pending = false;
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
@@ -448,11 +463,12 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
         const int vis = p.causal ? min(im.L, im.L - im.n + row / p.G + 1) : im.L;
         float m = -CUDART_INF_F, l = 0.f;
         const bool live = __any_sync(0xffffffffu, valid);
-        for (int i = 0; i < ny; ++i, ++g) {
-          if ((i & 1) != wg || pending) continue;
-          const int acc = g % kAccs;
-          pending = !wait_all(&bars->acc_full[acc], (g / kAccs) & 1, wc);
-          if (pending) continue;
+        for (int i = wg; i < ny; i += 2) {
+          if (pending) break;
+          const int acc = wg * kGroupAccs + na % kGroupAccs;
+          pending = !wait_all(&bars->acc_full[acc], (na / kGroupAccs) & 1, wc);
+          if (pending) break;
+          ++na;
           tc_fence_after();
           if (live) {
             const int kb = im.key0 + i * kTile;
@@ -524,14 +540,15 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
         }
         if (tile + 1 < end) next = lse_of(tile + 1);
         const int first = tile * tile_rows, nr = min(tile_rows, im.rows - first);
-        for (int i = 0; i < ny; ++i, ++g) {
-          if ((i & 1) != wg || pending) continue;
-          const int acc = g % kAccs, j = im.key0 + i * kTile + t;
+        for (int i = wg; i < ny; i += 2) {
+          if (pending) break;
+          const int acc = wg * kGroupAccs + na % kGroupAccs, j = im.key0 + i * kTile + t;
           const bool keeps = tile + 1 == end && j < im.L;  // this key's sum is complete: store it
           const bool adds = keeps && j < im.L - im.n && p.decay != 0.f;
           const float old = adds ? p.scores[at0 + j] : 0.f;
-          pending = !wait_all(&bars->acc_full[acc], (g / kAccs) & 1, wc);
-          if (pending) continue;
+          pending = !wait_all(&bars->acc_full[acc], (na / kGroupAccs) & 1, wc);
+          if (pending) break;
+          ++na;
           tc_fence_after();
           // rows below `from` do not see key j
           const int from = p.causal ? max(0, j - (im.L - im.n)) * p.G - first : 0;

@@ -155,6 +155,21 @@ def test_many_queries(n, L, dtype):
     b.check(b.run(), before)
 
 
+@pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (32, 2, 32), (8, 8, 64)])
+def test_prompts_from_the_first_token(Hq, Hkv, bs):
+    """No context before the queries: row tiles that see one, two, ... K tiles
+    of a range, in odd and even numbers, and short sequences of one K tile in a
+    row; over and over, since only the timing of the roles could go wrong."""
+    lens = [700, 128, 90, 33, 127, 385, 64, 1100, 100, 100, 1]
+    b = Batch(Hq + bs, lens, lens, Hq, Hkv, 128, bs)
+    before = b.old.clone()
+    first = b.run(out=b.old.clone())
+    b.check(first, before)
+    for _ in range(50):
+        assert torch.equal(b.run(out=b.old.clone()), first)
+    assert pkv.device_errors() == 0
+
+
 def test_chunk_equals_steps():
     """Scores of a prompt's tokens: all queries at once, or one step after
     another with decay 1, add up to the same."""
