@@ -12,7 +12,7 @@
 // that is, is known from the kept positions; a barrier is passed only when
 // the last one did not cover it.  With an eighth of the tokens kept, a round's
 // rows come from eight times as far, and few barriers are left (one a round
-// instead cost the long case below 73 us).
+// instead: 73 us for 4 sequences of 131072 tokens in FP8, 64 us this way).
 //
 // The heads' rows are independent of each other, and the scores of the rows: a
 // (sequence, head)'s rows, K and V together (one address computation), are
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) compact_kernel(const CompactPa
   const int work = p.cluster == 1 ? blockIdx.x : blockIdx.x / p.cluster;
   const int threads = blockDim.x;
   // the rows' clusters first: taking turns with the scores' short ones, a part of
-  // them was left for a second wave of blocks (the long case below: 72 us)
+  // them was left for a second wave of blocks (the long FP8 case: 72 us, not 64)
   const bool rows = work < p.pairs;
   const int sh = rows ? work : work - p.pairs;
   const int s = sh / p.Hkv, h = sh - s * p.Hkv;

