@@ -763,6 +763,8 @@ def _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, int
     rows = (T, Hkv, D)
     if k.shape != rows or v.shape != rows or ks[2] != 1 or ks[1] != D or vs[2] != 1 or vs[1] != D:
         raise ValueError(f"k and v must be [{T}, {Hkv}, {D}] with contiguous heads")
+    if T > 1 and 0 in (qs[0], ks[0], vs[0]):  # the C call takes a stride of 0 for dense
+        raise ValueError("q, k and v must not repeat one token's row (a token stride of 0)")
     if positions.shape != (T,) or positions.dtype != torch.int64 or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int64 [T]")
     if slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():
@@ -776,8 +778,8 @@ def _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, int
         raise ValueError("q_out must be contiguous and match q")
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(),
             slot_mapping.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, NB, bs, shape[1],
-            Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude, qs[0] if T else 0, ks[0] if T else 0,
-            vs[0] if T else 0, DTYPE[dtype])
+            Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, amplitude, qs[0] if T > 1 else 0,
+            ks[0] if T > 1 else 0, vs[0] if T > 1 else 0, DTYPE[dtype])
     return args, q_out
 
 

@@ -226,3 +226,22 @@ def test_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(kc, want_k)
+
+
+def test_one_token_of_any_stride_and_repeated_rows():
+    """A lone token's stride does not matter; one row repeated over several
+    tokens (a stride of 0, which the C call takes for dense) is refused."""
+    kc = torch.zeros(2, 16, 2, 64, device="cuda")
+    vc = torch.zeros_like(kc)
+    f = pkv.rope_frequencies(64)
+    i64 = lambda x: torch.tensor(x, dtype=torch.int64, device="cuda")  # noqa: E731
+    row = torch.randn(1, 2, 64, device="cuda")
+    want = pkv.paged_kv_write_rope(row, row, row, i64([5]), f, i64([3]), kc, vc)
+    lone = row.as_strided((1, 2, 64), (0, 64, 1))
+    assert torch.equal(pkv.paged_kv_write_rope(lone, lone, lone, i64([5]), f, i64([4]), kc, vc), want)
+    assert torch.equal(kc[0, 3], kc[0, 4]) and torch.equal(vc[0, 4], row[0])
+    many, dense = row.expand(3, 2, 64), row.repeat(3, 1, 1)
+    for at in range(3):
+        rows = [many if i == at else dense for i in range(3)]
+        with pytest.raises(ValueError):
+            pkv.paged_kv_write_rope(*rows, i64([0, 1, 2]), f, i64([0, 1, 2]), kc, vc)
