@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads) stats_kernel(const ScoreParams p) {
       float k[X::E];
       X::load_k(p, bt, j, h, lane, k);
       const float z = group_dot<X::E>(k, q, lane) * p.scale_log2;
-      if (j < vis) {
+      if (j < vis && z != -CUDART_INF_F) {  // a logit of -inf weighs nothing, also before the first finite one
         const float mn = fmaxf(m, z);
         l = l * fast_exp2(m - mn) + fast_exp2(z - mn);
         m = mn;

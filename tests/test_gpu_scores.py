@@ -280,6 +280,30 @@ def test_nan_in_masked_places():
     assert torch.isfinite(got[:2, :, :90]).all() and torch.isnan(got[:2, :, 90:]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_logits_of_minus_infinity(n, dtype):
+    """Infinite keys whose logits are -inf weigh nothing: the first key, a run
+    that fills whole tiles, every seventh after it."""
+    L = 700
+    b = Batch(55 + n, [L], [n], 8, 2, 128, 16, torch.float32 if dtype == "f32" else torch.bfloat16)
+    off = sorted({0, *range(128, 400), *range(400, L - n, 7)})
+    b.q[..., 0] = -1.0
+    for j in off:
+        b.kc[b.tables[0, j // 16], j % 16, :, 0] = math.inf
+        b.K[b.tables[0, j // 16], j % 16, :, 0] = math.inf
+    before = b.old.clone()
+    got = b.run(decay=0.0, out=b.old.clone()).cpu().numpy()
+    q, K = to_f64(b.q), b.keys(0)
+    paid = ob.scores_update(q, K, before[0, :, :L].cpu().numpy(), b.scale, True, 0.0)
+    seen = np.setdiff1d(np.arange(L), off)
+    # the bounds of Batch.check, over the finite keys
+    dots = np.abs(q).reshape(-1, 128).max(0) @ np.abs(K[seen]).reshape(-1, 128).max(0)
+    rel = 2 * b.scale * 130 * 2.0 ** -24 * dots + 2 * 2.0 ** -22 + 1.3e-4
+    assert np.all(np.abs(got[0, :, :L] - paid) <= rel * paid + n * b.Hq * 2.0 ** -120)
+    assert np.all(got[0][:, off] == 0.0)
+
+
 def test_same_bits_each_time_and_workspaces():
     """Equal calls give equal bits, with the least workspace too the same
     numbers; back-to-back calls share the cached workspace."""
