@@ -586,7 +586,9 @@ struct Stats {
       Dot::load_q(q, nt, row, t);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        vis[nt][e] = p.causal ? min(sp.L, sp.L - sp.n + (nt * 8 + 2 * t + e) / p.G + 1) : sp.L;
+        const int mine = nt * 8 + 2 * t + e;
+        // padding rows see nothing: their zeros against an infinite key are NaN
+        vis[nt][e] = mine >= sp.rows ? 0 : p.causal ? min(sp.L, sp.L - sp.n + mine / p.G + 1) : sp.L;
         m[nt][e] = -CUDART_INF_F;
         l[nt][e] = 0.f;
       }

@@ -281,7 +281,7 @@ def test_nan_in_masked_places():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n", [1, 4, 40])
+@pytest.mark.parametrize("n", [1, 3, 4, 40])
 def test_logits_of_minus_infinity(n, dtype):
     """Infinite keys whose logits are -inf weigh nothing: the first key, a run
     that fills whole tiles, every seventh after it."""
