@@ -924,7 +924,7 @@ def paged_attention_scores_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, block_t
                                  score_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
                                  workspace: torch.Tensor | None = None, max_query_len: int = 0) -> torch.Tensor:
     """``paged_attention_scores`` over an FP8 K pool read as code * k_scale
-    (q bf16, head_dim 128)."""
+    (q bf16 with |q| below 65504, head_dim 128)."""
     dev = _device_of(q, k_cache, block_tables, context_lens, query_start_loc, scores, score_rows)
     _check_fp8_pools(k_cache, k_cache)
     if q.dtype != torch.bfloat16:

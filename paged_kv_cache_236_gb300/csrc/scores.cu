@@ -1210,6 +1210,12 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   if (p.num_blocks > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "num_blocks exceeds int32");
   if ((p.B + p.T) * p.Hkv > (((int64_t)1 << 31) - 1) / ((keys + 127) / 128))
     return fail(PKV_ERR_UNSUPPORTED, "too much work for one call");
+  // bf16: more rows go to the tensor-core kernel (its operands come through tensor maps)
+  p.tensor = !f8 && dtype == PKV_DTYPE_BF16;
+  p.tile_tok = 128 / p.G;
+  const int64_t most_tokens = std::min({p.T, keys, max_query_len > 0 ? (int64_t)max_query_len : p.T});
+  if (p.tensor && most_tokens > (int64_t)kMaxRowTiles * p.tile_tok)
+    return fail(PKV_ERR_UNSUPPORTED, "too many query rows per kv head of a sequence (split the queries over calls)");
   if (p.B == 0 || p.T == 0) return PKV_OK;
   if (!p.q || !p.kc || !p.tables || !p.lens || !p.qsl || !p.scores || !p.out)
     return fail(PKV_ERR_INVALID_ARG, "null pointer");
@@ -1244,9 +1250,6 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   p.max_query = max_query_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   typedef __nv_bfloat16 bf16;
-  // bf16: more rows go to the tensor-core kernel (its operands come through tensor maps)
-  p.tensor = !f8 && dtype == PKV_DTYPE_BF16;
-  p.tile_tok = 128 / p.G;
   CUtensorMap qmap, kmap;
   pkv_status mst;
   if (p.tensor && !only_few) {

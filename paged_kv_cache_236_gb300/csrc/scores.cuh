@@ -12,6 +12,10 @@ constexpr int kFewChunk = 128;  // keys of a stats unit (few rows)
 constexpr int kFewLeast = 32;   // of a short one
 constexpr int kColChunk = 256;  // keys of a column unit (few rows)
 constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
+// Row tiles of a sequence the tensor-core kernel takes: a column item goes
+// through all of them (8 key tiles each, below 1 us a tile), and the waits of
+// the roles that stand by, up to two items long, end after 2 s.
+constexpr int kMaxRowTiles = 1 << 16;
 constexpr int kChunk = 256;   // keys of a work unit (other rows)
 enum { kFew = 1, kTensor = 2, kOther = 3 };
 constexpr int kRowGroup = 8;  // rows of a work unit (other rows)

@@ -57,6 +57,12 @@ def test_scores_refusals(lib):
     for bad in (dict(B=-1), dict(T=-1), dict(NB=0), dict(mb=0), dict(rows=0), dict(maxlen=0), dict(scale=0.0),
                 dict(scale=math.nan), dict(decay=-0.5), dict(decay=math.inf), dict(decay=math.nan)):
         assert scores(lib, **bad) == 1, bad
+    # row tiles of one sequence: 2 tokens each with 64 heads to a kv head
+    wide = dict(Hq=64, Hkv=1, D=64, NB=1 << 20, mb=1 << 14, maxlen=1 << 20)
+    assert scores(lib, T=(1 << 17) + 1, **wide) == 2 and b"query rows" in lib.pkv_last_error()
+    assert scores(lib, T=1 << 17, **wide) == 1                          # allowed: stops at the null pointers
+    assert scores(lib, T=(1 << 17) + 1, **{**wide, "maxlen": 4096}) == 1  # no sequence has so many
+    assert scores(lib, T=(1 << 17) + 1, dt=0, **wide) == 1              # fp32 has no such limit
     assert scores(lib, k_scale=0.0) == 1 and scores(lib, D=64, k_scale=1.0) == 2
 
 
