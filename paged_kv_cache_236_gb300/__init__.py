@@ -217,6 +217,10 @@ _ws_cache: dict = {}
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
+    if torch.cuda.is_current_stream_capturing():
+        # a graph keeps its own: a cached one is replaced when a later call
+        # wants more, and graphs captured on one stream may be replayed on two
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:

@@ -347,6 +347,42 @@ def test_graph_replay_follows_its_inputs():
         b.lens = held
 
 
+def test_graphs_keep_their_own_workspace():
+    """Two steps captured on one stream without a workspace, and later eager
+    calls there that need a larger one: each replay is right, also both at
+    once on two streams."""
+    pair = [Batch(75 + i, [900 + 50 * i, 300], [1, 1 + 39 * i], 8, 2, 128, 16) for i in range(2)]
+    large = Batch(79, [6000, 5000], [40, 1], 8, 2, 128, 16)
+    want = [b.run(out=b.old.clone()) for b in pair]
+    want_large = large.run(out=large.old.clone())
+    outs = [b.old.clone() for b in pair]
+    graphs = [torch.cuda.CUDAGraph() for _ in pair]
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for b in pair:
+            b.run(out=b.old.clone())  # eager on the stream of the captures
+        for b, g, out in zip(pair, graphs, outs):
+            with torch.cuda.graph(g, stream=st):
+                b.run(out=out)
+        got = large.run(out=large.old.clone())
+    torch.cuda.synchronize()
+    assert torch.equal(got, want_large)
+    fill = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(32)]
+    streams = [torch.cuda.Stream() for _ in pair]
+    for _ in range(20):
+        for b, out in zip(pair, outs):
+            out.copy_(b.old)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert all(bool((x == 7).all()) for x in fill)
+    assert pkv.device_errors() == 0
+
+
 def test_other_stream():
     b = Batch(81, [5000, 300], [1, 1], 8, 2, 128, 16)
     want = b.run(out=torch.zeros_like(b.old)).clone()
