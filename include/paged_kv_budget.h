@@ -71,7 +71,7 @@ extern "C" {
  * earlier one) sets PKV_DEVERR_BAD_SEQUENCE and leaves its row as it was.  An
  * out-of-pool block id is read as a block of zeros and sets
  * PKV_DEVERR_BLOCK_OUT_OF_RANGE, as in paged_attention_forward.
- * bf16: a sequence has at most 65536 * floor(128 / group) queries (group: q
+ * bf16 queries: a sequence has at most 65536 * floor(128 / group) queries (group: q
  * heads per kv head); a call whose num_tokens, max_context and max_query_len
  * would allow more returns PKV_ERR_UNSUPPORTED.
  */
@@ -87,7 +87,7 @@ pkv_status paged_attention_scores(const void* q, const void* k_cache, const int3
 /*
  * paged_attention_scores_fp8kv - the same over an FP8 K pool (E4M3 codes read
  * as code * k_scale; q bf16; head_dim 128), as paged_attention_forward_fp8kv.
- * Sequences of few rows round q to fp16: |q| must stay below 65504.
+ * q is rounded to fp16: |q| must stay below 65504.
  */
 pkv_status paged_attention_scores_fp8kv(const void* q, const void* k_cache, const int32_t* block_tables,
                                         const int32_t* context_lens, const int32_t* query_start_loc,

@@ -146,7 +146,8 @@ pkv_status device_state(int* sms, int** err) {
 
 pkv_status cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
-pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D) {
+pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D, bool codes) {
+  if (codes) return encode_pool_map(map, pool, PKV_DTYPE_FP8_E4M3, NB, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_NONE);
   return encode_pool_map(map, pool, PKV_DTYPE_BF16, NB, bs, Hkv, D, 64, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 

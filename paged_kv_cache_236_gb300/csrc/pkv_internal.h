@@ -226,7 +226,7 @@ pkv_status device_state(int* sms, int** err);
 // Tensor maps of a bf16 block pool, boxes of one block of one kv head by 64
 // columns, and of bf16 rows [T, Hq, D], boxes of G heads of `tokens` tokens by
 // 64 columns (both 128-byte swizzled; call device_state first).
-pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D);
+pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D, bool codes);
 pkv_status rows_map(CUtensorMap* map, const void* q, int64_t T, int Hq, int D, int G, int tokens);
 
 // Sets the message to `what` and the error's name; returns PKV_ERR_CUDA.

@@ -24,10 +24,11 @@
 // When only these kernels have work, each block of few_kernel makes the plan
 // itself, in shared memory, instead of a launch before it.
 //
-// More rows in bf16: the tensor-core kernel of scores_mma.cu.
+// More rows of bf16 queries (bf16 or FP8 pools): the tensor-core kernel of
+// scores_mma.cu.
 //
-// Other rows: stats_kernel, lse_kernel, columns_kernel, which compute the
-// logits twice.
+// More rows in fp32, whose products no tensor-core format keeps: stats_kernel,
+// lse_kernel, columns_kernel, which compute the logits twice.
 //
 // Every sum has a fixed order (no float atomics).
 //
@@ -378,15 +379,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t codes_to_f16(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
-  const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // bf16 rows: 16-byte piece c of lane t is d = 32 c + 8 t .. + 7, two k-steps.
@@ -912,15 +904,8 @@ __global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(co
 }
 
 // ---------------------------------------------------------------------------
-// other rows
+// more rows in fp32
 // ---------------------------------------------------------------------------
-// E of a lane's consecutive elements of a row, as fp32.
-template <typename T, int E>
-__device__ __forceinline__ void load_row(const T* p, float (&x)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; ++i) x[i] = (float)p[i];
-}
-
 // Logits (times scale * log2 e) of a row group against one key: lane l
 // returns the logit of row l >> 2 (kRowGroup == 8 rows, 4 lanes each).
 template <int E>
@@ -949,7 +934,7 @@ __device__ __forceinline__ float group_dot(const float (&k)[E], const float (&q)
   return x;
 }
 
-template <typename TQ, typename TK, int D>
+template <int D>
 struct Tile {
   static constexpr int E = D / 32;
   // Row group rg of kv head h: the lane's slice of each of its rows' q
@@ -961,8 +946,9 @@ struct Tile {
       const int row = rg * kRowGroup + r;
       if (row < rows) {
         const int i = row / p.G, g = row - i * p.G;
-        const TQ* src = static_cast<const TQ*>(p.q) + ((int64_t)(qstart + i) * p.Hq + h * p.G + g) * D + lane * E;
-        load_row<TQ, E>(src, q[r]);
+        const float* src = static_cast<const float*>(p.q) + ((int64_t)(qstart + i) * p.Hq + h * p.G + g) * D + lane * E;
+#pragma unroll
+        for (int j = 0; j < E; ++j) q[r][j] = src[j];
       } else {
 #pragma unroll
         for (int j = 0; j < E; ++j) q[r][j] = 0.f;
@@ -973,9 +959,10 @@ struct Tile {
   __device__ static void load_k(const ScoreParams& p, const int32_t* bt, int j, int h, int lane, float (&k)[E]) {
     const int b = bt[j / p.bs];
     if (b >= 0 && b < p.num_blocks) {
-      const TK* src =
-          static_cast<const TK*>(p.kc) + (((int64_t)b * p.bs + j % p.bs) * p.Hkv + h) * D + lane * E;
-      load_row<TK, E>(src, k);
+      const float* src =
+          static_cast<const float*>(p.kc) + (((int64_t)b * p.bs + j % p.bs) * p.Hkv + h) * D + lane * E;
+#pragma unroll
+      for (int i = 0; i < E; ++i) k[i] = src[i];
     } else {
       raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
 #pragma unroll
@@ -984,9 +971,9 @@ struct Tile {
   }
 };
 
-template <typename TQ, typename TK, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) stats_kernel(const ScoreParams p) {
-  using X = Tile<TQ, TK, D>;
+  using X = Tile<D>;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
   const int64_t total = p.off[kStat][p.B];
@@ -1032,9 +1019,9 @@ __global__ void __launch_bounds__(kThreads) lse_kernel(const ScoreParams p) {
   }
 }
 
-template <typename TQ, typename TK, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) columns_kernel(const ScoreParams p) {
-  using X = Tile<TQ, TK, D>;
+  using X = Tile<D>;
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
   const int64_t total = p.off[kCol][p.B];
@@ -1140,18 +1127,22 @@ cudaError_t launch_few(const ScoreParams& p, int sms, cudaStream_t s) {
   return launch_pdl(few_columns_kernel, dim3(sms * kColBlocks), dim3(kColThreads), held_bytes(p.B), s, p);
 }
 
-template <typename TQ, typename TK, int D, typename Dot>
-cudaError_t launch(const ScoreParams& p, bool only_few, bool one_tile, int sms, cudaStream_t s) {
+// The plan and the few-row sequences.
+template <typename Dot>
+cudaError_t launch(const ScoreParams& p, bool one_tile, int sms, cudaStream_t s) {
   if (p.own_plan)
     start_few_kernel<<<1, 32, 0, s>>>(p.counters);
   else
     plan_scores_kernel<<<1, std::min(kPlanThreads, (p.B + 31) / 32 * 32), 0, s>>>(p);
-  cudaError_t e = one_tile ? launch_few<Dot, 1>(p, sms, s) : launch_few<Dot, 2>(p, sms, s);
-  if (e != cudaSuccess || only_few || p.tensor) return e;
+  return one_tile ? launch_few<Dot, 1>(p, sms, s) : launch_few<Dot, 2>(p, sms, s);
+}
+
+template <int D>
+cudaError_t launch_other(const ScoreParams& p, int sms, cudaStream_t s) {
   const int grid = sms * 8;
-  stats_kernel<TQ, TK, D><<<grid, kThreads, 0, s>>>(p);
+  stats_kernel<D><<<grid, kThreads, 0, s>>>(p);
   lse_kernel<<<grid, kThreads, 0, s>>>(p);
-  columns_kernel<TQ, TK, D><<<grid, kThreads, 0, s>>>(p);
+  columns_kernel<D><<<grid, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -1210,8 +1201,8 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   if (p.num_blocks > ((int64_t)1 << 31) - 1) return fail(PKV_ERR_UNSUPPORTED, "num_blocks exceeds int32");
   if ((p.B + p.T) * p.Hkv > (((int64_t)1 << 31) - 1) / ((keys + 127) / 128))
     return fail(PKV_ERR_UNSUPPORTED, "too much work for one call");
-  // bf16: more rows go to the tensor-core kernel (its operands come through tensor maps)
-  p.tensor = !f8 && dtype == PKV_DTYPE_BF16;
+  // more rows of bf16 queries go to the tensor-core kernel (its operands come through tensor maps)
+  p.tensor = dtype == PKV_DTYPE_BF16;
   p.tile_tok = 128 / p.G;
   const int64_t most_tokens = std::min({p.T, keys, max_query_len > 0 ? (int64_t)max_query_len : p.T});
   if (p.tensor && most_tokens > (int64_t)kMaxRowTiles * p.tile_tok)
@@ -1249,23 +1240,22 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   p.few_chunk = std::max(p.bs, 4 * units <= warps ? kFewLeast : 2 * units <= warps ? 2 * kFewLeast : kFewChunk);
   p.max_query = max_query_len;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  typedef __nv_bfloat16 bf16;
   CUtensorMap qmap, kmap;
   pkv_status mst;
   if (p.tensor && !only_few) {
     if ((mst = rows_map(&qmap, p.q, p.T, p.Hq, D, p.G, p.tile_tok)) != PKV_OK) return mst;
-    if ((mst = pool_map(&kmap, p.kc, p.num_blocks, p.bs, p.Hkv, D)) != PKV_OK) return mst;
+    if ((mst = pool_map(&kmap, p.kc, p.num_blocks, p.bs, p.Hkv, D, f8)) != PKV_OK) return mst;
   }
   cudaError_t e;
   if (f8)
-    e = launch<bf16, __nv_fp8_e4m3, 128, DotFp8>(p, only_few, one_tile, sms, s);
-  else if (dtype == PKV_DTYPE_BF16)
-    e = D == 128 ? launch<bf16, bf16, 128, DotBf16<128>>(p, only_few, one_tile, sms, s)
-                 : launch<bf16, bf16, 64, DotBf16<64>>(p, only_few, one_tile, sms, s);
+    e = launch<DotFp8>(p, one_tile, sms, s);
+  else if (p.tensor)
+    e = D == 128 ? launch<DotBf16<128>>(p, one_tile, sms, s) : launch<DotBf16<64>>(p, one_tile, sms, s);
   else
-    e = D == 128 ? launch<float, float, 128, DotF32<128>>(p, only_few, one_tile, sms, s)
-                 : launch<float, float, 64, DotF32<64>>(p, only_few, one_tile, sms, s);
-  if (e == cudaSuccess && p.tensor && !only_few) e = launch_scores_mma(p, D, qmap, kmap, sms, s);
+    e = D == 128 ? launch<DotF32<128>>(p, one_tile, sms, s) : launch<DotF32<64>>(p, one_tile, sms, s);
+  if (e == cudaSuccess && !only_few)
+    e = p.tensor ? launch_scores_mma(p, D, f8, qmap, kmap, sms, s)
+                 : D == 128 ? launch_other<128>(p, sms, s) : launch_other<64>(p, sms, s);
   if (e != cudaSuccess) return cuda_error(e, "paged_attention_scores launch");
   return PKV_OK;
 }

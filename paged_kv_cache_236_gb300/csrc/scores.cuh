@@ -2,6 +2,9 @@
 // sequence's work and the queues the kernels take it from.
 #pragma once
 
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 
@@ -16,9 +19,9 @@ constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
 // through all of them (8 key tiles each, below 1 us a tile), and the waits of
 // the roles that stand by, up to two items long, end after 2 s.
 constexpr int kMaxRowTiles = 1 << 16;
-constexpr int kChunk = 256;   // keys of a work unit (other rows)
+constexpr int kChunk = 256;   // keys of a work unit (more rows in fp32)
 enum { kFew = 1, kTensor = 2, kOther = 3 };
-constexpr int kRowGroup = 8;  // rows of a work unit (other rows)
+constexpr int kRowGroup = 8;  // rows of a work unit (more rows in fp32)
 
 // Offsets of each sequence's work, as prefix sums: the unit queues of the
 // kernels below (few-row stats and columns; other rows' stats and columns),
@@ -86,9 +89,21 @@ __device__ __forceinline__ void st_release(int* p, int v) {
   asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-// The tensor-core kernel for bf16 sequences of more than kFewRows rows
-// (scores_mma.cu).
-cudaError_t launch_scores_mma(const ScoreParams& p, int D, const CUtensorMap& qmap, const CUtensorMap& kmap, int sms,
-                              cudaStream_t s);
+// Two E4M3 codes as an fp16 pair, exactly.
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+// A bf16 pair as an fp16 pair: the 8 bits of mantissa fit; magnitudes above
+// 65504 become infinite, those below 2^-14 are off by at most 2^-25.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  const __half2 h = __floats2half2_rn(bf16_lo(w), bf16_hi(w));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The tensor-core kernel for sequences of more than kFewRows rows of bf16
+// queries (scores_mma.cu); f8: FP8 pools.
+cudaError_t launch_scores_mma(const ScoreParams& p, int D, bool f8, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                              int sms, cudaStream_t s);
 
 }  // namespace pkv

@@ -1,7 +1,8 @@
 // Attention weight paid to each cached token, for sequences of many rows
-// (prefill chunks, observation windows, wide verify steps) in bf16:
-// tcgen05.mma with TMEM accumulators.  paged_attention_scores (scores.cu)
-// plans the work; this kernel does both passes over the keys.
+// (prefill chunks, observation windows, wide verify steps) of bf16 queries,
+// over bf16 or FP8 pools: tcgen05.mma with TMEM accumulators.
+// paged_attention_scores (scores.cu) plans the work; this kernel does both
+// passes over the keys.
 //
 // With z[r][j] = scale * log2(e) * q_r . k_j for the rows r of one kv head:
 //   stats items    rows on M:  S = Q K^T, (max, sum of exp2) of each row over
@@ -26,7 +27,11 @@
 // keys' sums in shared memory between row tiles).  The Q tile is resident, the
 // range's K tiles are streamed.
 //
-// Roles (416 threads, one CTA per SM, persistent):
+// FP8 pools: K's tiles of codes come to a ring of their own and become fp16
+// tiles, exactly, which the MMAs read; the resident Q tile becomes fp16 in
+// place.
+//
+// Roles (416 threads, 672 with the converters; one CTA per SM, persistent):
 //   warps 0, 3   producers, one per 64-column half of the tiles (one warp's
 //                2 KB boxes go at about 100 cycles each): K by one
 //                {64, 1, block_size, 1} box per physical block, Q by one
@@ -43,9 +48,12 @@
 //   warp 12      closes stats items: when both groups have written an item's
 //                partials it counts the item, and the head's last one makes it
 //                combine the rows' lse and announce them; the groups go on
-//                without a fence or a wait for the count.
+//                without a fence or a wait for the count;
+//   warps 13-20  (FP8) converters: 8 warps took 139 us where 4 took 148 (prompt
+//                windows) and 227 us against 237 (verify batch).
 // Shared memory: 2 resident tiles and a 4-stage ring of streamed ones (192 KB
-// at head_dim 128).  TMEM: four 128-column accumulators.
+// at head_dim 128), or a 3-stage ring and two tiles of codes (as much).  TMEM:
+// four 128-column accumulators.
 //
 // The wait for a head's lse ends: every stats item it depends on was taken
 // from the queue before the column item, by a CTA that works its items off in
@@ -62,9 +70,10 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreadsMma = 416;
+constexpr int kThreadsMma = 416, kConverters = 256;
 constexpr int kTile = 128;      // rows or keys of a tile
-constexpr int kStages = 4;      // streamed tiles
+constexpr int kCodeTiles = 2;   // streamed tiles of codes, not yet converted (FP8)
+constexpr int kCodeBytes = kTile * 128;
 // Accumulators: two for each epilogue group, counted by group.  A ring that
 // both groups share would let a group that has few K tiles (row tiles that see
 // one K tile of the range all belong to group 0) test a barrier whose previous
@@ -73,12 +82,11 @@ constexpr int kStages = 4;      // streamed tiles
 constexpr int kGroupAccs = 2;
 constexpr int kAccs = 2 * kGroupAccs;
 constexpr int kItems = 2;       // item ring
+constexpr int kMaxStages = 4;
 constexpr int kRangeTiles = kTcRange / kTile;
 constexpr int kIds = kTcRange / 8;  // block ids of a range, at most
 constexpr int kHeldSeqs = 256;  // sequences whose plan is kept in shared memory
 constexpr float kRaise = 8.0f;  // log2 units a row maximum may exceed its reference by
-constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false);
-constexpr uint32_t kIdesc16 = idesc_bf16(128, 16, false, false);  // N = 16; N / 8 sits at bit 17
 
 enum { kDone = 0, kStats = 1, kCols = 2 };
 
@@ -91,18 +99,27 @@ struct alignas(16) Item {
 };
 
 struct Bars {
-  uint64_t x_full[2][2], x_empty[2];             // resident tile [buffer][half]
-  uint64_t y_full[kStages][2], y_empty[kStages];  // streamed tile [stage][half]
+  uint64_t x_full[2][2], x_empty[2];                // resident tile [buffer][half]
+  uint64_t y_full[kMaxStages][2], y_empty[kMaxStages];  // streamed tile [stage][half] (FP8: [stage][0], converted)
+  uint64_t x_conv[2];                               // FP8: resident tile converted
+  uint64_t c_full[kCodeTiles], c_empty[kCodeTiles];  // FP8: streamed tile of codes
   uint64_t acc_full[kAccs], acc_empty[kAccs];
   uint64_t item_full[kItems], item_empty[kItems], item_closed[kItems];
 };
 
-template <int D>
+template <int D, bool F8>
 struct Lay {
+  static constexpr int kStages = F8 ? 3 : kMaxStages;  // streamed tiles
+  static constexpr int kThreads = kThreadsMma + (F8 ? kConverters : 0);
+  // fp16 operands: the types' bits 7-12 are zero; N / 8 sits at bit 17
+  static constexpr uint32_t kTypes = F8 ? ~0x1F80u : ~0u;
+  static constexpr uint32_t kIdesc128 = idesc_bf16(128, 128, false, false) & kTypes;
+  static constexpr uint32_t kIdesc16 = idesc_bf16(128, 16, false, false) & kTypes;
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kXOff = 0;
   static constexpr int kYOff = 2 * kTileBytes;
-  static constexpr int kItemOff = kYOff + kStages * kTileBytes;
+  static constexpr int kCodeOff = kYOff + kStages * kTileBytes;
+  static constexpr int kItemOff = kCodeOff + (F8 ? kCodeTiles * kCodeBytes : 0);
   static constexpr int kIdOff = kItemOff + kItems * (int)sizeof(Item);
   static constexpr int kLseOff = kIdOff + kItems * kIds * 4;   // [group][2][128] negated lse
   static constexpr int kSumOff = kLseOff + 2 * 2 * kTile * 4;  // [tile of the range][128] column sums
@@ -111,7 +128,7 @@ struct Lay {
   static constexpr int kSmem = kPlanOff + kHeldSeqs * (int)sizeof(SeqPlan) + 2 * (kHeldSeqs + 1) * 8 + 1024;
 };
 static_assert(sizeof(Item) % 16 == 0, "item slot");
-static_assert(Lay<128>::kSmem <= 232448, "shared memory per CTA");
+static_assert(Lay<128, false>::kSmem <= 232448 && Lay<128, true>::kSmem <= 232448, "shared memory per CTA");
 
 __device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
@@ -137,12 +154,13 @@ __device__ __forceinline__ void add_weights(const uint32_t (&z)[32], const float
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreParams p,
-                                                                    const __grid_constant__ CUtensorMap qmap,
-                                                                    const __grid_constant__ CUtensorMap kmap) {
-  using Y = Lay<D>;
-  constexpr int kHalves = D / 64;
+template <int D, bool F8>
+__global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(const ScoreParams p,
+                                                                             const __grid_constant__ CUtensorMap qmap,
+                                                                             const __grid_constant__ CUtensorMap kmap) {
+  using Y = Lay<D, F8>;
+  constexpr int kHalves = D / 64, kStages = Y::kStages;
+  constexpr int kYHalves = F8 ? 1 : kHalves;  // barriers that announce a streamed tile
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* bars = reinterpret_cast<Bars*>(smem + Y::kBarOff);
@@ -158,8 +176,15 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
       mbar_init(&bars->x_empty[b], 1);
     }
     for (int i = 0; i < kStages; ++i) {
-      for (int h = 0; h < 2; ++h) mbar_init(&bars->y_full[i][h], 1);
+      for (int h = 0; h < 2; ++h) mbar_init(&bars->y_full[i][h], F8 ? kConverters : 1);
       mbar_init(&bars->y_empty[i], 1);
+    }
+    if (F8) {
+      for (int b = 0; b < 2; ++b) mbar_init(&bars->x_conv[b], kConverters);
+      for (int i = 0; i < kCodeTiles; ++i) {
+        mbar_init(&bars->c_full[i], 1);
+        mbar_init(&bars->c_empty[i], kConverters);
+      }
     }
     for (int i = 0; i < kAccs; ++i) {
       mbar_init(&bars->acc_full[i], 1);
@@ -167,7 +192,8 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      mbar_init(&bars->item_empty[i], kHalves + 1 + 8 + 1);  // producers, the MMA thread, the groups' warps, the closer
+      // producers, the MMA thread, the groups' warps, the closer, the converters' warps
+      mbar_init(&bars->item_empty[i], kHalves + 1 + 8 + 1 + (F8 ? kConverters / 32 : 0));
       mbar_init(&bars->item_closed[i], 256);
     }
     fence_mbar_init();
@@ -321,7 +347,20 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
           ++nx;
 #pragma unroll
           for (int i = 0; i < kRangeTiles; ++i) {
-            if (i < ny && ok) {
+            if (F8) {  // the first producer's: a key's codes are one 128-byte row
+              if (half == 0 && i < ny && ok) {
+                const int c = g % kCodeTiles;
+                ok = wait_all(&bars->c_empty[c], ((g / kCodeTiles) & 1) ^ 1, wc);
+                if (ok) {
+                  if (lane == 0) mbar_arrive_expect_tx(&bars->c_full[c], kCodeBytes);
+                  __syncwarp();
+                  if (lane < nb_per_tile)
+                    tma_load_4d(smem + Y::kCodeOff + c * kCodeBytes + lane * p.bs * 128, &kmap, &bars->c_full[c], 0,
+                                im.h, 0, id[i]);
+                  ++g;
+                }
+              }
+            } else if (i < ny && ok) {
               const int st = g % kStages;
               ok = wait_all(&bars->y_empty[st], ((g / kStages) & 1) ^ 1, wc);
               if (ok) {
@@ -338,7 +377,10 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
       }
       // none of this warp's copies may be in flight when the CTA ends (after
       // an ordinary end the MMA thread has waited for all of them)
-      for (int j = max(0, g - kStages); j < g; ++j) wait_all(&bars->y_full[j % kStages][half], (j / kStages) & 1, wc);
+      if (F8)
+        for (int j = max(0, g - kCodeTiles); j < g; ++j) wait_all(&bars->c_full[j % kCodeTiles], (j / kCodeTiles) & 1, wc);
+      else
+        for (int j = max(0, g - kStages); j < g; ++j) wait_all(&bars->y_full[j % kStages][half], (j / kStages) & 1, wc);
       for (int j = max(0, nx - 2); j < nx; ++j) wait_all(&bars->x_full[j & 1][half], (j >> 1) & 1, wc);
     }
   } else if (warp == 1) {
@@ -359,17 +401,20 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
           const int ny = tiles_seen(p, im, tile);
           if (ny == 0) continue;
           const int xb = nx & 1;
-          for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
+          if (F8)
+            ok = mbar_wait(&bars->x_conv[xb], (nx >> 1) & 1, wc);
+          else
+            for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
           if (!ok) break;
           ++nx;
           const uint64_t dx = desc_add(dx0, xb * Y::kTileBytes);
           // stats: rows on M; columns: rows on N, a multiple of 16 of them
           const int nr = (min(tile_rows, im.rows - tile * tile_rows) + 15) & ~15;
-          const uint32_t idesc = im.type == kStats ? kIdesc128 : kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
+          const uint32_t idesc = im.type == kStats ? Y::kIdesc128 : Y::kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
           for (int i = 0; i < ny; ++i, ++g) {
             const int st = g % kStages, wg = i & 1, k = wg == 0 ? na[0] : na[1];
             const int acc = wg * kGroupAccs + k % kGroupAccs;
-            for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->y_full[st][h], (g / kStages) & 1, wc);
+            for (int h = 0; h < kYHalves && ok; ++h) ok = mbar_wait(&bars->y_full[st][h], (g / kStages) & 1, wc);
             if (!ok || !mbar_wait(&bars->acc_empty[acc], ((k / kGroupAccs) & 1) ^ 1, wc)) {
               ok = false;
               break;
@@ -435,6 +480,61 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
       __threadfence();
       __syncwarp();
       if (lane == 0) st_release(ready + sh, 1);
+    }
+  } else if (F8 && warp >= 13) {
+    // ================================================================ converters
+    const int c = threadIdx.x - 13 * 32;
+    int g = 0, nx = 0;  // streamed and resident tiles so far
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      const int sl = it % kItems;
+      if (!wait_all(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
+      const Item im = items[sl];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
+      if (im.type == kDone) break;
+      for (int tile = im.tile0; tile < im.tile0 + im.tiles && ok; ++tile) {
+        const int ny = tiles_seen(p, im, tile);
+        if (ny == 0) continue;
+        // q, in place: whatever place the swizzle gave a value
+        const int xb = nx & 1;
+        for (int h = 0; h < kHalves && ok; ++h) ok = wait_all(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
+        if (!ok) break;
+        uint4* q = reinterpret_cast<uint4*>(smem + Y::kXOff + xb * Y::kTileBytes);
+#pragma unroll 4
+        for (int i = c; i < Y::kTileBytes / 16; i += kConverters) {
+          const uint4 v = q[i];
+          q[i] = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->x_conv[xb]);
+        ++nx;
+        for (int i = 0; i < ny; ++i, ++g) {
+          const int st = g % kStages, ct = g % kCodeTiles;
+          ok = wait_all(&bars->y_empty[st], ((g / kStages) & 1) ^ 1, wc) &&
+               wait_all(&bars->c_full[ct], (g / kCodeTiles) & 1, wc);
+          if (!ok) break;
+          // 16 codes of a key at a time, to the swizzled halves the MMAs read
+          const uint4* src = reinterpret_cast<const uint4*>(smem + Y::kCodeOff + ct * kCodeBytes);
+          uint8_t* dst = smem + Y::kYOff + st * Y::kTileBytes;
+#pragma unroll 4
+          for (int k = 0; k < kCodeBytes / 16 / kConverters; ++k) {
+            const int at = k * kConverters + c, key = at >> 3, ch = at & 7;
+            const uint4 v = src[at];
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = codes_to_f16(in[e >> 1] >> 16 * (e & 1) & 0xffffu);
+            uint8_t* row = dst + (ch >> 2) * kHalf + key * 128;
+            const int j0 = (ch & 3) * 2;
+            *reinterpret_cast<uint4*>(row + ((j0 ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(row + (((j0 + 1) ^ (key & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->y_full[st][0]);
+          mbar_arrive(&bars->c_empty[ct]);
+        }
+      }
     }
   } else {
     // ================================================================ epilogue groups
@@ -593,7 +693,7 @@ __global__ void __launch_bounds__(kThreadsMma, 1) scores_mma_kernel(const ScoreP
   if (warp == 1) tmem_dealloc(tmem, kAccs * 128);
 }
 
-template <int D>
+template <int D, bool F8>
 cudaError_t launch_t(const ScoreParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, int sms, cudaStream_t s) {
   static unsigned long long done_mask = 0;
   int dev = 0;
@@ -601,18 +701,19 @@ cudaError_t launch_t(const ScoreParams& p, const CUtensorMap& qmap, const CUtens
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(scores_mma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D>::kSmem);
+    e = cudaFuncSetAttribute(scores_mma_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, F8>::kSmem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
   }
-  return launch_pdl(scores_mma_kernel<D>, dim3(sms), dim3(kThreadsMma), Lay<D>::kSmem, s, p, qmap, kmap);
+  return launch_pdl(scores_mma_kernel<D, F8>, dim3(sms), dim3(Lay<D, F8>::kThreads), Lay<D, F8>::kSmem, s, p, qmap, kmap);
 }
 
 }  // namespace
 
-cudaError_t launch_scores_mma(const ScoreParams& p, int D, const CUtensorMap& qmap, const CUtensorMap& kmap, int sms,
-                              cudaStream_t s) {
-  return D == 64 ? launch_t<64>(p, qmap, kmap, sms, s) : launch_t<128>(p, qmap, kmap, sms, s);
+cudaError_t launch_scores_mma(const ScoreParams& p, int D, bool f8, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                              int sms, cudaStream_t s) {
+  if (f8) return launch_t<128, true>(p, qmap, kmap, sms, s);
+  return D == 64 ? launch_t<64, false>(p, qmap, kmap, sms, s) : launch_t<128, false>(p, qmap, kmap, sms, s);
 }
 
 }  // namespace pkv

@@ -155,13 +155,14 @@ def test_many_queries(n, L, dtype):
     b.check(b.run(), before)
 
 
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (32, 2, 32), (8, 8, 64)])
-def test_prompts_from_the_first_token(Hq, Hkv, bs):
+def test_prompts_from_the_first_token(Hq, Hkv, bs, f8):
     """No context before the queries: row tiles that see one, two, ... K tiles
     of a range, in odd and even numbers, and short sequences of one K tile in a
     row; over and over, since only the timing of the roles could go wrong."""
     lens = [700, 128, 90, 33, 127, 385, 64, 1100, 100, 100, 1]
-    b = Batch(Hq + bs, lens, lens, Hq, Hkv, 128, bs)
+    b = Batch(Hq + bs, lens, lens, Hq, Hkv, 128, bs, f8=f8)
     before = b.old.clone()
     first = b.run(out=b.old.clone())
     b.check(first, before)
