@@ -70,19 +70,21 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreadsMma = 416, kConverters = 256;
+constexpr int kFirstConverter = 14;  // warp
+constexpr int kThreadsMma = kFirstConverter * 32, kConverters = 256;
 constexpr int kTile = 128;      // rows or keys of a tile
-constexpr int kCodeTiles = 2;   // streamed tiles of codes, not yet converted (FP8)
-constexpr int kCodeBytes = kTile * 128;
-// Accumulators: two for each epilogue group, counted by group.  A ring that
-// both groups share would let a group that has few K tiles (row tiles that see
-// one K tile of the range all belong to group 0) test a barrier whose previous
-// phase is not complete, and take the phase before that one, of the same
-// parity, for its own.
-constexpr int kGroupAccs = 2;
-constexpr int kAccs = 2 * kGroupAccs;
+constexpr int kCodeBytes = kTile * 128;  // an FP8 tile
+// Each of the two epilogue groups has its own issuing warp, two streamed tiles
+// and two accumulators: slots 2 w and 2 w + 1, in turn.  Every barrier's phases
+// are so waited for in order.  Slots that both groups share would let a group
+// that has few K tiles (row tiles that see one K tile of the range all belong to
+// group 0) test a barrier whose previous phase is not complete, and take the
+// phase before that one, of the same parity, for its own.
+constexpr int kGroupSlots = 2;
+constexpr int kSlots = 2 * kGroupSlots;
+__device__ __forceinline__ int slot_of(int wg, int k) { return wg * kGroupSlots + k % kGroupSlots; }
+__device__ __forceinline__ uint32_t phase_of(int k) { return k / kGroupSlots & 1; }
 constexpr int kItems = 2;       // item ring
-constexpr int kMaxStages = 4;
 constexpr int kRangeTiles = kTcRange / kTile;
 constexpr int kIds = kTcRange / 8;  // block ids of a range, at most
 constexpr int kHeldSeqs = 256;  // sequences whose plan is kept in shared memory
@@ -100,16 +102,14 @@ struct alignas(16) Item {
 
 struct Bars {
   uint64_t x_full[2][2], x_empty[2];                // resident tile [buffer][half]
-  uint64_t y_full[kMaxStages][2], y_empty[kMaxStages];  // streamed tile [stage][half] (FP8: [stage][0], converted)
-  uint64_t x_conv[2];                               // FP8: resident tile converted
-  uint64_t c_full[kCodeTiles], c_empty[kCodeTiles];  // FP8: streamed tile of codes
-  uint64_t acc_full[kAccs], acc_empty[kAccs];
+  uint64_t y_full[kSlots][2], y_empty[kSlots];      // streamed tile [slot][half] (FP8: [slot][0], converted)
+  uint64_t x_conv[2], c_full[kSlots];               // FP8: resident tile converted; a slot's codes
+  uint64_t acc_full[kSlots], acc_empty[kSlots];
   uint64_t item_full[kItems], item_empty[kItems], item_closed[kItems];
 };
 
 template <int D, bool F8>
 struct Lay {
-  static constexpr int kStages = F8 ? 3 : kMaxStages;  // streamed tiles
   static constexpr int kThreads = kThreadsMma + (F8 ? kConverters : 0);
   // fp16 operands: the types' bits 7-12 are zero; N / 8 sits at bit 17
   static constexpr uint32_t kTypes = F8 ? ~0x1F80u : ~0u;
@@ -118,8 +118,7 @@ struct Lay {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kXOff = 0;
   static constexpr int kYOff = 2 * kTileBytes;
-  static constexpr int kCodeOff = kYOff + kStages * kTileBytes;
-  static constexpr int kItemOff = kCodeOff + (F8 ? kCodeTiles * kCodeBytes : 0);
+  static constexpr int kItemOff = kYOff + kSlots * kTileBytes;
   static constexpr int kIdOff = kItemOff + kItems * (int)sizeof(Item);
   static constexpr int kLseOff = kIdOff + kItems * kIds * 4;   // [group][2][128] negated lse
   static constexpr int kSumOff = kLseOff + 2 * 2 * kTile * 4;  // [tile of the range][128] column sums
@@ -159,7 +158,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
                                                                              const __grid_constant__ CUtensorMap qmap,
                                                                              const __grid_constant__ CUtensorMap kmap) {
   using Y = Lay<D, F8>;
-  constexpr int kHalves = D / 64, kStages = Y::kStages;
+  constexpr int kHalves = D / 64;
   constexpr int kYHalves = F8 ? 1 : kHalves;  // barriers that announce a streamed tile
   extern __shared__ __align__(16) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -173,33 +172,26 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       for (int h = 0; h < 2; ++h) mbar_init(&bars->x_full[b][h], 1);
-      mbar_init(&bars->x_empty[b], 1);
+      mbar_init(&bars->x_empty[b], 2);  // the issuing warps
+      mbar_init(&bars->x_conv[b], kConverters);
     }
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
       for (int h = 0; h < 2; ++h) mbar_init(&bars->y_full[i][h], F8 ? kConverters : 1);
       mbar_init(&bars->y_empty[i], 1);
-    }
-    if (F8) {
-      for (int b = 0; b < 2; ++b) mbar_init(&bars->x_conv[b], kConverters);
-      for (int i = 0; i < kCodeTiles; ++i) {
-        mbar_init(&bars->c_full[i], 1);
-        mbar_init(&bars->c_empty[i], kConverters);
-      }
-    }
-    for (int i = 0; i < kAccs; ++i) {
+      mbar_init(&bars->c_full[i], 1);
       mbar_init(&bars->acc_full[i], 1);
       mbar_init(&bars->acc_empty[i], 4);  // the four warps of the group that read it
     }
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&bars->item_full[i], 1);
-      // producers, the MMA thread, the groups' warps, the closer, the converters' warps
-      mbar_init(&bars->item_empty[i], kHalves + 1 + 8 + 1 + (F8 ? kConverters / 32 : 0));
+      // producers, the issuing warps, the groups' warps, the closer, the converters' warps
+      mbar_init(&bars->item_empty[i], kHalves + 2 + 8 + 1 + (F8 ? kConverters / 32 : 0));
       mbar_init(&bars->item_closed[i], 256);
     }
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, kAccs * 128);
+    tmem_alloc(tmem_slot, kSlots * 128);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -319,7 +311,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
       }
       const int nb_per_tile = kTile / p.bs;
       const int q_bytes = p.tile_tok * p.G * 128;  // one 64-column half of a row tile
-      int g = 0, nx = 0;  // streamed and resident tiles so far
+      int ny0 = 0, ny1 = 0, nx = 0;  // streamed tiles of either group and resident tiles so far
       bool ok = true;
       for (int it = 0; ok; ++it) {
         const int sl = it % kItems;
@@ -347,101 +339,91 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
           ++nx;
 #pragma unroll
           for (int i = 0; i < kRangeTiles; ++i) {
-            if (F8) {  // the first producer's: a key's codes are one 128-byte row
-              if (half == 0 && i < ny && ok) {
-                const int c = g % kCodeTiles;
-                ok = wait_all(&bars->c_empty[c], ((g / kCodeTiles) & 1) ^ 1, wc);
-                if (ok) {
-                  if (lane == 0) mbar_arrive_expect_tx(&bars->c_full[c], kCodeBytes);
-                  __syncwarp();
-                  if (lane < nb_per_tile)
-                    tma_load_4d(smem + Y::kCodeOff + c * kCodeBytes + lane * p.bs * 128, &kmap, &bars->c_full[c], 0,
-                                im.h, 0, id[i]);
-                  ++g;
-                }
-              }
-            } else if (i < ny && ok) {
-              const int st = g % kStages;
-              ok = wait_all(&bars->y_empty[st], ((g / kStages) & 1) ^ 1, wc);
+            // FP8: the first producer's alone, a key's codes are one 128-byte row
+            if (i < ny && ok && (!F8 || half == 0)) {
+              int& k = i & 1 ? ny1 : ny0;
+              const int st = slot_of(i & 1, k);
+              ok = wait_all(&bars->y_empty[st], phase_of(k) ^ 1, wc);
               if (ok) {
-                if (lane == 0) mbar_arrive_expect_tx(&bars->y_full[st][half], kTile * 128);
+                uint64_t* full = F8 ? &bars->c_full[st] : &bars->y_full[st][half];
+                if (lane == 0) mbar_arrive_expect_tx(full, kTile * 128);
                 __syncwarp();
                 if (lane < nb_per_tile)
-                  tma_load_4d(smem + Y::kYOff + st * Y::kTileBytes + half * kHalf + lane * p.bs * 128, &kmap,
-                              &bars->y_full[st][half], half * 64, im.h, 0, id[i]);
-                ++g;
+                  tma_load_4d(smem + Y::kYOff + st * Y::kTileBytes + half * kHalf + lane * p.bs * 128, &kmap, full,
+                              half * 64, im.h, 0, id[i]);
+                ++k;
               }
             }
           }
         }
       }
       // none of this warp's copies may be in flight when the CTA ends (after
-      // an ordinary end the MMA thread has waited for all of them)
-      if (F8)
-        for (int j = max(0, g - kCodeTiles); j < g; ++j) wait_all(&bars->c_full[j % kCodeTiles], (j / kCodeTiles) & 1, wc);
-      else
-        for (int j = max(0, g - kStages); j < g; ++j) wait_all(&bars->y_full[j % kStages][half], (j / kStages) & 1, wc);
+      // an ordinary end the issuing warps have waited for all of them)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int n = w ? ny1 : ny0;
+        for (int k = max(0, n - kGroupSlots); k < n; ++k)
+          wait_all(F8 ? &bars->c_full[slot_of(w, k)] : &bars->y_full[slot_of(w, k)][half], phase_of(k), wc);
+      }
       for (int j = max(0, nx - 2); j < nx; ++j) wait_all(&bars->x_full[j & 1][half], (j >> 1) & 1, wc);
     }
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 13) {
     // ================================================================ MMA issuer
-    if (lane == 0) {
-      const uint64_t dx0 = desc_k(smem_base + Y::kXOff), dy0 = desc_k(smem_base + Y::kYOff);
-      int g = 0, nx = 0;       // streamed and resident tiles so far
-      int na[2] = {0, 0};      // accumulators of each group so far
-      bool ok = true;
-      for (int it = 0; ok; ++it) {
-        const int sl = it % kItems;
-        if (!mbar_wait(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
-        const Item im = items[sl];
-        mbar_arrive(&bars->item_empty[sl]);
-        if (im.type == kDone) break;
-        const int tile_rows = p.tile_tok * p.G;
-        for (int tile = im.tile0; tile < im.tile0 + im.tiles && ok; ++tile) {
-          const int ny = tiles_seen(p, im, tile);
-          if (ny == 0) continue;
-          const int xb = nx & 1;
-          if (F8)
-            ok = mbar_wait(&bars->x_conv[xb], (nx >> 1) & 1, wc);
-          else
-            for (int h = 0; h < kHalves && ok; ++h) ok = mbar_wait(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
+    // The warp stays together and only the issue itself is one lane's, so that
+    // descriptors and counters are warp-uniform.
+    const uint64_t dx0 = desc_k(smem_base + Y::kXOff), dy0 = desc_k(smem_base + Y::kYOff);
+    const bool issues = lane == 0;
+    const int wg = warp == 1 ? 0 : 1;
+    int k = 0, nx = 0;  // this group's tiles and resident tiles so far
+    bool ok = true;
+    for (int it = 0; ok; ++it) {
+      const int sl = it % kItems;
+      if (!wait_all(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
+      const Item im = items[sl];
+      __syncwarp();
+      if (issues) mbar_arrive(&bars->item_empty[sl]);
+      if (im.type == kDone) break;
+      const int tile_rows = p.tile_tok * p.G;
+      for (int tile = im.tile0; tile < im.tile0 + im.tiles && ok; ++tile) {
+        const int ny = tiles_seen(p, im, tile);
+        if (ny == 0) continue;
+        const int xb = nx & 1;
+        if (F8)
+          ok = wait_all(&bars->x_conv[xb], (nx >> 1) & 1, wc);
+        else
+          for (int h = 0; h < kHalves && ok; ++h) ok = wait_all(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
+        if (!ok) break;
+        ++nx;
+        const uint64_t dx = desc_add(dx0, xb * Y::kTileBytes);
+        // stats: rows on M; columns: rows on N, a multiple of 16 of them
+        const int nr = (min(tile_rows, im.rows - tile * tile_rows) + 15) & ~15;
+        const uint32_t idesc = im.type == kStats ? Y::kIdesc128 : Y::kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
+        // the tile is waited for also where the group has no K tile of it, so that
+        // the arrival counts for its own phase
+        if (wg >= ny && issues) mbar_arrive(&bars->x_empty[xb]);
+        for (int i = wg; i < ny; i += 2, ++k) {
+          const int st = slot_of(wg, k);
+          for (int h = 0; h < kYHalves && ok; ++h) ok = wait_all(&bars->y_full[st][h], phase_of(k), wc);
+          ok = ok && wait_all(&bars->acc_empty[st], phase_of(k) ^ 1, wc);
           if (!ok) break;
-          ++nx;
-          const uint64_t dx = desc_add(dx0, xb * Y::kTileBytes);
-          // stats: rows on M; columns: rows on N, a multiple of 16 of them
-          const int nr = (min(tile_rows, im.rows - tile * tile_rows) + 15) & ~15;
-          const uint32_t idesc = im.type == kStats ? Y::kIdesc128 : Y::kIdesc16 + ((uint32_t)(nr - 16) >> 3 << 17);
-          for (int i = 0; i < ny; ++i, ++g) {
-            const int st = g % kStages, wg = i & 1, k = wg == 0 ? na[0] : na[1];
-            const int acc = wg * kGroupAccs + k % kGroupAccs;
-            for (int h = 0; h < kYHalves && ok; ++h) ok = mbar_wait(&bars->y_full[st][h], (g / kStages) & 1, wc);
-            if (!ok || !mbar_wait(&bars->acc_empty[acc], ((k / kGroupAccs) & 1) ^ 1, wc)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint64_t dy = desc_add(dy0, st * Y::kTileBytes);
-            const uint64_t da = im.type == kStats ? dx : dy, db = im.type == kStats ? dy : dx;
+          tc_fence_after();
+          const uint64_t dy = desc_add(dy0, st * Y::kTileBytes);
+          const uint64_t da = im.type == kStats ? dx : dy, db = im.type == kStats ? dy : dx;
+          if (issues) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              umma_bf16(tmem + acc * 128, desc_add(da, (kk >> 2) * kHalf + (kk & 3) * 32),
+              umma_bf16(tmem + st * 128, desc_add(da, (kk >> 2) * kHalf + (kk & 3) * 32),
                         desc_add(db, (kk >> 2) * kHalf + (kk & 3) * 32), idesc, kk > 0 ? 1u : 0u);
-            umma_commit(&bars->acc_full[acc]);
-            if (wg == 0)
-              ++na[0];
-            else
-              ++na[1];
+            umma_commit(&bars->acc_full[st]);
             umma_commit(&bars->y_empty[st]);
-            if (i == ny - 1) umma_commit(&bars->x_empty[xb]);
+            if (i + 2 >= ny) umma_commit(&bars->x_empty[xb]);
           }
+          __syncwarp();
         }
       }
-      // leaving: the MMAs already issued finish before TMEM is freed
-#pragma unroll
-      for (int w = 0; w < 2; ++w)
-        for (int j = max(0, na[w] - kGroupAccs); j < na[w]; ++j)
-          mbar_wait(&bars->acc_full[w * kGroupAccs + j % kGroupAccs], (j / kGroupAccs) & 1, wc);
     }
+    // leaving: the MMAs already issued finish before TMEM is freed
+    for (int j = max(0, k - kGroupSlots); j < k; ++j) wait_all(&bars->acc_full[slot_of(wg, j)], phase_of(j), wc);
     __syncwarp();
   } else if (warp == 12) {
     // ================================================================ closer
@@ -481,10 +463,10 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
       __syncwarp();
       if (lane == 0) st_release(ready + sh, 1);
     }
-  } else if (F8 && warp >= 13) {
+  } else if (F8 && warp >= kFirstConverter) {
     // ================================================================ converters
-    const int c = threadIdx.x - 13 * 32;
-    int g = 0, nx = 0;  // streamed and resident tiles so far
+    const int c = threadIdx.x - kFirstConverter * 32;
+    int ny0 = 0, ny1 = 0, nx = 0;  // streamed tiles of either group and resident tiles so far
     bool ok = true;
     for (int it = 0; ok; ++it) {
       const int sl = it % kItems;
@@ -509,22 +491,31 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
         fence_proxy_async_smem();
         mbar_arrive(&bars->x_conv[xb]);
         ++nx;
-        for (int i = 0; i < ny; ++i, ++g) {
-          const int st = g % kStages, ct = g % kCodeTiles;
-          ok = wait_all(&bars->y_empty[st], ((g / kStages) & 1) ^ 1, wc) &&
-               wait_all(&bars->c_full[ct], (g / kCodeTiles) & 1, wc);
-          if (!ok) break;
-          // 16 codes of a key at a time, to the swizzled halves the MMAs read
-          const uint4* src = reinterpret_cast<const uint4*>(smem + Y::kCodeOff + ct * kCodeBytes);
+        for (int i = 0; i < ny; ++i) {
+          int& k = i & 1 ? ny1 : ny0;
+          const int st = slot_of(i & 1, k);
+          ok = wait_all(&bars->c_full[st], phase_of(k), wc);
+          // 16 codes of a key at a time, all read before any of the fp16 tile, which
+          // covers them, is written: to the swizzled halves the MMAs read
+          constexpr int kEach = kCodeBytes / 16 / kConverters;
           uint8_t* dst = smem + Y::kYOff + st * Y::kTileBytes;
-#pragma unroll 4
-          for (int k = 0; k < kCodeBytes / 16 / kConverters; ++k) {
-            const int at = k * kConverters + c, key = at >> 3, ch = at & 7;
-            const uint4 v = src[at];
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          const uint4* src = reinterpret_cast<const uint4*>(dst);
+          uint4 v[kEach];
+          if (ok) {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) v[e] = src[e * kConverters + c];
+          }
+          if (barrier_any(3, kConverters, !ok)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int e = 0; e < kEach; ++e) {
+            const int at = e * kConverters + c, key = at >> 3, ch = at & 7;
+            const uint32_t in[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
             uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = codes_to_f16(in[e >> 1] >> 16 * (e & 1) & 0xffffu);
+            for (int o = 0; o < 8; ++o) w[o] = codes_to_f16(in[o >> 1] >> 16 * (o & 1) & 0xffffu);
             uint8_t* row = dst + (ch >> 2) * kHalf + key * 128;
             const int j0 = (ch & 3) * 2;
             *reinterpret_cast<uint4*>(row + ((j0 ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -532,7 +523,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
           }
           fence_proxy_async_smem();
           mbar_arrive(&bars->y_full[st][0]);
-          mbar_arrive(&bars->c_empty[ct]);
+          ++k;
         }
       }
     }
@@ -546,7 +537,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
     float* sums = reinterpret_cast<float*>(smem + Y::kSumOff) + t;
     const int tile_rows = p.tile_tok * p.G;
     const f32x2 scale2 = pk2(p.scale_log2, p.scale_log2);
-    int na = 0, n_nl = 0;  // this group's accumulators and lse buffers so far
+    int k = 0, n_nl = 0;  // this group's tiles and lse buffers so far
     bool pending = false;
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
@@ -566,10 +557,10 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
         const bool live = __any_sync(0xffffffffu, valid);
         for (int i = wg; i < ny; i += 2) {
           if (pending) break;
-          const int acc = wg * kGroupAccs + na % kGroupAccs;
-          pending = !wait_all(&bars->acc_full[acc], (na / kGroupAccs) & 1, wc);
+          const int acc = slot_of(wg, k);
+          pending = !wait_all(&bars->acc_full[acc], phase_of(k), wc);
           if (pending) break;
-          ++na;
+          ++k;
           tc_fence_after();
           if (live) {
             const int kb = im.key0 + i * kTile;
@@ -643,13 +634,13 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
         const int first = tile * tile_rows, nr = min(tile_rows, im.rows - first);
         for (int i = wg; i < ny; i += 2) {
           if (pending) break;
-          const int acc = wg * kGroupAccs + na % kGroupAccs, j = im.key0 + i * kTile + t;
+          const int acc = slot_of(wg, k), j = im.key0 + i * kTile + t;
           const bool keeps = tile + 1 == end && j < im.L;  // this key's sum is complete: store it
           const bool adds = keeps && j < im.L - im.n && p.decay != 0.f;
           const float old = adds ? p.scores[at0 + j] : 0.f;
-          pending = !wait_all(&bars->acc_full[acc], (na / kGroupAccs) & 1, wc);
+          pending = !wait_all(&bars->acc_full[acc], phase_of(k), wc);
           if (pending) break;
-          ++na;
+          ++k;
           tc_fence_after();
           // rows below `from` do not see key j
           const int from = p.causal ? max(0, j - (im.L - im.n)) * p.G - first : 0;
@@ -690,7 +681,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kAccs * 128);
+  if (warp == 1) tmem_dealloc(tmem, kSlots * 128);
 }
 
 template <int D, bool F8>
