@@ -13,30 +13,39 @@
 //                  is a sum within the thread, and no weight leaves it.
 // Swapping the operands costs nothing: Q and K are both K-major tiles.
 //
-// What bounds it: the exponentials.  A 128 x 128 tile is 16384 of them, 1024
-// cycles of the SM's 16 a cycle, in each pass, next to 512 cycles of MMA; with
-// few rows (a verify window of 40) K's 32 KB a tile from HBM instead, twice.
+// What bounds it: the epilogue groups, with many rows.  A 128 x 128 tile is
+// 16384 exponentials in each pass and takes a group 1700 cycles, two groups at a
+// time, next to 512 cycles of MMA (64 queries of 4 heads on 8 sequences of 6000
+// to 16384 keys: 136 us; 128 queries: 241 us).  With few rows (a verify window
+// of 40) K's 32 KB a tile from HBM instead, twice: 5 queries of 8 heads on 32 x
+// 8192 keys 177 us, 6.1 TB/s.
+// One thread that issued both groups' MMAs took 1500 cycles a tile and held
+// them up (192 us and, 128 queries, 282 us; with its warp converged, so that
+// descriptors and counters are uniform, 267 us).  Not faster: four groups of one
+// accumulator each, with that one issuer (128 queries: 390 us); TMEM loads a chunk ahead of
+// their use (278 us against 241).
 // All stats items come before the column items.  Interleaved, a sequence's
 // column items a short way behind its stats items so that they find K in L2,
 // the waits for the lse cost more than the reads (verify batch 199 to 280 us
-// over distances of one to two items an SM, 194 us this way; prompt windows
-// 140 to 210 us against 120).
+// over distances of one to two items an SM, against 194 us of the time).  The
+// column items in reverse order, from the keys read last, wait for the last lse
+// (verify batch 200 us against 192, prompt windows 135 against 117).
 //
 // An item is a range of keys of a head against one row tile (stats) or all row
 // tiles that see any of it, one after the other (columns; each thread keeps its
 // keys' sums in shared memory between row tiles).  The Q tile is resident, the
 // range's K tiles are streamed.
 //
-// FP8 pools: K's tiles of codes come to a ring of their own and become fp16
-// tiles, exactly, which the MMAs read; the resident Q tile becomes fp16 in
-// place.
+// FP8 pools: a K tile's codes come to the slot that the converters make an fp16
+// tile of, exactly, which the MMAs read; the resident Q tile becomes fp16 in place.
 //
-// Roles (416 threads, 672 with the converters; one CTA per SM, persistent):
+// Roles (448 threads, 704 with the converters; one CTA per SM, persistent):
 //   warps 0, 3   producers, one per 64-column half of the tiles (one warp's
 //                2 KB boxes go at about 100 cycles each): K by one
 //                {64, 1, block_size, 1} box per physical block, Q by one
 //                {64, G, 128 / G} box;
-//   warp 1       TMEM allocation, and the thread that issues the MMAs;
+//   warps 1, 13  issue the MMAs, one for each epilogue group (warp 1 also
+//                allocates TMEM);
 //   warp 2       takes items from the queue, looks them up in the plan (in
 //                shared memory up to kHeldSeqs sequences), reads the range's
 //                block ids and publishes both in a ring (a producer
@@ -49,11 +58,11 @@
 //                partials it counts the item, and the head's last one makes it
 //                combine the rows' lse and announce them; the groups go on
 //                without a fence or a wait for the count;
-//   warps 13-20  (FP8) converters: 8 warps took 139 us where 4 took 148 (prompt
-//                windows) and 227 us against 237 (verify batch).
-// Shared memory: 2 resident tiles and a 4-stage ring of streamed ones (192 KB
-// at head_dim 128), or a 3-stage ring and two tiles of codes (as much).  TMEM:
-// four 128-column accumulators.
+//   warps 14-21  (FP8) converters: 8 warps took 139 us where 4 took 148 (prompt
+//                windows) and 227 us against 237 (verify batch); 130 and 204 us
+//                with two issuers.
+// Shared memory: 2 resident tiles and two streamed ones for either group (192 KB
+// at head_dim 128).  TMEM: four 128-column accumulators.
 //
 // The wait for a head's lse ends: every stats item it depends on was taken
 // from the queue before the column item, by a CTA that works its items off in
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
     }
     const int64_t n_stat = o_stat[p.B], n_all = n_stat + o_col[p.B];
     // Items are taken no earlier than a slot is free: with three slots and one
-    // item more in hand the SMs ended unevenly (prompt windows 145 us, not 120).
+    // item more in hand the SMs ended unevenly (prompt windows 145 us, 120 then).
     for (int it = 0;; ++it) {
       const int sl = it % kItems;
       if (!wait_all(&bars->item_empty[sl], ((it / kItems) & 1) ^ 1, wc)) break;
