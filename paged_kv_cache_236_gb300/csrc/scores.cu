@@ -162,7 +162,7 @@ __device__ __forceinline__ void plan_block(const ScoreParams& p) {
     v[kLse] = (int64_t)p.Hkv * sp.rows;
     if (sp.kind == kOther) {
       v[kStat] = work * ((sp.rows + kRowGroup - 1) / kRowGroup);
-      v[kCol] = work;
+      v[kCol] = (int64_t)p.Hkv * ((sp.L + kColTile - 1) / kColTile);
     } else if (sp.kind == kTensor) {
       v[kTcStat] = work * sp.tiles;
       v[kTcCol] = work;
@@ -906,159 +906,217 @@ __global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(co
 // ---------------------------------------------------------------------------
 // more rows in fp32
 // ---------------------------------------------------------------------------
-// Logits (times scale * log2 e) of a row group against one key: lane l
-// returns the logit of row l >> 2 (kRowGroup == 8 rows, 4 lanes each).
-template <int E>
-__device__ __forceinline__ float group_dot(const float (&k)[E], const float (&q)[kRowGroup][E], int lane) {
-  float a[kRowGroup];
-#pragma unroll
-  for (int r = 0; r < kRowGroup; ++r) {
-    a[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) a[r] = fmaf(k[i], q[r][i], a[r]);
-  }
-#pragma unroll
-  for (int lvl = 0; lvl < 3; ++lvl) {
-    const int off = 16 >> lvl, half = kRowGroup >> (lvl + 1);
-    const bool up = lane & off;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float send = up ? a[i] : a[i + half];
-      const float keep = up ? a[i + half] : a[i];
-      a[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
-    }
-  }
-  float x = a[0];
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  return x;
-}
+// A block's tile of the product: kRowGroup rows against kTileKeys keys, thread
+// (rg, kg) = (tid / 16, tid % 16) with rows 4 rg .. + 3 and keys kg, kg + 16, + 32,
+// + 48.  Rows of shared memory are 4 floats longer than D: eight keys' 16-byte
+// pieces take all banks, and the two rg of a warp read as one.  For 4 values of d a
+// thread reads 8 pieces (12 cycles of the SM's shared memory for a warp) and makes
+// 64 products (16 cycles of its FMA lanes).
+constexpr int kTileThreads = 128;
+constexpr int kTileKeys = kColTile;
+constexpr int kTileBlocks = 4;  // of an SM: two passes of loads and products go on beside each other
 
 template <int D>
 struct Tile {
-  static constexpr int E = D / 32;
-  // Row group rg of kv head h: the lane's slice of each of its rows' q
-  // (rows past the end: zeros).
-  __device__ static void load_q(const ScoreParams& p, int qstart, int rows, int h, int rg, int lane,
-                                float (&q)[kRowGroup][E]) {
-#pragma unroll
-    for (int r = 0; r < kRowGroup; ++r) {
-      const int row = rg * kRowGroup + r;
-      if (row < rows) {
-        const int i = row / p.G, g = row - i * p.G;
-        const float* src = static_cast<const float*>(p.q) + ((int64_t)(qstart + i) * p.Hq + h * p.G + g) * D + lane * E;
-#pragma unroll
-        for (int j = 0; j < E; ++j) q[r][j] = src[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < E; ++j) q[r][j] = 0.f;
-      }
+  static constexpr int kPitch = D + 4;
+  static constexpr int kSmem = (kTileKeys + kRowGroup) * kPitch * (int)sizeof(float);
+  const float* k;  // [kTileKeys][kPitch]
+  const float* q;  // [kRowGroup][kPitch]
+
+  // Rows of the row group rg of kv head h (past the end: zeros).  Ends with the
+  // copies under way.
+  __device__ static void load_q(const ScoreParams& p, const SeqPlan& sp, int qstart, int h, int rg, float* q) {
+    const uint32_t dst = smem_u32(q);
+    for (int i = threadIdx.x; i < kRowGroup * (D / 4); i += kTileThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4, row = rg * kRowGroup + r;
+      const bool ok = row < sp.rows;
+      const int t = ok ? row / p.G : 0, g = ok ? row - t * p.G : 0;
+      copy16(dst + (r * kPitch + d) * 4,
+             static_cast<const float*>(p.q) + ((int64_t)(qstart + t) * p.Hq + h * p.G + g) * D + d, ok);
     }
   }
-  // The lane's slice of key j of kv head h (a block outside the pool: zeros).
-  __device__ static void load_k(const ScoreParams& p, const int32_t* bt, int j, int h, int lane, float (&k)[E]) {
-    const int b = bt[j / p.bs];
-    if (b >= 0 && b < p.num_blocks) {
-      const float* src =
-          static_cast<const float*>(p.kc) + (((int64_t)b * p.bs + j % p.bs) * p.Hkv + h) * D + lane * E;
-#pragma unroll
-      for (int i = 0; i < E; ++i) k[i] = src[i];
-    } else {
-      raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
-#pragma unroll
-      for (int i = 0; i < E; ++i) k[i] = 0.f;
+  // Keys j0 .. of kv head h (past the sequence, or in a block outside the pool: zeros).
+  __device__ static void load_k(const ScoreParams& p, const SeqPlan& sp, const int32_t* bt, int h, int j0, float* k) {
+    const uint32_t dst = smem_u32(k);
+    for (int i = threadIdx.x; i < kTileKeys * (D / 4); i += kTileThreads) {
+      const int key = i / (D / 4), d = i % (D / 4) * 4, j = j0 + key;
+      const int b = j < sp.L ? __ldg(bt + (j >> p.bs_log)) : 0;
+      const bool in = b >= 0 && b < p.num_blocks;
+      if (!in) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+      const bool ok = in && j < sp.L;
+      const int64_t at = ok ? (((int64_t)b * p.bs + (j & (p.bs - 1))) * p.Hkv + h) * D + d : 0;
+      copy16(dst + (key * kPitch + d) * 4, static_cast<const float*>(p.kc) + at, ok);
     }
+  }
+  // z[i][j]: logit (times scale * log2 e) of row 4 rg + i and key kg + 16 j.  fp32
+  // products and sums, two of them at a time over even and odd pairs of d.
+  __device__ __forceinline__ void product(float scale_log2, float (&z)[4][4]) const {
+    const int kg = threadIdx.x & 15, rg = threadIdx.x >> 4;
+    f32x2 acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+    const float* qr = q + rg * 4 * kPitch;
+    const float* kr = k + kg * kPitch;
+#pragma unroll 2
+    for (int d = 0; d < D; d += 4) {
+      ulonglong2 x[4], y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(qr + i * kPitch + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(kr + j * 16 * kPitch + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, acc[i][j]));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 v = up2(acc[i][j]);
+        z[i][j] = (v.x + v.y) * scale_log2;
+      }
   }
 };
 
+// Keys that row `row` of a kv head sees.
+__device__ __forceinline__ int keys_seen(const ScoreParams& p, const SeqPlan& sp, int row) {
+  return row >= sp.rows ? 0 : p.causal ? sp.L - sp.n + row / p.G + 1 : sp.L;
+}
+
+// (max, sum) of each row over a chunk of keys; a block's unit is a row group and
+// a chunk.
 template <int D>
-__global__ void __launch_bounds__(kThreads) stats_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) stats_kernel(const ScoreParams p) {
   using X = Tile<D>;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  extern __shared__ __align__(16) uint8_t smem[];
+  float* k = reinterpret_cast<float*>(smem);
+  float* q = k + kTileKeys * X::kPitch;
+  const X tile{k, q};
+  const int lane = threadIdx.x & 31, kg = threadIdx.x & 15, rg4 = threadIdx.x >> 4;
   const int64_t total = p.off[kStat][p.B];
-  for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < total; u += warps) {
+  for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
     const int s = find_seq(p.off[kStat], p.B, u, lane);
     const SeqPlan sp = p.plan[s];
-    const int rows = sp.rows, groups = (rows + kRowGroup - 1) / kRowGroup;
+    const int groups = (sp.rows + kRowGroup - 1) / kRowGroup;
     int64_t v = u - p.off[kStat][s];
     const int c = (int)(v % sp.chunks);
     v /= sp.chunks;
     const int rg = (int)(v % groups), h = (int)(v / groups);
-    float q[kRowGroup][X::E];
-    X::load_q(p, p.qsl[s], rows, h, rg, lane, q);
     const int32_t* bt = p.tables + (int64_t)s * p.max_blocks;
-    const int row = rg * kRowGroup + (lane >> 2);
-    const int vis = row >= rows ? 0 : p.causal ? sp.L - sp.n + row / p.G + 1 : sp.L;
-    const int ke = min(sp.L, (c + 1) * kChunk);
-    float m = -CUDART_INF_F, l = 0.f;
-    for (int j = c * kChunk; j < ke; ++j) {
-      float k[X::E];
-      X::load_k(p, bt, j, h, lane, k);
-      const float z = group_dot<X::E>(k, q, lane) * p.scale_log2;
-      if (j < vis && z != -CUDART_INF_F) {  // a logit of -inf weighs nothing, also before the first finite one
-        const float mn = fmaxf(m, z);
-        l = l * fast_exp2(m - mn) + fast_exp2(z - mn);
-        m = mn;
+    const int row0 = rg * kRowGroup + rg4 * 4;
+    const int last = min(sp.rows, (rg + 1) * kRowGroup) - 1;
+    const int ke = min(keys_seen(p, sp, last), (c + 1) * kChunk);  // no row of the group sees more
+    float m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -CUDART_INF_F;
+      l[i] = 0.f;
+    }
+    for (int j0 = c * kChunk; j0 < ke; j0 += kTileKeys) {
+      __syncthreads();  // the last tile has been read
+      if (j0 == c * kChunk) X::load_q(p, sp, p.qsl[s], h, rg, q);
+      X::load_k(p, sp, bt, h, j0, k);
+      copy_commit();
+      copy_wait<0>();
+      __syncthreads();
+      float z[4][4];
+      tile.product(p.scale_log2, z);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int see = keys_seen(p, sp, row0 + i) - j0 - kg;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j * 16 >= see) z[i][j] = -CUDART_INF_F;
+        const float mn = fmaxf(fmax3(m[i], z[i][0], z[i][1]), fmaxf(z[i][2], z[i][3]));
+        const float mu = mn == -CUDART_INF_F ? 0.f : mn;
+        l[i] = fmaf(l[i], fast_exp2(m[i] - mu), (fast_exp2(z[i][0] - mu) + fast_exp2(z[i][1] - mu)) +
+                                                    (fast_exp2(z[i][2] - mu) + fast_exp2(z[i][3] - mu)));
+        m[i] = mn;
       }
     }
-    if (row < rows && (lane & 3) == 0) p.part[sp.part + ((int64_t)h * rows + row) * sp.chunks + c] = make_float2(m, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mm = m[i];
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+      float ll = l[i] * fast_exp2(m[i] - (mm == -CUDART_INF_F ? 0.f : mm));
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+      if (kg == 0 && row0 + i < sp.rows)
+        p.part[sp.part + ((int64_t)h * sp.rows + row0 + i) * sp.chunks + c] = make_float2(mm, ll);
+    }
   }
 }
 
-// lse of each row (one warp a row).
+// lse of each row (one warp a row); blockIdx.y: the sequence.
 __global__ void __launch_bounds__(kThreads) lse_kernel(const ScoreParams p) {
   const int lane = threadIdx.x & 31;
-  for (int s = 0; s < p.B; ++s) {
-    const SeqPlan sp = p.plan[s];
-    if (sp.kind != kOther) continue;
-    for (int w = (blockIdx.x * kThreads + threadIdx.x) >> 5; w < p.Hkv * sp.rows; w += (gridDim.x * kThreads) >> 5) {
-      const float x = row_lse(p.part + sp.part + (int64_t)w * sp.chunks, sp.chunks, lane);
-      if (lane == 0) p.lse[sp.lse + w] = x;
-    }
+  const SeqPlan sp = p.plan[blockIdx.y];
+  if (sp.kind != kOther) return;
+  for (int w = (blockIdx.x * kThreads + threadIdx.x) >> 5; w < p.Hkv * sp.rows; w += (gridDim.x * kThreads) >> 5) {
+    const float x = row_lse(p.part + sp.part + (int64_t)w * sp.chunks, sp.chunks, lane);
+    if (lane == 0) p.lse[sp.lse + w] = x;
   }
 }
 
+// The weights of kTileKeys keys summed over the rows, and their scores; a block's
+// unit is a tile of keys and all row groups that see any of it.
 template <int D>
-__global__ void __launch_bounds__(kThreads) columns_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kTileThreads, kTileBlocks) columns_kernel(const ScoreParams p) {
   using X = Tile<D>;
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float sums[kTileThreads / 16][kTileKeys];
+  float* k = reinterpret_cast<float*>(smem);
+  float* q = k + kTileKeys * X::kPitch;
+  const X tile{k, q};
+  const int lane = threadIdx.x & 31, kg = threadIdx.x & 15, rg4 = threadIdx.x >> 4;
   const int64_t total = p.off[kCol][p.B];
-  for (int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5; u < total; u += warps) {
+  for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
     const int s = find_seq(p.off[kCol], p.B, u, lane);
     const SeqPlan sp = p.plan[s];
-    const int rows = sp.rows, groups = (rows + kRowGroup - 1) / kRowGroup;
+    const int groups = (sp.rows + kRowGroup - 1) / kRowGroup, tiles = (sp.L + kTileKeys - 1) / kTileKeys;
     const int64_t v = u - p.off[kCol][s];
-    const int c = (int)(v % sp.chunks), h = (int)(v / sp.chunks);
+    const int j0 = (int)(v % tiles) * kTileKeys, h = (int)(v / tiles);
     const int32_t* bt = p.tables + (int64_t)s * p.max_blocks;
     const int qstart = p.qsl[s];
-    for (int j0 = c * kChunk; j0 < min(sp.L, (c + 1) * kChunk); j0 += 32) {
-      const int nk = min(32, sp.L - j0);
-      float paid = 0.f;  // of key j0 + lane
-      for (int rg = 0; rg < groups; ++rg) {
-        float q[kRowGroup][X::E];
-        X::load_q(p, qstart, rows, h, rg, lane, q);
-        const int row = rg * kRowGroup + (lane >> 2);
-        const int i = row / p.G;
-        const int vis = row >= rows ? 0 : p.causal ? sp.L - sp.n + i + 1 : sp.L;
-        const float lse = row < rows ? p.lse[sp.lse + (int64_t)h * rows + row] : 0.f;
-        for (int j = 0; j < nk; ++j) {
-          float k[X::E];
-          X::load_k(p, bt, j0 + j, h, lane, k);
-          const float z = group_dot<X::E>(k, q, lane) * p.scale_log2;
-          float w = j0 + j < vis ? fast_exp2(z - lse) : 0.f;
+    // the first row that sees key j0
+    const int first = p.causal ? max(0, j0 - (sp.L - sp.n)) * p.G : 0;
+    float paid[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int rg = first / kRowGroup; rg < groups; ++rg) {
+      __syncthreads();  // the last tile, and the last unit's sums, have been read
+      if (rg == first / kRowGroup) X::load_k(p, sp, bt, h, j0, k);
+      X::load_q(p, sp, qstart, h, rg, q);
+      copy_commit();
+      const int row0 = rg * kRowGroup + rg4 * 4;
+      float lse[4];
 #pragma unroll
-          for (int d = 4; d < 32; d <<= 1) w += __shfl_xor_sync(0xffffffffu, w, d);
-          if (lane == j) paid += w;
-        }
+      for (int i = 0; i < 4; ++i)
+        lse[i] = row0 + i < sp.rows ? __ldg(p.lse + sp.lse + (int64_t)h * sp.rows + row0 + i) : 0.f;
+      copy_wait<0>();
+      __syncthreads();
+      float z[4][4];
+      tile.product(p.scale_log2, z);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int see = keys_seen(p, sp, row0 + i) - j0 - kg;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) paid[j] += j * 16 < see ? fast_exp2(z[i][j] - lse[i]) : 0.f;
       }
-      const int j = j0 + lane;
-      if (j < sp.L) {
-        const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len + j;
-        if (j < sp.L - sp.n && p.decay != 0.f) paid = fmaf(p.decay, p.scores[at], paid);
-        p.out[at] = paid;
-      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[rg4][kg + 16 * j] = paid[j];
+    __syncthreads();
+    const int j = j0 + threadIdx.x;
+    if (threadIdx.x < kTileKeys && j < sp.L) {
+      float x = 0.f;
+#pragma unroll
+      for (int r = 0; r < kTileThreads / 16; ++r) x += sums[r][threadIdx.x];
+      const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len + j;
+      if (j < sp.L - sp.n && p.decay != 0.f) x = fmaf(p.decay, p.scores[at], x);
+      p.out[at] = x;
     }
   }
 }
@@ -1139,10 +1197,20 @@ cudaError_t launch(const ScoreParams& p, bool one_tile, int sms, cudaStream_t s)
 
 template <int D>
 cudaError_t launch_other(const ScoreParams& p, int sms, cudaStream_t s) {
-  const int grid = sms * 8;
-  stats_kernel<D><<<grid, kThreads, 0, s>>>(p);
-  lse_kernel<<<grid, kThreads, 0, s>>>(p);
-  columns_kernel<D><<<grid, kThreads, 0, s>>>(p);
+  constexpr int kSmem = Tile<D>::kSmem;
+  static unsigned long long done_mask = 0;  // devices set up
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << (dev & 63)))) {
+    for (const void* f : {(const void*)stats_kernel<D>, (const void*)columns_kernel<D>})
+      if ((e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem)) != cudaSuccess) return e;
+    __atomic_fetch_or(&done_mask, 1ull << (dev & 63), __ATOMIC_RELEASE);
+  }
+  const dim3 grid(sms * kTileBlocks), lse_grid(std::max(1, std::min(16, 2048 / p.B)), p.B);
+  stats_kernel<D><<<grid, kTileThreads, kSmem, s>>>(p);
+  lse_kernel<<<lse_grid, kThreads, 0, s>>>(p);
+  columns_kernel<D><<<grid, kTileThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 

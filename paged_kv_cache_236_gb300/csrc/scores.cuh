@@ -21,7 +21,8 @@ constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
 constexpr int kMaxRowTiles = 1 << 16;
 constexpr int kChunk = 256;   // keys of a work unit (more rows in fp32)
 enum { kFew = 1, kTensor = 2, kOther = 3 };
-constexpr int kRowGroup = 8;  // rows of a work unit (more rows in fp32)
+constexpr int kColTile = 64;    // keys of its column unit
+constexpr int kRowGroup = 32;   // its rows
 
 // Offsets of each sequence's work, as prefix sums: the unit queues of the
 // kernels below (few-row stats and columns; other rows' stats and columns),
