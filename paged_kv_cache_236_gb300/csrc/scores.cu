@@ -906,15 +906,22 @@ __global__ void __launch_bounds__(kColThreads, kColBlocks) few_columns_kernel(co
 // ---------------------------------------------------------------------------
 // more rows in fp32
 // ---------------------------------------------------------------------------
-// A block's tile of the product: kRowGroup rows against kTileKeys keys, thread
-// (rg, kg) = (tid / 16, tid % 16) with rows 4 rg .. + 3 and keys kg, kg + 16, + 32,
-// + 48.  Rows of shared memory are 4 floats longer than D: eight keys' 16-byte
-// pieces take all banks, and the two rg of a warp read as one.  For 4 values of d a
-// thread reads 8 pieces (12 cycles of the SM's shared memory for a warp) and makes
-// 64 products (16 cycles of its FMA lanes).
+// A block's tile of the product: kRowGroup rows against kTileKeys keys; warp w has
+// rows 8 w .. + 7, lane l keys l and l + 32.  Rows of shared memory are 4 floats
+// longer than D, so that eight keys' 16-byte pieces take all banks.  For 4 values of
+// d a warp reads 2 pieces of keys (4 cycles of shared memory each) and 8 of rows (a
+// broadcast each) and makes 64 products a lane, 16 cycles of the SM's FMA lanes.
+//
+// Bound by latency: of a tile's 17000 cycles, four blocks beside each other, 6000 go
+// into the copies, 8000 into the products (a third of the FMA rate over all).
+// 40 rows against 16 x 8192 keys of 8 heads of 128: 993 us; 4 rows and 4 keys a
+// thread, 16 lanes to a row group: 1186; 128 keys a tile and two blocks an SM: 1240;
+// three blocks without spills: 1124.
 constexpr int kTileThreads = 128;
+constexpr int kWarpRows = kRowGroup / (kTileThreads / 32);
 constexpr int kTileKeys = kColTile;
-constexpr int kTileBlocks = 4;  // of an SM: two passes of loads and products go on beside each other
+constexpr int kLaneKeys = kTileKeys / 32;
+constexpr int kTileBlocks = 4;  // of an SM: some load while others multiply
 
 template <int D>
 struct Tile {
@@ -938,43 +945,58 @@ struct Tile {
   // Keys j0 .. of kv head h (past the sequence, or in a block outside the pool: zeros).
   __device__ static void load_k(const ScoreParams& p, const SeqPlan& sp, const int32_t* bt, int h, int j0, float* k) {
     const uint32_t dst = smem_u32(k);
-    for (int i = threadIdx.x; i < kTileKeys * (D / 4); i += kTileThreads) {
-      const int key = i / (D / 4), d = i % (D / 4) * 4, j = j0 + key;
+    constexpr int kLanes = D / 4;  // that read a key's row
+    const int d = threadIdx.x % kLanes * 4, token = p.Hkv * D;
+    const int64_t block = (int64_t)p.bs * token;
+    const float* src = static_cast<const float*>(p.kc) + h * D + d;
+#pragma unroll 4
+    for (int key = threadIdx.x / kLanes; key < kTileKeys; key += kTileThreads / kLanes) {
+      const int j = j0 + key;
       const int b = j < sp.L ? __ldg(bt + (j >> p.bs_log)) : 0;
       const bool in = b >= 0 && b < p.num_blocks;
       if (!in) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
       const bool ok = in && j < sp.L;
-      const int64_t at = ok ? (((int64_t)b * p.bs + (j & (p.bs - 1))) * p.Hkv + h) * D + d : 0;
-      copy16(dst + (key * kPitch + d) * 4, static_cast<const float*>(p.kc) + at, ok);
+      const float* at = src + (int64_t)(ok ? b : 0) * block + (ok ? (j & (p.bs - 1)) * token : 0);
+      copy16(dst + (key * kPitch + d) * 4, at, ok);
     }
   }
-  // z[i][j]: logit (times scale * log2 e) of row 4 rg + i and key kg + 16 j.  fp32
-  // products and sums, two of them at a time over even and odd pairs of d.
-  __device__ __forceinline__ void product(float scale_log2, float (&z)[4][4]) const {
-    const int kg = threadIdx.x & 15, rg = threadIdx.x >> 4;
-    f32x2 acc[4][4];
+  // z[i][j]: logit (times scale * log2 e) of the warp's row i and key lane + 32 j.
+  // fp32 products and sums, two of them at a time over even and odd d.
+  __device__ __forceinline__ void product(float scale_log2, float (&z)[kWarpRows][kLaneKeys]) const {
+    f32x2 acc[kWarpRows][kLaneKeys];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kWarpRows; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = 0;
-    const float* qr = q + rg * 4 * kPitch;
-    const float* kr = k + kg * kPitch;
-#pragma unroll 2
-    for (int d = 0; d < D; d += 4) {
-      ulonglong2 x[4], y[4];
+      for (int j = 0; j < kLaneKeys; ++j) acc[i][j] = 0;
+    const float* qr = q + (threadIdx.x >> 5) * kWarpRows * kPitch;
+    const float* kr = k + (threadIdx.x & 31) * kPitch;
+    // a step's pieces are read while the step before is multiplied
+    ulonglong2 x[2][kWarpRows], y[2][kLaneKeys];
+    auto read = [&](int at, int d) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(qr + i * kPitch + d);
+      for (int j = 0; j < kLaneKeys; ++j) y[at][j] = *reinterpret_cast<const ulonglong2*>(kr + j * 32 * kPitch + d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(kr + j * 16 * kPitch + d);
+      for (int i = 0; i < kWarpRows; ++i) x[at][i] = *reinterpret_cast<const ulonglong2*>(qr + i * kPitch + d);
+    };
+    auto multiply = [&](int at) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kWarpRows; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, acc[i][j]));
+        for (int j = 0; j < kLaneKeys; ++j)
+          acc[i][j] = fma2(x[at][i].y, y[at][j].y, fma2(x[at][i].x, y[at][j].x, acc[i][j]));
+    };
+    read(0, 0);
+#pragma unroll 1
+    for (int d = 0; d < D; d += 8) {
+      read(1, d + 4);
+      multiply(0);
+      if (d + 8 < D) read(0, d + 8);
+      multiply(1);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kWarpRows; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kLaneKeys; ++j) {
         const float2 v = up2(acc[i][j]);
         z[i][j] = (v.x + v.y) * scale_log2;
       }
@@ -984,6 +1006,18 @@ struct Tile {
 // Keys that row `row` of a kv head sees.
 __device__ __forceinline__ int keys_seen(const ScoreParams& p, const SeqPlan& sp, int row) {
   return row >= sp.rows ? 0 : p.causal ? sp.L - sp.n + row / p.G + 1 : sp.L;
+}
+// The same of rows row0 .. + 7, with one division.
+__device__ __forceinline__ void keys_seen(const ScoreParams& p, const SeqPlan& sp, int row0, int (&see)[kWarpRows]) {
+  int t = row0 / p.G, g = row0 - t * p.G;
+#pragma unroll
+  for (int i = 0; i < kWarpRows; ++i) {
+    see[i] = row0 + i >= sp.rows ? 0 : p.causal ? sp.L - sp.n + t + 1 : sp.L;
+    if (++g == p.G) {
+      g = 0;
+      ++t;
+    }
+  }
 }
 
 // (max, sum) of each row over a chunk of keys; a block's unit is a row group and
@@ -995,7 +1029,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) stats_kernel(const 
   float* k = reinterpret_cast<float*>(smem);
   float* q = k + kTileKeys * X::kPitch;
   const X tile{k, q};
-  const int lane = threadIdx.x & 31, kg = threadIdx.x & 15, rg4 = threadIdx.x >> 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t total = p.off[kStat][p.B];
   for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
     const int s = find_seq(p.off[kStat], p.B, u, lane);
@@ -1006,12 +1040,14 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) stats_kernel(const 
     v /= sp.chunks;
     const int rg = (int)(v % groups), h = (int)(v / groups);
     const int32_t* bt = p.tables + (int64_t)s * p.max_blocks;
-    const int row0 = rg * kRowGroup + rg4 * 4;
+    const int row0 = rg * kRowGroup + warp * kWarpRows;
     const int last = min(sp.rows, (rg + 1) * kRowGroup) - 1;
     const int ke = min(keys_seen(p, sp, last), (c + 1) * kChunk);  // no row of the group sees more
-    float m[4], l[4];
+    float m[kWarpRows], l[kWarpRows];
+    int seen[kWarpRows];
+    keys_seen(p, sp, row0, seen);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWarpRows; ++i) {
       m[i] = -CUDART_INF_F;
       l[i] = 0.f;
     }
@@ -1022,30 +1058,34 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) stats_kernel(const 
       copy_commit();
       copy_wait<0>();
       __syncthreads();
-      float z[4][4];
+      if (row0 >= sp.rows) continue;  // none of the warp's
+      float z[kWarpRows][kLaneKeys];
       tile.product(p.scale_log2, z);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int see = keys_seen(p, sp, row0 + i) - j0 - kg;
+      for (int i = 0; i < kWarpRows; ++i) {
+        const int see = seen[i] - j0 - lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j * 16 >= see) z[i][j] = -CUDART_INF_F;
-        const float mn = fmaxf(fmax3(m[i], z[i][0], z[i][1]), fmaxf(z[i][2], z[i][3]));
+        for (int j = 0; j < kLaneKeys; ++j)
+          if (j * 32 >= see) z[i][j] = -CUDART_INF_F;
+        float mn = m[i];
+#pragma unroll
+        for (int j = 0; j < kLaneKeys; ++j) mn = fmaxf(mn, z[i][j]);
         const float mu = mn == -CUDART_INF_F ? 0.f : mn;
-        l[i] = fmaf(l[i], fast_exp2(m[i] - mu), (fast_exp2(z[i][0] - mu) + fast_exp2(z[i][1] - mu)) +
-                                                    (fast_exp2(z[i][2] - mu) + fast_exp2(z[i][3] - mu)));
+        l[i] *= fast_exp2(m[i] - mu);
+#pragma unroll
+        for (int j = 0; j < kLaneKeys; ++j) l[i] += fast_exp2(z[i][j] - mu);
         m[i] = mn;
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kWarpRows; ++i) {
       float mm = m[i];
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+      for (int d = 1; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
       float ll = l[i] * fast_exp2(m[i] - (mm == -CUDART_INF_F ? 0.f : mm));
 #pragma unroll
-      for (int d = 1; d < 16; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-      if (kg == 0 && row0 + i < sp.rows)
+      for (int d = 1; d < 32; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+      if (lane == 0 && row0 + i < sp.rows)
         p.part[sp.part + ((int64_t)h * sp.rows + row0 + i) * sp.chunks + c] = make_float2(mm, ll);
     }
   }
@@ -1068,11 +1108,11 @@ template <int D>
 __global__ void __launch_bounds__(kTileThreads, kTileBlocks) columns_kernel(const ScoreParams p) {
   using X = Tile<D>;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float sums[kTileThreads / 16][kTileKeys];
+  __shared__ float sums[kTileThreads / 32][kTileKeys];
   float* k = reinterpret_cast<float*>(smem);
   float* q = k + kTileKeys * X::kPitch;
   const X tile{k, q};
-  const int lane = threadIdx.x & 31, kg = threadIdx.x & 15, rg4 = threadIdx.x >> 4;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t total = p.off[kCol][p.B];
   for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
     const int s = find_seq(p.off[kCol], p.B, u, lane);
@@ -1084,36 +1124,39 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) columns_kernel(cons
     const int qstart = p.qsl[s];
     // the first row that sees key j0
     const int first = p.causal ? max(0, j0 - (sp.L - sp.n)) * p.G : 0;
-    float paid[4] = {0.f, 0.f, 0.f, 0.f};
+    float paid[kLaneKeys] = {};
     for (int rg = first / kRowGroup; rg < groups; ++rg) {
       __syncthreads();  // the last tile, and the last unit's sums, have been read
       if (rg == first / kRowGroup) X::load_k(p, sp, bt, h, j0, k);
       X::load_q(p, sp, qstart, h, rg, q);
       copy_commit();
-      const int row0 = rg * kRowGroup + rg4 * 4;
-      float lse[4];
+      const int row0 = rg * kRowGroup + warp * kWarpRows;
+      float lse[kWarpRows];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kWarpRows; ++i)
         lse[i] = row0 + i < sp.rows ? __ldg(p.lse + sp.lse + (int64_t)h * sp.rows + row0 + i) : 0.f;
       copy_wait<0>();
       __syncthreads();
-      float z[4][4];
+      if (row0 >= sp.rows) continue;  // none of the warp's
+      float z[kWarpRows][kLaneKeys];
       tile.product(p.scale_log2, z);
+      int seen[kWarpRows];
+      keys_seen(p, sp, row0, seen);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int see = keys_seen(p, sp, row0 + i) - j0 - kg;
+      for (int i = 0; i < kWarpRows; ++i) {
+        const int see = seen[i] - j0 - lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) paid[j] += j * 16 < see ? fast_exp2(z[i][j] - lse[i]) : 0.f;
+        for (int j = 0; j < kLaneKeys; ++j) paid[j] += j * 32 < see ? fast_exp2(z[i][j] - lse[i]) : 0.f;
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sums[rg4][kg + 16 * j] = paid[j];
+    for (int j = 0; j < kLaneKeys; ++j) sums[warp][lane + 32 * j] = paid[j];
     __syncthreads();
     const int j = j0 + threadIdx.x;
     if (threadIdx.x < kTileKeys && j < sp.L) {
       float x = 0.f;
 #pragma unroll
-      for (int r = 0; r < kTileThreads / 16; ++r) x += sums[r][threadIdx.x];
+      for (int r = 0; r < kTileThreads / 32; ++r) x += sums[r][threadIdx.x];
       const int64_t at = ((int64_t)sp.row * p.Hkv + h) * p.max_len + j;
       if (j < sp.L - sp.n && p.decay != 0.f) x = fmaf(p.decay, p.scores[at], x);
       p.out[at] = x;
