@@ -155,14 +155,14 @@ def test_many_queries(n, L, dtype):
     b.check(b.run(), before)
 
 
-@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
 @pytest.mark.parametrize("Hq,Hkv,bs", [(8, 2, 16), (32, 2, 32), (8, 8, 64)])
-def test_prompts_from_the_first_token(Hq, Hkv, bs, f8):
+def test_prompts_from_the_first_token(Hq, Hkv, bs, dtype):
     """No context before the queries: row tiles that see one, two, ... K tiles
     of a range, in odd and even numbers, and short sequences of one K tile in a
     row; over and over, since only the timing of the roles could go wrong."""
     lens = [700, 128, 90, 33, 127, 385, 64, 1100, 100, 100, 1]
-    b = Batch(Hq + bs, lens, lens, Hq, Hkv, 128, bs, f8=f8)
+    b = Batch(Hq + bs, lens, lens, Hq, Hkv, 128, bs, torch.float32 if dtype == "f32" else torch.bfloat16, dtype == "fp8")
     before = b.old.clone()
     first = b.run(out=b.old.clone())
     b.check(first, before)
@@ -325,6 +325,23 @@ def test_same_bits_each_time_and_workspaces():
         x = b.run(out=torch.zeros_like(b.old))
         y = other.run(out=torch.zeros_like(other.old))
     assert torch.equal(x, first) and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("group,D", [(1, 128), (7, 64), (16, 128)])
+def test_least_workspace(group, D, dtype):
+    """Few rows whose logits there is no room for are computed twice."""
+    if dtype == "fp8" and D != 128:
+        pytest.skip("FP8 pools: head_dim 128")
+    lens, qlens = [900, 64, 1, 130, 257], [1, 2, 1, 0, 1]
+    b = Batch(group + D, lens, qlens, 2 * group, 2, D, 16, torch.float32 if dtype == "f32" else torch.bfloat16,
+              dtype == "fp8")
+    need = pkv.scores_workspace_min(len(lens), b.q.shape[0], 2 * group, 2, min(b.old.shape[2], b.tables.shape[1] * 16))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for causal, decay in ((True, 1.0), (False, 0.5)):
+        before = b.old.clone()
+        b.check(b.run(causal, decay, out=b.old.clone(), workspace=ws), before, causal=causal, decay=decay)
+    assert pkv.device_errors() == 0
 
 
 def test_graph_replay_follows_its_inputs():
