@@ -956,7 +956,7 @@ struct Tile {
       const bool in = b >= 0 && b < p.num_blocks;
       if (!in) raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
       const bool ok = in && j < sp.L;
-      const float* at = src + (int64_t)(ok ? b : 0) * block + (ok ? (j & (p.bs - 1)) * token : 0);
+      const float* at = src + (int64_t)(ok ? b : 0) * block + (ok ? (int64_t)(j & (p.bs - 1)) * token : 0);
       copy16(dst + (key * kPitch + d) * 4, at, ok);
     }
   }
