@@ -65,6 +65,14 @@ __device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {  // inclusiv
 
 constexpr int kPlanThreads = 1024;
 
+// Kept logits of a few-row sequence, rounded up so that the next one's start on
+// 16 bytes: rows padded to 4 and more are read as float4, and an odd number of
+// keys of rows padded to 2 ends between.
+__device__ __forceinline__ int64_t logits_kept(const ScoreParams& p, int L, int pad) {
+  return ((int64_t)p.Hkv * L * pad + 3) & ~(int64_t)3;
+}
+constexpr int kLogitSlack = 2;  // what the rounding adds to a sequence, at most
+
 // Keys of a few-row stats unit: the launch's (few units: short ones, so that
 // they spread over the SMs), longer for long sequences (fewer partials), whose
 // block ids a warp's lanes hold.
@@ -138,7 +146,7 @@ __device__ __forceinline__ void plan_block(const ScoreParams& p) {
     }
     const bool want_few = sp.n > 0 && sp.rows <= kFewRows;
     const int pad = sp.rows <= 2 ? 2 : sp.rows <= 4 ? 4 : sp.rows <= 8 ? 8 : 16;
-    const int64_t logits = want_few ? (int64_t)p.Hkv * sp.L * pad : 0;
+    const int64_t logits = want_few ? logits_kept(p, sp.L, pad) : 0;
     int64_t x = warp_scan(logits, lane);
     if (lane == 31) warp_sum[kSums][warp] = x;
     over_warps(kSums, 1);
@@ -254,7 +262,7 @@ __device__ __forceinline__ void plan_few(const ScoreParams& p, int64_t* stat, in
     mine[i][0] = (int64_t)p.Hkv * q.chunks;
     mine[i][1] = (int64_t)p.Hkv * ((q.L + kColChunk - 1) / kColChunk);
     mine[i][2] = mine[i][0] * q.rows;
-    mine[i][3] = (int64_t)p.Hkv * q.L * q.pad;
+    mine[i][3] = logits_kept(p, q.L, q.pad);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] += mine[i][k];
   }
@@ -1177,7 +1185,8 @@ struct Layout {
 };
 
 // Kept logits: at most 16 padded rows of each kv head, or twice the rows
-// there are, times the keys; no more than kLogitMax is asked for.
+// there are, times the keys; no more than kLogitMax is asked for.  The rounding
+// of each sequence's comes on top, so that it never decides what fits.
 constexpr size_t kLogitMax = (size_t)512 << 20;
 
 Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
@@ -1204,7 +1213,7 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
                        (size_t)(T * Hq) * (size_t)((keys + kChunk - 1) / kChunk + 1) + (size_t)B;
   at = align_up(at + parts * sizeof(float2));
   l.logit = l.least = at;
-  l.total = align_up(at + std::min(rows * (size_t)keys * sizeof(float), kLogitMax));
+  l.total = align_up(at + std::min(rows * (size_t)keys * sizeof(float), kLogitMax) + (size_t)B * kLogitSlack * sizeof(float));
   return l;
 }
 
@@ -1343,7 +1352,8 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   // every sequence has few rows (the plan holds them to the promised query
   // length), and their logits fit: the other kernels have nothing to do
   const int64_t most_rows = std::min<int64_t>(p.T, max_query_len > 0 ? max_query_len : p.T) * p.G;
-  const bool only_few = most_rows <= kFewRows && std::min(2 * p.T * p.Hq, (int64_t)kFewRows * p.B * p.Hkv) * keys <= p.logit_cap;
+  const bool only_few = most_rows <= kFewRows && std::min(2 * p.T * p.Hq, (int64_t)kFewRows * p.B * p.Hkv) * keys +
+                                                         (int64_t)p.B * kLogitSlack <= p.logit_cap;
   p.own_plan = only_few && p.B <= kHeldSeqs;
   const bool one_tile = most_rows <= 8;
   // stats units there may be at most, against the warps that take them

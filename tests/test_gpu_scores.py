@@ -428,3 +428,19 @@ def test_refusals():
         b.run(decay=-1.0)
     assert torch.equal(b.run(q=b.q[:0], out=torch.zeros_like(b.old),
                              query_start_loc=torch.zeros(2, dtype=torch.int32, device="cuda")), torch.zeros_like(b.old))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("Hkv,group", [(1, 1), (1, 2), (3, 1), (3, 2), (1, 3)])
+def test_wider_sequences_after_narrow_ones(Hkv, group, dtype):
+    """One or two rows over an odd number of keys (of all kv heads) end their
+    kept logits between 16-byte boundaries; the sequences after them have four
+    rows and more, whose logits are read 16 bytes at a time.  With the plan made
+    by the kernel (a promised query length) and by a launch of its own."""
+    lens = [3, 8, 1, 41, 129, 77, 255, 300, 5, 513]
+    for qlens, most in (([1, 3, 1, 2, 1, 5, 2, 5, 1, 5], 5), ([1, 3, 1, 2, 1, 5, 2, 9, 1, 20], 0)):
+        b = Batch(Hkv * 8 + group, lens, qlens, Hkv * group, Hkv, 128, 16,
+                  torch.float32 if dtype == "f32" else torch.bfloat16, dtype == "fp8")
+        before = b.old.clone()
+        b.check(b.run(out=b.old.clone(), max_query_len=most), before)
+        assert pkv.device_errors() == 0
