@@ -402,12 +402,16 @@ pkv_status pkv_event_elapsed_ms(void* start, void* stop, float* ms);
 /*
  * pkv_debug_fault - testing hook for the bounded in-kernel waits (no
  * counterpart on the source pages).  Arms the next paged_attention_forward /
- * _fp8kv call made on this thread, and only that call:
- *   wait_ns     > 0: every bounded wait of its attention kernels gives up
- *               after wait_ns nanoseconds instead of 2 s;
+ * _fp8kv or paged_attention_scores / _fp8kv call made on this thread, and
+ * only that call:
+ *   wait_ns     > 0: every bounded wait of its kernels gives up after wait_ns
+ *               nanoseconds instead of 2 s;
  *   fault_tile  > 0: in the first CTA of its decode-shaped attention kernel
  *               the K/V producer skips the loads of its fault_tile-th key tile
- *               (counting from 1), so the waits for that tile run out.
+ *               (counting from 1), so the waits for that tile run out; of a
+ *               scores call, in the first CTA of its tensor-core kernel, the
+ *               fault_tile-th of the query tiles and the first key tile to
+ *               each, counted together.
  * The kernel then sets PKV_DEVERR_TIMEOUT, every role of the CTA leaves
  * (tensor memory freed, copies in flight awaited) and the call's output is
  * unspecified; the device and later calls are unaffected.  (0, 0) disarms.

@@ -350,10 +350,10 @@ def profile_elapsed_ms(start, stop) -> float:
 
 
 def debug_fault(fault_tile: int, wait_ns: int) -> None:
-    """Testing hook (``pkv_debug_fault``): arm the next forward call of this
-    thread to give up its waits after ``wait_ns`` ns and, with
-    ``fault_tile`` >= 1, to skip the loads of one key tile in one CTA, so
-    that the bounded waits run out."""
+    """Testing hook (``pkv_debug_fault``): arm the next forward or scores
+    call of this thread to give up its waits after ``wait_ns`` ns and, with
+    ``fault_tile`` >= 1, to skip the loads of one tile in one CTA, so that the
+    bounded waits run out."""
     _check(lib().pkv_debug_fault(int(fault_tile), int(wait_ns)))
 
 

@@ -144,6 +144,13 @@ pkv_status device_state(int* sms, int** err) {
   return PKV_OK;
 }
 
+void take_debug_fault(int* fault_tile, uint64_t* wait_ns) {
+  *fault_tile = g_fault_tile;
+  *wait_ns = g_fault_wait_ns;
+  g_fault_tile = 0;
+  g_fault_wait_ns = 0;
+}
+
 pkv_status cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
 pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D, bool codes) {
@@ -565,10 +572,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   ap.out_al32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
   ap.mma_unit_rows = (kMmaRows / G) * G;
   ap.err = dev->err;
-  ap.wait_ns = g_fault_wait_ns;
-  ap.fault_tile = g_fault_tile;
-  g_fault_tile = 0;
-  g_fault_wait_ns = 0;
+  take_debug_fault(&ap.fault_tile, &ap.wait_ns);
 
   // side by side: the decode kernel does not wait for the tensor-core grid,
   // and the tensor-core grid starts once the planner's grid has completed

@@ -229,6 +229,10 @@ pkv_status device_state(int* sms, int** err);
 pkv_status pool_map(CUtensorMap* map, const void* pool, int64_t NB, int bs, int Hkv, int D, bool codes);
 pkv_status rows_map(CUtensorMap* map, const void* q, int64_t T, int Hq, int D, int G, int tokens);
 
+// The testing limits and fault that pkv_debug_fault armed for the next call of
+// this thread, and disarms them.
+void take_debug_fault(int* fault_tile, uint64_t* wait_ns);
+
 // Sets the message to `what` and the error's name; returns PKV_ERR_CUDA.
 pkv_status cuda_error(cudaError_t e, const char* what);
 

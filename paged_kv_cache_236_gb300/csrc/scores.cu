@@ -1360,6 +1360,7 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   const int64_t units = (int64_t)p.B * p.Hkv * ((keys + kFewChunk - 1) / kFewChunk), warps = (int64_t)sms * 8;
   p.few_chunk = std::max(p.bs, 4 * units <= warps ? kFewLeast : 2 * units <= warps ? 2 * kFewLeast : kFewChunk);
   p.max_query = max_query_len;
+  take_debug_fault(&p.fault_tile, &p.wait_ns);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   CUtensorMap qmap, kmap;
   pkv_status mst;

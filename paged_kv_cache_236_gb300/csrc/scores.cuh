@@ -64,6 +64,10 @@ struct ScoreParams {
   int B, Hq, Hkv, G, bs, bs_log, max_blocks, num_rows, max_len, causal;
   float scale_log2, decay;
   int* err;
+  // Testing only (0 in every ordinary call): a limit of the tensor-core kernel's
+  // waits other than 2 s, and the tile load of its first CTA that is left out.
+  uint64_t wait_ns;
+  int fault_tile;
 };
 
 // The sequence s with off[s] <= u < off[s + 1] (the whole warp calls it).

@@ -66,8 +66,8 @@
 //
 // The wait for a head's lse ends: every stats item it depends on was taken
 // from the queue before the column item, by a CTA that works its items off in
-// order.  All waits are bounded (2 s, then the device error word says so and
-// every role leaves); the 128 threads of a group settle failures at barriers
+// order.  All waits are bounded (2 s, or the launch's limit, then the device
+// error word says so and every role leaves); the 128 threads of a group settle failures at barriers
 // that OR them, so none is left waiting.
 #include <math_constants.h>
 
@@ -162,7 +162,10 @@ __device__ __forceinline__ void add_weights(const uint32_t (&z)[32], const float
   }
 }
 
-template <int D, bool F8>
+// kHook: the testing limit and fault are looked at (as arguments of every
+// launch they cost the FP8 kernel two spilled registers and 1 % of a verify
+// batch over FP8 pools).
+template <int D, bool F8, bool kHook>
 __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(const ScoreParams p,
                                                                              const __grid_constant__ CUtensorMap qmap,
                                                                              const __grid_constant__ CUtensorMap kmap) {
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
   Item* items = reinterpret_cast<Item*>(smem + Y::kItemOff);
   int* ids = reinterpret_cast<int*>(smem + Y::kIdOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const WaitCtl wc{p.err, (uint32_t)kWaitTimeoutNs};
+  const WaitCtl wc{p.err, kHook ? wait_limit(p.wait_ns) : (uint32_t)kWaitTimeoutNs};
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
           if (lane == 0) {
             const uint64_t t0 = globaltimer();
             while (ld_acquire(ready + (int64_t)s * p.Hkv + item.h) == 0) {
-              if (globaltimer() - t0 > kWaitTimeoutNs) {
+              if (globaltimer() - t0 > wc.limit_ns) {
                 raise_error(p.err, PKV_DEVERR_TIMEOUT);
                 ok = false;
                 break;
@@ -322,6 +325,10 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
       const int q_bytes = p.tile_tok * p.G * 128;  // one 64-column half of a row tile
       int ny0 = 0, ny1 = 0, nx = 0;  // streamed tiles of either group and resident tiles so far
       bool ok = true;
+      // testing only: the first producer of one CTA leaves out its fault_tile-th
+      // tile, of the resident tiles and the first streamed one to each, from 1, so
+      // that the waits for it run out
+      auto left_out = [&](int load) { return kHook && load == p.fault_tile && (half | blockIdx.x) == 0; };
       for (int it = 0; ok; ++it) {
         const int sl = it % kItems;
         if (!wait_all(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
@@ -340,7 +347,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
             ok = false;
             break;
           }
-          if (lane == 0) {
+          if (lane == 0 && !left_out(2 * nx + 1)) {
             mbar_arrive_expect_tx(&bars->x_full[xb][half], q_bytes);
             tma_load_3d(smem + Y::kXOff + xb * Y::kTileBytes + half * kHalf, &qmap, &bars->x_full[xb][half], half * 64,
                         im.h * p.G, im.qstart + tile * p.tile_tok);
@@ -355,9 +362,10 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
               ok = wait_all(&bars->y_empty[st], phase_of(k) ^ 1, wc);
               if (ok) {
                 uint64_t* full = F8 ? &bars->c_full[st] : &bars->y_full[st][half];
-                if (lane == 0) mbar_arrive_expect_tx(full, kTile * 128);
+                const bool out = i == 0 && left_out(2 * nx);
+                if (lane == 0 && !out) mbar_arrive_expect_tx(full, kTile * 128);
                 __syncwarp();
-                if (lane < nb_per_tile)
+                if (lane < nb_per_tile && !out)
                   tma_load_4d(smem + Y::kYOff + st * Y::kTileBytes + half * kHalf + lane * p.bs * 128, &kmap, full,
                               half * 64, im.h, 0, id[i]);
                 ++k;
@@ -693,7 +701,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
   if (warp == 1) tmem_dealloc(tmem, kSlots * 128);
 }
 
-template <int D, bool F8>
+template <int D, bool F8, bool kHook>
 cudaError_t launch_t(const ScoreParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, int sms, cudaStream_t s) {
   static unsigned long long done_mask = 0;
   int dev = 0;
@@ -701,19 +709,26 @@ cudaError_t launch_t(const ScoreParams& p, const CUtensorMap& qmap, const CUtens
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(scores_mma_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, F8>::kSmem);
+    e = cudaFuncSetAttribute(scores_mma_kernel<D, F8, kHook>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<D, F8>::kSmem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
   }
-  return launch_pdl(scores_mma_kernel<D, F8>, dim3(sms), dim3(Lay<D, F8>::kThreads), Lay<D, F8>::kSmem, s, p, qmap, kmap);
+  return launch_pdl(scores_mma_kernel<D, F8, kHook>, dim3(sms), dim3(Lay<D, F8>::kThreads), Lay<D, F8>::kSmem, s, p, qmap, kmap);
+}
+
+template <bool kHook>
+cudaError_t launch_hook(const ScoreParams& p, int D, bool f8, const CUtensorMap& qmap, const CUtensorMap& kmap, int sms,
+                        cudaStream_t s) {
+  if (f8) return launch_t<128, true, kHook>(p, qmap, kmap, sms, s);
+  return D == 64 ? launch_t<64, false, kHook>(p, qmap, kmap, sms, s) : launch_t<128, false, kHook>(p, qmap, kmap, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_scores_mma(const ScoreParams& p, int D, bool f8, const CUtensorMap& qmap, const CUtensorMap& kmap,
                               int sms, cudaStream_t s) {
-  if (f8) return launch_t<128, true>(p, qmap, kmap, sms, s);
-  return D == 64 ? launch_t<64, false>(p, qmap, kmap, sms, s) : launch_t<128, false>(p, qmap, kmap, sms, s);
+  if (p.wait_ns || p.fault_tile) return launch_hook<true>(p, D, f8, qmap, kmap, sms, s);  // testing only
+  return launch_hook<false>(p, D, f8, qmap, kmap, sms, s);
 }
 
 }  // namespace pkv

@@ -132,3 +132,31 @@ def test_tensor_core_prefill_wait_runs_out(head_dim, fault_tile):
     torch.cuda.synchronize()
     check_step(dw, out, what="after the fault")
     assert pkv.device_errors() == 0
+
+
+def _scores_after_fault(dtype, head_dim, fault_tile):
+    """About seven stats items of one query tile and, after them, four column
+    items of two to a CTA; the loads that can be left out are the query tiles and
+    the first key tile to each."""
+    from test_gpu_scores import Batch
+    b = Batch(75 + head_dim, [4096 - 40 * i for i in range(16)], [40] * 16, 32, 8, head_dim, 16, f8=dtype == "fp8")
+    want = b.run(out=b.old.clone())
+    pkv.device_errors(clear=True)
+    pkv.debug_fault(fault_tile, LIMIT_NS)
+    t0 = time.perf_counter()
+    b.run(out=b.old.clone())
+    flags = pkv.device_errors(clear=True)
+    secs = time.perf_counter() - t0
+    assert flags == pkv.DEVERR["timeout"], f"flags {flags:#x}"
+    assert secs < 1.5, f"the call took {secs:.2f} s: the short limit was not used"
+    assert torch.equal(b.run(out=b.old.clone()), want)
+    assert pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("head_dim", [128, 64])
+@pytest.mark.parametrize("fault_tile", [1, 2, 3, 10, 17, 20])
+def test_scores_wait_runs_out(head_dim, fault_tile):
+    """Scores of 160 rows: the tensor-core kernel (item fetch, two producers,
+    two issuers, the closer, two epilogue groups), a query tile and key tiles
+    of its stats and of its column items."""
+    _scores_after_fault("bf16", head_dim, fault_tile)
