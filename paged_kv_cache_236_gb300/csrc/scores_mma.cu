@@ -485,20 +485,34 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
     const int c = threadIdx.x - kFirstConverter * 32;
     int ny0 = 0, ny1 = 0, nx = 0;  // streamed tiles of either group and resident tiles so far
     bool ok = true;
+    // A wait that runs out in one warp may end well in another, so none leaves
+    // but from a barrier: a K tile's or, at the end and where a wait for an item or
+    // a resident tile ran out, one more.  Whichever of them the others are at, they
+    // meet there, and leave together if any wait ran out.
+    auto leave = [&](bool failed) { barrier_any(3, kConverters, failed); };
     for (int it = 0; ok; ++it) {
       const int sl = it % kItems;
-      if (!wait_all(&bars->item_full[sl], (it / kItems) & 1, wc)) break;
+      if (!wait_all(&bars->item_full[sl], (it / kItems) & 1, wc)) {
+        leave(true);
+        break;
+      }
       const Item im = items[sl];
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
-      if (im.type == kDone) break;
+      if (im.type == kDone) {
+        leave(false);
+        break;
+      }
       for (int tile = im.tile0; tile < im.tile0 + im.tiles && ok; ++tile) {
         const int ny = tiles_seen(p, im, tile);
         if (ny == 0) continue;
         // q, in place: whatever place the swizzle gave a value
         const int xb = nx & 1;
         for (int h = 0; h < kHalves && ok; ++h) ok = wait_all(&bars->x_full[xb][h], (nx >> 1) & 1, wc);
-        if (!ok) break;
+        if (!ok) {
+          leave(true);
+          break;
+        }
         uint4* q = reinterpret_cast<uint4*>(smem + Y::kXOff + xb * Y::kTileBytes);
 #pragma unroll 4
         for (int i = c; i < Y::kTileBytes / 16; i += kConverters) {

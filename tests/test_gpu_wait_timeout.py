@@ -160,3 +160,11 @@ def test_scores_wait_runs_out(head_dim, fault_tile):
     two issuers, the closer, two epilogue groups), a query tile and key tiles
     of its stats and of its column items."""
     _scores_after_fault("bf16", head_dim, fault_tile)
+
+
+@pytest.mark.parametrize("fault_tile", [1, 2, 3, 10, 17, 20])
+def test_scores_fp8_wait_runs_out(fault_tile):
+    """The same over FP8 pools: the eight converter warps leave together,
+    whichever of their waits (for a query tile, for codes, for the next item)
+    runs out."""
+    _scores_after_fault("fp8", 128, fault_tile)
