@@ -198,7 +198,10 @@ __device__ __forceinline__ void plan_block(const ScoreParams& p) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_scores_kernel(const ScoreParams p) {
   pdl_launch_dependents();  // few_kernel waits for this grid first of all
-  for (int64_t i = threadIdx.x; i < 2 * (int64_t)p.B * p.Hkv; i += blockDim.x) p.tickets[i] = 0;
+  if (p.tensor) {
+    for (int64_t i = threadIdx.x; i < most_tiles(p.B, p.T, p.tile_tok) * p.Hkv; i += blockDim.x) p.tickets[i] = 0;
+    for (int64_t i = threadIdx.x; i < (int64_t)p.B * p.Hkv; i += blockDim.x) p.ready[i] = 0;
+  }
   if (threadIdx.x < 2) p.counters[threadIdx.x] = 0;
   plan_block(p);
 }
@@ -1181,13 +1184,16 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
 struct Layout {
-  size_t off[kQueues], plan, tickets, counters, lse, part, logit, least, total;
+  size_t off[kQueues], plan, tickets, ready, counters, lse, part, logit, least, total;
 };
 
 // Kept logits: at most 16 padded rows of each kv head, or twice the rows
 // there are, times the keys; no more than kLogitMax is asked for.  The rounding
 // of each sequence's comes on top, so that it never decides what fits.
 constexpr size_t kLogitMax = (size_t)512 << 20;
+
+// Tokens of a row tile of the tensor-core kernel.
+int tile_tokens(int G) { return std::max(1, 128 / std::max(1, G)); }
 
 Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   Layout l{};
@@ -1199,7 +1205,9 @@ Layout layout(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t keys) {
   l.plan = at;
   at = align_up(at + (size_t)B * sizeof(SeqPlan));
   l.tickets = at;
-  at = align_up(at + (size_t)(2 * B * Hkv) * sizeof(int));
+  at = align_up(at + (size_t)(most_tiles(B, T, tile_tokens((int)(Hq / Hkv))) * Hkv) * sizeof(int));
+  l.ready = at;
+  at = align_up(at + (size_t)(B * Hkv) * sizeof(int));
   l.counters = at;
   at = align_up(at + 2 * sizeof(int));
   l.lse = at;
@@ -1323,7 +1331,7 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
     return fail(PKV_ERR_UNSUPPORTED, "too much work for one call");
   // more rows of bf16 queries go to the tensor-core kernel (its operands come through tensor maps)
   p.tensor = dtype == PKV_DTYPE_BF16;
-  p.tile_tok = 128 / p.G;
+  p.tile_tok = tile_tokens(p.G);
   const int64_t most_tokens = std::min({p.T, keys, max_query_len > 0 ? (int64_t)max_query_len : p.T});
   if (p.tensor && most_tokens > (int64_t)kMaxRowTiles * p.tile_tok)
     return fail(PKV_ERR_UNSUPPORTED, "too many query rows per kv head of a sequence (split the queries over calls)");
@@ -1343,6 +1351,7 @@ pkv_status scores_impl(ScoreParams p, int D, int max_query_len, bool f8, float k
   for (int k = 0; k < kQueues; ++k) p.off[k] = reinterpret_cast<int64_t*>(ws + lay.off[k]);
   p.plan = reinterpret_cast<SeqPlan*>(ws + lay.plan);
   p.tickets = reinterpret_cast<int*>(ws + lay.tickets);
+  p.ready = reinterpret_cast<int*>(ws + lay.ready);
   p.counters = reinterpret_cast<int*>(ws + lay.counters);
   p.lse = reinterpret_cast<float*>(ws + lay.lse);
   p.part = reinterpret_cast<float2*>(ws + lay.part);

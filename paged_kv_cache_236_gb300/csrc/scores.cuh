@@ -17,7 +17,9 @@ constexpr int kColChunk = 256;  // keys of a column unit (few rows)
 constexpr int kTcRange = 1024;  // keys of an item of the tensor-core kernel
 // Row tiles of a sequence the tensor-core kernel takes: a column item goes
 // through all of them (8 key tiles each, below 1 us a tile), and the waits of
-// the roles that stand by, up to two items long, end after 2 s.
+// the roles that stand by, up to two items long, end after 2 s.  (What one
+// closing warp does before a column item is one row tile's, whatever the
+// sequence: 4 rows a lane over at most 2^20 ranges of keys, some 0.5 s.)
 constexpr int kMaxRowTiles = 1 << 16;
 constexpr int kChunk = 256;   // keys of a work unit (more rows in fp32)
 enum { kFew = 1, kTensor = 2, kOther = 3 };
@@ -49,7 +51,8 @@ struct ScoreParams {
   float* out;
   int64_t* off[kQueues];  // [B + 1] each: first unit of each sequence in the queues
   SeqPlan* plan;    // [B]
-  int* tickets;     // tensor-core kernel: [B, Hkv] partials done, then [B, Hkv] lse ready
+  int* tickets;     // tensor-core kernel: stats items done of each row tile (tile_ticket)
+  int* ready;       // [B, Hkv] row tiles whose lse are complete
   int* counters;    // next of the tensor-core kernel's and of the few-row kernel's queue
   float2* part;     // (m, l) per (kv head, row, chunk) of a sequence
   float* lse;       // per (kv head, row) of a sequence
@@ -69,6 +72,14 @@ struct ScoreParams {
   uint64_t wait_ns;
   int fault_tile;
 };
+
+// Row tiles that a call may have for each kv head, at most, and the ticket of
+// one.  Sequences' ranges of queries are disjoint and ascend, so tiles counted
+// from floor(first query / tokens a tile) + s never meet another sequence's.
+__host__ __device__ constexpr int64_t most_tiles(int64_t B, int64_t T, int tile_tok) { return T / tile_tok + B; }
+__device__ __forceinline__ int* tile_ticket(const ScoreParams& p, int s, int h, int qstart, int tiles, int tile) {
+  return p.tickets + ((int64_t)(qstart / p.tile_tok + s) * p.Hkv + (int64_t)h * tiles + tile);
+}
 
 // The sequence s with off[s] <= u < off[s + 1] (the whole warp calls it).
 __device__ __forceinline__ int find_seq(const int64_t* off, int B, int64_t u, int lane) {
@@ -90,8 +101,8 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void st_release(int* p, int v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void add_release(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 // Two E4M3 codes as an fp16 pair, exactly.

@@ -6,8 +6,8 @@
 //
 // With z[r][j] = scale * log2(e) * q_r . k_j for the rows r of one kv head:
 //   stats items    rows on M:  S = Q K^T, (max, sum of exp2) of each row over
-//                  a range of keys; a head's last item to be closed combines
-//                  them to lse[r];
+//                  a range of keys; a row tile's last item to be closed
+//                  combines them to lse[r];
 //   column items   keys on M:  S^T = K Q^T, so that a thread holds one key's
 //                  logits of all rows: paid[j] = sum_r exp2(z[r][j] - lse[r])
 //                  is a sum within the thread, and no weight leaves it.
@@ -55,9 +55,11 @@
 //   warps 4-11   two groups of 128 threads (thread = accumulator lane), which
 //                take the item's tiles in turn;
 //   warp 12      closes stats items: when both groups have written an item's
-//                partials it counts the item, and the head's last one makes it
-//                combine the rows' lse and announce them; the groups go on
-//                without a fence or a wait for the count;
+//                partials it counts the item, and the row tile's last one makes
+//                it combine the rows' lse and announce them; the groups go on
+//                without a fence or a wait for the count (all rows of a head,
+//                by its last item, were rows * ranges partials for one warp to
+//                read while the columns waited);
 //   warps 14-21  (FP8) converters: 8 warps took 139 us where 4 took 148 (prompt
 //                windows) and 227 us against 237 (verify batch); 130 and 204 us
 //                with two issuers.
@@ -212,7 +214,6 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
   pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const uint32_t smem_base = smem_u32(smem);
-  int* ready = p.tickets + (int64_t)p.B * p.Hkv;
 
   if (warp == 2) {
     // ================================================================ items
@@ -294,7 +295,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
           bool ok = true;
           if (lane == 0) {
             const uint64_t t0 = globaltimer();
-            while (ld_acquire(ready + (int64_t)s * p.Hkv + item.h) == 0) {
+            while (ld_acquire(p.ready + (int64_t)s * p.Hkv + item.h) != sp.tiles) {
               if (globaltimer() - t0 > wc.limit_ns) {
                 raise_error(p.err, PKV_DEVERR_TIMEOUT);
                 ok = false;
@@ -455,19 +456,19 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
       if (!wait_all(&bars->item_closed[sl], ph, wc)) break;
       if (lane == 0) mbar_arrive(&bars->item_empty[sl]);
       if (im.type != kStats) continue;
-      const int64_t sh = (int64_t)im.s * p.Hkv + im.h;
       // the groups' writes are ordered before this fence by their arrivals
       __threadfence();
       int done = 0;
-      if (lane == 0) done = atomicAdd(p.tickets + sh, 1);
-      if (__shfl_sync(0xffffffffu, done, 0) != im.chunks * im.all_tiles - 1) continue;
-      // the head's last item: each row's lse from its partials, two a chunk
+      if (lane == 0) done = atomicAdd(tile_ticket(p, im.s, im.h, im.qstart, im.all_tiles, im.tile0), 1);
+      if (__shfl_sync(0xffffffffu, done, 0) != im.chunks - 1) continue;
+      // the row tile's last item: each row's lse from its partials, two a chunk
       __threadfence();
-      const int parts = 2 * im.chunks;
-      for (int r = lane; r < im.rows; r += 32) {
+      const int parts = 2 * im.chunks, tile_rows = p.tile_tok * p.G;
+      const int end = min(im.rows, (im.tile0 + 1) * tile_rows);
+      for (int r = im.tile0 * tile_rows + lane; r < end; r += 32) {
         const float4* part = reinterpret_cast<const float4*>(p.part + im.part + ((int64_t)im.h * im.rows + r) * parts);
         float m = -CUDART_INF_F, l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int c = 0; c < im.chunks; ++c) {
           const float4 v = __ldcg(part + c);
           const float mn = fmax3(m, v.x, v.z);
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
       }
       __threadfence();
       __syncwarp();
-      if (lane == 0) st_release(ready + sh, 1);
+      if (lane == 0) add_release(p.ready + (int64_t)im.s * p.Hkv + im.h, 1);
     }
   } else if (F8 && warp >= kFirstConverter) {
     // ================================================================ converters

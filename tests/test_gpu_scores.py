@@ -444,3 +444,40 @@ def test_wider_sequences_after_narrow_ones(Hkv, group, dtype):
         before = b.old.clone()
         b.check(b.run(out=b.old.clone(), max_query_len=most), before)
         assert pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("n,L", [(512, 1 << 20), (4096, 5000)])
+def test_many_row_tiles_over_many_ranges(n, L):
+    """The lse of a head's rows are combined row tile by row tile: 4096 rows
+    over 1024 ranges of keys are 8 million partials, which one warp would read
+    in tens of milliseconds while the column items wait.  No wait may last
+    longer than 10 ms here.
+
+    Tolerance: that of Batch.check, and the partials' running sum: each of the
+    ranges rescales it by an exponential (2^-22) and rounds twice (2^-24)."""
+    g = torch.Generator("cuda").manual_seed(n)
+    D, G, bs = 64, 8, 64
+    NB = -(-L // bs)
+    kc = torch.randn(NB, bs, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    q = torch.randn(n, G, D, generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randperm(NB, generator=g, device="cuda", dtype=torch.int32).view(1, NB)
+    old = torch.rand(1, 1, L, generator=g, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    call = lambda: pkv.paged_attention_scores(q, kc, table, i32([L]), i32([0, n]), old, 0.125, out=torch.empty_like(old))  # noqa: E731
+    call()  # sets up the kernel
+    pkv.debug_fault(0, 10_000_000)
+    got = call()
+    assert pkv.device_errors() == 0
+    Q, K = q.double().reshape(n * G, D), kc[table[0].long()].reshape(-1, D)[:L]
+    last = torch.arange(n, device="cuda").repeat_interleave(G).view(-1, 1) + (L - n)  # the key each row sees last
+    step = 8192
+    logits = lambda j: (Q @ K[j:j + step].double().T * 0.125).masked_fill_(  # noqa: E731
+        torch.arange(j, min(L, j + step), device="cuda") > last, -math.inf)
+    lse = torch.full((n * G, 1), -math.inf, dtype=torch.float64, device="cuda")
+    for j in range(0, L, step):
+        lse = torch.logaddexp(lse, logits(j).logsumexp(1, keepdim=True))
+    paid = torch.cat([(logits(j) - lse).exp_().sum(0) for j in range(0, L, step)])
+    want = paid + torch.where(torch.arange(L, device="cuda") < L - n, old[0, 0].double(), 0.0)
+    dots = float(Q.abs().amax(0) @ K.abs().amax(0).double())
+    rel = 2 * 0.125 * (D + 2) * 2.0 ** -24 * dots + 2 * 2.0 ** -22 + 1.3e-4 + -(-L // 1024) * (2.0 ** -22 + 2 * 2.0 ** -24)
+    assert torch.all((got[0, 0] - want).abs() <= rel * paid + 2.0 ** -22 * want + n * G * 2.0 ** -120)
