@@ -213,7 +213,17 @@ def workspace_min(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads
     return int(lib().paged_attention_workspace_min(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim))
 
 
-_ws_cache: dict = {}
+class _Scratch(threading.local):
+    """A thread's cached workspaces, per (device, stream).  A call is several
+    launches that pass its plan through the workspace, and it runs without the
+    interpreter's lock: two threads on one stream would put their launches
+    between one another's.  They go with the thread."""
+
+    def __init__(self):
+        self.buffers: dict = {}
+
+
+_scratch = _Scratch()
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
@@ -222,10 +232,10 @@ def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
         # wants more, and graphs captured on one stream may be replayed on two
         return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
-    ws = _ws_cache.get(key)
+    ws = _scratch.buffers.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        _ws_cache[key] = ws
+        _scratch.buffers[key] = ws
     return ws
 
 
@@ -239,14 +249,14 @@ def paged_attention_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     ``context_lens[s]`` counts sequence s's tokens after this step's write
     (its query tokens included); query i of n sits at position L - n + i.
     ``workspace`` (uint8, >= ``workspace_min``) defaults to a cached buffer
-    per (device, stream).  ``max_query_len`` is an optional host hint.
+    per (thread, device, stream).  ``max_query_len`` is an optional host hint.
     ``shared_prefix`` tells the call that consecutive sequences may start
     with the same physical blocks (prefix caching): runs of them then read
     their common prefix once (``PKV_HINT_SHARED_PREFIX``).
     """
     dev = _need_cuda(q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
-    args, out = _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, causal, out,
-                              workspace, max_query_len, shared_prefix, dev)
+    args, out, workspace = _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                         causal, out, workspace, max_query_len, shared_prefix, dev)
     with torch.cuda.device(dev):
         _check(lib().paged_attention_forward(*args))
     return out
@@ -254,7 +264,8 @@ def paged_attention_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
 
 def _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, causal, out, workspace,
                   max_query_len, shared_prefix, dev) -> tuple:
-    """Checks paged_attention_forward's tensors; returns (its C arguments, out)."""
+    """Checks paged_attention_forward's tensors; returns (its C arguments, out,
+    the workspace, to be kept until the call has returned)."""
     if q.dtype not in DTYPE or k_cache.dtype != q.dtype or v_cache.dtype != q.dtype:
         raise ValueError("q, k_cache, v_cache must share dtype bfloat16 or float32")
     if q.dim() != 3 or not q.is_contiguous():
@@ -289,7 +300,7 @@ def _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_l
             query_start_loc.data_ptr(), out.data_ptr(), B, T, Hq, Hkv, D, NB, bs, max(1, block_tables.shape[1]),
             int(max_query_len), float(scale), 1 if causal else 0, HINT_SHARED_PREFIX if shared_prefix else 0,
             workspace.data_ptr(), workspace.numel(), DTYPE[q.dtype], _stream(dev))
-    return args, out
+    return args, out, workspace
 
 
 def _new_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, Hkv: int, D: int, dtypes) -> tuple:
@@ -319,8 +330,8 @@ def paged_kv_write_attention_forward(k: torch.Tensor, v: torch.Tensor, slot_mapp
     fewer per step).  Same arguments and result as the two calls."""
     dev = _need_cuda(k, v, slot_mapping, q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
     Tn, ks, vs = _new_rows(k, v, slot_mapping, k_cache.shape[2], k_cache.shape[3], {k_cache.dtype})
-    args, out = _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, causal, out,
-                              workspace, max_query_len, shared_prefix, dev)
+    args, out, workspace = _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                         causal, out, workspace, max_query_len, shared_prefix, dev)
     with torch.cuda.device(dev):
         _check(lib().paged_kv_write_attention_forward(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), Tn, ks, vs,
                                                       *args))
@@ -592,8 +603,8 @@ def paged_attention_forward_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, v_cach
     """``paged_attention_forward`` over FP8 pools read as code * k_scale and
     code * v_scale; q and the result are bf16, head_dim 128."""
     dev = _need_cuda(q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
-    args, out = _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, k_scale,
-                                  v_scale, causal, out, workspace, max_query_len, dev)
+    args, out, workspace = _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                             k_scale, v_scale, causal, out, workspace, max_query_len, dev)
     with torch.cuda.device(dev):
         _check(lib().paged_attention_forward_fp8kv(*args))
     return out
@@ -612,8 +623,8 @@ def paged_kv_write_attention_forward_fp8kv(k: torch.Tensor, v: torch.Tensor, slo
     dev = _need_cuda(k, v, slot_mapping, q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
     _check_fp8_pools(k_cache, v_cache)
     Tn, ks, vs = _new_rows(k, v, slot_mapping, k_cache.shape[2], k_cache.shape[3], set(DTYPE))
-    args, out = _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, k_scale,
-                                  v_scale, causal, out, workspace, max_query_len, dev)
+    args, out, workspace = _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                             k_scale, v_scale, causal, out, workspace, max_query_len, dev)
     with torch.cuda.device(dev):
         _check(lib().paged_kv_write_attention_forward_fp8kv(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), Tn,
                                                             ks, vs, DTYPE[k.dtype], *args))
@@ -622,7 +633,8 @@ def paged_kv_write_attention_forward_fp8kv(k: torch.Tensor, v: torch.Tensor, slo
 
 def _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale, k_scale, v_scale,
                       causal, out, workspace, max_query_len, dev) -> tuple:
-    """Checks paged_attention_forward_fp8kv's tensors; returns (its C arguments, out)."""
+    """Checks paged_attention_forward_fp8kv's tensors; returns (its C arguments,
+    out, the workspace, to be kept until the call has returned)."""
     _check_fp8_pools(k_cache, v_cache)
     if q.dtype != torch.bfloat16 or q.dim() != 3 or not q.is_contiguous():
         raise ValueError("q must be contiguous bfloat16 [T, Hq, D]")
@@ -653,7 +665,7 @@ def _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_sta
             query_start_loc.data_ptr(), out.data_ptr(), B, T, Hq, Hkv, D, NB, bs, max(1, block_tables.shape[1]),
             int(max_query_len), float(scale), 1 if causal else 0, float(k_scale), float(v_scale), 0,
             workspace.data_ptr(), workspace.numel(), _stream(dev))
-    return args, out
+    return args, out, workspace
 
 
 # ----------------------------------------------------------------------------
@@ -856,7 +868,7 @@ def _check_scores(scores, Hkv, score_rows, B) -> tuple:
 def _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay, score_rows,
                  out, workspace, max_query_len, dev):
     """Checks paged_attention_scores' tensors; returns (its C arguments up to
-    the decay, (workspace, bytes), out)."""
+    the decay, the workspace, out)."""
     qs, pool, table = q.shape, k_cache.shape, block_tables.shape
     if len(qs) != 3 or not q.is_contiguous():
         raise ValueError("q must be contiguous [T, Hq, D]")
@@ -891,7 +903,7 @@ def _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores
             query_start_loc.data_ptr(), None if score_rows is None else score_rows.data_ptr(), scores.data_ptr(),
             out.data_ptr(), B, T, Hq, Hkv, D, NB, bs, width, rows, length, int(max_query_len),
             scale, 1 if causal else 0, decay)
-    return args, (workspace.data_ptr(), workspace.numel()), out
+    return args, workspace, out
 
 
 def paged_attention_scores(q: torch.Tensor, k_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -912,13 +924,13 @@ def paged_attention_scores(q: torch.Tensor, k_cache: torch.Tensor, block_tables:
     promises that no sequence has more queries (a sequence that does is flagged
     and left out).  The other arguments are ``paged_attention_forward``'s;
     ``workspace`` (uint8, >= ``scores_workspace_min``) defaults to the cached
-    buffer per (device, stream)."""
+    buffer per (thread, device, stream)."""
     dev = _device_of(q, k_cache, block_tables, context_lens, query_start_loc, scores, score_rows)
     if q.dtype not in DTYPE or k_cache.dtype != q.dtype:
         raise ValueError("q and k_cache must share dtype bfloat16 or float32")
     args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay,
                                  score_rows, out, workspace, max_query_len, dev)
-    _call(lib().paged_attention_scores, dev, *args, *ws, DTYPE[q.dtype])
+    _call(lib().paged_attention_scores, dev, *args, ws.data_ptr(), ws.numel(), DTYPE[q.dtype])
     return out
 
 
@@ -935,7 +947,7 @@ def paged_attention_scores_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, block_t
         raise ValueError("q must be bfloat16 with an FP8 cache")
     args, ws, out = _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores, scale, causal, decay,
                                  score_rows, out, workspace, max_query_len, dev)
-    _call(lib().paged_attention_scores_fp8kv, dev, *args, k_scale, *ws)
+    _call(lib().paged_attention_scores_fp8kv, dev, *args, k_scale, ws.data_ptr(), ws.numel())
     return out
 
 

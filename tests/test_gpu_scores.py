@@ -9,6 +9,7 @@ them) and the sums' (each running sum of up to 512 terms, rescaled with
 exponentials: 512 * 2^-22 < 1.3e-4).  Weights below 2^-126 flush to zero.
 """
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -481,3 +482,32 @@ def test_many_row_tiles_over_many_ranges(n, L):
     dots = float(Q.abs().amax(0) @ K.abs().amax(0).double())
     rel = 2 * 0.125 * (D + 2) * 2.0 ** -24 * dots + 2 * 2.0 ** -22 + 1.3e-4 + -(-L // 1024) * (2.0 ** -22 + 2 * 2.0 ** -24)
     assert torch.all((got[0, 0] - want).abs() <= rel * paid + 2.0 ** -22 * want + n * G * 2.0 ** -120)
+
+
+def test_two_threads_on_one_stream():
+    """Calls of different shapes from two threads, whose launches fall between
+    one another's on the stream they share: each has a workspace of its own, and
+    a third thread's larger calls leave theirs alone."""
+    many = [Batch(111, [900, 300, 2000], [1, 40, 3], 8, 2, 128, 16), Batch(112, [64] * 40, [1] * 40, 16, 4, 128, 16),
+            Batch(113, [6000, 5000], [70, 1], 8, 2, 128, 16)]
+    want = [b.run(out=b.old.clone()) for b in many]
+    outs = [[b.old.clone() for _ in range(60)] for b in many]
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(len(many)), []
+
+    def calls(b, mine):
+        try:
+            start.wait()
+            for out in mine:
+                b.run(out=out)
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=calls, args=a) for a in zip(many, outs)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and pkv.device_errors() == 0
+    for w, mine in zip(want, outs):
+        assert all(torch.equal(x, w) for x in mine)
