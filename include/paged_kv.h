@@ -400,6 +400,23 @@ void pkv_set_profile_mid_event(void* mid);
 pkv_status pkv_event_elapsed_ms(void* start, void* stop, float* ms);
 
 /*
+ * Scratch memory of captured calls.  A graph goes on using the workspace of
+ * the calls captured into it, so the caller keeps that memory for as long as
+ * the graph may run; these say when that ends.
+ *   pkv_capture_id     the id of the capture that `stream` is part of (unique in
+ *                      the process), 0 if it is not being captured
+ *   pkv_capture_watch  from now on the end of the graph that `stream` is being
+ *                      captured into is noted
+ *   pkv_capture_gone   takes one of the ids noted: its graph, what was cloned
+ *                      from it and everything instantiated are destroyed (or the
+ *                      capture came to nothing); 0 if there is none
+ * pkv_capture_watch outside a capture is PKV_ERR_INVALID_ARG.
+ */
+pkv_status pkv_capture_id(void* stream, uint64_t* id);
+pkv_status pkv_capture_watch(void* stream);
+pkv_status pkv_capture_gone(uint64_t* id);
+
+/*
  * pkv_debug_fault - testing hook for the bounded in-kernel waits (no
  * counterpart on the source pages).  Arms the next paged_attention_forward /
  * _fp8kv or paged_attention_scores / _fp8kv call made on this thread, and

@@ -115,6 +115,11 @@ def lib() -> ctypes.CDLL:
             L.pkv_event_elapsed_ms.argtypes = [c_vp, c_vp, ctypes.POINTER(c_f)]
             L.pkv_version.restype = ctypes.c_char_p
             L.pkv_version.argtypes = []
+            for name, args in (("pkv_capture_id", [c_vp, ctypes.POINTER(ctypes.c_uint64)]),
+                               ("pkv_capture_watch", [c_vp]),
+                               ("pkv_capture_gone", [ctypes.POINTER(ctypes.c_uint64)])):
+                getattr(L, name).restype = c_i32
+                getattr(L, name).argtypes = args
             L.pkv_debug_fault.restype = c_i32
             L.pkv_debug_fault.argtypes = [c_i32, c_i64]
             L.paged_kv_write_attention_forward.restype = c_i32
@@ -221,22 +226,69 @@ class _Scratch(threading.local):
 
     def __init__(self):
         self.buffers: dict = {}
+        self.pooled = 0  # id of a capture whose allocations a graph's memory pool serves
 
 
 _scratch = _Scratch()
+_graphs_hold: dict = {}  # capture id -> {stream: its workspaces, the one in use last}
+_graphs_lock = threading.Lock()
 
 
 def _workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
+    """Workspace of a call on dev's current stream (dev is the current device)."""
     if torch.cuda.is_current_stream_capturing():
-        # a graph keeps its own: a cached one is replaced when a later call
-        # wants more, and graphs captured on one stream may be replayed on two
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        return _graph_workspace(dev, nbytes)
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
     ws = _scratch.buffers.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
         _scratch.buffers[key] = ws
     return ws
+
+
+def _graph_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
+    """Workspace of a call that is being captured: the graph's own.  A cached
+    one is replaced when a later call wants more, and graphs captured on one
+    stream may be replayed on two.
+
+    Under ``torch.cuda.graph`` an allocation comes from the graph's memory
+    pool, which lasts as long as the graph.  Under any other capture it comes
+    from the memory all tensors share, so it is held here until the graph is
+    gone: one for each stream of the capture, which runs its calls in order."""
+    stream, found = _stream(dev), ctypes.c_uint64(0)
+    _check(lib().pkv_capture_id(stream, ctypes.byref(found)))
+    capture = found.value
+    with _graphs_lock:
+        _drop_graphs_gone()
+        first = capture not in _graphs_hold
+        if first and _scratch.pooled != capture and _in_graph_pool(torch.empty(1, dtype=torch.uint8, device=dev)):
+            _scratch.pooled = capture
+        if _scratch.pooled == capture:
+            return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        if first:
+            _check(lib().pkv_capture_watch(stream))
+        mine = _graphs_hold.setdefault(capture, {}).setdefault((dev.index, stream), [])
+        if not mine or mine[-1].numel() < nbytes:
+            mine.append(torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev))
+        return mine[-1]
+
+
+def _drop_graphs_gone() -> None:
+    """Gives up the workspaces of graphs that no longer exist (the lock held)."""
+    found = ctypes.c_uint64(0)
+    while True:
+        _check(lib().pkv_capture_gone(ctypes.byref(found)))
+        if found.value == 0:
+            return
+        _graphs_hold.pop(found.value, None)
+
+
+def _in_graph_pool(t: torch.Tensor) -> bool:
+    """Whether t's memory belongs to a private pool of the allocator."""
+    for segment in torch.cuda.memory_snapshot():
+        if 0 <= t.data_ptr() - segment["address"] < segment["total_size"]:
+            return tuple(segment.get("segment_pool_id", (0, 0))) != (0, 0)
+    return False
 
 
 def paged_attention_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -753,6 +805,14 @@ def _device_of(*tensors: torch.Tensor) -> int:
     return dev
 
 
+def _on(dev: int, fn, *args):
+    """fn(*args) with device dev current."""
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            return fn(*args)
+    return fn(*args)
+
+
 def _call(fn, dev: int, *args) -> None:
     """fn(*args, the current stream of device dev) with dev current."""
     if torch.cuda.current_device() != dev:
@@ -895,7 +955,7 @@ def _scores_args(q, k_cache, block_tables, context_lens, query_start_loc, scores
     width = max(1, table[1])
     context = min(length, width * bs)
     if workspace is None:
-        workspace = _workspace(q.device, scores_workspace_size(B, T, Hq, Hkv, context))
+        workspace = _on(dev, _workspace, q.device, scores_workspace_size(B, T, Hq, Hkv, context))
     elif workspace.dtype != torch.uint8 or workspace.get_device() != dev or \
             workspace.numel() < scores_workspace_min(B, T, Hq, Hkv, context):
         raise ValueError("workspace must be a uint8 CUDA tensor of at least scores_workspace_min bytes")
