@@ -627,7 +627,7 @@ struct Stats {
         if (ja >= vis[nt][e]) za[e] = -CUDART_INF_F;
         if (jb >= vis[nt][e]) zb[e] = -CUDART_INF_F;
         const float mn = fmax3(m[nt][e], za[e], zb[e]);
-        const float mu = mn == -CUDART_INF_F ? 0.f : mn;
+        const float mu = max_ref(mn);
         l[nt][e] = fmaf(l[nt][e], fast_exp2(m[nt][e] - mu), fast_exp2(za[e] - mu) + fast_exp2(zb[e] - mu));
         m[nt][e] = mn;
       }
@@ -648,7 +648,7 @@ struct Stats {
         float mm = m[nt][e];
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-        float ll = l[nt][e] * fast_exp2(m[nt][e] - (mm == -CUDART_INF_F ? 0.f : mm));
+        float ll = l[nt][e] * fast_exp2(m[nt][e] - max_ref(mm));
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
         const int r = nt * 8 + 2 * t + e;
@@ -669,16 +669,16 @@ __device__ __forceinline__ float row_lse(const float2* part, int chunks, int lan
       v[i] = c < chunks ? __ldcg(part + c) : make_float2(-CUDART_INF_F, 0.f);
     }
     const float mn = fmaxf(fmax3(m, v[0].x, v[1].x), fmaxf(v[2].x, v[3].x));
-    if (mn == -CUDART_INF_F) continue;
-    l *= fast_exp2(m - mn);
+    const float mu = max_ref(mn);
+    l *= fast_exp2(m - mu);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) l = fmaf(v[i].y, fast_exp2(v[i].x - mn), l);
+    for (int i = 0; i < 4; ++i) l = fmaf(v[i].y, fast_exp2(v[i].x - mu), l);
     m = mn;
   }
   float top = m;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  l = m == -CUDART_INF_F ? 0.f : l * fast_exp2(m - top);
+  l *= fast_exp2(m - max_ref(top));
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   return top + log2f(l);
@@ -817,8 +817,8 @@ __device__ __forceinline__ void rows_lse(const float2* part, int chunks, int row
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float mn = fmax3(m[r], v[r][0].x, v[r][1].x);
-      if (mn == -CUDART_INF_F) continue;
-      l[r] = l[r] * fast_exp2(m[r] - mn) + (v[r][0].y * fast_exp2(v[r][0].x - mn) + v[r][1].y * fast_exp2(v[r][1].x - mn));
+      const float mu = max_ref(mn);
+      l[r] = l[r] * fast_exp2(m[r] - mu) + (v[r][0].y * fast_exp2(v[r][0].x - mu) + v[r][1].y * fast_exp2(v[r][1].x - mu));
       m[r] = mn;
     }
   }
@@ -827,7 +827,7 @@ __device__ __forceinline__ void rows_lse(const float2* part, int chunks, int row
     float top = m[r];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float sum = m[r] == -CUDART_INF_F ? 0.f : l[r] * fast_exp2(m[r] - top);
+    float sum = l[r] * fast_exp2(m[r] - max_ref(top));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     lse[r] = r0 + r < rows ? top + log2f(sum) : CUDART_INF_F;
@@ -1081,7 +1081,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) stats_kernel(const 
         float mn = m[i];
 #pragma unroll
         for (int j = 0; j < kLaneKeys; ++j) mn = fmaxf(mn, z[i][j]);
-        const float mu = mn == -CUDART_INF_F ? 0.f : mn;
+        const float mu = max_ref(mn);
         l[i] *= fast_exp2(m[i] - mu);
 #pragma unroll
         for (int j = 0; j < kLaneKeys; ++j) l[i] += fast_exp2(z[i][j] - mu);
@@ -1093,7 +1093,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileBlocks) stats_kernel(const 
       float mm = m[i];
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-      float ll = l[i] * fast_exp2(m[i] - (mm == -CUDART_INF_F ? 0.f : mm));
+      float ll = l[i] * fast_exp2(m[i] - max_ref(mm));
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
       if (lane == 0 && row0 + i < sp.rows)

@@ -4,6 +4,7 @@
 
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <math_constants.h>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -104,6 +105,11 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 __device__ __forceinline__ void add_release(int* p, int v) {
   asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
+
+// The reference that the exponentials of a running maximum m are taken against.
+// A maximum of -inf is that of no keys or of logits of -inf, whose sum is 0, or
+// of logits that are all NaN, whose sum is NaN and has to stay so.
+__device__ __forceinline__ float max_ref(float m) { return m == -CUDART_INF_F ? 0.f : m; }
 
 // Two E4M3 codes as an fp16 pair, exactly.
 __device__ __forceinline__ uint32_t codes_to_f16(uint32_t two) {

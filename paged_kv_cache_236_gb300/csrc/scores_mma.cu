@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
         for (int c = 0; c < im.chunks; ++c) {
           const float4 v = __ldcg(part + c);
           const float mn = fmax3(m, v.x, v.z);
-          if (mn != -CUDART_INF_F) l = l * fast_exp2(m - mn) + (v.y * fast_exp2(v.x - mn) + v.w * fast_exp2(v.z - mn));
+          const float mu = max_ref(mn);
+          l = l * fast_exp2(m - mu) + (v.y * fast_exp2(v.x - mu) + v.w * fast_exp2(v.z - mu));
           m = mn;
         }
         p.lse[im.lse + (int64_t)im.h * im.rows + r] = m + log2f(l);

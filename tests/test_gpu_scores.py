@@ -511,3 +511,25 @@ def test_two_threads_on_one_stream():
     assert not failed and pkv.device_errors() == 0
     for w, mine in zip(want, outs):
         assert all(torch.equal(x, w) for x in mine)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("n", [1, 3, 4, 40])
+@pytest.mark.parametrize("first", [0, 1024])
+def test_keys_of_nan_among_others(first, n, dtype):
+    """A row that sees a NaN logit has no weights, also where the NaN keys fill
+    whole chunks of the sequence (1024 keys of 128, 256 and 1024 each), whose
+    maximum is none: all its keys get NaN.  The other kv head is as it was."""
+    L = 5000
+    b = Batch(135 + n, [L, 700], [n, n], 8, 2, 128, 16, torch.float32 if dtype == "f32" else torch.bfloat16,
+              dtype == "fp8")
+    want = b.run(out=b.old.clone())
+    for j in range(first, first + 1024):
+        b.kc[b.tables[0, j // 16], j % 16, 1] = 0x7F if dtype == "fp8" else math.nan
+    for workspace in (None, pkv.scores_workspace_min(2, 2 * n, 8, 2, b.old.shape[2])):
+        ws = None if workspace is None else torch.empty(workspace, dtype=torch.uint8, device="cuda")
+        got = b.run(out=b.old.clone(), workspace=ws)
+        assert torch.isnan(got[0, 1, :L]).all()
+        assert torch.isfinite(got[0, 0]).all() and torch.isfinite(got[1:]).all()
+        assert ws is not None or torch.equal(got[0, 0], want[0, 0]) and torch.equal(got[1:], want[1:])
+    assert pkv.device_errors() == 0
