@@ -850,6 +850,19 @@ __device__ __forceinline__ void few_columns(const ScoreParams& p, const SeqPlan&
     if (lane < 4) lse[r0 + lane] = lane == 0 ? x[0] : lane == 1 ? x[1] : lane == 2 ? x[2] : x[3];
   }
   __syncwarp();
+  // The last n - 1 keys, which not every row sees: a logit of -inf keeps a row
+  // out, but for one whose lse is NaN.
+  const int part = max(kb, sp.L - sp.n + 1);
+  if (p.causal && part < ke && __any_sync(0xffffffffu, lane < sp.rows && isnan(lse[min(lane, sp.rows - 1)]))) {
+    const int j = part + lane;  // n - 1 keys are fewer than kFewRows
+    if (j < ke) {
+      float paid = 0.f;
+#pragma unroll 1
+      for (int r = (j - (sp.L - sp.n)) * p.G; r < sp.rows; ++r) paid += fast_exp2(__ldcg(z + (int64_t)j * pad + r) - lse[r]);
+      p.out[at + j] = paid;
+    }
+    ke = part;
+  }
 #pragma unroll 1
   for (int j0 = kb + lane; j0 - lane < ke; j0 += kAt * 32) {
     float paid[kAt], old[kAt];

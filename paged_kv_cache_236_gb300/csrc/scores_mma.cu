@@ -152,15 +152,22 @@ __device__ __forceinline__ int tiles_seen(const ScoreParams& p, const Item& im, 
 }
 
 // Column items: 32 logits of one key against rows' negated lse: the sum of
-// their weights (in four running sums).
-__device__ __forceinline__ void add_weights(const uint32_t (&z)[32], const float* nlse, f32x2 scale2, f32x2 (&sum)[2]) {
+// their weights (in four running sums); kSome: of the rows in the mask alone,
+// the others weigh nothing, whatever their logits and lse (NaN too).
+template <bool kSome>
+__device__ __forceinline__ void add_weights(const uint32_t (&z)[32], const float* nlse, f32x2 scale2, uint32_t mask,
+                                            f32x2 (&sum)[2]) {
+  auto weight = [&](float x, int e) {
+    const float w = fast_exp2(x);
+    return !kSome || (mask >> e & 1) ? w : 0.f;
+  };
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
     const float4 b = *reinterpret_cast<const float4*>(nlse + i);
     const float2 x0 = up2(fma2(pk2(__uint_as_float(z[i]), __uint_as_float(z[i + 1])), scale2, pk2(b.x, b.y)));
     const float2 x1 = up2(fma2(pk2(__uint_as_float(z[i + 2]), __uint_as_float(z[i + 3])), scale2, pk2(b.z, b.w)));
-    sum[0] = add2(sum[0], pk2(fast_exp2(x0.x), fast_exp2(x0.y)));
-    sum[1] = add2(sum[1], pk2(fast_exp2(x1.x), fast_exp2(x1.y)));
+    sum[0] = add2(sum[0], pk2(weight(x0.x, i), weight(x0.y, i + 1)));
+    sum[1] = add2(sum[1], pk2(weight(x1.x, i + 2), weight(x1.y, i + 3)));
   }
 }
 
@@ -684,11 +691,12 @@ __global__ void __launch_bounds__(Lay<D, F8>::kThreads, 1) scores_mma_kernel(con
             tmem_ld32(lane_base + acc * 128 + c, z);
             tmem_wait_ld();
             if (!__all_sync(0xffffffffu, from <= c) || c + 32 > nr) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e < from || c + e >= nr) z[e] = 0xff800000u;  // -inf
+              // rows from .. nr - 1
+              const uint32_t below = from - c >= 32 ? ~0u : (1u << max(0, from - c)) - 1u;
+              add_weights<true>(z, nl + c, scale2, (nr - c >= 32 ? ~0u : (1u << (nr - c)) - 1u) & ~below, sum);
+            } else {
+              add_weights<false>(z, nl + c, scale2, ~0u, sum);
             }
-            add_weights(z, nl + c, scale2, sum);
           }
           tc_fence_before();
           __syncwarp();

@@ -533,3 +533,29 @@ def test_keys_of_nan_among_others(first, n, dtype):
         assert torch.isfinite(got[0, 0]).all() and torch.isfinite(got[1:]).all()
         assert ws is not None or torch.equal(got[0, 0], want[0, 0]) and torch.equal(got[1:], want[1:])
     assert pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("Hq,n", [(2, 4), (8, 3), (8, 4), (8, 40), (6, 150)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_of_nan_keep_to_what_they_see(causal, Hq, n, dtype):
+    """A NaN query makes the weights of the keys it sees NaN, and leaves those
+    of the step's later tokens, which it does not see, to the other rows."""
+    lens = [700, 1500, 300]
+    b = Batch(141 + Hq + n, lens, [n] * 3, Hq, 2, 128, 16, torch.float32 if dtype == "f32" else torch.bfloat16,
+              dtype == "fp8")
+    group, at = Hq // 2, n // 2 - 1
+    plain = b.run(causal, decay=0.0, out=b.old.clone())
+    b.check(plain, b.old, causal=causal, decay=0.0)
+    b.q[n + at, group:] = math.nan  # of the second sequence, the second kv head's
+    for workspace in (None, pkv.scores_workspace_min(3, 3 * n, Hq, 2, min(b.old.shape[2], b.tables.shape[1] * 16))):
+        ws = None if workspace is None else torch.empty(workspace, dtype=torch.uint8, device="cuda")
+        got = b.run(causal, decay=0.0, out=b.old.clone(), workspace=ws)
+        seen = 1500 - n + at + 1 if causal else 1500
+        assert torch.isnan(got[1, 1, :seen]).all()
+        if ws is None:
+            assert torch.equal(got[0], plain[0]) and torch.equal(got[2:], plain[2:]) and torch.equal(got[1, 0], plain[1, 0])
+        # the other rows' weights, one after another in another order: at most n * group additions of 2^-24 of the sum
+        assert torch.allclose(got[1, 1, seen:1500], plain[1, 1, seen:1500], rtol=5e-4 + n * group * 2.0 ** -23, atol=0)
+        assert torch.equal(got[1, 1, 1500:], plain[1, 1, 1500:])
+    assert pkv.device_errors() == 0
