@@ -144,7 +144,8 @@ pkv_status paged_kv_write(const void* k, const void* v, const int64_t* slot_mapp
  * rotated q; the pools get the rotated k and v as it is, at slot_mapping (as
  * paged_kv_write: slots < 0 are skipped, slots past the pool too, with
  * PKV_DEVERR_SLOT_OUT_OF_RANGE; q_out gets every token).  Rotated in fp32,
- * angles reduced exactly for any int64 position, rounded once.
+ * rounded once; angles are reduced to fp32's precision at any int64 position,
+ * for frequencies of magnitude below 2^32.
  *
  *   q           device, [num_tokens, num_q_heads, head_dim], token stride
  *               q_token_stride ELEMENTS (>= num_q_heads*head_dim; 0 means dense)

@@ -11,11 +11,10 @@
 //
 // The angle: a position of 2^17 and a frequency of 1 leave an fp32 product
 // 2^-7 radians off, so the angle is kept in turns as a 64-bit fraction: the
-// frequency in turns per position, a multiple of 2^-64 (its 53-bit mantissa
-// times 2^64 / (2 pi), shifted: integer arithmetic, the SM's fp64 units are
-// few), times the position modulo 2^64 is the fraction of a turn exactly but
-// for the frequency's own 2^-53.  sincospif of its signed value is then good to
-// fp32.
+// frequency in turns per position, a multiple of 2^-64 or, for far positions,
+// 2^-128 (its 53-bit mantissa times 2^64 / (2 pi), shifted: integer arithmetic,
+// the SM's fp64 units are few), times the position modulo 1.  sincospif of its
+// signed value, rounded to fp32, is then good to fp32.
 //
 // HBM-bound: q, k and v are read once and q_out and the pool rows written
 // once; a separate rotation would move q and k twice.  A warp takes one token,
@@ -62,6 +61,8 @@ struct RopeParams {
 constexpr int kWarps = 4;   // of a block
 constexpr int kBatch = 2;   // heads a lane loads at a time
 
+typedef unsigned __int128 u128;
+
 template <typename U, int N>
 struct alignas(sizeof(U) * N) Vec {
   U e[N];
@@ -98,22 +99,34 @@ __device__ __forceinline__ void store_rows(U* dst, const float (&x)[N]) {
   *reinterpret_cast<Vec<U, N>*>(dst) = o;
 }
 
-// Turns per position, times 2^64 (modulo 2^64), of a frequency in radians per
-// position: |f| = m * 2^(e - 52) with a whole m < 2^53, and 2^64 / (2 pi) as a
-// whole number.
-__device__ __forceinline__ uint64_t turns_of(double f) {
+// The fraction of a turn, times 2^64, at a position, of a frequency in radians
+// per position: |f| = m * 2^(e - 52) with a whole m < 2^53, and 1 / (2 pi) as a
+// whole number of 2^-64 or 2^-128.
+//
+// Positions of 32 bits and frequencies below 2: a frequency in turns of 2^-64 is
+// off by at most 3 of them, the angle by 2^-31 of a turn.  Others (3 % of a mixed
+// step's time where all took it): turns of 2^-128, the top half of the
+// product's 128 bits, a position's sign in its weight of 2^64.
+__device__ __forceinline__ int64_t angle_of(int64_t pos, double f) {
   const uint64_t bits = (uint64_t)__double_as_longlong(f);
   const int e = (int)((bits >> 52) & 2047) - 1023;
   const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e == -1023 ? 0 : 1ull << 52);
-  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;
-  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
-  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * kInv2Pi >> sh
-  uint64_t r;
-  if (sh >= 128) r = 0;
-  else if (sh >= 64) r = hi >> (sh - 64);
-  else if (sh > 0) r = (lo >> sh) | (hi << (64 - sh));
-  else r = sh > -64 ? lo << -sh : 0;
-  return bits >> 63 ? 0 - r : r;
+  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull, kInv2PiLow = 0x7F09D5F47D4D3770ull;
+  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * 2^(64 or 128) / (2 pi) >> sh
+  if (pos == (int)pos && e <= 0) {
+    const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+    const uint64_t r = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
+    return pos * (int64_t)(bits >> 63 ? 0 - r : r);
+  }
+  const u128 low = (u128)m * kInv2PiLow, high = (u128)m * kInv2Pi + (uint64_t)(low >> 64);  // high * 2^64 + low's low half
+  u128 r;
+  if (sh >= 192) r = 0;
+  else if (sh >= 64) r = high >> (sh - 64);
+  else if (sh >= 0) r = (high << (64 - sh)) | (uint64_t)low >> sh;
+  else r = sh > -128 ? ((high << 64) | (uint64_t)low) << -sh : 0;
+  if (bits >> 63) r = 0 - r;
+  const uint64_t part = (uint64_t)r, p = (uint64_t)pos;
+  return (int64_t)(p * (uint64_t)(r >> 64) + __umul64hi(p, part) - (pos < 0 ? part : 0));
 }
 
 // F8: the pools hold E4M3 codes.  U: the rows' element (uint16_t: bf16 bits).
@@ -139,16 +152,15 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rope_write_kernel(const RopePa
     fetch(p.k, p.k_stride, p.Hkv);
     fetch(p.v, p.v_stride, p.Hkv);
   }
-  const uint64_t pos = (uint64_t)p.positions[tok];
+  const int64_t pos = p.positions[tok];
   int64_t slot = p.slots[tok];
   if (slot >= p.num_slots) {
     if (lane == 0 && split == 0) raise_error(p.err, PKV_DEVERR_SLOT_OUT_OF_RANGE);
     slot = -1;
   }
   for (int j = lane; j < p.half; j += 32) {
-    const long long ang = (long long)(pos * turns_of(p.inv_freq[j]));
     float s, c;
-    sincospif(__ll2float_rn(ang) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
+    sincospif(__ll2float_rn(angle_of(pos, p.inv_freq[j])) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
     trig[j] = make_float2(c * p.amp, s * p.amp);
   }
   __syncwarp();

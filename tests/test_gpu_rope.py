@@ -245,3 +245,50 @@ def test_one_token_of_any_stride_and_repeated_rows():
         rows = [many if i == at else dense for i in range(3)]
         with pytest.raises(ValueError):
             pkv.paged_kv_write_rope(*rows, i64([0, 1, 2]), f, i64([0, 1, 2]), kc, vc)
+
+
+def _turns(positions, inv_freq):
+    """Fractions of a turn of positions x frequencies, in integers: 1 / (2 pi) to
+    400 bits by Machin's formula, frequencies as the rationals they are."""
+    one = 1 << 400
+
+    def arctan_of_1_over(x):
+        total = term = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+    two_pi = 8 * (4 * arctan_of_1_over(5) - arctan_of_1_over(239))
+    out = np.empty((len(positions), len(inv_freq)))
+    for i, f in enumerate(inv_freq):
+        num, den = float(f).as_integer_ratio()
+        for t, p in enumerate(positions):
+            turns = ((int(p) * num * one << 400) // (den * two_pi)) % one
+            out[t, i] = turns / one
+    return out
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_positions_of_any_size(interleaved):
+    """Every int64 position, to its ends, and frequencies up to 2^31, of either
+    sign: the bound of the near positions."""
+    pos = [1 << 31, (1 << 40) + 12345, 1 << 50, -(1 << 50) - 7, 3 * (1 << 60) + 99, (1 << 63) - 1, -(1 << 63), -(1 << 62) + 1]
+    inv = pkv.rope_frequencies(64)
+    inv[1], inv[5], inv[9], inv[13], inv[17] = 1e-300, 0.0, -0.3, 1000.1, float(2 ** 31) + 0.7
+    n = len(pos)
+    q, k, v = make(17, n, 3, 2, 64, torch.float32)
+    kc = torch.zeros(1, 16, 2, 64, device="cuda")
+    out = pkv.paged_kv_write_rope(q, k, v, torch.tensor(pos, dtype=torch.int64, device="cuda"), inv,
+                                  torch.arange(n, device="cuda"), kc, kc.clone(), interleaved=interleaved)
+    a = 2 * np.pi * _turns(pos, inv.cpu().numpy())
+    c, s = np.cos(a)[:, None], np.sin(a)[:, None]
+    first, second = (slice(0, 64, 2), slice(1, 64, 2)) if interleaved else (slice(0, 32), slice(32, 64))
+    for got, x in ((to_f64(out), to_f64(q)), (to_f64(kc)[0, :n], to_f64(k))):
+        want = np.empty_like(x)
+        want[..., first] = x[..., first] * c - x[..., second] * s
+        want[..., second] = x[..., second] * c + x[..., first] * s
+        # 2^31 * 2^-63 of a turn more than near positions, below 2e-9 radians
+        tol = 4.2e-7 * pair_sums(x, 64, interleaved)
+        assert np.all(np.abs(got - want) <= tol + 2.0 ** -24 * np.abs(want))
