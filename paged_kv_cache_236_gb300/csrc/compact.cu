@@ -149,13 +149,12 @@ struct ScoreMover {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       v.to[i] = -1;
-      if (l.src[i] < 0 || l.src[i] == l.r[i] || l.r[i] >= max_len) continue;
+      if (l.src[i] < 0) continue;
+      const bool past = l.src[i] >= max_len;
+      bad |= past;
+      if (l.src[i] == l.r[i] || l.r[i] >= max_len) continue;
       v.to[i] = l.r[i];
-      v.x[i] = 0.f;
-      if (l.src[i] < max_len)
-        v.x[i] = sc[l.src[i]];
-      else
-        bad = true;
+      v.x[i] = past ? 0.f : sc[l.src[i]];
     }
   }
   __device__ __forceinline__ void store(const Slot& v) {

@@ -224,3 +224,21 @@ def test_compact_bad_inputs():
                 dict(k_cache=kc[:, :, :, :32])):
         with pytest.raises(ValueError):
             pkv.paged_kv_compact(**{**dict(k_cache=kc, v_cache=vc, block_tables=i32(tables), kept=i32([[[1]]])), **bad})
+
+
+@pytest.mark.parametrize("kept,scores", [([0, 1, 2, 3, 4, 5], [0, 1, 2, 3]),    # stay where they are
+                                         ([0, 1, 3, 5, 6, 7], [0, 1, 3, None]),  # go past the scores too
+                                         ([0, 1, 2, 3, 9, -1], [0, 1, 2, 3])])
+def test_compact_positions_past_the_scores(kept, scores):
+    """A kept position that the running scores have no place for is reported,
+    whether its row moves or not, and whether it has a place after the move."""
+    rng = np.random.default_rng(9)
+    kc, vc = make_pool(rng, 4, 16, 1, 64, "bf16"), make_pool(rng, 4, 16, 1, 64, "bf16")
+    sc = torch.tensor([[[10.0, 11.0, 12.0, 13.0]]], device="cuda")
+    want = [0.0 if j is None else 10.0 + j for j in scores]
+    was = bits(kc).copy()
+    pkv.paged_kv_compact(kc, vc, i32([[2]]), i32([[kept]]), scores=sc)
+    assert pkv.device_errors() == pkv.DEVERR["block_out_of_range"]
+    assert sc.cpu().tolist() == [[want]]
+    live = [j for j in kept if j >= 0]
+    assert np.array_equal(bits(kc)[2, :len(live)], was[2, live])
