@@ -559,3 +559,20 @@ def test_rows_of_nan_keep_to_what_they_see(causal, Hq, n, dtype):
         assert torch.allclose(got[1, 1, seen:1500], plain[1, 1, seen:1500], rtol=5e-4 + n * group * 2.0 ** -23, atol=0)
         assert torch.equal(got[1, 1, 1500:], plain[1, 1, 1500:])
     assert pkv.device_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "fp8"])
+@pytest.mark.parametrize("most", [0, 4])
+@pytest.mark.parametrize("qsl,good", [([0, 4, 0, 4, 5], [0, 3]), ([0, 2, 2, 1, 5], [0]), ([1, 0, 1, 3, 5], [2, 3]),
+                                      ([0, 3, 1, 4, 5], [0, 3]), ([0, 1, 5, 4, 5], [0, 1])])
+def test_overlapping_queries_are_reported(qsl, good, most, dtype):
+    """A query_start_loc entry below an earlier one makes its sequences invalid
+    (reported, their rows as they were); the others get the scores of the
+    queries that are theirs."""
+    b = Batch(151, [100, 60, 80, 50], [1, 2, 1, 1], 8, 2, 128, 16, torch.float32 if dtype == "f32" else torch.bfloat16,
+              dtype == "fp8")
+    b.qsl, b.qlens = np.array(qsl), np.diff(qsl).tolist()
+    before = b.old.clone()
+    got = b.run(out=b.old.clone(), query_start_loc=torch.tensor(qsl, dtype=torch.int32, device="cuda"), max_query_len=most)
+    assert pkv.device_errors() == pkv.DEVERR["bad_sequence"]
+    b.check(got, before, seqs=good)
