@@ -102,22 +102,15 @@ __device__ __forceinline__ void store_rows(U* dst, const float (&x)[N]) {
 // The fraction of a turn, times 2^64, at a position, of a frequency in radians
 // per position: |f| = m * 2^(e - 52) with a whole m < 2^53, and 1 / (2 pi) as a
 // whole number of 2^-64 or 2^-128.
-//
-// Positions of 32 bits and frequencies below 2: a frequency in turns of 2^-64 is
-// off by at most 3 of them, the angle by 2^-31 of a turn.  Others (3 % of a mixed
-// step's time where all took it): turns of 2^-128, the top half of the
-// product's 128 bits, a position's sign in its weight of 2^64.
-__device__ __forceinline__ int64_t angle_of(int64_t pos, double f) {
+constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull, kInv2PiLow = 0x7F09D5F47D4D3770ull;
+
+// Any position and frequency: turns of 2^-128, the top half of the product's 128
+// bits, a position's sign in its weight of 2^64.
+__device__ __noinline__ int64_t far_angle(int64_t pos, double f) {
   const uint64_t bits = (uint64_t)__double_as_longlong(f);
   const int e = (int)((bits >> 52) & 2047) - 1023;
   const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e == -1023 ? 0 : 1ull << 52);
-  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull, kInv2PiLow = 0x7F09D5F47D4D3770ull;
-  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * 2^(64 or 128) / (2 pi) >> sh
-  if (pos == (int)pos && e <= 0) {
-    const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
-    const uint64_t r = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
-    return pos * (int64_t)(bits >> 63 ? 0 - r : r);
-  }
+  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * 2^128 / (2 pi) >> sh
   const u128 low = (u128)m * kInv2PiLow, high = (u128)m * kInv2Pi + (uint64_t)(low >> 64);  // high * 2^64 + low's low half
   u128 r;
   if (sh >= 192) r = 0;
@@ -127,6 +120,20 @@ __device__ __forceinline__ int64_t angle_of(int64_t pos, double f) {
   if (bits >> 63) r = 0 - r;
   const uint64_t part = (uint64_t)r, p = (uint64_t)pos;
   return (int64_t)(p * (uint64_t)(r >> 64) + __umul64hi(p, part) - (pos < 0 ? part : 0));
+}
+
+// Positions of 32 bits and frequencies below 2: a frequency in turns of 2^-64 is
+// off by at most 3 of them, the angle by less than 2^-31 of a turn.  (The others' way for
+// all: 3 % of a mixed step's time.)
+__device__ __forceinline__ int64_t angle_of(int64_t pos, double f) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(f);
+  const int e = (int)((bits >> 52) & 2047) - 1023;
+  if (pos != (int)pos || e > 0) return far_angle(pos, f);
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e == -1023 ? 0 : 1ull << 52);
+  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * 2^64 / (2 pi) >> sh
+  const uint64_t r = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
+  return pos * (int64_t)(bits >> 63 ? 0 - r : r);
 }
 
 // F8: the pools hold E4M3 codes.  U: the rows' element (uint16_t: bf16 bits).
