@@ -14,7 +14,9 @@
 // frequency in turns per position, a multiple of 2^-64 or, for far positions,
 // 2^-128 (its 53-bit mantissa times 2^64 / (2 pi), shifted: integer arithmetic,
 // the SM's fp64 units are few), times the position modulo 1.  sincospif of its
-// signed value, rounded to fp32, is then good to fp32.
+// signed value, rounded to fp32, is then good to fp32: that last rounding, 24
+// bits over half a turn, makes the rotated value's error 5.5e-8 (RMS, relative)
+// where exact angles would leave 3.7e-8, below what any 16-bit output shows.
 //
 // HBM-bound: q, k and v are read once and q_out and the pool rows written
 // once; a separate rotation would move q and k twice.  A warp takes one token,
@@ -26,7 +28,7 @@
 // of 256 threads to one or two tokens with the angles read from shared memory
 // for every head, spent its time on instructions and the block's barrier
 // (16384 tokens into FP8 pools: 168 us, 82 this way: 4.5 TB/s; 4216 tokens in
-// bf16: 27 and 26 us).
+// bf16: 27 and 25 us).
 // Values are rotated in fp32 and rounded once, to the output's type: an FP8
 // pool takes the code of the fp32 value, with no rounding to the row's type
 // in between.

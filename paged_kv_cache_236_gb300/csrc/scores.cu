@@ -33,8 +33,9 @@
 // Every sum has a fixed order (no float atomics).
 //
 // Measured: the decode batch (64 sequences of 512 to 4096 tokens, 8 kv heads of
-// 128 in bf16) 77 us, 4.1 TB/s of K; 4 x 131072 keys 214 us, 5.2 TB/s.  Short
-// calls are bound by their two launches and one unit's latency (20 us).
+// 128 in bf16) 77 us, 3.9 TB/s of K's 302 MB; 4 x 131072 keys 214 us, 5.0 TB/s of
+// its 1.07 GB.  Short calls are bound by their three launches (the queue's
+// counter or the plan, the stats, the columns) and one unit's latency (20 us).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -358,7 +359,7 @@ __device__ __forceinline__ Held hold_plan(const ScoreParams& p, uint8_t* smem) {
 //
 // K comes through a ring of 16-key tiles in shared memory that is the warp's
 // own, by asynchronous copies issued kStages tiles ahead, across units: while
-// a warp ends one unit (partials, fence, ticket) the first tiles of its next
+// a warp ends one unit (its partials) the first tiles of its next
 // are on their way.  With the tiles loaded into registers, two ahead but none
 // across units, the decode batch took 95 us where the ring took 84 (77 us
 // now): a unit of 32 KB is 12 us of streaming at the rate a warp gets, and

@@ -16,14 +16,15 @@
 // What bounds it: the epilogue groups, with many rows.  A 128 x 128 tile is
 // 16384 exponentials in each pass and takes a group 1700 cycles, two groups at a
 // time, next to 512 cycles of MMA (64 queries of 4 heads on 8 sequences of 6000
-// to 16384 keys: 136 us; 128 queries: 241 us).  With few rows (a verify window
+// to 16384 keys: 120 us; 128 queries: 216 us).  With few rows (a verify window
 // of 40) K's 32 KB a tile from HBM instead, twice: 5 queries of 8 heads on 32 x
 // 8192 keys 177 us, 6.1 TB/s.
 // One thread that issued both groups' MMAs took 1500 cycles a tile and held
 // them up (192 us and, 128 queries, 282 us; with its warp converged, so that
 // descriptors and counters are uniform, 267 us).  Not faster: four groups of one
 // accumulator each, with that one issuer (128 queries: 390 us); TMEM loads a chunk ahead of
-// their use (278 us against 241).
+// their use (278 us against 241 then).  A row tile's lse combined by the warp that
+// closes it, instead of a head's by one, took 128 queries from 241 to 216 us.
 // All stats items come before the column items.  Interleaved, a sequence's
 // column items a short way behind its stats items so that they find K in L2,
 // the waits for the lse cost more than the reads (verify batch 199 to 280 us
