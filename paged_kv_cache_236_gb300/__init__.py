@@ -289,7 +289,11 @@ def _drop_graphs_gone() -> None:
 
 
 def _in_graph_pool(t: torch.Tensor) -> bool:
-    """Whether t's memory belongs to a private pool of the allocator."""
+    """Whether t's memory, allocated under a capture, is the graph's: of a private
+    pool of the allocator, or a node of the graph itself (cudaMallocAsync)."""
+    backend = torch.cuda.get_allocator_backend()
+    if backend != "native":  # which alone can say
+        return backend == "cudaMallocAsync"
     for segment in torch.cuda.memory_snapshot():
         if 0 <= t.data_ptr() - segment["address"] < segment["total_size"]:
             return tuple(segment.get("segment_pool_id", (0, 0))) != (0, 0)

@@ -4,7 +4,7 @@
 //
 // The graph carries a user object whose destructor the runtime calls once the
 // graph, its clones and everything instantiated from them are destroyed.  The
-// destructor may run on a thread of the driver, where no CUDA call is allowed:
+// destructor may run on a thread of CUDA's own, where no CUDA call is allowed:
 // it only notes the id.
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -135,11 +135,11 @@ def test_tensor_core_prefill_wait_runs_out(head_dim, fault_tile):
 
 
 def _scores_after_fault(dtype, head_dim, fault_tile):
-    """About seven stats items of one query tile and, after them, four column
-    items of two to a CTA; the loads that can be left out are the query tiles and
-    the first key tile to each."""
+    """About ten stats items of one query tile and, after them, five column items
+    of two to a CTA; the loads that can be left out are the query tiles and the
+    first key tile to each."""
     from test_gpu_scores import Batch
-    b = Batch(75 + head_dim, [4096 - 40 * i for i in range(16)], [40] * 16, 32, 8, head_dim, 16, f8=dtype == "fp8")
+    b = Batch(75 + head_dim, [4096 - 40 * i for i in range(24)], [40] * 24, 32, 8, head_dim, 16, f8=dtype == "fp8")
     want = b.run(out=b.old.clone())
     pkv.device_errors(clear=True)
     pkv.debug_fault(fault_tile, LIMIT_NS)
@@ -154,7 +154,7 @@ def _scores_after_fault(dtype, head_dim, fault_tile):
 
 
 @pytest.mark.parametrize("head_dim", [128, 64])
-@pytest.mark.parametrize("fault_tile", [1, 2, 3, 10, 17, 20])
+@pytest.mark.parametrize("fault_tile", [1, 2, 3, 10, 15, 24])
 def test_scores_wait_runs_out(head_dim, fault_tile):
     """Scores of 160 rows: the tensor-core kernel (item fetch, two producers,
     two issuers, the closer, two epilogue groups), a query tile and key tiles
@@ -162,7 +162,7 @@ def test_scores_wait_runs_out(head_dim, fault_tile):
     _scores_after_fault("bf16", head_dim, fault_tile)
 
 
-@pytest.mark.parametrize("fault_tile", [1, 2, 3, 10, 17, 20])
+@pytest.mark.parametrize("fault_tile", [1, 2, 3, 10, 15, 24])
 def test_scores_fp8_wait_runs_out(fault_tile):
     """The same over FP8 pools: the eight converter warps leave together,
     whichever of their waits (for a query tile, for codes, for the next item)

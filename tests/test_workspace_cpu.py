@@ -106,3 +106,19 @@ def test_captures_without_a_graph_pool_hold_one_workspace_a_stream(stubbed, monk
     x, y = pkv._workspace(CPU, 1000), pkv._workspace(CPU, 1000)
     assert x.data_ptr() != y.data_ptr() and state.watched == [41, 42]
     assert kept() is None and not pkv._graphs_hold
+
+
+def test_memory_of_other_allocators(monkeypatch):
+    """Allocators without a snapshot: cudaMallocAsync makes nodes of the graph,
+    of a pluggable one nothing is known."""
+    monkeypatch.setattr(torch.cuda, "memory_snapshot", lambda: pytest.fail("not meaningful"))
+    for backend, owned in (("cudaMallocAsync", True), ("pluggable", False)):
+        monkeypatch.setattr(torch.cuda, "get_allocator_backend", lambda: backend)
+        assert pkv._in_graph_pool(torch.empty(1)) is owned
+    t = torch.empty(1)
+    monkeypatch.setattr(torch.cuda, "get_allocator_backend", lambda: "native")
+    for pool, owned in (((0, 0), False), ((0, 3), True), ((5, 0), True)):
+        segments = [{"address": 0, "total_size": 1, "segment_pool_id": (7, 7)},
+                    {"address": t.data_ptr() - 64, "total_size": 4096, "segment_pool_id": pool}]
+        monkeypatch.setattr(torch.cuda, "memory_snapshot", lambda: segments)
+        assert pkv._in_graph_pool(t) is owned
