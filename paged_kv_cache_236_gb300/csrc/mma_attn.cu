@@ -619,10 +619,15 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
           exps(m_ref);
           named_barrier(pair_bar, 64);
           const float mx = fmaxf(mloc, redm[(h ^ 1) * 128 + r]) * p.scale_log2;
-          if (mx > m_ref + kRescaleThreshold) {
+          const bool raise = mx > m_ref + kRescaleThreshold;
+          if (raise) {
             alpha = fast_exp2(m_ref - mx);  // 0 when m_ref is -inf
             rescale = m_ref != -CUDART_INF_F;
             m_ref = mx;
+          }
+          // for one row or more: by the whole warp, as TMEM stores must be (the
+          // other rows write what they wrote)
+          if (__any_sync(0xffffffffu, raise)) {
             tmem_wait_st();  // the first pass's P pieces land before they are rewritten
             exps(m_ref);
           }
