@@ -221,6 +221,32 @@ pkv_status paged_attention_forward(const void* q, const void* k_cache, const voi
                                    pkv_dtype dtype, void* stream);
 
 /*
+ * paged_attention_window_forward - paged_attention_forward, causal, of layers
+ * in which a query sees only its last `window` tokens and the sequence's first
+ * `num_sink` ("sinks"): the query at position p = L - n + i attends the keys
+ * j <= p with j > p - window or j < num_sink.
+ *
+ *   window      1 .. 2^30 (the query's own key counts)
+ *   num_sink    0 .. 2^30
+ *   the rest    as paged_attention_forward (same shapes, workspace and errors)
+ * Blocks between the sinks and the first query's window are not read, and
+ * block_tables entries of blocks that no query of the call sees may be
+ * anything: a caller may have given them back.  Rows before every query's
+ * window may hold anything, infinities and NaN included; a row of V that one
+ * query of a sequence sees must be finite even where another does not see it
+ * (as for the causal mask of paged_attention_forward).
+ */
+pkv_status paged_attention_window_forward(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* query_start_loc, void* out,
+                                          int32_t num_seqs, int64_t num_tokens, int32_t num_q_heads,
+                                          int32_t num_kv_heads, int32_t head_dim, int64_t num_blocks,
+                                          int32_t block_size, int32_t max_blocks_per_seq,
+                                          int32_t max_query_len, float scale, int32_t window, int32_t num_sink,
+                                          void* workspace, size_t workspace_bytes, pkv_dtype dtype,
+                                          void* stream);
+
+/*
  * paged_kv_write_attention_forward - paged_kv_write of a step's new K/V rows
  * followed by paged_attention_forward over the pools, in one call and one
  * launch fewer ("ADR 004", Consequences: the model writes a layer's new K/V

@@ -17,6 +17,7 @@ tensors are not on a CUDA device, the calls raise.
     paged_attention_scores(q, k_cache, block_tables, ..., scores, scale)
     paged_kv_select(scores, context_lens, budget)
     paged_kv_compact(k_cache, v_cache, block_tables, kept)     (eviction)
+    paged_attention_window_forward(q, k_cache, v_cache, ..., scale, window, num_sink)
 
 Block pool per layer: ``[num_blocks, block_size, num_kv_heads, head_dim]``
 ("ADR 004: Paged Attention Serving Integration", Decision 4 - a per-layer
@@ -40,7 +41,7 @@ __all__ = [
     "paged_kv_write_attention_forward", "paged_kv_write_attention_forward_fp8kv",
     "paged_kv_write_rope", "paged_kv_write_rope_fp8", "rope_frequencies", "rope_amplitude",
     "paged_attention_scores", "paged_attention_scores_fp8kv", "scores_workspace_size", "scores_workspace_min",
-    "paged_kv_select", "paged_kv_compact",
+    "paged_kv_select", "paged_kv_compact", "paged_attention_window_forward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -148,6 +149,7 @@ def lib() -> ctypes.CDLL:
                     ("paged_attention_forward_fp8kv", [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i32, c_i64, c_i32,
                                                        c_i32, c_i32, c_i64, c_i32, c_i32, c_i32, c_f, c_i32, c_f,
                                                        c_f, c_i32, c_vp, c_sz, c_vp]),
+                    ("paged_attention_window_forward", L.paged_attention_forward.argtypes),
                     ("paged_kv_write_rope", _ROPE_ARGS + [c_vp]),
                     ("paged_kv_write_rope_fp8", _ROPE_ARGS + [c_f, c_f, c_vp]),
                     ("paged_attention_scores", _SCORES_ARGS + [c_vp, c_sz, c_i32, c_vp]),
@@ -320,6 +322,33 @@ def paged_attention_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
                                          causal, out, workspace, max_query_len, shared_prefix, dev)
     with torch.cuda.device(dev):
         _check(lib().paged_attention_forward(*args))
+    return out
+
+
+def _window(window: int, num_sink: int, least: int) -> tuple:
+    window, num_sink = int(window), int(num_sink)
+    if not least <= window <= 1 << 30 or not 0 <= num_sink <= 1 << 30:
+        raise ValueError(f"window must be in [{least}, 2^30] and num_sink in [0, 2^30]")
+    return window, num_sink
+
+
+def paged_attention_window_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                   query_start_loc: torch.Tensor, scale: float, window: int, num_sink: int = 0, *,
+                                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                                   max_query_len: int = 0) -> torch.Tensor:
+    """``paged_attention_forward``, causal, in which a query sees its last
+    ``window`` tokens (its own among them) and the sequence's first
+    ``num_sink``.
+
+    Blocks that no query of the call sees are not read: their table entries may
+    be anything, so that a cache manager may take them back."""
+    dev = _need_cuda(q, k_cache, v_cache, block_tables, context_lens, query_start_loc)
+    seen = _window(window, num_sink, 1)
+    args, out, workspace = _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                         True, out, workspace, max_query_len, False, dev)
+    with torch.cuda.device(dev):
+        _check(lib().paged_attention_window_forward(*args[:17], *seen, *args[19:]))
     return out
 
 

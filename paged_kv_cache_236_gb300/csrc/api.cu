@@ -374,7 +374,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
                                int32_t head_dim, int64_t num_blocks, int32_t block_size, int32_t max_blocks_per_seq,
                                int32_t max_query_len, float scale, int32_t causal, int32_t hints, void* workspace,
                                size_t workspace_bytes, pkv_dtype dtype, bool kv_fp8, float k_scale, float v_scale,
-                               void* stream, const FusedWrite* fw = nullptr) {
+                               void* stream, const FusedWrite* fw = nullptr, int window = 0, int num_sink = 0) {
   g_msg[0] = 0;
   const int B = num_seqs, Hq = num_q_heads, Hkv = num_kv_heads, D = head_dim, bs = block_size;
   const int64_t T = num_tokens;
@@ -390,6 +390,8 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   if (!(scale > 0.f) || !isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale must be positive and finite");
   if ((int64_t)max_blocks_per_seq * bs > (int64_t)1 << 30) return fail(PKV_ERR_UNSUPPORTED, "context too long");
   if (T > ((int64_t)1 << 31) / ((int64_t)Hq * D)) return fail(PKV_ERR_UNSUPPORTED, "num_tokens too large");
+  // a window that no context outgrows hides nothing
+  if ((int64_t)window >= (int64_t)max_blocks_per_seq * bs) window = 0;
   if (B == 0 || T == 0) {
     if (!fw || fw->n == 0) return PKV_OK;
     // nothing to attend: the write alone
@@ -417,7 +419,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   const int G = Hq / Hkv;
 
   int dec_ctas = 1;
-  cudaError_t e = kv_fp8 ? decode_fp8_ctas_per_sm(&dec_ctas) : decode_ctas_per_sm(bf16, D, &dec_ctas);
+  cudaError_t e = kv_fp8 ? decode_fp8_ctas_per_sm(&dec_ctas) : decode_ctas_per_sm(bf16, D, window > 0, &dec_ctas);
   if (e != cudaSuccess) return cuda_fail(e, "decode kernel set-up");
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -465,6 +467,8 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   pp.bs = bs;
   pp.max_blocks = max_blocks_per_seq;
   pp.causal = causal ? 1 : 0;
+  pp.window = window;
+  pp.num_sink = num_sink;
   pp.mma_ok = mma_launch ? 1 : 0;
   pp.cascade = cascade ? 1 : 0;
   // The decode kernel runs beside the tensor-core kernel, on the SMs the plan
@@ -569,6 +573,8 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   ap.scale_log2 = (kv_fp8 ? scale * k_scale : scale) * 1.4426950408889634f;
   ap.v_scale = kv_fp8 ? v_scale : 1.f;
   ap.causal = causal ? 1 : 0;
+  ap.window = window;
+  ap.num_sink = num_sink;
   ap.out_al32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
   ap.mma_unit_rows = (kMmaRows / G) * G;
   ap.err = dev->err;
@@ -636,6 +642,23 @@ pkv_status paged_attention_forward(const void* q, const void* k_cache, const voi
   return forward_impl(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, num_seqs, num_tokens,
                       num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, max_query_len,
                       scale, causal, hints, workspace, workspace_bytes, dtype, false, 1.f, 1.f, stream);
+}
+
+pkv_status paged_attention_window_forward(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, const int32_t* context_lens,
+                                          const int32_t* query_start_loc, void* out, int32_t num_seqs,
+                                          int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                          int32_t head_dim, int64_t num_blocks, int32_t block_size,
+                                          int32_t max_blocks_per_seq, int32_t max_query_len, float scale,
+                                          int32_t window, int32_t num_sink, void* workspace, size_t workspace_bytes,
+                                          pkv_dtype dtype, void* stream) {
+  g_msg[0] = 0;
+  if (window < 1 || num_sink < 0) return fail(PKV_ERR_INVALID_ARG, "window must be >= 1 and num_sink >= 0");
+  if (window > 1 << 30 || num_sink > 1 << 30) return fail(PKV_ERR_UNSUPPORTED, "window or num_sink above 2^30");
+  return forward_impl(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, num_seqs, num_tokens,
+                      num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, max_query_len,
+                      scale, 1, 0, workspace, workspace_bytes, dtype, false, 1.f, 1.f, stream, nullptr, window,
+                      num_sink);
 }
 
 pkv_status paged_kv_write_attention_forward(const void* k, const void* v, const int64_t* slot_mapping,

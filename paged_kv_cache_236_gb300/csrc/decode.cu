@@ -186,7 +186,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-template <typename T, typename KV, int D>
+// WIN: a query sees its last p.window keys and the first p.num_sink (Hole: the
+// tiles between them are not read).
+template <typename T, typename KV, int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
                                                              const __grid_constant__ CUtensorMap kmap,
                                                              const __grid_constant__ CUtensorMap vmap) {
@@ -255,10 +257,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
       const int n = p.query_start_loc[it.seq + 1] - qstart;
       const int nblk = (L + p.bs - 1) / p.bs;
       const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
-      auto block_of = [&](int kbase) -> int {  // physical block for this lane in the tile at kbase
-        const int lb = kbase / p.bs + lane;
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kDecTileKeys);  // WIN
+      auto block_of = [&](int kbase) -> int {  // physical block for this lane in the tile at place kbase
+        const int lb = (WIN ? hole.key(kbase) : kbase) / p.bs + lane;
         int phys = (int)p.num_blocks;  // out of range: the box reads as zeros
-        if (lane < nb_per_tile && lb < nblk) {
+        if (lane < nb_per_tile && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
           const int b = __ldg(bt + lb);
           if (b >= 0 && (int64_t)b < p.num_blocks)
             phys = b;
@@ -286,13 +289,13 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
         if (lane == 0) {
           Meta& m = meta[stage];
           m.item = idx;
-          m.kbase = kbase;
+          m.kbase = WIN ? hole.key(kbase) : kbase;
           m.flags = ((kbase + kDecTileKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
           m.seq = it.seq;
           m.kvh = it.kvh;
           m.row0 = it.row0;
           m.nrows = it.nrows;
-          m.ke = it.ke;
+          m.ke = WIN ? hole.end(it.ke) : it.ke;
           m.part = it.part;
           m.grp = it.grp;
           m.L = L;
@@ -330,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
   f32x2 acc[kRP][C::kDPL / 2];
   float m_row = -CUDART_INF_F, l_row = 0.f;
   int vis_row = 0;  // keys visible to row `myrow` (absolute key < vis_row)
+  int lo_row = 0, lo_item = 0;  // WIN: first key of the row's window, and of the item's first row's
   int tile = 0;
   for (;;) {
     const int stage = tile % C::kStages;
@@ -371,6 +375,10 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
       }
       const int tok = (mt.row0 + myrow) / p.G;
       vis_row = myrow < mt.nrows ? min(mt.ke, p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
+      if constexpr (WIN) {
+        lo_row = mt.L - mt.n + tok + 1 - p.window;
+        lo_item = mt.L - mt.n + mt.row0 / p.G + 1 - p.window;
+      }
     }
     const uint8_t* ks = sbase + warp * kWarpKeys * C::kRowBytes;
     const uint8_t* vs = ks + C::kTileBytes;
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
       }
       const float s = group_transpose_sum(part, lane);
       const int key = wkb + rnd * kKeysPerRound + grp * kTPR + (j / kRP);
-      sc[rnd] = key < vis_row ? s : -CUDART_INF_F;
+      sc[rnd] = key < vis_row && !(WIN && key < lo_row && key >= p.num_sink) ? s : -CUDART_INF_F;
     }
 
     // ---- online softmax for row `myrow` (lanes with equal lane % 4)
@@ -441,11 +449,12 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
     }
     __syncwarp();
 
-    // ---- acc += P V over this warp's keys that exist (keys >= ke may hold garbage)
+    // ---- acc += P V over this warp's keys that exist (keys >= ke, and those before
+    // every row's window, may hold garbage)
     const int kcount = max(0, min(kWarpKeys, mt.ke - wkb));
 #pragma unroll
     for (int kk = 0; kk < kWarpKeys; ++kk) {
-      if (kk < kcount) {
+      if (kk < kcount && !(WIN && wkb + kk < lo_item && wkb + kk >= p.num_sink)) {
         const ulonglong2 p01 = *reinterpret_cast<const ulonglong2*>(pw + kk * kRP);
         const ulonglong2 p23 = *reinterpret_cast<const ulonglong2*>(pw + kk * kRP + 2);
         const f32x2 pp[4] = {p01.x, p01.y, p23.x, p23.y};
@@ -540,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
 }
 
 // The dynamic shared-memory opt-in is a per-device function attribute.
-template <typename T, typename KV, int D>
+template <typename T, typename KV, int D, bool WIN>
 cudaError_t prepare_decode(int* ctas_per_sm) {
   using C = Cfg<T, KV, D>;
   static unsigned long long done_mask = 0;  // one bit per device ordinal (< 64)
@@ -550,10 +559,10 @@ cudaError_t prepare_decode(int* ctas_per_sm) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(decode_kernel<T, KV, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(decode_kernel<T, KV, D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     int occ = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_kernel<T, KV, D>, kThreads, C::kSmem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, decode_kernel<T, KV, D, WIN>, kThreads, C::kSmem);
     if (e != cudaSuccess) return e;
     occupancy[dev] = occ < 1 ? 1 : occ;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
@@ -562,13 +571,13 @@ cudaError_t prepare_decode(int* ctas_per_sm) {
   return cudaSuccess;
 }
 
-template <typename T, typename KV, int D>
+template <typename T, typename KV, int D, bool WIN>
 cudaError_t launch_decode_t(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
                             cudaStream_t s) {
   using C = Cfg<T, KV, D>;
-  cudaError_t e = prepare_decode<T, KV, D>(nullptr);
+  cudaError_t e = prepare_decode<T, KV, D, WIN>(nullptr);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(decode_kernel<T, KV, D>, dim3(grid), dim3(kThreads), C::kSmem, s, p, kmap, vmap);
+  e = launch_pdl(decode_kernel<T, KV, D, WIN>, dim3(grid), dim3(kThreads), C::kSmem, s, p, kmap, vmap);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -577,12 +586,18 @@ using e4m3_t = __nv_fp8_e4m3;
 
 }  // namespace
 
-cudaError_t decode_ctas_per_sm(bool bf16, int D, int* ctas) {
-  if (bf16) return D == 128 ? prepare_decode<bf16_t, bf16_t, 128>(ctas) : prepare_decode<bf16_t, bf16_t, 64>(ctas);
-  return D == 128 ? prepare_decode<float, float, 128>(ctas) : prepare_decode<float, float, 64>(ctas);
+cudaError_t decode_ctas_per_sm(bool bf16, int D, bool window, int* ctas) {
+  if (window) {
+    if (bf16)
+      return D == 128 ? prepare_decode<bf16_t, bf16_t, 128, true>(ctas) : prepare_decode<bf16_t, bf16_t, 64, true>(ctas);
+    return D == 128 ? prepare_decode<float, float, 128, true>(ctas) : prepare_decode<float, float, 64, true>(ctas);
+  }
+  if (bf16)
+    return D == 128 ? prepare_decode<bf16_t, bf16_t, 128, false>(ctas) : prepare_decode<bf16_t, bf16_t, 64, false>(ctas);
+  return D == 128 ? prepare_decode<float, float, 128, false>(ctas) : prepare_decode<float, float, 64, false>(ctas);
 }
 
-cudaError_t decode_fp8_ctas_per_sm(int* ctas) { return prepare_decode<bf16_t, e4m3_t, 128>(ctas); }
+cudaError_t decode_fp8_ctas_per_sm(int* ctas) { return prepare_decode<bf16_t, e4m3_t, 128, false>(ctas); }
 
 int decode_smem_bytes(int D, int elem_bytes) {
   if (elem_bytes == 2) return D == 128 ? Cfg<bf16_t, bf16_t, 128>::kSmem : Cfg<bf16_t, bf16_t, 64>::kSmem;
@@ -591,17 +606,24 @@ int decode_smem_bytes(int D, int elem_bytes) {
 
 cudaError_t launch_decode(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, bool bf16, int grid,
                           cudaStream_t s) {
-  if (bf16) {
-    return p.D == 128 ? launch_decode_t<bf16_t, bf16_t, 128>(p, kmap, vmap, grid, s)
-                      : launch_decode_t<bf16_t, bf16_t, 64>(p, kmap, vmap, grid, s);
+  if (p.window > 0) {
+    if (bf16)
+      return p.D == 128 ? launch_decode_t<bf16_t, bf16_t, 128, true>(p, kmap, vmap, grid, s)
+                        : launch_decode_t<bf16_t, bf16_t, 64, true>(p, kmap, vmap, grid, s);
+    return p.D == 128 ? launch_decode_t<float, float, 128, true>(p, kmap, vmap, grid, s)
+                      : launch_decode_t<float, float, 64, true>(p, kmap, vmap, grid, s);
   }
-  return p.D == 128 ? launch_decode_t<float, float, 128>(p, kmap, vmap, grid, s)
-                    : launch_decode_t<float, float, 64>(p, kmap, vmap, grid, s);
+  if (bf16) {
+    return p.D == 128 ? launch_decode_t<bf16_t, bf16_t, 128, false>(p, kmap, vmap, grid, s)
+                      : launch_decode_t<bf16_t, bf16_t, 64, false>(p, kmap, vmap, grid, s);
+  }
+  return p.D == 128 ? launch_decode_t<float, float, 128, false>(p, kmap, vmap, grid, s)
+                    : launch_decode_t<float, float, 64, false>(p, kmap, vmap, grid, s);
 }
 
 cudaError_t launch_decode_fp8(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid,
                               cudaStream_t s) {
-  return launch_decode_t<bf16_t, e4m3_t, 128>(p, kmap, vmap, grid, s);
+  return launch_decode_t<bf16_t, e4m3_t, 128, false>(p, kmap, vmap, grid, s);
 }
 
 }  // namespace pkv

@@ -269,8 +269,10 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
 
 // NR: rows per item (4, 8 or 16; the MMA's N stays 16, extra columns unused).
 // F8: the pools hold E4M3 codes (q bf16): staged codes are converted to fp16
-// tiles and the MMAs run on fp16 operands.
-template <int NR, bool F8>
+// tiles and the MMAs run on fp16 operands.  WIN: a query sees its last
+// p.window keys and the first p.num_sink; the tiles between them are not read
+// (Hole), nor are blocks that no row of the item sees.
+template <int NR, bool F8, bool WIN>
 __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnParams p,
                                                             const __grid_constant__ CUtensorMap qmap,
                                                             const __grid_constant__ CUtensorMap kmap,
@@ -379,10 +381,11 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
       }
       const int nblk = (L + p.bs - 1) / p.bs;
       const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
       auto block_of = [&](int kbase) -> int {  // physical block of this lane's block in the tile
-        const int lb = kbase / p.bs + lane;
+        const int lb = (WIN ? hole.key(kbase) : kbase) / p.bs + lane;
         int phys_ = (int)p.num_blocks;  // out of range: the box reads as zeros
-        if (lane < nb_per_tile && lb < nblk) {
+        if (lane < nb_per_tile && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
           const int b = __ldg(bt + lb);
           if (b >= 0 && (int64_t)b < p.num_blocks)
             phys_ = b;
@@ -434,13 +437,13 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
         if (lane == 0) {
           Meta& m = meta[F8 ? (g & 3) : st];
           m.item = idx;
-          m.kbase = kbase;
+          m.kbase = WIN ? hole.key(kbase) : kbase;
           m.flags = ((kbase + kKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
           m.seq = it.seq;
           m.kvh = it.kvh;
           m.row0 = it.row0;
           m.nrows = it.nrows;
-          m.ke = it.ke;
+          m.ke = WIN ? hole.end(it.ke) : it.ke;
           m.part = it.part;
           m.grp = it.grp;
           m.L = L;
@@ -505,9 +508,10 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
       const int qstart = p.query_start_loc[it.seq];
       const int n = p.query_start_loc[it.seq + 1] - qstart;
       const int nblk = (L + p.bs - 1) / p.bs;
-      const int lb = it.kb / p.bs + lane;
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
+      const int lb = (WIN ? hole.key(it.kb) : it.kb) / p.bs + lane;
       int phys = (int)p.num_blocks;  // out of range: the box reads as zeros
-      if (lane < nb_per_tile && lb < nblk) {
+      if (lane < nb_per_tile && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
         const int b = __ldg(p.block_tables + (int64_t)it.seq * p.max_blocks + lb);
         if (b >= 0 && (int64_t)b < p.num_blocks)
           phys = b;
@@ -676,11 +680,13 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
       const bool row_writer = (lane & ((1 << (5 - kLog)) - 1)) == 0;
       float m_ref[NR], lsum[NR];
       int vis[NR];
+      int lo[WIN ? NR : 1];  // first key of a row's window
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         m_ref[r] = -CUDART_INF_F;
         lsum[r] = 0.f;
         vis[r] = 0;
+        if constexpr (WIN) lo[r] = 0;
       }
       Meta mt{};
       int it_cnt = -1;
@@ -709,6 +715,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
               lsum[r] = 0.f;
               const int tok = (mt.row0 + r) / p.G;
               vis[r] = r < mt.nrows ? min(mt.ke, p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
+              if constexpr (WIN) lo[r] = mt.L - mt.n + tok + 1 - p.window;
             }
           }
           kbase = meta[mi].kbase;
@@ -726,7 +733,9 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
         float v[NR], a[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-          v[r] = key < vis[r] ? __uint_as_float(sraw[r]) : -CUDART_INF_F;
+          bool seen = key < vis[r];
+          if constexpr (WIN) seen = seen && (key >= lo[r] || key < p.num_sink);
+          v[r] = seen ? __uint_as_float(sraw[r]) : -CUDART_INF_F;
           a[r] = v[r];
         }
         const float wmax = xreduce<NR>(a, lane, MaxOp());
@@ -790,11 +799,14 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
             tmem_wait_st();
           }
         }
-        if (kbase + kKeys > mt.L && !pending) {
-          // keys at or past the sequence's end hold arbitrary bits: zero their V
-          // rows (after the tile has landed) so that 0 * V stays 0
+        // a tile that holds keys before every row's window (row 0's comes first)
+        const bool early = WIN && kbase < lo[0] && kbase + kKeys > p.num_sink;
+        if ((kbase + kKeys > mt.L || early) && !pending) {
+          // keys at or past the sequence's end hold arbitrary bits, as those before
+          // the windows may: zero their V rows (after the tile has landed) so that
+          // 0 * V stays 0
           pending = !wait_all(F8 ? &bars->vc_full[st] : &bars->v_full[st], (g / Y::kStages) & 1, wc);
-          if (!pending && key >= mt.L) {
+          if (!pending && (key >= mt.L || (WIN && key < lo[0] && key >= p.num_sink))) {
             uint4* v0 = reinterpret_cast<uint4*>(smem + st * kStageBytes + kTileBytes + t * 128);
             uint4* v1 = reinterpret_cast<uint4*>(smem + st * kStageBytes + kTileBytes + kHalf + t * 128);
 #pragma unroll
@@ -978,7 +990,7 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
   if (p.no_wait && threadIdx.x == 0) pdl_wait();
 }
 
-template <int NR, bool F8>
+template <int NR, bool F8, bool WIN>
 cudaError_t launch_dectc_t(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                            const CUtensorMap& vmap, int grid, cudaStream_t s) {
   static unsigned long long done_mask = 0;
@@ -987,11 +999,11 @@ cudaError_t launch_dectc_t(const AttnParams& p, const CUtensorMap& qmap, const C
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    e = cudaFuncSetAttribute(dectc_kernel<NR, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<F8>::kSmem);
+    e = cudaFuncSetAttribute(dectc_kernel<NR, F8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<F8>::kSmem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
   }
-  e = launch_pdl(dectc_kernel<NR, F8>, dim3(grid), dim3(Lay<F8>::kThreads), Lay<F8>::kSmem, s, p, qmap, kmap,
+  e = launch_pdl(dectc_kernel<NR, F8, WIN>, dim3(grid), dim3(Lay<F8>::kThreads), Lay<F8>::kSmem, s, p, qmap, kmap,
                  vmap);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -1000,15 +1012,20 @@ cudaError_t launch_dectc_t(const AttnParams& p, const CUtensorMap& qmap, const C
 
 cudaError_t launch_dectc(const AttnParams& p, int rows, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  if (rows <= 4) return launch_dectc_t<4, false>(p, qmap, kmap, vmap, grid, s);
-  if (rows <= 8) return launch_dectc_t<8, false>(p, qmap, kmap, vmap, grid, s);
-  return launch_dectc_t<16, false>(p, qmap, kmap, vmap, grid, s);
+  if (p.window > 0) {
+    if (rows <= 4) return launch_dectc_t<4, false, true>(p, qmap, kmap, vmap, grid, s);
+    if (rows <= 8) return launch_dectc_t<8, false, true>(p, qmap, kmap, vmap, grid, s);
+    return launch_dectc_t<16, false, true>(p, qmap, kmap, vmap, grid, s);
+  }
+  if (rows <= 4) return launch_dectc_t<4, false, false>(p, qmap, kmap, vmap, grid, s);
+  if (rows <= 8) return launch_dectc_t<8, false, false>(p, qmap, kmap, vmap, grid, s);
+  return launch_dectc_t<16, false, false>(p, qmap, kmap, vmap, grid, s);
 }
 
 cudaError_t launch_dectc_fp8(const AttnParams& p, int rows, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int grid, cudaStream_t s) {
-  if (rows <= 4) return launch_dectc_t<4, true>(p, qmap, kmap, vmap, grid, s);
-  if (rows <= 8) return launch_dectc_t<8, true>(p, qmap, kmap, vmap, grid, s);
+  if (rows <= 4) return launch_dectc_t<4, true, false>(p, qmap, kmap, vmap, grid, s);
+  if (rows <= 8) return launch_dectc_t<8, true, false>(p, qmap, kmap, vmap, grid, s);
   return cudaErrorInvalidValue;  // more than 8 rows per item: the CUDA-core kernel serves FP8 pools
 }
 

@@ -181,8 +181,9 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* w,
 // D: head_dim, 64 or 128 (one or two 64-column halves of Q, K, V and the
 // output; the shared-memory and TMEM layouts are those of 128, with the
 // second halves unused at 64).  Each softmax thread owns D / 2 output
-// columns of its row.
-template <int D, bool kFaultHook>
+// columns of its row.  WIN: a query sees its last p.window keys and the
+// first p.num_sink (Hole: the tiles between them are not read).
+template <int D, bool kFaultHook, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams p,
                                                                const __grid_constant__ CUtensorMap qmap,
                                                                const __grid_constant__ CUtensorMap kmap,
@@ -247,11 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
   // and P buffer g % 2.  Item c of this CTA uses Q tile and slot c & 1
   // (parity (c >> 1) & 1); O's phases count items.
   const int nb = kKeys / p.bs;  // physical blocks per tile
-  // physical block of this lane's block in the tile of keys from kbase
-  auto block_of = [&](const int32_t* bt, int nblk, int kbase) -> int {
-    const int lb = kbase / p.bs + lane;
+  // physical block of this lane's block in the item's tile at place kbase
+  auto block_of = [&](const int32_t* bt, int nblk, int kbase, const Hole& hole) -> int {
+    const int lb = (WIN ? hole.key(kbase) : kbase) / p.bs + lane;
     int phys = (int)p.num_blocks;  // out of range: reads as zeros
-    if (lane < nb && lb < nblk) {
+    if (lane < nb && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
       const int b = __ldg(bt + lb);
       if (b >= 0 && (int64_t)b < p.num_blocks)
         phys = b;
@@ -319,12 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
           qstart = p.query_start_loc[it.seq];
           const int nblk = (L + p.bs - 1) / p.bs;
           const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
-          sl.phys0[lane] = block_of(bt, nblk, it.kb);
+          const int n = p.query_start_loc[it.seq + 1] - qstart;
+          sl.phys0[lane] = block_of(bt, nblk, it.kb, Hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys));
           if (lane == 0) {
             sl.it = it;
             sl.L = L;
             sl.qstart = qstart;
-            sl.n = p.query_start_loc[it.seq + 1] - qstart;
+            sl.n = n;
             sl.done = 0;
           }
         }
@@ -387,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
         const bool done = slots[qb].done != 0;
         const WorkItem it = slots[qb].it;
         const int L = slots[qb].L;
+        const Hole hole(L, slots[qb].n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
         int phys = slots[qb].phys0[lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->slot_free[qb]);
@@ -396,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
         const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
         for (int kbase = it.kb; kbase < it.ke; kbase += kKeys, ++g) {
           const int st = g % nst, ph = (g / nst) & 1;
-          const int next_phys = (kbase + kKeys < it.ke) ? block_of(bt, nblk, kbase + kKeys) : 0;
+          const int next_phys = (kbase + kKeys < it.ke) ? block_of(bt, nblk, kbase + kKeys, hole) : 0;
           // K stage g % 3 is free once Q K^T(g-3) is complete; V stage g % 2
           // once P.V(g-2) is complete (phase of pv_done[g % 2])
           if (!__all_sync(0xffffffffu, mbar_wait(is_v ? &bars->pv_done[st] : &bars->k_empty[st], ph ^ 1, wc))) {
@@ -539,13 +542,14 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
       const bool valid = r < it.nrows;
       const int row = it.row0 + r;
       const int tok = row / p.G, gh = row - tok * p.G;
-      const int vis = valid ? min(it.ke, p.causal ? L - n + tok + 1 : L) : 0;
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
+      const int vis = valid ? min(WIN ? hole.end(it.ke) : it.ke, p.causal ? L - n + tok + 1 : L) : 0;
       float m_ref = -CUDART_INF_F, l = 0.f;
       int owe = -1;  // after a failed wait: the pair barriers of the item not yet taken
       const int ntiles = (it.ke - it.kb + kKeys - 1) / kKeys;
       for (int j = 0; j < ntiles; ++j, ++g) {
         const int sb = g & 1, vs = g % kVStages;
-        const int kt = it.kb + j * kKeys;  // first key of the tile
+        const int kt = WIN ? hole.key(it.kb + j * kKeys) : it.kb + j * kKeys;  // first key of the tile
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (g >> 1) & 1, wc))) {
           owe = ntiles - j + 2;
           break;
@@ -568,6 +572,15 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
 #pragma unroll
           for (int cc = 0; cc < 64; ++cc)
             if (cc >= nvis) sraw[cc] = __float_as_uint(-CUDART_INF_F);
+        }
+        if constexpr (WIN) {
+          // keys nsink <= c < nlo of this half lie before the row's window
+          const int nlo = L - n + tok + 1 - p.window - (kt + 64 * h), nsink = p.num_sink - (kt + 64 * h);
+          if (__any_sync(0xffffffffu, nlo > 0) && nsink < 64) {
+#pragma unroll
+            for (int cc = 0; cc < 64; ++cc)
+              if (cc < nlo && cc >= nsink) sraw[cc] = __float_as_uint(-CUDART_INF_F);
+          }
         }
         // this half's max (raw S): four chains of three-operand max, two values a step
         float m4[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
@@ -656,14 +669,17 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
             tmem_st32(lane_base + kOCol + kOC * h + cc * 32, o);
           }
         }
-        if (kt + kKeys > L && h < kNH) {
-          // keys at or past the sequence's end hold arbitrary bits: zero their V
-          // rows (thread: key r of the tile, d-half h) so that 0 * V stays 0
+        // a tile that holds keys before every row's window
+        const bool early = WIN && kt < hole.lo && kt + kKeys > p.num_sink;
+        if ((kt + kKeys > L || early) && h < kNH) {
+          // keys at or past the sequence's end hold arbitrary bits, as those before
+          // the windows may: zero their V rows (thread: key r of the tile, d-half
+          // h) so that 0 * V stays 0
           if (!__all_sync(0xffffffffu, mbar_wait(&bars->v_full[vs][h], (g / kVStages) & 1, wc))) {
             owe = ntiles - j + 1;
             break;
           }
-          if (kt + r >= L) {
+          if (kt + r >= L || (WIN && kt + r < hole.lo && kt + r >= p.num_sink)) {
             uint4* v0 = reinterpret_cast<uint4*>(smem + kVOff + vs * kTileBytes + h * kHalfKV + r * 128);
 #pragma unroll
             for (int t = 0; t < 8; ++t) v0[t] = make_uint4(0, 0, 0, 0);
@@ -795,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D, bool kFaultHook>
+template <int D, bool kFaultHook, bool WIN>
 cudaError_t launch_mma_t(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
                          const CUtensorMap& vmap, const CUtensorMap& omap, int grid, cudaStream_t s) {
   static unsigned long long done_mask = 0;
@@ -806,10 +822,10 @@ cudaError_t launch_mma_t(const AttnParams& p, const CUtensorMap& qmap, const CUt
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
     // the register split needs the block launched with 128 registers per thread
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, mma_attn_kernel<D, kFaultHook>);
+    e = cudaFuncGetAttributes(&fa, mma_attn_kernel<D, kFaultHook, WIN>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(mma_attn_kernel<D, kFaultHook>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(mma_attn_kernel<D, kFaultHook, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
   }
@@ -817,10 +833,10 @@ cudaError_t launch_mma_t(const AttnParams& p, const CUtensorMap& qmap, const CUt
     // beside the decode kernel (p.no_wait): a plain launch, which starts once
     // the planner's grid has completed; started early, before the plan, it
     // delayed the pair on the mixed batch
-    mma_attn_kernel<D, kFaultHook><<<dim3(grid), dim3(kThreads), kSmem, s>>>(p, qmap, kmap, vmap, omap);
+    mma_attn_kernel<D, kFaultHook, WIN><<<dim3(grid), dim3(kThreads), kSmem, s>>>(p, qmap, kmap, vmap, omap);
     e = cudaGetLastError();
   } else {
-    e = launch_pdl(mma_attn_kernel<D, kFaultHook>, dim3(grid), dim3(kThreads), kSmem, s, p, qmap, kmap, vmap, omap);
+    e = launch_pdl(mma_attn_kernel<D, kFaultHook, WIN>, dim3(grid), dim3(kThreads), kSmem, s, p, qmap, kmap, vmap, omap);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -829,11 +845,18 @@ cudaError_t launch_mma_t(const AttnParams& p, const CUtensorMap& qmap, const CUt
 
 cudaError_t launch_mma(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
                        const CUtensorMap& omap, int grid, cudaStream_t s) {
+  if (p.window > 0) {
+    if (p.fault_tile)  // testing only
+      return p.D == 64 ? launch_mma_t<64, true, true>(p, qmap, kmap, vmap, omap, grid, s)
+                       : launch_mma_t<128, true, true>(p, qmap, kmap, vmap, omap, grid, s);
+    return p.D == 64 ? launch_mma_t<64, false, true>(p, qmap, kmap, vmap, omap, grid, s)
+                     : launch_mma_t<128, false, true>(p, qmap, kmap, vmap, omap, grid, s);
+  }
   if (p.fault_tile)  // testing only
-    return p.D == 64 ? launch_mma_t<64, true>(p, qmap, kmap, vmap, omap, grid, s)
-                     : launch_mma_t<128, true>(p, qmap, kmap, vmap, omap, grid, s);
-  return p.D == 64 ? launch_mma_t<64, false>(p, qmap, kmap, vmap, omap, grid, s)
-                   : launch_mma_t<128, false>(p, qmap, kmap, vmap, omap, grid, s);
+    return p.D == 64 ? launch_mma_t<64, true, false>(p, qmap, kmap, vmap, omap, grid, s)
+                     : launch_mma_t<128, true, false>(p, qmap, kmap, vmap, omap, grid, s);
+  return p.D == 64 ? launch_mma_t<64, false, false>(p, qmap, kmap, vmap, omap, grid, s)
+                   : launch_mma_t<128, false, false>(p, qmap, kmap, vmap, omap, grid, s);
 }
 
 }  // namespace pkv

@@ -101,6 +101,7 @@ struct PlanParams {
   int dec_unit_rows;  // rows per decode-shaped item (4 CUDA-core, 16 tensor-core)
   int mma_unit_rows;  // rows per tensor-core item: the whole tokens that fit 128 rows, floor(128 / G) * G
   int dec_tile_keys;  // key tile of the decode-shaped kernel (splits are multiples)
+  int window, num_sink;  // a query sees its last `window` keys and the first num_sink ones (window 0: all)
   int target_dec, target_mma;  // desired item counts
   int dec_ctas;     // CTAs of the decode-shaped kernel (one wave of items)
   int sms;          // SMs of the device (CTAs of the tensor-core kernel)
@@ -135,6 +136,26 @@ struct PlanParams {
   float wk_scale, wv_scale;
 };
 
+// The keys that an item of a windowed call leaves out: [at, at + len), whole
+// tiles between the first keys (seen by every query) and the window of its
+// first token tok0, whose first key is lo.  An item's kb and ke count the keys
+// without them: key(c) = c < at ? c : c + len.
+struct Hole {
+  int at, len, lo;
+#ifdef __CUDACC__
+  __device__ __forceinline__ Hole(int L, int n, int tok0, int window, int num_sink, int tile) {
+    lo = L - n + tok0 + 1 - window;
+    at = (num_sink + tile - 1) / tile * tile;
+    len = max(0, max(lo, 0) / tile * tile - at);
+  }
+  // key of a tile's first place, and the key bound of an item that ends at place c
+  __device__ __forceinline__ int key(int c) const { return c < at ? c : c + len; }
+  __device__ __forceinline__ int end(int c) const { return c <= at ? c : c + len; }
+  // no row of the item sees keys [k, k + count), for keys before the rows' own
+  __device__ __forceinline__ bool hides(int k, int count, int num_sink) const { return k >= num_sink && k + count <= lo; }
+#endif
+};
+
 struct AttnParams {
   const void* q;
   void* out;
@@ -155,6 +176,7 @@ struct AttnParams {
   int causal;
   int out_al32;      // out is 32-byte aligned (256-bit stores)
   int mma_unit_rows;  // rows of a full tensor-core item: floor(128 / G) * G (whole tokens)
+  int window, num_sink;  // as PlanParams
   // The decode kernel launches beside the tensor-core kernel, after every
   // CTA of that kernel has seen the plan complete (they signal dependents
   // only then): it skips the grid-dependency wait, which would also wait for
@@ -239,6 +261,6 @@ pkv_status cuda_error(cudaError_t e, const char* what);
 // Shared-memory bytes of the CUDA-core kernel, and its resident CTAs per SM
 // (also sets the kernel's shared-memory opt-in on the current device).
 int decode_smem_bytes(int D, int elem_bytes);
-cudaError_t decode_ctas_per_sm(bool bf16, int D, int* ctas);
+cudaError_t decode_ctas_per_sm(bool bf16, int D, bool window, int* ctas);
 
 }  // namespace pkv

@@ -109,11 +109,14 @@ __device__ __forceinline__ SeqDesc describe(const PlanParams& p, int s, const in
   return d;
 }
 
-// Keys a unit must visit: rows [u*unit_rows, ...) of the sequence.
-__device__ __forceinline__ int unit_keys(const SeqDesc& d, int u, int G, int causal) {
+// Keys a unit must visit: rows [u*unit_rows, ...) of the sequence.  With a
+// window, those that it leaves out are not counted.
+__device__ __forceinline__ int unit_keys(const SeqDesc& d, int u, const PlanParams& p) {
   const int r1 = min(d.rows, (u + 1) * d.unit_rows);
-  const int last_tok = (r1 - 1) / G;
-  return causal ? (d.L - d.n + last_tok + 1) : d.L;
+  const int last_tok = (r1 - 1) / p.G;
+  const int keys = p.causal ? (d.L - d.n + last_tok + 1) : d.L;
+  if (p.window == 0) return keys;
+  return keys - Hole(d.L, d.n, u * d.unit_rows / p.G, p.window, p.num_sink, d.mma ? kMmaTileKeys : p.dec_tile_keys).len;
 }
 
 __device__ __forceinline__ void split_of(int keys, int chunk, int tile, int& nsplit, int& per) {
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
   {
     UnitIter t{i0, i1, B, p.Hkv, 0, 0, 0, {}, seq_ln};
     for (iter_seek(t, p, seq_off); t.i < t.end; iter_next(t, p, seq_off))
-      (t.d.mma ? w_mma : w_dec) += (unsigned long long)(unit_keys(t.d, t.u, p.G, p.causal) - t.d.pre);
+      (t.d.mma ? w_mma : w_dec) += (unsigned long long)(unit_keys(t.d, t.u, p) - t.d.pre);
   }
   // warp sums, then one thread adds the warps' (no contended 64-bit atomics)
 #pragma unroll
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
         const SeqDesc& d = t.d;
         const int chunk = d.mma ? cm : cd;
         const int cb = d.mma ? kClasses : 0;
-        const int keys = unit_keys(d, t.u, p.G, p.causal) - d.pre;
+        const int keys = unit_keys(d, t.u, p) - d.pre;
         int ns, per;
         split_of(keys, chunk, d.mma ? kMmaTileKeys : p.dec_tile_keys, ns, per);
         if (ns > 1) add(cb + size_class(per, chunk), ns - 1);  // all splits but the last are full
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
       WorkItem* items = d.mma ? p.mma_items : p.dec_items;
       const int chunk = d.mma ? cm : cd;
       const int cbase = d.mma ? kClasses : 0;
-      const int kend = unit_keys(d, u, p.G, p.causal);
+      const int kend = unit_keys(d, u, p);
       const int keys = kend - d.pre;
       const int r0 = u * d.unit_rows;
       const int nr = min(d.rows - r0, d.unit_rows);
