@@ -168,6 +168,33 @@ pkv_status paged_kv_write_rope(const void* q, const void* k, const void* v, cons
                                int64_t v_token_stride, pkv_dtype dtype, void* stream);
 
 /*
+ * paged_kv_write_norm_rope - paged_kv_write_rope of heads that are normed
+ * first: each head x of q (of k) becomes
+ *   z = x / sqrt(mean(x^2) + eps) * q_weight (k_weight),
+ * which is then rotated to its token's position as paged_kv_write_rope does.
+ * v is not normed.  The norm is over head_dim; all of it is computed in fp32
+ * (the squares' sum must not overflow: |x| below 2^60) and rounded once.
+ *
+ *   q_weight, k_weight  device [head_dim] of weight_dtype (`dtype` or
+ *               PKV_DTYPE_F32), the same for all heads; NULL: ones
+ *   eps         positive and finite
+ *   k_out       device [num_tokens, num_kv_heads, head_dim], dense, or NULL: the
+ *               normed and rotated k as rows of `dtype`, of every token (may be
+ *               k itself when k is dense, must not overlap it otherwise).  With
+ *               it, k_cache, v_cache, v and slot_mapping may all be NULL: nothing
+ *               is scattered (pools of another format take the rows afterwards)
+ *   the rest    as paged_kv_write_rope
+ */
+pkv_status paged_kv_write_norm_rope(const void* q, const void* k, const void* v, const void* q_weight,
+                                    const void* k_weight, const int64_t* positions, const double* inv_freq,
+                                    const int64_t* slot_mapping, void* q_out, void* k_out, void* k_cache,
+                                    void* v_cache, int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                                    int32_t interleaved, float eps, float amplitude, int64_t q_token_stride,
+                                    int64_t k_token_stride, int64_t v_token_stride, pkv_dtype dtype,
+                                    pkv_dtype weight_dtype, void* stream);
+
+/*
  * paged_attention_workspace_size - bytes of device workspace that
  * paged_attention_forward wants for a batch of this shape (an upper bound
  * of what it uses; any smaller size >= paged_attention_workspace_min also
@@ -343,6 +370,21 @@ pkv_status paged_kv_write_rope_fp8(const void* q, const void* k, const void* v, 
                                    int32_t interleaved, float amplitude, int64_t q_token_stride,
                                    int64_t k_token_stride, int64_t v_token_stride, pkv_dtype dtype, float k_scale,
                                    float v_scale, void* stream);
+
+/*
+ * paged_kv_write_norm_rope_fp8 - paged_kv_write_norm_rope into FP8 pools: the
+ * codes are those of the fp32 values, by paged_kv_write_fp8's rule; q_out and
+ * k_out have q's dtype.
+ */
+pkv_status paged_kv_write_norm_rope_fp8(const void* q, const void* k, const void* v, const void* q_weight,
+                                        const void* k_weight, const int64_t* positions, const double* inv_freq,
+                                        const int64_t* slot_mapping, void* q_out, void* k_out, void* k_cache,
+                                        void* v_cache, int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t rotary_dim, int32_t interleaved, float eps, float amplitude,
+                                        int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                        pkv_dtype dtype, pkv_dtype weight_dtype, float k_scale, float v_scale,
+                                        void* stream);
 
 /*
  * paged_attention_forward_fp8kv - paged_attention_forward with FP8 pools:

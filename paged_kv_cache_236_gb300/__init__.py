@@ -18,6 +18,7 @@ tensors are not on a CUDA device, the calls raise.
     paged_kv_select(scores, context_lens, budget)
     paged_kv_compact(k_cache, v_cache, block_tables, kept)     (eviction)
     paged_attention_window_forward(q, k_cache, v_cache, ..., scale, window, num_sink)
+    paged_kv_write_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache)
 
 Block pool per layer: ``[num_blocks, block_size, num_kv_heads, head_dim]``
 ("ADR 004: Paged Attention Serving Integration", Decision 4 - a per-layer
@@ -42,6 +43,7 @@ __all__ = [
     "paged_kv_write_rope", "paged_kv_write_rope_fp8", "rope_frequencies", "rope_amplitude",
     "paged_attention_scores", "paged_attention_scores_fp8kv", "scores_workspace_size", "scores_workspace_min",
     "paged_kv_select", "paged_kv_compact", "paged_attention_window_forward",
+    "paged_kv_write_norm_rope", "paged_kv_write_norm_rope_fp8",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +80,7 @@ _lock = threading.Lock()
 
 c_vp, c_i32, c_i64, c_sz, c_f = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _ROPE_ARGS = [c_vp] * 9 + [c_i64, c_i64] + [c_i32] * 6 + [c_f, c_i64, c_i64, c_i64, c_i32]
+_NORM_ARGS = [c_vp] * 12 + [c_i64, c_i64] + [c_i32] * 6 + [c_f, c_f, c_i64, c_i64, c_i64, c_i32, c_i32]
 _SCORES_ARGS = [c_vp] * 8 + [c_i32, c_i64, c_i32, c_i32, c_i32, c_i64] + [c_i32] * 5 + [c_f, c_i32, c_f]
 
 
@@ -152,6 +155,8 @@ def lib() -> ctypes.CDLL:
                     ("paged_attention_window_forward", L.paged_attention_forward.argtypes),
                     ("paged_kv_write_rope", _ROPE_ARGS + [c_vp]),
                     ("paged_kv_write_rope_fp8", _ROPE_ARGS + [c_f, c_f, c_vp]),
+                    ("paged_kv_write_norm_rope", _NORM_ARGS + [c_vp]),
+                    ("paged_kv_write_norm_rope_fp8", _NORM_ARGS + [c_f, c_f, c_vp]),
                     ("paged_attention_scores", _SCORES_ARGS + [c_vp, c_sz, c_i32, c_vp]),
                     ("paged_attention_scores_fp8kv", _SCORES_ARGS + [c_f, c_vp, c_sz, c_vp]),
                     ("paged_kv_select", [c_vp] * 4 + [c_i32] * 7 + [c_vp]),
@@ -927,6 +932,110 @@ def paged_kv_write_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, p
     args, q_out = _rope_args(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, interleaved, amplitude,
                              q_out, dev)
     _call(lib().paged_kv_write_rope_fp8, dev, *args, k_scale, v_scale)
+    return q_out
+
+
+def _norm_rope_args(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache, eps,
+                    interleaved, amplitude, q_out, k_out, dev):
+    """Checks paged_kv_write_norm_rope's tensors; returns (its C arguments up
+    to the weights' dtype, q_out)."""
+    shape, dtype = q.shape, q.dtype
+    if dtype not in DTYPE or k.dtype != dtype:
+        raise ValueError("q, k and v must share dtype bfloat16 or float32")
+    if len(shape) != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, heads, D]")
+    T, Hq, D = shape
+    Hkv = k.shape[1]
+    NB = bs = 0
+    pools = (slot_mapping, k_cache, v_cache)
+    if all(t is None for t in pools):
+        if k_out is None:
+            raise ValueError("without pools, k_out must be given")
+        v = None
+    elif v is None or any(t is None for t in pools):
+        raise ValueError("v, slot_mapping, k_cache and v_cache go together")
+    else:
+        if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() or \
+                not v_cache.is_contiguous() or tuple(k_cache.shape[2:]) != (Hkv, D):
+            raise ValueError(f"caches must be contiguous [num_blocks, block_size, {Hkv}, {D}]")
+        NB, bs = k_cache.shape[:2]
+        if slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():
+            raise ValueError("slot_mapping must be contiguous int64 [T]")
+    strides = []
+    for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        if t is None:
+            strides.append(0)
+            continue
+        st = t.stride()
+        if t.dtype != dtype or t.shape != (T, heads, D) or st[2] != 1 or st[1] != D:
+            raise ValueError(f"{name} must be {[T, heads, D]} of q's dtype with contiguous heads")
+        if T > 1 and st[0] == 0:  # the C call takes a stride of 0 for dense
+            raise ValueError("q, k and v must not repeat one token's row (a token stride of 0)")
+        strides.append(st[0] if T > 1 else 0)
+    wdtype = dtype
+    for w in (q_weight, k_weight):
+        if w is None:
+            continue
+        if w.shape != (D,) or not w.is_contiguous() or w.dtype not in (dtype, torch.float32):
+            raise ValueError(f"weights must be contiguous [{D}] of q's dtype or float32")
+        wdtype = w.dtype
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must share a dtype")
+    if positions.shape != (T,) or positions.dtype != torch.int64 or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int64 [T]")
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() or \
+            not 0 < 2 * inv_freq.shape[0] <= D:
+        raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2] with rotary_dim <= head_dim")
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    for name, t, want in (("q_out", q_out, shape), ("k_out", k_out, k.shape)):
+        if t is not None and (t.shape != want or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev):
+            raise ValueError(f"{name} must be contiguous and match {name[0]}")
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    args = (q.data_ptr(), k.data_ptr(), at(v), at(q_weight), at(k_weight), positions.data_ptr(), inv_freq.data_ptr(),
+            at(slot_mapping), q_out.data_ptr(), at(k_out), at(k_cache), at(v_cache), T, NB, bs, Hq, Hkv, D,
+            2 * inv_freq.shape[0], 1 if interleaved else 0, eps, amplitude, *strides, DTYPE[dtype], DTYPE[wdtype])
+    return args, q_out
+
+
+def paged_kv_write_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor | None,
+                             q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, positions: torch.Tensor,
+                             inv_freq: torch.Tensor, slot_mapping: torch.Tensor | None = None,
+                             k_cache: torch.Tensor | None = None, v_cache: torch.Tensor | None = None, *,
+                             eps: float = 1e-6, interleaved: bool = False, amplitude: float = 1.0,
+                             q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None) -> torch.Tensor:
+    """``paged_kv_write_rope`` of heads normed first: each q and k head over its
+    root mean square (``sqrt(mean(x^2) + eps)``), times ``q_weight`` or
+    ``k_weight`` (``[D]`` of q's dtype or float32; None: ones), then rotated;
+    returns the rotated q.
+
+    ``k_out`` (contiguous, k's shape) also takes the normed and rotated k as
+    rows.  With it the pools may be left out, for those of another format
+    (``paged_kv_write_fp8block``).  ``q_out`` may be ``q`` itself, and
+    ``k_out`` ``k``, when contiguous."""
+    dev = _device_of(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache, k_out)
+    for t in (k_cache, v_cache):
+        if t is not None and t.dtype != q.dtype:
+            raise ValueError("q, k, v, k_cache, v_cache must share dtype bfloat16 or float32")
+    args, q_out = _norm_rope_args(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache,
+                                  eps, interleaved, amplitude, q_out, k_out, dev)
+    _call(lib().paged_kv_write_norm_rope, dev, *args)
+    return q_out
+
+
+def paged_kv_write_norm_rope_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
+                                 k_weight: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+                                 slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                 k_scale: float, v_scale: float, *, eps: float = 1e-6, interleaved: bool = False,
+                                 amplitude: float = 1.0, q_out: torch.Tensor | None = None,
+                                 k_out: torch.Tensor | None = None) -> torch.Tensor:
+    """``paged_kv_write_norm_rope`` into FP8 pools: the codes are those of the
+    fp32 values, encoded as ``paged_kv_write_fp8`` does."""
+    dev = _device_of(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache, k_out)
+    _check_fp8_pools(k_cache, v_cache)
+    args, q_out = _norm_rope_args(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache,
+                                  eps, interleaved, amplitude, q_out, k_out, dev)
+    _call(lib().paged_kv_write_norm_rope_fp8, dev, *args, k_scale, v_scale)
     return q_out
 
 

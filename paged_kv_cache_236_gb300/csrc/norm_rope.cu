@@ -1,0 +1,424 @@
+// RMS norm of each q and k head, their rotary positions, and the slot-mapping
+// scatter of the step's K/V rows, in one pass (paged_kv_write_norm_rope and its
+// FP8 form).
+//
+// For a head x of a token at position p, with weight w (ones where none is
+// given) and the angle a = p * inv_freq[i] of its pair i:
+//   r = 1 / sqrt(mean(x^2) + eps),   z = r w x,
+//   y1 = amp (z1 cos a - z2 sin a),  y2 = amp (z2 cos a + z1 sin a),
+// as in rope_write.cu, whose angles these are.  V is not normed.  Squares are
+// summed, and all of it computed, in fp32, and rounded once, to the output's
+// type.
+//
+// HBM-bound: rows are read once and written once; the norm, a pass of its own
+// over q and k elsewhere, costs no bytes here.  A warp takes a token, or some of
+// its heads where tokens are few; a lane owns one place of a head (two 16-byte
+// vectors: a pair's two sides), and its weights times cos and sin stay in
+// registers while it goes through the heads.  The sum of squares is shuffled
+// among the lanes of a head.
+#include <math.h>
+
+#include <algorithm>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "rope_rows.cuh"
+
+namespace pkv {
+namespace {
+
+struct NormParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* qw;  // weights [D], or NULL: ones
+  const void* kw;
+  const int64_t* positions;
+  const double* inv_freq;
+  const int64_t* slots;  // NULL: no pools
+  void* q_out;
+  void* k_out;  // dense rows, or NULL
+  void* kc;
+  void* vc;
+  int64_t T, num_slots, q_stride, k_stride, v_stride;  // strides in elements
+  int Hq, Hkv, D, half;
+  int interleaved, weights_f32, splits;
+  float eps, amp, k_scale, v_scale;
+  int* err;
+};
+
+constexpr int kWarps = 4;
+constexpr int kBatch = 2;  // heads a lane loads at a time
+
+// U: the rows' element (uint16_t: bf16 bits).  F8: the pools hold E4M3 codes.
+// WIDE: a head has more places than a warp has lanes (long heads, or heads
+// read by the element), so that its squares are summed in a pass of their own.
+template <typename U, int VEC, bool F8, bool INTER, bool WIDE>
+__global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams p) {
+  pdl_launch_dependents();  // what follows with programmatic launch reads nothing written here before it waits
+  extern __shared__ float2 trig_all[];  // [warps][half]
+  typedef Vec<U, VEC> V;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t tok = w / p.splits;
+  const int split = (int)(w - tok * p.splits);
+  if (tok >= p.T) return;
+  float2* trig = trig_all + warp * p.half;
+  // this token's rows on their way to L2 while the angles are computed
+  if (p.splits == 1) {
+    auto fetch = [&](const void* rows, int64_t stride, int heads) {
+      const char* at = static_cast<const char*>(rows) + tok * stride * (int64_t)sizeof(U);
+      for (int i = lane * 128; i < heads * p.D * (int)sizeof(U); i += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+    };
+    fetch(p.q, p.q_stride, p.Hq);
+    fetch(p.k, p.k_stride, p.Hkv);
+    if (p.slots) fetch(p.v, p.v_stride, p.Hkv);
+  }
+  const int64_t pos = p.positions[tok];
+  int64_t slot = p.slots ? p.slots[tok] : -1;
+  if (p.slots && slot >= p.num_slots) {
+    if (lane == 0 && split == 0) raise_error(p.err, PKV_DEVERR_SLOT_OUT_OF_RANGE);
+    slot = -1;
+  }
+  for (int j = lane; j < p.half; j += 32) trig[j] = turn_of(angle_of(pos, p.inv_freq[j]), p.amp);
+  __syncwarp();
+
+  const int places = (p.D / VEC + 1) / 2;  // of a head; the last may hold one vector
+  const int rot_places = p.half / VEC;
+  const int side = WIDE ? 1 : 32 / places;  // heads side by side
+  const int y = WIDE ? 0 : lane / places;
+  const bool idle = !WIDE && y >= side;  // lanes left over
+  const float inv_d = 1.f / (float)p.D;
+
+  auto weight = [&](const void* ws, int i) -> float {
+    if (!ws) return 1.f;
+    return p.weights_f32 ? static_cast<const float*>(ws)[i] : to_f(static_cast<const U*>(ws)[i]);
+  };
+  // a place's two columns
+  auto columns = [&](int x, int& ca, int& cb, bool& rot, bool& two) {
+    rot = x < rot_places;
+    ca = rot ? (INTER ? 2 * x * VEC : x * VEC) : 2 * p.half + 2 * (x - rot_places) * VEC;
+    cb = rot && !INTER ? p.half + x * VEC : ca + VEC;
+    two = cb + VEC <= p.D;
+  };
+  // The factors of a place's values: y1 = r (f[0] x1 - f[1] x2), y2 = r (f[2] x2 + f[3] x1) of each pair.
+  struct Factors {
+    float f[4][VEC];
+  };
+  auto factors = [&](const void* ws, int x, Factors& t) {
+    int ca, cb;
+    bool rot, two;
+    columns(x, ca, cb, rot, two);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      // the pair's two elements: (ca + e, cb + e), or, interleaved, (ca + 2e, ca + 2e + 1)
+      const bool pairs = rot && INTER;
+      const int i1 = pairs ? ca + 2 * e : ca + e, i2 = pairs ? ca + 2 * e + 1 : cb + e;
+      const float w1 = weight(ws, i1), w2 = two ? weight(ws, i2) : 0.f;
+      const float2 cs = rot ? trig[x * VEC + e] : make_float2(1.f, 0.f);
+      t.f[0][e] = cs.x * w1;
+      t.f[1][e] = cs.y * w2;
+      t.f[2][e] = cs.x * w2;
+      t.f[3][e] = cs.y * w1;
+    }
+  };
+  auto turned = [&](const Factors& t, const V& a, const V& b, float r, bool rot, bool two, float (&ya)[VEC],
+                    float (&yb)[VEC]) {
+    if (!rot) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        ya[e] = t.f[0][e] * to_f(a.e[e]) * r;
+        yb[e] = two ? t.f[2][e] * to_f(b.e[e]) * r : 0.f;
+      }
+    } else if (INTER) {
+      float in[2 * VEC], out[2 * VEC];
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        in[e] = to_f(a.e[e]);
+        in[VEC + e] = to_f(b.e[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        out[2 * e] = fmaf(in[2 * e], t.f[0][e], -in[2 * e + 1] * t.f[1][e]) * r;
+        out[2 * e + 1] = fmaf(in[2 * e + 1], t.f[2][e], in[2 * e] * t.f[3][e]) * r;
+      }
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        ya[e] = out[e];
+        yb[e] = out[VEC + e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float x1 = to_f(a.e[e]), x2 = to_f(b.e[e]);
+        ya[e] = fmaf(x1, t.f[0][e], -x2 * t.f[1][e]) * r;
+        yb[e] = fmaf(x2, t.f[2][e], x1 * t.f[3][e]) * r;
+      }
+    }
+  };
+  auto squares = [&](const V& a, const V& b, bool two) {
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float x1 = to_f(a.e[e]), x2 = two ? to_f(b.e[e]) : 0.f;
+      s = fmaf(x1, x1, s);
+      s = fmaf(x2, x2, s);
+    }
+    return s;
+  };
+  // sum over the lanes of a head (all the warp's lanes call it)
+  auto head_sum = [&](float s) {
+    if (WIDE || (places & (places - 1)) == 0) {
+      for (int o = WIDE ? 16 : places >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      return s;
+    }
+    float t = 0.f;
+    const int first = min(y, side - 1) * places;
+    for (int i = 0; i < places; ++i) t += __shfl_sync(0xffffffffu, s, first + i);
+    return t;
+  };
+
+  // A tensor's heads (src: the token's head 0), normed with ws and turned, or
+  // as they are: put(head, column a, column b, both, values)
+  auto go = [&](const U* src, int heads, const void* ws, bool norm, auto put) {
+    int ca, cb;
+    bool rot, two;
+    if constexpr (WIDE) {
+      for (int h = split; h < heads; h += p.splits) {
+        const U* row = src + (int64_t)h * p.D;
+        float r = 1.f;
+        if (norm) {
+          float s = 0.f;
+          for (int x = lane; x < places; x += 32) {
+            columns(x, ca, cb, rot, two);
+            V b{};
+            const V a = *reinterpret_cast<const V*>(row + ca);
+            if (two) b = *reinterpret_cast<const V*>(row + cb);
+            s += squares(a, b, two);
+          }
+          r = rsqrtf(fmaf(head_sum(s), inv_d, p.eps));
+        }
+        for (int x = lane; x < places; x += 32) {
+          columns(x, ca, cb, rot, two);
+          V b{};
+          const V a = *reinterpret_cast<const V*>(row + ca);
+          if (two) b = *reinterpret_cast<const V*>(row + cb);
+          if (norm) {
+            Factors t;
+            factors(ws, x, t);
+            float ya[VEC], yb[VEC];
+            turned(t, a, b, r, rot, two, ya, yb);
+            put(h, ca, cb, two, ya, yb, a, b);
+          } else {
+            float ya[VEC], yb[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              ya[e] = to_f(a.e[e]);
+              yb[e] = to_f(b.e[e]);
+            }
+            put(h, ca, cb, two, ya, yb, a, b);
+          }
+        }
+      }
+    } else {
+      const int x = idle ? 0 : lane - y * places;
+      columns(x, ca, cb, rot, two);
+      Factors t;
+      if (norm) factors(ws, x, t);
+      const int hstep = side * p.splits;
+      for (int base = split * side; base < heads; base += kBatch * hstep) {  // the same for every lane
+        V a[kBatch], b[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = base + y + i * hstep;
+          a[i] = b[i] = V{};
+          if (!idle && h < heads) {
+            a[i] = *reinterpret_cast<const V*>(src + (int64_t)h * p.D + ca);
+            if (two) b[i] = *reinterpret_cast<const V*>(src + (int64_t)h * p.D + cb);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int h = base + y + i * hstep;
+          float ya[VEC], yb[VEC];
+          if (norm) {
+            const float r = rsqrtf(fmaf(head_sum(squares(a[i], b[i], two)), inv_d, p.eps));
+            turned(t, a[i], b[i], r, rot, two, ya, yb);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              ya[e] = to_f(a[i].e[e]);
+              yb[e] = to_f(b[i].e[e]);
+            }
+          }
+          if (!idle && h < heads) put(h, ca, cb, two, ya, yb, a[i], b[i]);
+        }
+      }
+    }
+  };
+
+  U* qo = static_cast<U*>(p.q_out) + tok * p.Hq * (int64_t)p.D;
+  go(static_cast<const U*>(p.q) + tok * p.q_stride, p.Hq, p.qw, true,
+     [&](int h, int ca, int cb, bool two, const float (&ya)[VEC], const float (&yb)[VEC], const V&, const V&) {
+       U* dst = qo + (int64_t)h * p.D;
+       store_rows<U, VEC>(dst + ca, ya);
+       if (two) store_rows<U, VEC>(dst + cb, yb);
+     });
+  if (slot < 0 && !p.k_out) return;
+  const int64_t at = slot * p.Hkv * (int64_t)p.D;
+  U* ko = p.k_out ? static_cast<U*>(p.k_out) + tok * p.Hkv * (int64_t)p.D : nullptr;
+  go(static_cast<const U*>(p.k) + tok * p.k_stride, p.Hkv, p.kw, true,
+     [&](int h, int ca, int cb, bool two, const float (&ya)[VEC], const float (&yb)[VEC], const V&, const V&) {
+       if (ko) {
+         U* dst = ko + (int64_t)h * p.D;
+         store_rows<U, VEC>(dst + ca, ya);
+         if (two) store_rows<U, VEC>(dst + cb, yb);
+       }
+       if (slot < 0) return;
+       const int64_t to = at + (int64_t)h * p.D;
+       if constexpr (F8) {
+         store_codes<VEC>(static_cast<uint8_t*>(p.kc) + to + ca, ya, p.k_scale);
+         if (two) store_codes<VEC>(static_cast<uint8_t*>(p.kc) + to + cb, yb, p.k_scale);
+       } else {
+         store_rows<U, VEC>(static_cast<U*>(p.kc) + to + ca, ya);
+         if (two) store_rows<U, VEC>(static_cast<U*>(p.kc) + to + cb, yb);
+       }
+     });
+  if (slot < 0) return;
+  go(static_cast<const U*>(p.v) + tok * p.v_stride, p.Hkv, nullptr, false,
+     [&](int h, int ca, int cb, bool two, const float (&ya)[VEC], const float (&yb)[VEC], const V& a, const V& b) {
+       const int64_t to = at + (int64_t)h * p.D;
+       if constexpr (F8) {
+         store_codes<VEC>(static_cast<uint8_t*>(p.vc) + to + ca, ya, p.v_scale);
+         if (two) store_codes<VEC>(static_cast<uint8_t*>(p.vc) + to + cb, yb, p.v_scale);
+       } else {
+         *reinterpret_cast<V*>(static_cast<U*>(p.vc) + to + ca) = a;
+         if (two) *reinterpret_cast<V*>(static_cast<U*>(p.vc) + to + cb) = b;
+       }
+     });
+}
+
+pkv_status fail(pkv_status st, const char* msg) {
+  set_last_error(msg);
+  return st;
+}
+
+template <typename U, int VEC, bool F8, bool WIDE>
+cudaError_t launch_w(const NormParams& p, dim3 grid, size_t smem, cudaStream_t s) {
+  if (p.interleaved)
+    norm_rope_kernel<U, VEC, F8, true, WIDE><<<grid, kWarps * 32, smem, s>>>(p);
+  else
+    norm_rope_kernel<U, VEC, F8, false, WIDE><<<grid, kWarps * 32, smem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename U, bool F8>
+cudaError_t launch(const NormParams& p0, bool vec, int sms, cudaStream_t s) {
+  NormParams p = p0;
+  constexpr int kV = 16 / sizeof(U);
+  const int places = (p.D / (vec ? kV : 1) + 1) / 2, side = places <= 32 ? 32 / places : 1;
+  // few tokens: a token's heads are spread over several warps, down to one
+  // load of each lane
+  const int most = (std::max(p.Hq, p.Hkv) + side - 1) / side;
+  p.splits = 1;
+  while (p.T * p.splits < (int64_t)sms * 8 && p.splits < most) p.splits *= 2;
+  const dim3 grid((unsigned)((p.T * p.splits + kWarps - 1) / kWarps));
+  const size_t smem = (size_t)kWarps * p.half * sizeof(float2);
+  if (places > 32) return vec ? launch_w<U, kV, F8, true>(p, grid, smem, s) : launch_w<U, 1, F8, true>(p, grid, smem, s);
+  return vec ? launch_w<U, kV, F8, false>(p, grid, smem, s) : launch_w<U, 1, F8, false>(p, grid, smem, s);
+}
+
+pkv_status norm_rope(NormParams p, int64_t num_blocks, int block_size, int rotary, pkv_dtype dtype,
+                     pkv_dtype weight_dtype, bool f8, void* stream) {
+  set_last_error("");
+  if (dtype != PKV_DTYPE_BF16 && dtype != PKV_DTYPE_F32) return fail(PKV_ERR_UNSUPPORTED, "dtype");
+  if (weight_dtype != dtype && weight_dtype != PKV_DTYPE_F32)
+    return fail(PKV_ERR_UNSUPPORTED, "weight_dtype must be the rows' or float32");
+  const bool pools = p.kc || p.vc;
+  if (p.T < 0 || p.Hq <= 0 || p.Hkv <= 0 || p.D <= 0 || num_blocks < 0 || block_size < 0 ||
+      ((pools || f8) && (num_blocks == 0 || block_size == 0)))
+    return fail(PKV_ERR_INVALID_ARG, "sizes must be positive (num_tokens >= 0)");
+  if (rotary <= 0 || rotary % 2 != 0 || rotary > p.D)
+    return fail(PKV_ERR_INVALID_ARG, "rotary_dim must be even, positive and at most head_dim");
+  if (p.D > 1024) return fail(PKV_ERR_UNSUPPORTED, "head_dim above 1024");
+  const int64_t row_q = (int64_t)p.Hq * p.D, row = (int64_t)p.Hkv * p.D;
+  if (row > (1 << 24) || row_q > (1 << 24)) return fail(PKV_ERR_UNSUPPORTED, "heads * head_dim too large");
+  if (!(p.eps > 0.f) || !isfinite(p.eps)) return fail(PKV_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!(p.amp > 0.f) || !isfinite(p.amp)) return fail(PKV_ERR_INVALID_ARG, "amplitude must be positive and finite");
+  if (f8 && (!(p.k_scale > 0.f) || !isfinite(p.k_scale) || !(p.v_scale > 0.f) || !isfinite(p.v_scale)))
+    return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
+  if (p.q_stride == 0) p.q_stride = row_q;
+  if (p.k_stride == 0) p.k_stride = row;
+  if (p.v_stride == 0) p.v_stride = row;
+  if (p.q_stride < row_q || p.k_stride < row || p.v_stride < row)
+    return fail(PKV_ERR_INVALID_ARG, "token stride smaller than heads * head_dim");
+  if (p.T > (int64_t)1 << 30) return fail(PKV_ERR_UNSUPPORTED, "num_tokens too large");
+  if (p.T == 0) return PKV_OK;
+  if (!p.q || !p.k || !p.positions || !p.inv_freq || !p.q_out) return fail(PKV_ERR_INVALID_ARG, "null pointer");
+  if (!pools && !p.k_out) return fail(PKV_ERR_INVALID_ARG, "null pointer: neither pools nor k_out");
+  if (pools && (!p.kc || !p.vc || !p.v || !p.slots))
+    return fail(PKV_ERR_INVALID_ARG, "null pointer: pools want k_cache, v_cache, v and slot_mapping");
+  if (!pools) p.slots = nullptr;
+  const size_t es = dtype == PKV_DTYPE_BF16 ? 2 : 4, wes = weight_dtype == PKV_DTYPE_BF16 ? 2 : 4;
+  auto bits = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
+  if ((bits(p.kc) | bits(p.vc)) & 15u) return fail(PKV_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+  if ((bits(p.q) | bits(p.k) | bits(p.v) | bits(p.q_out) | bits(p.k_out)) & (es - 1) ||
+      (bits(p.qw) | bits(p.kw)) & (wes - 1) || (bits(p.positions) | bits(p.slots) | bits(p.inv_freq)) & 7u)
+    return fail(PKV_ERR_INVALID_ARG, "a tensor is not aligned to its elements");
+  int sms = 0;
+  pkv_status st = device_state(&sms, &p.err);
+  if (st != PKV_OK) return st;
+  p.half = rotary / 2;
+  p.weights_f32 = weight_dtype == PKV_DTYPE_F32 ? 1 : 0;
+  p.num_slots = num_blocks * block_size;
+  // 16-byte vectors where every row, every head and the rotary halves allow them
+  const int V = (int)(16 / es);
+  const bool vec = p.D % V == 0 && p.half % V == 0 && p.q_stride % V == 0 && p.k_stride % V == 0 &&
+                   (!pools || p.v_stride % V == 0) &&
+                   ((bits(p.q) | bits(p.k) | bits(p.v) | bits(p.q_out) | bits(p.k_out)) & 15u) == 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (es == 2)
+    e = f8 ? launch<uint16_t, true>(p, vec, sms, s) : launch<uint16_t, false>(p, vec, sms, s);
+  else
+    e = f8 ? launch<float, true>(p, vec, sms, s) : launch<float, false>(p, vec, sms, s);
+  if (e != cudaSuccess) return cuda_error(e, "paged_kv_write_norm_rope launch");
+  return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status paged_kv_write_norm_rope(const void* q, const void* k, const void* v, const void* q_weight,
+                                    const void* k_weight, const int64_t* positions, const double* inv_freq,
+                                    const int64_t* slot_mapping, void* q_out, void* k_out, void* k_cache,
+                                    void* v_cache, int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t rotary_dim,
+                                    int32_t interleaved, float eps, float amplitude, int64_t q_token_stride,
+                                    int64_t k_token_stride, int64_t v_token_stride, pkv_dtype dtype,
+                                    pkv_dtype weight_dtype, void* stream) {
+  pkv::NormParams p{q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, q_out, k_out, k_cache, v_cache,
+                    num_tokens, 0, q_token_stride, k_token_stride, v_token_stride, num_q_heads, num_kv_heads,
+                    head_dim, 0, interleaved ? 1 : 0, 0, 0, eps, amplitude, 1.f, 1.f, nullptr};
+  return pkv::norm_rope(p, num_blocks, block_size, rotary_dim, dtype, weight_dtype, false, stream);
+}
+
+pkv_status paged_kv_write_norm_rope_fp8(const void* q, const void* k, const void* v, const void* q_weight,
+                                        const void* k_weight, const int64_t* positions, const double* inv_freq,
+                                        const int64_t* slot_mapping, void* q_out, void* k_out, void* k_cache,
+                                        void* v_cache, int64_t num_tokens, int64_t num_blocks, int32_t block_size,
+                                        int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t rotary_dim, int32_t interleaved, float eps, float amplitude,
+                                        int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                                        pkv_dtype dtype, pkv_dtype weight_dtype, float k_scale, float v_scale,
+                                        void* stream) {
+  pkv::NormParams p{q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, q_out, k_out, k_cache, v_cache,
+                    num_tokens, 0, q_token_stride, k_token_stride, v_token_stride, num_q_heads, num_kv_heads,
+                    head_dim, 0, interleaved ? 1 : 0, 0, 0, eps, amplitude, k_scale, v_scale, nullptr};
+  return pkv::norm_rope(p, num_blocks, block_size, rotary_dim, dtype, weight_dtype, true, stream);
+}
+
+}  // extern "C"

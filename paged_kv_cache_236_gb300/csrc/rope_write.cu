@@ -32,13 +32,13 @@
 // Values are rotated in fp32 and rounded once, to the output's type: an FP8
 // pool takes the code of the fp32 value, with no rounding to the row's type
 // in between.
-#include <cuda_fp8.h>
 #include <math.h>
 
 #include <algorithm>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "rope_rows.cuh"
 
 namespace pkv {
 namespace {
@@ -62,81 +62,6 @@ struct RopeParams {
 
 constexpr int kWarps = 4;   // of a block
 constexpr int kBatch = 2;   // heads a lane loads at a time
-
-typedef unsigned __int128 u128;
-
-template <typename U, int N>
-struct alignas(sizeof(U) * N) Vec {
-  U e[N];
-};
-
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
-__device__ __forceinline__ void from_f(float x, float& y) { y = x; }
-__device__ __forceinline__ void from_f(float x, uint16_t& y) { y = __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
-
-// E4M3 codes of x / scale (IEEE division, nearest even, saturating), as
-// paged_kv_write_fp8 encodes.
-template <int N>
-__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], float scale) {
-  Vec<uint8_t, N> o;
-  if constexpr (N >= 2) {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[i], scale), __fdiv_rn(x[i + 1], scale)),
-                                                    __NV_SATFINITE, __NV_E4M3);
-      o.e[i] = (uint8_t)two;
-      o.e[i + 1] = (uint8_t)(two >> 8);
-    }
-  } else {
-    o.e[0] = (uint8_t)__nv_cvt_float_to_fp8(__fdiv_rn(x[0], scale), __NV_SATFINITE, __NV_E4M3);
-  }
-  *reinterpret_cast<Vec<uint8_t, N>*>(dst) = o;
-}
-template <typename U, int N>
-__device__ __forceinline__ void store_rows(U* dst, const float (&x)[N]) {
-  Vec<U, N> o;
-#pragma unroll
-  for (int i = 0; i < N; ++i) from_f(x[i], o.e[i]);
-  *reinterpret_cast<Vec<U, N>*>(dst) = o;
-}
-
-// The fraction of a turn, times 2^64, at a position, of a frequency in radians
-// per position: |f| = m * 2^(e - 52) with a whole m < 2^53, and 1 / (2 pi) as a
-// whole number of 2^-64 or 2^-128.
-constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull, kInv2PiLow = 0x7F09D5F47D4D3770ull;
-
-// Any position and frequency: turns of 2^-128, the top half of the product's 128
-// bits, a position's sign in its weight of 2^64.
-__device__ __noinline__ int64_t far_angle(int64_t pos, double f) {
-  const uint64_t bits = (uint64_t)__double_as_longlong(f);
-  const int e = (int)((bits >> 52) & 2047) - 1023;
-  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e == -1023 ? 0 : 1ull << 52);
-  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * 2^128 / (2 pi) >> sh
-  const u128 low = (u128)m * kInv2PiLow, high = (u128)m * kInv2Pi + (uint64_t)(low >> 64);  // high * 2^64 + low's low half
-  u128 r;
-  if (sh >= 192) r = 0;
-  else if (sh >= 64) r = high >> (sh - 64);
-  else if (sh >= 0) r = (high << (64 - sh)) | (uint64_t)low >> sh;
-  else r = sh > -128 ? ((high << 64) | (uint64_t)low) << -sh : 0;
-  if (bits >> 63) r = 0 - r;
-  const uint64_t part = (uint64_t)r, p = (uint64_t)pos;
-  return (int64_t)(p * (uint64_t)(r >> 64) + __umul64hi(p, part) - (pos < 0 ? part : 0));
-}
-
-// Positions of 32 bits and frequencies below 2: a frequency in turns of 2^-64 is
-// off by at most 3 of them, the angle by less than 2^-31 of a turn.  (The others' way for
-// all: 3 % of a mixed step's time.)
-__device__ __forceinline__ int64_t angle_of(int64_t pos, double f) {
-  const uint64_t bits = (uint64_t)__double_as_longlong(f);
-  const int e = (int)((bits >> 52) & 2047) - 1023;
-  if (pos != (int)pos || e > 0) return far_angle(pos, f);
-  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (e == -1023 ? 0 : 1ull << 52);
-  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
-  const int sh = 52 - (e == -1023 ? -1022 : e);  // m * 2^64 / (2 pi) >> sh
-  const uint64_t r = sh >= 128 ? 0 : sh >= 64 ? hi >> (sh - 64) : (lo >> sh) | (hi << (64 - sh));
-  return pos * (int64_t)(bits >> 63 ? 0 - r : r);
-}
 
 // F8: the pools hold E4M3 codes.  U: the rows' element (uint16_t: bf16 bits).
 template <typename U, int VEC, bool F8, bool INTER>
@@ -168,9 +93,7 @@ __global__ void __launch_bounds__(kWarps * 32, 5) rope_write_kernel(const RopePa
     slot = -1;
   }
   for (int j = lane; j < p.half; j += 32) {
-    float s, c;
-    sincospif(__ll2float_rn(angle_of(pos, p.inv_freq[j])) * 1.0842021724855044e-19f, &s, &c);  // 2^-63: half turns
-    trig[j] = make_float2(c * p.amp, s * p.amp);
+    trig[j] = turn_of(angle_of(pos, p.inv_freq[j]), p.amp);
   }
   __syncwarp();
 
