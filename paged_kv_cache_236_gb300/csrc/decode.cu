@@ -186,8 +186,8 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// WIN: a query sees its last p.window keys and the first p.num_sink (Hole: the
-// tiles between them are not read).
+// WIN: a query sees its last p.window keys and the first p.num_sink; the blocks
+// between them are not read (Hole; keys and lengths below are places then).
 template <typename T, typename KV, int D, bool WIN>
 __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
                                                              const __grid_constant__ CUtensorMap kmap,
@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
       const int n = p.query_start_loc[it.seq + 1] - qstart;
       const int nblk = (L + p.bs - 1) / p.bs;
       const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
-      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kDecTileKeys);  // WIN
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, p.bs);  // WIN
       auto block_of = [&](int kbase) -> int {  // physical block for this lane in the tile at place kbase
-        const int lb = (WIN ? hole.key(kbase) : kbase) / p.bs + lane;
+        const int lb = WIN ? hole.block(kbase + lane * p.bs, p.bs) : kbase / p.bs + lane;
         int phys = (int)p.num_blocks;  // out of range: the box reads as zeros
-        if (lane < nb_per_tile && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
+        if (lane < nb_per_tile && lb < nblk) {
           const int b = __ldg(bt + lb);
           if (b >= 0 && (int64_t)b < p.num_blocks)
             phys = b;
@@ -289,16 +289,16 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p,
         if (lane == 0) {
           Meta& m = meta[stage];
           m.item = idx;
-          m.kbase = WIN ? hole.key(kbase) : kbase;
+          m.kbase = kbase;
           m.flags = ((kbase + kDecTileKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
           m.seq = it.seq;
           m.kvh = it.kvh;
           m.row0 = it.row0;
           m.nrows = it.nrows;
-          m.ke = WIN ? hole.end(it.ke) : it.ke;
+          m.ke = it.ke;
           m.part = it.part;
           m.grp = it.grp;
-          m.L = L;
+          m.L = WIN ? L - hole.len : L;
           m.n = n;
           m.qstart = qstart;
           mbar_arrive_expect_tx(&full[stage], 2 * C::kTileBytes + (first ? it.nrows * C::kQRowBytes : 0));

@@ -270,8 +270,8 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
 // NR: rows per item (4, 8 or 16; the MMA's N stays 16, extra columns unused).
 // F8: the pools hold E4M3 codes (q bf16): staged codes are converted to fp16
 // tiles and the MMAs run on fp16 operands.  WIN: a query sees its last
-// p.window keys and the first p.num_sink; the tiles between them are not read
-// (Hole), nor are blocks that no row of the item sees.
+// p.window keys and the first p.num_sink; the blocks between them are not read
+// (Hole; keys and lengths below are places then).
 template <int NR, bool F8, bool WIN>
 __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnParams p,
                                                             const __grid_constant__ CUtensorMap qmap,
@@ -381,11 +381,11 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
       }
       const int nblk = (L + p.bs - 1) / p.bs;
       const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
-      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, p.bs);  // WIN
       auto block_of = [&](int kbase) -> int {  // physical block of this lane's block in the tile
-        const int lb = (WIN ? hole.key(kbase) : kbase) / p.bs + lane;
+        const int lb = WIN ? hole.block(kbase + lane * p.bs, p.bs) : kbase / p.bs + lane;
         int phys_ = (int)p.num_blocks;  // out of range: the box reads as zeros
-        if (lane < nb_per_tile && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
+        if (lane < nb_per_tile && lb < nblk) {
           const int b = __ldg(bt + lb);
           if (b >= 0 && (int64_t)b < p.num_blocks)
             phys_ = b;
@@ -437,16 +437,16 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
         if (lane == 0) {
           Meta& m = meta[F8 ? (g & 3) : st];
           m.item = idx;
-          m.kbase = WIN ? hole.key(kbase) : kbase;
+          m.kbase = kbase;
           m.flags = ((kbase + kKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
           m.seq = it.seq;
           m.kvh = it.kvh;
           m.row0 = it.row0;
           m.nrows = it.nrows;
-          m.ke = WIN ? hole.end(it.ke) : it.ke;
+          m.ke = it.ke;
           m.part = it.part;
           m.grp = it.grp;
-          m.L = L;
+          m.L = WIN ? L - hole.len : L;
           m.n = n;
           m.qstart = qstart;
           mbar_arrive_expect_tx(&bars->k_full[st], (F8 ? kCodeTile : kTileBytes) + (first ? 2 * kQHalf : 0));
@@ -508,10 +508,10 @@ __global__ void __launch_bounds__(Lay<F8>::kThreads, 1) dectc_kernel(const AttnP
       const int qstart = p.query_start_loc[it.seq];
       const int n = p.query_start_loc[it.seq + 1] - qstart;
       const int nblk = (L + p.bs - 1) / p.bs;
-      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
-      const int lb = (WIN ? hole.key(it.kb) : it.kb) / p.bs + lane;
+      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, p.bs);  // WIN
+      const int lb = WIN ? hole.block(it.kb + lane * p.bs, p.bs) : it.kb / p.bs + lane;
       int phys = (int)p.num_blocks;  // out of range: the box reads as zeros
-      if (lane < nb_per_tile && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
+      if (lane < nb_per_tile && lb < nblk) {
         const int b = __ldg(p.block_tables + (int64_t)it.seq * p.max_blocks + lb);
         if (b >= 0 && (int64_t)b < p.num_blocks)
           phys = b;

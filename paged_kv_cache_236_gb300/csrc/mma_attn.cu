@@ -182,7 +182,8 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* w,
 // output; the shared-memory and TMEM layouts are those of 128, with the
 // second halves unused at 64).  Each softmax thread owns D / 2 output
 // columns of its row.  WIN: a query sees its last p.window keys and the
-// first p.num_sink (Hole: the tiles between them are not read).
+// first p.num_sink; the blocks between them are not read (Hole; keys and
+// lengths below are places then).
 template <int D, bool kFaultHook, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams p,
                                                                const __grid_constant__ CUtensorMap qmap,
@@ -250,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
   const int nb = kKeys / p.bs;  // physical blocks per tile
   // physical block of this lane's block in the item's tile at place kbase
   auto block_of = [&](const int32_t* bt, int nblk, int kbase, const Hole& hole) -> int {
-    const int lb = (WIN ? hole.key(kbase) : kbase) / p.bs + lane;
+    const int lb = WIN ? hole.block(kbase + lane * p.bs, p.bs) : kbase / p.bs + lane;
     int phys = (int)p.num_blocks;  // out of range: reads as zeros
-    if (lane < nb && lb < nblk && !(WIN && hole.hides(lb * p.bs, p.bs, p.num_sink))) {
+    if (lane < nb && lb < nblk) {
       const int b = __ldg(bt + lb);
       if (b >= 0 && (int64_t)b < p.num_blocks)
         phys = b;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
           const int nblk = (L + p.bs - 1) / p.bs;
           const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
           const int n = p.query_start_loc[it.seq + 1] - qstart;
-          sl.phys0[lane] = block_of(bt, nblk, it.kb, Hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys));
+          sl.phys0[lane] = block_of(bt, nblk, it.kb, Hole(L, n, it.row0 / p.G, p.window, p.num_sink, p.bs));
           if (lane == 0) {
             sl.it = it;
             sl.L = L;
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
         const bool done = slots[qb].done != 0;
         const WorkItem it = slots[qb].it;
         const int L = slots[qb].L;
-        const Hole hole(L, slots[qb].n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
+        const Hole hole(L, slots[qb].n, it.row0 / p.G, p.window, p.num_sink, p.bs);  // WIN
         int phys = slots[qb].phys0[lane];
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->slot_free[qb]);
@@ -536,20 +537,21 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
       const ItemSlot& sl = slots[qb];
       const bool done = sl.done != 0;
       const WorkItem it = sl.it;
-      const int L = sl.L, qstart = sl.qstart, n = sl.n;
+      const int qstart = sl.qstart, n = sl.n;
+      const int L = WIN ? sl.L - Hole(sl.L, n, it.row0 / p.G, p.window, p.num_sink, p.bs).len : sl.L;
       mbar_arrive(&bars->slot_free[qb]);
       if (done) break;
       const bool valid = r < it.nrows;
       const int row = it.row0 + r;
       const int tok = row / p.G, gh = row - tok * p.G;
-      const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, kKeys);  // WIN
-      const int vis = valid ? min(WIN ? hole.end(it.ke) : it.ke, p.causal ? L - n + tok + 1 : L) : 0;
+      const int vis = valid ? min(it.ke, p.causal ? L - n + tok + 1 : L) : 0;
+      const int lo_item = WIN ? L - n + it.row0 / p.G + 1 - p.window : 0;  // first key of the first row's window
       float m_ref = -CUDART_INF_F, l = 0.f;
       int owe = -1;  // after a failed wait: the pair barriers of the item not yet taken
       const int ntiles = (it.ke - it.kb + kKeys - 1) / kKeys;
       for (int j = 0; j < ntiles; ++j, ++g) {
         const int sb = g & 1, vs = g % kVStages;
-        const int kt = WIN ? hole.key(it.kb + j * kKeys) : it.kb + j * kKeys;  // first key of the tile
+        const int kt = it.kb + j * kKeys;  // first key of the tile
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (g >> 1) & 1, wc))) {
           owe = ntiles - j + 2;
           break;
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
           }
         }
         // a tile that holds keys before every row's window
-        const bool early = WIN && kt < hole.lo && kt + kKeys > p.num_sink;
+        const bool early = WIN && kt < lo_item && kt + kKeys > p.num_sink;
         if ((kt + kKeys > L || early) && h < kNH) {
           // keys at or past the sequence's end hold arbitrary bits, as those before
           // the windows may: zero their V rows (thread: key r of the tile, d-half
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
             owe = ntiles - j + 1;
             break;
           }
-          if (kt + r >= L || (WIN && kt + r < hole.lo && kt + r >= p.num_sink)) {
+          if (kt + r >= L || (WIN && kt + r < lo_item && kt + r >= p.num_sink)) {
             uint4* v0 = reinterpret_cast<uint4*>(smem + kVOff + vs * kTileBytes + h * kHalfKV + r * 128);
 #pragma unroll
             for (int t = 0; t < 8; ++t) v0[t] = make_uint4(0, 0, 0, 0);

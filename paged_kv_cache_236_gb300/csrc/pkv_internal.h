@@ -137,22 +137,21 @@ struct PlanParams {
 };
 
 // The keys that an item of a windowed call leaves out: [at, at + len), whole
-// tiles between the first keys (seen by every query) and the window of its
-// first token tok0, whose first key is lo.  An item's kb and ke count the keys
-// without them: key(c) = c < at ? c : c + len.
+// blocks between the first keys (seen by every query) and the window of its
+// first token tok0.  Its kb, ke and key tiles count places, the keys without
+// them, so that a tile may hold the first keys and the window's side by side:
+// place p is key p < at ? p : p + len.  Past `at`, keys and lengths minus len are
+// places, in which the masks are those of a sequence of L - len keys.
 struct Hole {
-  int at, len, lo;
+  int at, len;
 #ifdef __CUDACC__
-  __device__ __forceinline__ Hole(int L, int n, int tok0, int window, int num_sink, int tile) {
-    lo = L - n + tok0 + 1 - window;
-    at = (num_sink + tile - 1) / tile * tile;
-    len = max(0, max(lo, 0) / tile * tile - at);
+  __device__ __forceinline__ Hole(int L, int n, int tok0, int window, int num_sink, int bs) {
+    const int lo = L - n + tok0 + 1 - window;  // first key of the window
+    at = (num_sink + bs - 1) / bs * bs;
+    len = max(0, max(lo, 0) / bs * bs - at);
   }
-  // key of a tile's first place, and the key bound of an item that ends at place c
-  __device__ __forceinline__ int key(int c) const { return c < at ? c : c + len; }
-  __device__ __forceinline__ int end(int c) const { return c <= at ? c : c + len; }
-  // no row of the item sees keys [k, k + count), for keys before the rows' own
-  __device__ __forceinline__ bool hides(int k, int count, int num_sink) const { return k >= num_sink && k + count <= lo; }
+  // block of a sequence's table that holds place p (a multiple of the block size)
+  __device__ __forceinline__ int block(int p, int bs) const { return (p < at ? p : p + len) / bs; }
 #endif
 };
 

@@ -116,7 +116,7 @@ __device__ __forceinline__ int unit_keys(const SeqDesc& d, int u, const PlanPara
   const int last_tok = (r1 - 1) / p.G;
   const int keys = p.causal ? (d.L - d.n + last_tok + 1) : d.L;
   if (p.window == 0) return keys;
-  return keys - Hole(d.L, d.n, u * d.unit_rows / p.G, p.window, p.num_sink, d.mma ? kMmaTileKeys : p.dec_tile_keys).len;
+  return keys - Hole(d.L, d.n, u * d.unit_rows / p.G, p.window, p.num_sink, p.bs).len;
 }
 
 __device__ __forceinline__ void split_of(int keys, int chunk, int tile, int& nsplit, int& per) {
