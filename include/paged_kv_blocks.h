@@ -201,7 +201,8 @@ pkv_status pkv_bm_stats(const pkv_block_manager* bm, int32_t* free_blocks, int32
  * [0, num_blocks), no destination twice, no destination that is also a
  * source (the block manager never produces either).  Pool bases, the block's
  * bytes and the layer stride's bytes must be multiples of 16.  num_copies ==
- * 0 is a no-op.  Asynchronous on `stream`: the copies are ordered before
+ * 0 is a no-op.  dtype is the pools' element (PKV_DTYPE_FP8_E4M3 among them).
+ * Asynchronous on `stream`: the copies are ordered before
  * later work on that stream (the step's paged_kv_write).
  */
 pkv_status paged_kv_copy_blocks(void* k_cache, void* v_cache, const int32_t* copies, int32_t num_copies,

@@ -19,6 +19,7 @@ tensors are not on a CUDA device, the calls raise.
     paged_kv_compact(k_cache, v_cache, block_tables, kept)     (eviction)
     paged_attention_window_forward(q, k_cache, v_cache, ..., scale, window, num_sink)
     paged_kv_write_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache)
+    paged_kv_write_fp8block(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales)
 
 Block pool per layer: ``[num_blocks, block_size, num_kv_heads, head_dim]``
 ("ADR 004: Paged Attention Serving Integration", Decision 4 - a per-layer
@@ -43,7 +44,7 @@ __all__ = [
     "paged_kv_write_rope", "paged_kv_write_rope_fp8", "rope_frequencies", "rope_amplitude",
     "paged_attention_scores", "paged_attention_scores_fp8kv", "scores_workspace_size", "scores_workspace_min",
     "paged_kv_select", "paged_kv_compact", "paged_attention_window_forward",
-    "paged_kv_write_norm_rope", "paged_kv_write_norm_rope_fp8",
+    "paged_kv_write_norm_rope", "paged_kv_write_norm_rope_fp8", "paged_kv_write_fp8block", "fp8block_write_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -155,6 +156,9 @@ def lib() -> ctypes.CDLL:
                     ("paged_attention_window_forward", L.paged_attention_forward.argtypes),
                     ("paged_kv_write_rope", _ROPE_ARGS + [c_vp]),
                     ("paged_kv_write_rope_fp8", _ROPE_ARGS + [c_f, c_f, c_vp]),
+                    ("paged_kv_write_fp8block", [c_vp] * 7 + [c_i64, c_i64, c_i32, c_i32, c_i32, c_i64, c_i64, c_vp, c_sz,
+                                                 c_i32, c_vp]),
+                    ("paged_kv_copy_block_scales", [c_vp, c_vp, c_vp, c_i32, c_i32, c_i64, c_i64, c_i32, c_vp]),
                     ("paged_kv_write_norm_rope", _NORM_ARGS + [c_vp]),
                     ("paged_kv_write_norm_rope_fp8", _NORM_ARGS + [c_f, c_f, c_vp]),
                     ("paged_attention_scores", _SCORES_ARGS + [c_vp, c_sz, c_i32, c_vp]),
@@ -163,6 +167,8 @@ def lib() -> ctypes.CDLL:
                     ("paged_kv_compact", [c_vp] * 7 + [c_i32] * 3 + [c_i64] + [c_i32] * 6 + [c_vp])):
                 getattr(L, name).restype = c_i32
                 getattr(L, name).argtypes = args
+            L.paged_kv_write_fp8block_workspace.restype = c_sz
+            L.paged_kv_write_fp8block_workspace.argtypes = [c_i64, c_i64, c_i32]
             for name in ("paged_attention_scores_workspace_size", "paged_attention_scores_workspace_min"):
                 getattr(L, name).restype = c_sz
                 getattr(L, name).argtypes = [c_i32, c_i64, c_i32, c_i32, c_i64]
@@ -623,17 +629,22 @@ class BlockManager:
         return {"free": f.value, "idle": i.value, "in_use": u.value, "cached": c.value}
 
 
-def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, copies) -> None:
+def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, copies, k_scales: torch.Tensor | None = None,
+                v_scales: torch.Tensor | None = None) -> None:
     """Copy-on-write on the device pool: block ``dst`` of every layer's K and
     V pool becomes a copy of block ``src`` for each host pair (src, dst) of
     ``copies`` (int32 [n, 2], as ``BlockManager.update`` / ``step`` return).
     Caches are ``[NB, bs, Hkv, D]`` or ``[layers, NB, bs, Hkv, D]`` (each
-    layer's pool contiguous).  Runs on the current stream."""
+    layer's pool contiguous), bf16, f32 or FP8.  ``k_scales, v_scales``
+    (float32 ``[NB, Hkv]`` or ``[layers, NB, Hkv]``): the blocks' rows of scales
+    (``paged_kv_write_fp8block``) go with them.  Runs on the current stream."""
     dev = _need_cuda(k_cache, v_cache)
     pairs = _host(copies, np.int32).reshape(-1, 2)
-    if k_cache.dtype not in DTYPE or v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or \
+    if k_cache.dtype not in _POOL_DTYPE or v_cache.dtype != k_cache.dtype or v_cache.shape != k_cache.shape or \
             v_cache.stride() != k_cache.stride():
-        raise ValueError("k_cache and v_cache must share dtype (bfloat16 or float32), shape and strides")
+        raise ValueError("k_cache and v_cache must share dtype (bfloat16, float32 or FP8), shape and strides")
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales go together")
     if k_cache.dim() == 4:
         layers, stride = 1, 0
         pool = k_cache
@@ -645,10 +656,19 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, copies) -> None:
     if not pool.is_contiguous():
         raise ValueError("each layer's pool must be contiguous")
     NB, bs, Hkv, D = pool.shape
+    for t in (k_scales, v_scales):
+        if t is not None and (t.shape != k_cache.shape[:-3] + (Hkv,) or t.dtype != torch.float32 or t.device != dev or
+                              t.stride() != k_scales.stride() or not (t[0] if t.dim() == 3 else t).is_contiguous()):
+            raise ValueError("k_scales and v_scales must be float32 [NB, Hkv] or [layers, NB, Hkv], alike, each layer's "
+                             "contiguous")
     with torch.cuda.device(dev):
         _check(lib().paged_kv_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(),
                                           pairs.ctypes.data if len(pairs) else None, len(pairs), layers, stride,
-                                          NB, bs, Hkv, D, DTYPE[k_cache.dtype], _stream(dev)))
+                                          NB, bs, Hkv, D, _POOL_DTYPE[k_cache.dtype], _stream(dev)))
+        if k_scales is not None:
+            _check(lib().paged_kv_copy_block_scales(k_scales.data_ptr(), v_scales.data_ptr(),
+                                                    pairs.ctypes.data if len(pairs) else None, len(pairs), layers,
+                                                    k_scales.stride(0) if layers > 1 else 0, NB, Hkv, _stream(dev)))
 
 
 # ----------------------------------------------------------------------------
@@ -657,6 +677,10 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, copies) -> None:
 # ----------------------------------------------------------------------------
 
 _FP8_TYPES = {torch.uint8} | ({torch.float8_e4m3fn} if hasattr(torch, "float8_e4m3fn") else set())
+
+
+_POOL_DTYPE = dict(DTYPE)
+_POOL_DTYPE.update({t: 2 for t in _FP8_TYPES})
 
 
 def _check_fp8_pools(k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
@@ -1180,10 +1204,6 @@ def paged_kv_select(scores: torch.Tensor, context_lens: torch.Tensor, budget: in
     return out
 
 
-_POOL_DTYPE = dict(DTYPE)
-_POOL_DTYPE.update({t: 2 for t in _FP8_TYPES})
-
-
 def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, kept: torch.Tensor, *,
                      dst_block_tables: torch.Tensor | None = None, scores: torch.Tensor | None = None,
                      score_rows: torch.Tensor | None = None) -> None:
@@ -1218,3 +1238,47 @@ def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
           None if dst_block_tables is None else dst_block_tables.data_ptr(), kept.data_ptr(),
           None if score_rows is None else score_rows.data_ptr(), None if scores is None else scores.data_ptr(), B, Hkv,
           D, NB, bs, max(1, table[1]), budget, rows, length, _POOL_DTYPE[dtype])
+
+
+# ----------------------------------------------------------------------------
+# FP8 pools with a scale for each block and kv head (include/paged_kv_fp8block.h)
+# ----------------------------------------------------------------------------
+
+def fp8block_write_workspace(num_tokens: int, num_blocks: int, block_size: int) -> int:
+    """Bytes of workspace that ``paged_kv_write_fp8block`` wants."""
+    return int(lib().paged_kv_write_fp8block_workspace(num_tokens, num_blocks, block_size))
+
+
+def _check_block_scales(k_cache, v_cache, k_scales, v_scales) -> None:
+    _check_fp8_pools(k_cache, v_cache)
+    shape = (k_cache.shape[0], k_cache.shape[2])
+    for t in (k_scales, v_scales):
+        if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError(f"k_scales and v_scales must be contiguous float32 {list(shape)}")
+
+
+def paged_kv_write_fp8block(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, *,
+                            workspace: torch.Tensor | None = None) -> None:
+    """Encode ``k, v [T, Hkv, D]`` (bf16 or f32) as E4M3 codes with a scale for
+    each block and kv head and scatter them at ``slot_mapping`` (< 0 skips).
+
+    ``k_scales, v_scales`` (float32 ``[NB, Hkv]``, zeros at first) hold powers
+    of two: a block's scale covers the largest row it holds.  It grows as rows
+    arrive, with the block's earlier codes moved to it, and starts anew when a
+    call writes the block's first slot."""
+    dev = _device_of(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales, workspace)
+    _check_block_scales(k_cache, v_cache, k_scales, v_scales)
+    NB, bs, Hkv, D = k_cache.shape
+    T, ks, vs = _new_rows(k, v, slot_mapping, Hkv, D, set(DTYPE))
+    if T > 1 and 0 in (ks, vs):  # the C call takes a stride of 0 for dense
+        raise ValueError("k and v must not repeat one token's row (a token stride of 0)")
+    need = fp8block_write_workspace(T, NB, bs)
+    if workspace is None:
+        workspace = _on(dev, _workspace, k.device, need) if need else None
+    elif workspace.dtype != torch.uint8 or workspace.numel() < need:
+        raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
+    _call(lib().paged_kv_write_fp8block, dev, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
+          v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), T, NB, bs, Hkv, D, ks if T > 1 else 0,
+          vs if T > 1 else 0, None if workspace is None else workspace.data_ptr(),
+          0 if workspace is None else workspace.numel(), DTYPE[k.dtype])
