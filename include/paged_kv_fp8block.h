@@ -81,6 +81,32 @@ pkv_status paged_kv_copy_block_scales(float* k_scales, float* v_scales, const in
                                       int32_t num_layers, int64_t layer_stride, int64_t num_blocks,
                                       int32_t num_kv_heads, void* stream);
 
+/*
+ * paged_attention_forward_fp8block - paged_attention_forward over such pools:
+ * softmax(scale * q k^T) v with k and v the values above, q and out bf16,
+ * head_dim 128.
+ *
+ *   window, num_sink  as paged_attention_window_forward; window 0: no window
+ *                     (num_sink is ignored).  A window needs causal != 0.
+ *   the rest          as paged_attention_forward (the same block sizes, groups,
+ *                     query counts, workspace and errors)
+ * Numerics: q is split into two E4M3 terms for each row's own power-of-two
+ * scale (exact to 2^-18 of the row's largest |q|; the tensor cores multiply
+ * codes by codes), logits and sums are fp32; a weight times its V scale is
+ * split into E5M2 terms of 9 bits together in calls of few rows, and rounded to
+ * fp16 in calls of many (at least 11 bits for those above 2^-21 of the row's
+ * largest).
+ */
+pkv_status paged_attention_forward_fp8block(const void* q, const void* k_cache, const void* v_cache,
+                                            const float* k_scales, const float* v_scales,
+                                            const int32_t* block_tables, const int32_t* context_lens,
+                                            const int32_t* query_start_loc, void* out, int32_t num_seqs,
+                                            int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int64_t num_blocks, int32_t block_size,
+                                            int32_t max_blocks_per_seq, int32_t max_query_len, float scale,
+                                            int32_t causal, int32_t window, int32_t num_sink, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,7 @@ tensors are not on a CUDA device, the calls raise.
     paged_attention_window_forward(q, k_cache, v_cache, ..., scale, window, num_sink)
     paged_kv_write_norm_rope(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, k_cache, v_cache)
     paged_kv_write_fp8block(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales)
+    paged_attention_forward_fp8block(q, k_cache, v_cache, k_scales, v_scales, ..., scale)
 
 Block pool per layer: ``[num_blocks, block_size, num_kv_heads, head_dim]``
 ("ADR 004: Paged Attention Serving Integration", Decision 4 - a per-layer
@@ -45,6 +46,7 @@ __all__ = [
     "paged_attention_scores", "paged_attention_scores_fp8kv", "scores_workspace_size", "scores_workspace_min",
     "paged_kv_select", "paged_kv_compact", "paged_attention_window_forward",
     "paged_kv_write_norm_rope", "paged_kv_write_norm_rope_fp8", "paged_kv_write_fp8block", "fp8block_write_workspace",
+    "paged_attention_forward_fp8block",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -158,6 +160,8 @@ def lib() -> ctypes.CDLL:
                     ("paged_kv_write_rope_fp8", _ROPE_ARGS + [c_f, c_f, c_vp]),
                     ("paged_kv_write_fp8block", [c_vp] * 7 + [c_i64, c_i64, c_i32, c_i32, c_i32, c_i64, c_i64, c_vp, c_sz,
                                                  c_i32, c_vp]),
+                    ("paged_attention_forward_fp8block", [c_vp] * 9 + [c_i32, c_i64, c_i32, c_i32, c_i32, c_i64, c_i32,
+                                                          c_i32, c_i32, c_f, c_i32, c_i32, c_i32, c_vp, c_sz, c_vp]),
                     ("paged_kv_copy_block_scales", [c_vp, c_vp, c_vp, c_i32, c_i32, c_i64, c_i64, c_i32, c_vp]),
                     ("paged_kv_write_norm_rope", _NORM_ARGS + [c_vp]),
                     ("paged_kv_write_norm_rope_fp8", _NORM_ARGS + [c_f, c_f, c_vp]),
@@ -1282,3 +1286,24 @@ def paged_kv_write_fp8block(k: torch.Tensor, v: torch.Tensor, slot_mapping: torc
           v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), T, NB, bs, Hkv, D, ks if T > 1 else 0,
           vs if T > 1 else 0, None if workspace is None else workspace.data_ptr(),
           0 if workspace is None else workspace.numel(), DTYPE[k.dtype])
+
+
+def paged_attention_forward_fp8block(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                     k_scales: torch.Tensor, v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                     context_lens: torch.Tensor, query_start_loc: torch.Tensor, scale: float,
+                                     causal: bool = True, *, window: int = 0, num_sink: int = 0,
+                                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                                     max_query_len: int = 0) -> torch.Tensor:
+    """``paged_attention_forward`` over FP8 pools whose blocks and kv heads have
+    scales of their own (``paged_kv_write_fp8block``); q and the result are
+    bf16, head_dim 128.  With ``window`` > 0 a query sees its last ``window``
+    tokens and the first ``num_sink`` (``paged_attention_window_forward``)."""
+    dev = _need_cuda(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, query_start_loc)
+    _check_block_scales(k_cache, v_cache, k_scales, v_scales)
+    seen = _window(window, num_sink, 0)
+    args, out, workspace = _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                                             1.0, 1.0, causal, out, workspace, max_query_len, dev)
+    with torch.cuda.device(dev):
+        _check(lib().paged_attention_forward_fp8block(*args[:3], k_scales.data_ptr(), v_scales.data_ptr(), *args[3:18],
+                                                      *seen, *args[21:]))
+    return out

@@ -16,6 +16,7 @@
 #include <string.h>
 
 #include "paged_kv.h"
+#include "paged_kv_fp8block.h"
 #include "pkv_internal.h"
 
 namespace {
@@ -365,16 +366,25 @@ static pkv_status check_fused_write(FusedWrite* fw, int Hkv, int D, bool kv_fp8,
   return PKV_OK;
 }
 
+// Pools with a scale for each block and kv head (paged_attention_forward_fp8block).
+struct BlockScales {
+  const float* k;
+  const float* v;
+};
+
 // The forward call; kv_fp8: the pools hold E4M3 codes (q and out bf16), read
 // as code * k_scale and code * v_scale.  fw: the step's new K/V rows, written
-// first (by extra CTAs of the planner's launch where the rows allow it).
+// first (by extra CTAs of the planner's launch where the rows allow it).  window
+// > 0: queries see their last `window` keys and the first num_sink.  blocks: the
+// pools' scales, where blocks have their own (k_scale and v_scale are then 1).
 static pkv_status forward_impl(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                                const int32_t* context_lens, const int32_t* query_start_loc, void* out,
                                int32_t num_seqs, int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                                int32_t head_dim, int64_t num_blocks, int32_t block_size, int32_t max_blocks_per_seq,
                                int32_t max_query_len, float scale, int32_t causal, int32_t hints, void* workspace,
                                size_t workspace_bytes, pkv_dtype dtype, bool kv_fp8, float k_scale, float v_scale,
-                               void* stream, const FusedWrite* fw = nullptr, int window = 0, int num_sink = 0) {
+                               void* stream, const FusedWrite* fw = nullptr, int window = 0, int num_sink = 0,
+                               const BlockScales* blocks = nullptr) {
   g_msg[0] = 0;
   const int B = num_seqs, Hq = num_q_heads, Hkv = num_kv_heads, D = head_dim, bs = block_size;
   const int64_t T = num_tokens;
@@ -405,6 +415,9 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
     return fail(PKV_ERR_INVALID_ARG, "null pointer");
   if (!aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache))
     return fail(PKV_ERR_INVALID_ARG, "q, out and the caches must be 16-byte aligned");
+  if (blocks && (!blocks->k || !blocks->v)) return fail(PKV_ERR_INVALID_ARG, "null pointer");
+  if (blocks && ((reinterpret_cast<uintptr_t>(blocks->k) | reinterpret_cast<uintptr_t>(blocks->v)) & 3u))
+    return fail(PKV_ERR_INVALID_ARG, "scales must be aligned to their elements");
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & (kAlign - 1)))
     return fail(PKV_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
   const WorkspaceLayout lay = workspace_layout(B, T, Hq, Hkv, D, workspace_bytes, 0, false);
@@ -440,7 +453,8 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   // host hint bounds every sequence's rows by 8, the CUDA-core kernel otherwise
   const bool f8tc = kv_fp8 && D == 128 && (G & (G - 1)) == 0 && max_query_len > 0 &&
                     (int64_t)max_query_len * G <= 8;
-  const bool dectc = (mma_ok && D == 128 && (G & (G - 1)) == 0 && G <= kTcDecRows) || f8tc;
+  // pools with block scales: a kernel that multiplies the codes, for any G
+  const bool dectc = (mma_ok && D == 128 && (G & (G - 1)) == 0 && G <= kTcDecRows) || f8tc || blocks;
   const int dec_rows_max = dectc ? kTcDecRows : kDecRows;
   // rows of softmax per key in that kernel: a power of two >= G (so items hold
   // whole tokens) covering the hinted query length; 16 when there is no hint
@@ -572,6 +586,10 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   ap.num_blocks = num_blocks;
   ap.scale_log2 = (kv_fp8 ? scale * k_scale : scale) * 1.4426950408889634f;
   ap.v_scale = kv_fp8 ? v_scale : 1.f;
+  if (blocks) {
+    ap.k_scales = blocks->k;
+    ap.v_scales = blocks->v;
+  }
   ap.causal = causal ? 1 : 0;
   ap.window = window;
   ap.num_sink = num_sink;
@@ -605,7 +623,17 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
     return cuda_fail(e, "profile event");
   ap.counter = &header->dec_counter;
   ap.items = dec_items;
-  if (dectc && kv_fp8) {
+  if (blocks) {
+    CUtensorMap kmap_sw, vmap_sw;
+    if ((st = encode_pool_map(&kmap_sw, k_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
+        PKV_OK)
+      return st;
+    if ((st = encode_pool_map(&vmap_sw, v_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
+        PKV_OK)
+      return st;
+    if ((e = launch_dec_fp8block(ap, tc_rows, kmap_sw, vmap_sw, dev->sms, s)) != cudaSuccess)
+      return cuda_fail(e, "decode (block scales) launch");
+  } else if (dectc && kv_fp8) {
     CUtensorMap qmap16;
     if ((st = encode_q_map(&qmap16, q, T, Hq, D, 64, G, kTcDecRows / G)) != PKV_OK) return st;
     // kmap / vmap (uint8, one {128, 1, bs, 1} box of codes per block) were encoded above
@@ -659,6 +687,27 @@ pkv_status paged_attention_window_forward(const void* q, const void* k_cache, co
                       num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, max_query_len,
                       scale, 1, 0, workspace, workspace_bytes, dtype, false, 1.f, 1.f, stream, nullptr, window,
                       num_sink);
+}
+
+pkv_status paged_attention_forward_fp8block(const void* q, const void* k_cache, const void* v_cache,
+                                            const float* k_scales, const float* v_scales,
+                                            const int32_t* block_tables, const int32_t* context_lens,
+                                            const int32_t* query_start_loc, void* out, int32_t num_seqs,
+                                            int64_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim, int64_t num_blocks, int32_t block_size,
+                                            int32_t max_blocks_per_seq, int32_t max_query_len, float scale,
+                                            int32_t causal, int32_t window, int32_t num_sink, void* workspace,
+                                            size_t workspace_bytes, void* stream) {
+  g_msg[0] = 0;
+  if (head_dim != 128) return fail(PKV_ERR_UNSUPPORTED, "block scales: head_dim %d (supported: 128)", head_dim);
+  if (window < 0 || num_sink < 0) return fail(PKV_ERR_INVALID_ARG, "window and num_sink must be >= 0");
+  if (window > 1 << 30 || num_sink > 1 << 30) return fail(PKV_ERR_UNSUPPORTED, "window or num_sink above 2^30");
+  if (window > 0 && !causal) return fail(PKV_ERR_INVALID_ARG, "a window needs causal attention");
+  const BlockScales blocks{k_scales, v_scales};
+  return forward_impl(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, out, num_seqs, num_tokens,
+                      num_q_heads, num_kv_heads, head_dim, num_blocks, block_size, max_blocks_per_seq, max_query_len,
+                      scale, causal, 0, workspace, workspace_bytes, PKV_DTYPE_BF16, true, 1.f, 1.f, stream, nullptr,
+                      window, num_sink, &blocks);
 }
 
 pkv_status paged_kv_write_attention_forward(const void* k, const void* v, const int64_t* slot_mapping,

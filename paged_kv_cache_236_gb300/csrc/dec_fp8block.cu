@@ -1,0 +1,869 @@
+// Attention of few rows per kv head (decode, short verify windows) over pools of
+// E4M3 codes with a scale for each block and kv head: tcgen05.mma on the codes
+// themselves (paged_attention_forward_fp8block).
+//
+// With codes ck, cv and block scales sk, sv, for rows r of one kv head:
+//   x[r][j] = scale log2(e) (q_r . ck_j) sk(j)          (log2 units)
+//   out_r   = sum_j 2^(x - m) sv(j) cv_j / sum_j 2^(x - m)
+//
+// The tensor cores multiply 8-bit operands at twice the 16-bit rate, but the
+// point here is that the pools' tiles are operands as they land: converted to
+// 16 bits first, as the kernel for pools of one scale does, a tile's chain
+// of loads, conversion and MMAs sets the pace, at a third of the HBM rate.  So
+// the other operand is split into 8-bit terms instead, which cost columns of
+// an MMA whose columns are mostly unused anyway:
+//   q    = 2^e (q1 + q2), E4M3 each, with e from the row's largest |q|: 8
+//          significant bits, bf16's own, down to 2^-18 of that largest value;
+//   w    = 2^(x - m) sv 2^11 = w1 + w2 + w3, E5M2 each: the top bytes of an fp16
+//          value and of what is left of it, twice; 9 bits, down to 2^-16 (a
+//          row's largest w is 2^11 to 2^15: E4M3's range would lose the many small
+//          weights beside a large one).
+// S^T [128 keys x 2 NR] = K [128 x 128 d] . [q1; q2]^T      (A K-major)
+// O^T [128 d x 3 NR]   += V^T [128 d x 128 keys] . [w1; w2; w3]^T   (A MN-major)
+// so a thread holds a key's logits (the sum of two columns), and a thread an
+// output column (of three).  sk(j) multiplies a thread's logits; sv(j) moves
+// its exponent, and the running reference m is one of x + log2 sv, so that w
+// stays within its range whatever the blocks' scales are; the denominator takes
+// w / (2^11 sv).
+//
+// Roles (384 threads, one CTA per SM, persistent, items from an atomic counter
+// in the planner's largest-first order), as in the bf16 kernel:
+//   warp 0    K producer: per 128-key tile one {128 bytes, 1, block_size, 1} box
+//             per block (128-byte swizzle), the tile's scales and metadata.
+//             Block ids are read two tiles ahead and scales one, so that
+//             neither's latency is waited for;
+//   warp 11   V producer;
+//   warp 1    TMEM allocation, the thread that issues the MMAs;
+//   warps 2-5 softmax (thread = key = TMEM lane);
+//   warps 6-9 epilogue (thread = output column = TMEM lane of O^T);
+//   warp 10   item fetch, and the split of the item's q rows.
+// Shared memory: 6 stages of K and V codes (192 KB).  TMEM: S^T and O^T
+// double-buffered.  Waits are bounded, and end as in the bf16 kernel.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <limits.h>
+#include <math_constants.h>
+
+#include "dec_rows.cuh"
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kStages = 6;
+constexpr int kKeys = kMmaTileKeys;       // 128 keys per tile
+constexpr int kTileBytes = kKeys * 128;   // K or V codes: 16 KB
+constexpr int kStageBytes = 2 * kTileBytes;
+constexpr int kFetchLeadTiles = 4;        // the next item is fetched when this many tiles are left to load
+constexpr float kRescaleThreshold = 4.0f;  // log2 units
+constexpr int kWeightExp = 11;            // weights are 2^11 times their value, at most 2^15
+constexpr int kMetaDone = 2, kMetaLast = 1, kMetaFirst = 4;
+constexpr uint32_t kTmemCols = 256;
+
+// N of the MMAs: q's and the weights' terms of NR rows
+constexpr int round16(int x) { return (x + 15) / 16 * 16; }
+template <int NR>
+struct Lay {
+  static constexpr int kNQ = round16(2 * NR), kNP = round16(3 * NR);
+  static constexpr uint32_t kSCol = 0, kOCol = 64;  // buffer b at + b * kNQ, + b * kNP
+  static constexpr int kQOff = kStages * kStageBytes;
+  static constexpr int kPOff = kQOff + 2 * kNQ * 128;
+  static constexpr int kMetaOff = kPOff + 2 * kNP * 128;
+  static constexpr int kScaleOff = kMetaOff + kStages * 64;           // [stage][16] float4
+  static constexpr int kRedOff = kScaleOff + kStages * 256;
+  static constexpr int kSlotOff = kRedOff + 2 * 4 * NR * 4;
+  static constexpr int kISlotOff = kSlotOff + 2 * 256;
+  static constexpr int kQsOff = kISlotOff + 2 * 320;
+  static constexpr int kBarOff = kQsOff + 2 * NR * 4;
+  static constexpr int kNumBars = 3 * kStages + 8 + 8 + 4 + 4 + 1;
+  static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
+  static constexpr uint32_t kIdescS = idesc_f8(128, kNQ, kE4m3, kE4m3, false, false);
+  static constexpr uint32_t kIdescO = idesc_f8(128, kNP, kE4m3, kE5m2, true, false);
+  static_assert(2 * kNQ <= 64 && 64 + 2 * kNP <= (int)kTmemCols, "TMEM columns");
+  static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+struct alignas(16) Meta {
+  int item, kbase, flags, seq;
+  int kvh, row0, nrows, ke;
+  int part, grp, L, n;
+  int qstart, qbuf, pad1, pad2;
+};
+static_assert(sizeof(Meta) == 64, "meta slot");
+
+struct Bars {
+  uint64_t k_full[kStages], v_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t o_full[2], o_empty[2], ml_full[2], ml_empty[2];
+  uint64_t islot_full[2], islot_free[2];
+  uint64_t q_full[2], q_empty[2];  // an item's q terms written; its last S issued and its row scales read
+  uint64_t fetch_go;
+};
+static_assert(sizeof(Bars) == Lay<4>::kNumBars * 8, "barrier block");
+
+// What a tile's block has of scales: K's, log2 of V's, 2^-11 / V's.
+struct alignas(16) Scales {
+  float k, log_v, inv_v, pad;
+};
+
+// An item as the fetch warp hands it to the producers: L counts places, the
+// keys without those from `at` on that a window leaves out (len of them).
+struct alignas(16) ItemSlot {
+  WorkItem it;
+  int idx, L, qstart, n;
+  int done, nblk, at, len;
+  int phys[32];       // blocks of the first tile (0 ..), of the second (16 ..)
+  float2 scales[16];  // K's and V's of the first tile's blocks
+};
+static_assert(sizeof(ItemSlot) == 320, "item slot");
+
+struct alignas(16) EpSlot {
+  Meta mt;
+  float m[16], l[16];
+  int done;
+  int pad[15];
+};
+static_assert(sizeof(EpSlot) == 256, "epilogue slot");
+
+// [2^-60, 2^60]; a NaN is the least
+__device__ __forceinline__ float clamp_scale(float s) {
+  return s >= 0x1p-60f ? fminf(s, 0x1p60f) : 0x1p-60f;
+}
+__device__ __forceinline__ Scales make_scales(float k, float v) {
+  Scales s;
+  s.k = clamp_scale(k);
+  const float c = clamp_scale(v);
+  s.log_v = log2f(c);  // exact for powers of two
+  s.inv_v = __fdiv_rn(1.f / (1 << kWeightExp), c);
+  s.pad = 0.f;
+  return s;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[N]) {
+  if constexpr (N == 8) {
+    tmem_ld8(taddr, v);
+  } else if constexpr (N == 16) {
+    tmem_ld16(taddr, v);
+  } else if constexpr (N == 32) {
+    tmem_ld32(taddr, v);
+  } else if constexpr (N == 12) {
+    tmem_ld8(taddr, v);
+    tmem_ld4(taddr + 8, v + 8);
+  } else if constexpr (N == 24) {
+    tmem_ld16(taddr, v);
+    tmem_ld8(taddr + 16, v + 16);
+  } else {
+    static_assert(N == 48, "columns");
+    tmem_ld32(taddr, v);
+    tmem_ld16(taddr + 32, v + 32);
+  }
+}
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t (&v)[N]) {
+  if constexpr (N == 12) {
+    tmem_st8(taddr, v);
+    tmem_st4(taddr + 8, v + 8);
+  } else if constexpr (N == 24) {
+    tmem_st16(taddr, v);
+    tmem_st8(taddr + 16, v + 16);
+  } else {
+    static_assert(N == 48, "columns");
+    tmem_st32(taddr, v);
+    tmem_st16(taddr + 32, v + 32);
+  }
+}
+
+// NR: rows per item (4, 8 or 16)
+template <int NR>
+__global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnParams p,
+                                                                   const __grid_constant__ CUtensorMap kmap,
+                                                                   const __grid_constant__ CUtensorMap vmap) {
+  using Y = Lay<NR>;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* bars = reinterpret_cast<Bars*>(smem + Y::kBarOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Y::kBarOff + Y::kNumBars * 8);
+  Meta* meta = reinterpret_cast<Meta*>(smem + Y::kMetaOff);
+  Scales* tile_scales = reinterpret_cast<Scales*>(smem + Y::kScaleOff);  // [stage][16]
+  float* red = reinterpret_cast<float*>(smem + Y::kRedOff);              // [2][4 warps][NR rows]
+  float* row_scales = reinterpret_cast<float*>(smem + Y::kQsOff);        // [2][NR]
+  ItemSlot* islots = reinterpret_cast<ItemSlot*>(smem + Y::kISlotOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WaitCtl wc{p.err, wait_limit(p.wait_ns)};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->kv_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->s_full[b], 1);
+      mbar_init(&bars->s_free[b], 128);
+      mbar_init(&bars->p_full[b], 128);
+      mbar_init(&bars->pv_done[b], 1);
+      mbar_init(&bars->o_full[b], 1);
+      mbar_init(&bars->o_empty[b], 128);
+      mbar_init(&bars->ml_full[b], 128);
+      mbar_init(&bars->ml_empty[b], 128);
+      mbar_init(&bars->islot_full[b], 32);
+      mbar_init(&bars->islot_free[b], 2);  // both producers read the slot
+      mbar_init(&bars->q_full[b], 32);
+      mbar_init(&bars->q_empty[b], 1 + 4);  // the MMA thread's commit, the four softmax warps
+    }
+    mbar_init(&bars->fetch_go, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // as in the bf16 kernel: beside the many-row kernel the plan is complete at launch
+  if (!p.no_wait) pdl_wait();
+  const int n_items = __ldcg(&p.header->n_dec);
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t smem_base = smem_u32(smem);
+  const int nb = kKeys / p.bs;  // blocks per tile
+
+  // block of table row `bt` that holds the places from `place`; num_blocks (the box
+  // reads as zeros) past the end and for ids out of range
+  auto block_of = [&](const int32_t* bt, int nblk, int at, int len, int place) -> int {
+    const int lb = (place < at ? place : place + len) / p.bs;
+    if (lb >= nblk) return (int)p.num_blocks;
+    const int b = __ldg(bt + lb);
+    if (b >= 0 && (int64_t)b < p.num_blocks) return b;
+    raise_error(p.err, PKV_DEVERR_BLOCK_OUT_OF_RANGE);
+    return (int)p.num_blocks;
+  };
+
+  if (warp == 0 || warp == 11) {
+    // ================================================================ K / V producers
+    const bool vprod = warp == 11;
+    if (lane == 0) prefetch_tensormap(vprod ? &vmap : &kmap);
+    uint64_t* fullb = vprod ? bars->v_full : bars->k_full;
+    int g = 0;
+    // leaving early: the copies of the tiles issued last land first
+    auto drain = [&]() {
+      for (int j = max(0, g - kStages); j < g; ++j)
+        __all_sync(0xffffffffu, mbar_wait(&fullb[j % kStages], (j / kStages) & 1, wc));
+    };
+    for (int c = 0;; ++c) {
+      const int qb = c & 1;
+      if (!wait_all(&bars->islot_full[qb], (c >> 1) & 1, wc)) {
+        drain();
+        break;
+      }
+      const ItemSlot& sl = islots[qb];
+      const bool done = sl.done != 0;
+      const WorkItem it = sl.it;
+      const int idx = sl.idx, L = sl.L, qstart = sl.qstart, n = sl.n, nblk = sl.nblk, at = sl.at, len = sl.len;
+      int phys = sl.phys[lane & 15], next = sl.phys[16 + (lane & 15)];
+      float2 sc = sl.scales[lane & 15];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->islot_free[qb]);
+      if (done) {
+        if (vprod) break;
+        const int st = g % kStages;
+        if (!wait_all(&bars->kv_empty[st], ((g / kStages) & 1) ^ 1, wc)) {
+          drain();
+          break;
+        }
+        if (lane == 0) {
+          meta[st].item = -1;
+          meta[st].flags = kMetaDone;
+          mbar_arrive(&bars->k_full[st]);
+        }
+        break;
+      }
+      const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
+      bool ok = true;
+      for (int kbase = it.kb; kbase < it.ke; kbase += kKeys, ++g) {
+        const int st = g % kStages;
+        const bool first = kbase == it.kb;
+        // the ids of the tile after the next, the scales of the next
+        int after = (int)p.num_blocks;
+        if (lane < nb && kbase + 2 * kKeys < it.ke) after = block_of(bt, nblk, at, len, kbase + 2 * kKeys + lane * p.bs);
+        float nk = 1.f, nv = 1.f;
+        if (!vprod && lane < nb && kbase + kKeys < it.ke && next < p.num_blocks) {
+          const int64_t i = (int64_t)next * p.Hkv + it.kvh;
+          nk = __ldg(p.k_scales + i);
+          nv = __ldg(p.v_scales + i);
+        }
+        if (!wait_all(&bars->kv_empty[st], ((g / kStages) & 1) ^ 1, wc)) {
+          ok = false;
+          break;
+        }
+        if (!vprod && lane == 0 && it.ke - kbase <= kFetchLeadTiles * kKeys &&
+            (first || it.ke - (kbase - kKeys) > kFetchLeadTiles * kKeys))
+          mbar_arrive(&bars->fetch_go);  // once per item: the next one may be taken now
+        if (!vprod && p.fault_tile == g + 1 && blockIdx.x == 0) {
+          // testing only: this tile is never loaded, so the waits for it run out
+          phys = next;
+          next = after;
+          sc = make_float2(nk, nv);
+          continue;
+        }
+        uint8_t* dst = smem + st * kStageBytes + (vprod ? kTileBytes : 0);
+        if (!vprod) {
+          if (lane < nb) tile_scales[st * 16 + lane] = make_scales(sc.x, sc.y);
+          if (lane == 0) {
+            Meta& m = meta[st];
+            m.item = idx;
+            m.kbase = kbase;
+            m.flags = ((kbase + kKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
+            m.seq = it.seq;
+            m.kvh = it.kvh;
+            m.row0 = it.row0;
+            m.nrows = it.nrows;
+            m.ke = it.ke;
+            m.part = it.part;
+            m.grp = it.grp;
+            m.L = L;
+            m.n = n;
+            m.qstart = qstart;
+            m.qbuf = qb;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&fullb[st], kTileBytes);
+        __syncwarp();
+        if (lane < nb) tma_load_4d(dst + lane * p.bs * 128, vprod ? &vmap : &kmap, &fullb[st], 0, it.kvh, 0, phys);
+        phys = next;
+        next = after;
+        sc = make_float2(nk, nv);
+      }
+      if (!ok) {
+        drain();
+        break;
+      }
+    }
+  } else if (warp == 10) {
+    // ================================================================ item fetch, q terms
+    for (int c = 0;; ++c) {
+      const int qb = c & 1;
+      if (c >= 1 && !wait_all(&bars->fetch_go, (c - 1) & 1, wc)) break;
+      if (c >= 2 && !wait_all(&bars->islot_free[qb], ((c - 2) >> 1) & 1, wc)) break;
+      int idx = 0;
+      if (lane == 0) idx = atomicAdd(p.counter, 1);
+      idx = __shfl_sync(0xffffffffu, idx, 0);
+      ItemSlot& sl = islots[qb];
+      if (idx >= n_items) {
+        if (lane == 0) sl.done = 1;
+        mbar_arrive(&bars->islot_full[qb]);  // every lane: count 32
+        break;
+      }
+      WorkItem it;
+      {
+        const int4* src = reinterpret_cast<const int4*>(p.items + idx);
+        const int4 a = __ldcg(src), b = __ldcg(src + 1);
+        it.seq = a.x; it.kvh = a.y; it.row0 = a.z; it.nrows = a.w;
+        it.kb = b.x; it.ke = b.y; it.part = b.z; it.grp = b.w;
+      }
+      const int L = p.context_lens[it.seq];
+      const int qstart = p.query_start_loc[it.seq];
+      const int n = p.query_start_loc[it.seq + 1] - qstart;
+      const int nblk = (L + p.bs - 1) / p.bs;
+      // this lane's element pairs of the item's q rows, on their way while the block ids are read
+      const __nv_bfloat16* q0 =
+          static_cast<const __nv_bfloat16*>(p.q) + ((int64_t)qstart * p.Hq + (int64_t)it.kvh * p.G) * 128;
+      uint2 raw[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        raw[r] = make_uint2(0, 0);
+        if (r < it.nrows) {
+          const int row = it.row0 + r, tok = row / p.G, gh = row - tok * p.G;
+          raw[r] = __ldg(reinterpret_cast<const uint2*>(q0 + ((int64_t)tok * p.Hq + gh) * 128) + lane);
+        }
+      }
+      int at = 0, len = 0;
+      if (p.window > 0) {
+        const Hole hole(L, n, it.row0 / p.G, p.window, p.num_sink, p.bs);
+        at = hole.at;
+        len = hole.len;
+      }
+      const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
+      const int tile = it.kb + (lane >> 4) * kKeys;
+      int phys = (int)p.num_blocks;
+      if ((lane & 15) < nb && tile < it.ke) phys = block_of(bt, nblk, at, len, tile + (lane & 15) * p.bs);
+      sl.phys[lane] = phys;
+      float sk = 1.f, sv = 1.f;
+      if (lane < nb && phys < p.num_blocks) {
+        const int64_t i = (int64_t)phys * p.Hkv + it.kvh;
+        sk = __ldg(p.k_scales + i);
+        sv = __ldg(p.v_scales + i);
+      }
+      if (lane < 16) sl.scales[lane] = make_float2(sk, sv);
+      if (lane == 0) {
+        sl.it = it;
+        sl.idx = idx;
+        sl.L = L - len;
+        sl.qstart = qstart;
+        sl.n = n;
+        sl.nblk = nblk;
+        sl.at = at;
+        sl.len = len;
+        sl.done = 0;
+      }
+      mbar_arrive(&bars->islot_full[qb]);  // every lane, after its own writes
+      // item c-2's q terms are no longer read
+      if (c >= 2 && !wait_all(&bars->q_empty[qb], ((c - 2) >> 1) & 1, wc)) break;
+      uint8_t* qd = smem + Y::kQOff + qb * Y::kNQ * 128;
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        const float x[4] = {bf16_lo(raw[r].x), bf16_hi(raw[r].x), bf16_lo(raw[r].y), bf16_hi(raw[r].y)};
+        float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // the row's power of two: its largest |q| becomes 128 to 256 (E4M3 ends at 448)
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 - 7, -110), 120);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float a = x[i] * down, b = x[i + 1] * down;
+          const uint32_t t = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)t, __NV_E4M3);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          const uint32_t u = __nv_cvt_float2_to_fp8x2(make_float2(a - f.x, b - f.y), __NV_SATFINITE, __NV_E4M3);
+          hi |= (t & 0xFFFFu) << (8 * i);
+          lo |= (u & 0xFFFFu) << (8 * i);
+        }
+        // rows r and NR + r, columns 4 lane ..: 16-byte chunk lane / 4, swizzled
+        const int c1 = (lane >> 2) ^ (r & 7), c2 = (lane >> 2) ^ ((NR + r) & 7);
+        *reinterpret_cast<uint32_t*>(qd + r * 128 + (c1 << 4) + (lane & 3) * 4) = hi;
+        *reinterpret_cast<uint32_t*>(qd + (NR + r) * 128 + (c2 << 4) + (lane & 3) * 4) = lo;
+        if (lane == r) row_scales[qb * NR + r] = __uint_as_float((uint32_t)(127 + e) << 23);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->q_full[qb]);
+    }
+  } else if (warp == 1) {
+    // ================================================================ MMA issuer
+    if (lane == 0) {
+      int g = 0, it_cnt = -1;
+      int pend = -1, pend_item = 0;   // tile whose P.V is still to be issued, and its item count
+      int last_s = -1, last_pv = -1;  // the last S and P.V issued
+      const uint64_t dk0 = desc_k(smem_base);
+      const uint64_t dv0 = desc_mn(smem_base + kTileBytes);
+      const uint64_t dq0 = desc_k(smem_base + Y::kQOff);
+      const uint64_t dp0 = desc_k(smem_base + Y::kPOff);
+      bool pend_first = false, pend_last = false;
+      auto issue_pv = [&]() -> bool {
+        const int b = pend & 1, st = pend % kStages, ob = pend_item & 1;
+        if (pend_first) {
+          // O^T[ob] is about to be overwritten: the epilogue of item pend_item-2 must have read it
+          if (!mbar_wait(&bars->o_empty[ob], ((pend_item >> 1) & 1) ^ 1, wc)) return false;
+        }
+        if (!mbar_wait(&bars->p_full[b], (pend >> 1) & 1, wc)) return false;
+        if (!mbar_wait(&bars->v_full[st], (pend / kStages) & 1, wc)) return false;
+        tc_fence_after();
+        const uint64_t dv = desc_add(dv0, st * kStageBytes);
+        const uint64_t dp = desc_add(dp0, b * Y::kNP * 128);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 32; ++kk)  // 32 keys: 4 KB of V's rows, 32 bytes of the weights'
+          umma_f8(tmem + Y::kOCol + ob * Y::kNP, desc_add(dv, kk * 4096), desc_add(dp, kk * 32), Y::kIdescO,
+                  (pend_first && kk == 0) ? 0u : 1u);
+        umma_commit(&bars->pv_done[b]);
+        umma_commit(&bars->kv_empty[st]);
+        if (pend_last) umma_commit(&bars->o_full[ob]);
+        last_pv = pend;
+        pend = -1;
+        return true;
+      };
+      bool ok = true;
+      for (;; ++g) {
+        const int st = g % kStages;
+        uint64_t* const kf = &bars->k_full[st];
+        const uint32_t kph = (g / kStages) & 1;
+        if (pend >= 0) {
+          // Whichever comes first: K(g) landed (then S(g), and P.V(pend) after
+          // it, as below) or P(pend) written (then P.V(pend) now).
+          const uint64_t t0 = globaltimer();
+          for (uint32_t i = 1;; ++i) {
+            if (mbar_test_wait(kf, kph)) break;
+            if (mbar_test_wait(&bars->p_full[pend & 1], (pend >> 1) & 1)) {
+              ok = issue_pv();
+              break;
+            }
+            if ((i & 63u) == 0 && globaltimer() - t0 > wc.limit_ns) {
+              raise_error(wc.err, PKV_DEVERR_TIMEOUT);
+              ok = false;
+              break;
+            }
+          }
+          if (!ok) break;
+        }
+        if (!mbar_wait(kf, kph, wc)) {
+          ok = false;
+          break;
+        }
+        const int flags = meta[st].flags;
+        if (flags & kMetaDone) {
+          if (pend >= 0) ok = issue_pv();
+          break;
+        }
+        if (flags & kMetaFirst) {
+          ++it_cnt;
+          if (!mbar_wait(&bars->q_full[it_cnt & 1], (it_cnt >> 1) & 1, wc)) {
+            ok = false;
+            break;
+          }
+        }
+        const int b = g & 1;
+        if (!mbar_wait(&bars->s_free[b], ((g >> 1) & 1) ^ 1, wc)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t dk = desc_add(dk0, st * kStageBytes);
+        const uint64_t dq = desc_add(dq0, (it_cnt & 1) * Y::kNQ * 128);
+#pragma unroll
+        for (int kk = 0; kk < 128 / 32; ++kk)
+          umma_f8(tmem + Y::kSCol + b * Y::kNQ, desc_add(dk, kk * 32), desc_add(dq, kk * 32), Y::kIdescS, kk > 0 ? 1u : 0u);
+        umma_commit(&bars->s_full[b]);
+        if (flags & kMetaLast) umma_commit(&bars->q_empty[it_cnt & 1]);
+        last_s = g;
+        if (pend >= 0 && !issue_pv()) {
+          ok = false;
+          break;
+        }
+        pend = g;
+        pend_item = it_cnt;
+        pend_first = (flags & kMetaFirst) != 0;
+        pend_last = (flags & kMetaLast) != 0;
+      }
+      if (!ok) {
+        // leaving early: let the MMAs already issued finish before TMEM is freed
+        if (last_s >= 0) mbar_wait(&bars->s_full[last_s & 1], (last_s >> 1) & 1, wc);
+        if (last_pv >= 0) mbar_wait(&bars->pv_done[last_pv & 1], (last_pv >> 1) & 1, wc);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ================================================================ softmax / epilogue
+    constexpr int kLog = NR == 4 ? 2 : NR == 8 ? 3 : 4;
+    const int q4 = warp & 3;
+    const int t = q4 * 32 + lane;  // key of the tile (S^T lane) / output column (O^T lane)
+    const uint32_t lane_base = tmem + ((uint32_t)(q4 * 32) << 16);
+    EpSlot* slots = reinterpret_cast<EpSlot*>(smem + Y::kSlotOff);
+    if (warp < 6) {
+      // ---------------------------------------------------------- softmax
+      // Failures of waits are carried in `pending` (warp-uniform) to the next
+      // agreement barrier (barrier 1 over the 4 softmax warps, which also
+      // exchanges the row maxima), where all four warps go on or leave.
+      const int my_row = lane >> (5 - kLog);  // row this lane holds after a reduction
+      const bool row_writer = (lane & ((1 << (5 - kLog)) - 1)) == 0;
+      float m_ref[NR], lsum[NR], unit[NR];  // unit: a row's scale times the logit scale (log2 units)
+      int vis[NR], lo[NR];
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        m_ref[r] = -CUDART_INF_F;
+        lsum[r] = unit[r] = 0.f;
+        vis[r] = lo[r] = 0;
+      }
+      Meta mt{};
+      int it_cnt = -1;
+      bool pending = false;
+      for (int g = 0;; ++g) {
+        const int st = g % kStages;
+        const int b = g & 1;
+        float* redb = red + b * 4 * NR;  // [4 warps][NR], double-buffered by tile
+        bool fail = pending || !wait_all(&bars->k_full[st], (g / kStages) & 1, wc);
+        const int flags = fail ? 0 : meta[st].flags;
+        const bool done = (flags & kMetaDone) != 0;
+        uint32_t sraw[2 * NR];
+#pragma unroll
+        for (int r = 0; r < 2 * NR; ++r) sraw[r] = 0;
+        int kbase = 0;
+        Scales sc{1.f, 0.f, 1.f, 0.f};
+        if (!fail && !done) {
+          if (flags & kMetaFirst) {
+            mt = meta[st];
+            ++it_cnt;
+            fail = !wait_all(&bars->q_full[mt.qbuf], (it_cnt >> 1) & 1, wc);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+              m_ref[r] = -CUDART_INF_F;
+              lsum[r] = 0.f;
+              unit[r] = row_scales[mt.qbuf * NR + r] * p.scale_log2;
+              const int tok = (mt.row0 + r) / p.G;
+              vis[r] = r < mt.nrows ? min(mt.ke, p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
+              lo[r] = p.window > 0 ? mt.L - mt.n + tok + 1 - p.window : INT_MIN;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->q_empty[mt.qbuf]);
+          }
+          kbase = meta[st].kbase;
+          sc = tile_scales[st * 16 + t / p.bs];
+          fail = !wait_all(&bars->s_full[b], (g >> 1) & 1, wc) || fail;
+          if (!fail) {
+            tc_fence_after();
+            tmem_ld_cols<2 * NR>(lane_base + Y::kSCol + b * Y::kNQ, sraw);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&bars->s_free[b]);
+          }
+        }
+        // ---- masked logits of this thread's key, V's scale in them; row maxima over the tile
+        const int key = kbase + t;
+        float v[NR], a[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const bool seen = key < vis[r] && (key >= lo[r] || key < p.num_sink);
+          const float s = (__uint_as_float(sraw[r]) + __uint_as_float(sraw[NR + r])) * sc.k;
+          v[r] = seen ? fmaf(s, unit[r], sc.log_v) : -CUDART_INF_F;
+          a[r] = v[r];
+        }
+        const float wmax = xreduce<NR>(a, lane, MaxOp());
+        if (row_writer) redb[q4 * NR + my_row] = wmax;
+        if (barrier_any(1, 128, fail || done)) {
+          // leaving: at the end of the work (nobody failed), tell the epilogue
+          if (!barrier_any(1, 128, fail)) {
+            const int ob = (it_cnt + 1) & 1;
+            if (wait_all(&bars->ml_empty[ob], (((it_cnt + 1) >> 1) & 1) ^ 1, wc)) {
+              if (t == 0) slots[ob].done = 1;
+              mbar_arrive(&bars->ml_full[ob]);
+            }
+          }
+          break;
+        }
+        float alpha[NR], m_use[NR];
+        bool any_rescale = false;
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float mx = fmaxf(fmaxf(redb[r], redb[NR + r]), fmaxf(redb[2 * NR + r], redb[3 * NR + r]));
+          alpha[r] = 1.f;
+          if (mx > m_ref[r] + kRescaleThreshold) {  // false while both are -inf
+            alpha[r] = fast_exp2(m_ref[r] - mx);    // 0 when m_ref is -inf
+            any_rescale |= m_ref[r] != -CUDART_INF_F;
+            m_ref[r] = mx;
+          }
+          m_use[r] = (m_ref[r] == -CUDART_INF_F ? 0.f : m_ref[r]) - kWeightExp;
+        }
+        any_rescale = any_rescale && !(flags & kMetaFirst);
+
+        // ---- the weights' three terms into this tile's P buffer: row i NR + r, column t, 128-byte swizzle
+        pending = !wait_all(&bars->pv_done[b], ((g >> 1) & 1) ^ 1, wc);  // P.V of tile g-2 is done
+        uint8_t* pbuf = smem + Y::kPOff + b * Y::kNP * 128 + (t & 15);
+        const int chunk = t >> 4;
+        auto at = [&](int row) { return pbuf + row * 128 + ((chunk ^ (row & 7)) << 4); };
+#pragma unroll
+        for (int r = 0; r < NR; r += 2) {
+          const float w0 = fast_exp2(v[r] - m_use[r]), w1 = fast_exp2(v[r + 1] - m_use[r + 1]);
+          lsum[r] = fmaf(lsum[r], alpha[r], w0 * sc.inv_v);
+          lsum[r + 1] = fmaf(lsum[r + 1], alpha[r + 1], w1 * sc.inv_v);
+          const __half2 h = __floats2half2_rn(w0, w1);
+          const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&h), t0 = b0 & 0xFF00FF00u;
+          const __half2 h1 = __hsub2(h, *reinterpret_cast<const __half2*>(&t0));  // exact
+          const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&h1), t1 = b1 & 0xFF00FF00u;
+          const __half2 h2 = __hsub2(h1, *reinterpret_cast<const __half2*>(&t1));
+          const uint32_t b2 = *reinterpret_cast<const uint32_t*>(&h2) + 0x00800080u;  // to nearest
+          if (!pending) {
+            *at(r) = (uint8_t)(b0 >> 8);
+            *at(r + 1) = (uint8_t)(b0 >> 24);
+            *at(NR + r) = (uint8_t)(b1 >> 8);
+            *at(NR + r + 1) = (uint8_t)(b1 >> 24);
+            *at(2 * NR + r) = (uint8_t)(b2 >> 8);
+            *at(2 * NR + r + 1) = (uint8_t)(b2 >> 24);
+          }
+        }
+        if (any_rescale && !pending) {
+          // O^T must hold every earlier tile's P.V before it is scaled; thread t
+          // owns O^T row t (output column t), whose columns i NR + r belong to row r
+          pending = !wait_all(&bars->pv_done[b ^ 1], ((g - 1) >> 1) & 1, wc);
+          if (!pending) {
+            tc_fence_after();
+            const uint32_t ocol = lane_base + Y::kOCol + (it_cnt & 1) * Y::kNP;
+            uint32_t o[3 * NR];
+            tmem_ld_cols<3 * NR>(ocol, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int r = 0; r < 3 * NR; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * alpha[r % NR]);
+            tmem_st_cols<3 * NR>(ocol, o);
+            tmem_wait_st();
+          }
+        }
+        // a tile that holds keys before every row's window (row 0's comes first)
+        const bool early = kbase < lo[0] && kbase + kKeys > p.num_sink;
+        if ((kbase + kKeys > mt.L || early) && !pending) {
+          // keys at or past the sequence's end hold arbitrary codes, as those before
+          // the windows may: zero their V rows (after the tile has landed) so that
+          // 0 * V stays 0
+          pending = !wait_all(&bars->v_full[st], (g / kStages) & 1, wc);
+          if (!pending && (key >= mt.L || (key < lo[0] && key >= p.num_sink))) {
+            uint4* v0 = reinterpret_cast<uint4*>(smem + st * kStageBytes + kTileBytes + t * 128);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v0[c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[b]);
+
+        if (!(flags & kMetaLast)) continue;
+        // ---- item end: row sums over the 128 key-threads, handed to the epilogue
+        float* reds = red + (b ^ 1) * 4 * NR;  // the other buffer of this tile pair
+        {
+          float c[NR];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) c[r] = lsum[r];
+          const float wsum = xreduce<NR>(c, lane, AddOp());
+          if (row_writer) reds[q4 * NR + my_row] = wsum;
+        }
+        if (barrier_any(1, 128, pending)) break;
+        const int ob = it_cnt & 1;
+        pending = !wait_all(&bars->ml_empty[ob], ((it_cnt >> 1) & 1) ^ 1, wc);
+        if (!pending) {
+          EpSlot& es = slots[ob];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            if (t == r) {
+              es.m[r] = m_ref[r];
+              es.l[r] = (reds[r] + reds[NR + r]) + (reds[2 * NR + r] + reds[3 * NR + r]);
+            }
+          }
+          if (t == 0) {
+            es.mt = mt;
+            es.done = 0;
+          }
+        }
+        // reds[] is rewritten two tiles from now; the slot is complete
+        if (barrier_any(1, 128, pending)) break;
+        mbar_arrive(&bars->ml_full[ob]);
+      }
+    } else {
+      // ---------------------------------------------------------- epilogue
+      // Over the 4 epilogue warps, barrier 3: agreement after each wait that
+      // decides what they do next; barrier 2: the split tickets' ordering.
+      const int d = t;
+      int* flag_last = reinterpret_cast<int*>(tmem_slot + 1);
+      bool pending = false;
+      auto out_row = [&](int seq_q, int kvh, int row) {
+        const int tok = row / p.G, gh = row - tok * p.G;
+        return static_cast<__nv_bfloat16*>(p.out) + ((int64_t)(seq_q + tok) * p.Hq + (int64_t)kvh * p.G + gh) * 128;
+      };
+      for (int it_cnt = 0;; ++it_cnt) {
+        const int ob = it_cnt & 1;
+        const bool fail = pending || !wait_all(&bars->ml_full[ob], (it_cnt >> 1) & 1, wc);
+        if (barrier_any(3, 128, fail)) break;
+        const EpSlot& es = slots[ob];
+        if (es.done) break;
+        const Meta mt = es.mt;
+        float mrow[NR], lrow[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          mrow[r] = es.m[r];
+          lrow[r] = es.l[r];
+        }
+        mbar_arrive(&bars->ml_empty[ob]);
+        pending = !wait_all(&bars->o_full[ob], (it_cnt >> 1) & 1, wc);
+        float acc[NR];
+        if (!pending) {
+          uint32_t o[3 * NR];
+          tc_fence_after();
+          tmem_ld_cols<3 * NR>(lane_base + Y::kOCol + ob * Y::kNP, o);
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(&bars->o_empty[ob]);
+          // smallest terms first; p.v_scale undoes the weights' factor
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            acc[r] = ((__uint_as_float(o[2 * NR + r]) + __uint_as_float(o[NR + r])) + __uint_as_float(o[r])) * p.v_scale;
+        }
+        if (mt.part < 0) {
+          if (pending) continue;  // leaves at the next agreement
+#pragma unroll
+          for (int r = 0; r < NR; ++r)
+            if (r < mt.nrows) out_row(mt.qstart, mt.kvh, mt.row0 + r)[d] = __float2bfloat16_rn(acc[r] / lrow[r]);
+          continue;
+        }
+        if (!pending) {
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            if (r < mt.nrows) {
+              p.part_acc[(int64_t)(mt.part + r) * 128 + d] = acc[r];
+              if (d == r) p.part_ml[mt.part + r] = make_float2(mrow[r], lrow[r]);
+            }
+          }
+        }
+        // The split that completes its merge group combines the group's partial
+        // rows: m = max m_p, l = sum l_p 2^(m_p - m), O = sum acc_p 2^(m_p - m) / l.
+        // Release: the barrier orders every thread's partial writes before
+        // thread 0's fence and ticket; acquire: thread 0's fence after the
+        // ticket, then the barrier, before anyone reads other splits' rows.
+        if (barrier_any(3, 128, pending)) break;
+        if (d == 0) {
+          __threadfence();
+          *flag_last = atomicAdd(p.tickets + mt.grp, 1);
+        }
+        named_barrier(2, 128);
+        const MergeGroup gr = load_group(p.groups + mt.grp);
+        if (*flag_last == gr.nsplit - 1) {
+          if (d == 0) __threadfence();
+          named_barrier(2, 128);
+          for (int r = 0; r < gr.nrows; ++r) {
+            float M = -CUDART_INF_F;
+#pragma unroll 8
+            for (int k = 0; k < gr.nsplit; ++k)
+              M = fmaxf(M, __ldcg(&p.part_ml[gr.part_base + k * gr.nrows + r]).x);
+            const float Mu = M == -CUDART_INF_F ? 0.f : M;
+            float lt = 0.f, sum = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < gr.nsplit; ++k) {
+              const int slot = gr.part_base + k * gr.nrows + r;
+              const float2 ml = __ldcg(&p.part_ml[slot]);
+              const float wt = fast_exp2(ml.x - Mu);
+              lt = fmaf(wt, ml.y, lt);
+              sum = fmaf(wt, __ldcg(&p.part_acc[(int64_t)slot * 128 + d]), sum);
+            }
+            out_row(mt.qstart, gr.kvh, gr.row0 + r)[d] = __float2bfloat16_rn(sum / lt);
+          }
+        }
+        named_barrier(2, 128);  // the flag is rewritten by the next split item
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  // as in the bf16 kernel: this grid's completion implies the many-row kernel's
+  if (p.no_wait && threadIdx.x == 0) pdl_wait();
+}
+
+template <int NR>
+cudaError_t launch_t(const AttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int grid, cudaStream_t s) {
+  static unsigned long long done_mask = 0;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(dec_fp8block_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<NR>::kSmem);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  AttnParams q = p;
+  q.v_scale = 1.f / (1 << kWeightExp);
+  e = launch_pdl(dec_fp8block_kernel<NR>, dim3(grid), dim3(kThreads), Lay<NR>::kSmem, s, q, kmap, vmap);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dec_fp8block(const AttnParams& p, int unit_rows, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                int grid, cudaStream_t s) {
+  if (unit_rows == 4) return launch_t<4>(p, kmap, vmap, grid, s);
+  if (unit_rows == 8) return launch_t<8>(p, kmap, vmap, grid, s);
+  return launch_t<16>(p, kmap, vmap, grid, s);
+}
+
+}  // namespace pkv

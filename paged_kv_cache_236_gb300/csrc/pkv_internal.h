@@ -172,6 +172,8 @@ struct AttnParams {
   int64_t num_blocks;
   float scale_log2;  // scale * log2(e) (times the K scale for an FP8 cache)
   float v_scale;     // output factor: the V scale for an FP8 cache, else 1
+  const float* k_scales;  // pools with block scales: [num_blocks, Hkv]
+  const float* v_scales;
   int causal;
   int out_al32;      // out is 32-byte aligned (256-bit stores)
   int mma_unit_rows;  // rows of a full tensor-core item: floor(128 / G) * G (whole tokens)
@@ -236,6 +238,10 @@ cudaError_t launch_dectc(const AttnParams& p, int rows, const CUtensorMap& qmap,
 // fp16, fp16 MMAs; kmap / vmap are uint8 maps with {128, 1, bs, 1} boxes
 cudaError_t launch_dectc_fp8(const AttnParams& p, int rows, const CUtensorMap& qmap, const CUtensorMap& kmap,
                              const CUtensorMap& vmap, int grid, cudaStream_t s);
+
+// Pools with block scales, calls of few rows (unit_rows: rows of an item, 4, 8 or 16)
+cudaError_t launch_dec_fp8block(const AttnParams& p, int unit_rows, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                int grid, cudaStream_t s);
 
 // Sets the thread-local message pkv_last_error returns.
 void set_last_error(const char* msg);

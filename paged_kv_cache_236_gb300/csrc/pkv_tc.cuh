@@ -152,6 +152,25 @@ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// D[tmem] (+)= A[smem] * B[smem], 8-bit inputs, fp32 accumulate.  The formats are
+// the instruction descriptor's: bits 7-9 of A, 10-12 of B, 0 E4M3, 1 E5M2; the
+// rest as idesc_bf16.  One MMA takes 32 elements (32 bytes) of K.  MN-major
+// 8-bit tiles are 128 elements (one 128-byte swizzled row) wide.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+constexpr uint32_t kE4m3 = 0, kE5m2 = 1;
+constexpr uint32_t idesc_f8(int M, int N, uint32_t a_format, uint32_t b_format, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | (a_format << 7) | (b_format << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
