@@ -446,7 +446,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
 
   // tensor-core path for multi-token rows: bf16, head_dim 64 or 128, any G
   // up to 128 (an item is the floor(128 / G) whole tokens that fit 128 rows)
-  const bool mma_ok = !kv_fp8 && bf16 && G <= kMmaRows;
+  const bool mma_ok = (!kv_fp8 || blocks) && bf16 && G <= kMmaRows;
   // decode-shaped rows: tensor-core kernel (keys on M, rows on N) for bf16,
   // head_dim 128 and G dividing 16; the CUDA-core kernel otherwise
   // FP8 pools: the same kernel on fp16 MMAs over converted tiles when the
@@ -454,7 +454,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   const bool f8tc = kv_fp8 && D == 128 && (G & (G - 1)) == 0 && max_query_len > 0 &&
                     (int64_t)max_query_len * G <= 8;
   // pools with block scales: a kernel that multiplies the codes, for any G
-  const bool dectc = (mma_ok && D == 128 && (G & (G - 1)) == 0 && G <= kTcDecRows) || f8tc || blocks;
+  const bool dectc = blocks || (mma_ok && D == 128 && (G & (G - 1)) == 0 && G <= kTcDecRows) || f8tc;
   const int dec_rows_max = dectc ? kTcDecRows : kDecRows;
   // rows of softmax per key in that kernel: a power of two >= G (so items hold
   // whole tokens) covering the hinted query length; 16 when there is no hint
@@ -602,7 +602,24 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   // and the tensor-core grid starts once the planner's grid has completed
   ap.no_wait = side_by_side ? 1 : 0;
   if (g_prof_start && (e = cudaEventRecord(g_prof_start, s)) != cudaSuccess) return cuda_fail(e, "profile event");
-  if (mma_launch) {
+  CUtensorMap kmap_codes, vmap_codes;
+  if (blocks) {
+    if ((st = encode_pool_map(&kmap_codes, k_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
+        PKV_OK)
+      return st;
+    if ((st = encode_pool_map(&vmap_codes, v_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
+        PKV_OK)
+      return st;
+  }
+  if (mma_launch && blocks) {
+    CUtensorMap qmap, omap;
+    if ((st = encode_q_map(&qmap, q, T, Hq, D, 64, G, kMmaRows / G)) != PKV_OK) return st;
+    if ((st = encode_q_map(&omap, out, T, Hq, D, 64, G, kMmaRows / G)) != PKV_OK) return st;
+    ap.counter = &header->mma_counter;
+    ap.items = mma_items;
+    if ((e = launch_mma_fp8block(ap, qmap, kmap_codes, vmap_codes, omap, dev->sms, s)) != cudaSuccess)
+      return cuda_fail(e, "mma (block scales) launch");
+  } else if (mma_launch) {
     CUtensorMap qmap, kmap_sw, vmap_sw;
     if ((st = encode_q_map(&qmap, q, T, Hq, D, 64, G, kMmaRows / G)) != PKV_OK) return st;
     if ((st = encode_pool_map(&kmap_sw, k_cache, dtype, num_blocks, bs, Hkv, D, 64, CU_TENSOR_MAP_SWIZZLE_128B)) !=
@@ -624,14 +641,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   ap.counter = &header->dec_counter;
   ap.items = dec_items;
   if (blocks) {
-    CUtensorMap kmap_sw, vmap_sw;
-    if ((st = encode_pool_map(&kmap_sw, k_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
-        PKV_OK)
-      return st;
-    if ((st = encode_pool_map(&vmap_sw, v_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
-        PKV_OK)
-      return st;
-    if ((e = launch_dec_fp8block(ap, tc_rows, kmap_sw, vmap_sw, dev->sms, s)) != cudaSuccess)
+    if ((e = launch_dec_fp8block(ap, tc_rows, kmap_codes, vmap_codes, dev->sms, s)) != cudaSuccess)
       return cuda_fail(e, "decode (block scales) launch");
   } else if (dectc && kv_fp8) {
     CUtensorMap qmap16;

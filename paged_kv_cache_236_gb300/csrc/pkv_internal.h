@@ -243,6 +243,10 @@ cudaError_t launch_dectc_fp8(const AttnParams& p, int rows, const CUtensorMap& q
 cudaError_t launch_dec_fp8block(const AttnParams& p, int unit_rows, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                 int grid, cudaStream_t s);
 
+// The same, calls of many rows (q and out in boxes of whole tokens, as launch_mma)
+cudaError_t launch_mma_fp8block(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, const CUtensorMap& omap, int grid, cudaStream_t s);
+
 // Sets the thread-local message pkv_last_error returns.
 void set_last_error(const char* msg);
 
