@@ -11,18 +11,18 @@
 //   Q K^T  multiplies K's codes as they land.  A row of q is 2^e (q1 + q2), E4M3
 //          each (e from the row's largest |q|: bf16's 8 bits, down to 2^-18 of
 //          that largest value), two chains of four MMAs of K = 32 into the same
-//          accumulator: as long as eight of K = 16 in bf16.  A warp splits the
-//          Q tile in place, a thread to a row.
-//   P V    takes fp16: V's codes are converted (exactly) by two warps, which zero
+//          accumulator: as long as eight of K = 16 in bf16.  Two warps split
+//          the Q tile in place.
+//   P V    takes fp16: V's codes are converted (exactly) by four warps, which zero
 //          the rows that no row of the item sees.  The weights carry V's scale:
-//          w = 2^(x + log2 sv - m + 11), with m a running reference of x + log2 sv
-//          (raised when a tile exceeds it by 4: w <= 2^15), fp16 with 11 bits down
-//          to 2^-25 of the row's largest; the denominator takes w / (2^11 sv).
+//          w = 2^(x + log2 sv - m + 7), with m a running reference of x + log2 sv
+//          (raised when a tile exceeds it by 8: w <= 2^15), fp16 with 11 bits down
+//          to 2^-21 of the row's largest; the denominator takes w / (2^7 sv).
 //          8-bit weights would take three terms each here, where the softmax
 //          warps' instructions are what is scarce.
 // Scales are applied by runs of 8 columns (no block is shorter).
 //
-// Roles (512 threads, one CTA per SM, persistent):
+// Roles (640 threads, one CTA per SM, persistent):
 //   warp 0     the thread issuing P.V;
 //   warp 1     TMEM allocation, the thread issuing Q K^T;
 //   warp 2     K producer: {128 bytes, 1, block_size, 1} boxes (128-byte
@@ -30,15 +30,16 @@
 //              tiles' scales (the softmax warps read them up to 5 tiles after the
 //              K stage they came with is free);
 //   warp 12    V producer: codes into a staging ring;
-//   warps 3,13 V converters;
+//   warps 16-19 V converters, one to each scheduler (with two of them, on two
+//              schedulers, those were late with their softmax rows: their exponentials
+//              and conversions share a pipe: 249 us against TODO);
 //   warps 4-11 softmax / correction / epilogue, two threads per row;
 //   warp 14    item fetch, Q and output stores;
-//   warp 15    splits the Q tile.
+//   warps 3,13,15 split the Q tile.
 // Shared memory: 2 Q tiles (64 KB), 3 stages of K codes (48 KB), 2 of V codes
 // (32 KB), 2 fp16 V tiles (64 KB).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
-#include <float.h>
 #include <limits.h>
 #include <math_constants.h>
 
@@ -49,15 +50,16 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kKeys = kMmaTileKeys;                 // 128 keys per tile
 constexpr int kKStages = 3, kVStages = 2;
 constexpr int kCodeTile = kKeys * 128;              // K or V codes of a tile (16 KB)
 constexpr int kHalfKV = kKeys * 128;                // one 64-column half of an fp16 V tile (16 KB)
 constexpr int kTileBytes = 2 * kHalfKV;             // an fp16 V tile: 32 KB
 constexpr int kScaleSlots = 8;
-constexpr int kConverters = 64;                     // threads
-constexpr int kWeightExp = 11;                      // weights are 2^11 times their value, at most 2^15
+constexpr int kConverters = 128;                    // threads
+constexpr int kSplitters = 96;                      // threads
+constexpr int kWeightExp = 7;                       // weights are 2^7 times their value, at most 2^15
 constexpr int kQBytes = kMmaRows * 128 * 2;         // 32 KB (two 16 KB halves)
 // shared-memory carve-up (offsets from a 1024-byte aligned base)
 constexpr int kQOff = 0;
@@ -78,13 +80,13 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 0;    // S buffer b at kSCol + 128 b
 constexpr uint32_t kPCol = 256;  // P buffer b at kPCol + 64 b
 constexpr uint32_t kOCol = 384;
-constexpr float kRescaleThreshold = 4.0f;  // log2 units
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
 // Register split between warpgroups (setmaxnreg): warpgroups 0 and 3 (MMA
 // issuers, producers, item fetch) give up registers that warpgroups 1 and 2
 // (softmax) take.  The sum must stay within what the block is launched with
 // (kThreads x the kernel's register count); the launcher checks the count.
-constexpr int kRegsLight = 64, kRegsSoftmax = 184;
-static_assert(2 * 128 * (kRegsLight + kRegsSoftmax) <= kThreads * 128, "register split above 128 per thread");
+constexpr int kRegs = 96, kRegsLight = 56, kRegsSoftmax = 152;
+static_assert(3 * 128 * kRegsLight + 2 * 128 * kRegsSoftmax <= kThreads * kRegs, "register split above the launch's");
 
 constexpr uint32_t kIdescS = idesc_f8(128, kKeys, kE4m3, kE4m3, false, false);
 // fp16 A and B: idesc_bf16 with the format fields 0
@@ -121,10 +123,10 @@ struct alignas(16) ItemSlot {
   float2 scales[16];
 };
 // readers of a slot: the 256 softmax threads, the two MMA-issuing threads, the
-// K / V producers, the converters' two warps, the splitting warp
-constexpr int kSlotReaders = 256 + 2 + 2 + 2 + 1;
+// K / V producers, the four converting and three splitting warps
+constexpr int kSlotReaders = 256 + 2 + 2 + 4 + 3;
 
-// What a tile's block has of scales: K's, log2 of V's, 2^-11 / V's.
+// What a tile's block has of scales: K's, log2 of V's, 2^-7 / V's.
 struct alignas(16) Scales {
   float k, log_v, inv_v, pad;
 };
@@ -158,56 +160,45 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One row of the Q tile in place: 128 bf16 in two 64-column halves kHalf apart
-// (16-byte chunk j at j ^ (r & 7) of the row) become 128 codes of q1 in the first
-// and of q2 in the second, swizzled alike.  Returns the row's scale 2^e.
-// Codes of columns 16 m .. are chunk m: of the first half, what they overwrite
-// (columns 8 m ..) is read by then; of the second, they wait until it is.
-__device__ __forceinline__ float split_row(uint8_t* row, int r) {
-  const int x = r & 7;
-  auto chunk = [&](int half, int j) { return reinterpret_cast<uint4*>(row + half * kHalf + ((j ^ x) << 4)); };
-  uint32_t top = 0;  // of |q|'s bf16 bits, two at a time
+// Rows row0 .. row1 - 1 (a multiple of 4) of a Q tile in place, by a warp, a row at a time (four
+// on their way): 128 bf16 in two 64-column halves kHalf apart (16-byte chunk j at
+// j ^ (r & 7) of the row) become 128 codes of q1 in the first and of q2 in the
+// second, swizzled alike.  scales[r]: 2^e.
+__device__ __forceinline__ void split_rows(uint8_t* tile, int row0, int row1, float* scales, int lane) {
+  // this lane's columns 4 lane .. + 3: 8 bytes of bf16, 4 codes
+  const int from = (lane >> 4) * kHalf + (lane & 1) * 8, fc = (lane & 15) >> 1;
+  const int to = (lane & 3) * 4, tc = lane >> 2;
+#pragma unroll 1
+  for (int r0 = row0; r0 < row1; r0 += 4) {
+    uint2 raw[4];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint4 w = *chunk(j >> 3, j & 7);
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < 4; ++i)
+      raw[i] = *reinterpret_cast<const uint2*>(tile + (r0 + i) * 128 + from + ((fc ^ ((r0 + i) & 7)) << 4));
+    __syncwarp();  // all of the rows is read before any of it is written
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, in[i] & 0x7FFF7FFFu);
-  }
-  const int biggest = max((int)(top & 0xFFFFu), (int)(top >> 16));
-  // the largest |q| becomes 128 to 256 (E4M3 ends at 448)
-  const int e = min(max((biggest >> 7) - 127 - 7, -50), 120);
-  const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-  uint4 late[8];
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t top2 = __vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu);
+      const int top = (int)__reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
+      // the largest |q| becomes 128 to 256 (E4M3 ends at 448)
+      const int e = min(max((top >> 7) - 127 - 7, -50), 120);
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      const float a[4] = {bf16_lo(raw[i].x) * down, bf16_hi(raw[i].x) * down, bf16_lo(raw[i].y) * down,
+                          bf16_hi(raw[i].y) * down};
+      uint32_t h[2], l[2];
 #pragma unroll
-  for (int m = 0; m < 8; ++m) {
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const uint4 w = *chunk(m >> 2, (2 * m + c) & 7);
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = bf16_lo(in[i]) * down, b = bf16_hi(in[i]) * down;
-        h[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
-        const uint32_t back = e4m3x2_to_f16x2(h[i]);
+      for (int k = 0; k < 2; ++k) {
+        h[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a[2 * k], a[2 * k + 1]), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
+        const uint32_t back = e4m3x2_to_f16x2(h[k]);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        l[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a - f.x, b - f.y), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
+        l[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a[2 * k] - f.x, a[2 * k + 1] - f.y), __NV_SATFINITE,
+                                                  __NV_E4M3) & 0xFFFFu;
       }
-      hi[2 * c] = h[0] | h[1] << 16;
-      hi[2 * c + 1] = h[2] | h[3] << 16;
-      lo[2 * c] = l[0] | l[1] << 16;
-      lo[2 * c + 1] = l[2] | l[3] << 16;
-    }
-    *chunk(0, m) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    late[m] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (m == 5 || m == 7) {  // the second half's first four chunks are read by then, or all
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *chunk(1, (m == 5 ? 0 : 4) + i) = late[(m == 5 ? 0 : 4) + i];
+      uint8_t* dst = tile + (r0 + i) * 128 + to + ((tc ^ ((r0 + i) & 7)) << 4);
+      *reinterpret_cast<uint32_t*>(dst) = h[0] | h[1] << 16;
+      *reinterpret_cast<uint32_t*>(dst + kHalf) = l[0] | l[1] << 16;
+      if (lane == i) scales[r0 + i] = __uint_as_float((uint32_t)(127 + e) << 23);
     }
   }
-  return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
 // N bf16 (2N bytes) of an output row, packed in pairs in w: 32-byte stores
@@ -240,14 +231,14 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + kNumBars * 8);
   ItemSlot* slots = reinterpret_cast<ItemSlot*>(smem + kSlotOff);
   float* row_scales = reinterpret_cast<float*>(smem + kRowScaleOff);      // [2][128]
-  Scales* tile_scales = reinterpret_cast<Scales*>(smem + kScaleOff);      // [kScaleSlots][16]
+  Scales* tile_scales = reinterpret_cast<Scales*>(smem + kScaleOff);      // [kScaleSlots][16 runs of 8 keys]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{p.err, wait_limit(p.wait_ns)};
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->q_full[b], 1);
-      mbar_init(&bars->q_split[b], 32);
+      mbar_init(&bars->q_split[b], kSplitters);
       mbar_init(&bars->q_empty[b], 1);
       mbar_init(&bars->slot_full[b], 32);
       mbar_init(&bars->slot_free[b], kSlotReaders);
@@ -426,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
       const bool is_v = warp == 12;
       const CUtensorMap* map = is_v ? &vmap : &kmap;
       if (lane == 0) prefetch_tensormap(map);
+      const int run_block = (lane & 15) * 8 / p.bs;  // block of the tile's run of 8 keys that this lane writes the scales of
       const int nst = is_v ? kVStages : kKStages;
       uint8_t* const ring = smem + (is_v ? kCOff : kKOff);
       uint64_t* const fullb = is_v ? bars->c_full : bars->k_full;
@@ -464,7 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           }
           if (!is_v) {
             // the slot's last reader was tile g-8's softmax: Q K^T(g-3) was issued after S(g-5) was read
-            if (lane < nb) tile_scales[(g & (kScaleSlots - 1)) * 16 + lane] = make_scales(sc);
+            const float2 mine = make_float2(__shfl_sync(0xffffffffu, sc.x, run_block), __shfl_sync(0xffffffffu, sc.y, run_block));
+            if (lane < 16) tile_scales[(g & (kScaleSlots - 1)) * 16 + lane] = make_scales(mine);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->sc_full[g & (kScaleSlots - 1)]);
           }
@@ -481,12 +474,18 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
       if (!ok) {  // leaving early: the copies of the tiles issued last land first
         for (int j = max(0, g - nst); j < g; ++j) __all_sync(0xffffffffu, mbar_wait(&fullb[j % nst], (j / nst) & 1, wc));
       }
-    } else if (warp == 3 || warp == 13) {
+    } else if (warp >= 16) {
       // ================================================================ V converters
       // Codes (rows of 128 bytes, chunk j at j ^ (key & 7)) become an fp16 tile of
       // two 64-column halves, swizzled alike; rows past the sequence's end, and
       // those before every row's window, become zeros whatever they hold.
-      const int t = (warp == 3 ? 0 : 32) + lane;
+      // A thread takes one chunk of every sixteenth key, so that its places within a
+      // tile are 2048 bytes apart.
+      const int t = (warp - 16) * 32 + lane;
+      const int ch = t & 7, x = (t >> 3) & 7, row = (t >> 3) * 128;
+      const int from = row + ((ch ^ x) << 4);
+      const int to = (ch >> 2) * kHalfKV + row;
+      const int to0 = to + (((2 * (ch & 3)) ^ x) << 4), to1 = to + (((2 * (ch & 3) + 1) ^ x) << 4);
       int g = 0;
       bool ok = true;
       for (int c = 0; ok; ++c) {
@@ -507,32 +506,42 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
             ok = false;
             break;
           }
-          const uint8_t* src = smem + kCOff + st * kCodeTile;
+          const uint8_t* src = smem + kCOff + st * kCodeTile + from;
           uint8_t* dst = smem + kVOff + st * kTileBytes;
-#pragma unroll 2
-          for (int u = t; u < kKeys * 8; u += kConverters) {
-            const int key = u >> 3, ch = u & 7, x = key & 7, k = kbase + key;
-            uint4 raw = *reinterpret_cast<const uint4*>(src + key * 128 + ((ch ^ x) << 4));
-            if (k >= L || (k < lo && k >= p.num_sink)) raw = make_uint4(0, 0, 0, 0);
-            const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-            uint32_t w[8];
+          const bool masked = kbase + kKeys > L || (kbase < lo && kbase + kKeys > p.num_sink);
+#pragma unroll 1
+          for (int i0 = 0; i0 < kKeys / 16; i0 += 4) {  // keys t / 8 + 16 i
+            uint4 raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 2048);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int k = kbase + (t >> 3) + 16 * (i0 + i);
+                if (k >= L || (k < lo && k >= p.num_sink)) raw[i] = make_uint4(0, 0, 0, 0);
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              w[2 * i] = e4m3x2_to_f16x2(in[i] & 0xFFFFu);
-              w[2 * i + 1] = e4m3x2_to_f16x2(in[i] >> 16);
+              const uint32_t in[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                w[2 * e] = e4m3x2_to_f16x2(in[e] & 0xFFFFu);
+                w[2 * e + 1] = e4m3x2_to_f16x2(in[e] >> 16);
+              }
+              *reinterpret_cast<uint4*>(dst + to0 + (i0 + i) * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(dst + to1 + (i0 + i) * 2048) = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            uint8_t* row = dst + (ch >> 2) * kHalfKV + key * 128;
-            const int j = (ch & 3) * 2;
-            *reinterpret_cast<uint4*>(row + ((j ^ x) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(row + (((j + 1) ^ x) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
           }
           fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
           mbar_arrive(&bars->v_full[st]);
           mbar_arrive(&bars->c_empty[st]);
         }
       }
-    } else if (warp == 15) {
+    } else if (warp == 3 || warp == 13 || warp == 15) {
       // ================================================================ Q split
+      const int part = warp == 3 ? 0 : warp == 13 ? 1 : 2;
       for (int c = 0;; ++c) {
         const int qb = c & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->slot_full[qb], (c >> 1) & 1, wc))) break;
@@ -541,9 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
         if (lane == 0) mbar_arrive(&bars->slot_free[qb]);
         if (done) break;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_full[qb], (c >> 1) & 1, wc))) break;
-        for (int r = lane; r < kMmaRows; r += 32)
-          row_scales[qb * kMmaRows + r] = split_row(smem + kQOff + qb * kQBytes + r * 128, r);
-        fence_proxy_async_smem();
+        // rows 44 part .. (40 for the last)
+        split_rows(smem + kQOff + qb * kQBytes, 44 * part, min(44 * part + 44, kMmaRows), row_scales + qb * kMmaRows, lane);
+        fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
         mbar_arrive(&bars->q_split[qb]);
       }
     } else if (warp == 1) {
@@ -671,7 +680,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
       const int tok = row / p.G, gh = row - tok * p.G;
       const int vis = valid ? min(it.ke, p.causal ? L - n + tok + 1 : L) : 0;
       if (barrier_any(6, 256, !__all_sync(0xffffffffu, mbar_wait(&bars->q_split[qb], (c >> 1) & 1, wc)))) break;
-      const float unit = row_scales[qb * kMmaRows + r] * p.scale_log2;  // of this row's accumulator, in log2 units
+      // of this row's accumulator, in log2 units; times the least K scale still a normal number
+      const float unit = fmaxf(row_scales[qb * kMmaRows + r] * p.scale_log2, 0x1p-66f);
       float m_ref = -CUDART_INF_F, l = 0.f;
       int owe = -1;  // after a failed wait: the pair barriers of the item not yet taken
       const int ntiles = (it.ke - it.kb + kKeys - 1) / kKeys;
@@ -715,8 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           owe = ntiles - j + 2;
           break;
         }
-        const Scales* scales = tile_scales + (g & (kScaleSlots - 1)) * 16;
-        auto scales_of = [&](int run) { return scales[(64 * h + 8 * run) / p.bs]; };  // of columns 8 run .. of this half
+        const Scales* scales = tile_scales + (g & (kScaleSlots - 1)) * 16 + 8 * h;
+        auto scales_of = [&](int run) { return scales[run]; };  // of columns 8 run .. of this half
         // this half's max of x + log2 sv: factors are positive, so of each run the largest S
         float mloc = -CUDART_INF_F;
 #pragma unroll
@@ -724,11 +734,11 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           const Scales sc = scales_of(run);
           auto at = [&](int i) { return __uint_as_float(sraw[8 * run + i]); };
           const float top = fmax3(fmax3(at(0), at(1), at(2)), fmax3(at(3), at(4), at(5)), fmaxf(at(6), at(7)));
-          mloc = fmaxf(mloc, fmaf(top, fmaxf(unit * sc.k, FLT_MIN), sc.log_v));
+          mloc = fmaxf(mloc, fmaf(top, unit * sc.k, sc.log_v));
         }
         float* redm = red + sb * 256;
         redm[h * 128 + r] = mloc;
-        // P of keys 64h .. 64h+63: 2^(x + log2 sv - m + 11), fp16 pairs (TMEM
+        // P of keys 64h .. 64h+63: 2^(x + log2 sv - m + 7), fp16 pairs (TMEM
         // columns 32h .. 32h+31 of P buffer sb); ps the sum of 2^(x - m)
         float ps = 0.f;
         auto exps = [&](float m) {
@@ -741,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
             for (int half = 0; half < 2; ++half) {
               const int run = 2 * grp + half;
               const Scales sc = scales_of(run);
-              const float u = fmaxf(unit * sc.k, FLT_MIN), b = nm + sc.log_v;
+              const float u = unit * sc.k, b = nm + sc.log_v;
               const f32x2 u2 = pk2(u, u), b2 = pk2(b, b);
               f32x2 sum = pk2(0.f, 0.f);
 #pragma unroll
@@ -760,35 +770,29 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
         };
         float alpha = 1.f;
         bool rescale = false;
-        if (j == 0) {
-          // first tile of the item: the row max first, then the exponentials
+        // The row max, exchanged between the row's pair; true if this row's reference rises
+        auto raise = [&]() {
           named_barrier(pair_bar, 64);
           const float mx = fmaxf(mloc, redm[(h ^ 1) * 128 + r]);
-          if (mx > m_ref + kRescaleThreshold) {  // false while both are -inf
-            alpha = fast_exp2(m_ref - mx);       // 0: m_ref is -inf here
-            m_ref = mx;
-          }
-          exps(m_ref);
-        } else {
-          // The reference max of the earlier tiles is known, so the
-          // exponentials go ahead of the pair's max exchange; they are redone
-          // in the rare case that the row max exceeds the reference by more
-          // than the threshold (or the row had no visible key before).
-          exps(m_ref);
-          named_barrier(pair_bar, 64);
-          const float mx = fmaxf(mloc, redm[(h ^ 1) * 128 + r]);
-          const bool raise = mx > m_ref + kRescaleThreshold;
-          if (raise) {
+          const bool up = mx > m_ref + kRescaleThreshold;  // false while both are -inf
+          if (up) {
             alpha = fast_exp2(m_ref - mx);  // 0 when m_ref is -inf
             rescale = m_ref != -CUDART_INF_F;
             m_ref = mx;
           }
-          // for one row or more: by the whole warp, as TMEM stores must be (the
-          // other rows write what they wrote)
-          if (__any_sync(0xffffffffu, raise)) {
-            tmem_wait_st();  // the first pass's P pieces land before they are rewritten
-            exps(m_ref);
-          }
+          return up;
+        };
+        // First tile of an item: the row max, then the exponentials.  Later ones:
+        // the reference is known, so the exponentials go ahead of the exchange and
+        // are redone in the rare case that it rises for a row of the warp (TMEM
+        // stores are the whole warp's).  One copy of their code: with three, the
+        // roles' code no longer fitted the instruction cache.
+        if (j == 0) raise();
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+          exps(m_ref);
+          if (j == 0 || pass == 1 || !__any_sync(0xffffffffu, raise())) break;
+          tmem_wait_st();  // the first pass's P pieces land before they are rewritten
         }
         l = fmaf(l, alpha, ps);
         if (__any_sync(0xffffffffu, rescale)) {
@@ -948,11 +952,11 @@ cudaError_t launch_mma_fp8block(const AttnParams& p, const CUtensorMap& qmap, co
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
-    // the register split needs the block launched with 128 registers per thread
+    // the register split needs the block launched with kRegs registers per thread
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, mma_fp8block_kernel);
     if (e != cudaSuccess) return e;
-    if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
+    if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(mma_fp8block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
