@@ -215,6 +215,9 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* w,
   }
 }
 
+// kRun: columns that surely share a block's scales, 8 or 16 (fewer loads and
+// factors: 3 % of a verify batch).
+template <int kRun>
 __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnParams p,
                                                                    const __grid_constant__ CUtensorMap qmap,
                                                                    const __grid_constant__ CUtensorMap kmap,
@@ -678,122 +681,126 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
       const bool valid = r < it.nrows;
       const int row = it.row0 + r;
       const int tok = row / p.G, gh = row - tok * p.G;
-      const int vis = valid ? min(it.ke, p.causal ? L - n + tok + 1 : L) : 0;
+      // rows past the item's are left as they come: their logits are 0 (or NaN), in no other row's way
+      const int vis = valid ? min(it.ke, p.causal ? L - n + tok + 1 : L) : INT_MAX;
+      const bool idle = q4 * 32 >= it.nrows;  // none of the warp's rows is the item's
       if (barrier_any(6, 256, !__all_sync(0xffffffffu, mbar_wait(&bars->q_split[qb], (c >> 1) & 1, wc)))) break;
       // of this row's accumulator, in log2 units; times the least K scale still a normal number
-      const float unit = fmaxf(row_scales[qb * kMmaRows + r] * p.scale_log2, 0x1p-66f);
+      const float unit = valid ? fmaxf(row_scales[qb * kMmaRows + r] * p.scale_log2, 0x1p-66f) : 0.f;
       float m_ref = -CUDART_INF_F, l = 0.f;
       int owe = -1;  // after a failed wait: the pair barriers of the item not yet taken
       const int ntiles = (it.ke - it.kb + kKeys - 1) / kKeys;
       for (int j = 0; j < ntiles; ++j, ++g) {
         const int sb = g & 1;
         const int kt = it.kb + j * kKeys;  // first key of the tile
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (g >> 1) & 1, wc))) {
-          owe = ntiles - j + 2;
+        const uint32_t s_half = lane_base + kSCol + 128 * sb + 64 * h, p_half = lane_base + kPCol + 64 * sb + 32 * h;
+        // S(g), and the P buffer free: the P.V of tile g-2, which read it, done
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (g >> 1) & 1, wc) &&
+                                         mbar_wait(&bars->pv_done[sb], ((g >> 1) & 1) ^ 1, wc) &&
+                                         mbar_wait(&bars->sc_full[g & (kScaleSlots - 1)], (g / kScaleSlots) & 1, wc))) {
+          owe = (idle ? 0 : ntiles - j) + 2;
           break;
+        }
+        if (idle) {  // nothing to do but keep the tiles' pace (its partner is as idle: they meet at the item's end)
+          mbar_arrive(&bars->s_free[sb]);
+          mbar_arrive(&bars->p_full[sb]);
+          continue;
         }
         tc_fence_after();
-        uint32_t sraw[64];
-        tmem_ld32(lane_base + kSCol + 128 * sb + 64 * h, sraw);
-        tmem_ld32(lane_base + kSCol + 128 * sb + 64 * h + 32, sraw + 32);
-        tmem_wait_ld();
-        tc_fence_before();
-        mbar_arrive(&bars->s_free[sb]);  // S buffer sb may take S(g+2)
-        // P buffer sb is free once the P.V of tile g-2, which read it, is done;
-        // the exponentials below write P to it in 8-column pieces
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->pv_done[sb], ((g >> 1) & 1) ^ 1, wc))) {
-          owe = ntiles - j + 2;
-          break;
-        }
-        const int nvis = vis - (kt + 64 * h);  // keys c < nvis of this half are visible
-        if (nvis < 64) {
-#pragma unroll
-          for (int cc = 0; cc < 64; ++cc)
-            if (cc >= nvis) sraw[cc] = __float_as_uint(-CUDART_INF_F);
-        }
-        if (p.window > 0) {
-          // keys nsink <= c < nlo of this half lie before the row's window
-          const int nlo = L - n + tok + 1 - p.window - (kt + 64 * h), nsink = p.num_sink - (kt + 64 * h);
-          if (__any_sync(0xffffffffu, nlo > 0) && nsink < 64) {
-#pragma unroll
-            for (int cc = 0; cc < 64; ++cc)
-              if (cc < nlo && cc >= nsink) sraw[cc] = __float_as_uint(-CUDART_INF_F);
-          }
-        }
-        // the tile's scales
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->sc_full[g & (kScaleSlots - 1)], (g / kScaleSlots) & 1, wc))) {
-          owe = ntiles - j + 2;
-          break;
+        // The keys of this half that the row sees, as bits: c < nvis and, with a
+        // window, not nsink <= c < nlo.
+        const int nvis = vis - (kt + 64 * h);
+        const int nlo = p.window > 0 && valid ? L - n + tok + 1 - p.window - (kt + 64 * h) : 0;
+        uint64_t seen = ~0ull;
+        const bool masked = __any_sync(0xffffffffu, nvis < 64 || nlo > 0);
+        if (masked) {
+          auto below = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1; };  // bits c < k
+          seen = below(nvis) & (below(p.num_sink - (kt + 64 * h)) | ~below(nlo));
         }
         const Scales* scales = tile_scales + (g & (kScaleSlots - 1)) * 16 + 8 * h;
-        auto scales_of = [&](int run) { return scales[run]; };  // of columns 8 run .. of this half
+        // Sixteen columns of S at a time, in loops, the next sixteen on their way: a
+        // row's 64 in registers, with the code unrolled over them, were 1200
+        // instructions a tile for each of three copies, and the instruction cache,
+        // which the other roles' code shares, set the pace.
+        auto columns = [&](int run, uint32_t (&z)[16]) {  // masked: columns 8 run .. + 15
+          if (masked) {
+            const uint32_t m = (uint32_t)(seen >> (8 * run));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!((m >> i) & 1)) z[i] = __float_as_uint(-CUDART_INF_F);
+          }
+        };
         // this half's max of x + log2 sv: factors are positive, so of each run the largest S
         float mloc = -CUDART_INF_F;
-#pragma unroll
-        for (int run = 0; run < 8; ++run) {
-          const Scales sc = scales_of(run);
-          auto at = [&](int i) { return __uint_as_float(sraw[8 * run + i]); };
-          const float top = fmax3(fmax3(at(0), at(1), at(2)), fmax3(at(3), at(4), at(5)), fmaxf(at(6), at(7)));
-          mloc = fmaxf(mloc, fmaf(top, unit * sc.k, sc.log_v));
-        }
-        float* redm = red + sb * 256;
-        redm[h * 128 + r] = mloc;
+        auto max_of = [&](int run, uint32_t (&z)[16]) {
+          columns(run, z);
+          auto at = [&](int i) { return __uint_as_float(z[i]); };
+          float t0 = fmax3(fmax3(at(0), at(1), at(2)), fmax3(at(3), at(4), at(5)), fmaxf(at(6), at(7)));
+          float t1 = fmax3(fmax3(at(8), at(9), at(10)), fmax3(at(11), at(12), at(13)), fmaxf(at(14), at(15)));
+          const Scales sc = scales[run];
+          if constexpr (kRun == 8) {
+            const Scales sd = scales[run + 1];
+            mloc = fmax3(mloc, fmaf(t0, unit * sc.k, sc.log_v), fmaf(t1, unit * sd.k, sd.log_v));
+          } else {
+            mloc = fmaxf(mloc, fmaf(fmaxf(t0, t1), unit * sc.k, sc.log_v));
+          }
+        };
         // P of keys 64h .. 64h+63: 2^(x + log2 sv - m + 7), fp16 pairs (TMEM
         // columns 32h .. 32h+31 of P buffer sb); ps the sum of 2^(x - m)
-        float ps = 0.f;
-        auto exps = [&](float m) {
-          const float nm = (m == -CUDART_INF_F ? 0.f : -m) + kWeightExp;
-          ps = 0.f;
+        float ps = 0.f, nm = 0.f;
+        auto exps_of = [&](int run, uint32_t (&z)[16]) {
+          columns(run, z);
+          uint32_t pk[8];
 #pragma unroll
-          for (int grp = 0; grp < 4; ++grp) {
-            uint32_t pk[8];
+          for (int half = 0; half < 16 / kRun; ++half) {
+            const Scales sc = scales[run + half];
+            const float u = unit * sc.k, b = nm + sc.log_v;
+            const f32x2 u2 = pk2(u, u), b2 = pk2(b, b);
+            f32x2 sum = pk2(0.f, 0.f);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int run = 2 * grp + half;
-              const Scales sc = scales_of(run);
-              const float u = unit * sc.k, b = nm + sc.log_v;
-              const f32x2 u2 = pk2(u, u), b2 = pk2(b, b);
-              f32x2 sum = pk2(0.f, 0.f);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int cc = 4 * run + i;
-                const float2 x = up2(fma2(pk2(__uint_as_float(sraw[2 * cc]), __uint_as_float(sraw[2 * cc + 1])), u2, b2));
-                const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
-                sum = add2(sum, pk2(e0, e1));
-                pk[4 * half + i] = pack_half(e0, e1);
-              }
-              const float2 s2 = up2(sum);
-              ps = fmaf(s2.x + s2.y, sc.inv_v, ps);
+            for (int i = 4 * half; i < 4 * half + kRun / 2; ++i) {
+              const float2 x = up2(fma2(pk2(__uint_as_float(z[2 * i]), __uint_as_float(z[2 * i + 1])), u2, b2));
+              const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
+              sum = add2(sum, pk2(e0, e1));
+              pk[i] = pack_half(e0, e1);
             }
-            tmem_st8(lane_base + kPCol + 64 * sb + 32 * h + 8 * grp, pk);
+            const float2 s2 = up2(sum);
+            ps = fmaf(s2.x + s2.y, sc.inv_v, ps);
+          }
+          tmem_st8(p_half + 4 * run, pk);
+        };
+        auto each = [&](auto&& use) {  // use(run, columns 8 run .. + 15 of this half's S)
+          uint32_t a[16], b[16];
+          tmem_ld16(s_half, a);
+          tmem_wait_ld();
+#pragma unroll 1
+          for (int run = 0; run < 8; run += 4) {
+            tmem_ld16(s_half + 8 * run + 16, b);
+            use(run, a);
+            tmem_wait_ld();
+            tmem_ld16(s_half + ((8 * run + 32) & 63), a);  // (the last time: the first again)
+            use(run + 2, b);
+            tmem_wait_ld();
           }
         };
+        each(max_of);
+        float* redm = red + sb * 256;
+        redm[h * 128 + r] = mloc;
+        named_barrier(pair_bar, 64);
+        // the running reference rises where the row's max exceeds it by the threshold
+        const float mx = fmaxf(mloc, redm[(h ^ 1) * 128 + r]);
         float alpha = 1.f;
         bool rescale = false;
-        // The row max, exchanged between the row's pair; true if this row's reference rises
-        auto raise = [&]() {
-          named_barrier(pair_bar, 64);
-          const float mx = fmaxf(mloc, redm[(h ^ 1) * 128 + r]);
-          const bool up = mx > m_ref + kRescaleThreshold;  // false while both are -inf
-          if (up) {
-            alpha = fast_exp2(m_ref - mx);  // 0 when m_ref is -inf
-            rescale = m_ref != -CUDART_INF_F;
-            m_ref = mx;
-          }
-          return up;
-        };
-        // First tile of an item: the row max, then the exponentials.  Later ones:
-        // the reference is known, so the exponentials go ahead of the exchange and
-        // are redone in the rare case that it rises for a row of the warp (TMEM
-        // stores are the whole warp's).  One copy of their code: with three, the
-        // roles' code no longer fitted the instruction cache.
-        if (j == 0) raise();
-#pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-          exps(m_ref);
-          if (j == 0 || pass == 1 || !__any_sync(0xffffffffu, raise())) break;
-          tmem_wait_st();  // the first pass's P pieces land before they are rewritten
+        if (mx > m_ref + kRescaleThreshold) {  // false while both are -inf
+          alpha = fast_exp2(m_ref - mx);       // 0 when m_ref is -inf
+          rescale = m_ref != -CUDART_INF_F;
+          m_ref = mx;
         }
+        nm = (m_ref == -CUDART_INF_F ? 0.f : -m_ref) + kWeightExp;
+        __syncwarp();
+        each(exps_of);
+        tc_fence_before();
+        mbar_arrive(&bars->s_free[sb]);  // S buffer sb may take S(g+2)
         l = fmaf(l, alpha, ps);
         if (__any_sync(0xffffffffu, rescale)) {
           // O must hold every earlier tile's P.V before it is scaled; the TMEM
@@ -805,21 +812,21 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           }
           tc_fence_after();
           const float f = rescale ? alpha : 1.f;
-#pragma unroll
-          for (int cc = 0; cc < kOC / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld32(lane_base + kOCol + kOC * h + cc * 32, o);
+#pragma unroll 1
+          for (int cc = 0; cc < kOC; cc += 16) {
+            uint32_t o[16];
+            tmem_ld16(lane_base + kOCol + kOC * h + cc, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
-            tmem_st32(lane_base + kOCol + kOC * h + cc * 32, o);
+            for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
+            tmem_st16(lane_base + kOCol + kOC * h + cc, o);
           }
         }
         tmem_wait_st();  // P (and a rescaled O) written
         tc_fence_before();
         mbar_arrive(&bars->p_full[sb]);
       }
-      // ---- epilogue: row sum of the pair, O (this thread's D / 2 output columns) / l.
+      // ---- epilogue: row sum of the pair, O (this thread's 64 output columns) / l.
       // The sums go through the max buffer the last tile did not use; the
       // second pair barrier keeps the next tile from overwriting them early.
       float ltot = 0.f;
@@ -835,48 +842,45 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
       for (int k = 0; k < owe; ++k) named_barrier(pair_bar, 64);
       if (barrier_any(6, 256, owe >= 0)) break;
       tc_fence_after();
-      uint32_t o[kOC];
-#pragma unroll
-      for (int cc = 0; cc < kOC / 32; ++cc) tmem_ld32(lane_base + kOCol + kOC * h + 32 * cc, o + 32 * cc);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(&bars->o_empty);
       // a full tile of whole tokens leaves through TMA stores from Q buffer qb
       // (its Q K^T are complete), in the Q tile's layout: row r, 16-byte
       // chunk j at chunk j ^ (r & 7) of the row (128-byte swizzle); this
-      // thread's columns kOC * h .. are chunks (kOC * h % 64) / 8 .. of half
-      // kOC * h / 64
+      // thread's columns are half h
       const bool staged = it.nrows == p.mma_unit_rows && it.part < 0;
-      if (valid) {
-        if (it.part < 0) {
-          const float inv = (1.f / (1 << kWeightExp)) / ltot;
-          uint32_t w[kOC / 2];
+      // a partial row keeps 2^-7 of its accumulator, a finished one its share of the row's sum
+      const float inv = (1.f / (1 << kWeightExp)) / (it.part < 0 ? ltot : 1.f);
+      __nv_bfloat16* orow = static_cast<__nv_bfloat16*>(p.out) +
+                            ((int64_t)(qstart + tok) * p.Hq + (int64_t)it.kvh * p.G + gh) * D + kOC * h;
+      float* prow = p.part_acc + (int64_t)(it.part + r) * D + kOC * h;  // (the workspace is 256-byte aligned)
+      uint8_t* srow = smem + kQOff + qb * kQBytes + h * kHalf + r * 128;
+#pragma unroll 1
+      for (int cc = 0; cc < kOC; cc += 16) {
+        uint32_t o[16];
+        __syncwarp();  // (the rows part below; TMEM loads are the whole warp's)
+        tmem_ld16(lane_base + kOCol + kOC * h + cc, o);
+        tmem_wait_ld();
+        if (!valid) continue;
 #pragma unroll
-          for (int u = 0; u < kOC / 2; ++u)
-            w[u] = pack_bf16(__uint_as_float(o[2 * u]) * inv, __uint_as_float(o[2 * u + 1]) * inv);
-          if (staged) {
-            uint8_t* srow = smem + kQOff + qb * kQBytes + (kOC * h / 64) * kHalf + r * 128;
+        for (int t = 0; t < 16; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * inv);
+        if (it.part >= 0) {
+          st_global_v8(prow + cc, o);
+          st_global_v8(prow + cc + 8, o + 8);
+          continue;
+        }
+        uint32_t w[8];
 #pragma unroll
-            for (int jj = 0; jj < kOC / 8; ++jj) {
-              const int j = ((kOC * h) % 64) / 8 + jj;
-              *reinterpret_cast<uint4*>(srow + ((j ^ (r & 7)) << 4)) =
-                  make_uint4(w[4 * jj], w[4 * jj + 1], w[4 * jj + 2], w[4 * jj + 3]);
-            }
-          } else {
-            __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                  ((int64_t)(qstart + tok) * p.Hq + (int64_t)it.kvh * p.G + gh) * D + kOC * h;
-            store_row<kOC>(orow, w, p.out_al32);
-          }
+        for (int t = 0; t < 8; ++t) w[t] = pack_bf16(__uint_as_float(o[2 * t]), __uint_as_float(o[2 * t + 1]));
+        if (staged) {
+          *reinterpret_cast<uint4*>(srow + (((cc >> 3) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(srow + ((((cc >> 3) + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
         } else {
-          // this split's partial row: D fp32 (the workspace is 256-byte aligned)
-          float* dst = p.part_acc + (int64_t)(it.part + r) * D + kOC * h;
-#pragma unroll
-          for (int u = 0; u < kOC; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * (1.f / (1 << kWeightExp)));
-#pragma unroll
-          for (int u = 0; u < kOC / 8; ++u) st_global_v8(dst + 8 * u, o + 8 * u);
-          if (h == 0) p.part_ml[it.part + r] = make_float2(m_ref, ltot);
+          store_row<16>(orow + cc, w, p.out_al32);
         }
       }
+      __syncwarp();
+      tc_fence_before();
+      mbar_arrive(&bars->o_empty);
+      if (valid && it.part >= 0 && h == 0) p.part_ml[it.part + r] = make_float2(m_ref, ltot);
       if (staged) fence_proxy_async_smem();  // the staged rows, for the TMA stores
       mbar_arrive(&bars->o_staged[qb]);
       if (it.grp >= 0) {
@@ -897,38 +901,42 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           named_barrier(5, 256);
           if (r < gr.nrows) {
             float M = -CUDART_INF_F;
-#pragma unroll 8
+#pragma unroll 4
             for (int sp = 0; sp < gr.nsplit; ++sp)
               M = fmaxf(M, __ldcg(&p.part_ml[gr.part_base + sp * gr.nrows + r]).x);
             const float Mu = M == -CUDART_INF_F ? 0.f : M;
-            float lsum = 0.f;
-            float acc[kOC];
-#pragma unroll
-            for (int cc = 0; cc < kOC; ++cc) acc[cc] = 0.f;
-            for (int sp = 0; sp < gr.nsplit; ++sp) {
-              const int slot = gr.part_base + sp * gr.nrows + r;
-              const float2 ml = __ldcg(&p.part_ml[slot]);
-              const float wt = fast_exp2(ml.x - Mu);
-              lsum = fmaf(wt, ml.y, lsum);
-              const float4* src = reinterpret_cast<const float4*>(p.part_acc + (int64_t)slot * D + kOC * h);
-#pragma unroll
-              for (int u = 0; u < kOC / 4; ++u) {
-                const float4 a = __ldcg(src + u);
-                acc[4 * u] = fmaf(wt, a.x, acc[4 * u]);
-                acc[4 * u + 1] = fmaf(wt, a.y, acc[4 * u + 1]);
-                acc[4 * u + 2] = fmaf(wt, a.z, acc[4 * u + 2]);
-                acc[4 * u + 3] = fmaf(wt, a.w, acc[4 * u + 3]);
-              }
-            }
-            const float inv = 1.f / lsum;
             const int grow = gr.row0 + r;
             const int gtok = grow / p.G, ggh = grow - gtok * p.G;
-            __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) +
+            __nv_bfloat16* mrow = static_cast<__nv_bfloat16*>(p.out) +
                                   ((int64_t)(qstart + gtok) * p.Hq + (int64_t)gr.kvh * p.G + ggh) * D + kOC * h;
-            uint32_t w[kOC / 2];
+#pragma unroll 1
+            for (int cc = 0; cc < kOC; cc += 16) {
+              float lsum = 0.f;
+              float acc[16];
 #pragma unroll
-            for (int u = 0; u < kOC / 2; ++u) w[u] = pack_bf16(acc[2 * u] * inv, acc[2 * u + 1] * inv);
-            store_row<kOC>(orow, w, p.out_al32);
+              for (int t = 0; t < 16; ++t) acc[t] = 0.f;
+#pragma unroll 2
+              for (int sp = 0; sp < gr.nsplit; ++sp) {
+                const int slot = gr.part_base + sp * gr.nrows + r;
+                const float2 ml = __ldcg(&p.part_ml[slot]);
+                const float wt = fast_exp2(ml.x - Mu);
+                lsum = fmaf(wt, ml.y, lsum);
+                const float4* src = reinterpret_cast<const float4*>(p.part_acc + (int64_t)slot * D + kOC * h + cc);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const float4 a = __ldcg(src + u);
+                  acc[4 * u] = fmaf(wt, a.x, acc[4 * u]);
+                  acc[4 * u + 1] = fmaf(wt, a.y, acc[4 * u + 1]);
+                  acc[4 * u + 2] = fmaf(wt, a.z, acc[4 * u + 2]);
+                  acc[4 * u + 3] = fmaf(wt, a.w, acc[4 * u + 3]);
+                }
+              }
+              const float minv = 1.f / lsum;
+              uint32_t w[8];
+#pragma unroll
+              for (int t = 0; t < 8; ++t) w[t] = pack_bf16(acc[2 * t] * minv, acc[2 * t + 1] * minv);
+              store_row<16>(mrow + cc, w, p.out_al32);
+            }
           }
         }
         named_barrier(5, 256);
@@ -942,10 +950,9 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-}  // namespace
-
-cudaError_t launch_mma_fp8block(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
-                                const CUtensorMap& vmap, const CUtensorMap& omap, int grid, cudaStream_t s) {
+template <int kRun>
+cudaError_t launch_t(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                     const CUtensorMap& omap, int grid, cudaStream_t s) {
   static unsigned long long done_mask = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -954,20 +961,28 @@ cudaError_t launch_mma_fp8block(const AttnParams& p, const CUtensorMap& qmap, co
   if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
     // the register split needs the block launched with kRegs registers per thread
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, mma_fp8block_kernel);
+    e = cudaFuncGetAttributes(&fa, mma_fp8block_kernel<kRun>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(mma_fp8block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(mma_fp8block_kernel<kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
   }
   if (p.no_wait) {  // beside the few-row kernel: a plain launch, as the bf16 kernel's
-    mma_fp8block_kernel<<<dim3(grid), dim3(kThreads), kSmem, s>>>(p, qmap, kmap, vmap, omap);
+    mma_fp8block_kernel<kRun><<<dim3(grid), dim3(kThreads), kSmem, s>>>(p, qmap, kmap, vmap, omap);
     e = cudaGetLastError();
   } else {
-    e = launch_pdl(mma_fp8block_kernel, dim3(grid), dim3(kThreads), kSmem, s, p, qmap, kmap, vmap, omap);
+    e = launch_pdl(mma_fp8block_kernel<kRun>, dim3(grid), dim3(kThreads), kSmem, s, p, qmap, kmap, vmap, omap);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_mma_fp8block(const AttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                const CUtensorMap& vmap, const CUtensorMap& omap, int grid, cudaStream_t s) {
+  return p.bs >= 16 ? launch_t<16>(p, qmap, kmap, vmap, omap, grid, s)
+                    : launch_t<8>(p, qmap, kmap, vmap, omap, grid, s);
 }
 
 }  // namespace pkv
