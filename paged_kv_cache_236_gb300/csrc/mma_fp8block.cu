@@ -694,10 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
         const int sb = g & 1;
         const int kt = it.kb + j * kKeys;  // first key of the tile
         const uint32_t s_half = lane_base + kSCol + 128 * sb + 64 * h, p_half = lane_base + kPCol + 64 * sb + 32 * h;
-        // S(g), and the P buffer free: the P.V of tile g-2, which read it, done
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], (g >> 1) & 1, wc) &&
-                                         mbar_wait(&bars->pv_done[sb], ((g >> 1) & 1) ^ 1, wc) &&
-                                         mbar_wait(&bars->sc_full[g & (kScaleSlots - 1)], (g / kScaleSlots) & 1, wc))) {
+        // S(g), the P buffer free (the P.V of tile g-2, which read it, done), the
+        // tile's scales; all three at once where they are there
+        uint64_t* const scb = &bars->sc_full[g & (kScaleSlots - 1)];
+        const uint32_t ph = (g >> 1) & 1, scph = (g / kScaleSlots) & 1;
+        if (!__all_sync(0xffffffffu, mbar_test_wait3(&bars->s_full[sb], ph, &bars->pv_done[sb], ph ^ 1, scb, scph)) &&
+            !__all_sync(0xffffffffu, mbar_wait(&bars->s_full[sb], ph, wc) && mbar_wait(&bars->pv_done[sb], ph ^ 1, wc) &&
+                                         mbar_wait(scb, scph, wc))) {
           owe = (idle ? 0 : ntiles - j) + 2;
           break;
         }
@@ -718,10 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           seen = below(nvis) & (below(p.num_sink - (kt + 64 * h)) | ~below(nlo));
         }
         const Scales* scales = tile_scales + (g & (kScaleSlots - 1)) * 16 + 8 * h;
-        // Sixteen columns of S at a time, in loops, the next sixteen on their way: a
-        // row's 64 in registers, with the code unrolled over them, were 1200
-        // instructions a tile for each of three copies, and the instruction cache,
-        // which the other roles' code shares, set the pace.
+        // S is read twice, 32 columns at a time, in loops: a row's 64 in registers,
+        // with the code unrolled over them and three copies of it, did not fit the
+        // instruction cache with the other roles' code, which then set the pace
+        // (prompt chunks 205 us; 157 with 16 columns at a time).
         auto columns = [&](int run, uint32_t (&z)[16]) {  // masked: columns 8 run .. + 15
           if (masked) {
             const uint32_t m = (uint32_t)(seen >> (8 * run));
@@ -771,16 +774,13 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
         };
         auto each = [&](auto&& use) {  // use(run, columns 8 run .. + 15 of this half's S)
           uint32_t a[16], b[16];
-          tmem_ld16(s_half, a);
-          tmem_wait_ld();
 #pragma unroll 1
           for (int run = 0; run < 8; run += 4) {
+            tmem_ld16(s_half + 8 * run, a);
             tmem_ld16(s_half + 8 * run + 16, b);
+            tmem_wait_ld();
             use(run, a);
-            tmem_wait_ld();
-            tmem_ld16(s_half + ((8 * run + 32) & 63), a);  // (the last time: the first again)
             use(run + 2, b);
-            tmem_wait_ld();
           }
         };
         each(max_of);
