@@ -29,9 +29,7 @@
 // Roles (384 threads, one CTA per SM, persistent, items from an atomic counter
 // in the planner's largest-first order), as in the bf16 kernel:
 //   warp 0    K producer: per 128-key tile one {128 bytes, 1, block_size, 1} box
-//             per block (128-byte swizzle), the tile's scales and metadata.
-//             Block ids are read two tiles ahead and scales one, so that
-//             neither's latency is waited for;
+//             per block (128-byte swizzle), the tile's scales and metadata;
 //   warp 11   V producer;
 //   warp 1    TMEM allocation, the thread that issues the MMAs;
 //   warps 2-5 softmax (thread = key = TMEM lane);
@@ -76,7 +74,7 @@ struct Lay {
   static constexpr int kRedOff = kScaleOff + kStages * 256;
   static constexpr int kSlotOff = kRedOff + 2 * 4 * NR * 4;
   static constexpr int kISlotOff = kSlotOff + 2 * 256;
-  static constexpr int kQsOff = kISlotOff + 2 * 320;
+  static constexpr int kQsOff = kISlotOff + 2 * 448;
   static constexpr int kBarOff = kQsOff + 2 * NR * 4;
   static constexpr int kNumBars = 3 * kStages + 8 + 8 + 4 + 4 + 1;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
@@ -115,10 +113,10 @@ struct alignas(16) ItemSlot {
   WorkItem it;
   int idx, L, qstart, n;
   int done, nblk, at, len;
-  int phys[32];       // blocks of the first tile (0 ..), of the second (16 ..)
-  float2 scales[16];  // K's and V's of the first tile's blocks
+  int phys[32];       // the first 32 blocks
+  float2 scales[32];  // K's and V's of them
 };
-static_assert(sizeof(ItemSlot) == 320, "item slot");
+static_assert(sizeof(ItemSlot) == 448, "item slot");
 
 struct alignas(16) EpSlot {
   Meta mt;
@@ -264,8 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       const bool done = sl.done != 0;
       const WorkItem it = sl.it;
       const int idx = sl.idx, L = sl.L, qstart = sl.qstart, n = sl.n, nblk = sl.nblk, at = sl.at, len = sl.len;
-      int phys = sl.phys[lane & 15], next = sl.phys[16 + (lane & 15)];
-      float2 sc = sl.scales[lane & 15];
+      // Block ids and scales are held 32 at a time, a lane to a block: those of the
+      // item's next 32 / nb tiles.  The next 32 are read while these are used
+      // (ids read two tiles ahead, a tile's at a time, stalled the loop for their
+      // latency in every tile, since the registers move on: 4.4 TB/s).
+      int phys = sl.phys[lane];
+      Scales sc = make_scales(sl.scales[lane].x, sl.scales[lane].y);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->islot_free[qb]);
       if (done) {
@@ -283,18 +285,24 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         break;
       }
       const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
+      const int group = 32 / nb;  // tiles that 32 blocks make
+      const int my_tile = lane / nb, my_block = lane % nb;
+      int next_phys = (int)p.num_blocks;
+      float2 next_sc = make_float2(1.f, 1.f);
       bool ok = true;
+      int tile = 0;  // of the group
       for (int kbase = it.kb; kbase < it.ke; kbase += kKeys, ++g) {
         const int st = g % kStages;
         const bool first = kbase == it.kb;
-        // the ids of the tile after the next, the scales of the next
-        int after = (int)p.num_blocks;
-        if (lane < nb && kbase + 2 * kKeys < it.ke) after = block_of(bt, nblk, at, len, kbase + 2 * kKeys + lane * p.bs);
-        float nk = 1.f, nv = 1.f;
-        if (!vprod && lane < nb && kbase + kKeys < it.ke && next < p.num_blocks) {
-          const int64_t i = (int64_t)next * p.Hkv + it.kvh;
-          nk = __ldg(p.k_scales + i);
-          nv = __ldg(p.v_scales + i);
+        if (tile == 0) {
+          const int place = kbase + group * kKeys + lane * p.bs;
+          next_phys = place < it.ke ? block_of(bt, nblk, at, len, place) : (int)p.num_blocks;
+        } else if (tile == 1 && !vprod) {
+          next_sc = make_float2(1.f, 1.f);
+          if (next_phys < p.num_blocks) {
+            const int64_t i = (int64_t)next_phys * p.Hkv + it.kvh;
+            next_sc = make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
+          }
         }
         if (!wait_all(&bars->kv_empty[st], ((g / kStages) & 1) ^ 1, wc)) {
           ok = false;
@@ -303,41 +311,40 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         if (!vprod && lane == 0 && it.ke - kbase <= kFetchLeadTiles * kKeys &&
             (first || it.ke - (kbase - kKeys) > kFetchLeadTiles * kKeys))
           mbar_arrive(&bars->fetch_go);  // once per item: the next one may be taken now
-        if (!vprod && p.fault_tile == g + 1 && blockIdx.x == 0) {
-          // testing only: this tile is never loaded, so the waits for it run out
-          phys = next;
-          next = after;
-          sc = make_float2(nk, nv);
-          continue;
-        }
-        uint8_t* dst = smem + st * kStageBytes + (vprod ? kTileBytes : 0);
-        if (!vprod) {
-          if (lane < nb) tile_scales[st * 16 + lane] = make_scales(sc.x, sc.y);
-          if (lane == 0) {
-            Meta& m = meta[st];
-            m.item = idx;
-            m.kbase = kbase;
-            m.flags = ((kbase + kKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
-            m.seq = it.seq;
-            m.kvh = it.kvh;
-            m.row0 = it.row0;
-            m.nrows = it.nrows;
-            m.ke = it.ke;
-            m.part = it.part;
-            m.grp = it.grp;
-            m.L = L;
-            m.n = n;
-            m.qstart = qstart;
-            m.qbuf = qb;
+        // testing only: this tile is never loaded, so the waits for it run out
+        if (vprod || p.fault_tile != g + 1 || blockIdx.x != 0) {
+          uint8_t* dst = smem + st * kStageBytes + (vprod ? kTileBytes : 0);
+          if (!vprod) {
+            if (my_tile == tile) tile_scales[st * 16 + my_block] = sc;
+            if (lane == 0) {
+              Meta& m = meta[st];
+              m.item = idx;
+              m.kbase = kbase;
+              m.flags = ((kbase + kKeys >= it.ke) ? kMetaLast : 0) | (first ? kMetaFirst : 0);
+              m.seq = it.seq;
+              m.kvh = it.kvh;
+              m.row0 = it.row0;
+              m.nrows = it.nrows;
+              m.ke = it.ke;
+              m.part = it.part;
+              m.grp = it.grp;
+              m.L = L;
+              m.n = n;
+              m.qstart = qstart;
+              m.qbuf = qb;
+            }
+            __syncwarp();
           }
+          if (lane == 0) mbar_arrive_expect_tx(&fullb[st], kTileBytes);
+          __syncwarp();
+          if (my_tile == tile)
+            tma_load_4d(dst + my_block * p.bs * 128, vprod ? &vmap : &kmap, &fullb[st], 0, it.kvh, 0, phys);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&fullb[st], kTileBytes);
-        __syncwarp();
-        if (lane < nb) tma_load_4d(dst + lane * p.bs * 128, vprod ? &vmap : &kmap, &fullb[st], 0, it.kvh, 0, phys);
-        phys = next;
-        next = after;
-        sc = make_float2(nk, nv);
+        if (++tile == group) {
+          tile = 0;
+          phys = next_phys;
+          sc = make_scales(next_sc.x, next_sc.y);
+        }
       }
       if (!ok) {
         drain();
@@ -389,17 +396,15 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         len = hole.len;
       }
       const int32_t* bt = p.block_tables + (int64_t)it.seq * p.max_blocks;
-      const int tile = it.kb + (lane >> 4) * kKeys;
-      int phys = (int)p.num_blocks;
-      if ((lane & 15) < nb && tile < it.ke) phys = block_of(bt, nblk, at, len, tile + (lane & 15) * p.bs);
+      const int place = it.kb + lane * p.bs;
+      const int phys = place < it.ke ? block_of(bt, nblk, at, len, place) : (int)p.num_blocks;
       sl.phys[lane] = phys;
-      float sk = 1.f, sv = 1.f;
-      if (lane < nb && phys < p.num_blocks) {
+      float2 sc = make_float2(1.f, 1.f);
+      if (phys < p.num_blocks) {
         const int64_t i = (int64_t)phys * p.Hkv + it.kvh;
-        sk = __ldg(p.k_scales + i);
-        sv = __ldg(p.v_scales + i);
+        sc = make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
       }
-      if (lane < 16) sl.scales[lane] = make_float2(sk, sv);
+      sl.scales[lane] = sc;
       if (lane == 0) {
         sl.it = it;
         sl.idx = idx;
