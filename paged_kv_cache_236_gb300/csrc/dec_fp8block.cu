@@ -462,12 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       bool pend_first = false, pend_last = false;
       auto issue_pv = [&]() -> bool {
         const int b = pend & 1, st = pend % kStages, ob = pend_item & 1;
-        if (pend_first) {
-          // O^T[ob] is about to be overwritten: the epilogue of item pend_item-2 must have read it
-          if (!mbar_wait(&bars->o_empty[ob], ((pend_item >> 1) & 1) ^ 1, wc)) return false;
-        }
-        if (!mbar_wait(&bars->p_full[b], (pend >> 1) & 1, wc)) return false;
-        if (!mbar_wait(&bars->v_full[st], (pend / kStages) & 1, wc)) return false;
+        // P and V there, and, on an item's first tile, O^T[ob], which is about to be
+        // overwritten, read by the epilogue of item pend_item-2
+        uint64_t *const pf = &bars->p_full[b], *const vf = &bars->v_full[st];
+        uint64_t* const of = pend_first ? &bars->o_empty[ob] : vf;
+        const uint32_t pph = (pend >> 1) & 1, vph = (pend / kStages) & 1;
+        const uint32_t oph = pend_first ? ((pend_item >> 1) & 1) ^ 1 : vph;
+        if (!mbar_test_wait3(pf, pph, vf, vph, of, oph) &&
+            (!mbar_wait(of, oph, wc) || !mbar_wait(pf, pph, wc) || !mbar_wait(vf, vph, wc)))
+          return false;
         tc_fence_after();
         const uint64_t dv = desc_add(dv0, st * kStageBytes);
         const uint64_t dp = desc_add(dp0, b * Y::kNP * 128);
@@ -485,9 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       bool ok = true;
       for (;; ++g) {
         const int st = g % kStages;
+        const int b = g & 1;
         uint64_t* const kf = &bars->k_full[st];
-        const uint32_t kph = (g / kStages) & 1;
-        if (pend >= 0) {
+        const uint32_t kph = (g / kStages) & 1, sph = ((g >> 1) & 1) ^ 1;
+        // K(g), and S buffer b read: at once where they are there (a wait that is over
+        // takes this thread 110 cycles, and its waits one by one took 1600 a tile)
+        const bool ready = mbar_test_wait3(kf, kph, &bars->s_free[b], sph, kf, kph);
+        if (!ready && pend >= 0) {
           // Whichever comes first: K(g) landed (then S(g), and P.V(pend) after
           // it, as below) or P(pend) written (then P.V(pend) now).
           const uint64_t t0 = globaltimer();
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
           }
           if (!ok) break;
         }
-        if (!mbar_wait(kf, kph, wc)) {
+        if (!ready && !mbar_wait(kf, kph, wc)) {
           ok = false;
           break;
         }
@@ -521,8 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
             break;
           }
         }
-        const int b = g & 1;
-        if (!mbar_wait(&bars->s_free[b], ((g >> 1) & 1) ^ 1, wc)) {
+        if (!ready && !mbar_wait(&bars->s_free[b], sph, wc)) {
           ok = false;
           break;
         }
@@ -561,10 +567,17 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
     if (warp < 6) {
       // ---------------------------------------------------------- softmax
       // Failures of waits are carried in `pending` (warp-uniform) to the next
-      // agreement barrier (barrier 1 over the 4 softmax warps, which also
-      // exchanges the row maxima), where all four warps go on or leave.
+      // agreement barrier (barrier 1 over the 4 softmax warps), where all four
+      // warps go on or leave.
+      // The weights are made with the reference as it stands, and the barrier
+      // that ends the tile tells whether a key of any warp exceeded it by the
+      // threshold; only then are the tile's row maxima found and exchanged and
+      // the weights made again (the first tile of an item, and few others).  The
+      // maxima in every tile were a chain of shuffles and a barrier before the
+      // exponentials: 1850 cycles a tile, 223 us for 4 x 131072 keys.
       const int my_row = lane >> (5 - kLog);  // row this lane holds after a reduction
       const bool row_writer = (lane & ((1 << (5 - kLog)) - 1)) == 0;
+      const int my_block = t / p.bs;
       float m_ref[NR], lsum[NR], unit[NR];  // unit: a row's scale times the logit scale (log2 units)
       int vis[NR], lo[NR];
 #pragma unroll
@@ -580,97 +593,56 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         const int st = g % kStages;
         const int b = g & 1;
         float* redb = red + b * 4 * NR;  // [4 warps][NR], double-buffered by tile
-        bool fail = pending || !wait_all(&bars->k_full[st], (g / kStages) & 1, wc);
+        uint64_t* const kf = &bars->k_full[st];
+        const uint32_t kph = (g / kStages) & 1, ph = (g >> 1) & 1;
+        // the tile's metadata (with its K), its S, and the P buffer free (P.V of
+        // tile g-2 done): all three at once where they are there
+        bool fail = pending;
+        if (!fail && !__all_sync(0xffffffffu, mbar_test_wait3(kf, kph, &bars->s_full[b], ph, &bars->pv_done[b], ph ^ 1))) {
+          fail = !wait_all(kf, kph, wc);
+          if (!fail && !(meta[st].flags & kMetaDone))
+            fail = !wait_all(&bars->s_full[b], ph, wc) || !wait_all(&bars->pv_done[b], ph ^ 1, wc);
+        }
         const int flags = fail ? 0 : meta[st].flags;
         const bool done = (flags & kMetaDone) != 0;
-        uint32_t sraw[2 * NR];
+        if (!fail && !done && (flags & kMetaFirst)) {
+          mt = meta[st];
+          ++it_cnt;
+          fail = !wait_all(&bars->q_full[mt.qbuf], (it_cnt >> 1) & 1, wc);
 #pragma unroll
-        for (int r = 0; r < 2 * NR; ++r) sraw[r] = 0;
-        int kbase = 0;
-        Scales sc{1.f, 0.f, 1.f, 0.f};
-        if (!fail && !done) {
-          if (flags & kMetaFirst) {
-            mt = meta[st];
-            ++it_cnt;
-            fail = !wait_all(&bars->q_full[mt.qbuf], (it_cnt >> 1) & 1, wc);
-#pragma unroll
-            for (int r = 0; r < NR; ++r) {
-              m_ref[r] = -CUDART_INF_F;
-              lsum[r] = 0.f;
-              unit[r] = row_scales[mt.qbuf * NR + r] * p.scale_log2;
-              const int tok = (mt.row0 + r) / p.G;
-              vis[r] = r < mt.nrows ? min(mt.ke, p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
-              lo[r] = p.window > 0 ? mt.L - mt.n + tok + 1 - p.window : INT_MIN;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->q_empty[mt.qbuf]);
+          for (int r = 0; r < NR; ++r) {
+            m_ref[r] = -CUDART_INF_F;
+            lsum[r] = 0.f;
+            unit[r] = row_scales[mt.qbuf * NR + r] * p.scale_log2;
+            const int tok = (mt.row0 + r) / p.G;
+            vis[r] = r < mt.nrows ? min(mt.ke, p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
+            lo[r] = p.window > 0 ? mt.L - mt.n + tok + 1 - p.window : INT_MIN;
           }
-          kbase = meta[st].kbase;
-          sc = tile_scales[st * 16 + t / p.bs];
-          fail = !wait_all(&bars->s_full[b], (g >> 1) & 1, wc) || fail;
-          if (!fail) {
-            tc_fence_after();
-            tmem_ld_cols<2 * NR>(lane_base + Y::kSCol + b * Y::kNQ, sraw);
-            tmem_wait_ld();
-            tc_fence_before();
-            mbar_arrive(&bars->s_free[b]);
-          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->q_empty[mt.qbuf]);
         }
-        // ---- masked logits of this thread's key, V's scale in them; row maxima over the tile
+        const bool ok = !fail && !done;
+        const int kbase = ok ? meta[st].kbase : 0;
         const int key = kbase + t;
-        float v[NR], a[NR];
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const bool seen = key < vis[r] && (key >= lo[r] || key < p.num_sink);
-          const float s = (__uint_as_float(sraw[r]) + __uint_as_float(sraw[NR + r])) * sc.k;
-          v[r] = seen ? fmaf(s, unit[r], sc.log_v) : -CUDART_INF_F;
-          a[r] = v[r];
-        }
-        const float wmax = xreduce<NR>(a, lane, MaxOp());
-        if (row_writer) redb[q4 * NR + my_row] = wmax;
-        if (barrier_any(1, 128, fail || done)) {
-          // leaving: at the end of the work (nobody failed), tell the epilogue
-          if (!barrier_any(1, 128, fail)) {
-            const int ob = (it_cnt + 1) & 1;
-            if (wait_all(&bars->ml_empty[ob], (((it_cnt + 1) >> 1) & 1) ^ 1, wc)) {
-              if (t == 0) slots[ob].done = 1;
-              mbar_arrive(&bars->ml_full[ob]);
-            }
-          }
-          break;
-        }
-        float alpha[NR], m_use[NR];
-        bool any_rescale = false;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float mx = fmaxf(fmaxf(redb[r], redb[NR + r]), fmaxf(redb[2 * NR + r], redb[3 * NR + r]));
-          alpha[r] = 1.f;
-          if (mx > m_ref[r] + kRescaleThreshold) {  // false while both are -inf
-            alpha[r] = fast_exp2(m_ref[r] - mx);    // 0 when m_ref is -inf
-            any_rescale |= m_ref[r] != -CUDART_INF_F;
-            m_ref[r] = mx;
-          }
-          m_use[r] = (m_ref[r] == -CUDART_INF_F ? 0.f : m_ref[r]) - kWeightExp;
-        }
-        any_rescale = any_rescale && !(flags & kMetaFirst);
-
-        // ---- the weights' three terms into this tile's P buffer: row i NR + r, column t, 128-byte swizzle
-        pending = !wait_all(&bars->pv_done[b], ((g >> 1) & 1) ^ 1, wc);  // P.V of tile g-2 is done
+        Scales sc{1.f, 0.f, 1.f, 0.f};
+        float v[NR], w[NR];  // log2 of the weights (V's scale in them); the weights
+        bool exceeds = false;
         uint8_t* pbuf = smem + Y::kPOff + b * Y::kNP * 128 + (t & 15);
         const int chunk = t >> 4;
         auto at = [&](int row) { return pbuf + row * 128 + ((chunk ^ (row & 7)) << 4); };
+        // the weights and their three terms in this tile's P buffer: row i NR + r, column t, 128-byte swizzle
+        auto make_weights = [&]() {
 #pragma unroll
-        for (int r = 0; r < NR; r += 2) {
-          const float w0 = fast_exp2(v[r] - m_use[r]), w1 = fast_exp2(v[r + 1] - m_use[r + 1]);
-          lsum[r] = fmaf(lsum[r], alpha[r], w0 * sc.inv_v);
-          lsum[r + 1] = fmaf(lsum[r + 1], alpha[r + 1], w1 * sc.inv_v);
-          const __half2 h = __floats2half2_rn(w0, w1);
-          const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&h), t0 = b0 & 0xFF00FF00u;
-          const __half2 h1 = __hsub2(h, *reinterpret_cast<const __half2*>(&t0));  // exact
-          const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&h1), t1 = b1 & 0xFF00FF00u;
-          const __half2 h2 = __hsub2(h1, *reinterpret_cast<const __half2*>(&t1));
-          const uint32_t b2 = *reinterpret_cast<const uint32_t*>(&h2) + 0x00800080u;  // to nearest
-          if (!pending) {
+          for (int r = 0; r < NR; r += 2) {
+            auto m_use = [&](int i) { return (m_ref[i] == -CUDART_INF_F ? 0.f : m_ref[i]) - kWeightExp; };
+            w[r] = fast_exp2(v[r] - m_use(r));
+            w[r + 1] = fast_exp2(v[r + 1] - m_use(r + 1));
+            const __half2 h = __floats2half2_rn(w[r], w[r + 1]);
+            const uint32_t b0 = *reinterpret_cast<const uint32_t*>(&h), t0 = b0 & 0xFF00FF00u;
+            const __half2 h1 = __hsub2(h, *reinterpret_cast<const __half2*>(&t0));  // exact
+            const uint32_t b1 = *reinterpret_cast<const uint32_t*>(&h1), t1 = b1 & 0xFF00FF00u;
+            const __half2 h2 = __hsub2(h1, *reinterpret_cast<const __half2*>(&t1));
+            const uint32_t b2 = *reinterpret_cast<const uint32_t*>(&h2) + 0x00800080u;  // to nearest
             *at(r) = (uint8_t)(b0 >> 8);
             *at(r + 1) = (uint8_t)(b0 >> 24);
             *at(NR + r) = (uint8_t)(b1 >> 8);
@@ -678,8 +650,65 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
             *at(2 * NR + r) = (uint8_t)(b2 >> 8);
             *at(2 * NR + r + 1) = (uint8_t)(b2 >> 24);
           }
+        };
+        if (ok) {
+          uint32_t sraw[2 * NR];
+          tc_fence_after();
+          tmem_ld_cols<2 * NR>(lane_base + Y::kSCol + b * Y::kNQ, sraw);
+          sc = tile_scales[st * 16 + my_block];
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(&bars->s_free[b]);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const bool seen = key < vis[r] && (key >= lo[r] || key < p.num_sink);
+            const float s = (__uint_as_float(sraw[r]) + __uint_as_float(sraw[NR + r])) * sc.k;
+            v[r] = seen ? fmaf(s, unit[r], sc.log_v) : -CUDART_INF_F;
+            exceeds |= v[r] > m_ref[r] + kRescaleThreshold;  // false while both are -inf
+          }
+          if (!(flags & kMetaFirst)) make_weights();
         }
-        if (any_rescale && !pending) {
+        bool any_rescale = false;
+        float alpha[NR];
+        if (barrier_any(1, 128, exceeds || !ok)) {
+          // leave, or raise the reference
+          if (barrier_any(1, 128, !ok)) {
+            // leaving: at the end of the work (nobody failed), tell the epilogue
+            if (!barrier_any(1, 128, fail)) {
+              const int ob = (it_cnt + 1) & 1;
+              if (wait_all(&bars->ml_empty[ob], (((it_cnt + 1) >> 1) & 1) ^ 1, wc)) {
+                if (t == 0) slots[ob].done = 1;
+                mbar_arrive(&bars->ml_full[ob]);
+              }
+            }
+            break;
+          }
+          float a[NR];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) a[r] = v[r];
+          const float wmax = xreduce<NR>(a, lane, MaxOp());
+          if (row_writer) redb[q4 * NR + my_row] = wmax;
+          named_barrier(1, 128);
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float mx = fmaxf(fmaxf(redb[r], redb[NR + r]), fmaxf(redb[2 * NR + r], redb[3 * NR + r]));
+            alpha[r] = 1.f;
+            if (mx > m_ref[r] + kRescaleThreshold) {
+              alpha[r] = fast_exp2(m_ref[r] - mx);  // 0 when m_ref is -inf
+              any_rescale |= m_ref[r] != -CUDART_INF_F;
+              m_ref[r] = mx;
+              lsum[r] *= alpha[r];
+            }
+          }
+          any_rescale = any_rescale && !(flags & kMetaFirst);
+          make_weights();
+        } else if (flags & kMetaFirst) {
+          make_weights();  // (none of the tile's keys is seen by any row)
+        }
+#pragma unroll
+        for (int r = 0; r < NR; ++r) lsum[r] = fmaf(w[r], sc.inv_v, lsum[r]);
+        pending = false;
+        if (any_rescale) {
           // O^T must hold every earlier tile's P.V before it is scaled; thread t
           // owns O^T row t (output column t), whose columns i NR + r belong to row r
           pending = !wait_all(&bars->pv_done[b ^ 1], ((g - 1) >> 1) & 1, wc);
