@@ -499,8 +499,11 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   pp.dec_tile_keys = dectc ? kMmaTileKeys : kDecTileKeys;
   // Four items per CTA of the decode kernels: fewer, longer items cost less
   // per item (pipeline restarts, partial writes, merges) than a finer tail
-  // saves (measured on the decode, mixed and long-context batches).
-  pp.target_dec = dectc ? dev->sms * 4 : dec_grid * 4;
+  // saves (measured on the decode, mixed and long-context batches).  Two where
+  // blocks have scales: its tiles take half the time and its items start no
+  // faster (decode batch 75.7 us, with three 82.8, with four 83.2; 4 x 131072 keys
+  // 207, 211 and 213 us).
+  pp.target_dec = blocks ? dev->sms * 2 : dectc ? dev->sms * 4 : dec_grid * 4;
   pp.dec_ctas = dectc ? dev->sms : dec_grid;
   // Items are fetched dynamically in largest-first order, so two per SM
   // balance the tensor-core kernel; every split costs a partial write and a

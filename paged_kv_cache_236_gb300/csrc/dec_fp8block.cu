@@ -26,12 +26,12 @@
 // stays within its range whatever the blocks' scales are; the denominator takes
 // w / (2^11 sv).
 //
-// Roles (384 threads, one CTA per SM, persistent, items from an atomic counter
+// Roles (416 threads, one CTA per SM, persistent, items from an atomic counter
 // in the planner's largest-first order), as in the bf16 kernel:
 //   warp 0    K producer: per 128-key tile one {128 bytes, 1, block_size, 1} box
 //             per block (128-byte swizzle), the tile's scales and metadata;
 //   warp 11   V producer;
-//   warp 1    TMEM allocation, the thread that issues the MMAs;
+//   warps 1,12 issue the MMAs, S and P.V (warp 1 also allocates TMEM);
 //   warps 2-5 softmax (thread = key = TMEM lane);
 //   warps 6-9 epilogue (thread = output column = TMEM lane of O^T);
 //   warp 10   item fetch, and the split of the item's q rows.
@@ -50,7 +50,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kStages = 6;
 constexpr int kKeys = kMmaTileKeys;       // 128 keys per tile
 constexpr int kTileBytes = kKeys * 128;   // K or V codes: 16 KB
@@ -76,7 +76,7 @@ struct Lay {
   static constexpr int kISlotOff = kSlotOff + 2 * 256;
   static constexpr int kQsOff = kISlotOff + 2 * 448;
   static constexpr int kBarOff = kQsOff + 2 * NR * 4;
-  static constexpr int kNumBars = 3 * kStages + 8 + 8 + 4 + 4 + 1;
+  static constexpr int kNumBars = 3 * kStages + 6 + 8 + 4 + 4 + 1;
   static constexpr int kSmem = kBarOff + kNumBars * 8 + 16 + 1024;
   static constexpr uint32_t kIdescS = idesc_f8(128, kNQ, kE4m3, kE4m3, false, false);
   static constexpr uint32_t kIdescO = idesc_f8(128, kNP, kE4m3, kE5m2, true, false);
@@ -93,8 +93,9 @@ struct alignas(16) Meta {
 static_assert(sizeof(Meta) == 64, "meta slot");
 
 struct Bars {
+  // kv_empty[st] is the P.V of the stage's tile done: its codes and its P read
   uint64_t k_full[kStages], v_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], s_free[2], p_full[2];
   uint64_t o_full[2], o_empty[2], ml_full[2], ml_empty[2];
   uint64_t islot_full[2], islot_free[2];
   uint64_t q_full[2], q_empty[2];  // an item's q terms written; its last S issued and its row scales read
@@ -188,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
   Meta* meta = reinterpret_cast<Meta*>(smem + Y::kMetaOff);
   Scales* tile_scales = reinterpret_cast<Scales*>(smem + Y::kScaleOff);  // [stage][16]
   float* red = reinterpret_cast<float*>(smem + Y::kRedOff);              // [2][4 warps][NR rows]
-  float* row_scales = reinterpret_cast<float*>(smem + Y::kQsOff);        // [2][NR]
+  float* row_scales = reinterpret_cast<float*>(smem + Y::kQsOff);        // [2][NR], times the logit scale
   ItemSlot* islots = reinterpret_cast<ItemSlot*>(smem + Y::kISlotOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{p.err, wait_limit(p.wait_ns)};
@@ -203,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       mbar_init(&bars->s_full[b], 1);
       mbar_init(&bars->s_free[b], 128);
       mbar_init(&bars->p_full[b], 128);
-      mbar_init(&bars->pv_done[b], 1);
       mbar_init(&bars->o_full[b], 1);
       mbar_init(&bars->o_empty[b], 128);
       mbar_init(&bars->ml_full[b], 128);
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       mbar_init(&bars->islot_full[b], 32);
       mbar_init(&bars->islot_free[b], 2);  // both producers read the slot
       mbar_init(&bars->q_full[b], 32);
-      mbar_init(&bars->q_empty[b], 1 + 4);  // the MMA thread's commit, the four softmax warps
+      mbar_init(&bars->q_empty[b], 1 + 4);  // the S issuer's commit, the four softmax warps
     }
     mbar_init(&bars->fetch_go, 1);
     fence_mbar_init();
@@ -444,119 +444,87 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         const int c1 = (lane >> 2) ^ (r & 7), c2 = (lane >> 2) ^ ((NR + r) & 7);
         *reinterpret_cast<uint32_t*>(qd + r * 128 + (c1 << 4) + (lane & 3) * 4) = hi;
         *reinterpret_cast<uint32_t*>(qd + (NR + r) * 128 + (c2 << 4) + (lane & 3) * 4) = lo;
-        if (lane == r) row_scales[qb * NR + r] = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (lane == r) row_scales[qb * NR + r] = __uint_as_float((uint32_t)(127 + e) << 23) * p.scale_log2;
       }
       fence_proxy_async_smem();
       mbar_arrive(&bars->q_full[qb]);
     }
   } else if (warp == 1) {
-    // ================================================================ MMA issuer
-    if (lane == 0) {
-      int g = 0, it_cnt = -1;
-      int pend = -1, pend_item = 0;   // tile whose P.V is still to be issued, and its item count
-      int last_s = -1, last_pv = -1;  // the last S and P.V issued
-      const uint64_t dk0 = desc_k(smem_base);
-      const uint64_t dv0 = desc_mn(smem_base + kTileBytes);
-      const uint64_t dq0 = desc_k(smem_base + Y::kQOff);
-      const uint64_t dp0 = desc_k(smem_base + Y::kPOff);
-      bool pend_first = false, pend_last = false;
-      auto issue_pv = [&]() -> bool {
-        const int b = pend & 1, st = pend % kStages, ob = pend_item & 1;
-        // P and V there, and, on an item's first tile, O^T[ob], which is about to be
-        // overwritten, read by the epilogue of item pend_item-2
-        uint64_t *const pf = &bars->p_full[b], *const vf = &bars->v_full[st];
-        uint64_t* const of = pend_first ? &bars->o_empty[ob] : vf;
-        const uint32_t pph = (pend >> 1) & 1, vph = (pend / kStages) & 1;
-        const uint32_t oph = pend_first ? ((pend_item >> 1) & 1) ^ 1 : vph;
-        if (!mbar_test_wait3(pf, pph, vf, vph, of, oph) &&
-            (!mbar_wait(of, oph, wc) || !mbar_wait(pf, pph, wc) || !mbar_wait(vf, vph, wc)))
-          return false;
-        tc_fence_after();
-        const uint64_t dv = desc_add(dv0, st * kStageBytes);
-        const uint64_t dp = desc_add(dp0, b * Y::kNP * 128);
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 32; ++kk)  // 32 keys: 4 KB of V's rows, 32 bytes of the weights'
-          umma_f8(tmem + Y::kOCol + ob * Y::kNP, desc_add(dv, kk * 4096), desc_add(dp, kk * 32), Y::kIdescO,
-                  (pend_first && kk == 0) ? 0u : 1u);
-        umma_commit(&bars->pv_done[b]);
-        umma_commit(&bars->kv_empty[st]);
-        if (pend_last) umma_commit(&bars->o_full[ob]);
-        last_pv = pend;
-        pend = -1;
-        return true;
-      };
-      bool ok = true;
-      for (;; ++g) {
-        const int st = g % kStages;
-        const int b = g & 1;
-        uint64_t* const kf = &bars->k_full[st];
-        const uint32_t kph = (g / kStages) & 1, sph = ((g >> 1) & 1) ^ 1;
-        // K(g), and S buffer b read: at once where they are there (a wait that is over
-        // takes this thread 110 cycles, and its waits one by one took 1600 a tile)
-        const bool ready = mbar_test_wait3(kf, kph, &bars->s_free[b], sph, kf, kph);
-        if (!ready && pend >= 0) {
-          // Whichever comes first: K(g) landed (then S(g), and P.V(pend) after
-          // it, as below) or P(pend) written (then P.V(pend) now).
-          const uint64_t t0 = globaltimer();
-          for (uint32_t i = 1;; ++i) {
-            if (mbar_test_wait(kf, kph)) break;
-            if (mbar_test_wait(&bars->p_full[pend & 1], (pend >> 1) & 1)) {
-              ok = issue_pv();
-              break;
-            }
-            if ((i & 63u) == 0 && globaltimer() - t0 > wc.limit_ns) {
-              raise_error(wc.err, PKV_DEVERR_TIMEOUT);
-              ok = false;
-              break;
-            }
-          }
-          if (!ok) break;
-        }
-        if (!ready && !mbar_wait(kf, kph, wc)) {
-          ok = false;
-          break;
-        }
-        const int flags = meta[st].flags;
-        if (flags & kMetaDone) {
-          if (pend >= 0) ok = issue_pv();
-          break;
-        }
-        if (flags & kMetaFirst) {
-          ++it_cnt;
-          if (!mbar_wait(&bars->q_full[it_cnt & 1], (it_cnt >> 1) & 1, wc)) {
-            ok = false;
-            break;
-          }
-        }
-        if (!ready && !mbar_wait(&bars->s_free[b], sph, wc)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t dk = desc_add(dk0, st * kStageBytes);
-        const uint64_t dq = desc_add(dq0, (it_cnt & 1) * Y::kNQ * 128);
+    // ================================================================ S issuer
+    // The issuing warps stay together and only the issue itself is one lane's, so
+    // that descriptors and counters are warp-uniform.  Waits are taken several at
+    // a time (one that is over takes 110 cycles), and S and P.V have a warp each:
+    // an MMA takes a warp 70 cycles to issue, and the eight of a tile with their
+    // waits and commits took one warp 1600, as long as a tile comes from HBM.
+    const bool issues = lane == 0;
+    const uint64_t dk0 = desc_k(smem_base), dq0 = desc_k(smem_base + Y::kQOff);
+    int g = 0, it_cnt = -1;
+    for (;; ++g) {
+      const int st = g % kStages, b = g & 1;
+      uint64_t* const kf = &bars->k_full[st];
+      const uint32_t kph = (g / kStages) & 1, sph = ((g >> 1) & 1) ^ 1;
+      // K(g) landed, S buffer b read
+      if (!__all_sync(0xffffffffu, mbar_test_wait3(kf, kph, &bars->s_free[b], sph, kf, kph)) &&
+          (!wait_all(kf, kph, wc) || (!(meta[st].flags & kMetaDone) && !wait_all(&bars->s_free[b], sph, wc))))
+        break;
+      const int flags = meta[st].flags;
+      if (flags & kMetaDone) break;
+      if (flags & kMetaFirst) {
+        ++it_cnt;
+        if (!wait_all(&bars->q_full[it_cnt & 1], (it_cnt >> 1) & 1, wc)) break;
+      }
+      tc_fence_after();
+      const uint64_t dk = desc_add(dk0, st * kStageBytes);
+      const uint64_t dq = desc_add(dq0, (it_cnt & 1) * Y::kNQ * 128);
+      const uint32_t d = tmem + Y::kSCol + b * Y::kNQ;
+      if (issues) {
 #pragma unroll
         for (int kk = 0; kk < 128 / 32; ++kk)
-          umma_f8(tmem + Y::kSCol + b * Y::kNQ, desc_add(dk, kk * 32), desc_add(dq, kk * 32), Y::kIdescS, kk > 0 ? 1u : 0u);
+          umma_f8(d, desc_add(dk, kk * 32), desc_add(dq, kk * 32), Y::kIdescS, kk > 0 ? 1u : 0u);
         umma_commit(&bars->s_full[b]);
         if (flags & kMetaLast) umma_commit(&bars->q_empty[it_cnt & 1]);
-        last_s = g;
-        if (pend >= 0 && !issue_pv()) {
-          ok = false;
-          break;
-        }
-        pend = g;
-        pend_item = it_cnt;
-        pend_first = (flags & kMetaFirst) != 0;
-        pend_last = (flags & kMetaLast) != 0;
       }
-      if (!ok) {
-        // leaving early: let the MMAs already issued finish before TMEM is freed
-        if (last_s >= 0) mbar_wait(&bars->s_full[last_s & 1], (last_s >> 1) & 1, wc);
-        if (last_pv >= 0) mbar_wait(&bars->pv_done[last_pv & 1], (last_pv >> 1) & 1, wc);
-      }
+      __syncwarp();
     }
-    __syncwarp();
+    // leaving: the MMAs already issued finish before TMEM is freed
+    if (g > 0) wait_all(&bars->s_full[(g - 1) & 1], ((g - 1) >> 1) & 1, wc);
+  } else if (warp == 12) {
+    // ================================================================ P.V issuer
+    const bool issues = lane == 0;
+    const uint64_t dv0 = desc_mn(smem_base + kTileBytes), dp0 = desc_k(smem_base + Y::kPOff);
+    int g = 0, it_cnt = -1;
+    for (;; ++g) {
+      const int st = g % kStages, b = g & 1;
+      const uint32_t sph = (g / kStages) & 1, pph = (g >> 1) & 1;
+      // the tile's metadata (with its K)
+      if (!wait_all(&bars->k_full[st], sph, wc)) break;
+      const int flags = meta[st].flags;
+      if (flags & kMetaDone) break;
+      const bool first = flags & kMetaFirst;
+      if (first) ++it_cnt;
+      const int ob = it_cnt & 1;
+      // P and V there, and, on an item's first tile, O^T[ob], which is about to be
+      // overwritten, read by the epilogue of the item before last
+      uint64_t *const pf = &bars->p_full[b], *const vf = &bars->v_full[st];
+      uint64_t* const of = first ? &bars->o_empty[ob] : vf;
+      const uint32_t oph = first ? ((it_cnt >> 1) & 1) ^ 1 : sph;
+      if (!__all_sync(0xffffffffu, mbar_test_wait3(pf, pph, vf, sph, of, oph)) &&
+          (!wait_all(of, oph, wc) || !wait_all(pf, pph, wc) || !wait_all(vf, sph, wc)))
+        break;
+      tc_fence_after();
+      const uint64_t dv = desc_add(dv0, st * kStageBytes);
+      const uint64_t dp = desc_add(dp0, b * Y::kNP * 128);
+      const uint32_t d = tmem + Y::kOCol + ob * Y::kNP, more = first ? 0u : 1u;
+      if (issues) {
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 32; ++kk)  // 32 keys: 4 KB of V's rows, 32 bytes of the weights'
+          umma_f8(d, desc_add(dv, kk * 4096), desc_add(dp, kk * 32), Y::kIdescO, kk == 0 ? more : 1u);
+        umma_commit(&bars->kv_empty[st]);
+        if (flags & kMetaLast) umma_commit(&bars->o_full[ob]);
+      }
+      __syncwarp();
+    }
+    if (g > 0) wait_all(&bars->kv_empty[(g - 1) % kStages], ((g - 1) / kStages) & 1, wc);
   } else {
     // ================================================================ softmax / epilogue
     constexpr int kLog = NR == 4 ? 2 : NR == 8 ? 3 : 4;
@@ -578,14 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       const int my_row = lane >> (5 - kLog);  // row this lane holds after a reduction
       const bool row_writer = (lane & ((1 << (5 - kLog)) - 1)) == 0;
       const int my_block = t / p.bs;
-      float m_ref[NR], lsum[NR], unit[NR];  // unit: a row's scale times the logit scale (log2 units)
-      int vis[NR], lo[NR];
+      float m_ref[NR], lsum[NR];
+      // a row's scale times the logit scale: in registers where they do (read in every
+      // tile from shared memory: 224 us against 207 for 4 x 131072 keys)
+      constexpr bool kHeld = NR <= 8;
+      float unit[kHeld ? NR : 1];
+      int ends[NR];  // keys a row may see end here (and its window starts p.window keys earlier)
 #pragma unroll
       for (int r = 0; r < NR; ++r) {
         m_ref[r] = -CUDART_INF_F;
-        lsum[r] = unit[r] = 0.f;
-        vis[r] = lo[r] = 0;
+        lsum[r] = 0.f;
+        ends[r] = 0;
       }
+      const int window = p.window > 0 ? p.window : 1 << 30;
       Meta mt{};
       int it_cnt = -1;
       bool pending = false;
@@ -597,11 +570,13 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         const uint32_t kph = (g / kStages) & 1, ph = (g >> 1) & 1;
         // the tile's metadata (with its K), its S, and the P buffer free (P.V of
         // tile g-2 done): all three at once where they are there
+        uint64_t* const ef = g < 2 ? kf : &bars->kv_empty[(g - 2) % kStages];
+        const uint32_t eph = g < 2 ? kph : ((g - 2) / kStages) & 1;
         bool fail = pending;
-        if (!fail && !__all_sync(0xffffffffu, mbar_test_wait3(kf, kph, &bars->s_full[b], ph, &bars->pv_done[b], ph ^ 1))) {
+        if (!fail && !__all_sync(0xffffffffu, mbar_test_wait3(kf, kph, &bars->s_full[b], ph, ef, eph))) {
           fail = !wait_all(kf, kph, wc);
           if (!fail && !(meta[st].flags & kMetaDone))
-            fail = !wait_all(&bars->s_full[b], ph, wc) || !wait_all(&bars->pv_done[b], ph ^ 1, wc);
+            fail = !wait_all(&bars->s_full[b], ph, wc) || !wait_all(ef, eph, wc);
         }
         const int flags = fail ? 0 : meta[st].flags;
         const bool done = (flags & kMetaDone) != 0;
@@ -613,13 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
           for (int r = 0; r < NR; ++r) {
             m_ref[r] = -CUDART_INF_F;
             lsum[r] = 0.f;
-            unit[r] = row_scales[mt.qbuf * NR + r] * p.scale_log2;
             const int tok = (mt.row0 + r) / p.G;
-            vis[r] = r < mt.nrows ? min(mt.ke, p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
-            lo[r] = p.window > 0 ? mt.L - mt.n + tok + 1 - p.window : INT_MIN;
+            if constexpr (kHeld) unit[r] = row_scales[mt.qbuf * NR + r];
+            ends[r] = r < mt.nrows ? (p.causal ? mt.L - mt.n + tok + 1 : mt.L) : 0;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars->q_empty[mt.qbuf]);
         }
         const bool ok = !fail && !done;
         const int kbase = ok ? meta[st].kbase : 0;
@@ -661,10 +633,15 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
           mbar_arrive(&bars->s_free[b]);
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
-            const bool seen = key < vis[r] && (key >= lo[r] || key < p.num_sink);
+            const bool seen = key < min(ends[r], mt.ke) && (key >= ends[r] - window || key < p.num_sink);
             const float s = (__uint_as_float(sraw[r]) + __uint_as_float(sraw[NR + r])) * sc.k;
-            v[r] = seen ? fmaf(s, unit[r], sc.log_v) : -CUDART_INF_F;
+            const float u = kHeld ? unit[kHeld ? r : 0] : row_scales[mt.qbuf * NR + r];  // (log2 units)
+            v[r] = seen ? fmaf(s, u, sc.log_v) : -CUDART_INF_F;
             exceeds |= v[r] > m_ref[r] + kRescaleThreshold;  // false while both are -inf
+          }
+          if (flags & kMetaLast) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->q_empty[mt.qbuf]);
           }
           if (!(flags & kMetaFirst)) make_weights();
         }
@@ -711,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         if (any_rescale) {
           // O^T must hold every earlier tile's P.V before it is scaled; thread t
           // owns O^T row t (output column t), whose columns i NR + r belong to row r
-          pending = !wait_all(&bars->pv_done[b ^ 1], ((g - 1) >> 1) & 1, wc);
+          pending = !wait_all(&bars->kv_empty[(g - 1) % kStages], ((g - 1) / kStages) & 1, wc);
           if (!pending) {
             tc_fence_after();
             const uint32_t ocol = lane_base + Y::kOCol + (it_cnt & 1) * Y::kNP;
@@ -725,13 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
           }
         }
         // a tile that holds keys before every row's window (row 0's comes first)
-        const bool early = kbase < lo[0] && kbase + kKeys > p.num_sink;
+        const int lo = ends[0] - window;
+        const bool early = kbase < lo && kbase + kKeys > p.num_sink;
         if ((kbase + kKeys > mt.L || early) && !pending) {
           // keys at or past the sequence's end hold arbitrary codes, as those before
           // the windows may: zero their V rows (after the tile has landed) so that
           // 0 * V stays 0
           pending = !wait_all(&bars->v_full[st], (g / kStages) & 1, wc);
-          if (!pending && (key >= mt.L || (key < lo[0] && key >= p.num_sink))) {
+          if (!pending && (key >= mt.L || (key < lo && key >= p.num_sink))) {
             uint4* v0 = reinterpret_cast<uint4*>(smem + st * kStageBytes + kTileBytes + t * 128);
 #pragma unroll
             for (int c = 0; c < 8; ++c) v0[c] = make_uint4(0, 0, 0, 0);
