@@ -32,7 +32,7 @@
 //   warp 12    V producer: codes into a staging ring;
 //   warps 16-19 V converters, one to each scheduler (with two of them, on two
 //              schedulers, those were late with their softmax rows: their exponentials
-//              and conversions share a pipe: 249 us against TODO);
+//              and conversions share a pipe: prompt chunks 249 us against 205);
 //   warps 4-11 softmax / correction / epilogue, two threads per row;
 //   warp 14    item fetch, Q and output stores;
 //   warps 3,13,15 split the Q tile.

@@ -49,6 +49,7 @@ struct NormParams {
 
 constexpr int kWarps = 4;
 constexpr int kBatch = 2;  // heads a lane loads at a time
+constexpr int kBulkSmem = 112 * 1024;  // two CTAs an SM at least
 
 // U: the rows' element (uint16_t: bf16 bits).  F8: the pools hold E4M3 codes.
 // WIDE: a head has more places than a warp has lanes (long heads, or heads
@@ -299,6 +300,205 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
      });
 }
 
+// The same for steps of many tokens: a warp goes from token to token, whose rows
+// come to shared memory by bulk copies (a token's while the SM's other warps
+// compute), so that registers do not hold what is on its way.  Vectors only and
+// heads of at most 32 places; weights and angles wait in shared memory too.
+// 16384 tokens of 32 and 8 heads of 128 into FP8 pools move 369 MB in 85.6 us,
+// 0.64 of a copy's rate.  The instructions (sums across lanes, conversions, FP8's
+// divisions; 0.58 of a scheduler's issue slots) are what it waits for: loops
+// unrolled further, 2 and 8 warps a CTA and a rotation without its angles were
+// within 2 %, two values an instruction took 90 us to 85.6.
+template <typename U, bool F8, bool INTER>
+__global__ void __launch_bounds__(kWarps * 32) norm_rope_bulk_kernel(const NormParams p, int token_bytes) {
+  pdl_launch_dependents();  // what follows with programmatic launch reads nothing written here before it waits
+  constexpr int VEC = 16 / sizeof(U);
+  typedef Vec<U, VEC> V;
+  // [2][D] weights, [warps][half] cos and sin, [warps] rows (128-byte aligned)
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t bars[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* weights = reinterpret_cast<float*>(smem);
+  float2* trig = reinterpret_cast<float2*>(weights + 2 * p.D) + warp * p.half;
+  uint8_t* rows = smem + ((2 * p.D * 4 + kWarps * p.half * 8 + 127) & ~127) + warp * token_bytes;
+  uint64_t* bar = bars + warp;
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < 2 * p.D; i += kWarps * 32) {
+    const void* ws = i < p.D ? p.qw : p.kw;
+    const int d = i < p.D ? i : i - p.D;
+    weights[i] = !ws ? 1.f : p.weights_f32 ? static_cast<const float*>(ws)[d] : to_f(static_cast<const U*>(ws)[d]);
+  }
+  __syncthreads();
+  const int q_bytes = p.Hq * p.D * (int)sizeof(U), kv_bytes = p.Hkv * p.D * (int)sizeof(U);
+  auto fetch = [&](int64_t tok) {  // by lane 0
+    mbar_arrive_expect_tx(bar, token_bytes);
+    auto copy = [&](int at, const void* src, int64_t stride, int bytes) {
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       smem_u32(rows + at)),
+                   "l"(static_cast<const U*>(src) + tok * stride), "r"(bytes), "r"(smem_u32(bar))
+                   : "memory");
+    };
+    copy(0, p.q, p.q_stride, q_bytes);
+    copy(q_bytes, p.k, p.k_stride, kv_bytes);
+    if (p.slots) copy(q_bytes + kv_bytes, p.v, p.v_stride, kv_bytes);
+  };
+
+  const int places = (p.D / VEC + 1) / 2, rot_places = p.half / VEC, side = 32 / places, y = lane / places;
+  const bool idle = y >= side;  // lanes left over
+  const int x = idle ? 0 : lane - y * places;
+  const bool rot = x < rot_places;
+  const int ca = rot ? (INTER ? 2 * x * VEC : x * VEC) : 2 * p.half + 2 * (x - rot_places) * VEC;
+  const int cb = rot && !INTER ? p.half + x * VEC : ca + VEC;
+  const bool two = cb + VEC <= p.D;
+  const float inv_d = 1.f / (float)p.D;
+  auto head_sum = [&](float s) {  // over the lanes of a head
+    if ((places & (places - 1)) == 0) {
+      for (int o = places >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      return s;
+    }
+    float t = 0.f;
+    const int first = min(y, side - 1) * places;
+    for (int i = 0; i < places; ++i) t += __shfl_sync(0xffffffffu, s, first + i);
+    return t;
+  };
+
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t tok = (int64_t)blockIdx.x * kWarps + warp;
+  if (tok < p.T && lane == 0) fetch(tok);
+  int64_t pos = tok < p.T ? p.positions[tok] : 0, slot = tok < p.T && p.slots ? p.slots[tok] : -1;
+  for (uint32_t phase = 0; tok < p.T; phase ^= 1) {
+    if (p.slots && slot >= p.num_slots) {
+      if (lane == 0) raise_error(p.err, PKV_DEVERR_SLOT_OUT_OF_RANGE);
+      slot = -1;
+    }
+    for (int j = lane; j < p.half; j += 32) trig[j] = turn_of(angle_of(pos, p.inv_freq[j]), p.amp);
+    const int64_t next = tok + step, at = slot * p.Hkv * (int64_t)p.D;
+    if (next < p.T) pos = p.positions[next];
+    const int64_t next_slot = next < p.T && p.slots ? p.slots[next] : -1;
+    __syncwarp();
+    if (!__all_sync(0xffffffffu, mbar_wait(bar, phase, p.err))) {  // (a copy that takes 2 s: reported)
+      mbar_wait(bar, phase, p.err);
+      break;
+    }
+    // A tensor's heads (`from` of the token's bytes on): put(head, values of columns ca .., of cb ..)
+    auto go = [&](int from, int heads, const float* ws, auto put) {
+      const U* src = reinterpret_cast<const U*>(rows + from);
+      // y1 = r (f0 x1 - f1 x2), y2 = r (f2 x2 + f3 x1) of each pair, two values an
+      // instruction; past the rotary part f1 = f3 = 0.  Interleaved, c holds (f0, f2)
+      // and d (-f1, f3) of each pair; else c, d are (f0 f0'), (-f1 -f1') of two
+      // pairs and c2, d2 their (f2 f2'), (f3 f3').
+      f32x2 c[VEC], d[VEC];  // (c2, d2: the second halves)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        // the pair's two elements: (ca + e, cb + e), or, interleaved, (ca + 2e, ca + 2e + 1)
+        const float w1 = INTER ? (two || 2 * e < VEC ? ws[ca + 2 * e] : 0.f) : ws[ca + e];
+        const float w2 = INTER ? (two || 2 * e < VEC ? ws[ca + 2 * e + 1] : 0.f) : two ? ws[cb + e] : 0.f;
+        const float2 cs = rot ? trig[x * VEC + e] : make_float2(1.f, 0.f);
+        if constexpr (INTER) {
+          c[e] = pk2(cs.x * w1, cs.x * w2);
+          d[e] = pk2(-cs.y * w2, cs.y * w1);
+        } else {
+          const int k = e >> 1;
+          auto set = [&](f32x2& v, float f) {
+            const float2 o = up2(v);
+            v = e & 1 ? pk2(o.x, f) : pk2(f, 0.f);
+          };
+          set(c[k], cs.x * w1);
+          set(d[k], -cs.y * w2);
+          set(c[VEC / 2 + k], cs.x * w2);
+          set(d[VEC / 2 + k], cs.y * w1);
+        }
+      }
+      for (int base = 0; base < heads; base += side) {  // the same for every lane
+        const int h = base + y;
+        const bool live = !idle && h < heads;
+        V a{}, b{};
+        if (live) {
+          a = *reinterpret_cast<const V*>(src + h * p.D + ca);
+          if (two) b = *reinterpret_cast<const V*>(src + h * p.D + cb);
+        }
+        f32x2 xa[VEC / 2], xb[VEC / 2], s2 = pk2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          xa[k] = pk2(to_f(a.e[2 * k]), to_f(a.e[2 * k + 1]));
+          xb[k] = pk2(to_f(b.e[2 * k]), to_f(b.e[2 * k + 1]));
+          s2 = fma2(xa[k], xa[k], s2);
+          s2 = fma2(xb[k], xb[k], s2);
+        }
+        const float2 s = up2(s2);
+        const float r = rsqrtf(fmaf(head_sum(s.x + s.y), inv_d, p.eps));
+        const f32x2 r2 = pk2(r, r);
+        float ya[VEC], yb[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+          f32x2 u, v;
+          if constexpr (INTER) {  // pairs are xa's, then xb's
+            auto swapped = [](f32x2 z) {
+              const float2 o = up2(z);
+              return pk2(o.y, o.x);
+            };
+            u = fma2(xa[k], c[k], mul2(swapped(xa[k]), d[k]));
+            v = fma2(xb[k], c[VEC / 2 + k], mul2(swapped(xb[k]), d[VEC / 2 + k]));
+          } else {
+            u = fma2(xa[k], c[k], mul2(xb[k], d[k]));
+            v = fma2(xb[k], c[VEC / 2 + k], mul2(xa[k], d[VEC / 2 + k]));
+          }
+          const float2 ua = up2(mul2(u, r2)), vb = up2(mul2(v, r2));
+          ya[2 * k] = ua.x;
+          ya[2 * k + 1] = ua.y;
+          yb[2 * k] = vb.x;
+          yb[2 * k + 1] = vb.y;
+        }
+        if (live) put(h, ya, yb);
+      }
+    };
+    U* qo = static_cast<U*>(p.q_out) + tok * p.Hq * (int64_t)p.D;
+    go(0, p.Hq, weights, [&](int h, const float (&ya)[VEC], const float (&yb)[VEC]) {
+      store_rows<U, VEC>(qo + h * p.D + ca, ya);
+      if (two) store_rows<U, VEC>(qo + h * p.D + cb, yb);
+    });
+    if (slot >= 0 || p.k_out) {
+      U* ko = p.k_out ? static_cast<U*>(p.k_out) + tok * p.Hkv * (int64_t)p.D : nullptr;
+      go(q_bytes, p.Hkv, weights + p.D, [&](int h, const float (&ya)[VEC], const float (&yb)[VEC]) {
+        if (ko) {
+          store_rows<U, VEC>(ko + h * p.D + ca, ya);
+          if (two) store_rows<U, VEC>(ko + h * p.D + cb, yb);
+        }
+        if (slot < 0) return;
+        const int64_t to = at + h * p.D;
+        if constexpr (F8) {
+          store_codes<VEC>(static_cast<uint8_t*>(p.kc) + to + ca, ya, p.k_scale);
+          if (two) store_codes<VEC>(static_cast<uint8_t*>(p.kc) + to + cb, yb, p.k_scale);
+        } else {
+          store_rows<U, VEC>(static_cast<U*>(p.kc) + to + ca, ya);
+          if (two) store_rows<U, VEC>(static_cast<U*>(p.kc) + to + cb, yb);
+        }
+      });
+    }
+    if (slot >= 0) {
+      const V* src = reinterpret_cast<const V*>(rows + q_bytes + kv_bytes);
+      for (int i = lane; i < p.Hkv * p.D / VEC; i += 32) {
+        const V a = src[i];
+        if constexpr (F8) {
+          float xa[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) xa[e] = to_f(a.e[e]);
+          store_codes<VEC>(static_cast<uint8_t*>(p.vc) + at + i * VEC, xa, p.v_scale);
+        } else {
+          *reinterpret_cast<V*>(static_cast<U*>(p.vc) + at + i * VEC) = a;
+        }
+      }
+    }
+    __syncwarp();  // the rows and the angles are read
+    tok = next;
+    slot = next_slot;
+    if (tok < p.T && lane == 0) fetch(tok);
+  }
+}
+
 pkv_status fail(pkv_status st, const char* msg) {
   set_last_error(msg);
   return st;
@@ -313,6 +513,27 @@ cudaError_t launch_w(const NormParams& p, dim3 grid, size_t smem, cudaStream_t s
   return cudaGetLastError();
 }
 
+template <typename U, bool F8, bool INTER>
+cudaError_t launch_bulk(const NormParams& p, int token_bytes, size_t smem, int sms, cudaStream_t s) {
+  static unsigned long long done_mask = 0;
+  int dev = 0, ctas = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  auto kernel = norm_rope_bulk_kernel<U, F8, INTER>;
+  if (!(__atomic_load_n(&done_mask, __ATOMIC_ACQUIRE) & (1ull << dev))) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkSmem);
+    if (e != cudaSuccess) return e;
+    __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
+  }
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, kWarps * 32, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = (p.T + kWarps - 1) / kWarps;
+  const int grid = (int)std::min<int64_t>(most, (int64_t)sms * std::max(ctas, 1));
+  kernel<<<grid, kWarps * 32, smem, s>>>(p, token_bytes);
+  return cudaGetLastError();
+}
+
 template <typename U, bool F8>
 cudaError_t launch(const NormParams& p0, bool vec, int sms, cudaStream_t s) {
   NormParams p = p0;
@@ -323,6 +544,14 @@ cudaError_t launch(const NormParams& p0, bool vec, int sms, cudaStream_t s) {
   const int most = (std::max(p.Hq, p.Hkv) + side - 1) / side;
   p.splits = 1;
   while (p.T * p.splits < (int64_t)sms * 8 && p.splits < most) p.splits *= 2;
+  // tokens enough for every warp to take whole ones: their rows by bulk copies,
+  // where four of them fit (32 and 8 heads of 128: 4216 tokens 36.5 us with a token's
+  // loads by its lanes, 28.1 so; 16384 tokens into FP8 pools 122 and 85.6 us)
+  const int64_t token = ((int64_t)p.Hq + (p.slots ? 2 : 1) * p.Hkv) * p.D * (int64_t)sizeof(U);
+  const int64_t bulk = (((int64_t)2 * p.D * 4 + kWarps * p.half * 8 + 127) & ~127) + kWarps * token;
+  if (p.splits == 1 && vec && places <= 32 && bulk <= kBulkSmem)
+    return p.interleaved ? launch_bulk<U, F8, true>(p, (int)token, (size_t)bulk, sms, s)
+                         : launch_bulk<U, F8, false>(p, (int)token, (size_t)bulk, sms, s);
   const dim3 grid((unsigned)((p.T * p.splits + kWarps - 1) / kWarps));
   const size_t smem = (size_t)kWarps * p.half * sizeof(float2);
   if (places > 32) return vec ? launch_w<U, kV, F8, true>(p, grid, smem, s) : launch_w<U, 1, F8, true>(p, grid, smem, s);
