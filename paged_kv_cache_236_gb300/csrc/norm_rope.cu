@@ -159,14 +159,14 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
     }
   };
   auto squares = [&](const V& a, const V& b, bool two) {
-    float s = 0.f;
+    float s[2] = {};  // the order of norm_rope_bulk_kernel: a row's bits do not depend on the step it comes in
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float x1 = to_f(a.e[e]), x2 = two ? to_f(b.e[e]) : 0.f;
-      s = fmaf(x1, x1, s);
-      s = fmaf(x2, x2, s);
+      s[e & 1] = fmaf(x1, x1, s[e & 1]);
+      s[e & 1] = fmaf(x2, x2, s[e & 1]);
     }
-    return s;
+    return s[0] + s[1];
   };
   // sum over the lanes of a head (all the warp's lanes call it)
   auto head_sum = [&](float s) {
