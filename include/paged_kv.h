@@ -488,8 +488,8 @@ pkv_status pkv_capture_gone(uint64_t* id);
 /*
  * pkv_debug_fault - testing hook for the bounded in-kernel waits (no
  * counterpart on the source pages).  Arms the next paged_attention_forward /
- * _fp8kv or paged_attention_scores / _fp8kv call made on this thread, and
- * only that call:
+ * _fp8kv / _fp8block, paged_attention_window_forward or paged_attention_scores /
+ * _fp8kv call made on this thread, and only that call:
  *   wait_ns     > 0: every bounded wait of its kernels gives up after wait_ns
  *               nanoseconds instead of 2 s;
  *   fault_tile  > 0: in the first CTA of its decode-shaped attention kernel

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
     if (lane == 0) prefetch_tensormap(vprod ? &vmap : &kmap);
     uint64_t* fullb = vprod ? bars->v_full : bars->k_full;
     int g = 0;
-    // leaving early: the copies of the tiles issued last land first
+    // leaving: the copies of the tiles issued last land first, whoever still waits for them
     auto drain = [&]() {
       for (int j = max(0, g - kStages); j < g; ++j)
         __all_sync(0xffffffffu, mbar_wait(&fullb[j % kStages], (j / kStages) & 1, wc));
@@ -271,12 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->islot_free[qb]);
       if (done) {
-        if (vprod) break;
+        if (vprod) {
+          drain();
+          break;
+        }
         const int st = g % kStages;
         if (!wait_all(&bars->kv_empty[st], ((g / kStages) & 1) ^ 1, wc)) {
           drain();
           break;
         }
+        drain();  // (before the arrival below, another phase of a barrier waited for)
         if (lane == 0) {
           meta[st].item = -1;
           meta[st].flags = kMetaDone;

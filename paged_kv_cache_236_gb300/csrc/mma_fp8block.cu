@@ -474,9 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           sc = nsc;
         }
       }
-      if (!ok) {  // leaving early: the copies of the tiles issued last land first
-        for (int j = max(0, g - nst); j < g; ++j) __all_sync(0xffffffffu, mbar_wait(&fullb[j % nst], (j / nst) & 1, wc));
-      }
+      // leaving: the copies of the tiles issued last land first, whoever still waits for them
+      for (int j = max(0, g - nst); j < g; ++j) __all_sync(0xffffffffu, mbar_wait(&fullb[j % nst], (j / nst) & 1, wc));
     } else if (warp >= 16) {
       // ================================================================ V converters
       // Codes (rows of 128 bytes, chunk j at j ^ (key & 7)) become an fp16 tile of
