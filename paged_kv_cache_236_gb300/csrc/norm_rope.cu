@@ -43,7 +43,8 @@ struct NormParams {
   int64_t T, num_slots, q_stride, k_stride, v_stride;  // strides in elements
   int Hq, Hkv, D, half;
   int interleaved, weights_f32, splits;
-  float eps, amp, k_scale, v_scale;
+  float eps, amp;
+  CodeScale k_scale, v_scale;  // of FP8 pools
   int* err;
 };
 
@@ -304,11 +305,11 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
 // come to shared memory by bulk copies (a token's while the SM's other warps
 // compute), so that registers do not hold what is on its way.  Vectors only and
 // heads of at most 32 places; weights and angles wait in shared memory too.
-// 16384 tokens of 32 and 8 heads of 128 into FP8 pools move 369 MB in 85.6 us,
-// 0.64 of a copy's rate.  The instructions (sums across lanes, conversions, FP8's
-// divisions; 0.58 of a scheduler's issue slots) are what it waits for: loops
-// unrolled further, 2 and 8 warps a CTA and a rotation without its angles were
-// within 2 %, two values an instruction took 90 us to 85.6.
+// 16384 tokens of 32 and 8 heads of 128 into FP8 pools move 369 MB in 74.3 us,
+// 0.73 of a copy's rate.  The instructions (sums across lanes, conversions; 0.58 of
+// a scheduler's issue slots) are what it waits for: loops unrolled further, 2 and 8
+// warps a CTA and a rotation without its angles were within 2 %, two values an
+// instruction took 90 us to 85.6, codes without a division to 74.3.
 template <typename U, bool F8, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_bulk_kernel(const NormParams p, int token_bytes) {
   pdl_launch_dependents();  // what follows with programmatic launch reads nothing written here before it waits
@@ -546,7 +547,7 @@ cudaError_t launch(const NormParams& p0, bool vec, int sms, cudaStream_t s) {
   while (p.T * p.splits < (int64_t)sms * 8 && p.splits < most) p.splits *= 2;
   // tokens enough for every warp to take whole ones: their rows by bulk copies,
   // where four of them fit (32 and 8 heads of 128: 4216 tokens 36.5 us with a token's
-  // loads by its lanes, 28.1 so; 16384 tokens into FP8 pools 122 and 85.6 us)
+  // loads by its lanes, 28.1 so; 16384 tokens into FP8 pools 122 and 74.3 us)
   const int64_t token = ((int64_t)p.Hq + (p.slots ? 2 : 1) * p.Hkv) * p.D * (int64_t)sizeof(U);
   const int64_t bulk = (((int64_t)2 * p.D * 4 + kWarps * p.half * 8 + 127) & ~127) + kWarps * token;
   if (p.splits == 1 && vec && places <= 32 && bulk <= kBulkSmem)
@@ -575,7 +576,7 @@ pkv_status norm_rope(NormParams p, int64_t num_blocks, int block_size, int rotar
   if (row > (1 << 24) || row_q > (1 << 24)) return fail(PKV_ERR_UNSUPPORTED, "heads * head_dim too large");
   if (!(p.eps > 0.f) || !isfinite(p.eps)) return fail(PKV_ERR_INVALID_ARG, "eps must be positive and finite");
   if (!(p.amp > 0.f) || !isfinite(p.amp)) return fail(PKV_ERR_INVALID_ARG, "amplitude must be positive and finite");
-  if (f8 && (!(p.k_scale > 0.f) || !isfinite(p.k_scale) || !(p.v_scale > 0.f) || !isfinite(p.v_scale)))
+  if (f8 && (!(p.k_scale.value > 0.f) || !isfinite(p.k_scale.value) || !(p.v_scale.value > 0.f) || !isfinite(p.v_scale.value)))
     return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
   if (p.q_stride == 0) p.q_stride = row_q;
   if (p.k_stride == 0) p.k_stride = row;
@@ -601,6 +602,8 @@ pkv_status norm_rope(NormParams p, int64_t num_blocks, int block_size, int rotar
   p.half = rotary / 2;
   p.weights_f32 = weight_dtype == PKV_DTYPE_F32 ? 1 : 0;
   p.num_slots = num_blocks * block_size;
+  p.k_scale = code_scale(p.k_scale.value);
+  p.v_scale = code_scale(p.v_scale.value);
   // 16-byte vectors where every row, every head and the rotary halves allow them
   const int V = (int)(16 / es);
   const bool vec = p.D % V == 0 && p.half % V == 0 && p.q_stride % V == 0 && p.k_stride % V == 0 &&
@@ -631,7 +634,7 @@ pkv_status paged_kv_write_norm_rope(const void* q, const void* k, const void* v,
                                     pkv_dtype weight_dtype, void* stream) {
   pkv::NormParams p{q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, q_out, k_out, k_cache, v_cache,
                     num_tokens, 0, q_token_stride, k_token_stride, v_token_stride, num_q_heads, num_kv_heads,
-                    head_dim, 0, interleaved ? 1 : 0, 0, 0, eps, amplitude, 1.f, 1.f, nullptr};
+                    head_dim, 0, interleaved ? 1 : 0, 0, 0, eps, amplitude, {1.f}, {1.f}, nullptr};
   return pkv::norm_rope(p, num_blocks, block_size, rotary_dim, dtype, weight_dtype, false, stream);
 }
 
@@ -646,7 +649,7 @@ pkv_status paged_kv_write_norm_rope_fp8(const void* q, const void* k, const void
                                         void* stream) {
   pkv::NormParams p{q, k, v, q_weight, k_weight, positions, inv_freq, slot_mapping, q_out, k_out, k_cache, v_cache,
                     num_tokens, 0, q_token_stride, k_token_stride, v_token_stride, num_q_heads, num_kv_heads,
-                    head_dim, 0, interleaved ? 1 : 0, 0, 0, eps, amplitude, k_scale, v_scale, nullptr};
+                    head_dim, 0, interleaved ? 1 : 0, 0, 0, eps, amplitude, {k_scale}, {v_scale}, nullptr};
   return pkv::norm_rope(p, num_blocks, block_size, rotary_dim, dtype, weight_dtype, true, stream);
 }
 

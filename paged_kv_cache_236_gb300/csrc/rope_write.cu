@@ -56,7 +56,8 @@ struct RopeParams {
   int64_t T, num_slots, q_stride, k_stride, v_stride;  // strides in elements
   int Hq, Hkv, D, half;  // half: pairs per head (rotary / 2)
   int interleaved, splits;  // splits: warps that share a token's heads
-  float amp, k_scale, v_scale;
+  float amp;
+  CodeScale k_scale, v_scale;  // of FP8 pools
   int* err;
 };
 
@@ -249,7 +250,7 @@ pkv_status rope_write(RopeParams p, int64_t num_blocks, int block_size, int rota
   const int64_t row_q = (int64_t)p.Hq * p.D, row = (int64_t)p.Hkv * p.D;
   if (row > (1 << 24) || row_q > (1 << 24)) return fail(PKV_ERR_UNSUPPORTED, "heads * head_dim too large");
   if (!(p.amp > 0.f) || !isfinite(p.amp)) return fail(PKV_ERR_INVALID_ARG, "amplitude must be positive and finite");
-  if (f8 && (!(p.k_scale > 0.f) || !isfinite(p.k_scale) || !(p.v_scale > 0.f) || !isfinite(p.v_scale)))
+  if (f8 && (!(p.k_scale.value > 0.f) || !isfinite(p.k_scale.value) || !(p.v_scale.value > 0.f) || !isfinite(p.v_scale.value)))
     return fail(PKV_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
   if (p.q_stride == 0) p.q_stride = row_q;
   if (p.k_stride == 0) p.k_stride = row;
@@ -270,6 +271,8 @@ pkv_status rope_write(RopeParams p, int64_t num_blocks, int block_size, int rota
   if (st != PKV_OK) return st;
   p.half = rotary / 2;
   p.num_slots = num_blocks * block_size;
+  p.k_scale = code_scale(p.k_scale.value);
+  p.v_scale = code_scale(p.v_scale.value);
   // 16-byte vectors where every row, every head and the rotary halves allow them
   const int V = (int)(16 / es);
   const bool vec = p.D % V == 0 && p.half % V == 0 && p.q_stride % V == 0 && p.k_stride % V == 0 &&
@@ -297,7 +300,7 @@ pkv_status paged_kv_write_rope(const void* q, const void* k, const void* v, cons
                                int64_t v_token_stride, pkv_dtype dtype, void* stream) {
   pkv::RopeParams p{q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, num_tokens, 0,
                     q_token_stride, k_token_stride, v_token_stride, num_q_heads, num_kv_heads, head_dim, 0,
-                    interleaved ? 1 : 0, 0, amplitude, 1.f, 1.f, nullptr};
+                    interleaved ? 1 : 0, 0, amplitude, {1.f}, {1.f}, nullptr};
   return pkv::rope_write(p, num_blocks, block_size, rotary_dim, dtype, false, stream);
 }
 
@@ -310,7 +313,7 @@ pkv_status paged_kv_write_rope_fp8(const void* q, const void* k, const void* v, 
                                    float v_scale, void* stream) {
   pkv::RopeParams p{q, k, v, positions, inv_freq, slot_mapping, q_out, k_cache, v_cache, num_tokens, 0,
                     q_token_stride, k_token_stride, v_token_stride, num_q_heads, num_kv_heads, head_dim, 0,
-                    interleaved ? 1 : 0, 0, amplitude, k_scale, v_scale, nullptr};
+                    interleaved ? 1 : 0, 0, amplitude, {k_scale}, {v_scale}, nullptr};
   return pkv::rope_write(p, num_blocks, block_size, rotary_dim, dtype, true, stream);
 }
 
