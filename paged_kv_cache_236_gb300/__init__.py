@@ -198,13 +198,15 @@ def _stream(device: torch.device) -> int:
 
 
 def _need_cuda(*tensors: torch.Tensor) -> torch.device:
-    dev = tensors[0].device
+    index = -1
     for t in tensors:
-        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        i = t.get_device() if isinstance(t, torch.Tensor) else -1  # (a microsecond less than its device)
+        if i < 0:
             raise ValueError("all tensors must be CUDA tensors (no CPU path)")
-        if t.device != dev:
+        if index >= 0 and i != index:
             raise ValueError("all tensors must be on the same device")
-    return dev
+        index = i
+    return tensors[0].device
 
 
 def paged_kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -362,8 +364,7 @@ def paged_attention_window_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cac
     seen = _window(window, num_sink, 1)
     args, out, workspace = _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
                                          True, out, workspace, max_query_len, False, dev)
-    with torch.cuda.device(dev):
-        _check(lib().paged_attention_window_forward(*args[:17], *seen, *args[19:]))
+    _check(_on(dev.index, lib().paged_attention_window_forward, *args[:17], *seen, *args[19:]))
     return out
 
 
@@ -395,10 +396,10 @@ def _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_l
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must match q")
-    with torch.cuda.device(dev):
+    if workspace is None:
+        workspace = _on(dev.index, _workspace, dev, workspace_size(B, T, Hq, Hkv, D))
+    else:
         need = workspace_min(B, T, Hq, Hkv, D)
-        if workspace is None:
-            workspace = _workspace(dev, workspace_size(B, T, Hq, Hkv, D))
         if workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
             raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
@@ -778,10 +779,10 @@ def _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_sta
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must match q")
-    with torch.cuda.device(dev):
+    if workspace is None:
+        workspace = _on(dev.index, _workspace, dev, workspace_size(B, T, Hq, Hkv, D))
+    else:
         need = workspace_min(B, T, Hq, Hkv, D)
-        if workspace is None:
-            workspace = _workspace(dev, workspace_size(B, T, Hq, Hkv, D))
         if workspace.dtype != torch.uint8 or workspace.device != dev or workspace.numel() < need:
             raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
@@ -863,9 +864,9 @@ def _device_of(*tensors: torch.Tensor) -> int:
     for t in tensors:
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        i = t.get_device() if isinstance(t, torch.Tensor) else -1
+        if i < 0:
             raise ValueError("all tensors must be CUDA tensors (no CPU path)")
-        i = t.get_device()
         if dev < 0:
             dev = i
         elif i != dev:
@@ -967,62 +968,63 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mappi
                     interleaved, amplitude, q_out, k_out, dev):
     """Checks paged_kv_write_norm_rope's tensors; returns (its C arguments up
     to the weights' dtype, q_out)."""
-    shape, dtype = q.shape, q.dtype
+    shape, rows, dtype = q.shape, k.shape, q.dtype
     if dtype not in DTYPE or k.dtype != dtype:
         raise ValueError("q, k and v must share dtype bfloat16 or float32")
-    if len(shape) != 3 or k.dim() != 3:
+    if len(shape) != 3 or len(rows) != 3:
         raise ValueError("q and k must be [T, heads, D]")
     T, Hq, D = shape
-    Hkv = k.shape[1]
+    Hkv = rows[1]
+    qs, ks = q.stride(), k.stride()
+    if rows[0] != T or rows[2] != D or qs[2] != 1 or qs[1] != D or ks[2] != 1 or ks[1] != D:
+        raise ValueError(f"q and k must be [{T}, heads, {D}] of one dtype with contiguous heads")
     NB = bs = 0
-    pools = (slot_mapping, k_cache, v_cache)
-    if all(t is None for t in pools):
+    strides = (qs[0], ks[0])
+    if slot_mapping is None and k_cache is None and v_cache is None:
         if k_out is None:
             raise ValueError("without pools, k_out must be given")
         v = None
-    elif v is None or any(t is None for t in pools):
+    elif v is None or slot_mapping is None or k_cache is None or v_cache is None:
         raise ValueError("v, slot_mapping, k_cache and v_cache go together")
     else:
-        if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() or \
-                not v_cache.is_contiguous() or tuple(k_cache.shape[2:]) != (Hkv, D):
+        pool, vs = k_cache.shape, v.stride()
+        if len(pool) != 4 or pool[2] != Hkv or pool[3] != D or v_cache.shape != pool or \
+                not k_cache.is_contiguous() or not v_cache.is_contiguous():
             raise ValueError(f"caches must be contiguous [num_blocks, block_size, {Hkv}, {D}]")
-        NB, bs = k_cache.shape[:2]
+        NB, bs = pool[0], pool[1]
+        if v.shape != rows or v.dtype != dtype or vs[2] != 1 or vs[1] != D:
+            raise ValueError(f"v must be {list(rows)} of q's dtype with contiguous heads")
         if slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():
             raise ValueError("slot_mapping must be contiguous int64 [T]")
-    strides = []
-    for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if t is None:
-            strides.append(0)
-            continue
-        st = t.stride()
-        if t.dtype != dtype or t.shape != (T, heads, D) or st[2] != 1 or st[1] != D:
-            raise ValueError(f"{name} must be {[T, heads, D]} of q's dtype with contiguous heads")
-        if T > 1 and st[0] == 0:  # the C call takes a stride of 0 for dense
-            raise ValueError("q, k and v must not repeat one token's row (a token stride of 0)")
-        strides.append(st[0] if T > 1 else 0)
-    wdtype = dtype
+        strides += (vs[0],)
+    if T > 1 and 0 in strides:  # the C call takes a stride of 0 for dense
+        raise ValueError("q, k and v must not repeat one token's row (a token stride of 0)")
+    strides = (strides + (0,))[:3] if T > 1 else (0, 0, 0)
+    wdtype = None
     for w in (q_weight, k_weight):
         if w is None:
             continue
         if w.shape != (D,) or not w.is_contiguous() or w.dtype not in (dtype, torch.float32):
             raise ValueError(f"weights must be contiguous [{D}] of q's dtype or float32")
+        if wdtype is not None and w.dtype != wdtype:
+            raise ValueError("q_weight and k_weight must share a dtype")
         wdtype = w.dtype
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError("q_weight and k_weight must share a dtype")
     if positions.shape != (T,) or positions.dtype != torch.int64 or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int64 [T]")
     if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous() or \
             not 0 < 2 * inv_freq.shape[0] <= D:
         raise ValueError("inv_freq must be contiguous float64 [rotary_dim / 2] with rotary_dim <= head_dim")
     if q_out is None:
-        q_out = torch.empty(shape, dtype=dtype, device=q.device)
-    for name, t, want in (("q_out", q_out, shape), ("k_out", k_out, k.shape)):
-        if t is not None and (t.shape != want or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev):
-            raise ValueError(f"{name} must be contiguous and match {name[0]}")
+        q_out = q.new_empty(shape)
+    elif q_out.shape != shape or q_out.dtype != dtype or not q_out.is_contiguous() or q_out.get_device() != dev:
+        raise ValueError("q_out must be contiguous and match q")
+    if k_out is not None and (k_out.shape != rows or k_out.dtype != dtype or not k_out.is_contiguous()):
+        raise ValueError("k_out must be contiguous and match k")
     at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     args = (q.data_ptr(), k.data_ptr(), at(v), at(q_weight), at(k_weight), positions.data_ptr(), inv_freq.data_ptr(),
             at(slot_mapping), q_out.data_ptr(), at(k_out), at(k_cache), at(v_cache), T, NB, bs, Hq, Hkv, D,
-            2 * inv_freq.shape[0], 1 if interleaved else 0, eps, amplitude, *strides, DTYPE[dtype], DTYPE[wdtype])
+            2 * inv_freq.shape[0], 1 if interleaved else 0, eps, amplitude, *strides, DTYPE[dtype],
+            DTYPE[wdtype or dtype])
     return args, q_out
 
 
@@ -1303,7 +1305,6 @@ def paged_attention_forward_fp8block(q: torch.Tensor, k_cache: torch.Tensor, v_c
     seen = _window(window, num_sink, 0)
     args, out, workspace = _fp8_forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
                                              1.0, 1.0, causal, out, workspace, max_query_len, dev)
-    with torch.cuda.device(dev):
-        _check(lib().paged_attention_forward_fp8block(*args[:3], k_scales.data_ptr(), v_scales.data_ptr(), *args[3:18],
-                                                      *seen, *args[21:]))
+    _check(_on(dev.index, lib().paged_attention_forward_fp8block, *args[:3], k_scales.data_ptr(), v_scales.data_ptr(),
+               *args[3:18], *seen, *args[21:]))
     return out
