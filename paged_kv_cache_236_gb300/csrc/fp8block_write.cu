@@ -19,10 +19,13 @@
 // flight before the maximum, the rows stay in registers until they are encoded.
 //
 // HBM-bound for prompts (rows in once, codes out once): 16384 tokens of 8 heads of
-// 128 in bf16 39.6 us, of which the table's launch and the leaders' three dependent
-// reads are a third (with 8-byte loads 46 us, without the rows' prefetch 53, with one
-// CTA of 512 threads an SM 70).  A decode step is a launch and four dependent reads
-// (slot, old scale, rows, codes of a block that grows): 12.5 us with the call.
+// 128 in bf16 25.9 us, of which the table's launch (4 us) and the leaders' three
+// dependent reads are a third (without the rows' prefetch 2.3 us more).  Its
+// instructions came next: 25 of a warp to each 32 elements held it at 39.6 us before a
+// lane kept its column, maxima were taken two at a time and block sizes shifts.  A
+// decode step is a launch and four dependent reads (slot, old scale, rows, codes of a
+// block that grows): 12.3 us with the call.
+#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -36,8 +39,10 @@ namespace pkv {
 namespace {
 
 constexpr int kScanTokens = 512;
-constexpr int kMaxWarps = 16;
-constexpr int kGroup = 16;  // tokens of a CTA past kScanTokens
+// (16384 tokens: 8 warps with 8 tokens 25.9 us, with 16 27.2, with 32 33; 16 warps
+// 33.4, which leaves a thread too few registers, 4 warps 28.8)
+constexpr int kMaxWarps = 8;
+constexpr int kGroup = 8;  // tokens of a CTA past kScanTokens
 constexpr int kMaxBlock = 64;
 constexpr int kHold = 8;    // 8-element pieces of a block's rows that a lane keeps in registers
 
@@ -51,7 +56,7 @@ struct WriteParams {
   float* vs;
   int* token_of;  // [num_slots], or NULL: scan
   int64_t T, num_slots, k_stride, v_stride;  // strides in elements
-  int bs, Hkv, D;
+  int bs, log_bs, Hkv, D;
   int* err;
 };
 
@@ -86,6 +91,16 @@ struct Raw8<uint16_t> {
       x[2 * i + 1] = bf16_hi(in[i]);
     }
   }
+  // the largest |x|, a NaN left out: two at a time
+  struct Top {
+    __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);
+    __device__ __forceinline__ void add(const Raw8& r) {
+      const uint32_t in[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&in[i])));
+    }
+    __device__ __forceinline__ float value() const { return fmaxf(__low2float(m), __high2float(m)); }
+  };
 };
 template <>
 struct Raw8<float> {
@@ -103,15 +118,26 @@ struct Raw8<float> {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
+  struct Top {
+    float m = 0.f;
+    __device__ __forceinline__ void add(const Raw8& r) {
+      float x[8];
+      r.get(x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+    }
+    __device__ __forceinline__ float value() const { return m; }
+  };
 };
 
 // Codes of eight values times `by`, and the values of eight codes.
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float by) {
   uint32_t c[4];
+  const f32x2 by2 = pk2(by, by);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    c[i] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * by, x[2 * i + 1] * by), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
-  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    c[i] = __nv_cvt_float2_to_fp8x2(up2(mul2(pk2(x[2 * i], x[2 * i + 1]), by2)), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(__byte_perm(c[0], c[1], 0x5410), __byte_perm(c[2], c[3], 0x5410));
 }
 __device__ __forceinline__ void values8(uint2 c, float (&x)[8]) {
   const uint32_t in[2] = {c.x, c.y};
@@ -134,11 +160,11 @@ __device__ __forceinline__ int need_exponent(float top) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 // One (head, K or V) of a block, by a warp.  members[o]: the token that writes
-// offset o, or -1; n_rows of them, their offsets in row_at.
-// PIECES: 8-element pieces of a row (head_dim / 8) where that is 8 or 16, so that
-// a piece's row and column are shifts; 0: any number.
+// offset o, or -1; rows[r], r < n_rows: those tokens and their offsets.
+// PIECES: 8-element pieces of a row (head_dim / 8) where that is 8 or 16 and
+// rows allow 16-byte loads, so that a lane keeps its column; 0: any.
 template <typename U, int PIECES>
-__device__ __forceinline__ void write_unit(const WriteParams& p, int64_t block, const int* members, const uint8_t* row_at,
+__device__ __forceinline__ void write_unit(const WriteParams& p, int64_t block, const int* members, const int2* rows,
                                            int n_rows, int h, bool is_v, bool vec, int lane) {
   const U* src = static_cast<const U*>(is_v ? p.v : p.k) + (int64_t)h * p.D;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
@@ -147,71 +173,64 @@ __device__ __forceinline__ void write_unit(const WriteParams& p, int64_t block, 
   float* scale_at = (is_v ? p.vs : p.ks) + block * p.Hkv + h;
   const bool begins = members[0] >= 0;
   const float held = begins ? 0.f : *scale_at;
-  const int pieces = PIECES ? PIECES : p.D / 8, total = n_rows * pieces;
-  // piece i of the rows: of row i / pieces, elements 8 (i % pieces) ..
-  auto load = [&](int i, Raw8<U>& x) {
-    const int r = i / pieces;
-    x.load(src + members[row_at[r]] * stride + 8 * (i - r * pieces), vec);
-  };
-  auto top_of = [](const Raw8<U>& raw, float top) {
-    float x[8];
-    raw.get(x);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-    return top;
-  };
+  const int pieces = PIECES ? PIECES : p.D / 8;
+  // the lane's j-th piece: of row row_of(j), elements col_of(j) ..
+  constexpr int kStep = PIECES ? 32 / PIECES : 1;
+  const int r0 = lane / pieces, c0 = 8 * (lane - r0 * pieces);
+  auto row_of = [&](int j) { return PIECES ? r0 + kStep * j : (lane + 32 * j) / pieces; };
+  auto col_of = [&](int j) { return PIECES ? c0 : 8 * (lane + 32 * j - row_of(j) * pieces); };
+  auto load = [&](int j, Raw8<U>& x) { x.load(src + rows[row_of(j)].x * stride + col_of(j), PIECES || vec); };
   Raw8<U> raw[kHold];
 #pragma unroll
   for (int j = 0; j < kHold; ++j)
-    if (lane + 32 * j < total) load(lane + 32 * j, raw[j]);
-  float top = 0.f;  // (a NaN is left out)
+    if (row_of(j) < n_rows) load(j, raw[j]);
+  typename Raw8<U>::Top most;
 #pragma unroll
   for (int j = 0; j < kHold; ++j)
-    if (lane + 32 * j < total) top = top_of(raw[j], top);
+    if (row_of(j) < n_rows) most.add(raw[j]);
 #pragma unroll 1
-  for (int i = lane + 32 * kHold; i < total; i += 32) {
+  for (int j = kHold; row_of(j) < n_rows; ++j) {
     Raw8<U> x;
-    load(i, x);
-    top = top_of(x, top);
+    load(j, x);
+    most.add(x);
   }
+  float top = most.value();
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float need = pow2(need_exponent(top));
   const float old = held > 0.f ? held : 0.f;  // (a NaN is none)
   const float now = fmaxf(old, need), inv = 1.f / now;
-  auto put = [&](int i, const Raw8<U>& raw) {
-    const int r = i / pieces;
+  auto put = [&](int j, const Raw8<U>& raw) {
     float x[8];
     raw.get(x);
-    *reinterpret_cast<uint2*>(pool + row_at[r] * pitch + 8 * (i - r * pieces)) = codes8(x, inv);
+    *reinterpret_cast<uint2*>(pool + rows[row_of(j)].y * pitch + col_of(j)) = codes8(x, inv);
   };
 #pragma unroll
   for (int j = 0; j < kHold; ++j)
-    if (lane + 32 * j < total) put(lane + 32 * j, raw[j]);
+    if (row_of(j) < n_rows) put(j, raw[j]);
 #pragma unroll 1
-  for (int i = lane + 32 * kHold; i < total; i += 32) {
+  for (int j = kHold; row_of(j) < n_rows; ++j) {
     Raw8<U> x;
-    load(i, x);
-    put(i, x);
+    load(j, x);
+    put(j, x);
   }
   if (!begins && now > old) {
     // the codes that stay, at the new scale
     const float ratio = old * inv;
-    const int all = p.bs * pieces;
-    for (int i0 = lane; i0 < all; i0 += 32 * 4) {
+    for (int i = 0; row_of(i) < p.bs; i += 4) {
       uint2 codes[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 32 * j, o = i / pieces;
-        if (i < all && members[o] < 0) codes[j] = *reinterpret_cast<const uint2*>(pool + o * pitch + 8 * (i - o * pieces));
+        const int o = row_of(i + j);
+        if (o < p.bs && members[o] < 0) codes[j] = *reinterpret_cast<const uint2*>(pool + o * pitch + col_of(i + j));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = i0 + 32 * j, o = i / pieces;
-        if (i < all && members[o] < 0) {
+        const int o = row_of(i + j);
+        if (o < p.bs && members[o] < 0) {
           float x[8];
           values8(codes[j], x);
-          *reinterpret_cast<uint2*>(pool + o * pitch + 8 * (i - o * pieces)) = codes8(x, ratio);
+          *reinterpret_cast<uint2*>(pool + o * pitch + col_of(i + j)) = codes8(x, ratio);
         }
       }
     }
@@ -219,11 +238,12 @@ __device__ __forceinline__ void write_unit(const WriteParams& p, int64_t block, 
   if (lane == 0 && now != held) *scale_at = now;
 }
 
+// CTAs an SM: 16384 tokens in fp32 with one 56 us, two 35.9, three (registers spill) 53.
 template <typename U, int PIECES>
-__global__ void __launch_bounds__(kMaxWarps * 32, sizeof(U) == 2 && PIECES ? 2 : 1) write_blocks_kernel(const WriteParams p, int vec) {
-  // a CTA's blocks (those led by its tokens): the tokens by offset, the offsets written
+__global__ void __launch_bounds__(kMaxWarps * 32, sizeof(U) == 2 && PIECES ? 3 : 2) write_blocks_kernel(const WriteParams p, int vec) {
+  // a CTA's blocks (those led by its tokens): the tokens by offset; those there are, with their offsets
   __shared__ int members[kGroup][kMaxBlock];
-  __shared__ uint8_t row_at[kGroup][kMaxBlock];
+  __shared__ int2 rows[kGroup][kMaxBlock];
   __shared__ int n_rows[kGroup];
   __shared__ int64_t block_of[kGroup];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -235,7 +255,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(U) == 2 && PIECES ? 2 :
       if (s >= 0 && threadIdx.x == 0) raise_error(p.err, PKV_DEVERR_SLOT_OUT_OF_RANGE);
       return;
     }
-    const int64_t b = s / p.bs;
+    const int64_t b = s >> p.log_bs;
     for (int o = threadIdx.x; o < p.bs; o += blockDim.x) members[0][o] = -1;
     __syncthreads();
     for (int t = threadIdx.x; t < p.T; t += blockDim.x) {
@@ -263,8 +283,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(U) == 2 && PIECES ? 2 :
     int count = 0;
     const int64_t s = t < p.T ? p.slots[t] : -1;
     if (s >= 0 && s < p.num_slots) {
-      const int64_t b = s / p.bs;
-      const int mine = (int)(s - b * p.bs);
+      const int64_t b = s >> p.log_bs;
+      const int mine = (int)s & (p.bs - 1);
       int who[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -289,7 +309,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(U) == 2 && PIECES ? 2 :
           const int o = lane + 32 * j;
           if (o < p.bs) {
             members[g][o] = who[j];
-            if (who[j] >= 0) row_at[g][__popcll(m & ((1ull << o) - 1))] = (uint8_t)o;
+            if (who[j] >= 0) rows[g][__popcll(m & ((1ull << o) - 1))] = make_int2(who[j], o);
           }
         }
         if (lane == 0) block_of[g] = b;
@@ -299,10 +319,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, sizeof(U) == 2 && PIECES ? 2 :
   }
   __syncthreads();
   const int units = 2 * p.Hkv;
-  for (int g = 0; g < per; ++g) {
-    if (n_rows[g] == 0) continue;
+  for (uint32_t led = __ballot_sync(0xffffffffu, lane < per && n_rows[lane] > 0); led != 0; led &= led - 1) {
+    const int g = __ffs(led) - 1;
     for (int u = warp + blockIdx.y * warps; u < units; u += warps * gridDim.y)
-      write_unit<U, PIECES>(p, block_of[g], members[g], row_at[g], n_rows[g], u >> 1, u & 1, vec, lane);
+      write_unit<U, PIECES>(p, block_of[g], members[g], rows[g], n_rows[g], u >> 1, u & 1, vec, lane);
   }
 }
 
@@ -371,6 +391,7 @@ pkv_status paged_kv_write_fp8block(const void* k, const void* v, const int64_t* 
   p.k_stride = k_token_stride;
   p.v_stride = v_token_stride;
   p.bs = block_size;
+  p.log_bs = block_size == 8 ? 3 : block_size == 16 ? 4 : block_size == 32 ? 5 : 6;
   p.Hkv = num_kv_heads;
   p.D = head_dim;
   // 16 bytes at a time where every row start allows it
@@ -383,13 +404,16 @@ pkv_status paged_kv_write_fp8block(const void* k, const void* v, const int64_t* 
   }
   const int per = p.token_of ? kGroup : 1;
   const int warps = std::min(2 * p.Hkv, kMaxWarps);
-  // more heads than a CTA has warps for: several CTAs to a block
-  const dim3 grid((unsigned)((p.T + per - 1) / per), (unsigned)std::min((2 * p.Hkv + warps - 1) / warps, 1024));
+  // more heads than a CTA has warps for: several CTAs to a block, while the SMs hold
+  // them (16384 tokens with two in any case 31.5 us, with one 27.2)
+  const int64_t groups = (p.T + per - 1) / per;
+  const int64_t share = std::max<int64_t>(1, std::min<int64_t>((2 * p.Hkv + warps - 1) / warps, 3 * sms / groups));
+  const dim3 grid((unsigned)groups, (unsigned)std::min<int64_t>(share, 1024));
   auto launch = [&](auto kernel) {
     return p.token_of ? launch_pdl(kernel, grid, dim3(warps * 32), 0, s, p, vec)
                       : (kernel<<<grid, warps * 32, 0, s>>>(p, vec), cudaGetLastError());
   };
-  const int pieces = p.D / 8;
+  const int pieces = vec ? p.D / 8 : 0;
   cudaError_t e;
   if (es == 2)
     e = pieces == 16  ? launch(write_blocks_kernel<uint16_t, 16>)
