@@ -509,6 +509,12 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   // balance the tensor-core kernel; every split costs a partial write and a
   // merge, so no more are made than that.
   pp.target_mma = dev->sms * 2;
+  // Where blocks have scales an item costs some 4 tiles beside its own (its first
+  // tiles wait for one another, its last for the output; 2 tiles assumed: the verify
+  // batch 218 us).  With two items an SM, as above, and with this: the verify batch,
+  // 256 units of 64 tiles, 214 and 195 us; 128 queries on 60000 keys 296 and 191; 20
+  // chunks of 60 on 2000 to 9000 132 and 121; 64 sequences of 8 121 and 124.
+  pp.mma_item_keys = blocks ? 512 : 0;
   pp.min_chunk_dec = dectc ? 512 : 256;
   pp.min_chunk_mma = 512;
   pp.dec_cap = lay.dec_cap;

@@ -429,7 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
 
   // ---- shared-prefix groups
   __shared__ int sh_pre[4];  // prefix items, prefix partial rows, groups read once, groups
-  if (tid == 0) sh_pre[0] = sh_pre[1] = sh_pre[2] = sh_pre[3] = 0;
+  __shared__ int sh_mma_units;  // counted where mma_item_keys is given
+  if (tid == 0) sh_pre[0] = sh_pre[1] = sh_pre[2] = sh_pre[3] = sh_mma_units = 0;
   __syncthreads();
   if (p.cascade) {
     pdl_wait();  // the shared-prefix search (the predecessor) is complete
@@ -473,10 +474,17 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
   __shared__ int sh_mma_ctas;
   __shared__ int sh_state;
   unsigned long long w_dec = 0, w_mma = 0;
+  int n_mma = 0;
   {
     UnitIter t{i0, i1, B, p.Hkv, 0, 0, 0, {}, seq_ln};
-    for (iter_seek(t, p, seq_off); t.i < t.end; iter_next(t, p, seq_off))
+    for (iter_seek(t, p, seq_off); t.i < t.end; iter_next(t, p, seq_off)) {
       (t.d.mma ? w_mma : w_dec) += (unsigned long long)(unit_keys(t.d, t.u, p) - t.d.pre);
+      n_mma += t.d.mma ? 1 : 0;
+    }
+  }
+  if (p.mma_item_keys > 0) {
+    n_mma = __reduce_add_sync(0xffffffffu, n_mma);
+    if (lane == 0 && n_mma > 0) atomicAdd(&sh_mma_units, n_mma);
   }
   // warp sums, then one thread adds the warps' (no contended 64-bit atomics)
 #pragma unroll
@@ -528,6 +536,22 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
     const int tgt_mma = max(1, p.target_mma * mma_ctas / max(1, p.sms));
     unsigned long long cd = (wd + tgt_dec - 1) / (unsigned long long)tgt_dec;
     unsigned long long cm = (wm + tgt_mma - 1) / (unsigned long long)tgt_mma;
+    if (p.mma_item_keys > 0 && sh_mma_units > 0) {
+      // Few long units: as many splits to each as end soonest, were all of the mean
+      // length, with what an item costs beside its keys.
+      const float units = (float)sh_mma_units, mean = (float)wm / units;
+      if (mean > (float)cm) {
+        float best = 3.4e38f;
+        for (int ns = 1; ns <= 8 && (float)((ns - 1) * p.min_chunk_mma) < mean; ++ns) {
+          const float per = ceilf(mean / (float)ns);
+          const float t = ceilf(units * (float)ns / (float)mma_ctas) * (per + (float)p.mma_item_keys);
+          if (t < best) {
+            best = t;
+            cm = (unsigned long long)per;
+          }
+        }
+      }
+    }
     cd = max(cd, (unsigned long long)p.min_chunk_dec);
     cm = max(cm, (unsigned long long)p.min_chunk_mma);
     cd = (cd + p.dec_tile_keys - 1) / p.dec_tile_keys * p.dec_tile_keys;
