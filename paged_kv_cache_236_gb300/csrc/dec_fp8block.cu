@@ -35,6 +35,10 @@
 //   warps 2-5 softmax (thread = key = TMEM lane);
 //   warps 6-9 epilogue (thread = output column = TMEM lane of O^T);
 //   warp 10   item fetch, and the split of the item's q rows.
+// HBM-bound where contexts are long: 4 x 131072 keys (1.07 GB of codes, 2 MB of
+// scales) 207 us with the planner's 10, 5.5 TB/s while it streams; the decode batch (303 MB in
+// short items) 76 us, of which the planner, the start and the last items' merges are
+// a third.  A tile's softmax takes about as long as its bytes.
 // Shared memory: 6 stages of K and V codes (192 KB).  TMEM: S^T and O^T
 // double-buffered.  Waits are bounded, and end as in the bf16 kernel.
 #include <cuda_fp16.h>

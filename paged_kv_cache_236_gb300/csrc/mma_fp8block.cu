@@ -11,7 +11,7 @@
 //   Q K^T  multiplies K's codes as they land.  A row of q is 2^e (q1 + q2), E4M3
 //          each (e from the row's largest |q|: bf16's 8 bits, down to 2^-18 of
 //          that largest value), two chains of four MMAs of K = 32 into the same
-//          accumulator: as long as eight of K = 16 in bf16.  Two warps split
+//          accumulator: as long as eight of K = 16 in bf16.  Three warps split
 //          the Q tile in place.
 //   P V    takes fp16: V's codes are converted (exactly) by four warps, which zero
 //          the rows that no row of the item sees.  The weights carry V's scale:
@@ -21,6 +21,16 @@
 //          8-bit weights would take three terms each here, where the softmax
 //          warps' instructions are what is scarce.
 // Scales are applied by runs of 8 columns (no block is shorter).
+//
+// A tile of 128 x 128 takes about 2700 cycles (MMAs 1100 of them; the softmax
+// warps' chain: 200 for its waits, 600 for the maxima, 1400 for the weights, 100 to
+// 700 to hand them on), so that operations bound it and not bytes: chunks of 512 on up to 2048
+// (86 GFLOP) 150 us, 574 TFLOP/s; the verify batch (5 tokens of 8 heads on 8192
+// keys, 40 of a tile's 128 rows used) 195 us, 2.8 TB/s of codes.  Weights made with the
+// reference as it stands, and again where a tile exceeds it, took 182 and 228 us:
+// blocks' magnitudes differ, and a sixth of the tiles were made twice.  Loads of S
+// ahead of their use 151 and 217 (then 150 and 216); merges left to the splitting
+// warps 152, and 156 against 133 for 20 chunks of 60 tokens.
 //
 // Roles (640 threads, one CTA per SM, persistent):
 //   warp 0     the thread issuing P.V;
