@@ -42,6 +42,8 @@ extern "C" {
  * and, where the block goes on (old > 0 or 0 alike) and new > old, every code
  * of it that the call does not write becomes E4M3(RNE(value * old / new)).
  * Codes that the call does not write are otherwise left as they are.
+ * Rows are expected finite: an infinity saturates, and takes its scale to 2^60; a
+ * NaN has no part in the scale.
  *
  *   k, v            device, [num_tokens, num_kv_heads, head_dim] of `dtype`
  *                   (PKV_DTYPE_BF16 or _F32), token strides in ELEMENTS (0: dense)
@@ -95,7 +97,8 @@ pkv_status paged_kv_copy_block_scales(float* k_scales, float* v_scales, const in
  * codes by codes), logits and sums are fp32; a weight times its V scale is
  * split into E5M2 terms of 9 bits together in calls of few rows, and rounded to
  * fp16 in calls of many (at least 11 bits for those above 2^-21 of the row's
- * largest).
+ * largest).  q is expected finite (an infinity counts as a large finite value; a NaN
+ * makes its row NaN).
  */
 pkv_status paged_attention_forward_fp8block(const void* q, const void* k_cache, const void* v_cache,
                                             const float* k_scales, const float* v_scales,
