@@ -21,6 +21,7 @@
 #include <stdint.h>
 #include <stdio.h>
 
+#include <new>
 #include <unordered_set>
 
 #include "paged_kv_blocks.h"
@@ -91,7 +92,7 @@ pkv_status fail(pkv_status st, const char* msg, long long a = 0) {
 }
 
 // ids in range; no destination is a source or repeats
-pkv_status check_pairs(const int32_t* copies, int32_t num_copies, int64_t num_blocks) {
+pkv_status check_pairs(const int32_t* copies, int32_t num_copies, int64_t num_blocks) try {
   std::unordered_set<int32_t> dsts;
   for (int32_t i = 0; i < num_copies; ++i) {
     const int32_t s = copies[2 * i], d = copies[2 * i + 1];
@@ -103,6 +104,8 @@ pkv_status check_pairs(const int32_t* copies, int32_t num_copies, int64_t num_bl
     if (dsts.count(copies[2 * i]))
       return fail(PKV_ERR_INVALID_ARG, "block %lld is a source and a destination", copies[2 * i]);
   return PKV_OK;
+} catch (const std::bad_alloc&) {  // no exception passes a C entry
+  return fail(PKV_ERR_CUDA, "copy pairs: out of host memory");
 }
 
 // launch(list) for each group of pairs
