@@ -502,7 +502,9 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   // saves (measured on the decode, mixed and long-context batches).  Two where
   // blocks have scales: its tiles take half the time and its items start no
   // faster (decode batch 75.7 us, with three 82.8, with four 83.2; 4 x 131072 keys
-  // 207, 211 and 213 us).
+  // 207, 211 and 213 us), or as many as fill whole waves, where units are few (1 x
+  // 131072 keys 92 us with two, 75 so; 3 of 20000 to 100000 115 and 93; 32 x 4096 77
+  // and 70; 16 x 8192 78 and 68.5).
   pp.target_dec = blocks ? dev->sms * 2 : dectc ? dev->sms * 4 : dec_grid * 4;
   pp.dec_ctas = dectc ? dev->sms : dec_grid;
   // Items are fetched dynamically in largest-first order, so two per SM
@@ -514,7 +516,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   // batch 218 us).  With two items an SM, as above, and with this: the verify batch,
   // 256 units of 64 tiles, 214 and 195 us; 128 queries on 60000 keys 296 and 191; 20
   // chunks of 60 on 2000 to 9000 132 and 121; 64 sequences of 8 121 and 124.
-  pp.mma_item_keys = blocks ? 512 : 0;
+  pp.wave_item_keys = blocks ? 512 : 0;
   pp.min_chunk_dec = dectc ? 512 : 256;
   pp.min_chunk_mma = 512;
   pp.dec_cap = lay.dec_cap;

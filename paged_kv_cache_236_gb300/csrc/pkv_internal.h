@@ -108,7 +108,7 @@ struct PlanParams {
   int side_by_side;  // the decode kernel may run beside the tensor-core kernel (no prefix items)
   int kv_key_bytes;  // K+V bytes per key of one kv head (2 * head_dim * element size)
   int min_chunk_dec, min_chunk_mma;
-  int mma_item_keys;  // what a tensor-core item costs beside its keys, in keys (0: target_mma alone decides)
+  int wave_item_keys;  // > 0: few units are split by whole waves; what a tensor-core item costs beside its keys, in keys
   int dec_cap, mma_cap, merge_cap, part_cap;
   PlanHeader* header;
   WorkItem* dec_items;

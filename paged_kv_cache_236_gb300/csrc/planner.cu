@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
 
   // ---- shared-prefix groups
   __shared__ int sh_pre[4];  // prefix items, prefix partial rows, groups read once, groups
-  __shared__ int sh_mma_units;  // counted where mma_item_keys is given
-  if (tid == 0) sh_pre[0] = sh_pre[1] = sh_pre[2] = sh_pre[3] = sh_mma_units = 0;
+  __shared__ int sh_units[2];  // decode and tensor-core units, counted where wave_item_keys is given
+  if (tid == 0) sh_pre[0] = sh_pre[1] = sh_pre[2] = sh_pre[3] = sh_units[0] = sh_units[1] = 0;
   __syncthreads();
   if (p.cascade) {
     pdl_wait();  // the shared-prefix search (the predecessor) is complete
@@ -482,9 +482,11 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
       n_mma += t.d.mma ? 1 : 0;
     }
   }
-  if (p.mma_item_keys > 0) {
+  if (p.wave_item_keys > 0) {
     n_mma = __reduce_add_sync(0xffffffffu, n_mma);
-    if (lane == 0 && n_mma > 0) atomicAdd(&sh_mma_units, n_mma);
+    const int n_dec = __reduce_add_sync(0xffffffffu, i1 - i0) - n_mma;
+    if (lane == 0 && n_dec > 0) atomicAdd(&sh_units[0], n_dec);
+    if (lane == 0 && n_mma > 0) atomicAdd(&sh_units[1], n_mma);
   }
   // warp sums, then one thread adds the warps' (no contended 64-bit atomics)
 #pragma unroll
@@ -536,18 +538,37 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
     const int tgt_mma = max(1, p.target_mma * mma_ctas / max(1, p.sms));
     unsigned long long cd = (wd + tgt_dec - 1) / (unsigned long long)tgt_dec;
     unsigned long long cm = (wm + tgt_mma - 1) / (unsigned long long)tgt_mma;
-    if (p.mma_item_keys > 0 && sh_mma_units > 0) {
+    if (p.wave_item_keys > 0 && sh_units[1] > 0) {
       // Few long units: as many splits to each as end soonest, were all of the mean
       // length, with what an item costs beside its keys.
-      const float units = (float)sh_mma_units, mean = (float)wm / units;
+      const float units = (float)sh_units[1], mean = (float)wm / units;
       if (mean > (float)cm) {
         float best = 3.4e38f;
         for (int ns = 1; ns <= 8 && (float)((ns - 1) * p.min_chunk_mma) < mean; ++ns) {
           const float per = ceilf(mean / (float)ns);
-          const float t = ceilf(units * (float)ns / (float)mma_ctas) * (per + (float)p.mma_item_keys);
+          const float t = ceilf(units * (float)ns / (float)mma_ctas) * (per + (float)p.wave_item_keys);
           if (t < best) {
             best = t;
             cm = (unsigned long long)per;
+          }
+        }
+      }
+    }
+    if (p.wave_item_keys > 0 && sh_units[0] > 0) {
+      // The same for the decode items, as many as fill one to four waves: an item
+      // costs some 840 keys beside its own (5 us), a merge 50 to each split.
+      const int ctas = max(1, mma_ctas < p.sms ? p.dec_ctas * (p.sms - mma_ctas) / p.sms : p.dec_ctas);
+      const float mean = (float)wd / (float)sh_units[0];
+      if (mean > (float)cd) {
+        float best = 3.4e38f;
+        for (int waves = 1; waves <= 4; ++waves) {
+          const int ns = min(waves * ctas / sh_units[0], kMaxSplits);
+          if (ns == 0) continue;
+          const float per = ceilf(mean / (float)ns);
+          const float t = (float)waves * (per + 840.f) + (float)ns * 50.f;
+          if (t < best) {
+            best = t;
+            cd = (unsigned long long)per;
           }
         }
       }
