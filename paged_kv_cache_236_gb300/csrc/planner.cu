@@ -111,11 +111,12 @@ __device__ __forceinline__ SeqDesc describe(const PlanParams& p, int s, const in
 
 // Keys a unit must visit: rows [u*unit_rows, ...) of the sequence.  With a
 // window, those that it leaves out are not counted.
+template <bool WIN>
 __device__ __forceinline__ int unit_keys(const SeqDesc& d, int u, const PlanParams& p) {
   const int r1 = min(d.rows, (u + 1) * d.unit_rows);
   const int last_tok = (r1 - 1) / p.G;
   const int keys = p.causal ? (d.L - d.n + last_tok + 1) : d.L;
-  if (p.window == 0) return keys;
+  if constexpr (!WIN) return keys;
   return keys - Hole(d.L, d.n, u * d.unit_rows / p.G, p.window, p.num_sink, p.bs).len;
 }
 
@@ -406,6 +407,9 @@ __device__ __noinline__ void write_new_rows(const PlanParams& p) {
   }
 }
 
+// WAVES: wave_item_keys is given; WIN: there is a window.  (Instances of their own: the
+// code runs cold, and what these add cost the other calls 2 us.)
+template <bool WAVES, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
   // The attention kernel may start its prologue while this plans (it waits
   // for this grid).  This grid may start while its predecessor runs: the
@@ -429,8 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
 
   // ---- shared-prefix groups
   __shared__ int sh_pre[4];  // prefix items, prefix partial rows, groups read once, groups
-  __shared__ int sh_units[2];  // decode and tensor-core units, counted where wave_item_keys is given
-  if (tid == 0) sh_pre[0] = sh_pre[1] = sh_pre[2] = sh_pre[3] = sh_units[0] = sh_units[1] = 0;
+  __shared__ int sh_units[WAVES ? 2 : 1];  // decode and tensor-core units
+  if (tid == 0) sh_pre[0] = sh_pre[1] = sh_pre[2] = sh_pre[3] = 0;
+  if constexpr (WAVES)
+    if (tid == 0) sh_units[0] = sh_units[1] = 0;
   __syncthreads();
   if (p.cascade) {
     pdl_wait();  // the shared-prefix search (the predecessor) is complete
@@ -474,15 +480,15 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
   __shared__ int sh_mma_ctas;
   __shared__ int sh_state;
   unsigned long long w_dec = 0, w_mma = 0;
-  int n_mma = 0;
+  [[maybe_unused]] int n_mma = 0;
   {
     UnitIter t{i0, i1, B, p.Hkv, 0, 0, 0, {}, seq_ln};
     for (iter_seek(t, p, seq_off); t.i < t.end; iter_next(t, p, seq_off)) {
-      (t.d.mma ? w_mma : w_dec) += (unsigned long long)(unit_keys(t.d, t.u, p) - t.d.pre);
-      n_mma += t.d.mma ? 1 : 0;
+      (t.d.mma ? w_mma : w_dec) += (unsigned long long)(unit_keys<WIN>(t.d, t.u, p) - t.d.pre);
+      if constexpr (WAVES) n_mma += t.d.mma ? 1 : 0;
     }
   }
-  if (p.wave_item_keys > 0) {
+  if constexpr (WAVES) {
     n_mma = __reduce_add_sync(0xffffffffu, n_mma);
     const int n_dec = __reduce_add_sync(0xffffffffu, i1 - i0) - n_mma;
     if (lane == 0 && n_dec > 0) atomicAdd(&sh_units[0], n_dec);
@@ -538,37 +544,39 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
     const int tgt_mma = max(1, p.target_mma * mma_ctas / max(1, p.sms));
     unsigned long long cd = (wd + tgt_dec - 1) / (unsigned long long)tgt_dec;
     unsigned long long cm = (wm + tgt_mma - 1) / (unsigned long long)tgt_mma;
-    if (p.wave_item_keys > 0 && sh_units[1] > 0) {
-      // Few long units: as many splits to each as end soonest, were all of the mean
-      // length, with what an item costs beside its keys.
-      const float units = (float)sh_units[1], mean = (float)wm / units;
-      if (mean > (float)cm) {
-        float best = 3.4e38f;
-        for (int ns = 1; ns <= 8 && (float)((ns - 1) * p.min_chunk_mma) < mean; ++ns) {
-          const float per = ceilf(mean / (float)ns);
-          const float t = ceilf(units * (float)ns / (float)mma_ctas) * (per + (float)p.wave_item_keys);
-          if (t < best) {
-            best = t;
-            cm = (unsigned long long)per;
+    if constexpr (WAVES) {
+      if (sh_units[1] > 0) {
+        // Few long units: as many splits to each as end soonest, were all of the mean
+        // length, with what an item costs beside its keys.
+        const float units = (float)sh_units[1], mean = (float)wm / units;
+        if (mean > (float)cm) {
+          float best = 3.4e38f;
+          for (int ns = 1; ns <= 8 && (float)((ns - 1) * p.min_chunk_mma) < mean; ++ns) {
+            const float per = ceilf(mean / (float)ns);
+            const float t = ceilf(units * (float)ns / (float)mma_ctas) * (per + (float)p.wave_item_keys);
+            if (t < best) {
+              best = t;
+              cm = (unsigned long long)per;
+            }
           }
         }
       }
-    }
-    if (p.wave_item_keys > 0 && sh_units[0] > 0) {
-      // The same for the decode items, as many as fill one to four waves: an item
-      // costs some 840 keys beside its own (5 us), a merge 50 to each split.
-      const int ctas = max(1, mma_ctas < p.sms ? p.dec_ctas * (p.sms - mma_ctas) / p.sms : p.dec_ctas);
-      const float mean = (float)wd / (float)sh_units[0];
-      if (mean > (float)cd) {
-        float best = 3.4e38f;
-        for (int waves = 1; waves <= 4; ++waves) {
-          const int ns = min(waves * ctas / sh_units[0], kMaxSplits);
-          if (ns == 0) continue;
-          const float per = ceilf(mean / (float)ns);
-          const float t = (float)waves * (per + 840.f) + (float)ns * 50.f;
-          if (t < best) {
-            best = t;
-            cd = (unsigned long long)per;
+      if (sh_units[0] > 0) {
+        // The same for the decode items, as many as fill one to four waves: an item
+        // costs some 840 keys beside its own (5 us), a merge 50 to each split.
+        const int ctas = max(1, mma_ctas < p.sms ? p.dec_ctas * (p.sms - mma_ctas) / p.sms : p.dec_ctas);
+        const float mean = (float)wd / (float)sh_units[0];
+        if (mean > (float)cd) {
+          float best = 3.4e38f;
+          for (int waves = 1; waves <= 4; ++waves) {
+            const int ns = min(waves * ctas / sh_units[0], kMaxSplits);
+            if (ns == 0) continue;
+            const float per = ceilf(mean / (float)ns);
+            const float t = (float)waves * (per + 840.f) + (float)ns * 50.f;
+            if (t < best) {
+              best = t;
+              cd = (unsigned long long)per;
+            }
           }
         }
       }
@@ -611,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
         const SeqDesc& d = t.d;
         const int chunk = d.mma ? cm : cd;
         const int cb = d.mma ? kClasses : 0;
-        const int keys = unit_keys(d, t.u, p) - d.pre;
+        const int keys = unit_keys<WIN>(d, t.u, p) - d.pre;
         int ns, per;
         split_of(keys, chunk, d.mma ? kMmaTileKeys : p.dec_tile_keys, ns, per);
         if (ns > 1) add(cb + size_class(per, chunk), ns - 1);  // all splits but the last are full
@@ -733,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) plan_kernel(PlanParams p) {
       WorkItem* items = d.mma ? p.mma_items : p.dec_items;
       const int chunk = d.mma ? cm : cd;
       const int cbase = d.mma ? kClasses : 0;
-      const int kend = unit_keys(d, u, p);
+      const int kend = unit_keys<WIN>(d, u, p);
       const int keys = kend - d.pre;
       const int r0 = u * d.unit_rows;
       const int nr = min(d.rows - r0, d.unit_rows);
@@ -855,6 +863,8 @@ cudaError_t launch_prefix_search(const PlanParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_planner(const PlanParams& p, cudaStream_t s) {
+  static void (*const kKernels[4])(PlanParams) = {plan_kernel<false, false>, plan_kernel<false, true>,
+                                                  plan_kernel<true, false>, plan_kernel<true, true>};
   const size_t smem = (size_t)((p.B + 2) & ~1) * sizeof(int) + (p.B <= kPlanSmemSeqs ? (size_t)p.B * sizeof(int2) : 0);
   if (p.B > kMaxPlanSeqs) return cudaErrorInvalidValue;
   static unsigned long long done_mask = 0;
@@ -867,11 +877,13 @@ cudaError_t launch_planner(const PlanParams& p, cudaStream_t s) {
     static_assert(((kPlanSmemSeqs + 2) & ~1) * sizeof(int) + kPlanSmemSeqs * sizeof(int2) <=
                       ((kMaxPlanSeqs + 2) & ~1) * sizeof(int),
                   "planner shared memory");
-    e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    for (auto kernel : kKernels)
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     __atomic_fetch_or(&done_mask, 1ull << dev, __ATOMIC_RELEASE);
   }
-  e = launch_pdl(plan_kernel, dim3(1 + p.write_ctas), dim3(kThreads), smem, s, p);
+  e = launch_pdl(kKernels[(p.wave_item_keys > 0 ? 2 : 0) + (p.window > 0 ? 1 : 0)], dim3(1 + p.write_ctas),
+                 dim3(kThreads), smem, s, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
