@@ -114,3 +114,29 @@ def test_nothing_valid():
     pkv.paged_attention_forward_fp8block(*b.args[:7], none, b.args[8], out=out)
     assert torch.all(out == 3.0) and pkv.device_errors() == 0
     b.check(pkv.paged_attention_forward_fp8block(*b.args))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with the default workspaces of its own."""
+    few = Batch(31, [700, 33, 5000], [1, 1, 1], 8, 2, 16)
+    many = Batch(32, [700, 333, 60], [100, 1, 60], 8, 2, 16)
+    win = batch(33, [700, 333, 60], [100, 1, 60], 8, 2, 128, 16, torch.bfloat16)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        with torch.cuda.stream(streams[0]):
+            outs[0].append(pkv.paged_attention_forward_fp8block(*few.args, max_query_len=1))
+            outs[0].append(pkv.paged_attention_forward_fp8block(*many.args))
+        with torch.cuda.stream(streams[1]):
+            outs[1].append(pkv.paged_attention_forward_fp8block(*many.args))
+            outs[1].append(pkv.paged_attention_window_forward(win["q"], win["kc"], win["vc"], win["tables"], win["lens"],
+                                                              win["qsl"], 0.1, 100, 2))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert all(torch.equal(o[i], o[i % 2]) for i in range(len(o)))
+    few.check(outs[0][0])
+    many.check(outs[0][1])
+    assert torch.equal(outs[1][0], outs[0][1])
+    check(win, outs[1][1], 0.1, 100, 2, torch.bfloat16)
+    assert pkv.device_errors() == 0
