@@ -666,6 +666,8 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, copies, k_scales: 
                               t.stride() != k_scales.stride() or not (t[0] if t.dim() == 3 else t).is_contiguous()):
             raise ValueError("k_scales and v_scales must be float32 [NB, Hkv] or [layers, NB, Hkv], alike, each layer's "
                              "contiguous")
+    if layers > 1 and k_scales is not None and k_scales.stride(0) == 0:  # the C call takes a stride of 0 for dense
+        raise ValueError("k_scales and v_scales must not repeat one layer's (a layer stride of 0)")
     with torch.cuda.device(dev):
         _check(lib().paged_kv_copy_blocks(k_cache.data_ptr(), v_cache.data_ptr(),
                                           pairs.ctypes.data if len(pairs) else None, len(pairs), layers, stride,

@@ -1,0 +1,44 @@
+"""Tensors that repeat one row or layer (a stride of 0), which the C calls take
+for dense ones: the binding refuses them.  The library is stubbed, so that what
+a call would be given is seen without a GPU."""
+import contextlib
+
+import pytest
+import torch
+
+import paged_kv_cache_236_gb300 as pkv
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The C calls made, as (name, arguments): each is accepted and does nothing."""
+    made = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: made.append((name, a)) or 0
+
+    monkeypatch.setattr(pkv, "lib", Lib)
+    monkeypatch.setattr(pkv, "_need_cuda", lambda *t: torch.device("cpu"))
+    monkeypatch.setattr(pkv, "_stream", lambda dev: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    return made
+
+
+def pools(layers):
+    return torch.zeros(layers, 4, 16, 2, 32, dtype=torch.uint8), torch.zeros(layers, 4, 16, 2, 32, dtype=torch.uint8)
+
+
+def test_scales_of_one_layer_for_all(calls):
+    k, v = pools(3)
+    one = torch.ones(1, 4, 2)
+    with pytest.raises(ValueError, match="layer stride"):
+        pkv.copy_blocks(k, v, [[0, 1]], one.expand(3, 4, 2), one.expand(3, 4, 2))
+    assert not calls  # nothing of the call has run
+    # one layer has no stride, and layers may lie apart
+    pkv.copy_blocks(k[:1], v[:1], [[0, 1]], one.expand(1, 4, 2), one.expand(1, 4, 2))
+    pkv.copy_blocks(k[0], v[0], [[0, 1]], one[0], one[0])
+    apart = torch.ones(3, 5, 4, 2)[:, 0]
+    pkv.copy_blocks(k, v, [[0, 1]], apart, apart)
+    scales = [a for name, a in calls if name == "paged_kv_copy_block_scales"]
+    assert [(a[4], a[5]) for a in scales] == [(1, 0), (1, 0), (3, 40)]
