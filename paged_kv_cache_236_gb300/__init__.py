@@ -660,6 +660,8 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, copies, k_scales: 
         raise ValueError("caches must be [NB, bs, Hkv, D] or [layers, NB, bs, Hkv, D]")
     if not pool.is_contiguous():
         raise ValueError("each layer's pool must be contiguous")
+    if layers > 1 and stride == 0:  # the C call takes a stride of 0 for dense
+        raise ValueError("k_cache and v_cache must not repeat one layer's pool (a layer stride of 0)")
     NB, bs, Hkv, D = pool.shape
     for t in (k_scales, v_scales):
         if t is not None and (t.shape != k_cache.shape[:-3] + (Hkv,) or t.dtype != torch.float32 or t.device != dev or

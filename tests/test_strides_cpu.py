@@ -42,3 +42,15 @@ def test_scales_of_one_layer_for_all(calls):
     pkv.copy_blocks(k, v, [[0, 1]], apart, apart)
     scales = [a for name, a in calls if name == "paged_kv_copy_block_scales"]
     assert [(a[4], a[5]) for a in scales] == [(1, 0), (1, 0), (3, 40)]
+
+
+def test_a_pool_of_one_layer_for_all(calls):
+    k, v = (t[:1] for t in pools(1))
+    with pytest.raises(ValueError, match="layer stride"):
+        pkv.copy_blocks(k.expand(3, -1, -1, -1, -1), v.expand(3, -1, -1, -1, -1), [[0, 1]])
+    assert not calls
+    pkv.copy_blocks(k, v, [[0, 1]])
+    k, v = torch.zeros(3, 2, 4, 16, 2, 32).unbind(1)
+    pkv.copy_blocks(k, v, [[0, 1]])
+    layer = 4 * 16 * 2 * 32
+    assert [(a[4], a[5]) for _, a in calls] == [(1, layer), (3, 2 * layer)]
