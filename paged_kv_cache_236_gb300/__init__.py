@@ -228,10 +228,11 @@ def paged_kv_write(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     if v.shape[0] != T or slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or \
             not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be contiguous int64 [T]")
+    strides = _row_strides(T, k, v)
     with torch.cuda.device(dev):
         _check(lib().paged_kv_write(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
-                                    v_cache.data_ptr(), T, NB, bs, Hkv, D, k.stride(0) if T else 0,
-                                    v.stride(0) if T else 0, DTYPE[k_cache.dtype], _stream(dev)))
+                                    v_cache.data_ptr(), T, NB, bs, Hkv, D, *strides, DTYPE[k_cache.dtype],
+                                    _stream(dev)))
 
 
 def workspace_size(num_seqs: int, num_tokens: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
@@ -409,6 +410,14 @@ def _forward_args(q, k_cache, v_cache, block_tables, context_lens, query_start_l
     return args, out, workspace
 
 
+def _row_strides(T: int, *tensors: torch.Tensor) -> tuple:
+    """Token strides of ``tensors`` [T, ...] as the C calls take them."""
+    strides = tuple(t.stride(0) if T else 0 for t in tensors)
+    if T > 1 and 0 in strides:  # the C call takes a stride of 0 for dense
+        raise ValueError("k and v must not repeat one token's row (a token stride of 0)")
+    return strides
+
+
 def _new_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, Hkv: int, D: int, dtypes) -> tuple:
     """Checks a step's new K/V rows [T, Hkv, D] (contiguous heads) and returns
     (T, k token stride, v token stride)."""
@@ -421,7 +430,7 @@ def _new_rows(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, Hkv:
     if v.shape[0] != T or slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or \
             not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be contiguous int64 [T]")
-    return T, (k.stride(0) if T else 0), (v.stride(0) if T else 0)
+    return T, *_row_strides(T, k, v)
 
 
 def paged_kv_write_attention_forward(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
@@ -716,11 +725,11 @@ def paged_kv_write_fp8(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Ten
     if v.shape[0] != T or slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or \
             not slot_mapping.is_contiguous():
         raise ValueError("slot_mapping must be contiguous int64 [T]")
+    strides = _row_strides(T, k, v)
     with torch.cuda.device(dev):
         _check(lib().paged_kv_write_fp8(k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(),
-                                        v_cache.data_ptr(), T, NB, bs, Hkv, D, k.stride(0) if T else 0,
-                                        v.stride(0) if T else 0, DTYPE[k.dtype], float(k_scale), float(v_scale),
-                                        _stream(dev)))
+                                        v_cache.data_ptr(), T, NB, bs, Hkv, D, *strides, DTYPE[k.dtype],
+                                        float(k_scale), float(v_scale), _stream(dev)))
 
 
 def paged_attention_forward_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -1281,8 +1290,6 @@ def paged_kv_write_fp8block(k: torch.Tensor, v: torch.Tensor, slot_mapping: torc
     _check_block_scales(k_cache, v_cache, k_scales, v_scales)
     NB, bs, Hkv, D = k_cache.shape
     T, ks, vs = _new_rows(k, v, slot_mapping, Hkv, D, set(DTYPE))
-    if T > 1 and 0 in (ks, vs):  # the C call takes a stride of 0 for dense
-        raise ValueError("k and v must not repeat one token's row (a token stride of 0)")
     need = fp8block_write_workspace(T, NB, bs)
     if workspace is None:
         workspace = _on(dev, _workspace, k.device, need) if need else None

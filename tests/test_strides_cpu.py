@@ -54,3 +54,38 @@ def test_a_pool_of_one_layer_for_all(calls):
     pkv.copy_blocks(k, v, [[0, 1]])
     layer = 4 * 16 * 2 * 32
     assert [(a[4], a[5]) for _, a in calls] == [(1, layer), (3, 2 * layer)]
+
+
+WRITES = ["paged_kv_write", "paged_kv_write_fp8", "paged_kv_write_attention_forward",
+          "paged_kv_write_attention_forward_fp8kv"]
+
+
+@pytest.mark.parametrize("name", WRITES)
+def test_a_row_of_one_token_for_all(calls, monkeypatch, name):
+    """The strides that a write is given, and that it is not given a 0 for several tokens."""
+    monkeypatch.setattr(pkv, "_forward_args", lambda *a: ((), None, None))
+    monkeypatch.setattr(pkv, "_fp8_forward_args", lambda *a: ((), None, None))
+    fp8 = "fp8" in name
+    cache = torch.zeros(4, 16, 2, 32, dtype=torch.uint8 if fp8 else torch.float32)
+    at = torch.arange(5)
+    scales = (1.0, 1.0) if fp8 else ()
+
+    def write(k, v):
+        slots = at[:k.shape[0]]
+        if "attention" in name:
+            getattr(pkv, name)(k, v, slots, None, cache, cache, None, None, None, 0.1, *scales)
+        else:
+            getattr(pkv, name)(k, v, slots, cache, cache, *scales)
+
+    dense, one = torch.zeros(5, 2, 32), torch.zeros(1, 2, 32)
+    for k, v in ((one.expand(5, 2, 32), dense), (dense, one.expand(5, 2, 32))):
+        with pytest.raises(ValueError, match="token stride"):
+            write(k, v)
+    assert not calls
+    fused = torch.zeros(5, 4, 32)
+    write(dense, fused[:, :2])
+    write(one, one)
+    write(dense[:0], dense[:0])
+    assert [n for n, _ in calls] == [name] * 3
+    wide = [tuple(x for x in a if x in (64, 128)) for _, a in calls]
+    assert wide[0] == (64, 128) and wide[1] == (64, 64) and wide[2] == ()
