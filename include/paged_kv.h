@@ -173,7 +173,7 @@ pkv_status paged_kv_write_rope(const void* q, const void* k, const void* v, cons
  *   z = x / sqrt(mean(x^2) + eps) * q_weight (k_weight),
  * which is then rotated to its token's position as paged_kv_write_rope does.
  * v is not normed.  The norm is over head_dim; all of it is computed in fp32
- * (the squares' sum must not overflow: |x| below 2^60) and rounded once.
+ * (|x| below 2^60, whatever head_dim) and rounded once.
  *
  *   q_weight, k_weight  device [head_dim] of weight_dtype (`dtype` or
  *               PKV_DTYPE_F32), the same for all heads; NULL: ones

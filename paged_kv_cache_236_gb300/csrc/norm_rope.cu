@@ -51,6 +51,10 @@ struct NormParams {
 constexpr int kWarps = 4;
 constexpr int kBatch = 2;  // heads a lane loads at a time
 constexpr int kBulkSmem = 112 * 1024;  // two CTAs an SM at least
+// A lane's squares (at most 32 of them) are summed as they are, below 2^125 for |x| <
+// 2^60; an eighth of its sum goes to the head's, which 1024 elements would take past
+// fp32's range.  (A power of two: the same bits where both fit.)
+constexpr float kSumShare = 0.125f;
 
 // U: the rows' element (uint16_t: bf16 bits).  F8: the pools hold E4M3 codes.
 // WIDE: a head has more places than a warp has lanes (long heads, or heads
@@ -91,7 +95,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
   const int side = WIDE ? 1 : 32 / places;  // heads side by side
   const int y = WIDE ? 0 : lane / places;
   const bool idle = !WIDE && y >= side;  // lanes left over
-  const float inv_d = 1.f / (float)p.D;
+  const float inv_d = 1.f / kSumShare / (float)p.D;
 
   auto weight = [&](const void* ws, int i) -> float {
     if (!ws) return 1.f;
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
             if (two) b = *reinterpret_cast<const V*>(row + cb);
             s += squares(a, b, two);
           }
-          r = rsqrtf(fmaf(head_sum(s), inv_d, p.eps));
+          r = rsqrtf(fmaf(head_sum(s * kSumShare), inv_d, p.eps));
         }
         for (int x = lane; x < places; x += 32) {
           columns(x, ca, cb, rot, two);
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
           const int h = base + y + i * hstep;
           float ya[VEC], yb[VEC];
           if (norm) {
-            const float r = rsqrtf(fmaf(head_sum(squares(a[i], b[i], two)), inv_d, p.eps));
+            const float r = rsqrtf(fmaf(head_sum(squares(a[i], b[i], two) * kSumShare), inv_d, p.eps));
             turned(t, a[i], b[i], r, rot, two, ya, yb);
           } else {
 #pragma unroll
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_bulk_kernel(const NormP
   const int ca = rot ? (INTER ? 2 * x * VEC : x * VEC) : 2 * p.half + 2 * (x - rot_places) * VEC;
   const int cb = rot && !INTER ? p.half + x * VEC : ca + VEC;
   const bool two = cb + VEC <= p.D;
-  const float inv_d = 1.f / (float)p.D;
+  const float inv_d = 1.f / kSumShare / (float)p.D;
   auto head_sum = [&](float s) {  // over the lanes of a head
     if ((places & (places - 1)) == 0) {
       for (int o = places >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_bulk_kernel(const NormP
           s2 = fma2(xb[k], xb[k], s2);
         }
         const float2 s = up2(s2);
-        const float r = rsqrtf(fmaf(head_sum(s.x + s.y), inv_d, p.eps));
+        const float r = rsqrtf(fmaf(head_sum((s.x + s.y) * kSumShare), inv_d, p.eps));
         const f32x2 r2 = pk2(r, r);
         float ya[VEC], yb[VEC];
 #pragma unroll
