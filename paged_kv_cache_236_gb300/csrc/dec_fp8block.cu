@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         // the row's power of two: its largest |q| becomes 128 to 256 (E4M3 ends at 448)
-        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 - 7, -110), 120);
+        const int e = min(max((int)(__float_as_uint(top) >> 23) - 127 - 7, -126), 120);
         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
         uint32_t hi = 0, lo = 0;
 #pragma unroll

@@ -173,8 +173,14 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
 // Rows row0 .. row1 - 1 (a multiple of 4) of a Q tile in place, by a warp, a row at a time (four
 // on their way): 128 bf16 in two 64-column halves kHalf apart (16-byte chunk j at
 // j ^ (r & 7) of the row) become 128 codes of q1 in the first and of q2 in the
-// second, swizzled alike.  scales[r]: 2^e.
-__device__ __forceinline__ void split_rows(uint8_t* tile, int row0, int row1, float* scales, int lane) {
+// second, swizzled alike.  scales[r]: 2^e times the logit scale.
+__device__ __forceinline__ void split_rows(uint8_t* tile, int row0, int row1, float* scales, float scale_log2,
+                                           int lane) {
+  // The least e: 2^e scale_log2 stays in [2^-84, 2^-83], so that its product with a K
+  // scale (2^-60 or more) is not 0, which the masks' infinities must not meet.  Rows
+  // below 2^(e + 7) lose low bits: 2^-10 2^e of each of 128 elements, times values of
+  // K up to 448 * 2^60, is 2^-17 of a logit.
+  const int least = max(-84 - min(ilogbf(scale_log2), 127), -126);
   // this lane's columns 4 lane .. + 3: 8 bytes of bf16, 4 codes
   const int from = (lane >> 4) * kHalf + (lane & 1) * 8, fc = (lane & 15) >> 1;
   const int to = (lane & 3) * 4, tc = lane >> 2;
@@ -190,7 +196,7 @@ __device__ __forceinline__ void split_rows(uint8_t* tile, int row0, int row1, fl
       const uint32_t top2 = __vmaxu2(raw[i].x & 0x7FFF7FFFu, raw[i].y & 0x7FFF7FFFu);
       const int top = (int)__reduce_max_sync(0xffffffffu, max(top2 & 0xFFFFu, top2 >> 16));
       // the largest |q| becomes 128 to 256 (E4M3 ends at 448)
-      const int e = min(max((top >> 7) - 127 - 7, -50), 120);
+      const int e = min(max((top >> 7) - 127 - 7, least), 120);
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);
       const float a[4] = {bf16_lo(raw[i].x) * down, bf16_hi(raw[i].x) * down, bf16_lo(raw[i].y) * down,
                           bf16_hi(raw[i].y) * down};
@@ -206,7 +212,7 @@ __device__ __forceinline__ void split_rows(uint8_t* tile, int row0, int row1, fl
       uint8_t* dst = tile + (r0 + i) * 128 + to + ((tc ^ ((r0 + i) & 7)) << 4);
       *reinterpret_cast<uint32_t*>(dst) = h[0] | h[1] << 16;
       *reinterpret_cast<uint32_t*>(dst + kHalf) = l[0] | l[1] << 16;
-      if (lane == i) scales[r0 + i] = __uint_as_float((uint32_t)(127 + e) << 23);
+      if (lane == i) scales[r0 + i] = __uint_as_float((uint32_t)(127 + e) << 23) * scale_log2;
     }
   }
 }
@@ -243,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
   Bars* bars = reinterpret_cast<Bars*>(smem + kBarOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kBarOff + kNumBars * 8);
   ItemSlot* slots = reinterpret_cast<ItemSlot*>(smem + kSlotOff);
-  float* row_scales = reinterpret_cast<float*>(smem + kRowScaleOff);      // [2][128]
+  float* row_scales = reinterpret_cast<float*>(smem + kRowScaleOff);      // [2][128], times the logit scale
   Scales* tile_scales = reinterpret_cast<Scales*>(smem + kScaleOff);      // [kScaleSlots][16 runs of 8 keys]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WaitCtl wc{p.err, wait_limit(p.wait_ns)};
@@ -563,7 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
         if (done) break;
         if (!__all_sync(0xffffffffu, mbar_wait(&bars->q_full[qb], (c >> 1) & 1, wc))) break;
         // rows 44 part .. (40 for the last)
-        split_rows(smem + kQOff + qb * kQBytes, 44 * part, min(44 * part + 44, kMmaRows), row_scales + qb * kMmaRows, lane);
+        split_rows(smem + kQOff + qb * kQBytes, 44 * part, min(44 * part + 44, kMmaRows), row_scales + qb * kMmaRows,
+                   p.scale_log2, lane);
         fence_proxy_async_smem();  // generic-proxy writes, read by the tensor core
         mbar_arrive(&bars->q_split[qb]);
       }
@@ -694,8 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
       const int vis = valid ? min(it.ke, p.causal ? L - n + tok + 1 : L) : INT_MAX;
       const bool idle = q4 * 32 >= it.nrows;  // none of the warp's rows is the item's
       if (barrier_any(6, 256, !__all_sync(0xffffffffu, mbar_wait(&bars->q_split[qb], (c >> 1) & 1, wc)))) break;
-      // of this row's accumulator, in log2 units; times the least K scale still a normal number
-      const float unit = valid ? fmaxf(row_scales[qb * kMmaRows + r] * p.scale_log2, 0x1p-66f) : 0.f;
+      // of this row's accumulator, in log2 units; times any K scale not 0 (split_rows)
+      const float unit = valid ? row_scales[qb * kMmaRows + r] : 0.f;
       float m_ref = -CUDART_INF_F, l = 0.f;
       int owe = -1;  // after a failed wait: the pair barriers of the item not yet taken
       const int ntiles = (it.ke - it.kb + kKeys - 1) / kKeys;
