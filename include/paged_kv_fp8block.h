@@ -93,10 +93,10 @@ pkv_status paged_kv_copy_block_scales(float* k_scales, float* v_scales, const in
  *   the rest          as paged_attention_forward (the same block sizes, groups,
  *                     query counts, workspace and errors)
  * Numerics: q is split into two E4M3 terms for each row's own power-of-two
- * scale (exact to 2^-18 of the row's largest |q|, or to 2^-136 where that is
- * more; calls of many rows may leave out more of a row so small that none of its
- * logits moves by 2^-16; the tensor cores multiply
- * codes by codes), logits and sums are fp32; a weight times its V scale is
+ * scale (off by at most 2^-17 of the row's largest |q|, or by 2^-136 where that
+ * is more; calls of many rows may leave out more of a row so small that none of
+ * its logits moves by 2^-16; the tensor cores multiply codes by codes), logits
+ * and sums are fp32; a weight times its V scale is
  * split into E5M2 terms of 9 bits together in calls of few rows, and rounded to
  * fp16 in calls of many (at least 11 bits for those above 2^-21 of the row's
  * largest).  q is expected finite (an infinity counts as a large finite value; a NaN

@@ -12,8 +12,9 @@
 // of loads, conversion and MMAs sets the pace, at a third of the HBM rate.  So
 // the other operand is split into 8-bit terms instead, which cost columns of
 // an MMA whose columns are mostly unused anyway:
-//   q    = 2^e (q1 + q2), E4M3 each, with e from the row's largest |q|: 8
-//          significant bits, bf16's own, down to 2^-18 of that largest value;
+//   q    = 2^e (q1 + q2), E4M3 each, with e from the row's largest |q|, which
+//          becomes 2^7 to 2^8: 8 significant bits, bf16's own, but for what is
+//          below 2^-10, half of E4M3's least step: 2^-17 of the largest value;
 //   w    = 2^(x - m) sv 2^11 = w1 + w2 + w3, E5M2 each: the top bytes of an fp16
 //          value and of what is left of it, twice; 9 bits, down to 2^-16 (a
 //          row's largest w is 2^11 to 2^15: E4M3's range would lose the many small

@@ -9,8 +9,8 @@
 // it (mma_attn.cu: tiles, two issuing threads, epilogue, splits, waits).  What
 // differs:
 //   Q K^T  multiplies K's codes as they land.  A row of q is 2^e (q1 + q2), E4M3
-//          each (e from the row's largest |q|: bf16's 8 bits, down to 2^-18 of
-//          that largest value), two chains of four MMAs of K = 32 into the same
+//          each (e from the row's largest |q|: bf16's 8 bits, off by at most 2^-17
+//          of that largest value), two chains of four MMAs of K = 32 into the same
 //          accumulator: as long as eight of K = 16 in bf16.  Three warps split
 //          the Q tile in place.
 //   P V    takes fp16: V's codes are converted (exactly) by four warps, which zero

@@ -1,5 +1,5 @@
 """paged_attention_forward_fp8block at the ends of its ranges: q, K's scales and
-the logit scale by powers of two apart.
+the logit scale by powers of two apart, and the bound of q's split.
 
 Powers of two that cancel leave every logit what it was, so the tolerances are
 those of the operator's other tests: weights of 9 bits or more (2^-9 of each), q's
@@ -50,3 +50,37 @@ def test_rows_of_q_of_every_magnitude(n):
     b.q = (b.q.float() * size[:, None, None]).to(torch.bfloat16)
     b.up()
     b.check(pkv.paged_attention_forward_fp8block(*b.args))
+
+
+@pytest.mark.parametrize("n", [1, 64])
+@pytest.mark.parametrize("part", [0.5, 0.75, 1.0, 1.25, 1.5, 2.5, 3.0])
+def test_the_split_of_q_at_its_bound(n, part):
+    """An element of part * 2^-17 beside a largest one of 1 meets a large K: the logit is off by at
+    most 2^-17 |k|.  Two keys with V of 1 and 0, so that the output is the sigmoid of the logit; a
+    sixteenth of it for the weights' and the output's roundings (2^-8 of p, over p (1 - p) >= 0.18)."""
+    one = torch.tensor([448.0, 1.0]).to(torch.float8_e4m3fn).view(torch.uint8)
+    codes = torch.zeros(2, 1, 16, 1, 128, dtype=torch.uint8)
+    codes[0, 0, 0, 0, 1], codes[1, 0, 0] = one[0], one[1]
+    kc, vc = codes.cuda()
+    k_scale, v_scale = torch.full((1, 1), 2.0 ** 7, device="cuda"), torch.ones(1, 1, device="cuda")
+    q = torch.zeros(n, 8, 128, dtype=torch.bfloat16)
+    q[..., 0], q[..., 1] = 1.0, part * 2.0 ** -17
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    # n queries of two keys each: n sequences, or one of many rows with the mask left out
+    k = 448 * 2.0 ** 7
+    if n == 1:
+        args = i32(0).view(1, 1), i32(2), i32(0, 1)
+        out = pkv.paged_attention_forward_fp8block(q.cuda(), kc, vc, k_scale, v_scale, *args, 1.0)
+        p = to_f64(out)
+        logit = np.log(p / (1 - p))
+    else:  # keys 2 .. n - 1 are zeros too: the first key's odds against n - 1 others
+        blocks = n // 16
+        kc, vc = (torch.cat([c] + [torch.zeros_like(c)] * (blocks - 1)) for c in (kc, vc))
+        k_scale, v_scale = k_scale.repeat(blocks, 1), v_scale.repeat(blocks, 1)
+        vc[0, 0] = int(one[1])
+        args = i32(*range(blocks)).view(1, blocks), i32(n), i32(0, n)
+        out = pkv.paged_attention_forward_fp8block(q.cuda(), kc, vc, k_scale, v_scale, *args, 1.0, False)
+        p = to_f64(out)
+        logit = np.log(p * (n - 1) / (1 - p))
+    true = part * 2.0 ** -17 * k
+    assert np.all(np.abs(logit - true) <= 2.0 ** -17 * k + 1 / 16), (logit.min(), logit.max(), true)
