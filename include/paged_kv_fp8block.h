@@ -96,11 +96,13 @@ pkv_status paged_kv_copy_block_scales(float* k_scales, float* v_scales, const in
  * scale (off by at most 2^-17 of the row's largest |q|, or by 2^-136 where that
  * is more; calls of many rows may leave out more of a row so small that none of
  * its logits moves by 2^-16; the tensor cores multiply codes by codes), logits
- * and sums are fp32; a weight times its V scale is
- * split into E5M2 terms of 9 bits together in calls of few rows, and rounded to
- * fp16 in calls of many (at least 11 bits for those above 2^-21 of the row's
- * largest).  q is expected finite (an infinity counts as a large finite value; a NaN
- * makes its row NaN).
+ * and sums are fp32; a weight times its V scale is split into E5M2 terms of 9
+ * bits together in calls of few rows, and rounded to fp16 in calls of many (at
+ * least 11 bits for those above 2^-21 of the row's largest).
+ * q is expected finite, and a row's largest |q| times scale times a K scale it
+ * meets below 2^110, so that logits stay in fp32.  A NaN makes its row NaN; a row
+ * with an infinity, or past that bound, may be NaN or anything else.  Other rows are
+ * as without it.
  */
 pkv_status paged_attention_forward_fp8block(const void* q, const void* k_cache, const void* v_cache,
                                             const float* k_scales, const float* v_scales,

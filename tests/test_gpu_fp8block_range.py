@@ -1,5 +1,5 @@
 """paged_attention_forward_fp8block at the ends of its ranges: q, K's scales and
-the logit scale by powers of two apart, and the bound of q's split.
+the logit scale by powers of two apart, and rows of q that are not finite.
 
 Powers of two that cancel leave every logit what it was, so the tolerances are
 those of the operator's other tests: weights of 9 bits or more (2^-9 of each), q's
@@ -50,6 +50,23 @@ def test_rows_of_q_of_every_magnitude(n):
     b.q = (b.q.float() * size[:, None, None]).to(torch.bfloat16)
     b.up()
     b.check(pkv.paged_attention_forward_fp8block(*b.args))
+
+
+@pytest.mark.parametrize("n", QUERIES)
+def test_rows_of_q_that_are_not_finite(n):
+    """A NaN makes its row NaN, an infinity its row what it will: no other row moves."""
+    b = Batch(33, [600, 300], n, 8, 2, 16)
+    want = pkv.paged_attention_forward_fp8block(*b.args)
+    b.check(want)
+    q = b.args[0].clone()
+    last = q.shape[0] - 1
+    q[0, 1, 5], q[last, 6, 127], q[last, 2, 0] = float("nan"), float("inf"), float("-inf")
+    got = pkv.paged_attention_forward_fp8block(q, *b.args[1:])
+    assert pkv.device_errors() == 0
+    assert torch.isnan(got[0, 1]).all()
+    for t, h in ((0, 1), (last, 6), (last, 2)):
+        got[t, h] = want[t, h]
+    assert torch.equal(got, want)
 
 
 @pytest.mark.parametrize("n", [1, 64])
