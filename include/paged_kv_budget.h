@@ -27,6 +27,11 @@
  * unchanged.  Cached keys carry the rotation of the position they were
  * written at (paged_kv_write_rope takes positions apart from the slots).
  *
+ * Pools with a scale for each block (paged_kv_fp8block.h) are not for these calls,
+ * which know no such scales and cannot tell such pools from FP8 pools of one scale:
+ * scores of them would be of other keys, and rows moved between blocks would change
+ * their values, unreported.
+ *
  * Layouts, alignment, streams and errors are those of paged_kv.h.
  */
 #ifndef PAGED_KV_BUDGET_H_
@@ -141,8 +146,9 @@ pkv_status paged_kv_select(const float* scores, const int32_t* score_rows, const
  *                     either block_tables' entry j or a block that no sequence
  *                     of the call reads (pkv_bm_compact hands out such tables)
  *   scores            device float32 [num_rows, num_kv_heads, max_len] or NULL
- *   dtype             PKV_DTYPE_BF16, _F32 or _FP8_E4M3 (the pools' element);
- *                     head_dim * element size a multiple of 16
+ *   dtype             PKV_DTYPE_BF16, _F32 or _FP8_E4M3 (the pools' element, of
+ *                     one scale for a pool); head_dim * element size a multiple
+ *                     of 16
  * A block written in place must belong to this sequence alone (no other table
  * of the call or of a later step reads its old rows).  Positions not ascending
  * set PKV_DEVERR_BAD_SEQUENCE, and the rows of that head are unspecified.  A

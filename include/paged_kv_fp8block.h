@@ -17,6 +17,14 @@
  * The attention reads any scale; one outside [2^-60, 2^60] is taken as the
  * nearest end (a NaN as 2^-60).
  *
+ * The codes have the type and layout of paged_kv.h's FP8 pools, so that no call
+ * can tell the two apart.  Only the calls below, and paged_kv_copy_blocks together
+ * with paged_kv_copy_block_scales, are for these pools.  Calls that take one scale
+ * for a pool (all that end in _fp8 or _fp8kv, paged_attention_scores_fp8kv among
+ * them) read or write other values here, and paged_kv_compact moves codes between
+ * blocks whose scales differ: none of them reports it.  There is no scoring and no
+ * eviction of these pools' tokens.
+ *
  * Layouts, alignment, streams and errors are those of paged_kv.h.
  */
 #ifndef PAGED_KV_FP8BLOCK_H_

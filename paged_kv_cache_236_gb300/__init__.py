@@ -1187,7 +1187,8 @@ def paged_attention_scores_fp8kv(q: torch.Tensor, k_cache: torch.Tensor, block_t
                                  score_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
                                  workspace: torch.Tensor | None = None, max_query_len: int = 0) -> torch.Tensor:
     """``paged_attention_scores`` over an FP8 K pool read as code * k_scale
-    (q bf16 with |q| below 65504, head_dim 128)."""
+    (q bf16 with |q| below 65504, head_dim 128).  Not for pools with a scale for
+    each block (``paged_kv_write_fp8block``)."""
     dev = _device_of(q, k_cache, block_tables, context_lens, query_start_loc, scores, score_rows)
     _check_fp8_pools(k_cache, k_cache)
     if q.dtype != torch.bfloat16:
@@ -1233,7 +1234,9 @@ def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables:
     ``kept`` is ``paged_kv_select``'s int32 ``[num_seqs, Hkv, budget]``.  The
     rows go to ``dst_block_tables`` (default: in place): each of its blocks is
     the same entry of ``block_tables`` or a block no sequence of the call
-    reads, as ``BlockManager.compact`` returns.  Pools are bf16, f32 or FP8."""
+    reads, as ``BlockManager.compact`` returns.  Pools are bf16, f32 or FP8 with
+    one scale: codes move as they are, so that pools with a scale for each block
+    (``paged_kv_write_fp8block``), which look the same, would change their values."""
     dev = _device_of(k_cache, v_cache, block_tables, kept, dst_block_tables, scores, score_rows)
     pool, table, dtype = k_cache.shape, block_tables.shape, k_cache.dtype
     if dtype not in _POOL_DTYPE or v_cache.dtype != dtype:
@@ -1285,7 +1288,10 @@ def paged_kv_write_fp8block(k: torch.Tensor, v: torch.Tensor, slot_mapping: torc
     ``k_scales, v_scales`` (float32 ``[NB, Hkv]``, zeros at first) hold powers
     of two: a block's scale covers the largest row it holds.  It grows as rows
     arrive, with the block's earlier codes moved to it, and starts anew when a
-    call writes the block's first slot."""
+    call writes the block's first slot.
+
+    Such pools look like FP8 pools of one scale, and are not for the calls of
+    these (``..._fp8``, ``..._fp8kv``) nor for ``paged_kv_compact``."""
     dev = _device_of(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales, workspace)
     _check_block_scales(k_cache, v_cache, k_scales, v_scales)
     NB, bs, Hkv, D = k_cache.shape
