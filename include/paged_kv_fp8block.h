@@ -50,6 +50,10 @@ extern "C" {
  * and, where the block goes on (old > 0 or 0 alike) and new > old, every code
  * of it that the call does not write becomes E4M3(RNE(value * old / new)).
  * Codes that the call does not write are otherwise left as they are.
+ * A division by new is a product with its reciprocal in fp32.  For the powers of two
+ * that this call makes that is the same; a scale that the caller put there (finite;
+ * below 0 or a NaN it counts as 0) need not be one, and a code may then be its
+ * neighbour where the quotient lies within 2^-22 of the border between two.
  * Rows are expected finite: an infinity saturates, and takes its scale to 2^60; a
  * NaN has no part in the scale.
  *
