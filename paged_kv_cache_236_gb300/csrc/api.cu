@@ -431,8 +431,10 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   const bool bf16 = dtype == PKV_DTYPE_BF16;
   const int G = Hq / Hkv;
 
-  int dec_ctas = 1;
-  cudaError_t e = kv_fp8 ? decode_fp8_ctas_per_sm(&dec_ctas) : decode_ctas_per_sm(bf16, D, window > 0, &dec_ctas);
+  int dec_ctas = 1;  // of the CUDA-core kernel, which pools with block scales never run
+  cudaError_t e = blocks   ? cudaSuccess
+                  : kv_fp8 ? decode_fp8_ctas_per_sm(&dec_ctas)
+                           : decode_ctas_per_sm(bf16, D, window > 0, &dec_ctas);
   if (e != cudaSuccess) return cuda_fail(e, "decode kernel set-up");
 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -569,13 +571,11 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   if (cascade && (e = launch_prefix_search(pp, s)) != cudaSuccess) return cuda_fail(e, "prefix search launch");
   if ((e = launch_planner(pp, s)) != cudaSuccess) return cuda_fail(e, "planner launch");
 
+  // whole rows; codes with block scales are MMA operands as they land, in the MMAs' swizzle
+  const CUtensorMapSwizzle swizzle = blocks ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
   CUtensorMap kmap, vmap;
-  if ((st = encode_pool_map(&kmap, k_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_NONE)) !=
-      PKV_OK)
-    return st;
-  if ((st = encode_pool_map(&vmap, v_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_NONE)) !=
-      PKV_OK)
-    return st;
+  if ((st = encode_pool_map(&kmap, k_cache, kv_dtype, num_blocks, bs, Hkv, D, D, swizzle)) != PKV_OK) return st;
+  if ((st = encode_pool_map(&vmap, v_cache, kv_dtype, num_blocks, bs, Hkv, D, D, swizzle)) != PKV_OK) return st;
 
   AttnParams ap{};
   ap.q = q;
@@ -613,22 +613,13 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   // and the tensor-core grid starts once the planner's grid has completed
   ap.no_wait = side_by_side ? 1 : 0;
   if (g_prof_start && (e = cudaEventRecord(g_prof_start, s)) != cudaSuccess) return cuda_fail(e, "profile event");
-  CUtensorMap kmap_codes, vmap_codes;
-  if (blocks) {
-    if ((st = encode_pool_map(&kmap_codes, k_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
-        PKV_OK)
-      return st;
-    if ((st = encode_pool_map(&vmap_codes, v_cache, kv_dtype, num_blocks, bs, Hkv, D, D, CU_TENSOR_MAP_SWIZZLE_128B)) !=
-        PKV_OK)
-      return st;
-  }
   if (mma_launch && blocks) {
     CUtensorMap qmap, omap;
     if ((st = encode_q_map(&qmap, q, T, Hq, D, 64, G, kMmaRows / G)) != PKV_OK) return st;
     if ((st = encode_q_map(&omap, out, T, Hq, D, 64, G, kMmaRows / G)) != PKV_OK) return st;
     ap.counter = &header->mma_counter;
     ap.items = mma_items;
-    if ((e = launch_mma_fp8block(ap, qmap, kmap_codes, vmap_codes, omap, dev->sms, s)) != cudaSuccess)
+    if ((e = launch_mma_fp8block(ap, qmap, kmap, vmap, omap, dev->sms, s)) != cudaSuccess)
       return cuda_fail(e, "mma (block scales) launch");
   } else if (mma_launch) {
     CUtensorMap qmap, kmap_sw, vmap_sw;
@@ -652,7 +643,7 @@ static pkv_status forward_impl(const void* q, const void* k_cache, const void* v
   ap.counter = &header->dec_counter;
   ap.items = dec_items;
   if (blocks) {
-    if ((e = launch_dec_fp8block(ap, tc_rows, kmap_codes, vmap_codes, dev->sms, s)) != cudaSuccess)
+    if ((e = launch_dec_fp8block(ap, tc_rows, kmap, vmap, dev->sms, s)) != cudaSuccess)
       return cuda_fail(e, "decode (block scales) launch");
   } else if (dectc && kv_fp8) {
     CUtensorMap qmap16;
