@@ -47,6 +47,7 @@
 #include <limits.h>
 #include <math_constants.h>
 
+#include "block_scales.cuh"
 #include "dec_rows.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
@@ -108,11 +109,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) == Lay<4>::kNumBars * 8, "barrier block");
 
-// What a tile's block has of scales: K's, log2 of V's, 2^-11 / V's.
-struct alignas(16) Scales {
-  float k, log_v, inv_v, pad;
-};
-
 // An item as the fetch warp hands it to the producers: L counts places, the
 // keys without those from `at` on that a window leaves out (len of them).
 struct alignas(16) ItemSlot {
@@ -131,20 +127,6 @@ struct alignas(16) EpSlot {
   int pad[15];
 };
 static_assert(sizeof(EpSlot) == 256, "epilogue slot");
-
-// [2^-60, 2^60]; a NaN is the least
-__device__ __forceinline__ float clamp_scale(float s) {
-  return s >= 0x1p-60f ? fminf(s, 0x1p60f) : 0x1p-60f;
-}
-__device__ __forceinline__ Scales make_scales(float k, float v) {
-  Scales s;
-  s.k = clamp_scale(k);
-  const float c = clamp_scale(v);
-  s.log_v = log2f(c);  // exact for powers of two
-  s.inv_v = __fdiv_rn(1.f / (1 << kWeightExp), c);
-  s.pad = 0.f;
-  return s;
-}
 
 template <int N>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[N]) {
@@ -272,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       // (ids read two tiles ahead, a tile's at a time, stalled the loop for their
       // latency in every tile, since the registers move on: 4.4 TB/s).
       int phys = sl.phys[lane];
-      Scales sc = make_scales(sl.scales[lane].x, sl.scales[lane].y);
+      Scales sc = make_scales<kWeightExp>(sl.scales[lane]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->islot_free[qb]);
       if (done) {
@@ -352,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         if (++tile == group) {
           tile = 0;
           phys = next_phys;
-          sc = make_scales(next_sc.x, next_sc.y);
+          sc = make_scales<kWeightExp>(next_sc);
         }
       }
       if (!ok) {
@@ -441,13 +423,10 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
         uint32_t hi = 0, lo = 0;
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float a = x[i] * down, b = x[i + 1] * down;
-          const uint32_t t = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)t, __NV_E4M3);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          const uint32_t u = __nv_cvt_float2_to_fp8x2(make_float2(a - f.x, b - f.y), __NV_SATFINITE, __NV_E4M3);
-          hi |= (t & 0xFFFFu) << (8 * i);
-          lo |= (u & 0xFFFFu) << (8 * i);
+          uint32_t t, u;
+          split_e4m3(x[i] * down, x[i + 1] * down, t, u);
+          hi |= t << (8 * i);
+          lo |= u << (8 * i);
         }
         // rows r and NR + r, columns 4 lane ..: 16-byte chunk lane / 4, swizzled
         const int c1 = (lane >> 2) ^ (r & 7), c2 = (lane >> 2) ^ ((NR + r) & 7);

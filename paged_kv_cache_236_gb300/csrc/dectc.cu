@@ -164,13 +164,6 @@ struct alignas(16) EpSlot {
 static_assert(sizeof(EpSlot) == 256, "epilogue slot");
 static_assert(sizeof(Bars) == kNumBars * 8, "barrier block");
 
-// Two E4M3 codes (low byte first) as an fp16 pair, exactly (every E4M3
-// value is an fp16 value).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
-
 // One tile of codes (128 keys x 128 bytes, row-major) as the fp16 tile the
 // MMAs read: two 64-column halves kHalf apart, key r's 16-byte chunk j at
 // chunk j ^ (r & 7) of its 128-byte row (the 128-byte swizzle).  Thread c of

@@ -143,7 +143,7 @@ __device__ __forceinline__ void values8(uint2 c, float (&x)[8]) {
   const uint32_t in[2] = {c.x, c.y};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(in[i >> 1] >> (16 * (i & 1)) & 0xFFFFu), __NV_E4M3);
+    const uint32_t h = e4m3x2_to_f16x2(in[i >> 1] >> (16 * (i & 1)) & 0xFFFFu);
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;

@@ -164,20 +164,6 @@ static_assert(kKOff % 1024 == 0 && kVOff % 1024 == 0 && kTileBytes % 1024 == 0 &
               "swizzled tiles");
 static_assert(kBarOff % 8 == 0 && kSlotOff % alignof(ItemSlot) == 0 && kRedOff % 16 == 0, "alignment");
 
-// N bf16 (2N bytes) of an output row, packed in pairs in w: 32-byte stores
-// when the output is 32-byte aligned, else 16-byte ones.
-template <int N>
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* w, int al32) {
-  if (al32) {
-#pragma unroll
-    for (int u = 0; u < N / 16; ++u) st_global_v8(dst + 16 * u, w + 8 * u);
-  } else {
-#pragma unroll
-    for (int u = 0; u < N / 8; ++u)
-      *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-  }
-}
-
 // D: head_dim, 64 or 128 (one or two 64-column halves of Q, K, V and the
 // output; the shared-memory and TMEM layouts are those of 128, with the
 // second halves unused at 64).  Each softmax thread owns D / 2 output

@@ -53,6 +53,7 @@
 #include <limits.h>
 #include <math_constants.h>
 
+#include "block_scales.cuh"
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
 #include "pkv_tc.cuh"
@@ -136,22 +137,6 @@ struct alignas(16) ItemSlot {
 // K / V producers, the four converting and three splitting warps
 constexpr int kSlotReaders = 256 + 2 + 2 + 4 + 3;
 
-// What a tile's block has of scales: K's, log2 of V's, 2^-7 / V's.
-struct alignas(16) Scales {
-  float k, log_v, inv_v, pad;
-};
-// [2^-60, 2^60]; a NaN is the least
-__device__ __forceinline__ float clamp_scale(float s) { return s >= 0x1p-60f ? fminf(s, 0x1p60f) : 0x1p-60f; }
-__device__ __forceinline__ Scales make_scales(float2 kv) {
-  Scales s;
-  s.k = clamp_scale(kv.x);
-  const float c = clamp_scale(kv.y);
-  s.log_v = log2f(c);  // exact for powers of two
-  s.inv_v = __fdiv_rn(1.f / (1 << kWeightExp), c);
-  s.pad = 0.f;
-  return s;
-}
-
 static_assert(sizeof(ItemSlot) == 320, "item slot");
 static_assert(sizeof(Bars) == kNumBars * 8, "barrier block");
 static_assert(kVStages == 2, "V stage t % 2 is released by the P.V barrier of tile t");
@@ -160,11 +145,6 @@ static_assert(kKOff % 1024 == 0 && kCOff % 1024 == 0 && kVOff % 1024 == 0, "swiz
 static_assert(kBarOff % 8 == 0 && kSlotOff % alignof(ItemSlot) == 0 && kRedOff % 16 == 0 && kScaleOff % 16 == 0,
               "alignment");
 
-// Two E4M3 codes (low byte first) as an fp16 pair, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -202,32 +182,12 @@ __device__ __forceinline__ void split_rows(uint8_t* tile, int row0, int row1, fl
                           bf16_hi(raw[i].y) * down};
       uint32_t h[2], l[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        h[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a[2 * k], a[2 * k + 1]), __NV_SATFINITE, __NV_E4M3) & 0xFFFFu;
-        const uint32_t back = e4m3x2_to_f16x2(h[k]);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        l[k] = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a[2 * k] - f.x, a[2 * k + 1] - f.y), __NV_SATFINITE,
-                                                  __NV_E4M3) & 0xFFFFu;
-      }
+      for (int k = 0; k < 2; ++k) split_e4m3(a[2 * k], a[2 * k + 1], h[k], l[k]);
       uint8_t* dst = tile + (r0 + i) * 128 + to + ((tc ^ ((r0 + i) & 7)) << 4);
       *reinterpret_cast<uint32_t*>(dst) = h[0] | h[1] << 16;
       *reinterpret_cast<uint32_t*>(dst + kHalf) = l[0] | l[1] << 16;
       if (lane == i) scales[r0 + i] = __uint_as_float((uint32_t)(127 + e) << 23) * scale_log2;
     }
-  }
-}
-
-// N bf16 (2N bytes) of an output row, packed in pairs in w: 32-byte stores
-// when the output is 32-byte aligned, else 16-byte ones.
-template <int N>
-__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* w, int al32) {
-  if (al32) {
-#pragma unroll
-    for (int u = 0; u < N / 16; ++u) st_global_v8(dst + 16 * u, w + 8 * u);
-  } else {
-#pragma unroll
-    for (int u = 0; u < N / 8; ++u)
-      *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
   }
 }
 
@@ -476,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           if (!is_v) {
             // the slot's last reader was tile g-8's softmax: Q K^T(g-3) was issued after S(g-5) was read
             const float2 mine = make_float2(__shfl_sync(0xffffffffu, sc.x, run_block), __shfl_sync(0xffffffffu, sc.y, run_block));
-            if (lane < 16) tile_scales[(g & (kScaleSlots - 1)) * 16 + lane] = make_scales(mine);
+            if (lane < 16) tile_scales[(g & (kScaleSlots - 1)) * 16 + lane] = make_scales<kWeightExp>(mine);
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->sc_full[g & (kScaleSlots - 1)]);
           }

@@ -176,5 +176,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// N bf16 (2N bytes) of an output row, packed in pairs in w: 32-byte stores
+// when the output is 32-byte aligned, else 16-byte ones.
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* dst, const uint32_t* w, int al32) {
+  if (al32) {
+#pragma unroll
+    for (int u = 0; u < N / 16; ++u) st_global_v8(dst + 16 * u, w + 8 * u);
+  } else {
+#pragma unroll
+    for (int u = 0; u < N / 8; ++u)
+      *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+  }
+}
 
 }  // namespace pkv
