@@ -34,7 +34,9 @@
  * position L - n + i; with causal != 0 it attends keys 0 .. L-n+i, otherwise
  * all L keys.  Query head h reads kv head h / (num_q_heads / num_kv_heads).
  * The result is softmax(scale * q k^T) v accumulated in fp32 and cast to the
- * dtype of q (round to nearest even).
+ * dtype of q (round to nearest even).  The tensor-core kernels over bf16 pools
+ * round each softmax weight to bf16 before it meets V; sums of weights take them
+ * unrounded.
  *
  * Ownership: every buffer is the caller's (device memory unless stated);
  * the library allocates no device memory and keeps no state across calls

@@ -250,9 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       const WorkItem it = sl.it;
       const int idx = sl.idx, L = sl.L, qstart = sl.qstart, n = sl.n, nblk = sl.nblk, at = sl.at, len = sl.len;
       // Block ids and scales are held 32 at a time, a lane to a block: those of the
-      // item's next 32 / nb tiles.  The next 32 are read while these are used
-      // (ids read two tiles ahead, a tile's at a time, stalled the loop for their
-      // latency in every tile, since the registers move on: 4.4 TB/s).
+      // item's next 32 / nb tiles.  The next 32 are read while these are used, so that
+      // no tile waits for a read of its own.
       int phys = sl.phys[lane];
       Scales sc = make_scales<kWeightExp>(sl.scales[lane]);
       __syncwarp();
@@ -528,9 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1) dec_fp8block_kernel(const AttnPar
       // The weights are made with the reference as it stands, and the barrier
       // that ends the tile tells whether a key of any warp exceeded it by the
       // threshold; only then are the tile's row maxima found and exchanged and
-      // the weights made again (the first tile of an item, and few others).  The
-      // maxima in every tile were a chain of shuffles and a barrier before the
-      // exponentials: 1850 cycles a tile, 223 us for 4 x 131072 keys.
+      // the weights made again (the first tile of an item, and few others): maxima in
+      // every tile are a chain of shuffles and a barrier ahead of the exponentials.
       const int my_row = lane >> (5 - kLog);  // row this lane holds after a reduction
       const bool row_writer = (lane & ((1 << (5 - kLog)) - 1)) == 0;
       const int my_block = t / p.bs;

@@ -15,6 +15,7 @@
 // tile costs two small MMAs, with the rows on N:
 //   S^T [128 keys x 16 rows] = K [128 keys x 128 d] . Q^T        (A K-major, B K-major)
 //   O^T [128 d x 16 rows]   += V^T [128 d x 128 keys] . P^T      (A MN-major, B K-major)
+// (P in bf16, V's type, as an MMA wants it: up to 2^-8 of each weight)
 // so one thread per key does the softmax arithmetic for its key (16 values)
 // and one thread per output column writes the result, coalesced.
 //

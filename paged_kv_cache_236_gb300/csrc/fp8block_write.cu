@@ -19,10 +19,9 @@
 // flight before the maximum, the rows stay in registers until they are encoded.
 //
 // HBM-bound for prompts (rows in once, codes out once): 16384 tokens of 8 heads of
-// 128 in bf16 25.9 us, of which the table's launch (4 us) and the leaders' three
-// dependent reads are a third (without the rows' prefetch 2.3 us more).  Its
-// instructions came next: 25 of a warp to each 32 elements held it at 39.6 us before a
-// lane kept its column, maxima were taken two at a time and block sizes shifts.  A
+// 128 in bf16 25.4 us, of which the table's launch (4 us) and the leaders' three
+// dependent reads are a third; its instructions (49 % of the issue slots) come next,
+// so that a lane keeps its column and maxima are taken two at a time.  A
 // decode step is a launch and four dependent reads (slot, old scale, rows, codes of a
 // block that grows): 12.3 us with the call.
 #include <cuda_bf16.h>

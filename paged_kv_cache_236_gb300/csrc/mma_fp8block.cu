@@ -26,11 +26,7 @@
 // warps' chain: 200 for its waits, 600 for the maxima, 1400 for the weights, 100 to
 // 700 to hand them on), so that operations bound it and not bytes: chunks of 512 on up to 2048
 // (86 GFLOP) 150 us, 574 TFLOP/s; the verify batch (5 tokens of 8 heads on 8192
-// keys, 40 of a tile's 128 rows used) 195 us, 2.8 TB/s of codes.  Weights made with the
-// reference as it stands, and again where a tile exceeds it, took 182 and 228 us:
-// blocks' magnitudes differ, and a sixth of the tiles were made twice.  Loads of S
-// ahead of their use 151 and 217 (then 150 and 216); merges left to the splitting
-// warps 152, and 156 against 133 for 20 chunks of 60 tokens.
+// keys, 40 of a tile's 128 rows used) 192 us, 2.8 TB/s of codes.
 //
 // Roles (640 threads, one CTA per SM, persistent):
 //   warp 0     the thread issuing P.V;
@@ -40,9 +36,8 @@
 //              tiles' scales (the softmax warps read them up to 5 tiles after the
 //              K stage they came with is free);
 //   warp 12    V producer: codes into a staging ring;
-//   warps 16-19 V converters, one to each scheduler (with two of them, on two
-//              schedulers, those were late with their softmax rows: their exponentials
-//              and conversions share a pipe: prompt chunks 249 us against 205);
+//   warps 16-19 V converters, one to each scheduler, since conversions and the
+//              softmax warps' exponentials share a pipe;
 //   warps 4-11 softmax / correction / epilogue, two threads per row;
 //   warp 14    item fetch, Q and output stores;
 //   warps 3,13,15 split the Q tile.
@@ -92,9 +87,9 @@ constexpr uint32_t kSCol = 0;    // S buffer b at kSCol + 128 b
 constexpr uint32_t kPCol = 256;  // P buffer b at kPCol + 64 b
 constexpr uint32_t kOCol = 384;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
-// Register split between warpgroups (setmaxnreg): warpgroups 0 and 3 (MMA
-// issuers, producers, item fetch) give up registers that warpgroups 1 and 2
-// (softmax) take.  The sum must stay within what the block is launched with
+// Register split between warpgroups (setmaxnreg): warpgroups 0, 3 and 4 (MMA
+// issuers, producers, item fetch, Q split, converters) give up registers that
+// warpgroups 1 and 2 (softmax) take.  The sum must stay within what the block is launched with
 // (kThreads x the kernel's register count); the launcher checks the count.
 constexpr int kRegs = 96, kRegsLight = 56, kRegsSoftmax = 152;
 static_assert(3 * 128 * kRegsLight + 2 * 128 * kRegsSoftmax <= kThreads * kRegs, "register split above the launch's");
@@ -697,10 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_fp8block_kernel(const AttnPar
           seen = below(nvis) & (below(p.num_sink - (kt + 64 * h)) | ~below(nlo));
         }
         const Scales* scales = tile_scales + (g & (kScaleSlots - 1)) * 16 + 8 * h;
-        // S is read twice, 32 columns at a time, in loops: a row's 64 in registers,
-        // with the code unrolled over them and three copies of it, did not fit the
-        // instruction cache with the other roles' code, which then set the pace
-        // (prompt chunks 205 us; 157 with 16 columns at a time).
+        // S is read twice, 32 columns at a time, in loops: the code unrolled over a row's
+        // 64 columns did not fit the instruction cache beside the other roles' code.
         auto columns = [&](int run, uint32_t (&z)[16]) {  // masked: columns 8 run .. + 15
           if (masked) {
             const uint32_t m = (uint32_t)(seen >> (8 * run));

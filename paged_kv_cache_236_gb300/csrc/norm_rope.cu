@@ -311,9 +311,7 @@ __global__ void __launch_bounds__(kWarps * 32) norm_rope_kernel(const NormParams
 // heads of at most 32 places; weights and angles wait in shared memory too.
 // 16384 tokens of 32 and 8 heads of 128 into FP8 pools move 369 MB in 74.3 us,
 // 0.73 of a copy's rate.  The instructions (sums across lanes, conversions; 0.58 of
-// a scheduler's issue slots) are what it waits for: loops unrolled further, 2 and 8
-// warps a CTA and a rotation without its angles were within 2 %, two values an
-// instruction took 90 us to 85.6, codes without a division to 74.3.
+// a scheduler's issue slots) are what it waits for.
 template <typename U, bool F8, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) norm_rope_bulk_kernel(const NormParams p, int token_bytes) {
   pdl_launch_dependents();  // what follows with programmatic launch reads nothing written here before it waits
@@ -551,7 +549,8 @@ cudaError_t launch(const NormParams& p0, bool vec, int sms, cudaStream_t s) {
   while (p.T * p.splits < (int64_t)sms * 8 && p.splits < most) p.splits *= 2;
   // tokens enough for every warp to take whole ones: their rows by bulk copies,
   // where four of them fit (32 and 8 heads of 128: 4216 tokens 36.5 us with a token's
-  // loads by its lanes, 28.1 so; 16384 tokens into FP8 pools 122 and 74.3 us)
+  // loads by its lanes, 28.1 so; 16384 tokens into FP8 pools 122 and, with a division
+  // to each code as then, 85.6)
   const int64_t token = ((int64_t)p.Hq + (p.slots ? 2 : 1) * p.Hkv) * p.D * (int64_t)sizeof(U);
   const int64_t bulk = (((int64_t)2 * p.D * 4 + kWarps * p.half * 8 + 127) & ~127) + kWarps * token;
   if (p.splits == 1 && vec && places <= 32 && bulk <= kBulkSmem)
