@@ -1005,6 +1005,8 @@ def _norm_rope_args(q, k, v, q_weight, k_weight, positions, inv_freq, slot_mappi
                 not k_cache.is_contiguous() or not v_cache.is_contiguous():
             raise ValueError(f"caches must be contiguous [num_blocks, block_size, {Hkv}, {D}]")
         NB, bs = pool[0], pool[1]
+        if NB == 0 or bs == 0:  # their pointers are null, which the C call takes for no pools
+            raise ValueError("caches must have blocks")
         if v.shape != rows or v.dtype != dtype or vs[2] != 1 or vs[1] != D:
             raise ValueError(f"v must be {list(rows)} of q's dtype with contiguous heads")
         if slot_mapping.shape != (T,) or slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():

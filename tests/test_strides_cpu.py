@@ -1,6 +1,7 @@
-"""Tensors that repeat one row or layer (a stride of 0), which the C calls take
-for dense ones: the binding refuses them.  The library is stubbed, so that what
-a call would be given is seen without a GPU."""
+"""Tensors that the C calls would take for others, and that the binding refuses:
+those that repeat one row or layer (a stride of 0: dense), and pools without a
+block (a null pointer: none).  The library is stubbed, so that what a call would be
+given is seen without a GPU."""
 import contextlib
 
 import pytest
@@ -89,3 +90,22 @@ def test_a_row_of_one_token_for_all(calls, monkeypatch, name):
     assert [n for n, _ in calls] == [name] * 3
     wide = [tuple(x for x in a if x in (64, 128)) for _, a in calls]
     assert wide[0] == (64, 128) and wide[1] == (64, 64) and wide[2] == ()
+
+
+@pytest.mark.parametrize("shape", [(0, 16), (4, 0)])
+def test_pools_without_a_block(calls, monkeypatch, shape):
+    """Slots of a pool without a block are past it, and not left out unreported."""
+    monkeypatch.setattr(pkv, "_device_of", lambda *t: -1)
+    monkeypatch.setattr(pkv, "_call", lambda fn, dev, *a: fn(*a))
+    q = k = v = torch.zeros(3, 2, 32)
+    at, inv = torch.arange(3), torch.ones(16, dtype=torch.float64)
+
+    def write(kc, vc):
+        return pkv.paged_kv_write_norm_rope(q, k, v, None, None, at, inv, at, kc, vc, k_out=torch.zeros(3, 2, 32))
+
+    none = torch.zeros(*shape, 2, 32)
+    with pytest.raises(ValueError, match="blocks"):
+        write(none, none.clone())
+    assert not calls
+    write(torch.zeros(4, 16, 2, 32), torch.zeros(4, 16, 2, 32))
+    assert [n for n, _ in calls] == ["paged_kv_write_norm_rope"]
