@@ -610,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
         };
         float alpha = 1.f;
         bool rescale = false;
+        bool again = false;  // of the warp: a row's reference rose past the first tile
         if (j == 0) {
           // first tile of the item: the row max first, then the exponentials
           named_barrier(pair_bar, 64);
@@ -635,7 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
           }
           // for one row or more: by the whole warp, as TMEM stores must be (the
           // other rows write what they wrote)
-          if (__any_sync(0xffffffffu, raise)) {
+          again = __any_sync(0xffffffffu, raise);
+          if (again) {
             tmem_wait_st();  // the first pass's P pieces land before they are rewritten
             exps(m_ref);
           }
@@ -644,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) mma_attn_kernel(const AttnParams 
           const float2 a = up2(ps2[0]), b = up2(ps2[1]);
           l = fmaf(l, alpha, (a.x + a.y) + (b.x + b.y));
         }
-        if (__any_sync(0xffffffffu, rescale)) {
+        if (again && __any_sync(0xffffffffu, rescale)) {
           // O must hold every earlier tile's P.V before it is scaled; the TMEM
           // accesses are warp-wide, rows that keep their max scale by 1
           // P.V(g-1) complete
